@@ -353,6 +353,64 @@ int moe_field(const moe_cfg *cfg, int field, size_t *byte_offset, size_t *count)
 int moe_set_timing(moe_plan *plan, int enable);
 int moe_timings(moe_plan *plan, float *ms, int n);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the transformer block around the routed experts. They need no plan:
+ * every call takes its tensors, works on the current device (compute capability 10.3,
+ * else MOE_ERR_UNSUPPORTED) and is asynchronous on `stream`. Matrices are row-major
+ * with a leading dimension ld_* in elements (at least the row's length). Base pointers
+ * need the alignment of their element type only, unless stated. Inputs and outputs of
+ * a call do not overlap. n = 0 rows is a call that does nothing (gradients of weights
+ * are then zero). The first call on a device loads the kernels: make it before a
+ * stream capture; every later call may be captured.
+ * ------------------------------------------------------------------------- */
+enum moe_dtype {
+  MOE_BF16 = 0,
+  MOE_FP16 = 1,
+  MOE_FP32 = 2
+};
+
+enum moe_score {
+  MOE_SCORE_SOFTMAX = 0, /* exp(l_e) / sum_i exp(l_i) */
+  MOE_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-l_e)) */
+};
+
+/* Routing to experts from their scores l (moe_router). */
+typedef struct moe_router_cfg {
+  int E;           /* experts, 1..1024 */
+  int topk;        /* experts chosen for each token, 1..min(E, 32) */
+  int score;       /* enum moe_score */
+  int groups;      /* groups of E / groups consecutive experts (1..32, divides E); 1: none */
+  int topk_groups; /* groups that stay, 1..groups; topk <= topk_groups * E / groups */
+  int group_top;   /* a group is judged by the sum of its 1 or 2 largest s + bias */
+  int renorm;      /* 1: the chosen experts' scores are divided by their sum */
+  float scale;     /* factor of every weight, finite */
+} moe_router_cfg;
+
+/* For every token: s = score(l), c = s + bias; the topk_groups best groups stay, and of
+ * their experts the topk with the largest c, in descending order (equal c: the lower id;
+ * equal groups: the lower group). weight = s at the chosen id (without the bias), divided
+ * by the sum of the chosen s with renorm, times scale. Without a bias the order of the c
+ * is that of the l. The choice is that of 64-bit arithmetic.
+ * l = -inf masks an expert (s = 0); bias = -inf keeps it from being chosen while another
+ * is left. A token whose chosen s are all 0 has weights 0 and valid, distinct ids. A NaN
+ * score counts as -inf in the order, and the weights computed from it are NaN.
+ *  plan:   NULL, or the plan whose moe_plan_build reads these ids next: then E, topk and
+ *          n = W*T are the plan's, ids and w are 16-byte aligned, the call is timed in
+ *          slot [0] of moe_timings, and the routing of an earlier moe_gate is forgotten.
+ *  logits: [n][E] of `dtype` (enum moe_dtype), leading dimension ld.
+ *  bias:   NULL or [E] fp32.   ids: out [n][topk] int32.   w: out [n][topk] fp32. */
+int moe_router(moe_plan *plan, const moe_router_cfg *cfg, const void *logits, int dtype,
+               long long n, long long ld, const float *bias, int32_t *ids, float *w,
+               moe_stream_t stream);
+
+/* Gradient of the scores from the gradient of the weights, for the ids that moe_router
+ * chose (the choice itself, and so the bias, has none): d_logits, out [n][E] of `dtype`,
+ * leading dimension ld_d, written whole. d_w: [n][topk] fp32. The ids of a token are
+ * distinct; one out of range has no gradient. */
+int moe_router_backward(const moe_router_cfg *cfg, const float *d_w, const void *logits,
+                        const int32_t *ids, int dtype, long long n, long long ld,
+                        void *d_logits, long long ld_d, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

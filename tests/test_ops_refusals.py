@@ -1,0 +1,100 @@
+"""What the operators around the routed experts refuse, and their float64 test references'
+gradients against differences; no GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from tests import ops_ref as R
+from tile_signaled_grouped_gb300 import build as B
+
+B.build()
+from tile_signaled_grouped_gb300 import capi, ops  # noqa: E402
+
+ARG = capi.MOE_ERR_ARG
+
+
+def router(**kw):
+    base = dict(E=16, topk=2, score=0, groups=1, topk_groups=1, group_top=1, renorm=0, scale=1.0)
+    base.update(kw)
+    return capi.moe_router_cfg(*[base[f] for f, _ in capi.moe_router_cfg._fields_])
+
+
+@pytest.mark.parametrize("bad", [
+    dict(E=0), dict(E=1025), dict(topk=0), dict(topk=17), dict(E=64, topk=33), dict(score=2),
+    dict(score=-1), dict(groups=0), dict(groups=3), dict(E=66, groups=33), dict(topk_groups=0),
+    dict(topk_groups=2), dict(groups=4, topk_groups=1, topk=5), dict(group_top=0),
+    dict(group_top=3), dict(renorm=2), dict(scale=float("nan")), dict(scale=float("inf")),
+])
+def test_router_refuses_configurations(bad):
+    lib = capi.lib()
+    c = ctypes.byref(router(**bad))
+    assert lib.moe_router(None, c, 64, capi.MOE_FP32, 1, 2048, None, 64, 64, None) == ARG
+    assert lib.moe_router_backward(c, 64, 64, 64, capi.MOE_FP32, 1, 2048, 64, 2048, None) == ARG
+
+
+def test_router_refuses_arguments():
+    lib = capi.lib()
+    c = ctypes.byref(router())
+    ok = dict(plan=None, cfg=c, logits=64, dtype=capi.MOE_FP32, n=1, ld=16, bias=None, ids=64, w=64)
+    for bad in (dict(cfg=None), dict(logits=None), dict(logits=66), dict(dtype=3), dict(dtype=-1),
+                dict(n=-1), dict(n=1 << 32), dict(ld=15), dict(bias=2), dict(ids=None), dict(ids=65),
+                dict(w=None), dict(w=2)):
+        a = {**ok, **bad}
+        assert lib.moe_router(*a.values(), None) == ARG, bad
+    ok = dict(cfg=c, d_w=64, logits=64, ids=64, dtype=capi.MOE_BF16, n=1, ld=16, d=64, ld_d=16)
+    for bad in (dict(cfg=None), dict(d_w=None), dict(d_w=66), dict(logits=None), dict(logits=65),
+                dict(ids=None), dict(ids=2), dict(dtype=9), dict(n=-1), dict(ld=15), dict(d=None),
+                dict(d=65), dict(ld_d=15)):
+        a = {**ok, **bad}
+        assert lib.moe_router_backward(*a.values(), None) == ARG, bad
+    # no rows: nothing to do, whatever the pointers
+    assert lib.moe_router(None, c, None, capi.MOE_FP32, 0, 16, None, None, None, None) == 0
+
+
+def test_route_experts_refuses_tensors():
+    l = torch.zeros(4, 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.route_experts(l, 2)
+    with pytest.raises(ValueError, match="type"):
+        ops.route_experts(l.double(), 2)
+    with pytest.raises(ValueError, match="rows"):
+        ops.route_experts(torch.zeros(16, 4).t(), 2)
+    with pytest.raises(ValueError, match="rows"):
+        ops.route_experts(torch.zeros(16).expand(4, 16), 2)
+    with pytest.raises(ValueError, match="bias"):
+        ops.route_experts(l, 2, bias=torch.zeros(8))
+    with pytest.raises(ValueError, match="bias"):
+        ops.route_experts(l, 2, bias=torch.zeros(16, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="score"):
+        ops.route_experts(l, 2, score="tanh")
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="ids"):
+        ops.route_experts_backward(torch.zeros(4, 2), l, ids.long())
+    with pytest.raises(ValueError, match="d_w"):
+        ops.route_experts_backward(torch.zeros(4, 3), l, ids)
+    with pytest.raises(ValueError, match="ids"):
+        ops.route_experts_backward(torch.zeros(3, 2), l, ids[:3])
+
+
+def differences(f, x, g, h=1e-6):
+    """Central differences of sum(f(x) * g) for every element of x."""
+    d = np.zeros_like(x)
+    for i in np.ndindex(x.shape):
+        for sign in (1.0, -1.0):
+            y = x.copy()
+            y[i] += sign * h
+            d[i] += sign * (f(y) * g).sum() / (2 * h)
+    return d
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_reference_gradient_is_the_difference(score, renorm):
+    rng = np.random.default_rng(3)
+    l, dw = rng.normal(size=(3, 12)), rng.normal(size=(3, 4))
+    ids, _ = R.route(l, 4, score, renorm=renorm)
+    d = R.route_backward(dw, l, ids, score, renorm, 2.5)
+    want = differences(lambda v: R.weights(v, ids, score, renorm, 2.5), l, dw)
+    assert np.abs(d - want).max() < 1e-8

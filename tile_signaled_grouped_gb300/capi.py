@@ -37,6 +37,19 @@ class moe_cfg(ctypes.Structure):
     ]
 
 
+class moe_router_cfg(ctypes.Structure):
+    _fields_ = [
+        ("E", ctypes.c_int),
+        ("topk", ctypes.c_int),
+        ("score", ctypes.c_int),
+        ("groups", ctypes.c_int),
+        ("topk_groups", ctypes.c_int),
+        ("group_top", ctypes.c_int),
+        ("renorm", ctypes.c_int),
+        ("scale", ctypes.c_float),
+    ]
+
+
 def _parse_enums():
     """Enum constants of the header (MOE_OK, MOE_PLAN_*, MOE_RANK_*, ...)."""
     text = open(HEADER).read()
@@ -70,7 +83,7 @@ def load():
             f"{LIB_PATH} is missing: the CUDA library is not built "
             "(run tile_signaled_grouped_gb300.build.build() or __graft_entry__.build())")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, ip, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, ip, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
     P = ctypes.POINTER
     sig = {
         "moe_workspace_size": (ip, [P(moe_cfg), P(sz), P(sz), P(ip)]),
@@ -93,6 +106,8 @@ def load():
         "moe_plan_build_noalloc": (ip, [P(moe_cfg), vp, vp, sz, vp]),
         "moe_launch_info": (ip, [vp, P(ip), P(ip), P(ip), P(ip)]),
         "moe_set_schedule": (ip, [vp, ip, ip]),
+        "moe_router": (ip, [vp, P(moe_router_cfg), vp, ip, ll, ll, vp, vp, vp, vp]),
+        "moe_router_backward": (ip, [P(moe_router_cfg), vp, vp, vp, ip, ll, ll, vp, ll, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -229,3 +244,13 @@ def moe_launch_info(plan):
 
 def moe_set_schedule(plan, consumer_ctas: int, mgb: int):
     check(lib().moe_set_schedule(plan, consumer_ctas, mgb), "moe_set_schedule")
+
+
+def moe_router(plan, cfg: moe_router_cfg, logits, dtype, n, ld, bias, ids, w, stream):
+    check(lib().moe_router(plan, ctypes.byref(cfg), logits, dtype, n, ld, bias, ids, w, stream),
+          "moe_router")
+
+
+def moe_router_backward(cfg: moe_router_cfg, d_w, logits, ids, dtype, n, ld, d_logits, ld_d, stream):
+    check(lib().moe_router_backward(ctypes.byref(cfg), d_w, logits, ids, dtype, n, ld, d_logits,
+                                    ld_d, stream), "moe_router_backward")

@@ -54,6 +54,10 @@ struct moe_plan {
 
 namespace moe {
 
+// router.cu: moe_router without a plan.
+int router_forward(const moe_router_cfg* cfg, const void* logits, int dtype, long long n, long long ld,
+                   const float* bias, int32_t* ids, float* w, cudaStream_t s);
+
 int dims_from_cfg(const moe_cfg* c, Dims* d) {
   if (c == nullptr || d == nullptr) return MOE_ERR_ARG;
   if (c->W < 1 || c->W > MOE_MAX_RANKS || c->L < 1 || c->L > 256) return MOE_ERR_ARG;
@@ -375,6 +379,21 @@ int moe_route(moe_plan* p, const float* logits, const int32_t* forced, int32_t* 
   const DevPlan dp = dev_plan(p);
   tstart(p, kTRoute, s);
   CUDA_TRY(launch_route(dp, logits, forced, ids, w, s));
+  tstop(p, kTRoute, s);
+  p->gate_marked = false;
+  return MOE_OK;
+}
+
+int moe_router(moe_plan* p, const moe_router_cfg* cfg, const void* logits, int dtype, long long n,
+               long long ld, const float* bias, int32_t* ids, float* w, moe_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p == nullptr) return router_forward(cfg, logits, dtype, n, ld, bias, ids, w, s);
+  if (cfg == nullptr || cfg->E != p->d.E || cfg->topk != p->d.k || n != (long long)p->d.W * p->d.T ||
+      !aligned16(ids) || !aligned16(w))
+    return MOE_ERR_ARG;
+  tstart(p, kTRoute, s);
+  const int rc = router_forward(cfg, logits, dtype, n, ld, bias, ids, w, s);
+  if (rc != MOE_OK) return rc;
   tstop(p, kTRoute, s);
   p->gate_marked = false;
   return MOE_OK;

@@ -1,0 +1,153 @@
+"""The operators of a transformer block around the routed experts, on torch tensors.
+
+route_experts, layer_norm and linear with their backward passes: argument checks and
+output allocation over the C ABI; every computation is a launch of the library's
+kernels. A matrix is a tensor whose last dimension is contiguous and whose other
+dimensions are one run of rows (any 2-D tensor with a row stride; more dimensions as
+`view` can join them).
+
+Every call is asynchronous on `stream` (default: the current one) and may be captured
+into a CUDA graph after a first call. Outputs are allocated on that stream. Inputs
+written on another stream must be complete before it (an event or a synchronize) and
+stay alive until the call has run there.
+"""
+from __future__ import annotations
+
+import functools
+
+import torch
+
+from . import capi
+
+_DTYPES = {torch.bfloat16: capi.MOE_BF16, torch.float16: capi.MOE_FP16,
+           torch.float32: capi.MOE_FP32}
+_SCORES = {"softmax": capi.MOE_SCORE_SOFTMAX, "sigmoid": capi.MOE_SCORE_SIGMOID}
+
+
+class _Launch:
+    """The device and the stream of a call: its outputs are allocated and its kernels
+    enqueued there."""
+
+    __slots__ = ("handle", "guards")
+
+    def __init__(self, tensor, stream):
+        dev = tensor.device
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {dev}")
+        self.guards = ()
+        if dev.index != torch.cuda.current_device():
+            self.guards = (torch.cuda.device(dev),)
+        if stream is None:
+            self.handle = torch.cuda.current_stream(dev).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        elif stream.device != dev:
+            raise ValueError(f"stream of {stream.device} for tensors of {dev}")
+        self.handle = stream.cuda_stream
+        self.guards += (torch.cuda.stream(stream),)
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _dtype(t, what, allowed=None):
+    d = _DTYPES.get(t.dtype)
+    if d is None or (allowed is not None and t.dtype not in allowed):
+        names = ", ".join(str(a) for a in (allowed or _DTYPES))
+        raise ValueError(f"{what} has type {t.dtype}: expected {names}")
+    return d
+
+
+def _rows(t, what, cols=None, device=None):
+    """(rows, cols, leading dimension) of a matrix."""
+    if t.dim() == 2:  # the common case, without a view
+        m = t
+    elif t.dim() == 1:
+        m = t[None]
+    else:
+        try:
+            m = t.view(-1, t.shape[-1]) if t.dim() else None
+        except RuntimeError:
+            m = None
+    n, c = m.shape if m is not None else (0, 0)
+    if m is None or (c > 1 and m.stride(1) != 1) or (n > 1 and m.stride(0) < c):
+        raise ValueError(f"{what} must be rows of contiguous elements, got shape "
+                         f"{tuple(t.shape)} and strides {t.stride()}")
+    if cols is not None and c != cols:
+        raise ValueError(f"{what} has rows of {c} elements: expected {cols}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}: expected {device}")
+    return n, c, (m.stride(0) if n > 1 else c)
+
+
+def _vector(t, what, size, dtypes, device):
+    if t.shape != (size,) or not t.is_contiguous() or t.dtype not in dtypes or t.device != device:
+        raise ValueError(f"{what} must be {size} contiguous elements of "
+                         f"{', '.join(str(d) for d in dtypes)} on {device}, got {tuple(t.shape)} "
+                         f"of {t.dtype} on {t.device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# ------------------------------------------------------------------------------ routing
+@functools.lru_cache(maxsize=256)
+def router_cfg(E, topk, score="softmax", groups=1, topk_groups=1, group_top=1, renorm=False,
+               scale=1.0) -> capi.moe_router_cfg:
+    """The C configuration of a router; its limits are checked by the call that takes it."""
+    if score not in _SCORES:
+        raise ValueError(f"score {score!r}: expected one of {', '.join(_SCORES)}")
+    return capi.moe_router_cfg(E, topk, _SCORES[score], groups, topk_groups, group_top,
+                               int(bool(renorm)), scale)
+
+
+def route_experts(logits, topk, score="softmax", bias=None, groups=1, topk_groups=1, group_top=1,
+                  renorm=False, scale=1.0, stream=None):
+    """The topk experts of every token and their weights, from scores logits [..., E].
+
+    s = softmax or sigmoid of the logits; c = s + bias; of `groups` groups of consecutive
+    experts the topk_groups with the largest sums of their group_top (1 or 2) largest c
+    stay, and of their experts the topk with the largest c (equal: lower id). The weights
+    are the s of the chosen experts, divided by their sum with renorm, times scale.
+    Returns (ids int32 [..., topk], weights fp32 [..., topk]). bias: fp32 [E], used for
+    the choice alone. Masked experts have logits of -inf; a token whose chosen experts are
+    all masked has weights 0. The choice is that of 64-bit arithmetic."""
+    n, E, ld = _rows(logits, "logits")
+    dt = _dtype(logits, "logits")
+    if bias is not None:
+        _vector(bias, "bias", E, (torch.float32,), logits.device)
+    cfg = router_cfg(E, topk, score, groups, topk_groups, group_top, renorm, scale)
+    with _Launch(logits, stream) as s:
+        shape = (*logits.shape[:-1], topk)
+        ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        w = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        capi.moe_router(None, cfg, logits.data_ptr(), dt, n, ld, _ptr(bias), ids.data_ptr(),
+                        w.data_ptr(), s)
+    return ids, w
+
+
+def route_experts_backward(d_w, logits, ids, score="softmax", renorm=False, scale=1.0, stream=None):
+    """The gradient of the logits [..., E], in their type, from the gradient d_w [..., topk]
+    of the weights, for the logits and ids of a route_experts call with this score, renorm
+    and scale. The choice, and so the bias and the groups, has no gradient."""
+    n, E, ld = _rows(logits, "logits")
+    dt = _dtype(logits, "logits")
+    for t, what, dtype in ((ids, "ids", torch.int32), (d_w, "d_w", torch.float32)):
+        if (t.dtype != dtype or t.shape[:-1] != logits.shape[:-1] or not t.is_contiguous() or
+                t.shape[-1:] != ids.shape[-1:] or t.device != logits.device):
+            raise ValueError(f"{what} must be contiguous {dtype} of shape [..., topk] beside the "
+                             f"logits, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+    cfg = router_cfg(E, ids.shape[-1], score, 1, 1, 1, renorm, scale)
+    with _Launch(logits, stream) as s:
+        d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        capi.moe_router_backward(cfg, d_w.data_ptr(), logits.data_ptr(), ids.data_ptr(), dt, n, ld,
+                                 d.data_ptr(), E, s)
+    return d

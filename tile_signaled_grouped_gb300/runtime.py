@@ -82,6 +82,25 @@ class ExpertCombine:
                        self.ids.data_ptr(), self.w.data_ptr(), _stream_handle(stream))
         return self.ids, self.w
 
+    def route_experts(self, logits, router, bias=None, stream=None):
+        """Routing by a router's own rule (scores, balance bias, groups, renormalised
+        weights): ids and weights of the layer's tokens, for plan_build() and scale().
+
+        logits: [W, T, E] (or [W*T, E], rows may be strided) bf16, fp16 or fp32; router:
+        an ops.router_cfg with the layer's E and topk; bias: None or [E] fp32."""
+        from . import ops
+
+        n, E, ld = ops._rows(logits, "logits")
+        if E != self.W * self.L or n != self.W * self.T:
+            raise ValueError(f"logits hold {n} rows of {E}: expected {self.W * self.T} rows of "
+                             f"{self.W * self.L}")
+        if bias is not None:
+            ops._vector(bias, "bias", E, (torch.float32,), logits.device)
+        capi.moe_router(self.plan, router, logits.data_ptr(), ops._dtype(logits, "logits"), n, ld,
+                        None if bias is None else bias.data_ptr(), self.ids.data_ptr(),
+                        self.w.data_ptr(), _stream_handle(stream))
+        return self.ids, self.w
+
     def gate(self, x, w_router, forced_ids=None, stream=None, logits_out=None, splits=0):
         """Router scores of the token rows and their routing, in one kernel.
 
