@@ -411,6 +411,42 @@ int moe_router_backward(const moe_router_cfg *cfg, const float *d_w, const void 
                         const int32_t *ids, int dtype, long long n, long long ld,
                         void *d_logits, long long ld_d, moe_stream_t stream);
 
+/* Layer norm of n rows of D elements, forward and backward. */
+typedef struct moe_norm_args {
+  long long n;      /* rows */
+  int D;            /* elements of a row, 1..2^24 */
+  int dtype;        /* enum moe_dtype of the matrices */
+  int wtype;        /* of w, b, dw and db: dtype or MOE_FP32 */
+  float eps;        /* >= 0, finite (forward) */
+  const void *x;    /* forward: in [n][D] */
+  const void *r;    /* forward: in [n][D], the residual stream, or NULL */
+  const void *w;    /* in [D], or NULL: ones */
+  const void *b;    /* forward: in [D], or NULL: zeros */
+  void *y;          /* forward: out [n][D] */
+  void *z;          /* forward: out [n][D], x + r, or NULL; backward: in, the normalised rows */
+  float *mean;      /* [n]: forward: out or NULL; backward: in */
+  float *rstd;      /* [n]: forward: out or NULL; backward: in */
+  const void *dy;   /* backward: in [n][D], gradient of y */
+  const void *dz;   /* backward: in [n][D], gradient of z from elsewhere, or NULL */
+  void *dx;         /* backward: out [n][D], gradient of x (and of r) */
+  void *dw;         /* backward: out [D] or NULL */
+  void *db;         /* backward: out [D] or NULL */
+  long long ld_x, ld_r, ld_y, ld_z, ld_dy, ld_dz, ld_dx;
+} moe_norm_args;
+
+/* z = x + r, y = (z - mean) * rstd * w + b with mean and rstd = 1 / sqrt(variance + eps)
+ * of each row of z (fp32; the variance is the mean squared distance). y, and z where it is
+ * stored, are rounded once from fp32. */
+int moe_layer_norm(const moe_norm_args *args, moe_stream_t stream);
+
+/* dx = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dz with g = dy * w and
+ * xhat = (z - mean) * rstd; dw = sum over rows of dy * xhat; db = sum over rows of dy.
+ * workspace: at least moe_layer_norm_workspace(n, D) bytes (pure host arithmetic), used
+ * until the call has run on the stream. The sums are added in a fixed order. */
+size_t moe_layer_norm_workspace(long long n, int D);
+int moe_layer_norm_backward(const moe_norm_args *args, void *workspace, size_t workspace_bytes,
+                            moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

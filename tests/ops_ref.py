@@ -83,3 +83,62 @@ def weight_tolerance(l, k):
     f = np.where(np.isfinite(l), l, np.nan)
     span = float(np.nanmax(f) - np.nanmin(f)) if np.isfinite(l).any() else 0.0
     return U32 * (2 * span + 4 + 4 + 37 + 5 + 8)
+
+
+# ---------------------------------------------------------------------------- layer norm
+def layer_norm(x, w, b, eps, r=None):
+    """(y, z, mean, rstd) in float64."""
+    z = x if r is None else x + r
+    mean = z.mean(axis=1)
+    d = z - mean[:, None]
+    rstd = 1.0 / np.sqrt((d * d).mean(axis=1) + eps)
+    y = d * rstd[:, None]
+    y = y if w is None else y * w
+    return (y if b is None else y + b), z, mean, rstd
+
+
+def layer_norm_backward(dy, z, w, mean, rstd, dz=None):
+    """(dx, dw, db) in float64."""
+    xhat = (z - mean[:, None]) * rstd[:, None]
+    g = dy if w is None else dy * w
+    dx = rstd[:, None] * (g - g.mean(axis=1, keepdims=True) -
+                          xhat * (g * xhat).mean(axis=1, keepdims=True))
+    return (dx if dz is None else dx + dz), (dy * xhat).sum(axis=0), dy.sum(axis=0)
+
+
+def chain(D):
+    """Additions that one value passes through in a sum of D: at most 32 in a thread (or D /
+    1024 and a vector in the long-row kernels) and 10 across the warps of a CTA."""
+    return 32 + 10 + D / 1024 + 8
+
+
+def layer_norm_tolerance(x, w, b, eps, r=None):
+    """Bounds of the fp32 errors of (y, z, mean, rstd), before y and z are rounded."""
+    y, z, mean, rstd = layer_norm(x, w, b, eps, r)
+    c, D = chain(x.shape[1]), x.shape[1]
+    ez = U32 * np.abs(z) if r is not None else np.zeros_like(z)
+    em = (c + 2) * U32 * np.abs(z).mean(axis=1) + ez.mean(axis=1)
+    d = np.abs(z - mean[:, None])
+    ed = ez + em[:, None] + U32 * d
+    # var: each square moves by 2 d ed + ed^2; the sum by c roundings; sqrt halves it.
+    ev = (2 * d * ed + ed * ed).mean(axis=1) + (c + 3) * U32 * (d * d).mean(axis=1)
+    rel = 0.5 * ev * rstd * rstd * (1 + ev * rstd * rstd) + 4 * U32
+    aw = 1.0 if w is None else np.abs(w)
+    ab = 0.0 if b is None else np.abs(b)
+    ey = aw * (ed * rstd[:, None] * (1 + rel[:, None]) + d * rstd[:, None] * (rel[:, None] + 3 * U32))
+    return ey + U32 * (np.abs(y) + ab), ez, em + U32 * np.abs(mean), rel * rstd
+
+
+def layer_norm_backward_tolerance(dy, z, w, mean, rstd, dz=None):
+    """Bounds of the fp32 errors of (dx, dw, db), before they are rounded."""
+    c, n = chain(z.shape[1]), z.shape[0]
+    xhat = np.abs((z - mean[:, None]) * rstd[:, None])
+    g = np.abs(dy) if w is None else np.abs(dy * w)
+    m1, m2 = g.mean(axis=1, keepdims=True), (g * xhat).mean(axis=1, keepdims=True)
+    ex = rstd[:, None] * U32 * (4 * g + (c + 6) * m1 + (c + 12) * xhat * m2)
+    if dz is not None:
+        ex = ex + 2 * U32 * np.abs(dz)
+    # Rows: n / 304 of a thread (at least 152 CTAs where there are that many rows), eight
+    # row groups of a CTA, 304 / 8 of the CTAs, and eight warps.
+    rows = n / 152 + 8 + 38 + 8 + 4
+    return ex, rows * U32 * (np.abs(dy) * xhat).sum(axis=0), rows * U32 * np.abs(dy).sum(axis=0)

@@ -98,3 +98,76 @@ def test_route_reference_gradient_is_the_difference(score, renorm):
     d = R.route_backward(dw, l, ids, score, renorm, 2.5)
     want = differences(lambda v: R.weights(v, ids, score, renorm, 2.5), l, dw)
     assert np.abs(d - want).max() < 1e-8
+
+
+# ---------------------------------------------------------------------------- layer norm
+def norm_args(**kw):
+    base = dict(n=1, D=8, dtype=capi.MOE_BF16, wtype=capi.MOE_FP32, eps=1e-5, x=64, w=64, b=64, y=64,
+                z=64, mean=64, rstd=64, dy=64, dx=64, dw=64, db=64, ld_x=8, ld_r=8, ld_y=8, ld_z=8,
+                ld_dy=8, ld_dz=8, ld_dx=8)
+    base.update(kw)
+    return capi.moe_norm_args(**base)
+
+
+NORM_BOTH = [dict(n=-1), dict(n=1 << 32), dict(D=0), dict(D=(1 << 24) + 1), dict(dtype=3),
+             dict(dtype=-1), dict(wtype=capi.MOE_FP16), dict(dtype=capi.MOE_FP32, wtype=capi.MOE_BF16),
+             dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(w=66), dict(z=65),
+             dict(ld_z=7), dict(mean=66), dict(rstd=65)]
+
+
+@pytest.mark.parametrize("bad", NORM_BOTH + [dict(x=None), dict(x=65), dict(ld_x=7), dict(y=None),
+                                             dict(ld_y=7), dict(b=65), dict(r=65), dict(r=64, ld_r=7)])
+def test_layer_norm_refuses_arguments(bad):
+    assert capi.lib().moe_layer_norm(ctypes.byref(norm_args(**bad)), None) == ARG
+
+
+@pytest.mark.parametrize("bad", NORM_BOTH + [
+    dict(z=None), dict(dy=None), dict(dy=65), dict(ld_dy=7), dict(dx=None), dict(ld_dx=7),
+    dict(mean=None), dict(rstd=None), dict(dz=65), dict(dz=64, ld_dz=7), dict(dw=66), dict(db=66)])
+def test_layer_norm_backward_refuses_arguments(bad):
+    assert capi.lib().moe_layer_norm_backward(ctypes.byref(norm_args(**bad)), 64, 1 << 40, None) == ARG
+
+
+def test_layer_norm_backward_refuses_workspaces():
+    lib = capi.lib()
+    a = ctypes.byref(norm_args(n=10))
+    size = capi.moe_layer_norm_workspace(10, 8)
+    assert size >= 10 * 2 * 8 * 4
+    assert lib.moe_layer_norm_backward(a, None, size, None) == ARG
+    assert lib.moe_layer_norm_backward(a, 66, size, None) == ARG
+    assert lib.moe_layer_norm_backward(a, 64, size - 1, None) == capi.MOE_ERR_WORKSPACE
+    assert lib.moe_layer_norm(None, None) == ARG
+    assert lib.moe_layer_norm_backward(None, 64, size, None) == ARG
+    assert lib.moe_layer_norm(ctypes.byref(norm_args(n=0, x=None, y=None)), None) == 0
+    assert capi.moe_layer_norm_workspace(0, 8) == 0
+
+
+def test_layer_norm_refuses_tensors():
+    x, w = torch.zeros(4, 16), torch.ones(16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.layer_norm(x, w)
+    for bad, match in ((dict(x=x.double()), "type"), (dict(weight=torch.ones(8)), "weight"),
+                       (dict(weight=w.half()), "weight"), (dict(bias=torch.ones(16, 1)), "bias"),
+                       (dict(x=x.half(), weight=w, bias=w.half()), "differ"),
+                       (dict(residual=x[:2]), "residual"), (dict(residual=x.half()), "residual"),
+                       (dict(x=torch.zeros(16, 4).t(), weight=torch.ones(16)), "rows"),
+                       (dict(x=torch.tensor(1.0)), "rows")):
+        with pytest.raises(ValueError, match=match):
+            ops.layer_norm(**{**dict(x=x, weight=w), **bad})
+    m = torch.zeros(4)
+    ok = dict(dy=x, z=x, weight=w, mean=m, rstd=m)
+    for bad, match in ((dict(dy=x.half()), "dy"), (dict(dy=x[:2]), "dy"), (dict(dz=x[:, :8]), "dz"),
+                       (dict(mean=m[:2]), "mean"), (dict(rstd=m.double()), "rstd"),
+                       (dict(weight=w.half()), "weight"), (dict(z=x.double()), "type")):
+        with pytest.raises(ValueError, match=match):
+            ops.layer_norm_backward(**{**ok, **bad})
+
+
+def test_layer_norm_reference_gradient_is_the_difference():
+    rng = np.random.default_rng(5)
+    x, w, b, dy = (rng.normal(size=s) for s in ((3, 10), (10,), (10,), (3, 10)))
+    _, z, mean, rstd = R.layer_norm(x, w, b, 1e-3)
+    dx, dw, db = R.layer_norm_backward(dy, z, w, mean, rstd)
+    assert np.abs(dx - differences(lambda v: R.layer_norm(v, w, b, 1e-3)[0], x, dy)).max() < 1e-8
+    assert np.abs(dw - differences(lambda v: R.layer_norm(x, v, b, 1e-3)[0], w, dy)).max() < 1e-8
+    assert np.abs(db - differences(lambda v: R.layer_norm(x, w, v, 1e-3)[0], b, dy)).max() < 1e-8

@@ -50,6 +50,16 @@ class moe_router_cfg(ctypes.Structure):
     ]
 
 
+class moe_norm_args(ctypes.Structure):
+    _fields_ = (
+        [("n", ctypes.c_longlong), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+         ("wtype", ctypes.c_int), ("eps", ctypes.c_float)]
+        + [(f, ctypes.c_void_p) for f in ("x", "r", "w", "b", "y", "z", "mean", "rstd", "dy", "dz",
+                                          "dx", "dw", "db")]
+        + [(f, ctypes.c_longlong) for f in ("ld_x", "ld_r", "ld_y", "ld_z", "ld_dy", "ld_dz",
+                                            "ld_dx")])
+
+
 def _parse_enums():
     """Enum constants of the header (MOE_OK, MOE_PLAN_*, MOE_RANK_*, ...)."""
     text = open(HEADER).read()
@@ -107,6 +117,9 @@ def load():
         "moe_launch_info": (ip, [vp, P(ip), P(ip), P(ip), P(ip)]),
         "moe_set_schedule": (ip, [vp, ip, ip]),
         "moe_router": (ip, [vp, P(moe_router_cfg), vp, ip, ll, ll, vp, vp, vp, vp]),
+        "moe_layer_norm": (ip, [P(moe_norm_args), vp]),
+        "moe_layer_norm_workspace": (sz, [ll, ip]),
+        "moe_layer_norm_backward": (ip, [P(moe_norm_args), vp, sz, vp]),
         "moe_router_backward": (ip, [P(moe_router_cfg), vp, vp, vp, ip, ll, ll, vp, ll, vp]),
     }
     for name, (res, args) in sig.items():
@@ -254,3 +267,16 @@ def moe_router(plan, cfg: moe_router_cfg, logits, dtype, n, ld, bias, ids, w, st
 def moe_router_backward(cfg: moe_router_cfg, d_w, logits, ids, dtype, n, ld, d_logits, ld_d, stream):
     check(lib().moe_router_backward(ctypes.byref(cfg), d_w, logits, ids, dtype, n, ld, d_logits,
                                     ld_d, stream), "moe_router_backward")
+
+
+def moe_layer_norm(args: moe_norm_args, stream):
+    check(lib().moe_layer_norm(ctypes.byref(args), stream), "moe_layer_norm")
+
+
+def moe_layer_norm_workspace(n: int, D: int) -> int:
+    return lib().moe_layer_norm_workspace(n, D)
+
+
+def moe_layer_norm_backward(args: moe_norm_args, workspace, workspace_bytes, stream):
+    check(lib().moe_layer_norm_backward(ctypes.byref(args), workspace, workspace_bytes, stream),
+          "moe_layer_norm_backward")

@@ -151,3 +151,78 @@ def route_experts_backward(d_w, logits, ids, score="softmax", renorm=False, scal
         capi.moe_router_backward(cfg, d_w.data_ptr(), logits.data_ptr(), ids.data_ptr(), dt, n, ld,
                                  d.data_ptr(), E, s)
     return d
+
+
+# --------------------------------------------------------------------------- layer norm
+def _norm_params(what, t, x, D):
+    if t is not None:
+        _vector(t, what, D, (x.dtype, torch.float32), x.device)
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, residual=None, stats=False, stream=None):
+    """(y, z, mean, rstd): z = x + residual and y = (z - mean) * rstd * weight + bias, with
+    the mean and rstd = 1 / sqrt(variance + eps) of each row of z.
+
+    x, residual: [..., D] bf16, fp16 or fp32; weight, bias: [D] of that type or both fp32,
+    or None. y and z have x's type and are contiguous; z is x itself without a residual.
+    mean and rstd (fp32 [...]) are returned with stats, for layer_norm_backward, else None."""
+    n, D, ld = _rows(x, "x")
+    dt = _dtype(x, "x")
+    _norm_params("weight", weight, x, D)
+    _norm_params("bias", bias, x, D)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError(f"weight and bias differ in type: {weight.dtype} and {bias.dtype}")
+    p = weight if weight is not None else bias
+    ld_r = 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError(f"residual must be {tuple(x.shape)} of {x.dtype}, got "
+                             f"{tuple(residual.shape)} of {residual.dtype}")
+        ld_r = _rows(residual, "residual", D, x.device)[2]
+    with _Launch(x, stream) as s:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        z = torch.empty_like(y) if residual is not None else None
+        mean = rstd = None
+        if stats:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(mean)
+        capi.moe_layer_norm(capi.moe_norm_args(
+            n, D, dt, dt if p is None else _DTYPES[p.dtype], eps, x.data_ptr(), _ptr(residual),
+            _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(z), _ptr(mean), _ptr(rstd), None, None,
+            None, None, None, ld, ld_r, D, D), s)
+    return y, (x if z is None else z), mean, rstd
+
+
+def layer_norm_backward(dy, z, weight, mean, rstd, dz=None, bias=True, stream=None):
+    """(dx, dweight, dbias) of layer_norm from the gradient dy of y, for the z, mean and
+    rstd that it returned. dz: the gradient of z from elsewhere (the residual stream), added
+    to dx, which is the gradient of x and of the residual alike. dweight and dbias have the
+    weight's type (z's if weight is None, and no dweight then); dbias is None without bias."""
+    n, D, ld_z = _rows(z, "z")
+    dt = _dtype(z, "z")
+    _norm_params("weight", weight, z, D)
+    ld = {"dz": 0}
+    for t, what in ((dy, "dy"), (dz, "dz")):
+        if t is None and what == "dz":
+            continue
+        if t.shape != z.shape or t.dtype != z.dtype:
+            raise ValueError(f"{what} must be {tuple(z.shape)} of {z.dtype}, got {tuple(t.shape)} of "
+                             f"{t.dtype}")
+        ld[what] = _rows(t, what, D, z.device)[2]
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        if (t.shape != z.shape[:-1] or t.dtype != torch.float32 or not t.is_contiguous() or
+                t.device != z.device):
+            raise ValueError(f"{what} must be contiguous fp32 of shape {tuple(z.shape[:-1])}, got "
+                             f"{tuple(t.shape)} of {t.dtype}")
+    wt = z.dtype if weight is None else weight.dtype
+    with _Launch(z, stream) as s:
+        dx = torch.empty(z.shape, dtype=z.dtype, device=z.device)
+        dw = None if weight is None else torch.empty(D, dtype=wt, device=z.device)
+        db = torch.empty(D, dtype=wt, device=z.device) if bias else None
+        size = capi.moe_layer_norm_workspace(n, D)
+        work = torch.empty(size, dtype=torch.uint8, device=z.device)
+        capi.moe_layer_norm_backward(capi.moe_norm_args(
+            n, D, dt, _DTYPES[wt], 0.0, None, None, _ptr(weight), None, None, z.data_ptr(),
+            mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), _ptr(dz), dx.data_ptr(), _ptr(dw),
+            _ptr(db), 0, 0, 0, ld_z, ld["dy"], ld["dz"], D), work.data_ptr(), size, s)
+    return dx, dw, db
