@@ -447,6 +447,54 @@ size_t moe_layer_norm_workspace(long long n, int D);
 int moe_layer_norm_backward(const moe_norm_args *args, void *workspace, size_t workspace_bytes,
                             moe_stream_t stream);
 
+enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU,
+  MOE_ACT_GELU,      /* 0.5 z (1 + erf(z / sqrt(2))) */
+  MOE_ACT_GELU_TANH, /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+  MOE_ACT_SILU       /* z / (1 + exp(-z)) */
+};
+
+/* Matrix product with an epilogue, forward and backward. dtype is MOE_BF16 or MOE_FP16. x
+ * and w (and dy, to be read in place) have 16-byte aligned bases and leading dimensions
+ * that are multiples of 8; M, N and K are any, and the other matrices may lie anywhere. */
+typedef struct moe_linear_args {
+  long long M, N, K; /* M >= 0, N >= 1, K >= 1 */
+  int dtype;         /* of x, w, r, z, dy and dx */
+  int ytype;         /* of y: dtype or MOE_FP32 */
+  int btype;         /* of b and db: dtype or MOE_FP32 */
+  int dwtype;        /* of dw: dtype or MOE_FP32 */
+  int act;           /* enum moe_act */
+  const void *x;     /* in [M][K] (backward: only for dw) */
+  const void *w;     /* in [N][K] (backward: only for dx) */
+  const void *b;     /* forward: in [N] or NULL */
+  const void *r;     /* forward: in [M][N], the residual, or NULL */
+  void *y;           /* forward: out [M][N] */
+  void *z;           /* forward: out [M][N] or NULL; backward: in, if act is not none */
+  const void *dy;    /* backward: in [M][N], gradient of y (and of r) */
+  void *dx;          /* backward: out [M][K] or NULL */
+  void *dw;          /* backward: out [N][K] or NULL */
+  void *db;          /* backward: out [N] or NULL */
+  long long ld_x, ld_w, ld_r, ld_y, ld_z, ld_dy, ld_dx, ld_dw;
+} moe_linear_args;
+
+/* z = x w^T + b, y = act(z) + r: fp32 sums, y and z rounded once from fp32. */
+int moe_linear(const moe_linear_args *args, moe_stream_t stream);
+
+/* dz = dy * act'(z); db = sum over rows of dz; dx = dz w; dw = dz^T x. The products take
+ * dz rounded to dtype, db takes it in fp32; all sums are fp32, in a fixed order.
+ * workspace: at least moe_linear_workspace(M, N) bytes (pure host arithmetic), 256-byte
+ * aligned, used until the call has run on the stream. */
+size_t moe_linear_workspace(long long M, long long N);
+int moe_linear_backward(const moe_linear_args *args, void *workspace, size_t workspace_bytes,
+                        moe_stream_t stream);
+
+/* The products' device waits are bounded; one that runs out sets a sticky status of the
+ * device (its results are void). Synchronises `stream` and reads it: *code is 0 or
+ * MOE_DEV_TIMEOUT, *detail the wait. */
+int moe_ops_status(moe_stream_t stream, int *code, int *detail);
+int moe_ops_status_clear(moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

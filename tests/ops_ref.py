@@ -142,3 +142,62 @@ def layer_norm_backward_tolerance(dy, z, w, mean, rstd, dz=None):
     # row groups of a CTA, 304 / 8 of the CTAs, and eight warps.
     rows = n / 152 + 8 + 38 + 8 + 4
     return ex, rows * U32 * (np.abs(dy) * xhat).sum(axis=0), rows * U32 * np.abs(dy).sum(axis=0)
+
+
+# -------------------------------------------------------------------------------- linear
+# On float64 torch tensors (any device), since the sizes are larger here.
+def _t():
+    import torch
+
+    return torch
+
+
+C0, C1 = math.sqrt(2.0 / math.pi), 0.044715
+
+
+def act(z, kind):
+    t = _t()
+    if kind == "relu":
+        return t.where(z > 0, z, t.zeros_like(z))
+    if kind == "gelu":
+        return 0.5 * z * t.special.erfc(-z * math.sqrt(0.5))
+    if kind == "gelu_tanh":
+        return 0.5 * z * (1 + t.tanh(C0 * (z + C1 * z ** 3)))
+    if kind == "silu":
+        return z / (1 + t.exp(-z))
+    return z
+
+
+def act_grad(z, kind):
+    t = _t()
+    if kind == "relu":
+        return (z > 0).to(z.dtype)
+    if kind == "gelu":
+        return 0.5 * t.special.erfc(-z * math.sqrt(0.5)) + z * t.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if kind == "gelu_tanh":
+        th = t.tanh(C0 * (z + C1 * z ** 3))
+        return 0.5 * (1 + th) + 0.5 * z * (1 - th * th) * C0 * (1 + 3 * C1 * z * z)
+    if kind == "silu":
+        s = 1 / (1 + t.exp(-z))
+        return s * (1 + z * (1 - s))
+    return t.ones_like(z)
+
+
+def act_error(z, kind):
+    """Absolute fp32 errors of act(z) and act'(z). The fast exponential is within 2 + 1.2 |v|
+    steps of its argument v, the fast division within 2, erff within 2; the argument itself
+    carries four roundings."""
+    v = z.abs()
+    if kind == "gelu_tanh":
+        v = 2 * C0 * (v + C1 * v ** 3)
+    if kind in ("none", "relu"):
+        return 0 * v, 0 * v
+    v = v.clamp(max=45.0)  # beyond, the sigmoid is 0 or 1
+    steps = 32 + 16 * v
+    return act(z, kind).abs() * steps * U32 + 8 * U32 * z.abs(), steps * U32 * (1 + z.abs().clamp(max=30.0))
+
+
+def product_error(a, b, k):
+    """Of a @ b with k fp32 additions in any order: two half steps each, for sums that the
+    tensor cores cut off rather than round."""
+    return 2 * (k + 24) * U32 * (a.abs() @ b.abs())

@@ -171,3 +171,77 @@ def test_layer_norm_reference_gradient_is_the_difference():
     assert np.abs(dx - differences(lambda v: R.layer_norm(v, w, b, 1e-3)[0], x, dy)).max() < 1e-8
     assert np.abs(dw - differences(lambda v: R.layer_norm(x, v, b, 1e-3)[0], w, dy)).max() < 1e-8
     assert np.abs(db - differences(lambda v: R.layer_norm(x, w, v, 1e-3)[0], b, dy)).max() < 1e-8
+
+
+# -------------------------------------------------------------------------------- linear
+def linear_args(**kw):
+    base = dict(M=2, N=8, K=8, dtype=capi.MOE_BF16, ytype=capi.MOE_FP32, btype=capi.MOE_FP32,
+                dwtype=capi.MOE_FP32, act=capi.MOE_ACT_SILU, x=64, w=64, b=64, y=64, z=64, dy=64,
+                dx=64, dw=64, db=64, ld_x=8, ld_w=8, ld_r=8, ld_y=8, ld_z=8, ld_dy=8, ld_dx=8, ld_dw=8)
+    base.update(kw)
+    return capi.moe_linear_args(**base)
+
+
+LINEAR_BOTH = [dict(M=-1), dict(M=1 << 31), dict(N=0), dict(N=1 << 31), dict(K=0), dict(K=1 << 31),
+               dict(dtype=capi.MOE_FP32), dict(dtype=-1), dict(btype=capi.MOE_FP16), dict(act=-1),
+               dict(act=5), dict(x=None), dict(x=72), dict(ld_x=12), dict(ld_x=0), dict(w=None),
+               dict(w=72), dict(ld_w=12), dict(ld_w=0), dict(z=65), dict(ld_z=7)]
+
+
+@pytest.mark.parametrize("bad", LINEAR_BOTH + [
+    dict(ytype=capi.MOE_FP16), dict(y=None), dict(y=66), dict(ld_y=7), dict(r=65), dict(r=64, ld_r=7),
+    dict(b=66)])
+def test_linear_refuses_arguments(bad):
+    assert capi.lib().moe_linear(ctypes.byref(linear_args(**bad)), None) == ARG
+
+
+@pytest.mark.parametrize("bad", LINEAR_BOTH + [
+    dict(dwtype=capi.MOE_FP16), dict(z=None), dict(dy=None), dict(dy=65), dict(ld_dy=7), dict(dx=65),
+    dict(ld_dx=7), dict(dw=66), dict(ld_dw=7), dict(db=66)])
+def test_linear_backward_refuses_arguments(bad):
+    assert capi.lib().moe_linear_backward(ctypes.byref(linear_args(**bad)), 256, 1 << 40, None) == ARG
+
+
+def test_linear_backward_refuses_workspaces():
+    lib = capi.lib()
+    a = ctypes.byref(linear_args())
+    size = capi.moe_linear_workspace(2, 8)
+    assert lib.moe_linear_backward(a, None, size, None) == ARG
+    assert lib.moe_linear_backward(a, 128, size, None) == ARG
+    assert lib.moe_linear_backward(a, 256, size - 1, None) == capi.MOE_ERR_WORKSPACE
+    assert lib.moe_linear(None, None) == ARG
+    assert lib.moe_linear_backward(None, 256, size, None) == ARG
+    assert lib.moe_linear(ctypes.byref(linear_args(M=0, x=None, y=None)), None) == 0
+    assert capi.moe_linear_workspace(0, 8) == 0
+
+
+def test_linear_refuses_tensors():
+    h = torch.bfloat16
+    x, w = torch.zeros(4, 16, dtype=h), torch.zeros(24, 16, dtype=h)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.linear(x, w)
+    for bad, match in ((dict(x=x.float()), "type"), (dict(weight=w.half()), "type"),
+                       (dict(weight=w[:, :8]), "weight"), (dict(weight=w[0]), "weight"),
+                       (dict(x=torch.zeros(4, 18, dtype=h)[:, :16]), "16 bytes"),
+                       (dict(x=torch.zeros(4, 32, dtype=h)[:, 4:20]), "16 bytes"),
+                       (dict(act="tanh"), "act"), (dict(bias=torch.zeros(16)), "bias"),
+                       (dict(bias=torch.zeros(24, dtype=torch.float16)), "bias"),
+                       (dict(out_dtype=torch.float16), "out_dtype"),
+                       (dict(residual=x), "residual"),
+                       (dict(residual=torch.zeros(4, 24)), "residual")):
+        with pytest.raises(ValueError, match=match):
+            ops.linear(**{**dict(x=x, weight=w), **bad})
+    dy = torch.zeros(4, 24, dtype=h)
+    for bad, match in ((dict(dy=x), "dy"), (dict(dy=dy.float()), "dy"), (dict(act="silu"), "z"),
+                       (dict(z=dy), "z"), (dict(z=dy[:2], act="silu"), "z"),
+                       (dict(bias=torch.float16), "bias"), (dict(dw_dtype=torch.float16), "dw_dtype")):
+        with pytest.raises(ValueError, match=match):
+            ops.linear_backward(**{**dict(dy=dy, x=x, weight=w), **bad})
+
+
+@pytest.mark.parametrize("kind", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_activation_reference_gradient_is_the_difference(kind):
+    z = torch.linspace(-7, 7, 141, dtype=torch.float64) + 0.013
+    h = 1e-5
+    d = (R.act(z + h, kind) - R.act(z - h, kind)) / (2 * h)
+    assert (R.act_grad(z, kind) - d).abs().max() < 1e-8

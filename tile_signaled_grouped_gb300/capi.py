@@ -60,6 +60,15 @@ class moe_norm_args(ctypes.Structure):
                                             "ld_dx")])
 
 
+class moe_linear_args(ctypes.Structure):
+    _fields_ = (
+        [(f, ctypes.c_longlong) for f in ("M", "N", "K")]
+        + [(f, ctypes.c_int) for f in ("dtype", "ytype", "btype", "dwtype", "act")]
+        + [(f, ctypes.c_void_p) for f in ("x", "w", "b", "r", "y", "z", "dy", "dx", "dw", "db")]
+        + [(f, ctypes.c_longlong) for f in ("ld_x", "ld_w", "ld_r", "ld_y", "ld_z", "ld_dy",
+                                            "ld_dx", "ld_dw")])
+
+
 def _parse_enums():
     """Enum constants of the header (MOE_OK, MOE_PLAN_*, MOE_RANK_*, ...)."""
     text = open(HEADER).read()
@@ -117,6 +126,11 @@ def load():
         "moe_launch_info": (ip, [vp, P(ip), P(ip), P(ip), P(ip)]),
         "moe_set_schedule": (ip, [vp, ip, ip]),
         "moe_router": (ip, [vp, P(moe_router_cfg), vp, ip, ll, ll, vp, vp, vp, vp]),
+        "moe_linear": (ip, [P(moe_linear_args), vp]),
+        "moe_linear_workspace": (sz, [ll, ll]),
+        "moe_linear_backward": (ip, [P(moe_linear_args), vp, sz, vp]),
+        "moe_ops_status": (ip, [vp, P(ip), P(ip)]),
+        "moe_ops_status_clear": (ip, [vp]),
         "moe_layer_norm": (ip, [P(moe_norm_args), vp]),
         "moe_layer_norm_workspace": (sz, [ll, ip]),
         "moe_layer_norm_backward": (ip, [P(moe_norm_args), vp, sz, vp]),
@@ -280,3 +294,26 @@ def moe_layer_norm_workspace(n: int, D: int) -> int:
 def moe_layer_norm_backward(args: moe_norm_args, workspace, workspace_bytes, stream):
     check(lib().moe_layer_norm_backward(ctypes.byref(args), workspace, workspace_bytes, stream),
           "moe_layer_norm_backward")
+
+
+def moe_linear(args: moe_linear_args, stream):
+    check(lib().moe_linear(ctypes.byref(args), stream), "moe_linear")
+
+
+def moe_linear_workspace(M: int, N: int) -> int:
+    return lib().moe_linear_workspace(M, N)
+
+
+def moe_linear_backward(args: moe_linear_args, workspace, workspace_bytes, stream):
+    check(lib().moe_linear_backward(ctypes.byref(args), workspace, workspace_bytes, stream),
+          "moe_linear_backward")
+
+
+def moe_ops_status(stream):
+    code, detail = ctypes.c_int(), ctypes.c_int()
+    check(lib().moe_ops_status(stream, ctypes.byref(code), ctypes.byref(detail)), "moe_ops_status")
+    return code.value, detail.value
+
+
+def moe_ops_status_clear(stream):
+    check(lib().moe_ops_status_clear(stream), "moe_ops_status_clear")

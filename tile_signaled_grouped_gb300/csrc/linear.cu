@@ -1,0 +1,717 @@
+// Matrix product with bias, activation and residual in its epilogue, and its backward
+// pass, on tcgen05.
+//
+//   forward   z = x W^T + b,  y = act(z) + r            x [M][K], W [N][K]
+//   backward  dz = dy act'(z),  db = sum over rows of dz
+//             dx = dz W  [M][K],   dW = dz^T x  [N][K]
+//
+// Every product is D[i][j] = sum_k A(i, k) B(j, k) with fp32 accumulators in TMEM; an
+// operand lies in memory with k innermost (K-major) or with i or j innermost (MN-major):
+//   forward  A = x (K),   B = W (K)        i = m, j = n, k = k
+//   dx       A = dz (K),  B = W (MN)       i = m, j = k, k = n
+//   dW       A = dz (MN), B = x (MN)       i = n, j = k, k = m
+// TMA stages 64 k-elements of both operands with the 128-byte swizzle, and the tensor
+// cores read either layout, so no operand is ever transposed in memory. The bounds of the
+// tensor maps fill with zeros what lies past M, N and K.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "moe_common.cuh"
+#include "ops_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr long long kWaitNs = 4000000000LL;  // bound of every device-side wait
+
+// The sticky device status of these kernels: [0] code, [1] detail (moe_ops_status).
+__device__ uint32_t g_status[4];
+
+// ------------------------------------------------------------------- activations
+__device__ __forceinline__ float fast_sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluC1 = 0.044715f;
+
+// act(z). 0.5 (1 + tanh u) is the sigmoid of 2u. The fast exponential and division are
+// within 1e-6, far below half a step of the 16-bit results (fp32 results: same bound).
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
+  if (ACT == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+  if (ACT == MOE_ACT_GELU_TANH) return z * fast_sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
+  if (ACT == MOE_ACT_SILU) return z * fast_sigmoid(z);
+  return z;
+}
+// act'(z). Past 30 the derivatives are 0 or 1 to the last bit, and z there would only make
+// infinities times zero; NaN stays.
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+  if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  z = z > 30.f ? 30.f : z < -30.f ? -30.f : z;
+  if (ACT == MOE_ACT_GELU)
+    return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) +
+           z * 0.3989422804014327f * __expf(-0.5f * z * z);
+  if (ACT == MOE_ACT_GELU_TANH) {
+    const float q = fast_sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
+    return q + z * q * (1.0f - q) * (2.0f * kGeluC0) * (1.0f + 3.0f * kGeluC1 * z * z);
+  }
+  if (ACT == MOE_ACT_SILU) {
+    const float q = fast_sigmoid(z);
+    return q * (1.0f + z * (1.0f - q));
+  }
+  return 1.f;
+}
+
+// ------------------------------------------------------------------- the epilogue
+struct Epilogue {
+  void* y;        // [I][ld_y] of ytype
+  void* z;        // [I][ld_z] of dtype, before the activation, or null
+  const void* r;  // [I][ld_r] of dtype or null
+  const void* b;  // [J] of btype or null
+  long long ld_y, ld_z, ld_r;
+  int dtype, ytype, btype, act;
+  bool vy, vz, vr, vb;  // rows (b) start on 16 bytes
+};
+
+// Eight elements of a row from column j: in one or two 16-byte accesses where `vec` and
+// all eight are inside, else one by one.
+__device__ __forceinline__ void load8(const void* p, int dtype, long long at, int n, bool vec, float (&f)[8]) {
+  if (vec && n >= 8) {
+    if (dtype == MOE_FP32) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      const float4 u = __ldg(q), v = __ldg(q + 1);
+      f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+      return;
+    }
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(p) + at));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (dtype == MOE_BF16) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = h.x;
+        f[2 * i + 1] = h.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = i < n ? load_as_f32(p, dtype, at + i) : 0.f;
+}
+__device__ __forceinline__ void store8(void* p, int dtype, long long at, int n, bool vec, const float (&f)[8]) {
+  if (vec && n >= 8) {
+    if (dtype == MOE_FP32) {
+      float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+      q[0] = make_float4(f[0], f[1], f[2], f[3]);
+      q[1] = make_float4(f[4], f[5], f[6], f[7]);
+      return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (dtype == MOE_BF16) {
+        w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+      } else {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<unsigned short*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) store_from_f32(p, dtype, at + i, f[i]);
+}
+
+template <int ACT>
+__device__ __forceinline__ void act8(float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = act_of<ACT>(v[i]);
+}
+
+// Eight sums of row i from column j, n of them inside the matrix, to the outputs.
+__device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, int n, float (&v)[8]) {
+  float t[8];
+  if (e.b != nullptr) {
+    load8(e.b, e.btype, j, n, e.vb, t);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += t[q];
+  }
+  if (e.z != nullptr) store8(e.z, e.dtype, i * e.ld_z + j, n, e.vz, v);
+  switch (e.act) {  // the same for the whole grid
+    case MOE_ACT_RELU: act8<MOE_ACT_RELU>(v); break;
+    case MOE_ACT_GELU: act8<MOE_ACT_GELU>(v); break;
+    case MOE_ACT_GELU_TANH: act8<MOE_ACT_GELU_TANH>(v); break;
+    case MOE_ACT_SILU: act8<MOE_ACT_SILU>(v); break;
+    default: break;
+  }
+  if (e.r != nullptr) {
+    load8(e.r, e.dtype, i * e.ld_r + j, n, e.vr, t);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += t[q];
+  }
+  store8(e.y, e.ytype, i * e.ld_y + j, n, e.vy, v);
+}
+
+// ------------------------------------------------------------------- tensor-core pieces
+// Shared-memory matrix descriptor of an MN-major operand stored by TMA in boxes of 64
+// elements (128 bytes, the swizzle span) x 64 k-rows: 8 KB from one box to the next,
+// 1024 bytes from 8 k-rows to the next 8.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(8192 >> 4) << 16;  // leading-dimension offset: the next 64 elements
+  d |= (uint64_t)(1024 >> 4) << 32;  // stride-dimension offset: the next 8 k
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// Instruction descriptor: 16-bit A and B of one type, fp32 accumulator, M x N.
+__device__ __forceinline__ uint32_t idesc_16bit(bool bf16, bool a_mn, bool b_mn, int M, int N) {
+  const uint32_t t = bf16 ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+constexpr int kTileI = 128;
+constexpr int kMaxStages = 8;
+constexpr int kABytes = kTileI * kBlockK * 2;  // 16 KB
+constexpr int kTileThreads = 256;
+
+struct GemmArgs {
+  CUtensorMap ta, tb;
+  Epilogue e;
+  int I, J, nk;       // nk: 64-element blocks of k
+  int bn;             // columns of a tile: 16, 32, 64, 128 or 256 (64 or more if B is MN-major)
+  int stages, splits; // splits: CTAs of a cluster that share a tile, each with a range of k
+  int tiles_i, box_a; // box_a: rows of A's box (K-major)
+  bool bf16;
+};
+
+struct TileSmem {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t done;
+  uint32_t tmem;
+  int abort;
+};
+
+size_t tile_smem_bytes(int bn, int stages) {
+  const size_t pipe = (size_t)stages * (kABytes + bn * 128);
+  const size_t dump = (size_t)kTileI * (bn + 4) * 4;
+  return 1024 + std::max(pipe, dump) + sizeof(TileSmem);
+}
+
+// One tile of 128 x bn for each cluster of `splits` CTAs, each of which sums its range of
+// k in its TMEM. The partial sums then meet in shared memory: every CTA adds a share of
+// the tile's elements from all of them, in the order of the ranks, and finishes it. Warp 0
+// loads, warp 1 issues the products, all eight warps empty TMEM.
+template <bool AMN, bool BMN>
+__global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_constant__ GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int b_bytes = a.bn * 128, stage_bytes = kABytes + b_bytes;
+  const size_t pipe = max((size_t)a.stages * stage_bytes, (size_t)kTileI * (a.bn + 4) * 4);
+  TileSmem& sm = *reinterpret_cast<TileSmem*>(base + pipe);
+  float* dump = reinterpret_cast<float*>(base);  // [128][bn + 4], once the products are done
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cols = a.bn < 32 ? 32 : a.bn;
+  const int rank = (int)(blockIdx.x % a.splits), tile = (int)(blockIdx.x / a.splits);
+  const int i0 = (tile % a.tiles_i) * kTileI, j0 = (tile / a.tiles_i) * a.bn;
+  const int k_lo = (int)((long long)a.nk * rank / a.splits);
+  const int k_hi = (int)((long long)a.nk * (rank + 1) / a.splits);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    mbar_init(&sm.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    sm.abort = 0;
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem, cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp == 0 && lane == 0) {
+    const uint32_t bytes = (AMN ? kABytes : a.box_a * 128) + b_bytes;
+    int issued = 0;
+    for (int kb = k_lo; kb < k_hi; ++kb, ++issued) {
+      const int st = issued % a.stages;
+      if (!mbar_wait_bounded(&sm.empty[st], ((issued / a.stages) & 1) ^ 1, &sm.abort, kWaitNs, g_status,
+                             0x01000000u))
+        break;
+      uint8_t* as = base + (size_t)st * stage_bytes;
+      uint8_t* bs = as + kABytes;
+      mbar_arrive_expect_tx(&sm.full[st], bytes);
+      if (AMN) {
+        tma_load_2d(as, &a.ta, &sm.full[st], i0, kb * kBlockK);
+        tma_load_2d(as + 8192, &a.ta, &sm.full[st], i0 + 64, kb * kBlockK);
+      } else {
+        tma_load_2d(as, &a.ta, &sm.full[st], kb * kBlockK, i0);
+      }
+      if (BMN) {
+        for (int c = 0; c < a.bn / 64; ++c)
+          tma_load_2d(bs + c * 8192, &a.tb, &sm.full[st], j0 + c * 64, kb * kBlockK);
+      } else {
+        tma_load_2d(bs, &a.tb, &sm.full[st], kb * kBlockK, j0);
+      }
+    }
+    if (*(volatile int*)&sm.abort) {  // the copies in flight land before the CTA leaves
+      volatile int never = 0;
+      for (int n = max(0, issued - a.stages); n < issued; ++n)
+        mbar_wait_bounded(&sm.full[n % a.stages], (n / a.stages) & 1, &never, kWaitNs, g_status,
+                          0x02000000u);
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_16bit(a.bf16, AMN, BMN, kTileI, a.bn);
+    for (int kb = k_lo, n = 0; kb < k_hi; ++kb, ++n) {
+      const int st = n % a.stages;
+      if (!mbar_wait_bounded(&sm.full[st], (n / a.stages) & 1, &sm.abort, kWaitNs, g_status, 0x03000000u))
+        break;
+      tc_fence_after();
+      const uint32_t as = smem_u32(base + (size_t)st * stage_bytes), bs = as + kABytes;
+#pragma unroll
+      for (int k = 0; k < kBlockK / 16; ++k)
+        tc_mma(tmem, AMN ? sdesc_mn_sw128(as + k * 2048) : sdesc_k_sw128(as + k * 32),
+               BMN ? sdesc_mn_sw128(bs + k * 2048) : sdesc_k_sw128(bs + k * 32), idesc,
+               (n | k) != 0 ? 1u : 0u);
+      tc_commit(&sm.empty[st]);
+    }
+    tc_commit(&sm.done);  // also after a wait that ran out: no product outlives the CTA
+  }
+  __syncwarp();
+  volatile int never = 0;
+  bool ok = mbar_wait_bounded(&sm.done, 0, &never, 2 * kWaitNs, g_status, 0x04000000u);
+  ok = ok && *(volatile int*)&sm.abort == 0;
+  tc_fence_after();
+
+  // TMEM to shared memory: warp w reads lanes 32 (w & 3).. of column half w >> 2.
+  const int rows = min(kTileI, a.I - i0);
+  const int pitch = a.bn + 4;
+  __syncthreads();  // every wait above is over: the pipeline's memory is free
+  {
+    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+    for (int c = half * 32; c < a.bn; c += 64) {
+      uint32_t v[32];
+      tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+      tmem_ld_wait();
+      if (row < rows && k_hi > k_lo) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 4)
+          if (c + x < a.bn)
+            *reinterpret_cast<uint4*>(dump + (size_t)row * pitch + c + x) =
+                make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (a.splits > 1) cluster_sync_all();
+  if (ok) {
+    const int chunks = a.bn / 8, total = rows * chunks;
+    for (int it = rank * kTileThreads + threadIdx.x; it < total; it += a.splits * kTileThreads) {
+      const int row = it / chunks, c = (it % chunks) * 8;
+      if (j0 + c >= a.J) continue;
+      const float* p = dump + (size_t)row * pitch + c;
+      float v[8];
+      if (a.splits == 1) {
+        const float4 s = *reinterpret_cast<const float4*>(p), t = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = s.x, v[1] = s.y, v[2] = s.z, v[3] = s.w, v[4] = t.x, v[5] = t.y, v[6] = t.z, v[7] = t.w;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = 0.f;
+        for (int r = 0; r < a.splits; ++r) {
+          const uint32_t at = map_shared(p, (uint32_t)r);
+          const float4 s = ld_cluster_v4(at), t = ld_cluster_v4(at + 16);
+          v[0] += s.x, v[1] += s.y, v[2] += s.z, v[3] += s.w;
+          v[4] += t.x, v[5] += t.y, v[6] += t.z, v[7] += t.w;
+        }
+      }
+      finish8(a.e, i0 + row, j0 + c, a.J - j0 - c, v);
+    }
+  }
+  __syncthreads();
+  if (a.splits > 1) cluster_sync_all();  // the others have read this CTA's sums
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, cols);
+}
+
+// ------------------------------------------------------------------- dz and db
+struct ActGradArgs {
+  const void* dy;
+  const void* z;  // null without an activation
+  void* dz;       // null: only the sums
+  float* part;    // [gridDim.y][N] column sums, or null
+  long long ld_dy, ld_z, ld_dz;
+  int M, N, dtype, rows;  // rows of a CTA
+  bool vdy, vz;           // rows start on 16 bytes (dz's always do)
+};
+
+// dz = dy act'(z) and its column sums: a thread takes eight columns of every eighth row of
+// the CTA's range, warp w row w, w + 8, ...; the eight warps' sums are added in order. dz
+// is rounded to the operands' type for the products; the sums take it unrounded. Bound by
+// the bytes of dy, z and dz.
+template <int ACT>
+__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
+  __shared__ float red[8][32][9];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = (blockIdx.x * 32 + lane) * 8;
+  const int n = a.N - j;
+  const int lo = blockIdx.y * a.rows, hi = min(a.M, lo + a.rows);
+  float s[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s[q] = 0.f;
+  if (n > 0) {
+    for (int i = lo + warp; i < hi; i += 8) {
+      float d[8];
+      load8(a.dy, a.dtype, (long long)i * a.ld_dy + j, n, a.vdy, d);
+      if (ACT != MOE_ACT_NONE) {
+        float z[8];
+        load8(a.z, a.dtype, (long long)i * a.ld_z + j, n, a.vz, z);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[q] *= act_grad<ACT>(z[q]);
+      }
+      if (a.dz != nullptr) store8(a.dz, a.dtype, (long long)i * a.ld_dz + j, n, true, d);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] += d[q];
+    }
+  }
+  if (a.part == nullptr) return;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) red[warp][lane][q] = s[q];
+  __syncthreads();
+  const int c = threadIdx.x;  // one of the CTA's 256 columns
+  if (blockIdx.x * 256 + c < a.N) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += red[w][c >> 3][c & 7];
+    a.part[(size_t)blockIdx.y * a.N + blockIdx.x * 256 + c] = v;
+  }
+}
+
+// db from the row ranges' sums: eight warps share the ranges, then their sums in order.
+__global__ void __launch_bounds__(256) bias_grad_kernel(const float* part, int parts, int N, int btype,
+                                                       void* db) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < N)
+    for (int r = warp; r < parts; r += 8) s += part[(size_t)r * N + c];
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < N) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += red[i][lane];
+    store_from_f32(db, btype, c, v);
+  }
+}
+
+// ------------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::atomic<void*> cached{nullptr};
+  void* fn = cached.load(std::memory_order_relaxed);
+  if (fn == nullptr) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    cached.store(fn, std::memory_order_relaxed);
+  }
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+}
+
+// Map of a row-major [rows][cols] matrix of 16-bit elements: boxes of box_rows x 64
+// columns, 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap* m, const void* p, bool bf16, long long rows, long long cols, long long ld,
+              int box_rows) {
+  const auto encode = encoder();
+  if (encode == nullptr) return false;
+  if (rows == 1) ld = (cols + 7) / 8 * 8;  // the stride of a single row is never used
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operand {
+  const void* p;
+  long long ld;
+  bool mn;  // MN-major: [k][i or j] in memory
+};
+
+constexpr size_t kSmemMax = 227 * 1024;
+
+template <bool AMN, bool BMN>
+cudaError_t launch_tile(const GemmArgs& a, int tiles, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};  // bit d: device d may use all of its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(linear_tile_kernel<AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kSmemMax);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * a.splits));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = tile_smem_bytes(a.bn, a.stages);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)a.splits, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_tile_kernel<AMN, BMN>, a);
+}
+
+// D[i][j] = sum_k A(i, k) B(j, k) through the epilogue.
+int gemm(const Operand& A, const Operand& B, int I, int J, long long K, bool bf16, const Epilogue& e,
+         int num_sms, cudaStream_t s) {
+  GemmArgs a;
+  a.e = e;
+  a.I = I;
+  a.J = J;
+  a.nk = (int)((K + kBlockK - 1) / kBlockK);
+  a.bf16 = bf16;
+  a.tiles_i = (I + kTileI - 1) / kTileI;
+  // The narrowest tile that still gives every SM one, between 64 and 256 columns.
+  a.bn = 256;
+  while (a.bn > 64 && (long long)a.tiles_i * ((J + a.bn - 1) / a.bn) < num_sms) a.bn /= 2;
+  if (!B.mn)
+    while (a.bn > 16 && a.bn / 2 >= J) a.bn /= 2;
+  const long long tiles = (long long)a.tiles_i * ((J + a.bn - 1) / a.bn);
+  a.splits = 1;
+  while (a.splits < 8 && tiles * a.splits * 2 <= num_sms && a.nk >= a.splits * 2 * 2) a.splits *= 2;
+  if (tiles * a.splits > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  a.stages = std::min<int>(kMaxStages, (int)((kSmemMax - 1024 - sizeof(TileSmem)) / (kABytes + a.bn * 128)));
+  a.box_a = std::min(kTileI, (I + 7) / 8 * 8);
+  const bool ok = (A.mn ? make_map(&a.ta, A.p, bf16, K, I, A.ld, kBlockK)
+                        : make_map(&a.ta, A.p, bf16, I, K, A.ld, a.box_a)) &&
+                  (B.mn ? make_map(&a.tb, B.p, bf16, K, J, B.ld, kBlockK)
+                        : make_map(&a.tb, B.p, bf16, J, K, B.ld, a.bn));
+  if (!ok) return MOE_ERR_CUDA;
+  const cudaError_t rc = A.mn   ? launch_tile<true, true>(a, (int)tiles, s)
+                         : B.mn ? launch_tile<false, true>(a, (int)tiles, s)
+                                : launch_tile<false, false>(a, (int)tiles, s);
+  if (rc != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+bool vec_rows(const void* p, long long ld, int dtype, long long rows) {
+  return aligned_to(p, 16) && (rows == 1 || ld * type_bytes(dtype) % 16 == 0);
+}
+
+int check_linear(const moe_linear_args* p) {
+  if (p == nullptr) return MOE_ERR_ARG;
+  if (p->dtype != MOE_BF16 && p->dtype != MOE_FP16) return MOE_ERR_ARG;
+  if (p->M < 0 || p->M > INT32_MAX / 2 || p->N < 1 || p->N > INT32_MAX / 2 || p->K < 1 ||
+      p->K > INT32_MAX / 2)
+    return MOE_ERR_ARG;
+  if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_SILU) return MOE_ERR_ARG;
+  if (p->btype != p->dtype && p->btype != MOE_FP32) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+// A matrix that the tensor maps read: rows on 16 bytes.
+bool check_operand(const void* q, long long ld, long long rows, long long cols) {
+  return q != nullptr && aligned_to(q, 16) && (rows <= 1 || (ld >= cols && ld % 8 == 0 && ld <= INT32_MAX));
+}
+bool check_matrix(const void* q, long long ld, long long rows, long long cols, int dtype, bool need) {
+  if (q == nullptr) return !need;
+  return aligned_to(q, (size_t)type_bytes(dtype)) && (rows <= 1 || (ld >= cols && ld <= INT32_MAX));
+}
+
+// Backward workspace: dz (rows padded to 16 bytes), then the column sums' parts.
+constexpr int kBiasParts = 256;  // row ranges of the column sums at most
+size_t dz_bytes(long long M, long long N) { return ((size_t)M * ((N + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+
+template <int ACT>
+void launch_act_grad(const ActGradArgs& a, dim3 grid, cudaStream_t s) {
+  act_grad_kernel<ACT><<<grid, 256, 0, s>>>(a);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_linear(const moe_linear_args* p, moe_stream_t stream) {
+  int rc = check_linear(p);
+  if (rc != MOE_OK) return rc;
+  if (p->ytype != p->dtype && p->ytype != MOE_FP32) return MOE_ERR_ARG;
+  if (p->M == 0) return MOE_OK;
+  if (!check_operand(p->x, p->ld_x, p->M, p->K) || !check_operand(p->w, p->ld_w, p->N, p->K) ||
+      !check_matrix(p->y, p->ld_y, p->M, p->N, p->ytype, true) ||
+      !check_matrix(p->z, p->ld_z, p->M, p->N, p->dtype, false) ||
+      !check_matrix(p->r, p->ld_r, p->M, p->N, p->dtype, false) ||
+      !aligned_to(p->b, (size_t)type_bytes(p->btype)))
+    return MOE_ERR_ARG;
+  int sms = 0;
+  rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  Epilogue e{};
+  e.y = p->y;
+  e.z = p->z;
+  e.r = p->r;
+  e.b = p->b;
+  e.ld_y = p->ld_y;
+  e.ld_z = p->ld_z;
+  e.ld_r = p->ld_r;
+  e.dtype = p->dtype;
+  e.ytype = p->ytype;
+  e.btype = p->btype;
+  e.act = p->act;
+  e.vy = vec_rows(p->y, p->ld_y, p->ytype, p->M);
+  e.vz = vec_rows(p->z, p->ld_z, p->dtype, p->M);
+  e.vr = vec_rows(p->r, p->ld_r, p->dtype, p->M);
+  e.vb = aligned_to(p->b, 16);
+  return gemm({p->x, p->ld_x, false}, {p->w, p->ld_w, false}, (int)p->M, (int)p->N, p->K,
+              p->dtype == MOE_BF16, e, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_linear_workspace(long long M, long long N) {
+  if (M < 1 || N < 1) return 0;
+  return dz_bytes(M, N) + (size_t)kBiasParts * N * sizeof(float);
+}
+
+int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t workspace_bytes,
+                        moe_stream_t stream) {
+  int rc = check_linear(p);
+  if (rc != MOE_OK) return rc;
+  if (p->dwtype != p->dtype && p->dwtype != MOE_FP32) return MOE_ERR_ARG;
+  if (!check_matrix(p->dw, p->ld_dw, p->N, p->K, p->dwtype, false) ||
+      !aligned_to(p->db, (size_t)type_bytes(p->btype)))
+    return MOE_ERR_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if (p->M == 0) {  // no rows: the weights' gradients are zero
+    if (p->dw == nullptr && p->db == nullptr) return MOE_OK;
+    rc = ops_device(&sms);
+    if (rc != MOE_OK) return rc;
+    const size_t wt = (size_t)type_bytes(p->dwtype);
+    const size_t pitch = (p->N > 1 ? (size_t)p->ld_dw : (size_t)p->K) * wt;
+    if ((p->dw != nullptr && cudaMemset2DAsync(p->dw, pitch, 0, (size_t)p->K * wt, (size_t)p->N, s) !=
+                                 cudaSuccess) ||
+        (p->db != nullptr &&
+         cudaMemsetAsync(p->db, 0, (size_t)p->N * type_bytes(p->btype), s) != cudaSuccess)) {
+      cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+  }
+  const bool act = p->act != MOE_ACT_NONE;
+  if (!check_matrix(p->dy, p->ld_dy, p->M, p->N, p->dtype, true) ||
+      !check_matrix(p->z, p->ld_z, p->M, p->N, p->dtype, act) ||
+      !check_matrix(p->dx, p->ld_dx, p->M, p->K, p->dtype, false) ||
+      (p->dx != nullptr && !check_operand(p->w, p->ld_w, p->N, p->K)) ||
+      (p->dw != nullptr && !check_operand(p->x, p->ld_x, p->M, p->K)) || workspace == nullptr ||
+      !aligned_to(workspace, 256))
+    return MOE_ERR_ARG;
+  if (workspace_bytes < moe_linear_workspace(p->M, p->N)) return MOE_ERR_WORKSPACE;
+  rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  const int M = (int)p->M, N = (int)p->N;
+  const bool bf16 = p->dtype == MOE_BF16;
+  // dy itself where there is no activation and the tensor maps can read its rows.
+  const bool copy = act || !check_operand(p->dy, p->ld_dy, M, N);
+  const long long ld_dz = copy ? (p->N + 7) / 8 * 8 : p->ld_dy;
+  const void* dz = copy ? workspace : p->dy;
+  if (copy || p->db != nullptr) {
+    ActGradArgs g{};
+    g.dy = p->dy;
+    g.z = p->z;
+    g.dz = copy ? workspace : nullptr;
+    g.part = p->db != nullptr ? reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(M, N))
+                              : nullptr;
+    g.ld_dy = p->ld_dy;
+    g.ld_z = p->ld_z;
+    g.ld_dz = ld_dz;
+    g.M = M;
+    g.N = N;
+    g.dtype = p->dtype;
+    g.vdy = vec_rows(p->dy, p->ld_dy, p->dtype, M);
+    g.vz = vec_rows(p->z, p->ld_z, p->dtype, M);
+    const int bx = (N + 255) / 256;
+    const int want = std::max(1, std::min(kBiasParts, 8 * sms / bx));
+    g.rows = std::max(8, (M + want - 1) / want);
+    const int by = (M + g.rows - 1) / g.rows;
+    const dim3 grid((unsigned)bx, (unsigned)by);
+    switch (p->act) {
+      case MOE_ACT_RELU: launch_act_grad<MOE_ACT_RELU>(g, grid, s); break;
+      case MOE_ACT_GELU: launch_act_grad<MOE_ACT_GELU>(g, grid, s); break;
+      case MOE_ACT_GELU_TANH: launch_act_grad<MOE_ACT_GELU_TANH>(g, grid, s); break;
+      case MOE_ACT_SILU: launch_act_grad<MOE_ACT_SILU>(g, grid, s); break;
+      default: launch_act_grad<MOE_ACT_NONE>(g, grid, s); break;
+    }
+    if (p->db != nullptr) bias_grad_kernel<<<(N + 31) / 32, 256, 0, s>>>(g.part, by, N, p->btype, p->db);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  Epilogue e{};
+  e.dtype = p->dtype;
+  e.btype = p->dtype;
+  if (p->dx != nullptr) {
+    e.y = p->dx;
+    e.ld_y = p->ld_dx;
+    e.ytype = p->dtype;
+    e.vy = vec_rows(p->dx, p->ld_dx, p->dtype, M);
+    rc = gemm({dz, ld_dz, false}, {p->w, p->ld_w, true}, M, (int)p->K, N, bf16, e, sms, s);
+    if (rc != MOE_OK) return rc;
+  }
+  if (p->dw != nullptr) {
+    e.y = p->dw;
+    e.ld_y = p->ld_dw;
+    e.ytype = p->dwtype;
+    e.vy = vec_rows(p->dw, p->ld_dw, p->dwtype, N);
+    rc = gemm({dz, ld_dz, true}, {p->x, p->ld_x, true}, N, (int)p->K, M, bf16, e, sms, s);
+  }
+  return rc;
+}
+
+int moe_ops_status(moe_stream_t stream, int* code, int* detail) {
+  uint32_t v[2] = {0, 0};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cudaMemcpyFromSymbolAsync(v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  if (code != nullptr) *code = (int)v[0];
+  if (detail != nullptr) *detail = (int)v[1];
+  return MOE_OK;
+}
+
+int moe_ops_status_clear(moe_stream_t stream) {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess ||
+      cudaMemsetAsync(p, 0, sizeof(g_status), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -21,6 +21,9 @@ from . import capi
 
 _DTYPES = {torch.bfloat16: capi.MOE_BF16, torch.float16: capi.MOE_FP16,
            torch.float32: capi.MOE_FP32}
+_ACTS = {"none": capi.MOE_ACT_NONE, "relu": capi.MOE_ACT_RELU, "gelu": capi.MOE_ACT_GELU,
+         "gelu_tanh": capi.MOE_ACT_GELU_TANH, "silu": capi.MOE_ACT_SILU}
+_HALF = (torch.bfloat16, torch.float16)
 _SCORES = {"softmax": capi.MOE_SCORE_SOFTMAX, "sigmoid": capi.MOE_SCORE_SIGMOID}
 
 
@@ -226,3 +229,108 @@ def layer_norm_backward(dy, z, weight, mean, rstd, dz=None, bias=True, stream=No
             mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), _ptr(dz), dx.data_ptr(), _ptr(dw),
             _ptr(db), 0, 0, 0, ld_z, ld["dy"], ld["dz"], D), work.data_ptr(), size, s)
     return dx, dw, db
+
+
+# ------------------------------------------------------------------------------- linear
+def _operand(t, what, cols, dtype, device):
+    """Rows of a matrix that the tensor maps read: on 16 bytes."""
+    n, c, ld = _rows(t, what, cols, device)
+    if t.dtype != dtype:
+        raise ValueError(f"{what} has type {t.dtype}: expected {dtype}")
+    if t.data_ptr() % 16 or (n > 1 and ld % 8):
+        raise ValueError(f"{what} must have rows that start on 16 bytes (a row stride that is a "
+                         f"multiple of 8 elements), got a stride of {ld} and an address of "
+                         f"{t.data_ptr() % 16} modulo 16")
+    return n, c, ld
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError(f"act {act!r}: expected one of {', '.join(_ACTS)}")
+    return _ACTS[act]
+
+
+def linear(x, weight, bias=None, act="none", residual=None, preact=False, out_dtype=None,
+           stream=None):
+    """(y, z): z = x weight^T + bias, y = act(z) + residual, with fp32 sums.
+
+    x: [..., K], weight: [N, K], both bf16 or both fp16, rows on 16 bytes; bias: [N] of that
+    type or fp32; act: "none", "relu", "gelu", "gelu_tanh" or "silu"; residual: [..., N] of
+    x's type. y has out_dtype (x's type or fp32; default x's), z (with preact, for
+    linear_backward, else None) x's type; both are contiguous."""
+    dt = _dtype(x, "x", _HALF)
+    M, K, ld_x = _operand(x, "x", None, x.dtype, x.device)
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [N, K], got {tuple(weight.shape)}")
+    N, _, ld_w = _operand(weight, "weight", K, x.dtype, x.device)
+    a = _act(act)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"out_dtype {out_dtype}: expected {x.dtype} or torch.float32")
+    if bias is not None:
+        _vector(bias, "bias", N, (x.dtype, torch.float32), x.device)
+    shape, ld_r = (*x.shape[:-1], N), 0
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != x.dtype:
+            raise ValueError(f"residual must be {shape} of {x.dtype}, got {tuple(residual.shape)} of "
+                             f"{residual.dtype}")
+        ld_r = _rows(residual, "residual", N, x.device)[2]
+    with _Launch(x, stream) as s:
+        y = torch.empty(shape, dtype=out_dtype, device=x.device)
+        z = torch.empty(shape, dtype=x.dtype, device=x.device) if preact else None
+        capi.moe_linear(capi.moe_linear_args(
+            M, N, K, dt, _DTYPES[out_dtype], dt if bias is None else _DTYPES[bias.dtype], dt, a,
+            x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z), None,
+            None, None, None, ld_x, ld_w, ld_r, N, N), s)
+    return y, z
+
+
+def linear_backward(dy, x, weight, z=None, act="none", bias=None, dw_dtype=None, need_dx=True,
+                    need_dw=True, stream=None):
+    """(dx, dweight, dbias) of linear from the gradient dy of y (which is the residual's
+    gradient too), for its x, weight, act and the z that it returned with preact.
+
+    bias: the type of dbias (x's or torch.float32), or None for no dbias. dweight has
+    dw_dtype (x's type or fp32; default x's). The products take dy act'(z) rounded to x's
+    type."""
+    dt = _dtype(x, "x", _HALF)
+    M, K, ld_x = _operand(x, "x", None, x.dtype, x.device)
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [N, K], got {tuple(weight.shape)}")
+    N, _, ld_w = _operand(weight, "weight", K, x.dtype, x.device)
+    a = _act(act)
+    shape = (*x.shape[:-1], N)
+    if (z is None) != (a == capi.MOE_ACT_NONE):
+        raise ValueError("z is needed with an activation, and only then")
+    ld = {"z": 0}
+    for t, what in ((dy, "dy"), (z, "z")):
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype != x.dtype:
+            raise ValueError(f"{what} must be {shape} of {x.dtype}, got {tuple(t.shape)} of {t.dtype}")
+        ld[what] = _rows(t, what, N, x.device)[2]
+    dw_dtype = x.dtype if dw_dtype is None else dw_dtype
+    for t, what in ((dw_dtype, "dw_dtype"), (bias, "bias")):
+        if t is not None and t not in (x.dtype, torch.float32):
+            raise ValueError(f"{what} {t}: expected {x.dtype} or torch.float32")
+    with _Launch(x, stream) as s:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+        dw = torch.empty(N, K, dtype=dw_dtype, device=x.device) if need_dw else None
+        db = torch.empty(N, dtype=bias, device=x.device) if bias is not None else None
+        size = capi.moe_linear_workspace(M, N)
+        work = torch.empty(size, dtype=torch.uint8, device=x.device)
+        capi.moe_linear_backward(capi.moe_linear_args(
+            M, N, K, dt, dt, dt if bias is None else _DTYPES[bias], _DTYPES[dw_dtype], a, x.data_ptr(),
+            weight.data_ptr(), None, None, None, _ptr(z), dy.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db),
+            ld_x, ld_w, 0, 0, ld["z"], ld["dy"], K, K), work.data_ptr(), size, s)
+    return dx, dw, db
+
+
+def status(stream=None):
+    """(code, detail) of the products' device status: 0, or MOE_DEV_TIMEOUT after a device
+    wait ran out. Synchronises the stream; clear_status() clears it."""
+    return capi.moe_ops_status((stream or torch.cuda.current_stream()).cuda_stream)
+
+
+def clear_status(stream=None):
+    capi.moe_ops_status_clear((stream or torch.cuda.current_stream()).cuda_stream)
