@@ -274,17 +274,22 @@ def moe_set_schedule(plan, consumer_ctas: int, mgb: int):
 
 
 def moe_router(plan, cfg: moe_router_cfg, logits, dtype, n, ld, bias, ids, w, stream):
-    check(lib().moe_router(plan, ctypes.byref(cfg), logits, dtype, n, ld, bias, ids, w, stream),
-          "moe_router")
+    rc = lib().moe_router(plan, cfg, logits, dtype, n, ld, bias, ids, w, stream)
+    if rc:
+        check(rc, "moe_router")
 
 
 def moe_router_backward(cfg: moe_router_cfg, d_w, logits, ids, dtype, n, ld, d_logits, ld_d, stream):
-    check(lib().moe_router_backward(ctypes.byref(cfg), d_w, logits, ids, dtype, n, ld, d_logits,
-                                    ld_d, stream), "moe_router_backward")
+    rc = lib().moe_router_backward(cfg, d_w, logits, ids, dtype, n, ld, d_logits,
+                                    ld_d, stream)
+    if rc:
+        check(rc, "moe_router_backward")
 
 
 def moe_layer_norm(args: moe_norm_args, stream):
-    check(lib().moe_layer_norm(ctypes.byref(args), stream), "moe_layer_norm")
+    rc = lib().moe_layer_norm(args, stream)
+    if rc:
+        check(rc, "moe_layer_norm")
 
 
 def moe_layer_norm_workspace(n: int, D: int) -> int:
@@ -292,12 +297,15 @@ def moe_layer_norm_workspace(n: int, D: int) -> int:
 
 
 def moe_layer_norm_backward(args: moe_norm_args, workspace, workspace_bytes, stream):
-    check(lib().moe_layer_norm_backward(ctypes.byref(args), workspace, workspace_bytes, stream),
-          "moe_layer_norm_backward")
+    rc = lib().moe_layer_norm_backward(args, workspace, workspace_bytes, stream)
+    if rc:
+        check(rc, "moe_layer_norm_backward")
 
 
 def moe_linear(args: moe_linear_args, stream):
-    check(lib().moe_linear(ctypes.byref(args), stream), "moe_linear")
+    rc = lib().moe_linear(args, stream)
+    if rc:
+        check(rc, "moe_linear")
 
 
 def moe_linear_workspace(M: int, N: int) -> int:
@@ -305,15 +313,20 @@ def moe_linear_workspace(M: int, N: int) -> int:
 
 
 def moe_linear_backward(args: moe_linear_args, workspace, workspace_bytes, stream):
-    check(lib().moe_linear_backward(ctypes.byref(args), workspace, workspace_bytes, stream),
-          "moe_linear_backward")
+    rc = lib().moe_linear_backward(args, workspace, workspace_bytes, stream)
+    if rc:
+        check(rc, "moe_linear_backward")
 
 
 def moe_ops_status(stream):
     code, detail = ctypes.c_int(), ctypes.c_int()
-    check(lib().moe_ops_status(stream, ctypes.byref(code), ctypes.byref(detail)), "moe_ops_status")
+    rc = lib().moe_ops_status(stream, ctypes.byref(code), ctypes.byref(detail))
+    if rc:
+        check(rc, "moe_ops_status")
     return code.value, detail.value
 
 
 def moe_ops_status_clear(stream):
-    check(lib().moe_ops_status_clear(stream), "moe_ops_status_clear")
+    rc = lib().moe_ops_status_clear(stream)
+    if rc:
+        check(rc, "moe_ops_status_clear")

@@ -13,6 +13,7 @@ stay alive until the call has run there.
 """
 from __future__ import annotations
 
+import contextlib
 import functools
 
 import torch
@@ -23,41 +24,38 @@ _DTYPES = {torch.bfloat16: capi.MOE_BF16, torch.float16: capi.MOE_FP16,
            torch.float32: capi.MOE_FP32}
 _ACTS = {"none": capi.MOE_ACT_NONE, "relu": capi.MOE_ACT_RELU, "gelu": capi.MOE_ACT_GELU,
          "gelu_tanh": capi.MOE_ACT_GELU_TANH, "silu": capi.MOE_ACT_SILU}
+_FP32 = (torch.float32,)
 _HALF = (torch.bfloat16, torch.float16)
 _SCORES = {"softmax": capi.MOE_SCORE_SOFTMAX, "sigmoid": capi.MOE_SCORE_SIGMOID}
 
 
-class _Launch:
-    """The device and the stream of a call: its outputs are allocated and its kernels
-    enqueued there."""
+def _stream_here(t, stream):
+    """The raw handle of the current stream if a call on `t` runs there (no other stream is
+    asked for and t's device is the current one), else None: the call then enters _on and
+    starts again. One integer each from torch's binding: a public Stream object costs more
+    than the rest of a call's checks."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return None
 
-    __slots__ = ("handle", "guards")
 
-    def __init__(self, tensor, stream):
-        dev = tensor.device
-        if dev.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {dev}")
-        self.guards = ()
-        if dev.index != torch.cuda.current_device():
-            self.guards = (torch.cuda.device(dev),)
+@contextlib.contextmanager
+def _on(t, stream):
+    """Makes t's device, and `stream` (a torch stream or a raw handle) if given, current:
+    outputs and workspaces are then allocated for that stream."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"stream of {stream.device} for tensors of {t.device}")
+    with torch.cuda.device(t.device):
         if stream is None:
-            self.handle = torch.cuda.current_stream(dev).cuda_stream
-            return
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        elif stream.device != dev:
-            raise ValueError(f"stream of {stream.device} for tensors of {dev}")
-        self.handle = stream.cuda_stream
-        self.guards += (torch.cuda.stream(stream),)
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
 
 
 def _dtype(t, what, allowed=None):
@@ -68,33 +66,32 @@ def _dtype(t, what, allowed=None):
     return d
 
 
-def _rows(t, what, cols=None, device=None):
-    """(rows, cols, leading dimension) of a matrix."""
-    if t.dim() == 2:  # the common case, without a view
-        m = t
-    elif t.dim() == 1:
-        m = t[None]
-    else:
+def _rows(t, what, cols=None, dev=None):
+    """(rows, cols, leading dimension) of a matrix; `dev`: the device index it has to be on."""
+    m = t
+    if t.dim() != 2:
         try:
-            m = t.view(-1, t.shape[-1]) if t.dim() else None
+            m = t[None] if t.dim() == 1 else t.view(-1, t.shape[-1]) if t.dim() else None
         except RuntimeError:
             m = None
     n, c = m.shape if m is not None else (0, 0)
-    if m is None or (c > 1 and m.stride(1) != 1) or (n > 1 and m.stride(0) < c):
+    s0, s1 = m.stride() if m is not None else (0, 0)
+    if m is None or (c > 1 and s1 != 1) or (n > 1 and s0 < c):
         raise ValueError(f"{what} must be rows of contiguous elements, got shape "
                          f"{tuple(t.shape)} and strides {t.stride()}")
     if cols is not None and c != cols:
         raise ValueError(f"{what} has rows of {c} elements: expected {cols}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}: expected {device}")
-    return n, c, (m.stride(0) if n > 1 else c)
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}: expected device {dev}")
+    return n, c, (s0 if n > 1 else c)
 
 
-def _vector(t, what, size, dtypes, device):
-    if t.shape != (size,) or not t.is_contiguous() or t.dtype not in dtypes or t.device != device:
+def _vector(t, what, size, dtypes, dev):
+    if (t.dim() != 1 or t.shape[0] != size or t.dtype not in dtypes or t.get_device() != dev or
+            not t.is_contiguous()):
         raise ValueError(f"{what} must be {size} contiguous elements of "
-                         f"{', '.join(str(d) for d in dtypes)} on {device}, got {tuple(t.shape)} "
-                         f"of {t.dtype} on {t.device}")
+                         f"{', '.join(str(d) for d in dtypes)} beside the rows, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
 def _ptr(t):
@@ -126,14 +123,19 @@ def route_experts(logits, topk, score="softmax", bias=None, groups=1, topk_group
     n, E, ld = _rows(logits, "logits")
     dt = _dtype(logits, "logits")
     if bias is not None:
-        _vector(bias, "bias", E, (torch.float32,), logits.device)
+        _vector(bias, "bias", E, _FP32, logits.get_device())
     cfg = router_cfg(E, topk, score, groups, topk_groups, group_top, renorm, scale)
-    with _Launch(logits, stream) as s:
-        shape = (*logits.shape[:-1], topk)
-        ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
-        w = torch.empty(shape, dtype=torch.float32, device=logits.device)
-        capi.moe_router(None, cfg, logits.data_ptr(), dt, n, ld, _ptr(bias), ids.data_ptr(),
-                        w.data_ptr(), s)
+    s = _stream_here(logits, stream)
+    if s is None:
+        with _on(logits, stream):
+            return route_experts(logits, topk, score, bias, groups, topk_groups, group_top, renorm,
+                                 scale)
+    dev = logits.device
+    shape = (n, topk) if logits.dim() == 2 else (*logits.shape[:-1], topk)
+    ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    w = torch.empty(shape, dtype=torch.float32, device=dev)
+    capi.moe_router(None, cfg, logits.data_ptr(), dt, n, ld, _ptr(bias), ids.data_ptr(),
+                    w.data_ptr(), s)
     return ids, w
 
 
@@ -149,17 +151,20 @@ def route_experts_backward(d_w, logits, ids, score="softmax", renorm=False, scal
             raise ValueError(f"{what} must be contiguous {dtype} of shape [..., topk] beside the "
                              f"logits, got {tuple(t.shape)} of {t.dtype} on {t.device}")
     cfg = router_cfg(E, ids.shape[-1], score, 1, 1, 1, renorm, scale)
-    with _Launch(logits, stream) as s:
-        d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        capi.moe_router_backward(cfg, d_w.data_ptr(), logits.data_ptr(), ids.data_ptr(), dt, n, ld,
-                                 d.data_ptr(), E, s)
+    s = _stream_here(logits, stream)
+    if s is None:
+        with _on(logits, stream):
+            return route_experts_backward(d_w, logits, ids, score, renorm, scale)
+    d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    capi.moe_router_backward(cfg, d_w.data_ptr(), logits.data_ptr(), ids.data_ptr(), dt, n, ld,
+                             d.data_ptr(), E, s)
     return d
 
 
 # --------------------------------------------------------------------------- layer norm
 def _norm_params(what, t, x, D):
     if t is not None:
-        _vector(t, what, D, (x.dtype, torch.float32), x.device)
+        _vector(t, what, D, (x.dtype, torch.float32), x.get_device())
 
 
 def layer_norm(x, weight, bias=None, eps=1e-5, residual=None, stats=False, stream=None):
@@ -181,18 +186,21 @@ def layer_norm(x, weight, bias=None, eps=1e-5, residual=None, stats=False, strea
         if residual.shape != x.shape or residual.dtype != x.dtype:
             raise ValueError(f"residual must be {tuple(x.shape)} of {x.dtype}, got "
                              f"{tuple(residual.shape)} of {residual.dtype}")
-        ld_r = _rows(residual, "residual", D, x.device)[2]
-    with _Launch(x, stream) as s:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        z = torch.empty_like(y) if residual is not None else None
-        mean = rstd = None
-        if stats:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-            rstd = torch.empty_like(mean)
-        capi.moe_layer_norm(capi.moe_norm_args(
-            n, D, dt, dt if p is None else _DTYPES[p.dtype], eps, x.data_ptr(), _ptr(residual),
-            _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(z), _ptr(mean), _ptr(rstd), None, None,
-            None, None, None, ld, ld_r, D, D), s)
+        ld_r = _rows(residual, "residual", D, x.get_device())[2]
+    s = _stream_here(x, stream)
+    if s is None:
+        with _on(x, stream):
+            return layer_norm(x, weight, bias, eps, residual, stats)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    z = torch.empty_like(y) if residual is not None else None
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    capi.moe_layer_norm(capi.moe_norm_args(
+        n, D, dt, dt if p is None else _DTYPES[p.dtype], eps, x.data_ptr(), _ptr(residual),
+        _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(z), _ptr(mean), _ptr(rstd), None, None,
+        None, None, None, ld, ld_r, D, D), s)
     return y, (x if z is None else z), mean, rstd
 
 
@@ -211,30 +219,33 @@ def layer_norm_backward(dy, z, weight, mean, rstd, dz=None, bias=True, stream=No
         if t.shape != z.shape or t.dtype != z.dtype:
             raise ValueError(f"{what} must be {tuple(z.shape)} of {z.dtype}, got {tuple(t.shape)} of "
                              f"{t.dtype}")
-        ld[what] = _rows(t, what, D, z.device)[2]
+        ld[what] = _rows(t, what, D, z.get_device())[2]
     for t, what in ((mean, "mean"), (rstd, "rstd")):
         if (t.shape != z.shape[:-1] or t.dtype != torch.float32 or not t.is_contiguous() or
                 t.device != z.device):
             raise ValueError(f"{what} must be contiguous fp32 of shape {tuple(z.shape[:-1])}, got "
                              f"{tuple(t.shape)} of {t.dtype}")
     wt = z.dtype if weight is None else weight.dtype
-    with _Launch(z, stream) as s:
-        dx = torch.empty(z.shape, dtype=z.dtype, device=z.device)
-        dw = None if weight is None else torch.empty(D, dtype=wt, device=z.device)
-        db = torch.empty(D, dtype=wt, device=z.device) if bias else None
-        size = capi.moe_layer_norm_workspace(n, D)
-        work = torch.empty(size, dtype=torch.uint8, device=z.device)
-        capi.moe_layer_norm_backward(capi.moe_norm_args(
-            n, D, dt, _DTYPES[wt], 0.0, None, None, _ptr(weight), None, None, z.data_ptr(),
-            mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), _ptr(dz), dx.data_ptr(), _ptr(dw),
-            _ptr(db), 0, 0, 0, ld_z, ld["dy"], ld["dz"], D), work.data_ptr(), size, s)
+    s = _stream_here(z, stream)
+    if s is None:
+        with _on(z, stream):
+            return layer_norm_backward(dy, z, weight, mean, rstd, dz, bias)
+    dx = torch.empty(z.shape, dtype=z.dtype, device=z.device)
+    dw = None if weight is None else torch.empty(D, dtype=wt, device=z.device)
+    db = torch.empty(D, dtype=wt, device=z.device) if bias else None
+    size = capi.moe_layer_norm_workspace(n, D)
+    work = torch.empty(size, dtype=torch.uint8, device=z.device)
+    capi.moe_layer_norm_backward(capi.moe_norm_args(
+        n, D, dt, _DTYPES[wt], 0.0, None, None, _ptr(weight), None, None, z.data_ptr(),
+        mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), _ptr(dz), dx.data_ptr(), _ptr(dw),
+        _ptr(db), 0, 0, 0, ld_z, ld["dy"], ld["dz"], D), work.data_ptr(), size, s)
     return dx, dw, db
 
 
 # ------------------------------------------------------------------------------- linear
-def _operand(t, what, cols, dtype, device):
+def _operand(t, what, cols, dtype, dev):
     """Rows of a matrix that the tensor maps read: on 16 bytes."""
-    n, c, ld = _rows(t, what, cols, device)
+    n, c, ld = _rows(t, what, cols, dev)
     if t.dtype != dtype:
         raise ValueError(f"{what} has type {t.dtype}: expected {dtype}")
     if t.data_ptr() % 16 or (n > 1 and ld % 8):
@@ -258,30 +269,33 @@ def linear(x, weight, bias=None, act="none", residual=None, preact=False, out_dt
     type or fp32; act: "none", "relu", "gelu", "gelu_tanh" or "silu"; residual: [..., N] of
     x's type. y has out_dtype (x's type or fp32; default x's), z (with preact, for
     linear_backward, else None) x's type; both are contiguous."""
-    dt = _dtype(x, "x", _HALF)
-    M, K, ld_x = _operand(x, "x", None, x.dtype, x.device)
+    dt, dev, xt = _dtype(x, "x", _HALF), x.get_device(), x.dtype
+    M, K, ld_x = _operand(x, "x", None, xt, dev)
     if weight.dim() != 2:
         raise ValueError(f"weight must be [N, K], got {tuple(weight.shape)}")
-    N, _, ld_w = _operand(weight, "weight", K, x.dtype, x.device)
+    N, _, ld_w = _operand(weight, "weight", K, xt, dev)
     a = _act(act)
     out_dtype = x.dtype if out_dtype is None else out_dtype
     if out_dtype not in (x.dtype, torch.float32):
         raise ValueError(f"out_dtype {out_dtype}: expected {x.dtype} or torch.float32")
     if bias is not None:
-        _vector(bias, "bias", N, (x.dtype, torch.float32), x.device)
-    shape, ld_r = (*x.shape[:-1], N), 0
+        _vector(bias, "bias", N, (xt, torch.float32), dev)
+    shape, ld_r = (M, N) if x.dim() == 2 else (*x.shape[:-1], N), 0
     if residual is not None:
         if residual.shape != shape or residual.dtype != x.dtype:
             raise ValueError(f"residual must be {shape} of {x.dtype}, got {tuple(residual.shape)} of "
                              f"{residual.dtype}")
-        ld_r = _rows(residual, "residual", N, x.device)[2]
-    with _Launch(x, stream) as s:
-        y = torch.empty(shape, dtype=out_dtype, device=x.device)
-        z = torch.empty(shape, dtype=x.dtype, device=x.device) if preact else None
-        capi.moe_linear(capi.moe_linear_args(
-            M, N, K, dt, _DTYPES[out_dtype], dt if bias is None else _DTYPES[bias.dtype], dt, a,
-            x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z), None,
-            None, None, None, ld_x, ld_w, ld_r, N, N), s)
+        ld_r = _rows(residual, "residual", N, dev)[2]
+    s = _stream_here(x, stream)
+    if s is None:
+        with _on(x, stream):
+            return linear(x, weight, bias, act, residual, preact, out_dtype)
+    y = torch.empty(shape, dtype=out_dtype, device=x.device)
+    z = torch.empty(shape, dtype=x.dtype, device=x.device) if preact else None
+    capi.moe_linear(capi.moe_linear_args(
+        M, N, K, dt, _DTYPES[out_dtype], dt if bias is None else _DTYPES[bias.dtype], dt, a,
+        x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z), None,
+        None, None, None, ld_x, ld_w, ld_r, N, N), s)
     return y, z
 
 
@@ -293,13 +307,13 @@ def linear_backward(dy, x, weight, z=None, act="none", bias=None, dw_dtype=None,
     bias: the type of dbias (x's or torch.float32), or None for no dbias. dweight has
     dw_dtype (x's type or fp32; default x's). The products take dy act'(z) rounded to x's
     type."""
-    dt = _dtype(x, "x", _HALF)
-    M, K, ld_x = _operand(x, "x", None, x.dtype, x.device)
+    dt, dev, xt = _dtype(x, "x", _HALF), x.get_device(), x.dtype
+    M, K, ld_x = _operand(x, "x", None, xt, dev)
     if weight.dim() != 2:
         raise ValueError(f"weight must be [N, K], got {tuple(weight.shape)}")
-    N, _, ld_w = _operand(weight, "weight", K, x.dtype, x.device)
+    N, _, ld_w = _operand(weight, "weight", K, xt, dev)
     a = _act(act)
-    shape = (*x.shape[:-1], N)
+    shape = (M, N) if x.dim() == 2 else (*x.shape[:-1], N)
     if (z is None) != (a == capi.MOE_ACT_NONE):
         raise ValueError("z is needed with an activation, and only then")
     ld = {"z": 0}
@@ -308,21 +322,24 @@ def linear_backward(dy, x, weight, z=None, act="none", bias=None, dw_dtype=None,
             continue
         if t.shape != shape or t.dtype != x.dtype:
             raise ValueError(f"{what} must be {shape} of {x.dtype}, got {tuple(t.shape)} of {t.dtype}")
-        ld[what] = _rows(t, what, N, x.device)[2]
+        ld[what] = _rows(t, what, N, dev)[2]
     dw_dtype = x.dtype if dw_dtype is None else dw_dtype
     for t, what in ((dw_dtype, "dw_dtype"), (bias, "bias")):
         if t is not None and t not in (x.dtype, torch.float32):
             raise ValueError(f"{what} {t}: expected {x.dtype} or torch.float32")
-    with _Launch(x, stream) as s:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
-        dw = torch.empty(N, K, dtype=dw_dtype, device=x.device) if need_dw else None
-        db = torch.empty(N, dtype=bias, device=x.device) if bias is not None else None
-        size = capi.moe_linear_workspace(M, N)
-        work = torch.empty(size, dtype=torch.uint8, device=x.device)
-        capi.moe_linear_backward(capi.moe_linear_args(
-            M, N, K, dt, dt, dt if bias is None else _DTYPES[bias], _DTYPES[dw_dtype], a, x.data_ptr(),
-            weight.data_ptr(), None, None, None, _ptr(z), dy.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db),
-            ld_x, ld_w, 0, 0, ld["z"], ld["dy"], K, K), work.data_ptr(), size, s)
+    s = _stream_here(x, stream)
+    if s is None:
+        with _on(x, stream):
+            return linear_backward(dy, x, weight, z, act, bias, dw_dtype, need_dx, need_dw)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dw = torch.empty(N, K, dtype=dw_dtype, device=x.device) if need_dw else None
+    db = torch.empty(N, dtype=bias, device=x.device) if bias is not None else None
+    size = capi.moe_linear_workspace(M, N)
+    work = torch.empty(size, dtype=torch.uint8, device=x.device)
+    capi.moe_linear_backward(capi.moe_linear_args(
+        M, N, K, dt, dt, dt if bias is None else _DTYPES[bias], _DTYPES[dw_dtype], a, x.data_ptr(),
+        weight.data_ptr(), None, None, None, _ptr(z), dy.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db),
+        ld_x, ld_w, 0, 0, ld["z"], ld["dy"], K, K), work.data_ptr(), size, s)
     return dx, dw, db
 
 

@@ -95,7 +95,7 @@ class ExpertCombine:
             raise ValueError(f"logits hold {n} rows of {E}: expected {self.W * self.T} rows of "
                              f"{self.W * self.L}")
         if bias is not None:
-            ops._vector(bias, "bias", E, (torch.float32,), logits.device)
+            ops._vector(bias, "bias", E, (torch.float32,), logits.get_device())
         capi.moe_router(self.plan, router, logits.data_ptr(), ops._dtype(logits, "logits"), n, ld,
                         None if bias is None else bias.data_ptr(), self.ids.data_ptr(),
                         self.w.data_ptr(), _stream_handle(stream))
