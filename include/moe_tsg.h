@@ -441,7 +441,8 @@ int moe_layer_norm(const moe_norm_args *args, moe_stream_t stream);
 
 /* dx = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dz with g = dy * w and
  * xhat = (z - mean) * rstd; dw = sum over rows of dy * xhat; db = sum over rows of dy.
- * workspace: at least moe_layer_norm_workspace(n, D) bytes (pure host arithmetic), used
+ * workspace: at least moe_layer_norm_workspace(n, D) bytes (pure host arithmetic), 16-byte
+ * aligned, used
  * until the call has run on the stream. The sums are added in a fixed order. */
 size_t moe_layer_norm_workspace(long long n, int D);
 int moe_layer_norm_backward(const moe_norm_args *args, void *workspace, size_t workspace_bytes,

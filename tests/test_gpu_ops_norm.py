@@ -32,6 +32,12 @@ CASES = [
     (1, 1, "fp32", "fp32", False, True, True, 0),
     (9, 2, "bf16", "bf16", True, True, True, 6),
     (2000, 264, "fp16", "fp16", True, True, True, 0),
+    # rows from the ring of shared memory
+    (1300, 4096, "bf16", "fp32", True, True, True, 0),
+    (1217, 520, "fp16", "fp16", False, True, False, 8),
+    (700, 7168, "bf16", "bf16", True, True, True, 16),
+    (640, 8192, "fp32", "fp32", True, True, True, 0),
+    (1500, 1032, "fp32", "fp32", False, False, True, 4),
 ]
 
 

@@ -731,19 +731,6 @@ struct Operand {
   bool mn;  // MN-major: [k][i or j] in memory
 };
 
-constexpr size_t kSmemMax = 227 * 1024;
-
-// Lets `kernel` use all of a CTA's shared memory; once for each device (bit d of *ready).
-cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>* ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && ((ready->load(std::memory_order_relaxed) >> dev) & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
-  if (e == cudaSuccess && dev < 64) ready->fetch_or(1ull << dev, std::memory_order_relaxed);
-  return e;
-}
-
 template <bool AMN, bool BMN>
 cudaError_t launch_tile(const GemmArgs& a, int tiles, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
@@ -889,6 +876,36 @@ void launch_act_grad(const ActGradArgs& a, dim3 grid, cudaStream_t s) {
 }
 
 }  // namespace
+
+uint32_t* ops_status() {
+  static std::atomic<void*> table[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return nullptr;
+  void* p = table[dev].load(std::memory_order_relaxed);
+  if (p == nullptr) {
+    if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    table[dev].store(p, std::memory_order_relaxed);
+  }
+  return static_cast<uint32_t*>(p);
+}
+
+cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>* ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && ((ready->load(std::memory_order_relaxed) >> dev) & 1)) return cudaSuccess;
+  // Dynamic shared memory on top of the kernel's own.
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(kSmemMax - fa.sharedSizeBytes));
+  if (e == cudaSuccess && dev < 64) ready->fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -1041,8 +1058,8 @@ int moe_ops_status(moe_stream_t stream, int* code, int* detail) {
 }
 
 int moe_ops_status_clear(moe_stream_t stream) {
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess ||
+  void* p = ops_status();
+  if (p == nullptr ||
       cudaMemsetAsync(p, 0, sizeof(g_status), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;

@@ -17,8 +17,10 @@
 // Rows longer than the registers hold are read three times (forward) or twice
 // (backward) by a CTA of 1024 threads.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
+#include "moe_common.cuh"
 #include "ops_common.cuh"
 
 namespace moe {
@@ -42,6 +44,8 @@ struct NormArgs {
   long long n, ld_x, ld_r, ld_dy, ld_y, ld_z;
   int D, wtype, wpr;  // wpr: warps of a row
   float eps;
+  int stages;        // ring kernels: rows of shared memory
+  uint32_t* status;  // ring kernels: where a wait that ran out is recorded
   bool vx, vr, vdy, vy, vz;  // rows start on 16 bytes
   bool vw;                   // w and b start on 16 bytes
 };
@@ -52,36 +56,24 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-template <typename T>
-struct Vec {
-  static constexpr int kN = 16 / (int)sizeof(T);
-};
-
-// Elements [v N, v N + N) of a row of D as fp32; 0 past the row.
-template <typename T>
-__device__ __forceinline__ void load_vec(const T* row, int v, int D, bool vec, float (&f)[Vec<T>::kN]) {
-  constexpr int N = Vec<T>::kN;
+// Elements [v N, v N + N) of a row of D as fp32; 0 past the row. N is a 16-byte vector of
+// elements, or 1 for rows that do not start on 16 bytes (then neighbouring threads take
+// neighbouring elements: vectors taken apart would touch eight times the lines an access).
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const T* row, int v, int D, bool vec, float (&f)[N]) {
   const int c = v * N;
-  if (vec && c + N <= D) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row) + v);
-    const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = to_f32(e[i]);
+  if (N > 1 && vec && c + N <= D) {
+    if constexpr (N > 1) unpack<T>(__ldg(reinterpret_cast<const uint4*>(row) + v), f);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = c + i < D ? to_f32(row[c + i]) : 0.f;
   }
 }
-template <typename T>
-__device__ __forceinline__ void store_vec(T* row, int v, int D, bool vec, const float (&f)[Vec<T>::kN]) {
-  constexpr int N = Vec<T>::kN;
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* row, int v, int D, bool vec, const float (&f)[N]) {
   const int c = v * N;
-  if (vec && c + N <= D) {
-    uint4 u;
-    T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = from_f32<T>(f[i]);
-    reinterpret_cast<uint4*>(row)[v] = u;
+  if (N > 1 && vec && c + N <= D) {
+    if constexpr (N > 1) reinterpret_cast<uint4*>(row)[v] = pack<T>(f);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -89,17 +81,16 @@ __device__ __forceinline__ void store_vec(T* row, int v, int D, bool vec, const 
   }
 }
 // The same elements of w or b, of the rows' type or fp32; `none` where there is no array.
-template <typename T>
+template <typename T, int N>
 __device__ __forceinline__ void load_param(const void* p, int wtype, int v, int D, bool vec, float none,
-                                           float (&f)[Vec<T>::kN]) {
-  constexpr int N = Vec<T>::kN;
+                                           float (&f)[N]) {
   if (p == nullptr) {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = none;
   } else if (sizeof(T) == 2 && wtype == MOE_FP32) {
     const float* q = static_cast<const float*>(p);
     const int c = v * N;
-    if (vec && c + N <= D) {
+    if (N > 1 && vec && c + N <= D) {
 #pragma unroll
       for (int h = 0; h < N / 4; ++h) {
         const float4 u = __ldg(reinterpret_cast<const float4*>(q + c) + h);
@@ -113,15 +104,16 @@ __device__ __forceinline__ void load_param(const void* p, int wtype, int v, int 
       for (int i = 0; i < N; ++i) f[i] = c + i < D ? q[c + i] : 0.f;
     }
   } else {
-    load_vec<T>(static_cast<const T*>(p), v, D, vec, f);
+    load_vec<T, N>(static_cast<const T*>(p), v, D, vec, f);
   }
 }
 
 // The sums of NV values over the wpr warps of a row, in every thread. red: NV x 32 floats
-// of shared memory of this row's group; every thread of the CTA calls it. The warps' sums
-// are added in the same order by every thread.
-template <int NV>
-__device__ __forceinline__ void row_sum(float (&s)[NV], float* red, int wpr, int w_in_row) {
+// of shared memory of this row's group. The warps' sums are added in the same order by
+// every thread. Every thread of the row's group calls it; they meet at barrier 1 + group.
+// W: a power of two, at least wpr.
+template <int NV, int W = 32>
+__device__ __forceinline__ void row_sum(float (&s)[NV], float* red, int wpr, int w_in_row, int group) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) s[i] = warp_sum(s[i]);
   if (wpr == 1) return;
@@ -129,18 +121,22 @@ __device__ __forceinline__ void row_sum(float (&s)[NV], float* red, int wpr, int
   if (lane == 0)
 #pragma unroll
     for (int i = 0; i < NV; ++i) red[i * 32 + w_in_row] = s[i];
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * wpr) : "memory");
 #pragma unroll
-  for (int i = 0; i < NV; ++i) s[i] = warp_sum(lane < wpr ? red[i * 32 + lane] : 0.f);
+  for (int i = 0; i < NV; ++i) s[i] = (lane & (W - 1)) < wpr ? red[i * 32 + (lane & (W - 1))] : 0.f;
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] += __shfl_xor_sync(kAll, s[i], o);
 }
 
 // Warps of a CTA at most, by the elements a thread holds: what their registers allow.
 constexpr int max_warps(int ept) { return ept == 8 ? 32 : 16; }
 
 // wpr warps take a row, each thread EPT elements of it in 16-byte vectors.
-template <typename T, int EPT>
+template <typename T, int EPT, int N>
 __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int N = Vec<T>::kN, PERV = EPT / N;
+  constexpr int PERV = EPT / N;
   __shared__ float red[2][32][32];  // [sum][row of the CTA][warp of the row]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp / a.wpr, wr = warp % a.wpr, rows = (blockDim.x >> 5) / a.wpr;
@@ -156,17 +152,17 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_kernel(const __grid_
 #pragma unroll
   for (int i = 0; i < PERV; ++i) {
     const int v = t + i * step;
-    load_vec<T>(x, v, live ? a.D : 0, a.vx, f[i]);
+    load_vec<T, N>(x, v, live ? a.D : 0, a.vx, f[i]);
     if (r != nullptr) {
       float g[N];
-      load_vec<T>(r, v, live ? a.D : 0, a.vr, g);
+      load_vec<T, N>(r, v, live ? a.D : 0, a.vr, g);
 #pragma unroll
       for (int e = 0; e < N; ++e) f[i][e] += g[e];
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) s[0] += f[i][e];
   }
-  row_sum<1>(s, red[0][grp], a.wpr, wr);
+  row_sum<1>(s, red[0][grp], a.wpr, wr, grp);
   const float mean = s[0] / (float)a.D;
   float q[1] = {0.f};
 #pragma unroll
@@ -178,7 +174,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_kernel(const __grid_
       q[0] = fmaf(d, d, q[0]);
     }
   }
-  row_sum<1>(q, red[1][grp], a.wpr, wr);
+  row_sum<1>(q, red[1][grp], a.wpr, wr, grp);
   if (!live) return;
   const float rstd = 1.0f / sqrtf(q[0] / (float)a.D + a.eps);
   if (t == 0) {
@@ -191,30 +187,29 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_kernel(const __grid_
   for (int i = 0; i < PERV; ++i) {
     const int v = t + i * step;
     if (v * N >= a.D) break;
-    if (z != nullptr) store_vec<T>(z, v, a.D, a.vz, f[i]);
+    if (z != nullptr) store_vec<T, N>(z, v, a.D, a.vz, f[i]);
     float w[N], b[N];
-    load_param<T>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
-    load_param<T>(a.b, a.wtype, v, a.D, a.vw, 0.f, b);
+    load_param<T, N>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
+    load_param<T, N>(a.b, a.wtype, v, a.D, a.vw, 0.f, b);
 #pragma unroll
     for (int e = 0; e < N; ++e) f[i][e] = fmaf((f[i][e] - mean) * rstd, w[e], b[e]);
-    store_vec<T>(y, v, a.D, a.vy, f[i]);
+    store_vec<T, N>(y, v, a.D, a.vy, f[i]);
   }
 }
 
 // Rows of any length: one CTA a row, read three times.
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(kLoopThreads) norm_long_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int N = Vec<T>::kN;
   __shared__ float red[2][32];
   const int wr = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const long long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
   const T* r = a.r != nullptr ? static_cast<const T*>(a.r) + row * a.ld_r : nullptr;
   auto load = [&](int v, float (&f)[N]) {
-    load_vec<T>(x, v, a.D, a.vx, f);
+    load_vec<T, N>(x, v, a.D, a.vx, f);
     if (r != nullptr) {
       float g[N];
-      load_vec<T>(r, v, a.D, a.vr, g);
+      load_vec<T, N>(r, v, a.D, a.vr, g);
 #pragma unroll
       for (int e = 0; e < N; ++e) f[e] += g[e];
     }
@@ -227,7 +222,7 @@ __global__ void __launch_bounds__(kLoopThreads) norm_long_kernel(const __grid_co
 #pragma unroll
     for (int e = 0; e < N; ++e) s[0] += f[e];
   }
-  row_sum<1>(s, red[0], nw, wr);
+  row_sum<1>(s, red[0], nw, wr, 0);
   const float mean = s[0] / (float)a.D;
   for (int v = threadIdx.x; v < nv; v += blockDim.x) {
     float f[N];
@@ -238,7 +233,7 @@ __global__ void __launch_bounds__(kLoopThreads) norm_long_kernel(const __grid_co
       q[0] = fmaf(d, d, q[0]);
     }
   }
-  row_sum<1>(q, red[1], nw, wr);
+  row_sum<1>(q, red[1], nw, wr, 0);
   const float rstd = 1.0f / sqrtf(q[0] / (float)a.D + a.eps);
   if (threadIdx.x == 0) {
     if (a.mean != nullptr) a.mean[row] = mean;
@@ -249,20 +244,21 @@ __global__ void __launch_bounds__(kLoopThreads) norm_long_kernel(const __grid_co
   for (int v = threadIdx.x; v < nv; v += blockDim.x) {
     float f[N], w[N], b[N];
     load(v, f);
-    if (z != nullptr) store_vec<T>(z, v, a.D, a.vz, f);
-    load_param<T>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
-    load_param<T>(a.b, a.wtype, v, a.D, a.vw, 0.f, b);
+    if (z != nullptr) store_vec<T, N>(z, v, a.D, a.vz, f);
+    load_param<T, N>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
+    load_param<T, N>(a.b, a.wtype, v, a.D, a.vw, 0.f, b);
 #pragma unroll
     for (int e = 0; e < N; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[e], b[e]);
-    store_vec<T>(y, v, a.D, a.vy, f);
+    store_vec<T, N>(y, v, a.D, a.vy, f);
   }
 }
 
 // Backward. wpr warps take a row, the CTA's groups of warps take rows in turn.
-template <typename T, int EPT>
+template <typename T, int EPT, int N>
 __global__ void __launch_bounds__(32 * max_warps(EPT))
     norm_backward_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int N = Vec<T>::kN, PERV = EPT / N;
+  constexpr int PERV = EPT / N;
+  allow_dependent_launch();
   extern __shared__ float gather[];  // more than one row group: 2 x (EPT * wpr * 32)
   __shared__ float red[2][32][64];   // [row parity][row group][sum, warp]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -290,14 +286,14 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
-      load_vec<T>(z, v, D, a.vx, xh[i]);
-      load_vec<T>(dy, v, D, a.vdy, g[i]);
+      load_vec<T, N>(z, v, D, a.vx, xh[i]);
+      load_vec<T, N>(dy, v, D, a.vdy, g[i]);
     }
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
       float w[N];
-      load_param<T>(a.w, a.wtype, v, D, a.vw, 1.f, w);
+      load_param<T, N>(a.w, a.wtype, v, D, a.vw, 1.f, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         xh[i][e] = v * N + e < D ? (xh[i][e] - mean) * rstd : 0.f;
@@ -308,7 +304,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
         s[1] = fmaf(g[i][e], xh[i][e], s[1]);
       }
     }
-    row_sum<2>(s, red[parity][grp], a.wpr, wr);
+    row_sum<2>(s, red[parity][grp], a.wpr, wr, grp);
     parity ^= 1;  // the next row's sums do not overwrite what a slow warp still reads
     if (!live) continue;
     const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
@@ -321,10 +317,10 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
       float o[N];
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = 0.f;
-      if (dz != nullptr) load_vec<T>(dz, v, D, a.vr, o);
+      if (dz != nullptr) load_vec<T, N>(dz, v, D, a.vr, o);
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = fmaf(rstd, g[i][e] - m1 - xh[i][e] * m2, o[e]);
-      store_vec<T>(dx, v, D, a.vy, o);
+      store_vec<T, N>(dx, v, D, a.vy, o);
     }
   }
 
@@ -367,10 +363,10 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
 
 // Rows of any length: each thread adds its columns' products to the CTA's sums in the
 // workspace (no other thread touches them).
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int N = Vec<T>::kN;
   __shared__ float red[2][64];
+  allow_dependent_launch();
   const int wr = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int nv = (a.D + N - 1) / N;
   const float inv_d = 1.0f / (float)a.D;
@@ -385,9 +381,9 @@ __global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const 
     const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy;
     const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
     auto load = [&](int v, float (&xh)[N], float (&d)[N], float (&w)[N]) {
-      load_vec<T>(z, v, a.D, a.vx, xh);
-      load_vec<T>(dy, v, a.D, a.vdy, d);
-      load_param<T>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
+      load_vec<T, N>(z, v, a.D, a.vx, xh);
+      load_vec<T, N>(dy, v, a.D, a.vdy, d);
+      load_param<T, N>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) xh[e] = v * N + e < a.D ? (xh[e] - mean) * rstd : 0.f;
     };
@@ -406,7 +402,7 @@ __global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const 
         }
       }
     }
-    row_sum<2>(s, red[parity], nw, wr);
+    row_sum<2>(s, red[parity], nw, wr, 0);
     parity ^= 1;
     const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
     const T* dz = a.r != nullptr ? static_cast<const T*>(a.r) + row * a.ld_r : nullptr;
@@ -416,35 +412,451 @@ __global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const 
       load(v, xh, d, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = 0.f;
-      if (dz != nullptr) load_vec<T>(dz, v, a.D, a.vr, o);
+      if (dz != nullptr) load_vec<T, N>(dz, v, a.D, a.vr, o);
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = fmaf(rstd, d[e] * w[e] - m1 - xh[e] * m2, o[e]);
-      store_vec<T>(dx, v, a.D, a.vy, o);
+      store_vec<T, N>(dx, v, a.D, a.vy, o);
     }
   }
 }
 
-// dw and db from the CTAs' sums: 32 columns a CTA, eight warps share the rows; then their
-// eight sums in order.
-__global__ void __launch_bounds__(256) norm_params_kernel(const float* part, int rows, int D, int wtype,
-                                                         void* dw, void* db) {
-  __shared__ float red[2][8][32];
+// ------------------------------------------------------------------- ring kernels
+// Rows of 16-byte vectors from long matrices: persistent CTAs whose thread 0 keeps the next
+// rows coming in (bulk copies into a ring of shared memory), so that the loads never stop
+// for the reductions of a row: the kernels above only load between a CTA's start and its
+// first reduction (16384 x 4096 bf16 with a residual: 143 us against 95, 5.7 TB/s; backward
+// of 8192 x 7168: 257 us against 86, 5.5 TB/s). wpr warps share a row; a CTA holds as many
+// such groups as its warps allow, each with a ring of its own.
+constexpr int kMaxRing = 4;  // 2, 3, 4 and 8 stages measured within 2 %
+constexpr int kMaxGroups = 16;
+// Elements a thread. What a row costs beside its elements (waits, reductions, addresses:
+// some 200 instructions a thread) bounds these kernels before the memory does, so a thread
+// takes as many as the registers hold: 32 forward (16 for rows that one warp holds so), 16
+// backward with its two sums (8: 148 us against 89 for 8192 x 7168).
+constexpr int kForwardEpt = 32, kBackwardEpt = 16;
+constexpr long long kWaitNs = 4000000000LL;  // bound of every device-side wait
+
+struct RingState {
+  uint64_t full[kMaxRing];
+  int abort;
+};
+
+// A group's ring: a stage holds a row of x (forward) or of z and dy (backward), and of r
+// if there is one. What it can read from the launch's arguments it does not keep.
+template <typename T, bool BACK>
+struct Ring {
+  const NormArgs& a;
+  uint8_t* smem;
+  RingState* st;
+  int first, stride;  // the group's rows: first, first + stride, ...
+
+  __device__ __forceinline__ uint32_t bytes() const { return (uint32_t)a.D * sizeof(T); }
+  __device__ __forceinline__ int mats() const { return (BACK ? 2 : 1) + (a.r != nullptr ? 1 : 0); }
+  __device__ __forceinline__ const uint4* stage(int i) const {
+    return reinterpret_cast<const uint4*>(smem + (size_t)(i * mats()) * bytes());
+  }
+  // The group's leader: stage i receives row `row`.
+  __device__ __forceinline__ void load(int i, long long row) const {
+    uint64_t* bar = &st->full[i];
+    uint8_t* to = smem + (size_t)(i * mats()) * bytes();
+    mbar_arrive_expect_tx(bar, bytes() * mats());
+    bulk_load(to, static_cast<const T*>(a.x) + row * a.ld_x, bytes(), bar);
+    if (BACK) bulk_load(to + bytes(), static_cast<const T*>(a.dy) + row * a.ld_dy, bytes(), bar);
+    if (a.r != nullptr)
+      bulk_load(to + (BACK ? 2 : 1) * bytes(), static_cast<const T*>(a.r) + row * a.ld_r, bytes(), bar);
+  }
+};
+
+// Every thread of the CTA, once `st` of its group is set; `leader`: the group's first thread.
+template <typename T, bool BACK>
+__device__ __forceinline__ void ring_begin(const Ring<T, BACK>& g, bool leader) {
+  if (leader) {
+    for (int i = 0; i < g.a.stages; ++i) mbar_init(&g.st->full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    g.st->abort = 0;
+  }
+  __syncthreads();
+  if (leader)
+    for (int i = 0; i < g.a.stages; ++i) {
+      const long long row = g.first + (long long)i * g.stride;
+      if (row < g.a.n) g.load(i, row);
+    }
+}
+// The stage's phase is complete: its row is there. After a wait that ran out the group carries on
+// with what is there (the status says that its results are void), so that every thread
+// meets the same barriers.
+template <typename T, bool BACK>
+__device__ __forceinline__ void ring_wait(const Ring<T, BACK>& g, int stage, int phase) {
+  mbar_wait_bounded(&g.st->full[stage], phase, &g.st->abort, kWaitNs, g.a.status, 0x51000000u);
+}
+// After an abort: the copies in flight of the group's `rows` rows land before it leaves.
+template <typename T, bool BACK>
+__device__ __forceinline__ void ring_end(const Ring<T, BACK>& g, bool leader, int rows) {
+  if (leader && *(volatile int*)&g.st->abort) {
+    volatile int never = 0;
+    for (int it = max(0, rows - g.a.stages); it < rows; ++it)
+      mbar_wait_bounded(&g.st->full[it % g.a.stages], (it / g.a.stages) & 1, &never, kWaitNs, g.a.status,
+                        0x52000000u);
+  }
+}
+
+// Two fp32 values in a register pair: one instruction works on both (the same roundings as
+// two). The backward kernel's arithmetic is in pairs (8192 x 7168: 89 -> 86 us, 2048 x 7168:
+// 36 -> 32 us); in the forward kernel they cost more registers than its 64 (90 -> 98 us).
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  }
+  __device__ __forceinline__ float2 get() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& u, F2 (&f)[Vec<T>::kN / 2]) {
+  float g[Vec<T>::kN];
+  unpack<T>(u, g);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kN / 2; ++i) f[i] = F2(g[2 * i], g[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_pairs(const F2 (&f)[Vec<T>::kN / 2]) {
+  float g[Vec<T>::kN];
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kN / 2; ++i) {
+    const float2 p = f[i].get();
+    g[2 * i] = p.x;
+    g[2 * i + 1] = p.y;
+  }
+  return pack<T>(g);
+}
+// A vector of a row that the ring kernels write: 16 bytes where the rows allow it.
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* row, int v, bool vec, const F2 (&f)[Vec<T>::kN / 2]) {
+  const uint4 u = pack_pairs<T>(f);
+  if (vec) {
+    reinterpret_cast<uint4*>(row)[v] = u;
+  } else {
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kN; ++i) row[v * Vec<T>::kN + i] = e[i];
+  }
+}
+
+// The parameters of a thread's columns, kept in registers as they lie in memory: WT is the
+// rows' type or float.
+template <typename T, typename WT>
+struct Params {
+  static constexpr int kWords = Vec<T>::kN * (int)sizeof(WT) / 16;  // 16-byte words of a vector
+  uint4 u[kWords];
+  __device__ __forceinline__ void load(const void* p, int v, bool in, float none) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if (p != nullptr && in) {
+        u[i] = __ldg(static_cast<const uint4*>(p) + v * kWords + i);
+      } else {
+        float f[Vec<WT>::kN];
+#pragma unroll
+        for (int e = 0; e < Vec<WT>::kN; ++e) f[e] = none;
+        u[i] = pack<WT>(f);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(F2 (&f)[Vec<T>::kN / 2]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      // Unpacked anew for every row: left to itself the compiler keeps the unpacked values
+      // over the loop, twice the registers, and spills.
+      uint4 c = u[i];
+      asm volatile("" : "+r"(c.x), "+r"(c.y), "+r"(c.z), "+r"(c.w));
+      F2 q[Vec<WT>::kN / 2];
+      unpack_pairs<WT>(c, q);
+#pragma unroll
+      for (int e = 0; e < Vec<WT>::kN / 2; ++e) f[i * (Vec<WT>::kN / 2) + e] = q[e];
+    }
+  }
+};
+
+// The parameters stand in shared memory as they lie in global memory (the registers are the
+// row's). z leaves before the reductions, the row's distances from the mean replace it.
+template <typename T, typename WT, int EPT>
+__global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int N = Vec<T>::kN, PERV = EPT / N, WORDS = N * (int)sizeof(WT) / 16;
+  extern __shared__ __align__(128) uint8_t ring_smem[];  // [2][D] parameters, then the rings
+  __shared__ RingState rs[kMaxGroups];
+  __shared__ float red[kMaxGroups][2][32];
+  const int warp = threadIdx.x >> 5, grp = warp / a.wpr, wr = warp % a.wpr;
+  const int groups = (blockDim.x >> 5) / a.wpr;
+  const int t = wr * 32 + (threadIdx.x & 31), step = a.wpr * 32, nv = a.D / N;
+  const int words = nv * WORDS;  // 16-byte words of a parameter
+  uint4* ws = reinterpret_cast<uint4*>(ring_smem);
+  {
+    float one[Vec<WT>::kN], zero[Vec<WT>::kN];
+#pragma unroll
+    for (int e = 0; e < Vec<WT>::kN; ++e) one[e] = 1.f, zero[e] = 0.f;
+    const uint4 w1 = pack<WT>(one), b0 = pack<WT>(zero);
+    for (int i = threadIdx.x; i < words; i += blockDim.x) {
+      ws[i] = a.w != nullptr ? __ldg(static_cast<const uint4*>(a.w) + i) : w1;
+      ws[words + i] = a.b != nullptr ? __ldg(static_cast<const uint4*>(a.b) + i) : b0;
+    }
+  }
+  const int mats = a.r != nullptr ? 2 : 1;
+  // At most 2^31 rows, and an index past n by less than a stride: 64 bits where it matters.
+  const int first = (int)min((long long)blockIdx.x * groups + grp, a.n);
+  const Ring<T, false> g{a,
+                         ring_smem + (size_t)words * 32 + (size_t)grp * a.stages * mats * a.D * sizeof(T),
+                         &rs[grp], first, (int)gridDim.x * groups};
+  ring_begin(g, t == 0);
+  const float inv_d = 1.0f / (float)a.D;
+  int it = 0, st = 0, phase = 0;
+  for (long long row = g.first; row < a.n; row += g.stride, ++it) {
+    T* y = static_cast<T*>(a.y) + row * a.ld_y;
+    T* z = a.z != nullptr ? static_cast<T*>(a.z) + row * a.ld_z : nullptr;
+    ring_wait(g, st, phase);
+    const uint4* xs = g.stage(st);
+    F2 f[PERV][N / 2];
+    F2 s2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < PERV; ++i) {
+      const int v = t + i * step;
+      if (v < nv) {
+        unpack_pairs<T>(xs[v], f[i]);
+        if (mats == 2) {
+          F2 q[N / 2];
+          unpack_pairs<T>(xs[nv + v], q);
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) f[i][e] = f[i][e] + q[e];
+        }
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) s2 = s2 + f[i][e];
+      }
+    }
+    float s[1] = {s2.get().x + s2.get().y};
+    row_sum<1, 16>(s, red[grp][0], a.wpr, wr, grp);
+    // Every thread has read the stage: it takes the row `stages` ahead.
+    const long long next = row + (long long)a.stages * g.stride;
+    if (t == 0 && next < a.n) g.load(st, next);
+    if (++st == a.stages) {
+      st = 0;
+      phase ^= 1;
+    }
+    const float mean = s[0] * inv_d;
+    const F2 minus_mean(-mean, -mean);
+    F2 q2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < PERV; ++i) {
+      const int v = t + i * step;
+      if (v < nv) {
+        if (z != nullptr) store_pairs<T>(z, v, a.vz, f[i]);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          f[i][e] = f[i][e] + minus_mean;
+          q2 = fma2(f[i][e], f[i][e], q2);
+        }
+      }
+    }
+    float q[1] = {q2.get().x + q2.get().y};
+    row_sum<1, 16>(q, red[grp][1], a.wpr, wr, grp);
+    const float rstd = 1.0f / sqrtf(q[0] * inv_d + a.eps);
+    if (t == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    const F2 rr(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < PERV; ++i) {
+      const int v = t + i * step;
+      if (v >= nv) break;
+#pragma unroll
+      for (int h = 0; h < WORDS; ++h) {
+        F2 wf[Vec<WT>::kN / 2], bf[Vec<WT>::kN / 2];
+        unpack_pairs<WT>(ws[v * WORDS + h], wf);
+        unpack_pairs<WT>(ws[words + v * WORDS + h], bf);
+#pragma unroll
+        for (int e = 0; e < Vec<WT>::kN / 2; ++e) {
+          F2& x = f[i][h * (Vec<WT>::kN / 2) + e];
+          x = fma2(x * rr, wf[e], bf[e]);
+        }
+      }
+      store_pairs<T>(y, v, a.vy, f[i]);
+    }
+  }
+  ring_end(g, t == 0, it);
+}
+
+template <typename T, typename WT, int EPT>
+__global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int N = Vec<T>::kN, PERV = EPT / N;
+  allow_dependent_launch();
+  extern __shared__ __align__(128) uint8_t ring_smem[];
+  __shared__ RingState rs[kMaxGroups];
+  __shared__ float red[kMaxGroups][2][64];
+  const int warp = threadIdx.x >> 5, grp = warp / a.wpr, wr = warp % a.wpr;
+  const int groups = (blockDim.x >> 5) / a.wpr;
+  const int t = wr * 32 + (threadIdx.x & 31), step = a.wpr * 32, nv = a.D / N;
+  const float inv_d = 1.0f / (float)a.D;
+  // At most 2^31 rows, and an index past n by less than a stride: 64 bits where it matters.
+  const int first = (int)min((long long)blockIdx.x * groups + grp, a.n);
+  const Ring<T, true> g{a, ring_smem + (size_t)grp * a.stages * (a.r != nullptr ? 3 : 2) * a.D * sizeof(T), &rs[grp], first, (int)gridDim.x * groups};
+  ring_begin(g, t == 0);
+
+  Params<T, WT> w[PERV];
+#pragma unroll
+  for (int i = 0; i < PERV; ++i) {
+    const int v = t + i * step;
+    w[i].load(a.w, v, v < nv, 1.f);
+  }
+  F2 dw[PERV][N / 2], db[PERV][N / 2];
+#pragma unroll
+  for (int i = 0; i < PERV; ++i)
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) dw[i][e] = db[i][e] = F2(0.f, 0.f);
+  float mean_n = 0.f, rstd_n = 0.f;
+  if (g.first < a.n) {
+    mean_n = __ldg(a.mean + g.first);
+    rstd_n = __ldg(a.rstd + g.first);
+  }
+  int it = 0, st = 0, phase = 0;
+  for (long long row = g.first; row < a.n; row += g.stride, ++it) {
+    const float mean = mean_n, rstd = rstd_n;
+    if (row + g.stride < a.n) {  // the next row's, a row ahead
+      mean_n = __ldg(a.mean + row + g.stride);
+      rstd_n = __ldg(a.rstd + row + g.stride);
+    }
+    ring_wait(g, st, phase);
+    const uint4* zs = g.stage(st);
+    const F2 minus_mean(-mean, -mean), rr(rstd, rstd);
+    F2 xh[PERV][N / 2], d[PERV][N / 2];
+    uint4 up[PERV];
+    F2 s1(0.f, 0.f), s2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < PERV; ++i) {
+      const int v = t + i * step;
+      if (v < nv) {
+        F2 wf[N / 2];
+        unpack_pairs<T>(zs[v], xh[i]);
+        unpack_pairs<T>(zs[nv + v], d[i]);
+        if (a.r != nullptr) up[i] = zs[2 * nv + v];
+        w[i].get(wf);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          xh[i][e] = (xh[i][e] + minus_mean) * rr;
+          dw[i][e] = fma2(d[i][e], xh[i][e], dw[i][e]);
+          db[i][e] = db[i][e] + d[i][e];
+          d[i][e] = d[i][e] * wf[e];
+          s1 = s1 + d[i][e];
+          s2 = fma2(d[i][e], xh[i][e], s2);
+        }
+      }
+    }
+    float s[2] = {s1.get().x + s1.get().y, s2.get().x + s2.get().y};
+    row_sum<2, 16>(s, red[grp][it & 1], a.wpr, wr, grp);
+    const long long next = row + (long long)a.stages * g.stride;
+    if (t == 0 && next < a.n) g.load(st, next);
+    if (++st == a.stages) {
+      st = 0;
+      phase ^= 1;
+    }
+    const F2 m1(-s[0] * inv_d, -s[0] * inv_d), m2(-s[1] * inv_d, -s[1] * inv_d);
+    T* dx = static_cast<T*>(a.y) + row * a.ld_y;
+#pragma unroll
+    for (int i = 0; i < PERV; ++i) {
+      const int v = t + i * step;
+      if (v >= nv) break;
+      F2 o[N / 2];
+      if (a.r != nullptr) {
+        unpack_pairs<T>(up[i], o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) o[e] = F2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) o[e] = fma2(rr, fma2(xh[i][e], m2, d[i][e] + m1), o[e]);
+      store_pairs<T>(dx, v, a.vy, o);
+    }
+  }
+  ring_end(g, t == 0, it);
+  if (groups > 1) {
+    F2* gather = reinterpret_cast<F2*>(ring_smem);  // 2 x (EPT x step floats), after the ring
+    const int width = EPT * step / 2;
+    for (int q = 0; q < groups; ++q) {  // the groups' sums in their order
+      __syncthreads();
+      if (grp == q) {
+#pragma unroll
+        for (int i = 0; i < PERV; ++i)
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) {
+            F2* p = gather + ((size_t)i * (N / 2) + e) * step + t;
+            if (q > 0) {
+              dw[i][e] = dw[i][e] + p[0];
+              db[i][e] = db[i][e] + p[width];
+            }
+            if (q + 1 < groups) {
+              p[0] = dw[i][e];
+              p[width] = db[i][e];
+            }
+          }
+      }
+    }
+    if (grp != groups - 1) return;
+  }
+  float* pw = a.part + (size_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+  for (int i = 0; i < PERV; ++i) {
+    const int v = t + i * step;
+    if (v < nv)
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) {  // D is even: pairs on 8 bytes
+        *reinterpret_cast<float2*>(pw + v * N + 2 * e) = dw[i][e].get();
+        *reinterpret_cast<float2*>(pw + a.D + v * N + 2 * e) = db[i][e].get();
+      }
+  }
+}
+
+// dw and db from the CTAs' sums: 32 columns a CTA, sixteen warps share the rows, then
+// their sums in order. Launched to start while the kernel before it ends; it waits for
+// that kernel's sums itself.
+constexpr int kParamWarps = 16;
+__global__ void __launch_bounds__(32 * kParamWarps)
+    norm_params_kernel(const float* part, int rows, int D, int wtype, void* dw, void* db) {
+  __shared__ float red[2][kParamWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  wait_prior_grid();
   float s = 0.f, q = 0.f;
-  if (c < D)
-    for (int r = warp; r < rows; r += 8) {
+  if (c < D) {
+#pragma unroll 8
+    for (int r = warp; r < rows; r += kParamWarps) {
       const float* p = part + (size_t)r * 2 * D + c;
       s += p[0];
       q += p[D];
     }
+  }
   red[0][warp][lane] = s;
   red[1][warp][lane] = q;
   __syncthreads();
   if (warp < 2 && c < D) {
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += red[warp][i][lane];
+    for (int i = 0; i < kParamWarps; ++i) v += red[warp][i][lane];
     void* out = warp == 0 ? dw : db;
     if (out != nullptr) store_from_f32(out, wtype, c, v);
   }
@@ -473,13 +885,20 @@ bool rows16(const void* q, long long ld, const moe_norm_args* p) {
 struct NormShape {
   int ept, wpr, warps;  // ept 0: the long-row kernel
 };
-NormShape norm_shape(const moe_norm_args* p, int num_sms, bool backward) {
+NormShape norm_shape(const moe_norm_args* p, bool vec, int num_sms, bool backward) {
   auto wpr = [&](int ept) { return (p->D + 32 * ept - 1) / (32 * ept); };
   // Few rows: as many threads a row as there are. Else few enough that a warp keeps
   // several loads in flight; the backward pass holds two sums for each element too.
   const bool few = p->n < 2 * num_sms;
   NormShape s{};
-  s.ept = few || wpr(8) <= 4 ? 8 : backward || wpr(16) <= 8 ? 16 : 32;
+  if (few)
+    s.ept = 8;
+  else if (backward)
+    s.ept = p->D <= (vec ? 256 : 2048) ? 8 : 16;
+  else if (!vec)
+    s.ept = p->D <= 2048 ? 8 : p->D <= 8192 ? 16 : 32;
+  else
+    s.ept = p->D <= 256 ? 8 : p->D <= 512 || (p->D > 1024 && p->D <= 4096) ? 16 : 32;
   if (wpr(s.ept) > max_warps(s.ept)) s.ept = backward ? 16 : 32;
   s.wpr = wpr(s.ept);
   if (s.wpr > max_warps(s.ept)) return NormShape{0, 32, 32};
@@ -487,34 +906,114 @@ NormShape norm_shape(const moe_norm_args* p, int num_sms, bool backward) {
   return s;
 }
 
-template <typename T>
+constexpr int kRingBytes = 200 * 1024;  // shared memory of an SM that the rings share
+
+// Whether the ring kernel takes these rows, and its launch: 16-byte rows, enough of them
+// that every group walks two or more. 16 warps an SM of 128 registers a thread: one CTA
+// forward, one or two backward.
+struct RingShape {
+  int ept, wpr, groups, stages, ctas;  // ctas: on an SM; 0: not taken
+  size_t smem;
+};
+RingShape ring_shape(const moe_norm_args* p, bool aligned, int mats, int num_sms, bool backward) {
+  RingShape r{};
+  const size_t row = (size_t)p->D * type_bytes(p->dtype);
+  r.ept = backward ? kBackwardEpt : p->D <= 512 ? 16 : kForwardEpt;
+  r.wpr = (p->D + 32 * r.ept - 1) / (32 * r.ept);
+  if (!aligned || row % 16 != 0 || r.wpr > 16) return r;
+  r.groups = std::max(1, (backward ? 8 : 16) / r.wpr);
+  r.ctas = backward ? std::max(1, 16 / (r.wpr * r.groups)) : 1;
+  const size_t params = backward ? 0 : 2 * (size_t)p->D * type_bytes(p->wtype);
+  const size_t stage = (size_t)r.groups * mats * row, room = kRingBytes / r.ctas;
+  r.stages = room > params ? (int)std::min<size_t>(kMaxRing, (room - params) / stage) : 0;
+  r.smem = params + r.stages * stage;
+  // The groups' sums of the backward pass meet in the ring's memory.
+  if (r.stages < 2 || p->n < 2LL * r.ctas * r.groups * num_sms ||
+      (backward && r.groups > 1 && r.smem < (size_t)2 * r.ept * 32 * r.wpr * sizeof(float)))
+    r.ctas = 0;
+  return r;
+}
+
+template <typename K>
+cudaError_t launch_ring(K kernel, std::atomic<uint64_t>* ready, const NormArgs& a, const RingShape& r,
+                        int grid, cudaStream_t s) {
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), ready);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, 32 * r.wpr * r.groups, r.smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, typename WT>
+cudaError_t launch_ring_of(bool backward, const NormArgs& a, const RingShape& r, int grid, cudaStream_t s) {
+  static std::atomic<uint64_t> ready_f{0}, ready_n{0}, ready_b{0};
+  if (backward)
+    return launch_ring(norm_backward_ring_kernel<T, WT, kBackwardEpt>, &ready_b, a, r, grid, s);
+  return r.ept == 16 ? launch_ring(norm_ring_kernel<T, WT, 16>, &ready_n, a, r, grid, s)
+                     : launch_ring(norm_ring_kernel<T, WT, kForwardEpt>, &ready_f, a, r, grid, s);
+}
+int run_ring(bool backward, int dtype, NormArgs& a, const RingShape& r, int grid, cudaStream_t s) {
+  a.wpr = r.wpr;
+  a.stages = r.stages;
+  a.status = ops_status();
+  if (a.status == nullptr) return MOE_ERR_CUDA;
+  const bool wide = a.wtype == MOE_FP32;
+  cudaError_t e;
+  if (dtype == MOE_FP32)
+    e = launch_ring_of<float, float>(backward, a, r, grid, s);
+  else if (dtype == MOE_BF16)
+    e = wide ? launch_ring_of<__nv_bfloat16, float>(backward, a, r, grid, s)
+             : launch_ring_of<__nv_bfloat16, __nv_bfloat16>(backward, a, r, grid, s);
+  else
+    e = wide ? launch_ring_of<__half, float>(backward, a, r, grid, s)
+             : launch_ring_of<__half, __half>(backward, a, r, grid, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <typename T, int N>
 void launch_forward(const NormArgs& a, const NormShape& sh, cudaStream_t s) {
   if (sh.ept == 0) {
-    norm_long_kernel<T><<<(unsigned)a.n, kLoopThreads, 0, s>>>(a);
+    norm_long_kernel<T, N><<<(unsigned)a.n, kLoopThreads, 0, s>>>(a);
     return;
   }
   const int rows = sh.warps / sh.wpr, threads = 32 * sh.warps;
   const unsigned grid = (unsigned)((a.n + rows - 1) / rows);
   if (sh.ept == 8)
-    norm_kernel<T, 8><<<grid, threads, 0, s>>>(a);
+    norm_kernel<T, 8, N><<<grid, threads, 0, s>>>(a);
   else if (sh.ept == 16)
-    norm_kernel<T, 16><<<grid, threads, 0, s>>>(a);
+    norm_kernel<T, 16, N><<<grid, threads, 0, s>>>(a);
   else
-    norm_kernel<T, 32><<<grid, threads, 0, s>>>(a);
+    norm_kernel<T, 32, N><<<grid, threads, 0, s>>>(a);
 }
 
-template <typename T>
+template <typename T, int N>
 void launch_backward(const NormArgs& a, const NormShape& sh, int grid, cudaStream_t s) {
   if (sh.ept == 0) {
-    norm_backward_long_kernel<T><<<grid, kLoopThreads, 0, s>>>(a);
+    norm_backward_long_kernel<T, N><<<grid, kLoopThreads, 0, s>>>(a);
     return;
   }
   const int rows = sh.warps / sh.wpr, threads = 32 * sh.warps;
   const size_t smem = rows > 1 ? (size_t)2 * sh.ept * sh.wpr * 32 * sizeof(float) : 0;
   if (sh.ept == 8)
-    norm_backward_kernel<T, 8><<<grid, threads, smem, s>>>(a);
+    norm_backward_kernel<T, 8, N><<<grid, threads, smem, s>>>(a);
   else
-    norm_backward_kernel<T, 16><<<grid, threads, smem, s>>>(a);
+    norm_backward_kernel<T, 16, N><<<grid, threads, smem, s>>>(a);
+}
+template <typename T>
+void launch_rows(bool backward, bool vec, const NormArgs& a, const NormShape& sh, int grid, cudaStream_t s) {
+  constexpr int N = Vec<T>::kN;
+  if (backward)
+    vec ? launch_backward<T, N>(a, sh, grid, s) : launch_backward<T, 1>(a, sh, grid, s);
+  else
+    vec ? launch_forward<T, N>(a, sh, s) : launch_forward<T, 1>(a, sh, s);
+}
+int run_rows(bool backward, int dtype, bool vec, const NormArgs& a, const NormShape& sh, int grid,
+             cudaStream_t s) {
+  if (dtype == MOE_BF16)
+    launch_rows<__nv_bfloat16>(backward, vec, a, sh, grid, s);
+  else if (dtype == MOE_FP16)
+    launch_rows<__half>(backward, vec, a, sh, grid, s);
+  else
+    launch_rows<float>(backward, vec, a, sh, grid, s);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -558,16 +1057,14 @@ int moe_layer_norm(const moe_norm_args* p, moe_stream_t stream) {
   a.vy = rows16(p->y, p->ld_y, p);
   a.vz = rows16(p->z, p->ld_z, p);
   a.vw = aligned_to(p->w, 16) && aligned_to(p->b, 16);
-  const NormShape sh = norm_shape(p, sms, false);
-  a.wpr = sh.wpr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (p->dtype == MOE_BF16)
-    launch_forward<__nv_bfloat16>(a, sh, s);
-  else if (p->dtype == MOE_FP16)
-    launch_forward<__half>(a, sh, s);
-  else
-    launch_forward<float>(a, sh, s);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const int mats = p->r != nullptr ? 2 : 1;
+  const RingShape ring = ring_shape(p, a.vx && a.vw && (p->r == nullptr || a.vr), mats, sms, false);
+  if (ring.ctas > 0) return run_ring(false, p->dtype, a, ring, ring.ctas * sms, s);
+  const bool vec = a.vx && a.vy && (p->r == nullptr || a.vr) && (p->z == nullptr || a.vz);
+  const NormShape sh = norm_shape(p, vec, sms, false);
+  a.wpr = sh.wpr;
+  return run_rows(false, p->dtype, vec, a, sh, 0, s);
 }
 
 size_t moe_layer_norm_workspace(long long n, int D) {
@@ -596,7 +1093,7 @@ int moe_layer_norm_backward(const moe_norm_args* p, void* workspace, size_t work
   if (!check_rows(p->z, p->ld_z, p, true) || !check_rows(p->dy, p->ld_dy, p, true) ||
       !check_rows(p->dz, p->ld_dz, p, false) || !check_rows(p->dx, p->ld_dx, p, true) ||
       p->mean == nullptr || p->rstd == nullptr || !aligned_to(p->mean, 4) || !aligned_to(p->rstd, 4) ||
-      workspace == nullptr || !aligned_to(workspace, 4))
+      workspace == nullptr || !aligned_to(workspace, 16))
     return MOE_ERR_ARG;
   if (workspace_bytes < moe_layer_norm_workspace(p->n, p->D)) return MOE_ERR_WORKSPACE;
   rc = ops_device(&sms);
@@ -622,20 +1119,27 @@ int moe_layer_norm_backward(const moe_norm_args* p, void* workspace, size_t work
   a.vdy = rows16(p->dy, p->ld_dy, p);
   a.vy = rows16(p->dx, p->ld_dx, p);
   a.vw = aligned_to(p->w, 16);
-  const NormShape sh = norm_shape(p, sms, true);
-  a.wpr = sh.wpr;
-  const int rows = sh.ept == 0 ? 1 : sh.warps / sh.wpr;
-  const int grid = (int)std::min<long long>((p->n + rows - 1) / rows, std::min(kNormParts, 2 * sms));
-  if (p->dtype == MOE_BF16)
-    launch_backward<__nv_bfloat16>(a, sh, grid, s);
-  else if (p->dtype == MOE_FP16)
-    launch_backward<__half>(a, sh, grid, s);
-  else
-    launch_backward<float>(a, sh, grid, s);
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-  if (p->dw != nullptr || p->db != nullptr)
-    norm_params_kernel<<<(p->D + 31) / 32, 256, 0, s>>>(a.part, grid, p->D, p->wtype, p->dw, p->db);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const int mats = p->dz != nullptr ? 3 : 2;
+  const RingShape ring =
+      ring_shape(p, a.vx && a.vdy && a.vw && (p->dz == nullptr || a.vr), mats, sms, true);
+  int grid;
+  if (ring.ctas > 0) {
+    grid = std::min(kNormParts, ring.ctas * sms);
+    rc = run_ring(true, p->dtype, a, ring, grid, s);
+    if (rc != MOE_OK) return rc;
+  } else {
+    const bool vec = a.vx && a.vdy && a.vy && (p->dz == nullptr || a.vr);
+    const NormShape sh = norm_shape(p, vec, sms, true);
+    a.wpr = sh.wpr;
+    const int rows = sh.ept == 0 ? 1 : sh.warps / sh.wpr;
+    grid = (int)std::min<long long>((p->n + rows - 1) / rows, std::min(kNormParts, 2 * sms));
+    rc = run_rows(true, p->dtype, vec, a, sh, grid, s);
+    if (rc != MOE_OK) return rc;
+  }
+  if (p->dw == nullptr && p->db == nullptr) return MOE_OK;
+  const cudaError_t e = launch_behind(norm_params_kernel, dim3((p->D + 31) / 32), dim3(32 * kParamWarps), 0, s,
+                                      (const float*)a.part, grid, p->D, p->wtype, p->dw, p->db);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"
