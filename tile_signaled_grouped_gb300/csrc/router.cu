@@ -14,9 +14,10 @@
 //
 // Which experts are chosen is decided as in 64 bits. The scores are computed in 32 bits
 // with a known error bound; where two neighbours in the order of the winners (or the
-// last group kept and the first one dropped) lie within it, the token is decided again
-// with 64-bit scores. Without a bias the order of the c_e is that of the l_e, which
-// needs no rounding, so only sums of group scores can be close then.
+// last group kept and the first one dropped) lie within it, those that may belong on
+// either side are scored again in 64 bits and ordered by that. Without a bias the order of
+// the c_e is that of the l_e, which needs no rounding, so only sums of group scores can be
+// close then.
 #include <algorithm>
 #include <atomic>
 
@@ -64,6 +65,7 @@ struct RouterArgs {
   void* dl;             // backward: [n][ld_dl]
   long long n, ld, ld_dl;
   int dtype, E, k, G, TG, GT, score, renorm;
+  int lpg;  // lanes of a group: the largest power of two that leaves each one its own
   float scale;
 };
 
@@ -76,7 +78,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ float warp_max(float v) {
   return key_float(__reduce_max_sync(kAll, float_key(v == v ? v : -INFINITY)));
 }
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+// Within 5 steps of fp32 (expf 2, the fast division 2, two roundings); an exponential that
+// the fast division takes for infinity (beyond 2^126) belongs to a score below 1e-37.
+__device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 
 // The two largest of (a, b, ...) so far.
 template <typename F>
@@ -85,48 +89,14 @@ __device__ __forceinline__ void top2(F v, F& t1, F& t2) {
   t1 = v > t1 ? v : t1;
 }
 
-// Bit g of the result: group g stays. val: the E values a group is judged by, in shared
-// memory. Lanes share the groups evenly (a power of two of lanes for each). *last and
-// *first receive the smallest score kept and the largest dropped (-inf if none is).
-template <typename F>
-__device__ __forceinline__ uint32_t keep_groups(const RouterArgs& a, const F* val, int lane, F* last,
-                                                F* first) {
-  int lpg = 1;
-  while (lpg * 2 * a.G <= 32) lpg *= 2;
-  const int per = a.E / a.G, g = lane / lpg, sub = lane % lpg;
-  const F low = -INFINITY;
-  F t1 = low, t2 = low;
-  if (g < a.G)
-    for (int i = sub; i < per; i += lpg) top2(val[g * per + i], t1, t2);
-  for (int o = lpg / 2; o; o >>= 1) {
-    const F u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
-    top2(u1, t1, t2);
-    top2(u2, t1, t2);
-  }
-  F sum = a.GT > 1 && per > 1 ? t1 + t2 : t1;
-  sum = __shfl_sync(kAll, sum, min(lane * lpg, 31));  // lane g: group g
-  int rank = 0;
-  for (int h = 0; h < a.G; ++h) {
-    const F o = __shfl_sync(kAll, sum, h);
-    rank += (o > sum) | ((o == sum) & (h < lane));
-  }
-  const uint32_t in = __ballot_sync(kAll, lane < a.G);
-  const uint32_t kept = __ballot_sync(kAll, rank < a.TG) & in;
-  const uint32_t at_last = __ballot_sync(kAll, rank == a.TG - 1) & in;
-  const uint32_t at_first = __ballot_sync(kAll, rank == a.TG) & in;
-  const F vl = __shfl_sync(kAll, sum, at_last ? __ffs(at_last) - 1 : 0);
-  const F vf = __shfl_sync(kAll, sum, at_first ? __ffs(at_first) - 1 : 0);
-  *last = vl;
-  *first = at_first ? vf : low;
-  return kept;
-}
-
-// The token decided with 64-bit scores; returns the id of slot `lane` (lane < k). buf:
-// E doubles of shared memory. Rare, so short rather than fast.
-__device__ __noinline__ int route_exact(const RouterArgs& a, const void* row, double* buf, int lane) {
-  __syncwarp();
-  double mx = -INFINITY, sum = 0;
-  if (a.score == MOE_SCORE_SOFTMAX) {
+// What the order is decided by in 64 bits: the token's scores, and the sum of its
+// exponentials for a softmax (the whole warp computes it).
+struct Exact {
+  const RouterArgs& a;
+  const void* row;
+  double mx, sum;
+  __device__ Exact(const RouterArgs& args, const void* r, int lane) : a(args), row(r), mx(-INFINITY), sum(0) {
+    if (a.score != MOE_SCORE_SOFTMAX) return;
     for (int e = lane; e < a.E; e += 32) {
       const double l = load_as_f32(row, a.dtype, e);
       mx = l > mx ? l : mx;
@@ -135,35 +105,116 @@ __device__ __noinline__ int route_exact(const RouterArgs& a, const void* row, do
       const double v = __shfl_xor_sync(kAll, mx, o);
       mx = v > mx ? v : mx;
     }
-    for (int e = lane; e < a.E; e += 32) {
-      const double v = mx == -INFINITY ? 0.0 : exp((double)load_as_f32(row, a.dtype, e) - mx);
-      sum += v;
-    }
+    if (mx == -INFINITY) return;
+    for (int e = lane; e < a.E; e += 32) sum += exp((double)load_as_f32(row, a.dtype, e) - mx);
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
   }
-  for (int e = lane; e < a.E; e += 32) {
+  // c of expert e (NaN: -inf).
+  __device__ double at(int e) const {
     const double l = load_as_f32(row, a.dtype, e);
-    double c = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l))
-               : sum == 0.0                 ? 0.0
-                                            : exp(l - mx) / sum;
+    double c = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l)) : sum == 0.0 ? 0.0 : exp(l - mx) / sum;
     if (a.bias != nullptr) c += (double)__ldg(a.bias + e);
-    buf[e] = c == c ? c : -INFINITY;
+    return c == c ? c : -INFINITY;
   }
-  __syncwarp();
-  uint32_t kept = kAll;
-  if (a.G > 1) {
-    double x, y;
-    kept = keep_groups<double>(a, buf, lane, &x, &y);
-    __syncwarp();
+};
+
+// This group's score in 64 bits, in every lane.
+__device__ double exact_group(const Exact& x, int g, int lane) {
+  const int per = x.a.E / x.a.G;
+  double t1 = -INFINITY, t2 = -INFINITY;
+  for (int i = lane; i < per; i += 32) top2(x.at(g * per + i), t1, t2);
+  for (int o = 16; o; o >>= 1) {
+    const double u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
+    top2(u1, t1, t2);
+    top2(u2, t1, t2);
   }
-  if (a.bias == nullptr) {  // the order of the c is that of the scores
-    for (int e = lane; e < a.E; e += 32) {
-      const float l = load_as_f32(row, a.dtype, e);
-      buf[e] = l == l ? l : -INFINITY;
-    }
-    __syncwarp();
+  return x.a.GT > 1 && per > 1 ? t1 + t2 : t1;
+}
+
+// Group g's score stands in lane g (g < G); `may` and `sure` are the groups that may be and
+// that are certainly kept. The rest of the TG places goes by the 64-bit scores.
+__device__ __noinline__ uint32_t settle_groups(const RouterArgs& a, const void* row, uint32_t may,
+                                               uint32_t sure, int lane) {
+  const Exact x(a, row, lane);
+  double mine = -INFINITY;
+  for (uint32_t m = may; m; m &= m - 1) {
+    const double v = exact_group(x, __ffs(m) - 1, lane);
+    if (lane == __ffs(m) - 1) mine = v;
   }
+  int rank = 0;
+  for (uint32_t m = may; m; m &= m - 1) {
+    const int h = __ffs(m) - 1;
+    const double o = __shfl_sync(kAll, mine, h);
+    rank += (o > mine) | ((o == mine) & (h < lane));
+  }
+  return sure | (__ballot_sync(kAll, rank < a.TG - __popc(sure)) & may);
+}
+
+// Bit g of the result: group g stays. val: the E values a group is judged by, in shared
+// memory. Lanes share the groups evenly (a power of two of lanes for each). tol: what two
+// scores may differ by and still be in the other order.
+__device__ __forceinline__ uint32_t keep_groups(const RouterArgs& a, const void* row, const float* val,
+                                                int lane, float tol) {
+  const int per = a.E / a.G, g = lane / a.lpg, sub = lane % a.lpg;
+  float t1 = -INFINITY, t2 = -INFINITY;
+  if (g < a.G) {
+    const float* p = val + g * per;
+#pragma unroll 4
+    for (int i = sub; i < per; i += a.lpg) top2(p[i], t1, t2);
+  }
+  for (int o = a.lpg / 2; o; o >>= 1) {
+    const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
+    top2(u1, t1, t2);
+    top2(u2, t1, t2);
+  }
+  float sum = a.GT > 1 && per > 1 ? t1 + t2 : t1;
+  sum = __shfl_sync(kAll, sum, min(lane * a.lpg, 31));  // lane g: group g
+  int rank = 0;
+  for (int h = 0; h < a.G; ++h) {
+    const float o = __shfl_sync(kAll, sum, h);
+    rank += (o > sum) | ((o == sum) & (h < lane));
+  }
+  const uint32_t in = a.G < 32 ? (1u << a.G) - 1u : kAll;
+  const uint32_t kept = __ballot_sync(kAll, rank < a.TG) & in;
+  const uint32_t at_last = __ballot_sync(kAll, rank == a.TG - 1) & in;
+  const uint32_t at_first = __ballot_sync(kAll, rank == a.TG) & in;
+  if (at_last == 0 || at_first == 0) return kept;  // every group stays (or a score is NaN)
+  const float last = __shfl_sync(kAll, sum, __ffs(at_last) - 1);
+  const float first = __shfl_sync(kAll, sum, __ffs(at_first) - 1);
+  if (!(last - first <= tol)) return kept;  // also -inf - -inf: the ids have decided
+  const uint32_t sure = __ballot_sync(kAll, sum > last + tol) & in;
+  const uint32_t out = __ballot_sync(kAll, sum < first - tol) & in;
+  return settle_groups(a, row, in & ~(sure | out), sure, lane);
+}
+
+// Slot `lane`'s id where the m candidates in lanes 0.. (id in lane) hold every expert that
+// may be among the k: ordered by their 64-bit values, equal ones by id.
+__device__ __noinline__ int settle_slots(const RouterArgs& a, const void* row, int id, int m, int lane) {
+  const Exact x(a, row, lane);
+  const double mine = lane < m ? x.at(id) : -INFINITY;
+  int rank = 0;
+  for (int h = 0; h < m; ++h) {
+    const double o = __shfl_sync(kAll, mine, h);
+    const int oe = __shfl_sync(kAll, id, h);
+    rank += (o > mine) | ((o == mine) & (oe < id));
+  }
+  int got = 0;
+  for (int h = 0; h < m; ++h) {  // lane h's candidate goes to slot rank
+    const int r = __shfl_sync(kAll, rank, h), oe = __shfl_sync(kAll, id, h);
+    if (r == lane) got = oe;
+  }
+  return got;
+}
+
+// The k experts of the groups `kept` by their 64-bit values, where more than 32 of them may
+// be among the k; returns the id of slot `lane`. buf: E doubles of shared memory.
+__device__ __noinline__ int settle_all(const RouterArgs& a, const void* row, uint32_t kept, double* buf,
+                                       int lane) {
   const int per = a.E / a.G;
+  const Exact x(a, row, lane);
+  __syncwarp();
+  for (int e = lane; e < a.E; e += 32) buf[e] = x.at(e);
+  __syncwarp();
   uint32_t taken = 0;  // bit i: this lane's expert lane + 32 i
   int mine = 0;
   for (int j = 0; j < a.k; ++j) {
@@ -245,6 +296,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
       inv = 1.0f / sum;
     }
   }
+  uint32_t my_kept = kAll;
   float c[PER];  // what experts are ordered by (NaN: -inf)
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -262,70 +314,69 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
     }
     c[i] = v == v ? v : -INFINITY;
   }
-  // How far a score in 32 bits may be off: expf 2 ulp, the sum of the softmax PER + 5
-  // additions, a few roundings more; at most `eps` for s <= smax. c adds its own rounding.
+  // How far a score in 32 bits may be off: 5 steps of fp32 for the sigmoid; for the softmax
+  // 3 for the exponential and its argument, PER + 5 additions in the sum, 2 for the rest.
+  // At most `eps` for scores up to smax; c adds its own rounding.
   const float smax = a.score == MOE_SCORE_SIGMOID ? 1.0f : inv;
-  const float eps = (PER + 16) * 0x1p-23f * smax;
+  const float eps = (a.score == MOE_SCORE_SIGMOID ? 6.f : PER + 12.f) * 0x1p-23f * smax;
 
-  uint32_t kept = kAll;
-  bool close = false;
+  uint32_t open = 0;  // bit i: this lane's candidate i may be chosen
   if (a.G > 1) {
     __syncwarp();
-    float last, first;
-    kept = keep_groups<float>(a, reinterpret_cast<const float*>(buf), lane, &last, &first);
+    float tol = 0.f;  // judged by the l themselves: nothing is rounded
     if (by_score) {
-      float cm = 0.f;  // the largest finite |c|: a sum of two can cancel
+      float cm = smax;  // the largest finite |c|: a sum of two can cancel
       if (a.bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const float v = fabsf(c[i]);
-          cm = v < INFINITY ? fmaxf(cm, v) : cm;
-        }
+        for (int i = 0; i < PER; ++i) cm = fabsf(c[i]) < INFINITY ? fmaxf(cm, fabsf(c[i])) : cm;
         cm = warp_max(cm);
       }
-      close = last - first <= 4.f * eps + 0x1p-21f * fmaxf(cm, smax);  // -inf - -inf: not close
+      tol = 4.f * eps + 0x1p-21f * cm;
     }
-    __syncwarp();
-  }
-  const int per = a.E / a.G;
-  uint32_t my_key = 0, my_id = 0;  // round `lane`'s winner; round k's (the next in line) too
-  const int rounds = a.bias != nullptr ? a.k + 1 : a.k;
-  uint32_t past_key = 0;  // k = 32: the next in line has no lane of its own
-  if (PER <= 8) {
-    int e[PER];
-    int left = 0;
+    const uint32_t kept = keep_groups(a, row, reinterpret_cast<const float*>(buf), lane, by_score ? tol : -1.f);
+    const int per = a.E / a.G, qs = 32 / per, rs = 32 % per;
+    int q = lane / per, r = lane % per;  // of expert lane + 32 i: its group, its place there
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      e[i] = lane + 32 * i;
-      const bool ok = e[i] < a.E && (a.G == 1 || ((kept >> (e[i] / per)) & 1u));
+      open |= (lane + 32 * i < a.E && ((kept >> q) & 1u)) ? 1u << i : 0u;
+      q += qs;
+      r += rs;
+      if (r >= per) {
+        r -= per;
+        ++q;
+      }
+    }
+    if (PER > 8) __syncwarp();
+    my_kept = kept;
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) open |= lane + 32 * i < a.E ? 1u << i : 0u;
+  }
+
+  // Rounds: the warp's best candidate each. Lane j keeps round j's.
+  uint32_t my_key = 0, my_id = 0;
+  int rounds = a.bias != nullptr ? a.k + 1 : a.k;  // with a bias, the next in line too
+  uint32_t past_key = 0;  // the last round's
+  int e[PER <= 8 ? PER : 1];
+  int left = __popc(open);
+  uint32_t order = 0;  // PER <= 8: the candidates in their order, four bits each, the best lowest
+  if constexpr (PER <= 8) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool ok = (open >> i) & 1u;
       c[i] = ok ? c[i] : -INFINITY;
-      e[i] = ok ? e[i] : 0x7FFFFFFF;  // after every candidate, the ones at -inf too
-      left += ok;
+      e[i] = ok ? i : 15;  // after every candidate, the ones at -inf too
     }
     route_sort<PER>(c, e);
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t key = left > 0 ? float_key(c[0]) : 0u;  // 0: no candidate (keys are larger)
-      const uint32_t kmax = __reduce_max_sync(kAll, key);
-      const uint32_t emin = __reduce_min_sync(kAll, key == kmax ? (uint32_t)e[0] : kAll);
-      const bool win = left > 0 && (uint32_t)e[0] == emin;
 #pragma unroll
-      for (int i = 0; i + 1 < PER; ++i) {
-        c[i] = win ? c[i + 1] : c[i];
-        e[i] = win ? e[i + 1] : e[i];
-      }
-      left -= win;
-      my_key = lane == j ? kmax : my_key;
-      my_id = lane == j ? emin : my_id;
-      past_key = kmax;
-    }
-  } else {
-    uint32_t open = 0;  // bit i: this lane's candidate i may still be chosen
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      open |= (e < a.E && (a.G == 1 || ((kept >> (e / per)) & 1u))) ? 1u << i : 0u;
-    }
-    for (int j = 0; j < rounds; ++j) {
+    for (int i = 0; i < PER; ++i) order |= (uint32_t)e[i] << (4 * i);
+  }
+  auto round = [&](int j) {
+    uint32_t key, id;
+    if constexpr (PER <= 8) {
+      key = left > 0 ? float_key(c[0]) : 0u;  // 0: no candidate (keys are larger)
+      id = lane + 32 * (order & 15u);
+    } else {
       float bv = -INFINITY;
       int bi = -1;
 #pragma unroll
@@ -334,16 +385,25 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
         bv = better ? c[i] : bv;
         bi = better ? i : bi;
       }
-      const uint32_t be = bi >= 0 ? (uint32_t)(lane + 32 * bi) : kAll;
-      const uint32_t key = bi >= 0 ? float_key(bv) : 0u;
-      const uint32_t kmax = __reduce_max_sync(kAll, key);
-      const uint32_t emin = __reduce_min_sync(kAll, key == kmax ? be : kAll);
-      open &= (bi >= 0 && be == emin) ? ~(1u << bi) : kAll;
-      my_key = lane == j ? kmax : my_key;
-      my_id = lane == j ? emin : my_id;
-      past_key = kmax;
+      key = bi >= 0 ? float_key(bv) : 0u;
+      id = bi >= 0 ? (uint32_t)(lane + 32 * bi) : kAll;
     }
-  }
+    const uint32_t kmax = __reduce_max_sync(kAll, key);
+    const uint32_t emin = __reduce_min_sync(kAll, key == kmax ? id : kAll);
+    const bool win = key != 0u && id == emin;
+    if constexpr (PER <= 8) {
+#pragma unroll
+      for (int i = 0; i + 1 < PER; ++i) c[i] = win ? c[i + 1] : c[i];
+      order = win ? order >> 4 : order;
+      left -= win;
+    } else {
+      open &= win ? ~(1u << (id >> 5)) : kAll;
+    }
+    my_key = lane == j ? kmax : my_key;
+    my_id = lane == j ? emin : my_id;
+    past_key = kmax;
+  };
+  for (int j = 0; j < rounds; ++j) round(j);
   if (a.bias != nullptr) {
     // Neighbours of the order within their error, unless score and bias are equal (then
     // the ids decide, as they did).
@@ -354,13 +414,23 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
     if (lane < a.k && nk != 0u) {
       const float x = key_float(my_key), y = key_float(nk);
       amb = x - y <= 2.f * eps + 0x1p-22f * (fabsf(x) + fabsf(y));
-      if (amb && lane < 31 && (int)my_id < a.E && (int)ni < a.E)
+      if (amb && lane < 31)
         amb = load_as_f32(row, a.dtype, my_id) != load_as_f32(row, a.dtype, ni) ||
               __ldg(a.bias + my_id) != __ldg(a.bias + ni);
     }
-    close |= __any_sync(kAll, amb);
+    if (__any_sync(kAll, amb)) {
+      // Every candidate that may be among the k: those within the error of the k-th.
+      const float border = key_float(__shfl_sync(kAll, my_key, a.k - 1));
+      const float low = border - (2.f * eps + 0x1p-21f * fabsf(border));
+      auto more = [&] { return past_key != 0u && key_float(past_key) >= low; };
+      while (more() && rounds <= 32) round(rounds++);
+      // Without a candidate in line, `rounds` counts the round that found none.
+      if (more())
+        my_id = (uint32_t)settle_all(a, row, my_kept, buf, lane);
+      else
+        my_id = (uint32_t)settle_slots(a, row, (int)my_id, min(rounds - 1, 32), lane);
+    }
   }
-  if (close) my_id = (uint32_t)route_exact(a, row, buf, lane);
 
   const bool in = lane < a.k;
   const float t = in ? load_as_f32(row, a.dtype, my_id) : 0.f;
@@ -445,6 +515,8 @@ RouterArgs router_args(const moe_router_cfg* c, int dtype, long long n, long lon
   a.G = c->groups;
   a.TG = c->topk_groups;
   a.GT = c->group_top;
+  a.lpg = 1;
+  while (a.lpg * 2 * a.G <= 32) a.lpg *= 2;
   a.score = c->score;
   a.renorm = c->renorm;
   a.scale = c->scale;
