@@ -8,9 +8,9 @@
 //   largest c_e stay; the k largest c_e of those are chosen (equal: lower id or group)
 //   w_j = s_j                 or  s_j / (sum of the chosen s)      times `scale`
 //
-// A warp takes a token; lane l holds experts l, l + 32, ... in registers. Bound by
-// instructions at many tokens (the scores are 4 E bytes and the selection some hundred
-// warp instructions), by its chain of warp reductions at few.
+// A warp takes a token, its experts in the lanes' registers. Bound by instructions at many
+// tokens (the scores are 4 E bytes, the selection about a thousand warp instructions), by
+// its chain of warp reductions at few.
 //
 // Which experts are chosen is decided as in 64 bits. The scores are computed in 32 bits
 // with a known error bound; where two neighbours in the order of the winners (or the
@@ -65,6 +65,7 @@ struct RouterArgs {
   void* dl;             // backward: [n][ld_dl]
   long long n, ld, ld_dl;
   int dtype, E, k, G, TG, GT, score, renorm;
+  bool vec;  // scores and bias can be read by vectors of four
   int lpg;  // lanes of a group: the largest power of two that leaves each one its own
   float scale;
 };
@@ -150,25 +151,10 @@ __device__ __noinline__ uint32_t settle_groups(const RouterArgs& a, const void* 
   return sure | (__ballot_sync(kAll, rank < a.TG - __popc(sure)) & may);
 }
 
-// Bit g of the result: group g stays. val: the E values a group is judged by, in shared
-// memory. Lanes share the groups evenly (a power of two of lanes for each). tol: what two
-// scores may differ by and still be in the other order.
-__device__ __forceinline__ uint32_t keep_groups(const RouterArgs& a, const void* row, const float* val,
-                                                int lane, float tol) {
-  const int per = a.E / a.G, g = lane / a.lpg, sub = lane % a.lpg;
-  float t1 = -INFINITY, t2 = -INFINITY;
-  if (g < a.G) {
-    const float* p = val + g * per;
-#pragma unroll 4
-    for (int i = sub; i < per; i += a.lpg) top2(p[i], t1, t2);
-  }
-  for (int o = a.lpg / 2; o; o >>= 1) {
-    const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
-    top2(u1, t1, t2);
-    top2(u2, t1, t2);
-  }
-  float sum = a.GT > 1 && per > 1 ? t1 + t2 : t1;
-  sum = __shfl_sync(kAll, sum, min(lane * a.lpg, 31));  // lane g: group g
+// Bit g of the result: group g stays. sum: lane g's is group g's score (g < G). tol: what
+// two scores may differ by and still be in the other order.
+__device__ __forceinline__ uint32_t rank_groups(const RouterArgs& a, const void* row, float sum, int lane,
+                                                float tol) {
   int rank = 0;
   for (int h = 0; h < a.G; ++h) {
     const float o = __shfl_sync(kAll, sum, h);
@@ -185,6 +171,18 @@ __device__ __forceinline__ uint32_t keep_groups(const RouterArgs& a, const void*
   const uint32_t sure = __ballot_sync(kAll, sum > last + tol) & in;
   const uint32_t out = __ballot_sync(kAll, sum < first - tol) & in;
   return settle_groups(a, row, in & ~(sure | out), sure, lane);
+}
+
+// The sum of a group's group_top largest values, in lane g for group g: each of a group's
+// lpg lanes brings its two largest.
+__device__ __forceinline__ float group_sums(const RouterArgs& a, float t1, float t2, int lane) {
+  for (int o = a.lpg / 2; o; o >>= 1) {
+    const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
+    top2(u1, t1, t2);
+    top2(u2, t1, t2);
+  }
+  const float sum = a.GT > 1 && a.E > a.G ? t1 + t2 : t1;
+  return __shfl_sync(kAll, sum, min(lane * a.lpg, 31));
 }
 
 // Slot `lane`'s id where the m candidates in lanes 0.. (id in lane) hold every expert that
@@ -262,120 +260,166 @@ __device__ __forceinline__ float slot_weight(const RouterArgs& a, float t, bool 
   return S == 0.f ? 0.f : e / S;
 }
 
-// PER: experts a lane holds. Registers for the sorted list of a lane up to PER = 8; above,
-// each round looks through the lane's candidates again.
+// Four or eight scores of a lane, as one or two vector loads.
 template <int PER>
+__device__ __forceinline__ void load_scores(const void* row, int dtype, int e0, float (&l)[PER]) {
+  if (dtype == MOE_FP32) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + e0 + i));
+      l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; i += 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(row) + e0 + i));
+    const float2 p = dtype == MOE_BF16 ? unpack2<__nv_bfloat16>(v.x) : unpack2<__half>(v.x);
+    const float2 q = dtype == MOE_BF16 ? unpack2<__nv_bfloat16>(v.y) : unpack2<__half>(v.y);
+    l[i] = p.x, l[i + 1] = p.y, l[i + 2] = q.x, l[i + 3] = q.y;
+  }
+}
+
+// Lane l holds experts PER l .. PER l + PER - 1: registers for its sorted list up to
+// PER = 8; above, each round looks through the lane's candidates again. WHOLE: E = 32 PER
+// and a power of two of groups, so that a group is a run of whole lanes: its two largest
+// values are among the heads of those lanes' lists, and a group that goes takes its lanes
+// along. Otherwise the values that groups are judged by pass through shared memory.
+template <int PER, bool WHOLE>
 __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_constant__ RouterArgs a) {
+  static_assert(!WHOLE || PER <= 8, "sorted lists");
   extern __shared__ double smem_d[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long tok = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
   if (tok >= a.n) return;
   double* buf = smem_d + (size_t)warp * a.E;
-  const int tb = a.dtype == MOE_FP32 ? 4 : 2;
+  const int tb = a.dtype == MOE_FP32 ? 4 : 2, e0 = lane * PER;
   const void* row = static_cast<const char*>(a.logits) + (size_t)tok * a.ld * tb;
 
-  float l[PER];
+  float c[PER];  // the scores, then what experts are ordered by (NaN: -inf)
+  if (WHOLE && PER >= 4 && a.vec) {
+    if constexpr (PER >= 4) load_scores<PER>(row, a.dtype, e0, c);
+  } else {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < a.E ? load_as_f32(row, a.dtype, e) : -INFINITY;
+    for (int i = 0; i < PER; ++i)
+      c[i] = WHOLE || e0 + i < a.E ? load_as_f32(row, a.dtype, e0 + i) : -INFINITY;
   }
   const bool sums = a.G > 1 && a.GT > 1 && a.E > a.G;  // groups are judged by sums of scores
   const bool by_score = a.bias != nullptr || sums;     // else by the l themselves
   float mx = 0.f, inv = 1.f;
-  if (a.score == MOE_SCORE_SOFTMAX && (by_score || !a.renorm)) {
+  const bool soft = a.score == MOE_SCORE_SOFTMAX && (by_score || !a.renorm);
+  float s[PER];
+  if (soft) {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) m = fmaxf(m, l[i]);
+    for (int i = 0; i < PER; ++i) m = fmaxf(m, c[i]);
     mx = warp_max(m);
     float sum = 0.f;
-    if (mx != -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) sum += expf(l[i] - mx);
-      sum = warp_sum(sum);
-      inv = 1.0f / sum;
+    for (int i = 0; i < PER; ++i) {
+      s[i] = mx == -INFINITY ? 0.f : expf(c[i] - mx);
+      sum += s[i];
     }
+    sum = warp_sum(sum);
+    if (mx != -INFINITY) inv = 1.0f / sum;
   }
-  uint32_t my_kept = kAll;
-  float c[PER];  // what experts are ordered by (NaN: -inf)
+  auto score_of = [&](float l) {
+    return a.score == MOE_SCORE_SIGMOID ? sigmoid(l) : mx == -INFINITY ? 0.f : expf(l - mx) * inv;
+  };
+  if (a.bias != nullptr) {
+    float b[PER];
+    if (WHOLE && PER >= 4 && a.vec) {
+      if constexpr (PER >= 4) load_scores<PER>(a.bias, MOE_FP32, e0, b);
+    } else {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 32 * i;
-    float v = l[i];
-    if (by_score && e < a.E) {
-      const float s = a.score == MOE_SCORE_SIGMOID ? sigmoid(l[i])
-                      : mx == -INFINITY            ? 0.f
-                                                   : expf(l[i] - mx) * inv;
-      const float g = a.bias != nullptr ? s + __ldg(a.bias + e) : s;
-      if (a.bias != nullptr) v = g;
-      if (a.G > 1) reinterpret_cast<float*>(buf)[e] = g == g ? g : -INFINITY;
-    } else if (a.G > 1 && e < a.E) {
-      reinterpret_cast<float*>(buf)[e] = v == v ? v : -INFINITY;
+      for (int i = 0; i < PER; ++i) b[i] = WHOLE || e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.f;
     }
-    c[i] = v == v ? v : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = (soft ? s[i] * inv : sigmoid(c[i])) + b[i];
   }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) c[i] = c[i] == c[i] ? c[i] : -INFINITY;
   // How far a score in 32 bits may be off: 5 steps of fp32 for the sigmoid; for the softmax
   // 3 for the exponential and its argument, PER + 5 additions in the sum, 2 for the rest.
   // At most `eps` for scores up to smax; c adds its own rounding.
   const float smax = a.score == MOE_SCORE_SIGMOID ? 1.0f : inv;
   const float eps = (a.score == MOE_SCORE_SIGMOID ? 6.f : PER + 12.f) * 0x1p-23f * smax;
+  float tol = -1.f;  // of two groups' scores; judged by the l themselves, nothing is rounded
+  if (a.G > 1 && by_score) {
+    float cm = smax;  // the largest finite |c|: a sum of two can cancel
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) cm = fabsf(c[i]) < INFINITY ? fmaxf(cm, fabsf(c[i])) : cm;
+      cm = warp_max(cm);
+    }
+    tol = 4.f * eps + 0x1p-21f * cm;
+  }
 
+  uint32_t kept = kAll;
   uint32_t open = 0;  // bit i: this lane's candidate i may be chosen
-  if (a.G > 1) {
-    __syncwarp();
-    float tol = 0.f;  // judged by the l themselves: nothing is rounded
-    if (by_score) {
-      float cm = smax;  // the largest finite |c|: a sum of two can cancel
-      if (a.bias != nullptr) {
+  if constexpr (!WHOLE) {
+    if (a.G > 1) {
+      float* val = reinterpret_cast<float*>(buf);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) cm = fabsf(c[i]) < INFINITY ? fmaxf(cm, fabsf(c[i])) : cm;
-        cm = warp_max(cm);
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < a.E) {
+          const float v = a.bias == nullptr && sums ? score_of(c[i]) : c[i];
+          val[e0 + i] = v == v ? v : -INFINITY;
+        }
+      __syncwarp();
+      const int per = a.E / a.G, g = lane / a.lpg;
+      float t1 = -INFINITY, t2 = -INFINITY;
+      if (g < a.G)
+        for (int i = lane % a.lpg; i < per; i += a.lpg) top2(val[g * per + i], t1, t2);
+      kept = rank_groups(a, row, group_sums(a, t1, t2, lane), lane, tol);
+      int q = e0 / per, r = e0 % per;  // of expert e0 + i: its group, its place there
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        open |= (e0 + i < a.E && ((kept >> (q & 31)) & 1u)) ? 1u << i : 0u;
+        const bool next = ++r == per;
+        r = next ? 0 : r;
+        q += next;
       }
-      tol = 4.f * eps + 0x1p-21f * cm;
-    }
-    const uint32_t kept = keep_groups(a, row, reinterpret_cast<const float*>(buf), lane, by_score ? tol : -1.f);
-    const int per = a.E / a.G, qs = 32 / per, rs = 32 % per;
-    int q = lane / per, r = lane % per;  // of expert lane + 32 i: its group, its place there
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      open |= (lane + 32 * i < a.E && ((kept >> q) & 1u)) ? 1u << i : 0u;
-      q += qs;
-      r += rs;
-      if (r >= per) {
-        r -= per;
-        ++q;
-      }
+      for (int i = 0; i < PER; ++i) open |= e0 + i < a.E ? 1u << i : 0u;
     }
-    if (PER > 8) __syncwarp();
-    my_kept = kept;
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) open |= lane + 32 * i < a.E ? 1u << i : 0u;
   }
 
   // Rounds: the warp's best candidate each. Lane j keeps round j's.
   uint32_t my_key = 0, my_id = 0;
   int rounds = a.bias != nullptr ? a.k + 1 : a.k;  // with a bias, the next in line too
   uint32_t past_key = 0;  // the last round's
-  int e[PER <= 8 ? PER : 1];
-  int left = __popc(open);
+  int left = WHOLE ? PER : __popc(open);
   uint32_t order = 0;  // PER <= 8: the candidates in their order, four bits each, the best lowest
   if constexpr (PER <= 8) {
+    int e[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const bool ok = (open >> i) & 1u;
+      const bool ok = WHOLE || ((open >> i) & 1u);
       c[i] = ok ? c[i] : -INFINITY;
       e[i] = ok ? i : 15;  // after every candidate, the ones at -inf too
     }
     route_sort<PER>(c, e);
 #pragma unroll
     for (int i = 0; i < PER; ++i) order |= (uint32_t)e[i] << (4 * i);
+    if (WHOLE && a.G > 1) {
+      float t1 = c[0], t2 = PER > 1 ? c[PER > 1 ? 1 : 0] : -INFINITY;
+      if (a.bias == nullptr && sums) {
+        t1 = score_of(t1);
+        t2 = PER > 1 ? score_of(t2) : t2;
+        t1 = t1 == t1 ? t1 : -INFINITY;
+        t2 = t2 == t2 ? t2 : -INFINITY;
+      }
+      kept = rank_groups(a, row, group_sums(a, t1, t2, lane), lane, tol);
+      left = (kept >> (lane / a.lpg)) & 1u ? PER : 0;
+    }
   }
   auto round = [&](int j) {
     uint32_t key, id;
     if constexpr (PER <= 8) {
       key = left > 0 ? float_key(c[0]) : 0u;  // 0: no candidate (keys are larger)
-      id = lane + 32 * (order & 15u);
+      id = e0 + (order & 15u);
     } else {
       float bv = -INFINITY;
       int bi = -1;
@@ -386,7 +430,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
         bi = better ? i : bi;
       }
       key = bi >= 0 ? float_key(bv) : 0u;
-      id = bi >= 0 ? (uint32_t)(lane + 32 * bi) : kAll;
+      id = bi >= 0 ? (uint32_t)(e0 + bi) : kAll;
     }
     const uint32_t kmax = __reduce_max_sync(kAll, key);
     const uint32_t emin = __reduce_min_sync(kAll, key == kmax ? id : kAll);
@@ -397,7 +441,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
       order = win ? order >> 4 : order;
       left -= win;
     } else {
-      open &= win ? ~(1u << (id >> 5)) : kAll;
+      open &= win ? ~(1u << (id - e0)) : kAll;
     }
     my_key = lane == j ? kmax : my_key;
     my_id = lane == j ? emin : my_id;
@@ -426,7 +470,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
       while (more() && rounds <= 32) round(rounds++);
       // Without a candidate in line, `rounds` counts the round that found none.
       if (more())
-        my_id = (uint32_t)settle_all(a, row, my_kept, buf, lane);
+        my_id = (uint32_t)settle_all(a, row, kept, buf, lane);
       else
         my_id = (uint32_t)settle_slots(a, row, (int)my_id, min(rounds - 1, 32), lane);
     }
@@ -529,8 +573,15 @@ int router_warps(int E) { return E <= 512 ? kRouterWarps : kRouterWarps / 2; }
 template <int PER>
 void launch_router(const RouterArgs& a, cudaStream_t s) {
   const int warps = router_warps(a.E);
-  router_kernel<PER><<<(unsigned)((a.n + warps - 1) / warps), 32 * warps,
-                       (size_t)warps * a.E * sizeof(double), s>>>(a);
+  const unsigned grid = (unsigned)((a.n + warps - 1) / warps);
+  const size_t smem = (size_t)warps * a.E * sizeof(double);
+  if constexpr (PER <= 8) {
+    if (a.E == 32 * PER && (a.G & (a.G - 1)) == 0) {
+      router_kernel<PER, true><<<grid, 32 * warps, smem, s>>>(a);
+      return;
+    }
+  }
+  router_kernel<PER, false><<<grid, 32 * warps, smem, s>>>(a);
 }
 
 }  // namespace
@@ -552,6 +603,7 @@ int router_forward(const moe_router_cfg* cfg, const void* logits, int dtype, lon
   a.bias = bias;
   a.ids = ids;
   a.w = w;
+  a.vec = aligned_to(logits, 16) && ld % 8 == 0 && aligned_to(bias, 16);
   if (a.E <= 32) launch_router<1>(a, s);
   else if (a.E <= 64) launch_router<2>(a, s);
   else if (a.E <= 128) launch_router<4>(a, s);
