@@ -65,7 +65,7 @@ struct RouterArgs {
   void* dl;             // backward: [n][ld_dl]
   long long n, ld, ld_dl;
   int dtype, E, k, G, TG, GT, score, renorm;
-  bool vec;  // scores and bias can be read by vectors of four
+  bool vec;  // rows (and the bias) can be read and written by vectors of four
   int lpg;  // lanes of a group: the largest power of two that leaves each one its own
   float scale;
 };
@@ -491,35 +491,50 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
 //   softmax, renormalised dl_j = r_j (g_j - sum_i g_i r_i)
 //   softmax               dl_e = p_e ((g_j where e is chosen, else 0) - sum_i g_i p_i)
 // zero for the other experts except in the last, the only one that reads every score.
-// A warp takes a token and writes its whole row: the row is put together in shared
-// memory, so that the stores are coalesced. Bound by the row's bytes.
+// A warp takes a token, lane l experts PER l .. PER l + PER - 1: the chosen experts' values
+// reach their lanes through shared memory, and the row leaves in vectors. Bound by the
+// row's bytes and, at these lengths, by the instructions a row costs.
+template <int PER>
 __global__ void __launch_bounds__(32 * kRouterWarps)
     router_backward_kernel(const __grid_constant__ RouterArgs a) {
   extern __shared__ double smem_d[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * PER;
   const long long tok = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
   if (tok >= a.n) return;
-  float* g = reinterpret_cast<float*>(smem_d) + (size_t)warp * a.E;
+  float* g = reinterpret_cast<float*>(smem_d) + (size_t)warp * 32 * PER;  // [32 PER], to E and beyond
   const int tb = a.dtype == MOE_FP32 ? 4 : 2;
   const void* row = static_cast<const char*>(a.logits) + (size_t)tok * a.ld * tb;
   void* out = static_cast<char*>(a.dl) + (size_t)tok * a.ld_dl * tb;
+  const bool whole = a.E == 32 * PER && a.vec;  // vectors of four; `vec` covers both matrices
 
-  for (int e = lane; e < a.E; e += 32) g[e] = 0.f;
   const int id = lane < a.k ? __ldg(a.ids + tok * a.k + lane) : -1;
   const bool in = id >= 0 && id < a.E;  // others have no gradient
   const float t = in ? load_as_f32(row, a.dtype, id) : 0.f;
   const float gj = in ? a.scale * __ldg(a.dw + tok * a.k + lane) : 0.f;
   const bool all = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
+  float p[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) g[lane + 32 * i] = 0.f;
   float mx = 0.f, inv = 1.f;
   if (all) {
+    if (PER >= 4 && whole) {
+      if constexpr (PER >= 4) load_scores<PER>(row, a.dtype, e0, p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) p[i] = e0 + i < a.E ? load_as_f32(row, a.dtype, e0 + i) : -INFINITY;
+    }
     float m = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_as_f32(row, a.dtype, e));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = fmaxf(m, p[i]);
     mx = warp_max(m);
     float sum = 0.f;
-    if (mx != -INFINITY)
-      for (int e = lane; e < a.E; e += 32) sum += expf(load_as_f32(row, a.dtype, e) - mx);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      p[i] = mx == -INFINITY ? 0.f : expf(p[i] - mx);
+      sum += p[i];
+    }
     sum = warp_sum(sum);
-    inv = 1.0f / sum;
+    inv = mx == -INFINITY ? 0.f : 1.0f / sum;
   }
   const float r = slot_weight(a, t, in, mx, inv);
   const float dot = a.renorm || all ? warp_sum(in ? gj * r : 0.f) : 0.f;
@@ -528,10 +543,35 @@ __global__ void __launch_bounds__(32 * kRouterWarps)
   __syncwarp();
   if (in) g[id] = all ? gj : d;
   __syncwarp();
-  for (int e = lane; e < a.E; e += 32) {
-    float v = g[e];
-    if (all) v = mx == -INFINITY ? 0.f : expf(load_as_f32(row, a.dtype, e) - mx) * inv * (v - dot);
-    store_from_f32(out, a.dtype, e, v);
+  float v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    v[i] = g[e0 + i];
+    if (all) v[i] = p[i] * inv * (v[i] - dot);
+  }
+  if (PER >= 4 && whole) {
+    if constexpr (PER >= 4) {
+#pragma unroll
+      for (int i = 0; i < PER; i += 4) {
+        if (a.dtype == MOE_FP32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(out) + e0 + i) =
+              make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+          const uint2 u = a.dtype == MOE_BF16
+                              ? make_uint2(pack2<__nv_bfloat16>(v[i], v[i + 1]),
+                                           pack2<__nv_bfloat16>(v[i + 2], v[i + 3]))
+                              : make_uint2(pack2<__half>(v[i], v[i + 1]), pack2<__half>(v[i + 2], v[i + 3]));
+          *reinterpret_cast<uint2*>(static_cast<unsigned short*>(out) + e0 + i) = u;
+        }
+      }
+    }
+  } else {
+    // Rows of any length: neighbouring lanes write neighbouring experts.
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) g[e0 + i] = v[i];
+    __syncwarp();
+    for (int e = lane; e < a.E; e += 32) store_from_f32(out, a.dtype, e, g[e]);
   }
 }
 
@@ -582,6 +622,13 @@ void launch_router(const RouterArgs& a, cudaStream_t s) {
     }
   }
   router_kernel<PER, false><<<grid, 32 * warps, smem, s>>>(a);
+}
+
+template <int PER>
+void launch_router_backward(const RouterArgs& a, cudaStream_t s) {
+  const int warps = router_warps(a.E);
+  router_backward_kernel<PER><<<(unsigned)((a.n + warps - 1) / warps), 32 * warps,
+                                (size_t)warps * 32 * PER * sizeof(float), s>>>(a);
 }
 
 }  // namespace
@@ -637,8 +684,13 @@ extern "C" int moe_router_backward(const moe_router_cfg* cfg, const float* d_w, 
   a.ids = const_cast<int32_t*>(ids);
   a.dl = d_logits;
   a.ld_dl = ld_d;
-  const int warps = router_warps(a.E);
-  router_backward_kernel<<<(unsigned)((n + warps - 1) / warps), 32 * warps,
-                           (size_t)warps * a.E * sizeof(float), reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  a.vec = aligned_to(logits, 16) && ld % 8 == 0 && aligned_to(d_logits, 16) && ld_d % 8 == 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a.E <= 32) launch_router_backward<1>(a, s);
+  else if (a.E <= 64) launch_router_backward<2>(a, s);
+  else if (a.E <= 128) launch_router_backward<4>(a, s);
+  else if (a.E <= 256) launch_router_backward<8>(a, s);
+  else if (a.E <= 512) launch_router_backward<16>(a, s);
+  else launch_router_backward<32>(a, s);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
