@@ -186,6 +186,38 @@ constexpr int kMaxStages = 8;
 constexpr int kABytes = kTileI * kBlockK * 2;  // 16 KB
 constexpr int kTileThreads = 256;
 
+// The next stage of a ring. (A division by the ring's length, which only the launch knows,
+// costs these single threads more than the rest of a step: with `n % stages` a step took
+// 190 ns without any copy or product in it.)
+__device__ __forceinline__ void next_stage(int& st, uint32_t& phase, int stages) {
+  if (++st == stages) {
+    st = 0;
+    phase ^= 1;
+  }
+}
+
+// One lane of a converged warp, the same one every time. The single-thread roles run as whole
+// warps and ask this around what one thread issues: their addresses and descriptors then
+// stay uniform values, which tcgen05 and TMA take as they are.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+// Waits of a whole warp: every lane comes out with the same answer, so that no lane leaves
+// a role that the others carry on with.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase, volatile int* abort, uint32_t detail) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, phase, abort, kWaitNs, g_status, detail));
+}
+__device__ __forceinline__ bool warp_pwait(uint64_t* bar, uint32_t phase, volatile int* abort, uint32_t detail) {
+  return __all_sync(0xFFFFFFFFu, pwait(bar, phase, abort, kWaitNs, g_status, detail));
+}
+
 struct GemmArgs {
   CUtensorMap ta, tb;
   Epilogue e;
@@ -244,29 +276,31 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     const uint32_t bytes = (AMN ? kABytes : a.box_a * 128) + b_bytes;
-    int issued = 0;
+    int issued = 0, st = 0;
+    uint32_t phase = 1;
     for (int kb = k_lo; kb < k_hi; ++kb, ++issued) {
-      const int st = issued % a.stages;
-      if (!mbar_wait_bounded(&sm.empty[st], ((issued / a.stages) & 1) ^ 1, &sm.abort, kWaitNs, g_status,
-                             0x01000000u))
-        break;
-      uint8_t* as = base + (size_t)st * stage_bytes;
-      uint8_t* bs = as + kABytes;
-      mbar_arrive_expect_tx(&sm.full[st], bytes);
-      if (AMN) {
-        tma_load_2d(as, &a.ta, &sm.full[st], i0, kb * kBlockK);
-        tma_load_2d(as + 8192, &a.ta, &sm.full[st], i0 + 64, kb * kBlockK);
-      } else {
-        tma_load_2d(as, &a.ta, &sm.full[st], kb * kBlockK, i0);
+      if (!warp_wait(&sm.empty[st], phase, &sm.abort, 0x01000000u)) break;
+      if (elect_one()) {
+        uint8_t* as = base + (size_t)st * stage_bytes;
+        uint8_t* bs = as + kABytes;
+        mbar_arrive_expect_tx(&sm.full[st], bytes);
+        if (AMN) {
+          tma_load_2d(as, &a.ta, &sm.full[st], i0, kb * kBlockK);
+          tma_load_2d(as + 8192, &a.ta, &sm.full[st], i0 + 64, kb * kBlockK);
+        } else {
+          tma_load_2d(as, &a.ta, &sm.full[st], kb * kBlockK, i0);
+        }
+        if (BMN) {
+          for (int c = 0; c < a.bn / 64; ++c)
+            tma_load_2d(bs + c * 8192, &a.tb, &sm.full[st], j0 + c * 64, kb * kBlockK);
+        } else {
+          tma_load_2d(bs, &a.tb, &sm.full[st], kb * kBlockK, j0);
+        }
       }
-      if (BMN) {
-        for (int c = 0; c < a.bn / 64; ++c)
-          tma_load_2d(bs + c * 8192, &a.tb, &sm.full[st], j0 + c * 64, kb * kBlockK);
-      } else {
-        tma_load_2d(bs, &a.tb, &sm.full[st], kb * kBlockK, j0);
-      }
+      __syncwarp();
+      next_stage(st, phase, a.stages);
     }
     if (*(volatile int*)&sm.abort) {  // the copies in flight land before the CTA leaves
       volatile int never = 0;
@@ -274,22 +308,30 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
         mbar_wait_bounded(&sm.full[n % a.stages], (n / a.stages) & 1, &never, kWaitNs, g_status,
                           0x02000000u);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     const uint32_t idesc = idesc_16bit(a.bf16, AMN, BMN, kTileI, a.bn);
-    for (int kb = k_lo, n = 0; kb < k_hi; ++kb, ++n) {
-      const int st = n % a.stages;
-      if (!mbar_wait_bounded(&sm.full[st], (n / a.stages) & 1, &sm.abort, kWaitNs, g_status, 0x03000000u))
-        break;
+    const uint32_t s0 = (smem_u32(base) & 0x3FFFFu) >> 4;  // above lies the CTA's rank in its cluster
+    const uint64_t da = (AMN ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0;
+    const uint64_t db = (BMN ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0 + (kABytes >> 4);
+    constexpr uint32_t step_a = (AMN ? 2048 : 32) >> 4, step_b = (BMN ? 2048 : 32) >> 4;
+    int st = 0;
+    uint32_t phase = 0, accumulate = 0, at = 0;  // at: the stage's offset in 16-byte units
+    for (int kb = k_lo; kb < k_hi; ++kb) {
+      if (!warp_wait(&sm.full[st], phase, &sm.abort, 0x03000000u)) break;
       tc_fence_after();
-      const uint32_t as = smem_u32(base + (size_t)st * stage_bytes), bs = as + kABytes;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kBlockK / 16; ++k)
-        tc_mma(tmem, AMN ? sdesc_mn_sw128(as + k * 2048) : sdesc_k_sw128(as + k * 32),
-               BMN ? sdesc_mn_sw128(bs + k * 2048) : sdesc_k_sw128(bs + k * 32), idesc,
-               (n | k) != 0 ? 1u : 0u);
-      tc_commit(&sm.empty[st]);
+        for (int k = 0; k < kBlockK / 16; ++k)
+          tc_mma(tmem, da + at + k * step_a, db + at + k * step_b, idesc, k != 0 ? 1u : accumulate);
+        tc_commit(&sm.empty[st]);
+      }
+      __syncwarp();
+      accumulate = 1;
+      next_stage(st, phase, a.stages);
+      at = st == 0 ? 0 : at + (stage_bytes >> 4);
     }
-    tc_commit(&sm.done);  // also after a wait that ran out: no product outlives the CTA
+    // Also after a wait that ran out: no product outlives the CTA.
+    if (elect_one()) tc_commit(&sm.done);
   }
   __syncwarp();
   volatile int never = 0;
@@ -507,37 +549,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     const uint32_t bytes = 2 * (uint32_t)stage_bytes;
-    int n = 0;
+    int n = 0, st = 0;
+    uint32_t phase = 1;
     bool ok = true;
     for (int t = pair0; t < tiles && ok; t += pairs) {
       int ti, tj;
       pair_tile(a, t, &ti, &tj);
       const int i0 = ti * 256 + (int)crank * 128, j0 = tj * a.bn + (int)crank * (a.bn / 2);
       for (int kb = 0; kb < a.nk; ++kb, ++n) {
-        const int st = n % a.stages;
-        if (!pwait(&sm.empty[st], ((n / a.stages) & 1) ^ 1, &sm.abort, kWaitNs, g_status, 0x11000000u)) {
+        if (!warp_pwait(&sm.empty[st], phase, &sm.abort, 0x11000000u)) {
           ok = false;
           break;
         }
-        uint8_t* as = base + (size_t)st * stage_bytes;
-        uint8_t* bs = as + kABytes;
-        if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
-        const uint32_t fb = map_shared(&sm.full[st], 0);
-        const int k0 = kb * kBlockK;
-        if (a.a_mn) {
-          tma_load_2d_pair(as, &a.ta, fb, i0, k0);
-          tma_load_2d_pair(as + 8192, &a.ta, fb, i0 + 64, k0);
-        } else {
-          tma_load_2d_pair(as, &a.ta, fb, k0, i0);
+        if (elect_one()) {
+          uint8_t* as = base + (size_t)st * stage_bytes;
+          uint8_t* bs = as + kABytes;
+          if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
+          const uint32_t fb = map_shared(&sm.full[st], 0);
+          const int k0 = kb * kBlockK;
+          if (a.a_mn) {
+            tma_load_2d_pair(as, &a.ta, fb, i0, k0);
+            tma_load_2d_pair(as + 8192, &a.ta, fb, i0 + 64, k0);
+          } else {
+            tma_load_2d_pair(as, &a.ta, fb, k0, i0);
+          }
+          if (a.b_mn) {
+            for (int c = 0; c < a.bn / 128; ++c)
+              tma_load_2d_pair(bs + c * 8192, &a.tb, fb, j0 + c * 64, k0);
+          } else {
+            tma_load_2d_pair(bs, &a.tb, fb, k0, j0);
+          }
         }
-        if (a.b_mn) {
-          for (int c = 0; c < a.bn / 128; ++c)
-            tma_load_2d_pair(bs + c * 8192, &a.tb, fb, j0 + c * 64, k0);
-        } else {
-          tma_load_2d_pair(bs, &a.tb, fb, k0, j0);
-        }
+        __syncwarp();
+        next_stage(st, phase, a.stages);
       }
     }
     // Every copy this CTA issued has landed once the products that read its stage are done.
@@ -547,35 +593,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const long long left = kWaitNs - (long long)(globaltimer() - t0);
       pwait(&sm.empty[i % a.stages], (i / a.stages) & 1, &never, left > 0 ? left : 0, g_status, 0x12000000u);
     }
-  } else if (warp == 1 && lane == 0 && lead) {
+  } else if (warp == 1 && lead) {
     const uint32_t idesc = idesc_16bit(a.bf16, a.a_mn, a.b_mn, 256, a.bn);
-    const uint64_t da = a.a_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0);
-    const uint64_t db = a.b_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0);
+    const uint32_t s0 = (smem_u32(base) & 0x3FFFFu) >> 4;  // above lies the CTA's rank in its cluster
+    const uint64_t da = (a.a_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0;
+    const uint64_t db = (a.b_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0 + (kABytes >> 4);
     const uint32_t step_a = (a.a_mn ? 2048 : 32) >> 4, step_b = (a.b_mn ? 2048 : 32) >> 4;
-    int n = 0, it = 0;
+    int it = 0, st = 0;
+    uint32_t phase = 0, at = 0;  // at: the stage's offset in 16-byte units
     bool ok = true;
     for (int t = pair0; t < tiles && ok; t += pairs, ++it) {
       const int acc = it & 1;
-      if (!pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, kWaitNs, g_status, 0x21000000u)) break;
+      if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, 0x21000000u)) break;
       tc_fence_after();
       const uint32_t dt = tmem + (uint32_t)(acc * a.bn);
-      for (int kb = 0; kb < a.nk; ++kb, ++n) {
-        const int st = n % a.stages;
-        if (!pwait(&sm.full[st], (n / a.stages) & 1, &sm.abort, kWaitNs, g_status, 0x22000000u)) {
+      for (int kb = 0; kb < a.nk; ++kb) {
+        if (!warp_pwait(&sm.full[st], phase, &sm.abort, 0x22000000u)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t as = smem_u32(base + (size_t)st * stage_bytes) >> 4, bs = as + (kABytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kBlockK / 16; ++k)
-          tc_mma_pair(dt, da + as + k * step_a, db + bs + k * step_b, idesc, (kb | k) != 0 ? 1u : 0u);
-        tc_commit_pair(&sm.empty[st], 0x3);
+          for (int k = 0; k < kBlockK / 16; ++k)
+            tc_mma_pair(dt, da + at + k * step_a, db + at + k * step_b, idesc, (kb | k) != 0 ? 1u : 0u);
+          tc_commit_pair(&sm.empty[st], 0x3);
+        }
+        __syncwarp();
+        next_stage(st, phase, a.stages);
+        at = st == 0 ? 0 : at + (stage_bytes >> 4);
       }
-      if (ok) tc_commit_pair(&sm.tfull[acc], 0x3);
+      if (ok && elect_one()) tc_commit_pair(&sm.tfull[acc], 0x3);
+      __syncwarp();
     }
     // Every product issued is done before either CTA frees TMEM or leaves.
-    tc_commit_pair(&sm.drain, 0x1);
+    if (elect_one()) tc_commit_pair(&sm.drain, 0x1);
+    __syncwarp();
     volatile int never = 0;
     pwait(&sm.drain, 0, &never, kWaitNs, g_status, 0x23000000u);
   } else if (warp >= 2) {
@@ -586,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int ti, tj;
       pair_tile(a, t, &ti, &tj);
       const int acc = it & 1;
-      if (!pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, kWaitNs, g_status, 0x31000000u)) break;
+      if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, 0x31000000u)) break;
       tc_fence_after();
       const int row = ti * 256 + (int)crank * 128 + q * 32 + lane;
       const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * a.bn);
@@ -619,6 +672,135 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, cols);
+}
+
+// ------------------------------------------------------------------- few rows
+// Up to 16 rows of x: the weights are read once, and their bytes are the bound, so they
+// stream from global memory into registers, without the latency of a shared-memory
+// pipeline, and the products are mma.sync (16 x 8 x 16; the tokens are its 16 rows, eight
+// weight rows its columns). A sum over k may take the k in any order: lane (g, t) loads 16
+// bytes, elements 8 t .. 8 t + 7 of 32, of weight row g and of token rows g and g + 8, and
+// gives the first four to one product and the rest to the next, where the products expect
+// 2 t, 2 t + 1, 2 t + 8, 2 t + 9; both operands agree. `ks` warps share eight rows of the
+// weights, each with a range of k; their sums are added in the warps' order.
+constexpr int kRowsMax = 16;  // rows of x
+constexpr int kRowsWarps = 8;
+constexpr int kRowsUnroll = 8;  // steps of 32 k whose loads are in flight together
+
+struct RowsArgs {
+  const void* x;
+  const void* w;
+  Epilogue e;
+  long long ld_x, ld_w;
+  int M, N, K, ks;
+};
+
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+// Elements k .. k + 7 of a row of K, zeros past it.
+__device__ __forceinline__ uint4 load_tail(const unsigned short* row, int k, int K) {
+  unsigned short u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = k + i < K ? __ldg(row + k + i) : (unsigned short)0;
+  return make_uint4(u[0] | (uint32_t)u[1] << 16, u[2] | (uint32_t)u[3] << 16, u[4] | (uint32_t)u[5] << 16,
+                    u[6] | (uint32_t)u[7] << 16);
+}
+template <bool BF16>
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// act of a value whose kind is known at run time.
+__device__ __forceinline__ float act_any(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return act_of<MOE_ACT_RELU>(z);
+    case MOE_ACT_GELU: return act_of<MOE_ACT_GELU>(z);
+    case MOE_ACT_GELU_TANH: return act_of<MOE_ACT_GELU_TANH>(z);
+    case MOE_ACT_SILU: return act_of<MOE_ACT_SILU>(z);
+    default: return z;
+  }
+}
+
+// HIGH: token rows 8 .. 15 are there too.
+template <bool BF16, bool HIGH>
+__global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ float part[kRowsWarps][16][9];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int per = kRowsWarps / a.ks;  // groups of eight weight rows in the CTA
+  const int kw = warp % a.ks;
+  const long long n0 = ((long long)blockIdx.x * per + warp / a.ks) * 8;
+  const unsigned short* wrow = static_cast<const unsigned short*>(a.w) + (n0 + g) * a.ld_w;
+  const unsigned short* x0 = static_cast<const unsigned short*>(a.x) + g * a.ld_x;
+  const unsigned short* x1 = x0 + 8 * a.ld_x;
+  const bool in_w = n0 + g < a.N, in_0 = g < a.M, in_1 = HIGH && g + 8 < a.M;
+  const int steps = (a.K + 31) / 32;
+  const int lo = (int)((long long)steps * kw / a.ks), hi = (int)((long long)steps * (kw + 1) / a.ks);
+  const int full = a.K / 32;  // steps without a tail
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
+  auto product = [&](const uint4& w, const uint4& p, const uint4& q) {
+    mma_16x8x16<BF16>(d, p.x, q.x, p.y, q.y, w.x, w.y);
+    mma_16x8x16<BF16>(d, p.z, q.z, p.w, q.w, w.z, w.w);
+  };
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  int s = lo;
+  const int end = min(hi, full);
+  for (; s + kRowsUnroll <= end; s += kRowsUnroll) {
+    uint4 w[kRowsUnroll], p[kRowsUnroll], q[HIGH ? kRowsUnroll : 1];
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u) w[u] = in_w ? load_stream(wrow + (s + u) * 32 + t * 8) : zero;
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u) {
+      const int k = (s + u) * 32 + t * 8;
+      p[u] = in_0 ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : zero;
+      if (HIGH) q[u] = in_1 ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u) product(w[u], p[u], HIGH ? q[HIGH ? u : 0] : zero);
+  }
+  for (; s < hi; ++s) {
+    const int k = s * 32 + t * 8;
+    const bool vec = k + 8 <= a.K;
+    const uint4 w = !in_w ? zero : vec ? load_stream(wrow + k) : load_tail(wrow, k, a.K);
+    const uint4 p = !in_0 ? zero : vec ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : load_tail(x0, k, a.K);
+    const uint4 q = !in_1 ? zero : vec ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : load_tail(x1, k, a.K);
+    product(w, p, q);
+  }
+  part[warp][g][2 * t] = d[0];
+  part[warp][g][2 * t + 1] = d[1];
+  if (HIGH) {
+    part[warp][g + 8][2 * t] = d[2];
+    part[warp][g + 8][2 * t + 1] = d[3];
+  }
+  __syncthreads();
+  // Output (token i, group q, column c): consecutive threads along the columns.
+  const int rows = min(a.M, HIGH ? 16 : 8), wide = per * 8;
+  for (int o = threadIdx.x; o < rows * wide; o += blockDim.x) {
+    const int i = o / wide, q = (o % wide) / 8, c = o % 8;
+    const long long j = ((long long)blockIdx.x * per + q) * 8 + c;
+    if (j >= a.N) continue;
+    float v = 0.f;
+    for (int r = 0; r < a.ks; ++r) v += part[q * a.ks + r][i][c];
+    if (a.e.b != nullptr) v += load_as_f32(a.e.b, a.e.btype, j);
+    if (a.e.z != nullptr) store_from_f32(a.e.z, a.e.dtype, i * a.e.ld_z + j, v);
+    v = act_any(v, a.e.act);
+    if (a.e.r != nullptr) v += load_as_f32(a.e.r, a.e.dtype, i * a.e.ld_r + j);
+    store_from_f32(a.e.y, a.e.ytype, i * a.e.ld_y + j, v);
+  }
 }
 
 // ------------------------------------------------------------------- dz and db
@@ -799,6 +981,35 @@ int gemm_pair(const Operand& A, const Operand& B, int I, int J, int nk, long lon
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The product of a few token rows.
+int gemm_rows(const moe_linear_args* p, const Epilogue& e, cudaStream_t s) {
+  RowsArgs a;
+  a.x = p->x;
+  a.w = p->w;
+  a.e = e;
+  a.ld_x = p->ld_x;
+  a.ld_w = p->ld_w;
+  a.M = (int)p->M;
+  a.N = (int)p->N;
+  a.K = (int)p->K;
+  // As many warps to a row of the weights as have kRowsUnroll steps each.
+  a.ks = kRowsWarps;
+  while (a.ks > 1 && p->K < 32LL * kRowsUnroll * a.ks) a.ks /= 2;
+  const long long groups = (p->N + 7) / 8;
+  const int per = kRowsWarps / a.ks;
+  const unsigned grid = (unsigned)((groups + per - 1) / per);
+  const bool bf16 = p->dtype == MOE_BF16, high = p->M > 8;
+  if (bf16 && high)
+    linear_rows_kernel<true, true><<<grid, 32 * kRowsWarps, 0, s>>>(a);
+  else if (bf16)
+    linear_rows_kernel<true, false><<<grid, 32 * kRowsWarps, 0, s>>>(a);
+  else if (high)
+    linear_rows_kernel<false, true><<<grid, 32 * kRowsWarps, 0, s>>>(a);
+  else
+    linear_rows_kernel<false, false><<<grid, 32 * kRowsWarps, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // D[i][j] = sum_k A(i, k) B(j, k) through the epilogue.
 int gemm(const Operand& A, const Operand& B, int I, int J, long long K, bool bf16, const Epilogue& e,
          int num_sms, cudaStream_t s) {
@@ -942,6 +1153,7 @@ int moe_linear(const moe_linear_args* p, moe_stream_t stream) {
   e.vz = row_bytes(p->z, p->ld_z, p->dtype, p->M);
   e.vr = row_bytes(p->r, p->ld_r, p->dtype, p->M);
   e.vb = aligned_to(p->b, 16);
+  if (p->M <= kRowsMax) return gemm_rows(p, e, reinterpret_cast<cudaStream_t>(stream));
   return gemm({p->x, p->ld_x, false}, {p->w, p->ld_w, false}, (int)p->M, (int)p->N, p->K,
               p->dtype == MOE_BF16, e, sms, reinterpret_cast<cudaStream_t>(stream));
 }
