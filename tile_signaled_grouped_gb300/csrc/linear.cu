@@ -675,15 +675,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // ------------------------------------------------------------------- few rows
-// Up to 16 rows of x: the weights are read once, and their bytes are the bound, so they
+// Up to 8 rows of x: the weights are read once, and their bytes are the bound, so they
 // stream from global memory into registers, without the latency of a shared-memory
-// pipeline, and the products are mma.sync (16 x 8 x 16; the tokens are its 16 rows, eight
-// weight rows its columns). A sum over k may take the k in any order: lane (g, t) loads 16
-// bytes, elements 8 t .. 8 t + 7 of 32, of weight row g and of token rows g and g + 8, and
+// pipeline, and the products are mma.sync (16 x 8 x 16; the tokens are its first eight rows,
+// eight weight rows its columns). A sum over k may take the k in any order: lane (g, t)
+// loads 16 bytes, elements 8 t .. 8 t + 7 of 32, of weight row g and of token row g, and
 // gives the first four to one product and the rest to the next, where the products expect
 // 2 t, 2 t + 1, 2 t + 8, 2 t + 9; both operands agree. `ks` warps share eight rows of the
-// weights, each with a range of k; their sums are added in the warps' order.
-constexpr int kRowsMax = 16;  // rows of x
+// weights, each with a range of k; their sums are added in the warps' order. CTAs walk the
+// rows of the weights, and the next batch of loads, of the next rows at the end of a row,
+// is on its way while a batch is multiplied. (16 rows of x in this form took 14 us for
+// 2048 x 7168, where the tiles take 12.)
+constexpr int kRowsMax = 8;  // rows of x
 constexpr int kRowsWarps = 8;
 constexpr int kRowsUnroll = 8;  // steps of 32 k whose loads are in flight together
 
@@ -691,22 +694,29 @@ struct RowsArgs {
   const void* x;
   const void* w;
   Epilogue e;
-  long long ld_x, ld_w;
+  long long ld_x, ld_w, blocks;  // blocks: of 8 (kRowsWarps / ks) weight rows
   int M, N, K, ks;
 };
 
 __device__ __forceinline__ uint4 load_stream(const void* p) {
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
-// Elements k .. k + 7 of a row of K, zeros past it.
-__device__ __forceinline__ uint4 load_tail(const unsigned short* row, int k, int K) {
+__device__ __forceinline__ uint4 load_tokens(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+// The first n of eight elements, zeros for the others.
+__device__ __forceinline__ uint4 load_tail(const unsigned short* p, int n) {
   unsigned short u[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = k + i < K ? __ldg(row + k + i) : (unsigned short)0;
+  for (int i = 0; i < 8; ++i) u[i] = i < n ? __ldg(p + i) : (unsigned short)0;
   return make_uint4(u[0] | (uint32_t)u[1] << 16, u[2] | (uint32_t)u[3] << 16, u[4] | (uint32_t)u[5] << 16,
                     u[6] | (uint32_t)u[7] << 16);
 }
@@ -736,70 +746,77 @@ __device__ __forceinline__ float act_any(float z, int act) {
   }
 }
 
-// HIGH: token rows 8 .. 15 are there too.
-template <bool BF16, bool HIGH>
-__global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const __grid_constant__ RowsArgs a) {
-  __shared__ float part[kRowsWarps][16][9];
+template <bool BF16>
+__global__ void __launch_bounds__(32 * kRowsWarps, 2) linear_rows_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ float part[2][kRowsWarps][8][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per = kRowsWarps / a.ks;  // groups of eight weight rows in the CTA
   const int kw = warp % a.ks;
-  const long long n0 = ((long long)blockIdx.x * per + warp / a.ks) * 8;
-  const unsigned short* wrow = static_cast<const unsigned short*>(a.w) + (n0 + g) * a.ld_w;
-  const unsigned short* x0 = static_cast<const unsigned short*>(a.x) + g * a.ld_x;
-  const unsigned short* x1 = x0 + 8 * a.ld_x;
-  const bool in_w = n0 + g < a.N, in_0 = g < a.M, in_1 = HIGH && g + 8 < a.M;
-  const int steps = (a.K + 31) / 32;
-  const int lo = (int)((long long)steps * kw / a.ks), hi = (int)((long long)steps * (kw + 1) / a.ks);
-  const int full = a.K / 32;  // steps without a tail
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
-  auto product = [&](const uint4& w, const uint4& p, const uint4& q) {
-    mma_16x8x16<BF16>(d, p.x, q.x, p.y, q.y, w.x, w.y);
-    mma_16x8x16<BF16>(d, p.z, q.z, p.w, q.w, w.z, w.w);
+  // Rows past the end are stood in for by the last one (the first token): what they give is
+  // not written, and no load needs a condition, which would keep a batch's loads apart.
+  const unsigned short* x0 = static_cast<const unsigned short*>(a.x) + (g < a.M ? g * a.ld_x : 0) + t * 8;
+  auto row_of = [&](long long block) {
+    const long long n = min((block * per + warp / a.ks) * 8 + g, (long long)a.N - 1);
+    return static_cast<const unsigned short*>(a.w) + n * a.ld_w + t * 8;
   };
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  int s = lo;
+  const int steps = (a.K + 31) / 32, full = a.K / 32;  // full: steps without a tail
+  const int lo = (int)((long long)steps * kw / a.ks), hi = (int)((long long)steps * (kw + 1) / a.ks);
   const int end = min(hi, full);
-  for (; s + kRowsUnroll <= end; s += kRowsUnroll) {
-    uint4 w[kRowsUnroll], p[kRowsUnroll], q[HIGH ? kRowsUnroll : 1];
+  float d[4];
+  auto product = [&](const uint4& w, const uint4& p) {
+    mma_16x8x16<BF16>(d, p.x, 0u, p.y, 0u, w.x, w.y);
+    mma_16x8x16<BF16>(d, p.z, 0u, p.w, 0u, w.z, w.w);
+  };
+  uint4 w[kRowsUnroll];
+  const unsigned short* row = row_of(blockIdx.x);
+  // A batch past the end loads its last step again and leaves the product out.
+  if (lo < end) {
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u) w[u] = in_w ? load_stream(wrow + (s + u) * 32 + t * 8) : zero;
+    for (int u = 0; u < kRowsUnroll; ++u) w[u] = load_stream(row + min(lo + u, end - 1) * 32);
+  }
+  int parity = 0;
+  for (long long block = blockIdx.x; block < a.blocks; block += gridDim.x, parity ^= 1) {
+    const unsigned short* after = block + gridDim.x < a.blocks ? row_of(block + gridDim.x) : row;
+    d[0] = d[1] = d[2] = d[3] = 0.f;
+    for (int s = lo; s < end; s += kRowsUnroll) {
+      uint4 next[kRowsUnroll], p[kRowsUnroll];
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u) {
-      const int k = (s + u) * 32 + t * 8;
-      p[u] = in_0 ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : zero;
-      if (HIGH) q[u] = in_1 ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : zero;
+      for (int u = 0; u < kRowsUnroll; ++u) p[u] = load_tokens(x0 + min(s + u, end - 1) * 32);
+      const bool last = s + kRowsUnroll >= end;
+      const unsigned short* from = last ? after : row;
+      const int at = last ? lo : s + kRowsUnroll;
+#pragma unroll
+      for (int u = 0; u < kRowsUnroll; ++u) next[u] = load_stream(from + min(at + u, end - 1) * 32);
+#pragma unroll
+      for (int u = 0; u < kRowsUnroll; ++u)
+        if (s + u < end) product(w[u], p[u]);
+#pragma unroll
+      for (int u = 0; u < kRowsUnroll; ++u) w[u] = next[u];
     }
-#pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u) product(w[u], p[u], HIGH ? q[HIGH ? u : 0] : zero);
-  }
-  for (; s < hi; ++s) {
-    const int k = s * 32 + t * 8;
-    const bool vec = k + 8 <= a.K;
-    const uint4 w = !in_w ? zero : vec ? load_stream(wrow + k) : load_tail(wrow, k, a.K);
-    const uint4 p = !in_0 ? zero : vec ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : load_tail(x0, k, a.K);
-    const uint4 q = !in_1 ? zero : vec ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : load_tail(x1, k, a.K);
-    product(w, p, q);
-  }
-  part[warp][g][2 * t] = d[0];
-  part[warp][g][2 * t + 1] = d[1];
-  if (HIGH) {
-    part[warp][g + 8][2 * t] = d[2];
-    part[warp][g + 8][2 * t + 1] = d[3];
-  }
-  __syncthreads();
-  // Output (token i, group q, column c): consecutive threads along the columns.
-  const int rows = min(a.M, HIGH ? 16 : 8), wide = per * 8;
-  for (int o = threadIdx.x; o < rows * wide; o += blockDim.x) {
-    const int i = o / wide, q = (o % wide) / 8, c = o % 8;
-    const long long j = ((long long)blockIdx.x * per + q) * 8 + c;
-    if (j >= a.N) continue;
-    float v = 0.f;
-    for (int r = 0; r < a.ks; ++r) v += part[q * a.ks + r][i][c];
-    if (a.e.b != nullptr) v += load_as_f32(a.e.b, a.e.btype, j);
-    if (a.e.z != nullptr) store_from_f32(a.e.z, a.e.dtype, i * a.e.ld_z + j, v);
-    v = act_any(v, a.e.act);
-    if (a.e.r != nullptr) v += load_as_f32(a.e.r, a.e.dtype, i * a.e.ld_r + j);
-    store_from_f32(a.e.y, a.e.ytype, i * a.e.ld_y + j, v);
+    if (hi > full) {  // the tail of k
+      const int k = full * 32;
+      const bool vec = k + t * 8 + 8 <= a.K;
+      product(vec ? load_stream(row + k) : load_tail(row + k, a.K - k - t * 8),
+              vec ? load_tokens(x0 + k) : load_tail(x0 + k, a.K - k - t * 8));
+    }
+    row = after;
+    part[parity][warp][g][2 * t] = d[0];
+    part[parity][warp][g][2 * t + 1] = d[1];
+    __syncthreads();
+    // Output (token i, group q, column c): consecutive threads along the columns.
+    const int wide = per * 8;
+    for (int o = threadIdx.x; o < a.M * wide; o += blockDim.x) {
+      const int i = o / wide, q = (o % wide) / 8, c = o % 8;
+      const long long j = (block * per + q) * 8 + c;
+      if (j >= a.N) continue;
+      float v = 0.f;
+      for (int r = 0; r < a.ks; ++r) v += part[parity][q * a.ks + r][i][c];
+      if (a.e.b != nullptr) v += load_as_f32(a.e.b, a.e.btype, j);
+      if (a.e.z != nullptr) store_from_f32(a.e.z, a.e.dtype, i * a.e.ld_z + j, v);
+      v = act_any(v, a.e.act);
+      if (a.e.r != nullptr) v += load_as_f32(a.e.r, a.e.dtype, i * a.e.ld_r + j);
+      store_from_f32(a.e.y, a.e.ytype, i * a.e.ld_y + j, v);
+    }
   }
 }
 
@@ -982,7 +999,7 @@ int gemm_pair(const Operand& A, const Operand& B, int I, int J, int nk, long lon
 }
 
 // The product of a few token rows.
-int gemm_rows(const moe_linear_args* p, const Epilogue& e, cudaStream_t s) {
+int gemm_rows(const moe_linear_args* p, const Epilogue& e, int num_sms, cudaStream_t s) {
   RowsArgs a;
   a.x = p->x;
   a.w = p->w;
@@ -992,21 +1009,19 @@ int gemm_rows(const moe_linear_args* p, const Epilogue& e, cudaStream_t s) {
   a.M = (int)p->M;
   a.N = (int)p->N;
   a.K = (int)p->K;
-  // As many warps to a row of the weights as have kRowsUnroll steps each.
-  a.ks = kRowsWarps;
-  while (a.ks > 1 && p->K < 32LL * kRowsUnroll * a.ks) a.ks /= 2;
+  // Fewer warps to a row of the weights, and so fewer sums to put together, while the rows
+  // still make 1.4 CTAs for every SM, and where a warp would have less than a batch of k.
   const long long groups = (p->N + 7) / 8;
+  a.ks = kRowsWarps;
+  while (a.ks > 1 && (p->K < 32LL * kRowsUnroll * a.ks || 10 * groups * (a.ks / 2) >= 14LL * num_sms * kRowsWarps))
+    a.ks /= 2;
   const int per = kRowsWarps / a.ks;
-  const unsigned grid = (unsigned)((groups + per - 1) / per);
-  const bool bf16 = p->dtype == MOE_BF16, high = p->M > 8;
-  if (bf16 && high)
-    linear_rows_kernel<true, true><<<grid, 32 * kRowsWarps, 0, s>>>(a);
-  else if (bf16)
-    linear_rows_kernel<true, false><<<grid, 32 * kRowsWarps, 0, s>>>(a);
-  else if (high)
-    linear_rows_kernel<false, true><<<grid, 32 * kRowsWarps, 0, s>>>(a);
+  a.blocks = (p->N + 8 * per - 1) / (8 * per);
+  const unsigned grid = (unsigned)std::min<long long>(a.blocks, 2 * num_sms);
+  if (p->dtype == MOE_BF16)
+    linear_rows_kernel<true><<<grid, 32 * kRowsWarps, 0, s>>>(a);
   else
-    linear_rows_kernel<false, false><<<grid, 32 * kRowsWarps, 0, s>>>(a);
+    linear_rows_kernel<false><<<grid, 32 * kRowsWarps, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1153,7 +1168,7 @@ int moe_linear(const moe_linear_args* p, moe_stream_t stream) {
   e.vz = row_bytes(p->z, p->ld_z, p->dtype, p->M);
   e.vr = row_bytes(p->r, p->ld_r, p->dtype, p->M);
   e.vb = aligned_to(p->b, 16);
-  if (p->M <= kRowsMax) return gemm_rows(p, e, reinterpret_cast<cudaStream_t>(stream));
+  if (p->M <= kRowsMax) return gemm_rows(p, e, sms, reinterpret_cast<cudaStream_t>(stream));
   return gemm({p->x, p->ld_x, false}, {p->w, p->ld_w, false}, (int)p->M, (int)p->N, p->K,
               p->dtype == MOE_BF16, e, sms, reinterpret_cast<cudaStream_t>(stream));
 }
