@@ -137,14 +137,21 @@ __device__ __forceinline__ void act8(float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = act_of<ACT>(v[i]);
 }
 
-// Eight sums of row i from column j, n of them inside the matrix, to the outputs.
-__device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, int n, float (&v)[8]) {
-  float t[8];
+// The bias of eight columns from j, n of them inside the matrix; zeros without one.
+__device__ __forceinline__ void bias8(const Epilogue& e, int j, int n, float (&b)[8]) {
   if (e.b != nullptr) {
-    load8(e.b, e.btype, j, n, e.vb, t);
+    load8(e.b, e.btype, j, n, e.vb, b);
+  } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] += t[q];
+    for (int q = 0; q < 8; ++q) b[q] = 0.f;
   }
+}
+
+// Eight sums of row i from column j, n of them inside the matrix, to the outputs.
+__device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, int n, const float (&b)[8],
+                                        float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] += b[q];
   if (e.z != nullptr) store8(e.z, e.dtype, i * e.ld_z + j, n, e.vz != 0, v);
   switch (e.act) {  // the same for the whole grid
     case MOE_ACT_RELU: act8<MOE_ACT_RELU>(v); break;
@@ -154,6 +161,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, i
     default: break;
   }
   if (e.r != nullptr) {
+    float t[8];
     load8(e.r, e.dtype, i * e.ld_r + j, n, e.vr != 0, t);
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] += t[q];
@@ -239,6 +247,51 @@ size_t tile_smem_bytes(int bn, int stages) {
   const size_t pipe = (size_t)stages * (kABytes + bn * 128);
   const size_t dump = (size_t)kTileI * (bn + 4) * 4;
   return 1024 + std::max(pipe, dump) + sizeof(TileSmem);
+}
+
+// This CTA's share of a tile's elements: the partial sums of all S CTAs of the cluster, added
+// in the order of the ranks, through the epilogue. A thread keeps to eight columns, whose
+// bias it has, and takes every (256 S / chunks)-th row; a row's loads from all S are in flight
+// together, since shared memory of another CTA is far away.
+template <int S>
+__device__ __forceinline__ void join_tile(const GemmArgs& a, const float* dump, int rank, int rows, int i0,
+                                          int j, int c, const float (&bias)[8]) {
+  constexpr int U = S <= 2 ? 2 : 1;
+  const int chunks = a.bn / 8, pitch = a.bn + 4, each = kTileThreads / chunks;
+  const int n = a.J - j;
+  if (n <= 0) return;
+  uint32_t base[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) base[r] = S > 1 ? map_shared(dump, (uint32_t)r) : 0u;
+  for (int row0 = rank * each + (int)threadIdx.x / chunks; row0 < rows; row0 += U * S * each) {
+    float4 s[U][S], t[U][S];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = min(row0 + u * S * each, rows - 1) * pitch + c;
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+        if (S == 1) {
+          s[u][r] = *reinterpret_cast<const float4*>(dump + at);
+          t[u][r] = *reinterpret_cast<const float4*>(dump + at + 4);
+        } else {
+          s[u][r] = ld_cluster_v4(base[r] + at * 4);
+          t[u][r] = ld_cluster_v4(base[r] + at * 4 + 16);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = row0 + u * S * each;
+      if (row >= rows) break;
+      float v[8] = {s[u][0].x, s[u][0].y, s[u][0].z, s[u][0].w, t[u][0].x, t[u][0].y, t[u][0].z, t[u][0].w};
+#pragma unroll
+      for (int r = 1; r < S; ++r) {
+        v[0] += s[u][r].x, v[1] += s[u][r].y, v[2] += s[u][r].z, v[3] += s[u][r].w;
+        v[4] += t[u][r].x, v[5] += t[u][r].y, v[6] += t[u][r].z, v[7] += t[u][r].w;
+      }
+      finish8(a.e, i0 + row, j, n, bias, v);
+    }
+  }
 }
 
 // One tile of 128 x bn for each cluster of `splits` CTAs, each of which sums its range of
@@ -334,6 +387,10 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
     if (elect_one()) tc_commit(&sm.done);
   }
   __syncwarp();
+  // The bias of the columns this thread will finish is on its way during the products.
+  const int c0 = ((int)threadIdx.x % (a.bn / 8)) * 8;
+  float bias[8];
+  bias8(a.e, j0 + c0, a.J - j0 - c0, bias);
   volatile int never = 0;
   bool ok = mbar_wait_bounded(&sm.done, 0, &never, 2 * kWaitNs, g_status, 0x04000000u);
   ok = ok && *(volatile int*)&sm.abort == 0;
@@ -362,26 +419,11 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
   __syncthreads();
   if (a.splits > 1) cluster_sync_all();
   if (ok) {
-    const int chunks = a.bn / 8, total = rows * chunks;
-    for (int it = rank * kTileThreads + threadIdx.x; it < total; it += a.splits * kTileThreads) {
-      const int row = it / chunks, c = (it % chunks) * 8;
-      if (j0 + c >= a.J) continue;
-      const float* p = dump + (size_t)row * pitch + c;
-      float v[8];
-      if (a.splits == 1) {
-        const float4 s = *reinterpret_cast<const float4*>(p), t = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = s.x, v[1] = s.y, v[2] = s.z, v[3] = s.w, v[4] = t.x, v[5] = t.y, v[6] = t.z, v[7] = t.w;
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = 0.f;
-        for (int r = 0; r < a.splits; ++r) {
-          const uint32_t at = map_shared(p, (uint32_t)r);
-          const float4 s = ld_cluster_v4(at), t = ld_cluster_v4(at + 16);
-          v[0] += s.x, v[1] += s.y, v[2] += s.z, v[3] += s.w;
-          v[4] += t.x, v[5] += t.y, v[6] += t.z, v[7] += t.w;
-        }
-      }
-      finish8(a.e, i0 + row, j0 + c, a.J - j0 - c, v);
+    switch (a.splits) {
+      case 1: join_tile<1>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
+      case 2: join_tile<2>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
+      case 4: join_tile<4>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
+      default: join_tile<8>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
     }
   }
   __syncthreads();
@@ -484,10 +526,11 @@ __device__ __forceinline__ void finish32(const Epilogue& e, long long i, int j, 
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (8 * c < n) {
-        float t[8];
+        float t[8], b[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) t[q] = v[8 * c + q];
-        finish8(e, i, j + 8 * c, n - 8 * c, t);
+        bias8(e, j + 8 * c, n - 8 * c, b);
+        finish8(e, i, j + 8 * c, n - 8 * c, b, t);
       }
     }
     return;
@@ -1025,14 +1068,49 @@ int gemm_rows(const moe_linear_args* p, const Epilogue& e, int num_sms, cudaStre
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Which kernel and tiles take a product: the least of an estimate in microseconds, fitted to
+// measurements of 16 to 1024 rows at 2048 x 7168, 8192 x 2048, 1536 x 4096, 4096 x 1024 and
+// 512 x 1000 (within 20 % of them, and its choice within 10 % of the best there).
+// A step of 64 k takes a CTA 0.2 us, or what its bytes take at 165 GB/s an SM or 18 TB/s for
+// all; a pair's 256 x 256 x 64 takes 0.29 us. Starting, filling the pipeline and ending cost
+// 4 us (pairs: 7), an epilogue 0.1 us for 1000 elements. Joining S partial tiles costs 1.5 us
+// and what S CTAs read from one another's shared memory at 16 GB/s each. Clusters of 1, 2, 4 and 8 of these CTAs: 152, 76,
+// 36 and 15 fit on the GPU at once.
+struct TileChoice {
+  int bn, splits;  // bn -1: the pair kernel
+  double us;
+};
+TileChoice choose_tiles(int I, int J, int nk, bool b_mn, int num_sms) {
+  const long long ti = (I + kTileI - 1) / kTileI;
+  const long long t256 = ((long long)I + 255) / 256 * (((long long)J + 255) / 256);
+  const long long pairs = num_sms / 2;
+  TileChoice best{-1, 1, 7.0 + (double)((t256 + pairs - 1) / pairs) * nk * 0.29};
+  const int rows = std::min(I, kTileI);
+  for (int bn = b_mn ? 64 : 16; bn <= 256; bn *= 2) {
+    if (bn < 64 && bn < J) continue;  // under 64 columns only for all of J
+    const long long tiles = ti * ((J + bn - 1) / bn);
+    const double bytes = (double)(rows + bn) * 128;
+    for (int s = 1; s <= 8; s *= 2) {
+      if (nk < 2 * s && s > 1) break;
+      const long long fit = s == 1 ? num_sms : s == 2 ? num_sms / 2 : s == 4 ? 36LL * num_sms / 152 : 15LL * num_sms / 152;
+      const double waves = (double)((tiles + fit - 1) / std::max(1LL, fit));
+      const double busy = (double)(std::min(tiles, fit) * s);
+      const double step = std::max(0.2, std::max(bytes / 165e3, bytes * busy / 18e6));
+      const double join = s == 1 ? rows * bn * 1e-4 : 1.5 + (double)rows * bn * 4 / 16e3;
+      const double us = 4.0 + waves * (step * ((nk + s - 1) / s) + join);
+      if (us < best.us) best = TileChoice{bn, s, us};
+    }
+    if (bn >= J && bn >= 64) break;
+  }
+  return best;
+}
+
 // D[i][j] = sum_k A(i, k) B(j, k) through the epilogue.
 int gemm(const Operand& A, const Operand& B, int I, int J, long long K, bool bf16, const Epilogue& e,
          int num_sms, cudaStream_t s) {
   const int nk = (int)((K + kBlockK - 1) / kBlockK);
-  // Pairs from 24 tiles of 256 x 256 on: 256 x 8192 x 2048 (32 tiles) takes 22 us against
-  // 33 us of single CTAs, 512 x 2048 x 7168 (16 tiles) 49 us against 44.
-  if ((long long)((I + 255) / 256) * ((J + 255) / 256) >= 24)
-    return gemm_pair(A, B, I, J, nk, K, bf16, e, num_sms, s);
+  const TileChoice tc = choose_tiles(I, J, nk, B.mn, num_sms);
+  if (tc.bn < 0) return gemm_pair(A, B, I, J, nk, K, bf16, e, num_sms, s);
   GemmArgs a;
   a.e = e;
   a.I = I;
@@ -1040,14 +1118,9 @@ int gemm(const Operand& A, const Operand& B, int I, int J, long long K, bool bf1
   a.nk = nk;
   a.bf16 = bf16;
   a.tiles_i = (I + kTileI - 1) / kTileI;
-  // The narrowest tile that still gives every SM one, between 64 and 256 columns.
-  a.bn = 256;
-  while (a.bn > 64 && (long long)a.tiles_i * ((J + a.bn - 1) / a.bn) < num_sms) a.bn /= 2;
-  if (!B.mn)
-    while (a.bn > 16 && a.bn / 2 >= J) a.bn /= 2;
+  a.bn = tc.bn;
+  a.splits = tc.splits;
   const long long tiles = (long long)a.tiles_i * ((J + a.bn - 1) / a.bn);
-  a.splits = 1;
-  while (a.splits < 8 && tiles * a.splits * 2 <= num_sms && a.nk >= a.splits * 2 * 2) a.splits *= 2;
   if (tiles * a.splits > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   a.stages = std::min<int>(kMaxStages, (int)((kSmemMax - 1024 - sizeof(TileSmem)) / (kABytes + a.bn * 128)));
   a.box_a = std::min(kTileI, (I + 7) / 8 * 8);
