@@ -106,7 +106,9 @@ def test_linear(case):
     check(x, w, b, r, act, DT[out] if out else None, dy)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 24, 8), (5, 64, 200), (70, 90, 128), (300, 700, 96)])
+@pytest.mark.parametrize("M,N,K", [(1, 24, 8), (5, 64, 200), (70, 90, 128), (300, 700, 96),
+                                   (2304, 1536, 2056), (4100, 1030, 776), (700, 5000, 3000),
+                                   (6000, 300, 2500)])
 def test_whole_numbers_are_exact(M, N, K):
     """Small integers: every product and sum is exact in fp32, so the fp32 results are too.
     A wrong, missing or doubled element shows."""

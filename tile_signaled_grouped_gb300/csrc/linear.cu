@@ -65,6 +65,12 @@ __device__ __forceinline__ float act_grad(float z) {
   return 1.f;
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cl_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cl_addr) : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------- the epilogue
 struct Epilogue {
   void* y;        // [I][ld_y] of ytype
@@ -147,19 +153,59 @@ __device__ __forceinline__ void bias8(const Epilogue& e, int j, int n, float (&b
   }
 }
 
-// Eight sums of row i from column j, n of them inside the matrix, to the outputs.
-__device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, int n, const float (&b)[8],
-                                        float (&v)[8]) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) v[q] += b[q];
-  if (e.z != nullptr) store8(e.z, e.dtype, i * e.ld_z + j, n, e.vz != 0, v);
-  switch (e.act) {  // the same for the whole grid
+__device__ __forceinline__ void act8_any(float (&v)[8], int act) {
+  switch (act) {  // the same for the whole grid
     case MOE_ACT_RELU: act8<MOE_ACT_RELU>(v); break;
     case MOE_ACT_GELU: act8<MOE_ACT_GELU>(v); break;
     case MOE_ACT_GELU_TANH: act8<MOE_ACT_GELU_TANH>(v); break;
     case MOE_ACT_SILU: act8<MOE_ACT_SILU>(v); break;
     default: break;
   }
+}
+
+// Elements at[0] .. at[7] of an array, those of `mask`, one by one: the type is asked once.
+__device__ __forceinline__ void scatter8(void* p, int dtype, const long long (&at)[8], uint32_t mask,
+                                         const float (&f)[8]) {
+  if (dtype == MOE_FP32) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if ((mask >> q) & 1u) static_cast<float*>(p)[at[q]] = f[q];
+  } else if (dtype == MOE_BF16) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if ((mask >> q) & 1u) static_cast<__nv_bfloat16*>(p)[at[q]] = __float2bfloat16_rn(f[q]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if ((mask >> q) & 1u) static_cast<__half*>(p)[at[q]] = __float2half_rn(f[q]);
+  }
+}
+// Eight sums at rows i[q] and columns j[q], those of `mask`, whose residuals are r.
+__device__ __forceinline__ void finish_scattered(const Epilogue& e, const long long (&i)[8],
+                                                 const long long (&j)[8], uint32_t mask, const float (&r)[8],
+                                                 float (&v)[8]) {
+  long long at[8];
+  if (e.z != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) at[q] = i[q] * e.ld_z + j[q];
+    scatter8(e.z, e.dtype, at, mask, v);
+  }
+  act8_any(v, e.act);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    v[q] += r[q];
+    at[q] = i[q] * e.ld_y + j[q];
+  }
+  scatter8(e.y, e.ytype, at, mask, v);
+}
+
+// Eight sums of row i from column j, n of them inside the matrix, to the outputs.
+__device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, int n, const float (&b)[8],
+                                        float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] += b[q];
+  if (e.z != nullptr) store8(e.z, e.dtype, i * e.ld_z + j, n, e.vz != 0, v);
+  act8_any(v, e.act);
   if (e.r != nullptr) {
     float t[8];
     load8(e.r, e.dtype, i * e.ld_r + j, n, e.vr != 0, t);
@@ -167,6 +213,26 @@ __device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, i
     for (int q = 0; q < 8; ++q) v[q] += t[q];
   }
   store8(e.y, e.ytype, i * e.ld_y + j, n, e.vy != 0, v);
+}
+
+// act of a value whose kind is known at run time.
+__device__ __forceinline__ float act_any(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return act_of<MOE_ACT_RELU>(z);
+    case MOE_ACT_GELU: return act_of<MOE_ACT_GELU>(z);
+    case MOE_ACT_GELU_TANH: return act_of<MOE_ACT_GELU_TANH>(z);
+    case MOE_ACT_SILU: return act_of<MOE_ACT_SILU>(z);
+    default: return z;
+  }
+}
+
+// One sum of row i and column j to the outputs.
+__device__ __forceinline__ void finish1(const Epilogue& e, long long i, long long j, float v) {
+  if (e.b != nullptr) v += load_as_f32(e.b, e.btype, j);
+  if (e.z != nullptr) store_from_f32(e.z, e.dtype, i * e.ld_z + j, v);
+  v = act_any(v, e.act);
+  if (e.r != nullptr) v += load_as_f32(e.r, e.dtype, i * e.ld_r + j);
+  store_from_f32(e.y, e.ytype, i * e.ld_y + j, v);
 }
 
 // ------------------------------------------------------------------- tensor-core pieces
@@ -294,6 +360,47 @@ __device__ __forceinline__ void join_tile(const GemmArgs& a, const float* dump, 
   }
 }
 
+// The same where rows do not start on 16 bytes: neighbouring threads take neighbouring
+// columns, eight elements a thread at a time.
+template <int S>
+__device__ __forceinline__ void join_tile_any(const GemmArgs& a, const float* dump, int rank, int rows,
+                                              int i0, int j0) {
+  const int pitch = a.bn + 4, total = rows * a.bn, shift = 31 - __clz(a.bn);
+  uint32_t base[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) base[r] = map_shared(dump, (uint32_t)r);
+  for (int it = rank * kTileThreads + (int)threadIdx.x; it < total; it += 8 * S * kTileThreads) {
+    float v[8], r[8];
+    long long i[8], j[8];
+    uint32_t mask = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int x = min(it + u * S * kTileThreads, total - 1), c = x & (a.bn - 1), row = x >> shift;
+      const int at = (row * pitch + c) * 4;
+      mask |= (it + u * S * kTileThreads < total && j0 + c < a.J) ? 1u << u : 0u;
+      i[u] = i0 + row;
+      j[u] = min(j0 + c, a.J - 1);
+      r[u] = a.e.r != nullptr ? load_as_f32(a.e.r, a.e.dtype, i[u] * a.e.ld_r + j[u]) : 0.f;
+      v[u] = a.e.b != nullptr ? load_as_f32(a.e.b, a.e.btype, j[u]) : 0.f;
+      float s[S];
+#pragma unroll
+      for (int q = 0; q < S; ++q) s[q] = ld_cluster_f32(base[q] + at);
+#pragma unroll
+      for (int q = 1; q < S; ++q) s[0] += s[q];
+      v[u] += s[0];
+    }
+    finish_scattered(a.e, i, j, mask, r, v);
+  }
+}
+template <int S>
+__device__ __forceinline__ void join(const GemmArgs& a, const float* dump, int rank, int rows, int i0, int j0,
+                                     int c0, const float (&bias)[8]) {
+  if (a.e.vy != 0 && (a.e.z == nullptr || a.e.vz != 0) && (a.e.r == nullptr || a.e.vr != 0))
+    join_tile<S>(a, dump, rank, rows, i0, j0 + c0, c0, bias);
+  else
+    join_tile_any<S>(a, dump, rank, rows, i0, j0);
+}
+
 // One tile of 128 x bn for each cluster of `splits` CTAs, each of which sums its range of
 // k in its TMEM. The partial sums then meet in shared memory: every CTA adds a share of
 // the tile's elements from all of them, in the order of the ranks, and finishes it. Warp 0
@@ -328,6 +435,7 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  wait_prior_grid();  // behind a kernel that allows it, all of the above ran beside that one
 
   if (warp == 0) {
     const uint32_t bytes = (AMN ? kABytes : a.box_a * 128) + b_bytes;
@@ -420,10 +528,10 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
   if (a.splits > 1) cluster_sync_all();
   if (ok) {
     switch (a.splits) {
-      case 1: join_tile<1>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
-      case 2: join_tile<2>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
-      case 4: join_tile<4>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
-      default: join_tile<8>(a, dump, rank, rows, i0, j0 + c0, c0, bias); break;
+      case 1: join<1>(a, dump, rank, rows, i0, j0, c0, bias); break;
+      case 2: join<2>(a, dump, rank, rows, i0, j0, c0, bias); break;
+      case 4: join<4>(a, dump, rank, rows, i0, j0, c0, bias); break;
+      default: join<8>(a, dump, rank, rows, i0, j0, c0, bias); break;
     }
   }
   __syncthreads();
@@ -436,7 +544,7 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
 // Many tiles: a persistent kernel of clusters of two CTAs, each pair with one tcgen05.mma
 // of 256 rows at a time (cta_group::2). A CTA stages its own 128 rows of A and half of B's
 // columns, so a 256 x 256 x 64 step loads 64 KB for the pair; the accumulators of two
-// tiles (2 x bn columns of TMEM) alternate, so that eight epilogue warps empty one while
+// tiles (2 x 256 columns of TMEM) alternate, so that eight epilogue warps empty one while
 // the next is summed. The pairs take tiles in turn; eight row tiles share a group of
 // columns, so the tiles in flight share their operands in L2.
 constexpr int kPairMaxStages = 8;
@@ -444,14 +552,28 @@ constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
 constexpr int kPairGroup = 8;  // row tiles that walk the columns together
 
-struct PairArgs {
+struct PairProduct {
   CUtensorMap ta, tb;
   Epilogue e;
   int I, J, nk;
-  int bn;  // columns of a tile
-  int stages;
   int tiles_i, tiles_j;
-  bool bf16, a_mn, b_mn;
+  bool a_mn, b_mn;
+  bool any_rows;  // rows of the outputs or the residual that do not start on 16 bytes
+};
+constexpr int kPairCols = 256;   // columns of a tile
+constexpr int kPairRounds = 24;  // tiles of a product that a pair takes at most by `live`
+
+// One product, whose tiles the pairs take in turn (products = 1: tile p, p + pairs, ...), or
+// the two of a backward pass in one launch. Then pair p takes, of product q in round k, the
+// tile that its rank numbers among the live[q][k] pairs that take one; the ranks count from
+// pair 0 in the first product and from the last pair in the second, so that the pairs with
+// a tile less of the first get one more of the second.
+struct PairArgs {
+  PairProduct p[2];
+  int products, stages;
+  bool bf16;
+  bool any_rows;  // of one of the products: a patch of shared memory for every epilogue warp
+  uint16_t live[2][kPairRounds];
 };
 
 struct PairSmem {
@@ -462,17 +584,52 @@ struct PairSmem {
   int abort;
 };
 
-size_t pair_smem_bytes(int bn, int stages) {
-  return 1024 + (size_t)stages * (kABytes + bn * 64) + sizeof(PairSmem);
+constexpr int kPairStageBytes = kABytes + kPairCols * 64;  // a CTA's rows of A and half of B
+constexpr int kPatchPitch = 33;
+constexpr int kPatchBytes = kPairEpiWarps * 32 * kPatchPitch * 4;
+size_t pair_smem_bytes(int stages, bool any_rows) {
+  return 1024 + (size_t)stages * kPairStageBytes + (any_rows ? kPatchBytes : 0) + sizeof(PairSmem);
 }
 
-// Tile t of the order: groups of kPairGroup row tiles, inside a group column by column.
-__device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int* ti, int* tj) {
-  const int per = kPairGroup * a.tiles_j, g = t / per, r = t - g * per;
-  const int rows = min(kPairGroup, a.tiles_i - g * kPairGroup);
-  *tj = r / rows;
-  *ti = g * kPairGroup + r - *tj * rows;
-}
+// The tiles of one pair in their order; every role of both CTAs walks the same.
+struct PairWalk {
+  const PairArgs& a;
+  int pair, pairs;
+  int q, ti, tj;  // the product and the tile, once next() has said there is one
+  int k, base;
+
+  __device__ __forceinline__ PairWalk(const PairArgs& args, int p, int n)
+      : a(args), pair(p), pairs(n), q(0), ti(0), tj(0), k(0), base(0) {}
+
+  __device__ __forceinline__ bool next() {
+    int t;
+    if (a.products == 1) {
+      t = base + pair;
+      base += pairs;
+      if (t >= a.p[0].tiles_i * a.p[0].tiles_j) return false;
+    } else {
+      while (true) {
+        const int rank = q == 0 ? pair : pairs - 1 - pair;
+        const int live = k < kPairRounds ? a.live[q][k] : 0;
+        if (rank < live) {
+          t = base + rank;
+          base += live;
+          ++k;
+          break;
+        }
+        if (q == 1) return false;
+        q = 1;
+        k = base = 0;
+      }
+    }
+    // Groups of kPairGroup row tiles, inside a group column by column.
+    const int cols = a.p[q].tiles_j, per = kPairGroup * cols, g = t / per, r = t - g * per;
+    const int rows = min(kPairGroup, a.p[q].tiles_i - g * kPairGroup);
+    tj = r / rows;
+    ti = g * kPairGroup + r - tj * rows;
+    return true;
+  }
+};
 
 // 32 sums of row i from column j, n of them inside the matrix, to the outputs: 32 bytes (a
 // sector) a store where the rows allow it.
@@ -522,7 +679,7 @@ __device__ __forceinline__ void act32(float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = act_of<ACT>(v[i]);
 }
 __device__ __forceinline__ void finish32(const Epilogue& e, long long i, int j, int n, float (&v)[32]) {
-  if (n < 32 || e.vy == 0 || (e.z != nullptr && e.vz == 0) || (e.r != nullptr && e.vr == 0) || !e.vb) {
+  if (n < 32 || !e.vb) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (8 * c < n) {
@@ -558,18 +715,43 @@ __device__ __forceinline__ void finish32(const Epilogue& e, long long i, int j, 
   store32(e.y, e.ytype, i * e.ld_y + j, e.vy >= 32, v);
 }
 
+// A warp's 32 x 32 sums (lane l has row l), `rows` x n of them inside the matrix, where rows do
+// not start on 16 bytes: turned round in shared memory, so that the lanes are neighbouring
+// columns of one row. (Without it, 34 us for a tile.)
+__device__ __forceinline__ void finish_patch(const Epilogue& e, float* patch, long long i0, int rows, int j,
+                                             int n, const float (&v)[32], int lane) {
+  __syncwarp();  // the patch's last readers
+#pragma unroll
+  for (int x = 0; x < 32; ++x) patch[lane * kPatchPitch + x] = v[x];
+  __syncwarp();
+  if (lane >= n) return;
+  const float bias = e.b != nullptr ? load_as_f32(e.b, e.btype, j + lane) : 0.f;
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    float f[8], t[8];
+    long long i[8], c[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int row = min(r0 + r, rows - 1);
+      i[r] = i0 + row;
+      c[r] = j + lane;
+      t[r] = e.r != nullptr ? load_as_f32(e.r, e.dtype, i[r] * e.ld_r + c[r]) : 0.f;
+      f[r] = patch[row * kPatchPitch + lane] + bias;
+    }
+    finish_scattered(e, i, c, (1u << min(8, rows - r0)) - 1u, t, f);
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  const int b_bytes = a.bn * 64, stage_bytes = kABytes + b_bytes;  // this CTA's half of B
-  PairSmem& sm = *reinterpret_cast<PairSmem*>(base + (size_t)a.stages * stage_bytes);
+  uint8_t* after = base + (size_t)a.stages * kPairStageBytes;
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(after + (a.any_rows ? kPatchBytes : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
-  const uint32_t cols = 2 * a.bn;
-  const int tiles = a.tiles_i * a.tiles_j, pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  PairWalk walk(a, blockIdx.x >> 1, gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -584,45 +766,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sm.abort = 0;
   }
-  if (warp == 1) tmem_alloc_pair(&sm.tmem, cols);
+  if (warp == 1) tmem_alloc_pair(&sm.tmem, 2 * kPairCols);
   tc_fence_before();
   __syncthreads();
   __syncwarp();
   cluster_sync_all();  // both CTAs: barriers initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  wait_prior_grid();  // behind a kernel that allows it, all of the above ran beside that one
 
   if (warp == 0) {
-    const uint32_t bytes = 2 * (uint32_t)stage_bytes;
+    constexpr uint32_t bytes = 2 * kPairStageBytes;
     int n = 0, st = 0;
     uint32_t phase = 1;
     bool ok = true;
-    for (int t = pair0; t < tiles && ok; t += pairs) {
-      int ti, tj;
-      pair_tile(a, t, &ti, &tj);
-      const int i0 = ti * 256 + (int)crank * 128, j0 = tj * a.bn + (int)crank * (a.bn / 2);
-      for (int kb = 0; kb < a.nk; ++kb, ++n) {
+    while (ok && walk.next()) {
+      const PairProduct& p = a.p[walk.q];
+      const int i0 = walk.ti * 256 + (int)crank * 128;
+      const int j0 = walk.tj * kPairCols + (int)crank * (kPairCols / 2);
+      for (int kb = 0; kb < p.nk; ++kb, ++n) {
         if (!warp_pwait(&sm.empty[st], phase, &sm.abort, 0x11000000u)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          uint8_t* as = base + (size_t)st * stage_bytes;
+          uint8_t* as = base + (size_t)st * kPairStageBytes;
           uint8_t* bs = as + kABytes;
           if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
           const uint32_t fb = map_shared(&sm.full[st], 0);
           const int k0 = kb * kBlockK;
-          if (a.a_mn) {
-            tma_load_2d_pair(as, &a.ta, fb, i0, k0);
-            tma_load_2d_pair(as + 8192, &a.ta, fb, i0 + 64, k0);
+          if (p.a_mn) {
+            tma_load_2d_pair(as, &p.ta, fb, i0, k0);
+            tma_load_2d_pair(as + 8192, &p.ta, fb, i0 + 64, k0);
           } else {
-            tma_load_2d_pair(as, &a.ta, fb, k0, i0);
+            tma_load_2d_pair(as, &p.ta, fb, k0, i0);
           }
-          if (a.b_mn) {
-            for (int c = 0; c < a.bn / 128; ++c)
-              tma_load_2d_pair(bs + c * 8192, &a.tb, fb, j0 + c * 64, k0);
+          if (p.b_mn) {
+            for (int c = 0; c < kPairCols / 128; ++c)
+              tma_load_2d_pair(bs + c * 8192, &p.tb, fb, j0 + c * 64, k0);
           } else {
-            tma_load_2d_pair(bs, &a.tb, fb, k0, j0);
+            tma_load_2d_pair(bs, &p.tb, fb, k0, j0);
           }
         }
         __syncwarp();
@@ -637,20 +820,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       pwait(&sm.empty[i % a.stages], (i / a.stages) & 1, &never, left > 0 ? left : 0, g_status, 0x12000000u);
     }
   } else if (warp == 1 && lead) {
-    const uint32_t idesc = idesc_16bit(a.bf16, a.a_mn, a.b_mn, 256, a.bn);
     const uint32_t s0 = (smem_u32(base) & 0x3FFFFu) >> 4;  // above lies the CTA's rank in its cluster
-    const uint64_t da = (a.a_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0;
-    const uint64_t db = (a.b_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0 + (kABytes >> 4);
-    const uint32_t step_a = (a.a_mn ? 2048 : 32) >> 4, step_b = (a.b_mn ? 2048 : 32) >> 4;
     int it = 0, st = 0;
     uint32_t phase = 0, at = 0;  // at: the stage's offset in 16-byte units
     bool ok = true;
-    for (int t = pair0; t < tiles && ok; t += pairs, ++it) {
+    for (; ok && walk.next(); ++it) {
+      const PairProduct& p = a.p[walk.q];
+      const uint32_t idesc = idesc_16bit(a.bf16, p.a_mn, p.b_mn, 256, kPairCols);
+      const uint64_t da = (p.a_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0;
+      const uint64_t db = (p.b_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0 + (kABytes >> 4);
+      const uint32_t step_a = (p.a_mn ? 2048 : 32) >> 4, step_b = (p.b_mn ? 2048 : 32) >> 4;
       const int acc = it & 1;
       if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, 0x21000000u)) break;
       tc_fence_after();
-      const uint32_t dt = tmem + (uint32_t)(acc * a.bn);
-      for (int kb = 0; kb < a.nk; ++kb) {
+      const uint32_t dt = tmem + (uint32_t)(acc * kPairCols);
+      for (int kb = 0; kb < p.nk; ++kb) {
         if (!warp_pwait(&sm.full[st], phase, &sm.abort, 0x22000000u)) {
           ok = false;
           break;
@@ -664,7 +848,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
         next_stage(st, phase, a.stages);
-        at = st == 0 ? 0 : at + (stage_bytes >> 4);
+        at = st == 0 ? 0 : at + (kPairStageBytes >> 4);
       }
       if (ok && elect_one()) tc_commit_pair(&sm.tfull[acc], 0x3);
       __syncwarp();
@@ -678,17 +862,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the columns
     const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
     int it = 0;
-    for (int t = pair0; t < tiles; t += pairs, ++it) {
-      int ti, tj;
-      pair_tile(a, t, &ti, &tj);
+    for (; walk.next(); ++it) {
+      const PairProduct& p = a.p[walk.q];
       const int acc = it & 1;
       if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, 0x31000000u)) break;
       tc_fence_after();
-      const int row = ti * 256 + (int)crank * 128 + q * 32 + lane;
-      const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * a.bn);
-      const int c1 = (half + 1) * (a.bn / 2);
+      const int row = walk.ti * 256 + (int)crank * 128 + q * 32 + lane;
+      const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kPairCols);
+      const int c1 = (half + 1) * (kPairCols / 2);
 #pragma unroll 1
-      for (int c = half * (a.bn / 2); c < c1; c += 32) {
+      for (int c = half * (kPairCols / 2); c < c1; c += 32) {
         uint32_t v[32];
         tmem_ld32(src + c, v);
         tmem_ld_wait();
@@ -697,13 +880,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty[acc]);
         }
-        const int j = tj * a.bn + c;
-        if (row < a.I && j < a.J) {
-          float f[32];
+        const int j = walk.tj * kPairCols + c;
+        if (j >= p.J) continue;
+        float f[32];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
-          finish32(a.e, row, j, a.J - j, f);
-        }
+        for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
+        if (p.any_rows)  // whole warps: row - lane is the first of its 32 rows
+          finish_patch(p.e, reinterpret_cast<float*>(after) + (warp - 2) * 32 * kPatchPitch, row - lane,
+                       min(32, p.I - (row - lane)), j, min(32, p.J - j), f, lane);
+        else if (row < p.I)
+          finish32(p.e, row, j, p.J - j, f);
       }
     }
   }
@@ -714,7 +900,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, cols);
+  if (warp == 1) tmem_dealloc_pair(tmem, 2 * kPairCols);
 }
 
 // ------------------------------------------------------------------- few rows
@@ -776,17 +962,6 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// act of a value whose kind is known at run time.
-__device__ __forceinline__ float act_any(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return act_of<MOE_ACT_RELU>(z);
-    case MOE_ACT_GELU: return act_of<MOE_ACT_GELU>(z);
-    case MOE_ACT_GELU_TANH: return act_of<MOE_ACT_GELU_TANH>(z);
-    case MOE_ACT_SILU: return act_of<MOE_ACT_SILU>(z);
-    default: return z;
-  }
 }
 
 template <bool BF16>
@@ -854,11 +1029,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2) linear_rows_kernel(const _
       if (j >= a.N) continue;
       float v = 0.f;
       for (int r = 0; r < a.ks; ++r) v += part[parity][q * a.ks + r][i][c];
-      if (a.e.b != nullptr) v += load_as_f32(a.e.b, a.e.btype, j);
-      if (a.e.z != nullptr) store_from_f32(a.e.z, a.e.dtype, i * a.e.ld_z + j, v);
-      v = act_any(v, a.e.act);
-      if (a.e.r != nullptr) v += load_as_f32(a.e.r, a.e.dtype, i * a.e.ld_r + j);
-      store_from_f32(a.e.y, a.e.ytype, i * a.e.ld_y + j, v);
+      finish1(a.e, i, j, v);
     }
   }
 }
@@ -871,66 +1042,116 @@ struct ActGradArgs {
   float* part;    // [gridDim.y][N] column sums, or null
   long long ld_dy, ld_z, ld_dz;
   int M, N, dtype, rows;  // rows of a CTA
-  bool vdy, vz;           // rows start on 16 bytes (dz's always do)
 };
 
-// dz = dy act'(z) and its column sums: a thread takes eight columns of every eighth row of
-// the CTA's range, warp w row w, w + 8, ...; the eight warps' sums are added in order. dz
-// is rounded to the operands' type for the products; the sums take it unrounded. Bound by
-// the bytes of dy, z and dz.
-template <int ACT>
-__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
-  __shared__ float red[8][32][9];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = (blockIdx.x * 32 + lane) * 8;
-  const int n = a.N - j;
-  const int lo = blockIdx.y * a.rows, hi = min(a.M, lo + a.rows);
-  float s[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) s[q] = 0.f;
-  if (n > 0) {
-    for (int i = lo + warp; i < hi; i += 8) {
-      float d[8];
-      load8(a.dy, a.dtype, (long long)i * a.ld_dy + j, n, a.vdy, d);
-      if (ACT != MOE_ACT_NONE) {
-        float z[8];
-        load8(a.z, a.dtype, (long long)i * a.ld_z + j, n, a.vz, z);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) d[q] *= act_grad<ACT>(z[q]);
-      }
-      if (a.dz != nullptr) store8(a.dz, a.dtype, (long long)i * a.ld_dz + j, n, true, d);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) s[q] += d[q];
-    }
-  }
-  if (a.part == nullptr) return;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) red[warp][lane][q] = s[q];
-  __syncthreads();
-  const int c = threadIdx.x;  // one of the CTA's 256 columns
-  if (blockIdx.x * 256 + c < a.N) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) v += red[w][c >> 3][c & 7];
-    a.part[(size_t)blockIdx.y * a.N + blockIdx.x * 256 + c] = v;
-  }
+// Eight elements of 16 bits as fp32.
+__device__ __forceinline__ void unpack8(const uint4& u, int dtype, float (&f)[8]) {
+  if (dtype == MOE_BF16)
+    unpack<__nv_bfloat16>(u, f);
+  else
+    unpack<__half>(u, f);
 }
 
-// db from the row ranges' sums: eight warps share the ranges, then their sums in order.
-__global__ void __launch_bounds__(256) bias_grad_kernel(const float* part, int parts, int N, int btype,
-                                                       void* db) {
-  __shared__ float red[8][32];
+// dz = dy act'(z) and its column sums, for the rows of a range; 256 columns a CTA. dz is
+// rounded to the operands' type for the products; the sums take it unrounded. Bound by the
+// bytes of dy, z and dz. VEC: rows on 16 bytes and N a multiple of 8; a thread takes eight
+// columns of four rows at a time, warp w rows 4 w .. of every 32, and all eight loads leave
+// before the first is used; the eight warps' sums are added in order. Otherwise a thread
+// takes one column, so that neighbouring threads read neighbouring elements.
+constexpr int kActRows = 4;
+template <int ACT, bool VEC>
+__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
+  __shared__ float red[VEC ? 8 : 1][32][9];
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lo = blockIdx.y * a.rows, hi = min(a.M, lo + a.rows);
+  const int c = blockIdx.x * 256 + threadIdx.x;  // the column whose sum this thread writes
+  float sum = 0.f;
+  if constexpr (VEC) {
+    const int j = (blockIdx.x * 32 + lane) * 8;
+    const unsigned short* dy = static_cast<const unsigned short*>(a.dy) + j;
+    const unsigned short* z = static_cast<const unsigned short*>(a.z) + j;
+    float s[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s[q] = 0.f;
+    if (j < a.N) {
+      for (int i0 = lo + warp * kActRows; i0 < hi; i0 += 8 * kActRows) {
+        uint4 du[kActRows], zu[kActRows];
+#pragma unroll
+        for (int r = 0; r < kActRows; ++r) {
+          const long long i = min(i0 + r, hi - 1);
+          du[r] = __ldg(reinterpret_cast<const uint4*>(dy + i * a.ld_dy));
+          if (ACT != MOE_ACT_NONE) zu[r] = __ldg(reinterpret_cast<const uint4*>(z + i * a.ld_z));
+        }
+#pragma unroll
+        for (int r = 0; r < kActRows; ++r) {
+          if (i0 + r < hi) {
+            float d[8];
+            unpack8(du[r], a.dtype, d);
+            if (ACT != MOE_ACT_NONE) {
+              float v[8];
+              unpack8(zu[r], a.dtype, v);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) d[q] *= act_grad<ACT>(v[q]);
+            }
+            if (a.dz != nullptr) store8(a.dz, a.dtype, (long long)(i0 + r) * a.ld_dz + j, 8, true, d);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s[q] += d[q];
+          }
+        }
+      }
+    }
+    if (a.part == nullptr) return;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) red[warp][lane][q] = s[q];
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += red[w][threadIdx.x >> 3][threadIdx.x & 7];
+  } else {
+    const int j = min(c, a.N - 1);
+    for (int i0 = lo; i0 < hi; i0 += kActRows) {
+      float d[kActRows], z[kActRows];
+#pragma unroll
+      for (int r = 0; r < kActRows; ++r) {
+        const long long i = min(i0 + r, hi - 1);
+        d[r] = load_as_f32(a.dy, a.dtype, i * a.ld_dy + j);
+        z[r] = ACT != MOE_ACT_NONE ? load_as_f32(a.z, a.dtype, i * a.ld_z + j) : 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < kActRows; ++r) {
+        if (i0 + r < hi) {
+          if (ACT != MOE_ACT_NONE) d[r] *= act_grad<ACT>(z[r]);
+          if (a.dz != nullptr && c < a.N) store_from_f32(a.dz, a.dtype, (long long)(i0 + r) * a.ld_dz + c, d[r]);
+          sum += d[r];
+        }
+      }
+    }
+    if (a.part == nullptr) return;
+  }
+  if (c < a.N) a.part[(size_t)blockIdx.y * a.N + c] = sum;
+}
+
+// db from the row ranges' sums: sixteen warps share the ranges, then their sums in order.
+// Starts while the kernel before it ends, and the products behind it start beside it.
+constexpr int kBiasWarps = 16;
+__global__ void __launch_bounds__(32 * kBiasWarps)
+    bias_grad_kernel(const float* part, int parts, int N, int btype, void* db) {
+  __shared__ float red[kBiasWarps][32];
+  allow_dependent_launch();
+  wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < N)
-    for (int r = warp; r < parts; r += 8) s += part[(size_t)r * N + c];
+  if (c < N) {
+#pragma unroll 8
+    for (int r = warp; r < parts; r += kBiasWarps) s += part[(size_t)r * N + c];
+  }
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < N) {
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += red[i][lane];
+    for (int i = 0; i < kBiasWarps; ++i) v += red[i][lane];
     store_from_f32(db, btype, c, v);
   }
 }
@@ -983,11 +1204,13 @@ cudaError_t launch_tile(const GemmArgs& a, int tiles, cudaStream_t s) {
   cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = tile_smem_bytes(a.bn, a.stages);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)a.splits, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, linear_tile_kernel<AMN, BMN>, a);
 }
 
@@ -1011,34 +1234,94 @@ int pair_clusters(int num_sms) {
   return n;
 }
 
-int gemm_pair(const Operand& A, const Operand& B, int I, int J, int nk, long long K, bool bf16,
-              const Epilogue& e, int num_sms, cudaStream_t s) {
+// A product D[i][j] = sum_k A(i, k) B(j, k) through the epilogue.
+struct Product {
+  Operand A, B;
+  int I, J;
+  long long K;
+  Epilogue e;
+  int nk() const { return (int)((K + kBlockK - 1) / kBlockK); }
+  long long tiles256() const { return ((long long)I + 255) / 256 * (((long long)J + 255) / 256); }
+};
+
+bool aligned_rows(const Epilogue& e) {
+  return e.vy != 0 && (e.z == nullptr || e.vz != 0) && (e.r == nullptr || e.vr != 0);
+}
+
+bool pair_product(const Product& g, bool bf16, PairProduct* p) {
+  p->e = g.e;
+  p->I = g.I;
+  p->J = g.J;
+  p->nk = g.nk();
+  p->tiles_i = (g.I + 255) / 256;
+  p->tiles_j = (g.J + kPairCols - 1) / kPairCols;
+  p->a_mn = g.A.mn;
+  p->b_mn = g.B.mn;
+  p->any_rows = !aligned_rows(g.e);
+  return (g.A.mn ? make_map(&p->ta, g.A.p, bf16, g.K, g.I, g.A.ld, kBlockK)
+                 : make_map(&p->ta, g.A.p, bf16, g.I, g.K, g.A.ld, kTileI)) &&
+         (g.B.mn ? make_map(&p->tb, g.B.p, bf16, g.K, g.J, g.B.ld, kBlockK)
+                 : make_map(&p->tb, g.B.p, bf16, g.J, g.K, g.B.ld, kPairCols / 2));
+}
+
+int launch_pairs(PairArgs& a, int pairs, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  constexpr int bn = 256;
-  PairArgs a;
-  a.e = e;
-  a.I = I;
-  a.J = J;
-  a.nk = nk;
-  a.bn = bn;
-  a.stages = std::min<int>(kPairMaxStages,
-                           (int)((kSmemMax - 1024 - sizeof(PairSmem)) / (kABytes + bn * 64)));
-  a.tiles_i = (I + 255) / 256;
-  a.tiles_j = (J + bn - 1) / bn;
-  a.bf16 = bf16;
-  a.a_mn = A.mn;
-  a.b_mn = B.mn;
-  const bool ok = (A.mn ? make_map(&a.ta, A.p, bf16, K, I, A.ld, kBlockK)
-                        : make_map(&a.ta, A.p, bf16, I, K, A.ld, kTileI)) &&
-                  (B.mn ? make_map(&a.tb, B.p, bf16, K, J, B.ld, kBlockK)
-                        : make_map(&a.tb, B.p, bf16, J, K, B.ld, bn / 2));
-  if (!ok || allow_smem(reinterpret_cast<const void*>(linear_pair_kernel), &ready) != cudaSuccess) {
+  a.any_rows = a.p[0].any_rows || (a.products == 2 && a.p[1].any_rows);
+  a.stages = std::min<int>(kPairMaxStages, (int)((kSmemMax - pair_smem_bytes(0, a.any_rows)) / kPairStageBytes));
+  if (allow_smem(reinterpret_cast<const void*>(linear_pair_kernel), &ready) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
-  const int pairs = std::min(pair_clusters(num_sms), a.tiles_i * a.tiles_j);
-  linear_pair_kernel<<<2 * pairs, kPairThreads, pair_smem_bytes(bn, a.stages), s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaError_t e = launch_behind(linear_pair_kernel, dim3(2 * pairs), dim3(kPairThreads),
+                                      pair_smem_bytes(a.stages, a.any_rows), s, a);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int gemm_pair(const Product& g, bool bf16, int num_sms, cudaStream_t s) {
+  PairArgs a;
+  a.products = 1;
+  a.bf16 = bf16;
+  if (g.tiles256() > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  if (!pair_product(g, bf16, &a.p[0])) return MOE_ERR_CUDA;
+  return launch_pairs(a, (int)std::min<long long>(pair_clusters(num_sms), g.tiles256()), s);
+}
+
+// How the pairs share the tiles of two products: the longer tiles (of `first`) in turn, then
+// each of the others to the pairs with the least steps so far. Returns the steps of the pair
+// with the most, or 0 where a pair would take more than kPairRounds tiles of one.
+long long share_tiles(const Product& first, const Product& second, int pairs, uint16_t (*live)[kPairRounds]) {
+  const long long n0 = first.tiles256(), n1 = second.tiles256();
+  if (n0 > (long long)pairs * kPairRounds || n1 > (long long)pairs * kPairRounds) return 0;
+  for (int k = 0; k < kPairRounds; ++k) live[0][k] = (uint16_t)std::max(0LL, std::min<long long>(pairs, n0 - (long long)k * pairs));
+  // Pairs 0 .. more - 1 have `rounds` tiles of the first product, the others one less; a group's
+  // pairs get their tiles of the second together, the last time perhaps only some of them.
+  const long long rounds = (n0 + pairs - 1) / pairs;
+  const int more = (int)(n0 - (rounds - 1) * pairs);
+  const long long size[2] = {more, pairs - more};
+  const long long load[2] = {rounds * first.nk(), (rounds - 1) * first.nk()};
+  long long got[2] = {0, 0}, some[2] = {0, 0}, left = n1;
+  while (left > 0) {
+    const long long at0 = load[0] + got[0] * second.nk(), at1 = load[1] + got[1] * second.nk();
+    const int g = size[1] == 0 || at0 < at1 ? 0 : 1;
+    if (left >= size[g]) {
+      ++got[g];
+      left -= size[g];
+    } else {
+      some[g] = left;
+      left = 0;
+    }
+  }
+  long long most = 0;
+  for (int g = 0; g < 2; ++g)
+    if (size[g] > 0) most = std::max(most, load[g] + (got[g] + (some[g] > 0)) * second.nk());
+  // live[1][k]: the pairs with more than k tiles. The ranks (from the last pair) hand them out
+  // to the second group first, which has at least as many each.
+  for (int k = 0; k < kPairRounds; ++k) {
+    long long c = 0;
+    for (int g = 0; g < 2; ++g) c += got[g] > k ? size[g] : got[g] == k ? some[g] : 0;
+    live[1][k] = (uint16_t)c;
+  }
+  return got[0] > kPairRounds - 1 || got[1] > kPairRounds - 1 ? 0 : most;
 }
 
 // The product of a few token rows.
@@ -1073,18 +1356,20 @@ int gemm_rows(const moe_linear_args* p, const Epilogue& e, int num_sms, cudaStre
 // 512 x 1000 (within 20 % of them, and its choice within 10 % of the best there).
 // A step of 64 k takes a CTA 0.2 us, or what its bytes take at 165 GB/s an SM or 18 TB/s for
 // all; a pair's 256 x 256 x 64 takes 0.29 us. Starting, filling the pipeline and ending cost
-// 4 us (pairs: 7), an epilogue 0.1 us for 1000 elements. Joining S partial tiles costs 1.5 us
+// 4 us (pairs: 7), an epilogue 0.1 us for 1000 elements (0.35 us where rows do not start on
+// 16 bytes; 7 us for a pair). Joining S partial tiles costs 1.5 us
 // and what S CTAs read from one another's shared memory at 16 GB/s each. Clusters of 1, 2, 4 and 8 of these CTAs: 152, 76,
 // 36 and 15 fit on the GPU at once.
+constexpr double kPairStart = 7.0, kPairStep = 0.29;
 struct TileChoice {
   int bn, splits;  // bn -1: the pair kernel
   double us;
 };
-TileChoice choose_tiles(int I, int J, int nk, bool b_mn, int num_sms) {
+TileChoice choose_tiles(int I, int J, int nk, bool b_mn, bool aligned, int num_sms) {
   const long long ti = (I + kTileI - 1) / kTileI;
   const long long t256 = ((long long)I + 255) / 256 * (((long long)J + 255) / 256);
   const long long pairs = num_sms / 2;
-  TileChoice best{-1, 1, 7.0 + (double)((t256 + pairs - 1) / pairs) * nk * 0.29};
+  TileChoice best{-1, 1, kPairStart + (aligned ? 0.0 : 7.0) + (double)((t256 + pairs - 1) / pairs) * nk * kPairStep};
   const int rows = std::min(I, kTileI);
   for (int bn = b_mn ? 64 : 16; bn <= 256; bn *= 2) {
     if (bn < 64 && bn < J) continue;  // under 64 columns only for all of J
@@ -1096,7 +1381,8 @@ TileChoice choose_tiles(int I, int J, int nk, bool b_mn, int num_sms) {
       const double waves = (double)((tiles + fit - 1) / std::max(1LL, fit));
       const double busy = (double)(std::min(tiles, fit) * s);
       const double step = std::max(0.2, std::max(bytes / 165e3, bytes * busy / 18e6));
-      const double join = s == 1 ? rows * bn * 1e-4 : 1.5 + (double)rows * bn * 4 / 16e3;
+      const double join = (s == 1 ? 0.0 : 1.5 + (double)rows * bn * 4 / 16e3) +
+                          rows * bn * (aligned ? s == 1 ? 1e-4 : 0.0 : 3.5e-4) / s;
       const double us = 4.0 + waves * (step * ((nk + s - 1) / s) + join);
       if (us < best.us) best = TileChoice{bn, s, us};
     }
@@ -1105,14 +1391,14 @@ TileChoice choose_tiles(int I, int J, int nk, bool b_mn, int num_sms) {
   return best;
 }
 
-// D[i][j] = sum_k A(i, k) B(j, k) through the epilogue.
-int gemm(const Operand& A, const Operand& B, int I, int J, long long K, bool bf16, const Epilogue& e,
-         int num_sms, cudaStream_t s) {
-  const int nk = (int)((K + kBlockK - 1) / kBlockK);
-  const TileChoice tc = choose_tiles(I, J, nk, B.mn, num_sms);
-  if (tc.bn < 0) return gemm_pair(A, B, I, J, nk, K, bf16, e, num_sms, s);
+int gemm(const Product& g, bool bf16, int num_sms, cudaStream_t s) {
+  const Operand &A = g.A, &B = g.B;
+  const int I = g.I, J = g.J, nk = g.nk();
+  const long long K = g.K;
+  const TileChoice tc = choose_tiles(I, J, nk, B.mn, aligned_rows(g.e), num_sms);
+  if (tc.bn < 0) return gemm_pair(g, bf16, num_sms, s);
   GemmArgs a;
-  a.e = e;
+  a.e = g.e;
   a.I = I;
   a.J = J;
   a.nk = nk;
@@ -1137,6 +1423,26 @@ int gemm(const Operand& A, const Operand& B, int I, int J, long long K, bool bf1
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+// The two products of a backward pass: in one launch of the pair kernel where that is
+// estimated to take less than one after the other.
+int gemm_both(const Product& x, const Product& y, bool bf16, int num_sms, cudaStream_t s) {
+  const Product& first = x.nk() >= y.nk() ? x : y;
+  const Product& second = x.nk() >= y.nk() ? y : x;
+  const int pairs = pair_clusters(num_sms);
+  PairArgs a;
+  const long long most = first.tiles256() + second.tiles256() >= pairs ? share_tiles(first, second, pairs, a.live) : 0;
+  const double apart = choose_tiles(x.I, x.J, x.nk(), x.B.mn, aligned_rows(x.e), num_sms).us +
+                       choose_tiles(y.I, y.J, y.nk(), y.B.mn, aligned_rows(y.e), num_sms).us;
+  if (most > 0 && kPairStart + (double)most * kPairStep < apart) {
+    a.products = 2;
+    a.bf16 = bf16;
+    if (!pair_product(first, bf16, &a.p[0]) || !pair_product(second, bf16, &a.p[1])) return MOE_ERR_CUDA;
+    return launch_pairs(a, pairs, s);
+  }
+  const int rc = gemm(x, bf16, num_sms, s);
+  return rc != MOE_OK ? rc : gemm(y, bf16, num_sms, s);
 }
 
 // Bytes on which every row of a matrix starts: 32, 16 or 0 (any).
@@ -1170,8 +1476,11 @@ constexpr int kBiasParts = 256;  // row ranges of the column sums at most
 size_t dz_bytes(long long M, long long N) { return ((size_t)M * ((N + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
 
 template <int ACT>
-void launch_act_grad(const ActGradArgs& a, dim3 grid, cudaStream_t s) {
-  act_grad_kernel<ACT><<<grid, 256, 0, s>>>(a);
+void launch_act_grad(const ActGradArgs& a, bool vec, dim3 grid, cudaStream_t s) {
+  if (vec)
+    act_grad_kernel<ACT, true><<<grid, 256, 0, s>>>(a);
+  else
+    act_grad_kernel<ACT, false><<<grid, 256, 0, s>>>(a);
 }
 
 }  // namespace
@@ -1242,8 +1551,8 @@ int moe_linear(const moe_linear_args* p, moe_stream_t stream) {
   e.vr = row_bytes(p->r, p->ld_r, p->dtype, p->M);
   e.vb = aligned_to(p->b, 16);
   if (p->M <= kRowsMax) return gemm_rows(p, e, sms, reinterpret_cast<cudaStream_t>(stream));
-  return gemm({p->x, p->ld_x, false}, {p->w, p->ld_w, false}, (int)p->M, (int)p->N, p->K,
-              p->dtype == MOE_BF16, e, sms, reinterpret_cast<cudaStream_t>(stream));
+  return gemm(Product{{p->x, p->ld_x, false}, {p->w, p->ld_w, false}, (int)p->M, (int)p->N, p->K, e},
+              p->dtype == MOE_BF16, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moe_linear_workspace(long long M, long long N) {
@@ -1306,42 +1615,43 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
     g.M = M;
     g.N = N;
     g.dtype = p->dtype;
-    g.vdy = row_bytes(p->dy, p->ld_dy, p->dtype, M) != 0;
-    g.vz = row_bytes(p->z, p->ld_z, p->dtype, M) != 0;
+    const bool vec = N % 8 == 0 && row_bytes(p->dy, p->ld_dy, p->dtype, M) != 0 &&
+                     (!act || row_bytes(p->z, p->ld_z, p->dtype, M) != 0);
     const int bx = (N + 255) / 256;
-    const int want = std::max(1, std::min(kBiasParts, 8 * sms / bx));
-    g.rows = std::max(8, (M + want - 1) / want);
+    const int want = std::max(1, std::min(kBiasParts, 8 * sms / bx));  // ranges: eight CTAs an SM
+    g.rows = ((M + want - 1) / want + 8 * kActRows - 1) / (8 * kActRows) * (8 * kActRows);
     const int by = (M + g.rows - 1) / g.rows;
     const dim3 grid((unsigned)bx, (unsigned)by);
     switch (p->act) {
-      case MOE_ACT_RELU: launch_act_grad<MOE_ACT_RELU>(g, grid, s); break;
-      case MOE_ACT_GELU: launch_act_grad<MOE_ACT_GELU>(g, grid, s); break;
-      case MOE_ACT_GELU_TANH: launch_act_grad<MOE_ACT_GELU_TANH>(g, grid, s); break;
-      case MOE_ACT_SILU: launch_act_grad<MOE_ACT_SILU>(g, grid, s); break;
-      default: launch_act_grad<MOE_ACT_NONE>(g, grid, s); break;
+      case MOE_ACT_RELU: launch_act_grad<MOE_ACT_RELU>(g, vec, grid, s); break;
+      case MOE_ACT_GELU: launch_act_grad<MOE_ACT_GELU>(g, vec, grid, s); break;
+      case MOE_ACT_GELU_TANH: launch_act_grad<MOE_ACT_GELU_TANH>(g, vec, grid, s); break;
+      case MOE_ACT_SILU: launch_act_grad<MOE_ACT_SILU>(g, vec, grid, s); break;
+      default: launch_act_grad<MOE_ACT_NONE>(g, vec, grid, s); break;
     }
-    if (p->db != nullptr) bias_grad_kernel<<<(N + 31) / 32, 256, 0, s>>>(g.part, by, N, p->btype, p->db);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (p->db != nullptr && launch_behind(bias_grad_kernel, dim3((N + 31) / 32), dim3(32 * kBiasWarps), 0, s,
+                                          (const float*)g.part, by, N, p->btype, p->db) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   Epilogue e{};
   e.dtype = p->dtype;
   e.btype = p->dtype;
-  if (p->dx != nullptr) {
-    e.y = p->dx;
-    e.ld_y = p->ld_dx;
-    e.ytype = p->dtype;
-    e.vy = row_bytes(p->dx, p->ld_dx, p->dtype, M);
-    rc = gemm({dz, ld_dz, false}, {p->w, p->ld_w, true}, M, (int)p->K, N, bf16, e, sms, s);
-    if (rc != MOE_OK) return rc;
-  }
-  if (p->dw != nullptr) {
-    e.y = p->dw;
-    e.ld_y = p->ld_dw;
-    e.ytype = p->dwtype;
-    e.vy = row_bytes(p->dw, p->ld_dw, p->dwtype, N);
-    rc = gemm({dz, ld_dz, true}, {p->x, p->ld_x, true}, N, (int)p->K, M, bf16, e, sms, s);
-  }
-  return rc;
+  e.vb = true;
+  Product to_x{{dz, ld_dz, false}, {p->w, p->ld_w, true}, M, (int)p->K, N, e};
+  to_x.e.y = p->dx;
+  to_x.e.ld_y = p->ld_dx;
+  to_x.e.ytype = p->dtype;
+  to_x.e.vy = row_bytes(p->dx, p->ld_dx, p->dtype, M);
+  Product to_w{{dz, ld_dz, true}, {p->x, p->ld_x, true}, N, (int)p->K, M, e};
+  to_w.e.y = p->dw;
+  to_w.e.ld_y = p->ld_dw;
+  to_w.e.ytype = p->dwtype;
+  to_w.e.vy = row_bytes(p->dw, p->ld_dw, p->dwtype, N);
+  if (p->dx != nullptr && p->dw != nullptr) return gemm_both(to_x, to_w, bf16, sms, s);
+  if (p->dx != nullptr) return gemm(to_x, bf16, sms, s);
+  if (p->dw != nullptr) return gemm(to_w, bf16, sms, s);
+  return MOE_OK;
 }
 
 int moe_ops_status(moe_stream_t stream, int* code, int* detail) {

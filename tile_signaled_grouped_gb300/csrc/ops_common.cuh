@@ -42,7 +42,7 @@ cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>* ready);
 // allowed it (allow_dependent_launch) or left; it calls wait_prior_grid() before it reads or
 // writes anything that kernel touches. After a kernel that allows nothing: an ordinary launch.
 template <typename K, typename... A>
-cudaError_t launch_behind(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_behind(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
