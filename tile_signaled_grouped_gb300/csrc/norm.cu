@@ -46,8 +46,6 @@ struct NormArgs {
   float eps;
   int stages;        // ring kernels: rows of shared memory
   uint32_t* status;  // ring kernels: where a wait that ran out is recorded
-  bool vx, vr, vdy, vy, vz;  // rows start on 16 bytes
-  bool vw;                   // w and b start on 16 bytes
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -56,55 +54,85 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Elements [v N, v N + N) of a row of D as fp32; 0 past the row. N is a 16-byte vector of
-// elements, or 1 for rows that do not start on 16 bytes (then neighbouring threads take
-// neighbouring elements: vectors taken apart would touch eight times the lines an access).
+// What a thread reads at once: N elements, a 16-byte vector of them (the rows start on 16
+// bytes and D is a multiple of N) or one (neighbouring threads then take neighbouring
+// elements: vectors taken apart would touch eight times the lines an access).
 template <typename T, int N>
-__device__ __forceinline__ void load_vec(const T* row, int v, int D, bool vec, float (&f)[N]) {
-  const int c = v * N;
-  if (N > 1 && vec && c + N <= D) {
-    if constexpr (N > 1) unpack<T>(__ldg(reinterpret_cast<const uint4*>(row) + v), f);
-  } else {
+struct Word {
+  using type = uint4;
+};
+template <typename T>
+struct Word<T, 1> {
+  using type = T;
+};
+__device__ __forceinline__ uint4 load_word(const uint4* p) { return __ldg(p); }
+__device__ __forceinline__ float load_word(const float* p) { return __ldg(p); }
+__device__ __forceinline__ __nv_bfloat16 load_word(const __nv_bfloat16* p) {
+  return __ushort_as_bfloat16(__ldg(reinterpret_cast<const unsigned short*>(p)));
+}
+__device__ __forceinline__ __half load_word(const __half* p) {
+  return __ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(p)));
+}
+
+// Words first, first + step, ... of a row of nv words, as fp32; zeros past it, and everywhere
+// unless `live`. All loads leave before the first is used: none stands behind a condition
+// (a word past the row is its last one, and is dropped afterwards).
+template <typename T, int N, int PERV>
+__device__ __forceinline__ void load_row(const T* row, int first, int step, int nv, bool live,
+                                         float (&f)[PERV][N]) {
+  using W = typename Word<T, N>::type;
+  W u[PERV];
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = c + i < D ? to_f32(row[c + i]) : 0.f;
+  for (int i = 0; i < PERV; ++i) u[i] = load_word(reinterpret_cast<const W*>(row) + min(first + i * step, nv - 1));
+#pragma unroll
+  for (int i = 0; i < PERV; ++i) {
+    const bool in = live && first + i * step < nv;
+    if constexpr (N == 1) {
+      f[i][0] = to_f32(u[i]);
+    } else {
+      unpack<T>(u[i], f[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[i][e] = in ? f[i][e] : 0.f;
   }
 }
 template <typename T, int N>
-__device__ __forceinline__ void store_vec(T* row, int v, int D, bool vec, const float (&f)[N]) {
-  const int c = v * N;
-  if (N > 1 && vec && c + N <= D) {
-    if constexpr (N > 1) reinterpret_cast<uint4*>(row)[v] = pack<T>(f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (c + i < D) row[c + i] = from_f32<T>(f[i]);
-  }
+__device__ __forceinline__ void store_word(T* row, int v, const float (&f)[N]) {
+  if constexpr (N == 1)
+    row[v] = from_f32<T>(f[0]);
+  else
+    reinterpret_cast<uint4*>(row)[v] = pack<T>(f);
 }
-// The same elements of w or b, of the rows' type or fp32; `none` where there is no array.
-template <typename T, int N>
-__device__ __forceinline__ void load_param(const void* p, int wtype, int v, int D, bool vec, float none,
-                                           float (&f)[N]) {
+// The same words of w or b, of the rows' type or fp32; `none` where there is no array. The
+// type is asked once, and the loads come before a row's stores, which no later load may pass.
+template <typename T, int N, int PERV>
+__device__ __forceinline__ void load_params(const void* p, int wtype, int first, int step, int nv, float none,
+                                            float (&f)[PERV][N]) {
   if (p == nullptr) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = none;
+    for (int i = 0; i < PERV; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[i][e] = none;
   } else if (sizeof(T) == 2 && wtype == MOE_FP32) {
     const float* q = static_cast<const float*>(p);
-    const int c = v * N;
-    if (N > 1 && vec && c + N <= D) {
 #pragma unroll
-      for (int h = 0; h < N / 4; ++h) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(q + c) + h);
-        f[4 * h] = u.x;
-        f[4 * h + 1] = u.y;
-        f[4 * h + 2] = u.z;
-        f[4 * h + 3] = u.w;
+    for (int i = 0; i < PERV; ++i) {
+      const int v = min(first + i * step, nv - 1);
+      if constexpr (N == 1) {
+        f[i][0] = __ldg(q + v);
+      } else {
+#pragma unroll
+        for (int h = 0; h < N / 4; ++h) {
+          const float4 u = __ldg(reinterpret_cast<const float4*>(q) + v * (N / 4) + h);
+          f[i][4 * h] = u.x;
+          f[i][4 * h + 1] = u.y;
+          f[i][4 * h + 2] = u.z;
+          f[i][4 * h + 3] = u.w;
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = c + i < D ? q[c + i] : 0.f;
     }
   } else {
-    load_vec<T, N>(static_cast<const T*>(p), v, D, vec, f);
+    load_row<T, N, PERV>(static_cast<const T*>(p), first, step, nv, true, f);
   }
 }
 
@@ -133,7 +161,7 @@ __device__ __forceinline__ void row_sum(float (&s)[NV], float* red, int wpr, int
 // Warps of a CTA at most, by the elements a thread holds: what their registers allow.
 constexpr int max_warps(int ept) { return ept == 8 ? 32 : 16; }
 
-// wpr warps take a row, each thread EPT elements of it in 16-byte vectors.
+// wpr warps take a row, each thread EPT elements of it.
 template <typename T, int EPT, int N>
 __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_kernel(const __grid_constant__ NormArgs a) {
   constexpr int PERV = EPT / N;
@@ -143,37 +171,33 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_kernel(const __grid_
   const long long row = (long long)blockIdx.x * rows + grp;
   const bool live = row < a.n;
   const long long rr = live ? row : 0;
-  const T* x = static_cast<const T*>(a.x) + rr * a.ld_x;
-  const T* r = a.r != nullptr ? static_cast<const T*>(a.r) + rr * a.ld_r : nullptr;
-  const int t = wr * 32 + lane, step = a.wpr * 32;
+  const int t = wr * 32 + lane, step = a.wpr * 32, nv = a.D / N;
 
   float f[PERV][N];
   float s[1] = {0.f};
+  load_row<T, N, PERV>(static_cast<const T*>(a.x) + rr * a.ld_x, t, step, nv, live, f);
+  if (a.r != nullptr) {
+    float g[PERV][N];
+    load_row<T, N, PERV>(static_cast<const T*>(a.r) + rr * a.ld_r, t, step, nv, live, g);
 #pragma unroll
-  for (int i = 0; i < PERV; ++i) {
-    const int v = t + i * step;
-    load_vec<T, N>(x, v, live ? a.D : 0, a.vx, f[i]);
-    if (r != nullptr) {
-      float g[N];
-      load_vec<T, N>(r, v, live ? a.D : 0, a.vr, g);
+    for (int i = 0; i < PERV; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[i][e] += g[e];
-    }
+      for (int e = 0; e < N; ++e) f[i][e] += g[i][e];
+  }
+#pragma unroll
+  for (int i = 0; i < PERV; ++i)
 #pragma unroll
     for (int e = 0; e < N; ++e) s[0] += f[i][e];
-  }
   row_sum<1>(s, red[0][grp], a.wpr, wr, grp);
   const float mean = s[0] / (float)a.D;
   float q[1] = {0.f};
 #pragma unroll
-  for (int i = 0; i < PERV; ++i) {
-    const int c = (t + i * step) * N;
+  for (int i = 0; i < PERV; ++i)
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const float d = c + e < a.D ? f[i][e] - mean : 0.f;
+      const float d = t + i * step < nv ? f[i][e] - mean : 0.f;
       q[0] = fmaf(d, d, q[0]);
     }
-  }
   row_sum<1>(q, red[1][grp], a.wpr, wr, grp);
   if (!live) return;
   const float rstd = 1.0f / sqrtf(q[0] / (float)a.D + a.eps);
@@ -183,55 +207,68 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_kernel(const __grid_
   }
   T* y = static_cast<T*>(a.y) + row * a.ld_y;
   T* z = a.z != nullptr ? static_cast<T*>(a.z) + row * a.ld_z : nullptr;
+  constexpr int B = EPT > 16 ? 16 / N : PERV;  // words whose parameters are held at once
 #pragma unroll
-  for (int i = 0; i < PERV; ++i) {
-    const int v = t + i * step;
-    if (v * N >= a.D) break;
-    if (z != nullptr) store_vec<T, N>(z, v, a.D, a.vz, f[i]);
-    float w[N], b[N];
-    load_param<T, N>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
-    load_param<T, N>(a.b, a.wtype, v, a.D, a.vw, 0.f, b);
+  for (int i0 = 0; i0 < PERV; i0 += B) {
+    float w[B][N], b[B][N];
+    load_params<T, N, B>(a.w, a.wtype, t + i0 * step, step, nv, 1.f, w);
+    load_params<T, N, B>(a.b, a.wtype, t + i0 * step, step, nv, 0.f, b);
 #pragma unroll
-    for (int e = 0; e < N; ++e) f[i][e] = fmaf((f[i][e] - mean) * rstd, w[e], b[e]);
-    store_vec<T, N>(y, v, a.D, a.vy, f[i]);
+    for (int i = 0; i < B; ++i) {
+      const int v = t + (i0 + i) * step;
+      if (v < nv) {
+        if (z != nullptr) store_word<T, N>(z, v, f[i0 + i]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[i0 + i][e] = fmaf((f[i0 + i][e] - mean) * rstd, w[i][e], b[i][e]);
+        store_word<T, N>(y, v, f[i0 + i]);
+      }
+    }
   }
 }
+
+constexpr int kLoopWords = 4;  // words of a thread in flight in the long-row kernels
 
 // Rows of any length: one CTA a row, read three times.
 template <typename T, int N>
 __global__ void __launch_bounds__(kLoopThreads) norm_long_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int P = kLoopWords;
   __shared__ float red[2][32];
-  const int wr = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int wr = threadIdx.x >> 5, nw = blockDim.x >> 5, step = blockDim.x, nv = a.D / N;
   const long long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
   const T* r = a.r != nullptr ? static_cast<const T*>(a.r) + row * a.ld_r : nullptr;
-  auto load = [&](int v, float (&f)[N]) {
-    load_vec<T, N>(x, v, a.D, a.vx, f);
+  auto load = [&](int v, float (&f)[P][N]) {
+    load_row<T, N, P>(x, v, step, nv, true, f);
     if (r != nullptr) {
-      float g[N];
-      load_vec<T, N>(r, v, a.D, a.vr, g);
+      float g[P][N];
+      load_row<T, N, P>(r, v, step, nv, true, g);
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] += g[e];
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[i][e] += g[i][e];
     }
   };
   float s[1] = {0.f}, q[1] = {0.f};
-  const int nv = (a.D + N - 1) / N;
-  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-    float f[N];
+  for (int v = threadIdx.x; v < nv; v += P * step) {
+    float f[P][N];
     load(v, f);
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[0] += f[e];
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[0] += f[i][e];
   }
   row_sum<1>(s, red[0], nw, wr, 0);
   const float mean = s[0] / (float)a.D;
-  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-    float f[N];
+  for (int v = threadIdx.x; v < nv; v += P * step) {
+    float f[P][N];
     load(v, f);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float d = v * N + e < a.D ? f[e] - mean : 0.f;
-      q[0] = fmaf(d, d, q[0]);
-    }
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float d = v + i * step < nv ? f[i][e] - mean : 0.f;
+        q[0] = fmaf(d, d, q[0]);
+      }
   }
   row_sum<1>(q, red[1], nw, wr, 0);
   const float rstd = 1.0f / sqrtf(q[0] / (float)a.D + a.eps);
@@ -241,15 +278,19 @@ __global__ void __launch_bounds__(kLoopThreads) norm_long_kernel(const __grid_co
   }
   T* y = static_cast<T*>(a.y) + row * a.ld_y;
   T* z = a.z != nullptr ? static_cast<T*>(a.z) + row * a.ld_z : nullptr;
-  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-    float f[N], w[N], b[N];
+  for (int v = threadIdx.x; v < nv; v += P * step) {
+    float f[P][N], w[P][N], b[P][N];
     load(v, f);
-    if (z != nullptr) store_vec<T, N>(z, v, a.D, a.vz, f);
-    load_param<T, N>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
-    load_param<T, N>(a.b, a.wtype, v, a.D, a.vw, 0.f, b);
+    load_params<T, N, P>(a.w, a.wtype, v, step, nv, 1.f, w);
+    load_params<T, N, P>(a.b, a.wtype, v, step, nv, 0.f, b);
 #pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[e], b[e]);
-    store_vec<T, N>(y, v, a.D, a.vy, f);
+    for (int i = 0; i < P; ++i) {
+      if (v + i * step >= nv) break;
+      if (z != nullptr) store_word<T, N>(z, v + i * step, f[i]);
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[i][e] = fmaf((f[i][e] - mean) * rstd, w[i][e], b[i][e]);
+      store_word<T, N>(y, v + i * step, f[i]);
+    }
   }
 }
 
@@ -263,7 +304,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
   __shared__ float red[2][32][64];   // [row parity][row group][sum, warp]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp / a.wpr, wr = warp % a.wpr, rows = (blockDim.x >> 5) / a.wpr;
-  const int t = wr * 32 + lane, step = a.wpr * 32;
+  const int t = wr * 32 + lane, step = a.wpr * 32, nv = a.D / N;
   const float inv_d = 1.0f / (float)a.D;
 
   float dw[PERV][N], db[PERV][N];
@@ -277,29 +318,28 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
     const long long row = row0 + grp;
     const bool live = row < a.n;
     const long long rr = live ? row : 0;
-    const int D = live ? a.D : 0;
-    const T* z = static_cast<const T*>(a.x) + rr * a.ld_x;
-    const T* dy = static_cast<const T*>(a.dy) + rr * a.ld_dy;
     const float mean = live ? __ldg(a.mean + row) : 0.f, rstd = live ? __ldg(a.rstd + row) : 0.f;
-    float xh[PERV][N], g[PERV][N];
+    float xh[PERV][N], g[PERV][N], o[PERV][N], w[PERV][N];
     float s[2] = {0.f, 0.f};
+    load_row<T, N, PERV>(static_cast<const T*>(a.x) + rr * a.ld_x, t, step, nv, live, xh);
+    load_row<T, N, PERV>(static_cast<const T*>(a.dy) + rr * a.ld_dy, t, step, nv, live, g);
+    if (a.r != nullptr) {
+      load_row<T, N, PERV>(static_cast<const T*>(a.r) + rr * a.ld_r, t, step, nv, live, o);
+    } else {
 #pragma unroll
-    for (int i = 0; i < PERV; ++i) {
-      const int v = t + i * step;
-      load_vec<T, N>(z, v, D, a.vx, xh[i]);
-      load_vec<T, N>(dy, v, D, a.vdy, g[i]);
+      for (int i = 0; i < PERV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[i][e] = 0.f;
     }
+    load_params<T, N, PERV>(a.w, a.wtype, t, step, nv, 1.f, w);
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
-      const int v = t + i * step;
-      float w[N];
-      load_param<T, N>(a.w, a.wtype, v, D, a.vw, 1.f, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        xh[i][e] = v * N + e < D ? (xh[i][e] - mean) * rstd : 0.f;
+        xh[i][e] = t + i * step < nv ? (xh[i][e] - mean) * rstd : 0.f;
         dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
         db[i][e] += g[i][e];
-        g[i][e] *= w[e];
+        g[i][e] *= w[i][e];
         s[0] += g[i][e];
         s[1] = fmaf(g[i][e], xh[i][e], s[1]);
       }
@@ -308,19 +348,14 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
     parity ^= 1;  // the next row's sums do not overwrite what a slow warp still reads
     if (!live) continue;
     const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
-    const T* dz = a.r != nullptr ? static_cast<const T*>(a.r) + row * a.ld_r : nullptr;
     T* dx = static_cast<T*>(a.y) + row * a.ld_y;
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
-      if (v * N >= D) break;
-      float o[N];
+      if (v >= nv) break;
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = 0.f;
-      if (dz != nullptr) load_vec<T, N>(dz, v, D, a.vr, o);
-#pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = fmaf(rstd, g[i][e] - m1 - xh[i][e] * m2, o[e]);
-      store_vec<T, N>(dx, v, D, a.vy, o);
+      for (int e = 0; e < N; ++e) o[i][e] = fmaf(rstd, g[i][e] - m1 - xh[i][e] * m2, o[i][e]);
+      store_word<T, N>(dx, v, o[i]);
     }
   }
 
@@ -353,10 +388,10 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
   for (int i = 0; i < PERV; ++i)
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const int c = (t + i * step) * N + e;
-      if (c < a.D) {
-        pw[c] = dw[i][e];
-        pw[a.D + c] = db[i][e];
+      const int v = t + i * step;
+      if (v < nv) {
+        pw[v * N + e] = dw[i][e];
+        pw[a.D + v * N + e] = db[i][e];
       }
     }
 }
@@ -365,57 +400,78 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
 // workspace (no other thread touches them).
 template <typename T, int N>
 __global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int P = N > 1 ? 1 : kLoopWords;
   __shared__ float red[2][64];
   allow_dependent_launch();
-  const int wr = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int nv = (a.D + N - 1) / N;
+  const int wr = threadIdx.x >> 5, nw = blockDim.x >> 5, step = blockDim.x, nv = a.D / N;
   const float inv_d = 1.0f / (float)a.D;
   float* pw = a.part + (size_t)blockIdx.x * 2 * a.D;
   float* pb = pw + a.D;
-  for (int v = threadIdx.x; v < nv; v += blockDim.x)
-    for (int e = 0; e < N; ++e)
-      if (v * N + e < a.D) pw[v * N + e] = pb[v * N + e] = 0.f;
+  for (int v = threadIdx.x; v < nv; v += step)
+#pragma unroll
+    for (int e = 0; e < N; ++e) pw[v * N + e] = pb[v * N + e] = 0.f;
   int parity = 0;
   for (long long row = blockIdx.x; row < a.n; row += gridDim.x) {
     const T* z = static_cast<const T*>(a.x) + row * a.ld_x;
     const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy;
     const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
-    auto load = [&](int v, float (&xh)[N], float (&d)[N], float (&w)[N]) {
-      load_vec<T, N>(z, v, a.D, a.vx, xh);
-      load_vec<T, N>(dy, v, a.D, a.vdy, d);
-      load_param<T, N>(a.w, a.wtype, v, a.D, a.vw, 1.f, w);
+    auto load = [&](int v, float (&xh)[P][N], float (&d)[P][N], float (&w)[P][N]) {
+      load_row<T, N, P>(z, v, step, nv, true, xh);
+      load_row<T, N, P>(dy, v, step, nv, true, d);
+      load_params<T, N, P>(a.w, a.wtype, v, step, nv, 1.f, w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) xh[e] = v * N + e < a.D ? (xh[e] - mean) * rstd : 0.f;
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) xh[i][e] = v + i * step < nv ? (xh[i][e] - mean) * rstd : 0.f;
     };
     float s[2] = {0.f, 0.f};
-    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-      float xh[N], d[N], w[N];
+    for (int v = threadIdx.x; v < nv; v += P * step) {
+      float xh[P][N], d[P][N], w[P][N], sw[P][N], sb[P][N];
       load(v, xh, d, w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float g = d[e] * w[e];
-        s[0] += g;
-        s[1] = fmaf(g, xh[e], s[1]);
-        if (v * N + e < a.D) {
-          pw[v * N + e] = fmaf(d[e], xh[e], pw[v * N + e]);
-          pb[v * N + e] += d[e];
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int c = min(v + i * step, nv - 1) * N + e;
+          sw[i][e] = pw[c];
+          sb[i][e] = pb[c];
         }
-      }
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float g = d[i][e] * w[i][e];
+          s[0] += g;
+          s[1] = fmaf(g, xh[i][e], s[1]);
+          if (v + i * step < nv) {
+            pw[(v + i * step) * N + e] = fmaf(d[i][e], xh[i][e], sw[i][e]);
+            pb[(v + i * step) * N + e] = sb[i][e] + d[i][e];
+          }
+        }
     }
     row_sum<2>(s, red[parity], nw, wr, 0);
     parity ^= 1;
     const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
     const T* dz = a.r != nullptr ? static_cast<const T*>(a.r) + row * a.ld_r : nullptr;
     T* dx = static_cast<T*>(a.y) + row * a.ld_y;
-    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-      float xh[N], d[N], w[N], o[N];
+    for (int v = threadIdx.x; v < nv; v += P * step) {
+      float xh[P][N], d[P][N], w[P][N], o[P][N];
       load(v, xh, d, w);
+      if (dz != nullptr) {
+        load_row<T, N, P>(dz, v, step, nv, true, o);
+      } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = 0.f;
-      if (dz != nullptr) load_vec<T, N>(dz, v, a.D, a.vr, o);
+        for (int i = 0; i < P; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = fmaf(rstd, d[e] * w[e] - m1 - xh[e] * m2, o[e]);
-      store_vec<T, N>(dx, v, a.D, a.vy, o);
+          for (int e = 0; e < N; ++e) o[i][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (v + i * step >= nv) break;
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[i][e] = fmaf(rstd, d[i][e] * w[i][e] - m1 - xh[i][e] * m2, o[i][e]);
+        store_word<T, N>(dx, v + i * step, o[i]);
+      }
     }
   }
 }
@@ -548,17 +604,9 @@ __device__ __forceinline__ uint4 pack_pairs(const F2 (&f)[Vec<T>::kN / 2]) {
   }
   return pack<T>(g);
 }
-// A vector of a row that the ring kernels write: 16 bytes where the rows allow it.
 template <typename T>
-__device__ __forceinline__ void store_pairs(T* row, int v, bool vec, const F2 (&f)[Vec<T>::kN / 2]) {
-  const uint4 u = pack_pairs<T>(f);
-  if (vec) {
-    reinterpret_cast<uint4*>(row)[v] = u;
-  } else {
-    const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int i = 0; i < Vec<T>::kN; ++i) row[v * Vec<T>::kN + i] = e[i];
-  }
+__device__ __forceinline__ void store_pairs(T* row, int v, const F2 (&f)[Vec<T>::kN / 2]) {
+  reinterpret_cast<uint4*>(row)[v] = pack_pairs<T>(f);
 }
 
 // The parameters of a thread's columns, kept in registers as they lie in memory: WT is the
@@ -665,7 +713,7 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
       if (v < nv) {
-        if (z != nullptr) store_pairs<T>(z, v, a.vz, f[i]);
+        if (z != nullptr) store_pairs<T>(z, v, f[i]);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
           f[i][e] = f[i][e] + minus_mean;
@@ -696,7 +744,7 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
           x = fma2(x * rr, wf[e], bf[e]);
         }
       }
-      store_pairs<T>(y, v, a.vy, f[i]);
+      store_pairs<T>(y, v, f[i]);
     }
   }
   ring_end(g, t == 0, it);
@@ -790,7 +838,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
       }
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) o[e] = fma2(rr, fma2(xh[i][e], m2, d[i][e] + m1), o[e]);
-      store_pairs<T>(dx, v, a.vy, o);
+      store_pairs<T>(dx, v, o);
     }
   }
   ring_end(g, t == 0, it);
@@ -875,9 +923,9 @@ bool check_rows(const void* q, long long ld, const moe_norm_args* p, bool need) 
   return ld >= p->D && ld <= INT32_MAX && aligned_to(q, (size_t)type_bytes(p->dtype));
 }
 bool check_vec(const void* q, int dtype) { return aligned_to(q, (size_t)type_bytes(dtype)); }
-// Whether every row of a matrix starts on 16 bytes.
+// Whether every row of a matrix (if there is one) starts on 16 bytes.
 bool rows16(const void* q, long long ld, const moe_norm_args* p) {
-  return aligned_to(q, 16) && (p->n == 1 || ld * type_bytes(p->dtype) % 16 == 0);
+  return q == nullptr || aligned_to(q, 16) && (p->n == 1 || ld * type_bytes(p->dtype) % 16 == 0);
 }
 
 // Warps of a row and of a CTA: a row lies in the registers of wpr warps, EPT elements a
@@ -894,9 +942,9 @@ NormShape norm_shape(const moe_norm_args* p, bool vec, int num_sms, bool backwar
   if (few)
     s.ept = 8;
   else if (backward)
-    s.ept = p->D <= (vec ? 256 : 2048) ? 8 : 16;
+    s.ept = p->D <= 256 || (!vec && wpr(8) <= max_warps(8)) ? 8 : 16;
   else if (!vec)
-    s.ept = p->D <= 2048 ? 8 : p->D <= 8192 ? 16 : 32;
+    s.ept = wpr(8) <= 16 ? 8 : wpr(16) <= 16 ? 16 : 32;
   else
     s.ept = p->D <= 256 ? 8 : p->D <= 512 || (p->D > 1024 && p->D <= 4096) ? 16 : 32;
   if (wpr(s.ept) > max_warps(s.ept)) s.ept = backward ? 16 : 32;
@@ -920,7 +968,7 @@ RingShape ring_shape(const moe_norm_args* p, bool aligned, int mats, int num_sms
   const size_t row = (size_t)p->D * type_bytes(p->dtype);
   r.ept = backward ? kBackwardEpt : p->D <= 512 ? 16 : kForwardEpt;
   r.wpr = (p->D + 32 * r.ept - 1) / (32 * r.ept);
-  if (!aligned || row % 16 != 0 || r.wpr > 16) return r;
+  if (!aligned || r.wpr > 16) return r;
   r.groups = std::max(1, (backward ? 8 : 16) / r.wpr);
   r.ctas = backward ? std::max(1, 16 / (r.wpr * r.groups)) : 1;
   const size_t params = backward ? 0 : 2 * (size_t)p->D * type_bytes(p->wtype);
@@ -1052,16 +1100,13 @@ int moe_layer_norm(const moe_norm_args* p, moe_stream_t stream) {
   a.D = p->D;
   a.wtype = p->wtype;
   a.eps = p->eps;
-  a.vx = rows16(p->x, p->ld_x, p);
-  a.vr = rows16(p->r, p->ld_r, p);
-  a.vy = rows16(p->y, p->ld_y, p);
-  a.vz = rows16(p->z, p->ld_z, p);
-  a.vw = aligned_to(p->w, 16) && aligned_to(p->b, 16);
+  const bool vec = (size_t)p->D * type_bytes(p->dtype) % 16 == 0 && rows16(p->x, p->ld_x, p) &&
+                   rows16(p->r, p->ld_r, p) && rows16(p->y, p->ld_y, p) && rows16(p->z, p->ld_z, p) &&
+                   aligned_to(p->w, 16) && aligned_to(p->b, 16);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int mats = p->r != nullptr ? 2 : 1;
-  const RingShape ring = ring_shape(p, a.vx && a.vw && (p->r == nullptr || a.vr), mats, sms, false);
+  const RingShape ring = ring_shape(p, vec, mats, sms, false);
   if (ring.ctas > 0) return run_ring(false, p->dtype, a, ring, ring.ctas * sms, s);
-  const bool vec = a.vx && a.vy && (p->r == nullptr || a.vr) && (p->z == nullptr || a.vz);
   const NormShape sh = norm_shape(p, vec, sms, false);
   a.wpr = sh.wpr;
   return run_rows(false, p->dtype, vec, a, sh, 0, s);
@@ -1114,21 +1159,18 @@ int moe_layer_norm_backward(const moe_norm_args* p, void* workspace, size_t work
   a.ld_y = p->ld_dx;
   a.D = p->D;
   a.wtype = p->wtype;
-  a.vx = rows16(p->z, p->ld_z, p);
-  a.vr = rows16(p->dz, p->ld_dz, p);
-  a.vdy = rows16(p->dy, p->ld_dy, p);
-  a.vy = rows16(p->dx, p->ld_dx, p);
-  a.vw = aligned_to(p->w, 16);
+  const bool vec = (size_t)p->D * type_bytes(p->dtype) % 16 == 0 && rows16(p->z, p->ld_z, p) &&
+                   rows16(p->dz, p->ld_dz, p) && rows16(p->dy, p->ld_dy, p) && rows16(p->dx, p->ld_dx, p) &&
+                   aligned_to(p->w, 16);
   const int mats = p->dz != nullptr ? 3 : 2;
   const RingShape ring =
-      ring_shape(p, a.vx && a.vdy && a.vw && (p->dz == nullptr || a.vr), mats, sms, true);
+      ring_shape(p, vec, mats, sms, true);
   int grid;
   if (ring.ctas > 0) {
     grid = std::min(kNormParts, ring.ctas * sms);
     rc = run_ring(true, p->dtype, a, ring, grid, s);
     if (rc != MOE_OK) return rc;
   } else {
-    const bool vec = a.vx && a.vdy && a.vy && (p->dz == nullptr || a.vr);
     const NormShape sh = norm_shape(p, vec, sms, true);
     a.wpr = sh.wpr;
     const int rows = sh.ept == 0 ? 1 : sh.warps / sh.wpr;
