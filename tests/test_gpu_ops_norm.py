@@ -38,6 +38,14 @@ CASES = [
     (700, 7168, "bf16", "bf16", True, True, True, 16),
     (640, 8192, "fp32", "fp32", True, True, True, 0),
     (1500, 1032, "fp32", "fp32", False, False, True, 4),
+    # and rows that start anywhere
+    (1300, 4097, "bf16", "fp32", True, True, True, 0),
+    (1250, 1531, "fp16", "fp16", True, True, True, 5),
+    (700, 5003, "fp32", "fp32", True, True, False, 3),
+    (640, 8191, "bf16", "bf16", False, True, True, 1),
+    (4900, 37, "fp32", "fp32", True, False, True, 2),
+    (4900, 301, "bf16", "bf16", True, True, True, 0),
+    (2700, 1024, "fp16", "fp32", True, True, True, 5),
 ]
 
 

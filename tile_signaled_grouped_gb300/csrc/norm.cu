@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const 
 }
 
 // ------------------------------------------------------------------- ring kernels
-// Rows of 16-byte vectors from long matrices: persistent CTAs whose thread 0 keeps the next
+// Long matrices: persistent CTAs whose thread 0 keeps the next
 // rows coming in (bulk copies into a ring of shared memory), so that the loads never stop
 // for the reductions of a row: the kernels above only load between a CTA's start and its
 // first reduction (16384 x 4096 bf16 with a residual: 143 us against 95, 5.7 TB/s; backward
@@ -499,7 +499,9 @@ struct RingState {
 
 // A group's ring: a stage holds a row of x (forward) or of z and dy (backward), and of r
 // if there is one. What it can read from the launch's arguments it does not keep.
-template <typename T, bool BACK>
+// AL: rows start on 16 bytes and D is a multiple of a vector. Otherwise a stage holds the
+// 16-byte blocks that a row touches, and the row starts in it where it starts in the first.
+template <typename T, bool BACK, bool AL>
 struct Ring {
   const NormArgs& a;
   uint8_t* smem;
@@ -507,25 +509,76 @@ struct Ring {
   int first, stride;  // the group's rows: first, first + stride, ...
 
   __device__ __forceinline__ uint32_t bytes() const { return (uint32_t)a.D * sizeof(T); }
+  __device__ __forceinline__ uint32_t pitch() const { return AL ? bytes() : (bytes() + 15u) / 16u * 16u + 16u; }
   __device__ __forceinline__ int mats() const { return (BACK ? 2 : 1) + (a.r != nullptr ? 1 : 0); }
-  __device__ __forceinline__ const uint4* stage(int i) const {
-    return reinterpret_cast<const uint4*>(smem + (size_t)(i * mats()) * bytes());
+  // Matrix m's row in stage i.
+  __device__ __forceinline__ const uint4* stage(int i, int m) const {
+    return reinterpret_cast<const uint4*>(smem + (size_t)(i * mats() + m) * pitch());
+  }
+  // The blocks that a row of p touches, [*lo, *hi), without those that reach out of the matrix
+  // (its first and last row alone have such).
+  __device__ __forceinline__ void blocks(const T* p, long long ld, long long row, uintptr_t* lo,
+                                         uintptr_t* hi) const {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(p), at = begin + (uintptr_t)(row * ld) * sizeof(T);
+    const uintptr_t end = begin + (uintptr_t)((a.n - 1) * ld + a.D) * sizeof(T);
+    *lo = at & ~(uintptr_t)15;
+    *hi = (at + bytes() + 15) & ~(uintptr_t)15;
+    if (*lo < begin) *lo += 16;
+    if (*hi > end) *hi -= 16;
+  }
+  // Row `row` of p to `to`: the blocks by a bulk copy; what lies outside them by hand.
+  __device__ __forceinline__ void copy(uint8_t* to, const T* p, long long ld, long long row,
+                                       uint64_t* bar) const {
+    uintptr_t lo, hi;
+    blocks(p, ld, row, &lo, &hi);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) + (uintptr_t)(row * ld) * sizeof(T);
+    uint8_t* place = to + (lo - (at & ~(uintptr_t)15));
+    bulk_load(place, reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+  }
+  __device__ __forceinline__ void edges(uint8_t* to, const T* p, long long ld, long long row) const {
+    uintptr_t lo, hi;
+    blocks(p, ld, row, &lo, &hi);
+    const T* src = p + row * ld;
+    T* dst = reinterpret_cast<T*>(to + (reinterpret_cast<uintptr_t>(src) & 15));
+    for (int e = 0; e < a.D && reinterpret_cast<uintptr_t>(src + e) < lo; ++e) dst[e] = src[e];
+    for (int e = a.D - 1; e >= 0 && reinterpret_cast<uintptr_t>(src + e) >= hi; --e) dst[e] = src[e];
+  }
+  __device__ __forceinline__ uint32_t size(const T* p, long long ld, long long row) const {
+    uintptr_t lo, hi;
+    blocks(p, ld, row, &lo, &hi);
+    return (uint32_t)(hi - lo);
   }
   // The group's leader: stage i receives row `row`.
   __device__ __forceinline__ void load(int i, long long row) const {
     uint64_t* bar = &st->full[i];
-    uint8_t* to = smem + (size_t)(i * mats()) * bytes();
-    mbar_arrive_expect_tx(bar, bytes() * mats());
-    bulk_load(to, static_cast<const T*>(a.x) + row * a.ld_x, bytes(), bar);
-    if (BACK) bulk_load(to + bytes(), static_cast<const T*>(a.dy) + row * a.ld_dy, bytes(), bar);
-    if (a.r != nullptr)
-      bulk_load(to + (BACK ? 2 : 1) * bytes(), static_cast<const T*>(a.r) + row * a.ld_r, bytes(), bar);
+    uint8_t* to = smem + (size_t)(i * mats()) * pitch();
+    const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.dy), *r = static_cast<const T*>(a.r);
+    uint8_t *to_dy = to + pitch(), *to_r = to + (BACK ? 2 : 1) * pitch();
+    if constexpr (AL) {
+      mbar_arrive_expect_tx(bar, bytes() * mats());
+      bulk_load(to, x + row * a.ld_x, bytes(), bar);
+      if (BACK) bulk_load(to_dy, dy + row * a.ld_dy, bytes(), bar);
+      if (r != nullptr) bulk_load(to_r, r + row * a.ld_r, bytes(), bar);
+    } else {
+      if (row == 0 || row == a.n - 1) {
+        edges(to, x, a.ld_x, row);
+        if (BACK) edges(to_dy, dy, a.ld_dy, row);
+        if (r != nullptr) edges(to_r, r, a.ld_r, row);
+      }
+      // Orders what was written by hand into the stage, now or before, with the copies.
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive_expect_tx(bar, size(x, a.ld_x, row) + (BACK ? size(dy, a.ld_dy, row) : 0u) +
+                                     (r != nullptr ? size(r, a.ld_r, row) : 0u));
+      copy(to, x, a.ld_x, row, bar);
+      if (BACK) copy(to_dy, dy, a.ld_dy, row, bar);
+      if (r != nullptr) copy(to_r, r, a.ld_r, row, bar);
+    }
   }
 };
 
 // Every thread of the CTA, once `st` of its group is set; `leader`: the group's first thread.
-template <typename T, bool BACK>
-__device__ __forceinline__ void ring_begin(const Ring<T, BACK>& g, bool leader) {
+template <typename T, bool BACK, bool AL>
+__device__ __forceinline__ void ring_begin(const Ring<T, BACK, AL>& g, bool leader) {
   if (leader) {
     for (int i = 0; i < g.a.stages; ++i) mbar_init(&g.st->full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -541,13 +594,13 @@ __device__ __forceinline__ void ring_begin(const Ring<T, BACK>& g, bool leader) 
 // The stage's phase is complete: its row is there. After a wait that ran out the group carries on
 // with what is there (the status says that its results are void), so that every thread
 // meets the same barriers.
-template <typename T, bool BACK>
-__device__ __forceinline__ void ring_wait(const Ring<T, BACK>& g, int stage, int phase) {
+template <typename T, bool BACK, bool AL>
+__device__ __forceinline__ void ring_wait(const Ring<T, BACK, AL>& g, int stage, int phase) {
   mbar_wait_bounded(&g.st->full[stage], phase, &g.st->abort, kWaitNs, g.a.status, 0x51000000u);
 }
 // After an abort: the copies in flight of the group's `rows` rows land before it leaves.
-template <typename T, bool BACK>
-__device__ __forceinline__ void ring_end(const Ring<T, BACK>& g, bool leader, int rows) {
+template <typename T, bool BACK, bool AL>
+__device__ __forceinline__ void ring_end(const Ring<T, BACK, AL>& g, bool leader, int rows) {
   if (leader && *(volatile int*)&g.st->abort) {
     volatile int never = 0;
     for (int it = max(0, rows - g.a.stages); it < rows; ++it)
@@ -604,9 +657,80 @@ __device__ __forceinline__ uint4 pack_pairs(const F2 (&f)[Vec<T>::kN / 2]) {
   }
   return pack<T>(g);
 }
+// Sixteen bytes from byte `at` (below 16) of two neighbouring words.
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint32_t at) {
+  uint32_t w[5];
+  switch (at >> 2) {  // the same for the whole warp
+    case 0: w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x; break;
+    case 1: w[0] = lo.y, w[1] = lo.z, w[2] = lo.w, w[3] = hi.x, w[4] = hi.y; break;
+    case 2: w[0] = lo.z, w[1] = lo.w, w[2] = hi.x, w[3] = hi.y, w[4] = hi.z; break;
+    default: w[0] = lo.w, w[1] = hi.x, w[2] = hi.y, w[3] = hi.z, w[4] = hi.w; break;
+  }
+  const uint32_t bits = (at & 3u) * 8u;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+// Where a row of p starts in its first 16-byte block.
 template <typename T>
-__device__ __forceinline__ void store_pairs(T* row, int v, const F2 (&f)[Vec<T>::kN / 2]) {
-  reinterpret_cast<uint4*>(row)[v] = pack_pairs<T>(f);
+__device__ __forceinline__ uint32_t block_offset(const T* p, long long ld, long long row) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(p + row * ld) & 15);
+}
+// Vector v of a row in the ring that starts `at` bytes into its first block.
+template <bool AL>
+__device__ __forceinline__ uint4 ring_vec(const uint4* row, int v, uint32_t at) {
+  return AL ? row[v] : shifted(row[v], row[v + 1], at);
+}
+// Zeros past the row's D elements in its last vector.
+template <typename T, bool AL>
+__device__ __forceinline__ void trim(F2 (&f)[Vec<T>::kN / 2], int v, int D) {
+  constexpr int N = Vec<T>::kN;
+  if constexpr (!AL) {
+    if (v * N + N <= D) return;
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      const float2 p = f[e].get();
+      f[e] = F2(v * N + 2 * e < D ? p.x : 0.f, v * N + 2 * e + 1 < D ? p.y : 0.f);
+    }
+  }
+}
+// Vector v (v < nv) of each lane to a row of D elements; a warp's lanes hold neighbouring
+// vectors. Where the row does not start on 16 bytes, the part of its neighbour's vector that
+// belongs to a lane's 16-byte block comes to it by a shuffle, and only the ends of the warp's
+// run of vectors and of the row are stored by the element. Every lane of the warp calls it.
+template <typename T, bool AL>
+__device__ __forceinline__ void store_vecs(T* row, int v, int nv, int D, const uint4& u) {
+  constexpr int N = Vec<T>::kN;
+  if constexpr (AL) {
+    if (v < nv) reinterpret_cast<uint4*>(row)[v] = u;
+  } else {
+    const int lane = threadIdx.x & 31;
+    const uint32_t at = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
+    const int skip = (int)(at / sizeof(T));  // elements of a block that are the vector's before
+    uint4 p;
+    p.x = __shfl_up_sync(kAll, u.x, 1);
+    p.y = __shfl_up_sync(kAll, u.y, 1);
+    p.z = __shfl_up_sync(kAll, u.z, 1);
+    p.w = __shfl_up_sync(kAll, u.w, 1);
+    const uint4 b = at == 0 ? u : shifted(p, u, 16u - at);
+    const bool joined = at == 0 || (lane > 0 && v > 0);  // b is the block from element v N - skip
+    const int from = v * N - skip;
+    if (v < nv && joined && from + N <= D) {
+      *reinterpret_cast<uint4*>(row + from) = b;
+    } else if (v < nv) {
+      const uint4 src = make_uint4(joined ? b.x : u.x, joined ? b.y : u.y, joined ? b.z : u.z, joined ? b.w : u.w);
+      const T* e = reinterpret_cast<const T*>(&src);
+      const int first = joined ? from : v * N, count = min(joined ? N : N - skip, D - first);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < count) row[first + i] = e[i];
+    }
+    if (v < nv && skip > 0 && (lane == 31 || v + 1 == nv)) {  // no lane after this one takes its end
+      const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i >= N - skip && v * N + i < D) row[v * N + i] = e[i];
+    }
+  }
 }
 
 // The parameters of a thread's columns, kept in registers as they lie in memory: WT is the
@@ -615,15 +739,20 @@ template <typename T, typename WT>
 struct Params {
   static constexpr int kWords = Vec<T>::kN * (int)sizeof(WT) / 16;  // 16-byte words of a vector
   uint4 u[kWords];
-  __device__ __forceinline__ void load(const void* p, int v, bool in, float none) {
+  // `none` without an array, and past its D elements.
+  __device__ __forceinline__ void load(const void* p, int v, int D, float none) {
+    constexpr int E = Vec<WT>::kN;
+    const bool aligned = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      if (p != nullptr && in) {
+      const int c = (v * kWords + i) * E;
+      if (p != nullptr && aligned && c + E <= D) {
         u[i] = __ldg(static_cast<const uint4*>(p) + v * kWords + i);
       } else {
-        float f[Vec<WT>::kN];
+        float f[E];
 #pragma unroll
-        for (int e = 0; e < Vec<WT>::kN; ++e) f[e] = none;
+        for (int e = 0; e < E; ++e)
+          f[e] = p != nullptr && c + e < D ? to_f32(static_cast<const WT*>(p)[c + e]) : none;
         u[i] = pack<WT>(f);
       }
     }
@@ -645,7 +774,7 @@ struct Params {
 
 // The parameters stand in shared memory as they lie in global memory (the registers are the
 // row's). z leaves before the reductions, the row's distances from the mean replace it.
-template <typename T, typename WT, int EPT>
+template <typename T, typename WT, int EPT, bool AL>
 __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant__ NormArgs a) {
   constexpr int N = Vec<T>::kN, PERV = EPT / N, WORDS = N * (int)sizeof(WT) / 16;
   extern __shared__ __align__(128) uint8_t ring_smem[];  // [2][D] parameters, then the rings
@@ -653,25 +782,24 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
   __shared__ float red[kMaxGroups][2][32];
   const int warp = threadIdx.x >> 5, grp = warp / a.wpr, wr = warp % a.wpr;
   const int groups = (blockDim.x >> 5) / a.wpr;
-  const int t = wr * 32 + (threadIdx.x & 31), step = a.wpr * 32, nv = a.D / N;
+  const int t = wr * 32 + (threadIdx.x & 31), step = a.wpr * 32, nv = (a.D + N - 1) / N;
   const int words = nv * WORDS;  // 16-byte words of a parameter
   uint4* ws = reinterpret_cast<uint4*>(ring_smem);
-  {
-    float one[Vec<WT>::kN], zero[Vec<WT>::kN];
+  for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+    Params<T, WT> w, b;
+    w.load(a.w, i, a.D, 1.f);
+    b.load(a.b, i, a.D, 0.f);
 #pragma unroll
-    for (int e = 0; e < Vec<WT>::kN; ++e) one[e] = 1.f, zero[e] = 0.f;
-    const uint4 w1 = pack<WT>(one), b0 = pack<WT>(zero);
-    for (int i = threadIdx.x; i < words; i += blockDim.x) {
-      ws[i] = a.w != nullptr ? __ldg(static_cast<const uint4*>(a.w) + i) : w1;
-      ws[words + i] = a.b != nullptr ? __ldg(static_cast<const uint4*>(a.b) + i) : b0;
+    for (int h = 0; h < WORDS; ++h) {
+      ws[i * WORDS + h] = w.u[h];
+      ws[words + i * WORDS + h] = b.u[h];
     }
   }
   const int mats = a.r != nullptr ? 2 : 1;
   // At most 2^31 rows, and an index past n by less than a stride: 64 bits where it matters.
   const int first = (int)min((long long)blockIdx.x * groups + grp, a.n);
-  const Ring<T, false> g{a,
-                         ring_smem + (size_t)words * 32 + (size_t)grp * a.stages * mats * a.D * sizeof(T),
-                         &rs[grp], first, (int)gridDim.x * groups};
+  Ring<T, false, AL> g{a, ring_smem + (size_t)words * 32, &rs[grp], first, (int)gridDim.x * groups};
+  g.smem += (size_t)grp * a.stages * mats * g.pitch();
   ring_begin(g, t == 0);
   const float inv_d = 1.0f / (float)a.D;
   int it = 0, st = 0, phase = 0;
@@ -679,20 +807,23 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
     T* y = static_cast<T*>(a.y) + row * a.ld_y;
     T* z = a.z != nullptr ? static_cast<T*>(a.z) + row * a.ld_z : nullptr;
     ring_wait(g, st, phase);
-    const uint4* xs = g.stage(st);
+    const uint4 *xs = g.stage(st, 0), *rs_row = g.stage(st, 1);
+    const uint32_t at_x = AL ? 0u : block_offset(static_cast<const T*>(a.x), a.ld_x, row);
+    const uint32_t at_r = AL || mats == 1 ? 0u : block_offset(static_cast<const T*>(a.r), a.ld_r, row);
     F2 f[PERV][N / 2];
     F2 s2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
       if (v < nv) {
-        unpack_pairs<T>(xs[v], f[i]);
+        unpack_pairs<T>(ring_vec<AL>(xs, v, at_x), f[i]);
         if (mats == 2) {
           F2 q[N / 2];
-          unpack_pairs<T>(xs[nv + v], q);
+          unpack_pairs<T>(ring_vec<AL>(rs_row, v, at_r), q);
 #pragma unroll
           for (int e = 0; e < N / 2; ++e) f[i][e] = f[i][e] + q[e];
         }
+        trim<T, AL>(f[i], v, a.D);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) s2 = s2 + f[i][e];
       }
@@ -712,13 +843,13 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
+      if (z != nullptr) store_vecs<T, AL>(z, v, nv, a.D, pack_pairs<T>(f[i]));
       if (v < nv) {
-        if (z != nullptr) store_pairs<T>(z, v, f[i]);
 #pragma unroll
-        for (int e = 0; e < N / 2; ++e) {
-          f[i][e] = f[i][e] + minus_mean;
-          q2 = fma2(f[i][e], f[i][e], q2);
-        }
+        for (int e = 0; e < N / 2; ++e) f[i][e] = f[i][e] + minus_mean;
+        trim<T, AL>(f[i], v, a.D);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) q2 = fma2(f[i][e], f[i][e], q2);
       }
     }
     float q[1] = {q2.get().x + q2.get().y};
@@ -732,25 +863,26 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
-      if (v >= nv) break;
+      if (AL && v >= nv) break;
 #pragma unroll
       for (int h = 0; h < WORDS; ++h) {
+        const int at = (AL ? v : min(v, nv - 1)) * WORDS + h;
         F2 wf[Vec<WT>::kN / 2], bf[Vec<WT>::kN / 2];
-        unpack_pairs<WT>(ws[v * WORDS + h], wf);
-        unpack_pairs<WT>(ws[words + v * WORDS + h], bf);
+        unpack_pairs<WT>(ws[at], wf);
+        unpack_pairs<WT>(ws[words + at], bf);
 #pragma unroll
         for (int e = 0; e < Vec<WT>::kN / 2; ++e) {
           F2& x = f[i][h * (Vec<WT>::kN / 2) + e];
           x = fma2(x * rr, wf[e], bf[e]);
         }
       }
-      store_pairs<T>(y, v, f[i]);
+      store_vecs<T, AL>(y, v, nv, a.D, pack_pairs<T>(f[i]));
     }
   }
   ring_end(g, t == 0, it);
 }
 
-template <typename T, typename WT, int EPT>
+template <typename T, typename WT, int EPT, bool AL>
 __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
   constexpr int N = Vec<T>::kN, PERV = EPT / N;
   allow_dependent_launch();
@@ -759,18 +891,19 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
   __shared__ float red[kMaxGroups][2][64];
   const int warp = threadIdx.x >> 5, grp = warp / a.wpr, wr = warp % a.wpr;
   const int groups = (blockDim.x >> 5) / a.wpr;
-  const int t = wr * 32 + (threadIdx.x & 31), step = a.wpr * 32, nv = a.D / N;
+  const int t = wr * 32 + (threadIdx.x & 31), step = a.wpr * 32, nv = (a.D + N - 1) / N;
   const float inv_d = 1.0f / (float)a.D;
   // At most 2^31 rows, and an index past n by less than a stride: 64 bits where it matters.
   const int first = (int)min((long long)blockIdx.x * groups + grp, a.n);
-  const Ring<T, true> g{a, ring_smem + (size_t)grp * a.stages * (a.r != nullptr ? 3 : 2) * a.D * sizeof(T), &rs[grp], first, (int)gridDim.x * groups};
+  Ring<T, true, AL> g{a, ring_smem, &rs[grp], first, (int)gridDim.x * groups};
+  g.smem += (size_t)grp * a.stages * g.mats() * g.pitch();
   ring_begin(g, t == 0);
 
   Params<T, WT> w[PERV];
 #pragma unroll
   for (int i = 0; i < PERV; ++i) {
     const int v = t + i * step;
-    w[i].load(a.w, v, v < nv, 1.f);
+    w[i].load(a.w, v, a.D, 1.f);
   }
   F2 dw[PERV][N / 2], db[PERV][N / 2];
 #pragma unroll
@@ -790,7 +923,10 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
       rstd_n = __ldg(a.rstd + row + g.stride);
     }
     ring_wait(g, st, phase);
-    const uint4* zs = g.stage(st);
+    const uint4 *zs = g.stage(st, 0), *ds = g.stage(st, 1), *us = g.stage(st, 2);
+    const uint32_t at_z = AL ? 0u : block_offset(static_cast<const T*>(a.x), a.ld_x, row);
+    const uint32_t at_d = AL ? 0u : block_offset(static_cast<const T*>(a.dy), a.ld_dy, row);
+    const uint32_t at_u = AL || a.r == nullptr ? 0u : block_offset(static_cast<const T*>(a.r), a.ld_r, row);
     const F2 minus_mean(-mean, -mean), rr(rstd, rstd);
     F2 xh[PERV][N / 2], d[PERV][N / 2];
     uint4 up[PERV];
@@ -800,13 +936,16 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
       const int v = t + i * step;
       if (v < nv) {
         F2 wf[N / 2];
-        unpack_pairs<T>(zs[v], xh[i]);
-        unpack_pairs<T>(zs[nv + v], d[i]);
-        if (a.r != nullptr) up[i] = zs[2 * nv + v];
+        unpack_pairs<T>(ring_vec<AL>(zs, v, at_z), xh[i]);
+        unpack_pairs<T>(ring_vec<AL>(ds, v, at_d), d[i]);
+        if (a.r != nullptr) up[i] = ring_vec<AL>(us, v, at_u);
         w[i].get(wf);
 #pragma unroll
+        for (int e = 0; e < N / 2; ++e) xh[i][e] = (xh[i][e] + minus_mean) * rr;
+        trim<T, AL>(xh[i], v, a.D);
+        trim<T, AL>(d[i], v, a.D);
+#pragma unroll
         for (int e = 0; e < N / 2; ++e) {
-          xh[i][e] = (xh[i][e] + minus_mean) * rr;
           dw[i][e] = fma2(d[i][e], xh[i][e], dw[i][e]);
           db[i][e] = db[i][e] + d[i][e];
           d[i][e] = d[i][e] * wf[e];
@@ -828,7 +967,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
 #pragma unroll
     for (int i = 0; i < PERV; ++i) {
       const int v = t + i * step;
-      if (v >= nv) break;
+      if (AL && v >= nv) break;
       F2 o[N / 2];
       if (a.r != nullptr) {
         unpack_pairs<T>(up[i], o);
@@ -838,7 +977,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
       }
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) o[e] = fma2(rr, fma2(xh[i][e], m2, d[i][e] + m1), o[e]);
-      store_pairs<T>(dx, v, o);
+      store_vecs<T, AL>(dx, v, nv, a.D, pack_pairs<T>(o));
     }
   }
   ring_end(g, t == 0, it);
@@ -872,9 +1011,16 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
     const int v = t + i * step;
     if (v < nv)
 #pragma unroll
-      for (int e = 0; e < N / 2; ++e) {  // D is even: pairs on 8 bytes
-        *reinterpret_cast<float2*>(pw + v * N + 2 * e) = dw[i][e].get();
-        *reinterpret_cast<float2*>(pw + a.D + v * N + 2 * e) = db[i][e].get();
+      for (int e = 0; e < N / 2; ++e) {
+        const int c = v * N + 2 * e;
+        const float2 p = dw[i][e].get(), q = db[i][e].get();
+        if (AL) {  // D is even: pairs on 8 bytes
+          *reinterpret_cast<float2*>(pw + c) = p;
+          *reinterpret_cast<float2*>(pw + a.D + c) = q;
+        } else {
+          if (c < a.D) pw[c] = p.x, pw[a.D + c] = q.x;
+          if (c + 1 < a.D) pw[c + 1] = p.y, pw[a.D + c + 1] = q.y;
+        }
       }
   }
 }
@@ -956,22 +1102,25 @@ NormShape norm_shape(const moe_norm_args* p, bool vec, int num_sms, bool backwar
 
 constexpr int kRingBytes = 200 * 1024;  // shared memory of an SM that the rings share
 
-// Whether the ring kernel takes these rows, and its launch: 16-byte rows, enough of them
-// that every group walks two or more. 16 warps an SM of 128 registers a thread: one CTA
+// Whether the ring kernel takes these rows, and its launch: 64 bytes a row or more, and enough
+// rows that every group walks two or more. 16 warps an SM of 128 registers a thread: one CTA
 // forward, one or two backward.
 struct RingShape {
+  bool aligned;
   int ept, wpr, groups, stages, ctas;  // ctas: on an SM; 0: not taken
   size_t smem;
 };
 RingShape ring_shape(const moe_norm_args* p, bool aligned, int mats, int num_sms, bool backward) {
   RingShape r{};
-  const size_t row = (size_t)p->D * type_bytes(p->dtype);
+  const size_t bytes = (size_t)p->D * type_bytes(p->dtype);
+  const size_t row = aligned ? bytes : (bytes + 15) / 16 * 16 + 16;  // in a stage
+  r.aligned = aligned;
   r.ept = backward ? kBackwardEpt : p->D <= 512 ? 16 : kForwardEpt;
   r.wpr = (p->D + 32 * r.ept - 1) / (32 * r.ept);
-  if (!aligned || r.wpr > 16) return r;
+  if (bytes < 64 || r.wpr > 16) return r;
   r.groups = std::max(1, (backward ? 8 : 16) / r.wpr);
   r.ctas = backward ? std::max(1, 16 / (r.wpr * r.groups)) : 1;
-  const size_t params = backward ? 0 : 2 * (size_t)p->D * type_bytes(p->wtype);
+  const size_t params = backward ? 0 : 2 * ((size_t)p->D + 7) / 8 * 8 * type_bytes(p->wtype);
   const size_t stage = (size_t)r.groups * mats * row, room = kRingBytes / r.ctas;
   r.stages = room > params ? (int)std::min<size_t>(kMaxRing, (room - params) / stage) : 0;
   r.smem = params + r.stages * stage;
@@ -990,13 +1139,18 @@ cudaError_t launch_ring(K kernel, std::atomic<uint64_t>* ready, const NormArgs& 
   kernel<<<grid, 32 * r.wpr * r.groups, r.smem, s>>>(a);
   return cudaGetLastError();
 }
-template <typename T, typename WT>
-cudaError_t launch_ring_of(bool backward, const NormArgs& a, const RingShape& r, int grid, cudaStream_t s) {
+template <typename T, typename WT, bool AL>
+cudaError_t launch_ring_as(bool backward, const NormArgs& a, const RingShape& r, int grid, cudaStream_t s) {
   static std::atomic<uint64_t> ready_f{0}, ready_n{0}, ready_b{0};
   if (backward)
-    return launch_ring(norm_backward_ring_kernel<T, WT, kBackwardEpt>, &ready_b, a, r, grid, s);
-  return r.ept == 16 ? launch_ring(norm_ring_kernel<T, WT, 16>, &ready_n, a, r, grid, s)
-                     : launch_ring(norm_ring_kernel<T, WT, kForwardEpt>, &ready_f, a, r, grid, s);
+    return launch_ring(norm_backward_ring_kernel<T, WT, kBackwardEpt, AL>, &ready_b, a, r, grid, s);
+  return r.ept == 16 ? launch_ring(norm_ring_kernel<T, WT, 16, AL>, &ready_n, a, r, grid, s)
+                     : launch_ring(norm_ring_kernel<T, WT, kForwardEpt, AL>, &ready_f, a, r, grid, s);
+}
+template <typename T, typename WT>
+cudaError_t launch_ring_of(bool backward, const NormArgs& a, const RingShape& r, int grid, cudaStream_t s) {
+  return r.aligned ? launch_ring_as<T, WT, true>(backward, a, r, grid, s)
+                   : launch_ring_as<T, WT, false>(backward, a, r, grid, s);
 }
 int run_ring(bool backward, int dtype, NormArgs& a, const RingShape& r, int grid, cudaStream_t s) {
   a.wpr = r.wpr;
