@@ -109,6 +109,11 @@ def router_cfg(E, topk, score="softmax", groups=1, topk_groups=1, group_top=1, r
                                int(bool(renorm)), scale)
 
 
+def score_name(cfg: capi.moe_router_cfg) -> str:
+    """The score of a router configuration by its name here."""
+    return next(k for k, v in _SCORES.items() if v == cfg.score)
+
+
 def route_experts(logits, topk, score="softmax", bias=None, groups=1, topk_groups=1, group_top=1,
                   renorm=False, scale=1.0, stream=None):
     """The topk experts of every token and their weights, from scores logits [..., E].
