@@ -1,22 +1,27 @@
-"""Build the in-tree shared library libmoe_tsg.so for sm_103a with nvcc.
+"""Build the in-tree shared library libmoe_tsg.so for sm_103a with nvcc, and its torch
+binding _torch_ops.so with the host compiler.
 
 Each translation unit compiles in parallel into _build/, then one nvcc link
 produces tile_signaled_grouped_gb300/libmoe_tsg.so (CUDA runtime linked
-statically, so the library needs only the driver at run time).
+statically, so the library needs only the driver at run time) and one host link the
+binding, which loads that library from its own folder.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_tsg.so")
+BINDING = os.path.join(PKG, "_torch_ops.so")
 SOURCES = ["api.cu", "plan.cu", "ffn.cu", "ffn_pair.cu", "consumer.cu", "route_scale.cu", "gate.cu",
            "plan_noalloc.cu", "gate_rows.cu", "router.cu", "norm.cu",
            "linear.cu"]
@@ -48,10 +53,35 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _torch() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found")
+    return os.path.dirname(spec.origin)
+
+
+def _compile_binding() -> str:
+    obj = os.path.join(BUILD, "torch_ops.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(_torch(), "include"),
+           os.path.join(_torch(), "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          *[f for i in inc for f in ("-isystem", i)], "-DTORCH_EXTENSION_NAME=_torch_ops", "-c",
+          os.path.join(CSRC, "torch_ops.cpp"), "-o", obj], "the torch binding's compilation")
+    return obj
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(ROOT, "include", "moe_tsg.h"))
     deps.append(os.path.abspath(__file__))
@@ -63,14 +93,18 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose, extra), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "nvcc link")
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding.result(), "-L" + PKG,
+          "-l:libmoe_tsg.so", "-L" + os.path.join(_torch(), "lib"), "-lc10", "-lc10_cuda",
+          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "the torch binding's link")
+    os.replace(tmp, BINDING)
     return LIB
 
 

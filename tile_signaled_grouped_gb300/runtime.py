@@ -90,15 +90,10 @@ class ExpertCombine:
         an ops.router_cfg with the layer's E and topk; bias: None or [E] fp32."""
         from . import ops
 
-        n, E, ld = ops._rows(logits, "logits")
-        if E != self.W * self.L or n != self.W * self.T:
-            raise ValueError(f"logits hold {n} rows of {E}: expected {self.W * self.T} rows of "
-                             f"{self.W * self.L}")
-        if bias is not None:
-            ops._vector(bias, "bias", E, (torch.float32,), logits.get_device())
-        capi.moe_router(self.plan, router, logits.data_ptr(), ops._dtype(logits, "logits"), n, ld,
-                        None if bias is None else bias.data_ptr(), self.ids.data_ptr(),
-                        self.w.data_ptr(), _stream_handle(stream))
+        ops.native().route_plan(self.plan, self.W * self.T, router.E, router.topk, router.score,
+                                router.groups, router.topk_groups, router.group_top,
+                                router.renorm, router.scale, logits, bias, self.ids, self.w,
+                                _stream_handle(stream))
         return self.ids, self.w
 
     def gate(self, x, w_router, forced_ids=None, stream=None, logits_out=None, splits=0):
