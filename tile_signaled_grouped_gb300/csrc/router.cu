@@ -9,8 +9,10 @@
 //   w_j = s_j                 or  s_j / (sum of the chosen s)      times `scale`
 //
 // A warp takes a token, its experts in the lanes' registers. Bound by instructions at many
-// tokens (the scores are 4 E bytes, the selection about a thousand warp instructions), by
-// its chain of warp reductions at few.
+// tokens: 16384 x 256 with a bias and 4 of 8 groups, k = 8, takes 16 us (1.1 TB/s of scores)
+// for 670 warp instructions a token: 75 to load, 75 for the scores, 55 to sort a lane's eight,
+// 125 for the groups, 20 a round, 50 to find the ids, 40 to judge how close the order is, 75
+// for the weights (1.7 us of it pass while the last tokens decided in 64 bits end). At few tokens by its chain of warp reductions: 3.2 us for one.
 //
 // Which experts are chosen is decided as in 64 bits. The scores are computed in 32 bits
 // with a known error bound; where two neighbours in the order of the winners (or the
@@ -66,7 +68,7 @@ struct RouterArgs {
   long long n, ld, ld_dl;
   int dtype, E, k, G, TG, GT, score, renorm;
   bool vec;  // rows (and the bias) can be read and written by vectors of four
-  int lpg;  // lanes of a group: the largest power of two that leaves each one its own
+  int lpg, lpg_log2;  // lanes of a group: the largest power of two that leaves each one its own
   float scale;
 };
 
@@ -75,13 +77,31 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
-// The largest value of the warp; NaN counts as -inf.
-__device__ __forceinline__ float warp_max(float v) {
-  return key_float(__reduce_max_sync(kAll, float_key(v == v ? v : -INFINITY)));
+// The largest and the smallest value of the warp without its NaN; NaN if there is no other.
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
+__device__ __forceinline__ float redux_min(float v) {
+  float r;
+  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// The largest value of the warp; NaN counts as -inf.
+__device__ __forceinline__ float warp_max(float v) { return redux_max(v == v ? v : -INFINITY); }
 // Within 5 steps of fp32 (expf 2, the fast division 2, two roundings); an exponential that
 // the fast division takes for infinity (beyond 2^126) belongs to a score below 1e-37.
 __device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+// For the order alone: within 4 * 2^-23 of s, not relative to it. exp(-l) = 2^(-l log2 e) is off
+// by (1.5 + |l|) 2^-23 of itself (the product's rounding, 2^-22.5 for ex2), which s (1 - s)
+// turns into less than 0.5 * 2^-23; the sum's rounding and the reciprocal add 2 s 2^-23.
+__device__ __forceinline__ float sigmoid_near(float l) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  return s;
+}
 
 // The two largest of (a, b, ...) so far.
 template <typename F>
@@ -151,38 +171,70 @@ __device__ __noinline__ uint32_t settle_groups(const RouterArgs& a, const void* 
   return sure | (__ballot_sync(kAll, rank < a.TG - __popc(sure)) & may);
 }
 
-// Bit g of the result: group g stays. sum: lane g's is group g's score (g < G). tol: what
-// two scores may differ by and still be in the other order.
-__device__ __forceinline__ uint32_t rank_groups(const RouterArgs& a, const void* row, float sum, int lane,
-                                                float tol) {
-  int rank = 0;
-  for (int h = 0; h < a.G; ++h) {
-    const float o = __shfl_sync(kAll, sum, h);
-    rank += (o > sum) | ((o == sum) & (h < lane));
-  }
+// rank_groups where the last group kept and the first one dropped are too close to call.
+__device__ __noinline__ uint32_t settle_ranks(const RouterArgs& a, const void* row, float sum, float last,
+                                              float first, float tol, int lane) {
+  const float s = __shfl_sync(kAll, sum, min(lane * a.lpg, 31));  // lane g: group g's
   const uint32_t in = a.G < 32 ? (1u << a.G) - 1u : kAll;
-  const uint32_t kept = __ballot_sync(kAll, rank < a.TG) & in;
-  const uint32_t at_last = __ballot_sync(kAll, rank == a.TG - 1) & in;
-  const uint32_t at_first = __ballot_sync(kAll, rank == a.TG) & in;
-  if (at_last == 0 || at_first == 0) return kept;  // every group stays (or a score is NaN)
-  const float last = __shfl_sync(kAll, sum, __ffs(at_last) - 1);
-  const float first = __shfl_sync(kAll, sum, __ffs(at_first) - 1);
-  if (!(last - first <= tol)) return kept;  // also -inf - -inf: the ids have decided
-  const uint32_t sure = __ballot_sync(kAll, sum > last + tol) & in;
-  const uint32_t out = __ballot_sync(kAll, sum < first - tol) & in;
-  return settle_groups(a, row, in & ~(sure | out), sure, lane);
+  const uint32_t sure = __ballot_sync(kAll, s > last + tol) & in;
+  const uint32_t out = __ballot_sync(kAll, s < first - tol) & in;
+  const uint32_t kept = settle_groups(a, row, in & ~(sure | out), sure, lane);
+  const int g = lane >> a.lpg_log2;
+  return __ballot_sync(kAll, g < a.G && ((kept >> (g & 31)) & 1u));
 }
 
-// The sum of a group's group_top largest values, in lane g for group g: each of a group's
-// lpg lanes brings its two largest.
-__device__ __forceinline__ float group_sums(const RouterArgs& a, float t1, float t2, int lane) {
-  for (int o = a.lpg / 2; o; o >>= 1) {
+// Which groups stay: bits g LPG .. g LPG + LPG - 1 of the result are group g's, and so are those
+// lanes, each of which brings the two largest values t1 and t2 that it saw. A group's lanes share
+// its comparisons with the others. eps: what a value may be off by beside the rounding of a sum
+// with a bias; negative where none is.
+template <int LPG, bool WHOLE>
+__device__ __forceinline__ uint32_t rank_groups_of(const RouterArgs& a, const void* row, float t1, float t2,
+                                                   bool sums, float eps, float smax, int lane) {
+#pragma unroll
+  for (int o = LPG / 2; o; o >>= 1) {
     const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
-    top2(u1, t1, t2);
-    top2(u2, t1, t2);
+    t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
+    t1 = fmaxf(t1, u1);
   }
-  const float sum = a.GT > 1 && a.E > a.G ? t1 + t2 : t1;
-  return __shfl_sync(kAll, sum, min(lane * a.lpg, 31));
+  const float sum = sums ? t1 + t2 : t1;
+  const int G = WHOLE ? 32 / LPG : a.G, g = lane / LPG, q = lane % LPG;
+  int rank = 0;
+#pragma unroll
+  for (int h0 = 0; h0 < 32 / LPG; h0 += LPG) {
+    if (!WHOLE && h0 >= G) break;
+    const int h = h0 + q;
+    const float o = __shfl_sync(kAll, sum, h * LPG);  // h past the last group does not count
+    rank += (h < G) & ((o > sum) | ((o == sum) & (h < g)));
+  }
+#pragma unroll
+  for (int o = LPG / 2; o; o >>= 1) rank += __shfl_xor_sync(kAll, rank, o);
+  const bool in = g < G, stays = in && rank < a.TG;
+  const uint32_t kept = __ballot_sync(kAll, stays);
+  if (eps >= 0.f) {
+    // What two sums may differ by and still be in the other order. The largest finite term
+    // counts, not the sum: a sum of two can cancel.
+    float m = smax;
+    if (a.bias != nullptr) {
+      m = fabsf(t1) < INFINITY ? fmaxf(m, fabsf(t1)) : m;
+      m = redux_max(fabsf(t2) < INFINITY ? fmaxf(m, fabsf(t2)) : m);
+    }
+    const float tol = 4.f * eps + 0x1p-21f * m;
+    const float last = redux_min(stays ? sum : NAN), first = redux_max(in && !stays ? sum : NAN);
+    // Not for -inf - -inf, where the ids have decided, nor where every group stays.
+    if (last - first <= tol) return settle_ranks(a, row, sum, last, first, tol, lane);
+  }
+  return kept;
+}
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t rank_groups(const RouterArgs& a, const void* row, float t1, float t2,
+                                                bool sums, float eps, float smax, int lane) {
+  switch (a.lpg_log2) {  // unrolled, less than half the instructions of loops over a.lpg
+    case 0: return rank_groups_of<1, WHOLE>(a, row, t1, t2, sums, eps, smax, lane);
+    case 1: return rank_groups_of<2, WHOLE>(a, row, t1, t2, sums, eps, smax, lane);
+    case 2: return rank_groups_of<4, WHOLE>(a, row, t1, t2, sums, eps, smax, lane);
+    case 3: return rank_groups_of<8, WHOLE>(a, row, t1, t2, sums, eps, smax, lane);
+    default: return rank_groups_of<16, WHOLE>(a, row, t1, t2, sums, eps, smax, lane);
+  }
 }
 
 // Slot `lane`'s id where the m candidates in lanes 0.. (id in lane) hold every expert that
@@ -219,7 +271,7 @@ __device__ __noinline__ int settle_all(const RouterArgs& a, const void* row, uin
     double bv = -INFINITY;
     int be = 0x7FFFFFFF;
     for (int i = 0, e = lane; e < a.E; ++i, e += 32) {
-      const bool ok = !((taken >> i) & 1u) && (a.G == 1 || ((kept >> (e / per)) & 1u));
+      const bool ok = !((taken >> i) & 1u) && (a.G == 1 || ((kept >> (e / per * a.lpg)) & 1u));
       if (ok && (be == 0x7FFFFFFF || buf[e] > bv)) {
         bv = buf[e];
         be = e;
@@ -260,6 +312,28 @@ __device__ __forceinline__ float slot_weight(const RouterArgs& a, float t, bool 
   return S == 0.f ? 0.f : e / S;
 }
 
+// A lane's values, the largest first: sorting networks of 1, 5 and 19 comparators (Batcher).
+template <int PER>
+__device__ __forceinline__ void sort_values(float (&v)[PER]) {
+  auto order = [&](int i, int j) {
+    const float x = v[i], y = v[j];
+    v[i] = fmaxf(x, y);
+    v[j] = fminf(x, y);
+  };
+  if constexpr (PER == 2) {
+    order(0, 1);
+  } else if constexpr (PER == 4) {
+    order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+  } else if constexpr (PER == 8) {
+    order(0, 1), order(2, 3), order(4, 5), order(6, 7);
+    order(0, 2), order(1, 3), order(4, 6), order(5, 7);
+    order(1, 2), order(5, 6);
+    order(0, 4), order(1, 5), order(2, 6), order(3, 7);
+    order(2, 4), order(3, 5);
+    order(1, 2), order(3, 4), order(5, 6);
+  }
+}
+
 // Four or eight scores of a lane, as one or two vector loads.
 template <int PER>
 __device__ __forceinline__ void load_scores(const void* row, int dtype, int e0, float (&l)[PER]) {
@@ -280,19 +354,59 @@ __device__ __forceinline__ void load_scores(const void* row, int dtype, int e0, 
   }
 }
 
-// Lane l holds experts PER l .. PER l + PER - 1: registers for its sorted list up to
-// PER = 8; above, each round looks through the lane's candidates again. WHOLE: E = 32 PER
-// and a power of two of groups, so that a group is a run of whole lanes: its two largest
-// values are among the heads of those lanes' lists, and a group that goes takes its lanes
-// along. Otherwise the values that groups are judged by pass through shared memory.
+// A lane's values to shared memory and back: vectors of up to four beside the other lanes' (no
+// bank conflicts, which one run of eight for each lane would have).
+template <int PER>
+__device__ __forceinline__ void put_values(float* vals, int lane, const float (&v)[PER]) {
+  if constexpr (PER >= 4) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 4)
+      reinterpret_cast<float4*>(vals)[i * 8 + lane] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) vals[i * 32 + lane] = v[i];
+  }
+}
+template <int PER>
+__device__ __forceinline__ void get_values(const float* vals, int lane, float (&v)[PER]) {
+  if constexpr (PER >= 4) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const float4 u = reinterpret_cast<const float4*>(vals)[i * 8 + lane];
+      v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = vals[i * 32 + lane];
+  }
+}
+constexpr int kSlotBytes = 33 * 8 + 8;
+template <int PER>
+constexpr int kWarpBytes = kSlotBytes + 32 * (2 * PER + (PER <= 8 ? 2 : 0)) * (int)sizeof(float);
+
+// Lane l holds experts PER l .. PER l + PER - 1. Up to PER = 8 it sorts their values once, its
+// best in a register and the rest in shared memory, from where a round's winner takes its next;
+// which expert a value was is found after the rounds, from the values' places (a sort of pairs
+// and lists shifted in registers took 23 us where this takes 16). Above, each round looks
+// through the lane's candidates again. WHOLE: E = 32 PER and a power of two of groups, so that a
+// group is a run of whole lanes: its two largest values are among the heads of those lanes'
+// lists, and a group that goes takes its lanes along. Otherwise the values that groups are
+// judged by pass through shared memory. Six CTAs an SM: 3 % faster than the four of 64 registers.
 template <int PER, bool WHOLE>
-__global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_constant__ RouterArgs a) {
+__global__ void __launch_bounds__(32 * kRouterWarps, PER <= 8 ? 6 : 1)
+    router_kernel(const __grid_constant__ RouterArgs a) {
   static_assert(!WHOLE || PER <= 8, "sorted lists");
-  extern __shared__ double smem_d[];
+  extern __shared__ double2 smem_d[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long tok = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
   if (tok >= a.n) return;
-  double* buf = smem_d + (size_t)warp * a.E;
+  // A warp's shared memory: 33 slots, the values (PER <= 8, or of groups) and the lanes' lists
+  // of them (PER <= 8), which the 64-bit values may replace.
+  char* mem = reinterpret_cast<char*>(smem_d) + (size_t)warp * kWarpBytes<PER>;
+  float2* slot = reinterpret_cast<float2*>(mem);
+  double* buf = reinterpret_cast<double*>(mem + kSlotBytes);
+  float* vals = reinterpret_cast<float*>(buf);
+  float* list = vals + 32 * PER;
   const int tb = a.dtype == MOE_FP32 ? 4 : 2, e0 = lane * PER;
   const void* row = static_cast<const char*>(a.logits) + (size_t)tok * a.ld * tb;
 
@@ -324,7 +438,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
     if (mx != -INFINITY) inv = 1.0f / sum;
   }
   auto score_of = [&](float l) {
-    return a.score == MOE_SCORE_SIGMOID ? sigmoid(l) : mx == -INFINITY ? 0.f : expf(l - mx) * inv;
+    return a.score == MOE_SCORE_SIGMOID ? sigmoid_near(l) : mx == -INFINITY ? 0.f : expf(l - mx) * inv;
   };
   if (a.bias != nullptr) {
     float b[PER];
@@ -335,74 +449,67 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
       for (int i = 0; i < PER; ++i) b[i] = WHOLE || e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = (soft ? s[i] * inv : sigmoid(c[i])) + b[i];
+    for (int i = 0; i < PER; ++i) c[i] = (soft ? s[i] * inv : sigmoid_near(c[i])) + b[i];
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) c[i] = c[i] == c[i] ? c[i] : -INFINITY;
+  for (int i = 0; i < PER; ++i) c[i] = fmaxf(c[i], -INFINITY);  // of NaN and a number the number
   // How far a score in 32 bits may be off: 5 steps of fp32 for the sigmoid; for the softmax
   // 3 for the exponential and its argument, PER + 5 additions in the sum, 2 for the rest.
   // At most `eps` for scores up to smax; c adds its own rounding.
   const float smax = a.score == MOE_SCORE_SIGMOID ? 1.0f : inv;
   const float eps = (a.score == MOE_SCORE_SIGMOID ? 6.f : PER + 12.f) * 0x1p-23f * smax;
-  float tol = -1.f;  // of two groups' scores; judged by the l themselves, nothing is rounded
-  if (a.G > 1 && by_score) {
-    float cm = smax;  // the largest finite |c|: a sum of two can cancel
-    if (a.bias != nullptr) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) cm = fabsf(c[i]) < INFINITY ? fmaxf(cm, fabsf(c[i])) : cm;
-      cm = warp_max(cm);
-    }
-    tol = 4.f * eps + 0x1p-21f * cm;
-  }
+  const float group_eps = by_score ? eps : -1.f;  // judged by the l themselves, nothing is rounded
 
   uint32_t kept = kAll;
   uint32_t open = 0;  // bit i: this lane's candidate i may be chosen
   if constexpr (!WHOLE) {
     if (a.G > 1) {
-      float* val = reinterpret_cast<float*>(buf);
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (e0 + i < a.E) {
           const float v = a.bias == nullptr && sums ? score_of(c[i]) : c[i];
-          val[e0 + i] = v == v ? v : -INFINITY;
+          vals[e0 + i] = v == v ? v : -INFINITY;
         }
       __syncwarp();
-      const int per = a.E / a.G, g = lane / a.lpg;
+      const int per = a.E / a.G, g = lane >> a.lpg_log2;
       float t1 = -INFINITY, t2 = -INFINITY;
       if (g < a.G)
-        for (int i = lane % a.lpg; i < per; i += a.lpg) top2(val[g * per + i], t1, t2);
-      kept = rank_groups(a, row, group_sums(a, t1, t2, lane), lane, tol);
+        for (int i = lane & (a.lpg - 1); i < per; i += a.lpg) top2(vals[g * per + i], t1, t2);
+      kept = rank_groups<WHOLE>(a, row, t1, t2, sums, group_eps, smax, lane);
       int q = e0 / per, r = e0 % per;  // of expert e0 + i: its group, its place there
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        open |= (e0 + i < a.E && ((kept >> (q & 31)) & 1u)) ? 1u << i : 0u;
+        open |= (e0 + i < a.E && ((kept >> ((q << a.lpg_log2) & 31)) & 1u)) ? 1u << i : 0u;
         const bool next = ++r == per;
         r = next ? 0 : r;
         q += next;
       }
+      __syncwarp();  // what is chosen from takes their place
     } else {
 #pragma unroll
       for (int i = 0; i < PER; ++i) open |= e0 + i < a.E ? 1u << i : 0u;
     }
   }
 
-  // Rounds: the warp's best candidate each. Lane j keeps round j's.
-  uint32_t my_key = 0, my_id = 0;
-  int rounds = a.bias != nullptr ? a.k + 1 : a.k;  // with a bias, the next in line too
-  uint32_t past_key = 0;  // the last round's
-  int left = WHOLE ? PER : __popc(open);
-  uint32_t order = 0;  // PER <= 8: the candidates in their order, four bits each, the best lowest
+  // Rounds: the warp's best candidate each. Round j's winner writes slot j. NaN: no candidate.
+  float head = NAN;  // PER <= 8: this lane's best, then the rest in their order from list[at]
+  int at = lane * (PER + 1);
   if constexpr (PER <= 8) {
-    int e[PER];
+    if constexpr (!WHOLE) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const bool ok = WHOLE || ((open >> i) & 1u);
-      c[i] = ok ? c[i] : -INFINITY;
-      e[i] = ok ? i : 15;  // after every candidate, the ones at -inf too
+      for (int i = 0; i < PER; ++i) c[i] = (open >> i) & 1u ? c[i] : NAN;
     }
-    route_sort<PER>(c, e);
+    put_values<PER>(vals, lane, c);
+    if constexpr (!WHOLE) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) order |= (uint32_t)e[i] << (4 * i);
+      for (int i = 0; i < PER; ++i) c[i] = fmaxf(c[i], -INFINITY);  // after every candidate
+    }
+    sort_values<PER>(c);
+    const int n = WHOLE ? PER : __popc(open);
+#pragma unroll
+    for (int i = 1; i < PER; ++i) list[at + i - 1] = i < n ? c[i] : NAN;
+    list[at + PER - 1] = NAN;
+    head = n > 0 ? c[0] : NAN;
     if (WHOLE && a.G > 1) {
       float t1 = c[0], t2 = PER > 1 ? c[PER > 1 ? 1 : 0] : -INFINITY;
       if (a.bias == nullptr && sums) {
@@ -411,52 +518,73 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
         t1 = t1 == t1 ? t1 : -INFINITY;
         t2 = t2 == t2 ? t2 : -INFINITY;
       }
-      kept = rank_groups(a, row, group_sums(a, t1, t2, lane), lane, tol);
-      left = (kept >> (lane / a.lpg)) & 1u ? PER : 0;
+      kept = rank_groups<WHOLE>(a, row, t1, t2, sums, group_eps, smax, lane);
+      head = (kept >> lane) & 1u ? head : NAN;
     }
   }
-  auto round = [&](int j) {
-    uint32_t key, id;
-    if constexpr (PER <= 8) {
-      key = left > 0 ? float_key(c[0]) : 0u;  // 0: no candidate (keys are larger)
-      id = e0 + (order & 15u);
-    } else {
-      float bv = -INFINITY;
-      int bi = -1;
+  int rounds = 0;
+  float past = NAN;  // the last round's
+  auto round = [&] {
+    float v = head;
+    int bi = -1;
+    if constexpr (PER > 8) {
+      v = NAN;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const bool better = ((open >> i) & 1u) & ((c[i] > bv) | (bi < 0));
-        bv = better ? c[i] : bv;
+        const bool better = ((open >> i) & 1u) & ((c[i] > v) | (bi < 0));
+        v = better ? c[i] : v;
         bi = better ? i : bi;
       }
-      key = bi >= 0 ? float_key(bv) : 0u;
-      id = bi >= 0 ? (uint32_t)(e0 + bi) : kAll;
     }
-    const uint32_t kmax = __reduce_max_sync(kAll, key);
-    const uint32_t emin = __reduce_min_sync(kAll, key == kmax ? id : kAll);
-    const bool win = key != 0u && id == emin;
-    if constexpr (PER <= 8) {
-#pragma unroll
-      for (int i = 0; i + 1 < PER; ++i) c[i] = win ? c[i + 1] : c[i];
-      order = win ? order >> 4 : order;
-      left -= win;
-    } else {
-      open &= win ? ~(1u << (id - e0)) : kAll;
+    past = redux_max(v);
+    // Equal ones: the lowest id is the lowest lane's, whose candidates are in that order too.
+    const bool win = lane == __ffs(__ballot_sync(kAll, v == past)) - 1;
+    if (win) {
+      slot[rounds] = make_float2(v, __int_as_float(PER > 8 ? e0 + bi : at));
+      if constexpr (PER > 8)
+        open &= ~(1u << bi);
+      else
+        head = list[at++];
     }
-    my_key = lane == j ? kmax : my_key;
-    my_id = lane == j ? emin : my_id;
-    past_key = kmax;
+    ++rounds;
   };
-  for (int j = 0; j < rounds; ++j) round(j);
+  const int need = a.bias != nullptr ? a.k + 1 : a.k;  // with a bias, the next in line too
+  // The id of slot `lane` in the lanes that have one (the last round may have found none).
+  auto slot_id = [&] {
+    __syncwarp();
+    int id = 0;
+    if (lane < rounds - (past == past ? 0 : 1)) {
+      const float2 w = slot[lane];
+      id = __float_as_int(w.y);
+      if constexpr (PER <= 8) {
+        // The value's place among its lane's candidates: of the equal ones that whose rank, the
+        // larger ones and those before it, was the winner's place in the list.
+        const int from = id / (PER + 1);
+        float v[PER];
+        get_values<PER>(vals, from, v);
+        uint32_t same = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) same |= v[i] == w.x ? 1u << i : 0u;
+        if (same & (same - 1)) {
+          int skip = id % (PER + 1);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) skip -= v[i] > w.x;
+          for (; skip > 0; --skip) same &= same - 1;
+        }
+        id = from * PER + __ffs(same) - 1;
+      }
+    }
+    return id;
+  };
+  while (rounds < need) round();
+  int my_id = slot_id();
   if (a.bias != nullptr) {
     // Neighbours of the order within their error, unless score and bias are equal (then
     // the ids decide, as they did).
-    uint32_t nk = __shfl_down_sync(kAll, my_key, 1);
-    const uint32_t ni = __shfl_down_sync(kAll, my_id, 1);
-    if (lane == 31) nk = past_key;  // only asked for k = 32
+    const int ni = __shfl_down_sync(kAll, my_id, 1);
     bool amb = false;
-    if (lane < a.k && nk != 0u) {
-      const float x = key_float(my_key), y = key_float(nk);
+    if (lane < a.k) {
+      const float x = slot[lane].x, y = lane + 1 < a.k ? slot[lane + 1].x : past;
       amb = x - y <= 2.f * eps + 0x1p-22f * (fabsf(x) + fabsf(y));
       if (amb && lane < 31)
         amb = load_as_f32(row, a.dtype, my_id) != load_as_f32(row, a.dtype, ni) ||
@@ -464,15 +592,15 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
     }
     if (__any_sync(kAll, amb)) {
       // Every candidate that may be among the k: those within the error of the k-th.
-      const float border = key_float(__shfl_sync(kAll, my_key, a.k - 1));
+      const float border = slot[a.k - 1].x;
       const float low = border - (2.f * eps + 0x1p-21f * fabsf(border));
-      auto more = [&] { return past_key != 0u && key_float(past_key) >= low; };
-      while (more() && rounds <= 32) round(rounds++);
+      while (past >= low && rounds <= 32) round();
+      my_id = slot_id();
       // Without a candidate in line, `rounds` counts the round that found none.
-      if (more())
-        my_id = (uint32_t)settle_all(a, row, kept, buf, lane);
+      if (past >= low)
+        my_id = settle_all(a, row, kept, buf, lane);
       else
-        my_id = (uint32_t)settle_slots(a, row, (int)my_id, min(rounds - 1, 32), lane);
+        my_id = settle_slots(a, row, my_id, min(rounds - 1, 32), lane);
     }
   }
 
@@ -480,7 +608,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
   const float t = in ? load_as_f32(row, a.dtype, my_id) : 0.f;
   const float w = slot_weight(a, t, in, mx, inv);
   if (in) {
-    a.ids[tok * a.k + lane] = (int32_t)my_id;
+    a.ids[tok * a.k + lane] = my_id;
     a.w[tok * a.k + lane] = a.scale * w;
   }
 }
@@ -497,7 +625,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const __grid_
 template <int PER>
 __global__ void __launch_bounds__(32 * kRouterWarps)
     router_backward_kernel(const __grid_constant__ RouterArgs a) {
-  extern __shared__ double smem_d[];
+  extern __shared__ double2 smem_d[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * PER;
   const long long tok = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
   if (tok >= a.n) return;
@@ -599,8 +727,8 @@ RouterArgs router_args(const moe_router_cfg* c, int dtype, long long n, long lon
   a.G = c->groups;
   a.TG = c->topk_groups;
   a.GT = c->group_top;
-  a.lpg = 1;
-  while (a.lpg * 2 * a.G <= 32) a.lpg *= 2;
+  while ((2 << a.lpg_log2) * a.G <= 32) ++a.lpg_log2;
+  a.lpg = 1 << a.lpg_log2;
   a.score = c->score;
   a.renorm = c->renorm;
   a.scale = c->scale;
@@ -614,7 +742,7 @@ template <int PER>
 void launch_router(const RouterArgs& a, cudaStream_t s) {
   const int warps = router_warps(a.E);
   const unsigned grid = (unsigned)((a.n + warps - 1) / warps);
-  const size_t smem = (size_t)warps * a.E * sizeof(double);
+  const size_t smem = (size_t)warps * kWarpBytes<PER>;
   if constexpr (PER <= 8) {
     if (a.E == 32 * PER && (a.G & (a.G - 1)) == 0) {
       router_kernel<PER, true><<<grid, 32 * warps, smem, s>>>(a);
