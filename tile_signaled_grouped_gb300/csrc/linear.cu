@@ -36,7 +36,8 @@ constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluC1 = 0.044715f;
 
 // act(z). 0.5 (1 + tanh u) is the sigmoid of 2u. The fast exponential and division are
-// within 1e-6, far below half a step of the 16-bit results (fp32 results: same bound).
+// within 1e-6 of themselves, far below half a step of a 16-bit result; an fp32 result is off
+// by that.
 template <int ACT>
 __device__ __forceinline__ float act_of(float z) {
   if (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
@@ -404,7 +405,9 @@ __device__ __forceinline__ void join(const GemmArgs& a, const float* dump, int r
 // One tile of 128 x bn for each cluster of `splits` CTAs, each of which sums its range of
 // k in its TMEM. The partial sums then meet in shared memory: every CTA adds a share of
 // the tile's elements from all of them, in the order of the ranks, and finishes it. Warp 0
-// loads, warp 1 issues the products, all eight warps empty TMEM.
+// loads, warp 1 issues the products, all eight warps empty TMEM. Bound by its start, the
+// pipeline's first loads and the end: 333 x 517 x 1000 takes 9 us, of which its products are at
+// most 16 steps of 0.2 us.
 template <bool AMN, bool BMN>
 __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_constant__ GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -546,7 +549,9 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
 // columns, so a 256 x 256 x 64 step loads 64 KB for the pair; the accumulators of two
 // tiles (2 x 256 columns of TMEM) alternate, so that eight epilogue warps empty one while
 // the next is summed. The pairs take tiles in turn; eight row tiles share a group of
-// columns, so the tiles in flight share their operands in L2.
+// columns, so the tiles in flight share their operands in L2. Bound by the tensor cores:
+// 8192 x 8192 x 2048 with both outputs takes 161 to 172 us (1.6 to 1.7 PFLOP/s), 8192^3 646 us
+// (1.7), both products of 4096^3 155 us (1.78).
 constexpr int kPairMaxStages = 8;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
@@ -913,8 +918,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // 2 t, 2 t + 1, 2 t + 8, 2 t + 9; both operands agree. `ks` warps share eight rows of the
 // weights, each with a range of k; their sums are added in the warps' order. CTAs walk the
 // rows of the weights, and the next batch of loads, of the next rows at the end of a row,
-// is on its way while a batch is multiplied. (16 rows of x in this form took 14 us for
-// 2048 x 7168, where the tiles take 12.)
+// is on its way while a batch is multiplied. One row by 2048 x 7168: 7.4 to 8.5 us (3.4 to
+// 4 TB/s, of which 2 us are the launch and its first loads); by 8192 x 8192: 26 us, 5.2 TB/s.
+// (16 rows of x in this form took 14 us for 2048 x 7168, where the tiles take 12.)
 constexpr int kRowsMax = 8;  // rows of x
 constexpr int kRowsWarps = 8;
 constexpr int kRowsUnroll = 8;  // steps of 32 k whose loads are in flight together
@@ -1056,8 +1062,9 @@ __device__ __forceinline__ void unpack8(const uint4& u, int dtype, float (&f)[8]
 // rounded to the operands' type for the products; the sums take it unrounded. Bound by the
 // bytes of dy, z and dz. VEC: rows on 16 bytes and N a multiple of 8; a thread takes eight
 // columns of four rows at a time, warp w rows 4 w .. of every 32, and all eight loads leave
-// before the first is used; the eight warps' sums are added in order. Otherwise a thread
-// takes one column, so that neighbouring threads read neighbouring elements.
+// before the first is used; the eight warps' sums are added in order: 10.9 us for 4096 x 1536
+// (3.5 TB/s; cold, under a profiler). Otherwise a thread takes one column, so that neighbouring
+// threads read neighbouring elements.
 constexpr int kActRows = 4;
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
@@ -1292,7 +1299,8 @@ int gemm_pair(const Product& g, bool bf16, int num_sms, cudaStream_t s) {
 long long share_tiles(const Product& first, const Product& second, int pairs, uint16_t (*live)[kPairRounds]) {
   const long long n0 = first.tiles256(), n1 = second.tiles256();
   if (n0 > (long long)pairs * kPairRounds || n1 > (long long)pairs * kPairRounds) return 0;
-  for (int k = 0; k < kPairRounds; ++k) live[0][k] = (uint16_t)std::max(0LL, std::min<long long>(pairs, n0 - (long long)k * pairs));
+  for (int k = 0; k < kPairRounds; ++k)
+    live[0][k] = (uint16_t)std::max(0LL, std::min<long long>(pairs, n0 - (long long)k * pairs));
   // Pairs 0 .. more - 1 have `rounds` tiles of the first product, the others one less; a group's
   // pairs get their tiles of the second together, the last time perhaps only some of them.
   const long long rounds = (n0 + pairs - 1) / pairs;
@@ -1339,7 +1347,8 @@ int gemm_rows(const moe_linear_args* p, const Epilogue& e, int num_sms, cudaStre
   // still make 1.4 CTAs for every SM, and where a warp would have less than a batch of k.
   const long long groups = (p->N + 7) / 8;
   a.ks = kRowsWarps;
-  while (a.ks > 1 && (p->K < 32LL * kRowsUnroll * a.ks || 10 * groups * (a.ks / 2) >= 14LL * num_sms * kRowsWarps))
+  while (a.ks > 1 && (p->K < 32LL * kRowsUnroll * a.ks ||
+                      10 * groups * (a.ks / 2) >= 14LL * num_sms * kRowsWarps))
     a.ks /= 2;
   const int per = kRowsWarps / a.ks;
   a.blocks = (p->N + 8 * per - 1) / (8 * per);
@@ -1357,9 +1366,9 @@ int gemm_rows(const moe_linear_args* p, const Epilogue& e, int num_sms, cudaStre
 // A step of 64 k takes a CTA 0.2 us, or what its bytes take at 165 GB/s an SM or 18 TB/s for
 // all; a pair's 256 x 256 x 64 takes 0.29 us. Starting, filling the pipeline and ending cost
 // 4 us (pairs: 7), an epilogue 0.1 us for 1000 elements (0.35 us where rows do not start on
-// 16 bytes; 7 us for a pair). Joining S partial tiles costs 1.5 us
-// and what S CTAs read from one another's shared memory at 16 GB/s each. Clusters of 1, 2, 4 and 8 of these CTAs: 152, 76,
-// 36 and 15 fit on the GPU at once.
+// 16 bytes; 7 us for a pair). Joining S partial tiles costs 1.5 us and what S CTAs read from
+// one another's shared memory at 16 GB/s each. Clusters of 1, 2, 4 and 8 of these CTAs: 152,
+// 76, 36 and 15 fit on the GPU at once.
 constexpr double kPairStart = 7.0, kPairStep = 0.29;
 struct TileChoice {
   int bn, splits;  // bn -1: the pair kernel
@@ -1369,7 +1378,8 @@ TileChoice choose_tiles(int I, int J, int nk, bool b_mn, bool aligned, int num_s
   const long long ti = (I + kTileI - 1) / kTileI;
   const long long t256 = ((long long)I + 255) / 256 * (((long long)J + 255) / 256);
   const long long pairs = num_sms / 2;
-  TileChoice best{-1, 1, kPairStart + (aligned ? 0.0 : 7.0) + (double)((t256 + pairs - 1) / pairs) * nk * kPairStep};
+  TileChoice best{-1, 1, kPairStart + (aligned ? 0.0 : 7.0) +
+                             (double)((t256 + pairs - 1) / pairs) * nk * kPairStep};
   const int rows = std::min(I, kTileI);
   for (int bn = b_mn ? 64 : 16; bn <= 256; bn *= 2) {
     if (bn < 64 && bn < J) continue;  // under 64 columns only for all of J
@@ -1377,7 +1387,10 @@ TileChoice choose_tiles(int I, int J, int nk, bool b_mn, bool aligned, int num_s
     const double bytes = (double)(rows + bn) * 128;
     for (int s = 1; s <= 8; s *= 2) {
       if (nk < 2 * s && s > 1) break;
-      const long long fit = s == 1 ? num_sms : s == 2 ? num_sms / 2 : s == 4 ? 36LL * num_sms / 152 : 15LL * num_sms / 152;
+      const long long fit = s == 1   ? num_sms
+                            : s == 2 ? num_sms / 2
+                            : s == 4 ? 36LL * num_sms / 152
+                                     : 15LL * num_sms / 152;
       const double waves = (double)((tiles + fit - 1) / std::max(1LL, fit));
       const double busy = (double)(std::min(tiles, fit) * s);
       const double step = std::max(0.2, std::max(bytes / 165e3, bytes * busy / 18e6));
@@ -1432,7 +1445,8 @@ int gemm_both(const Product& x, const Product& y, bool bf16, int num_sms, cudaSt
   const Product& second = x.nk() >= y.nk() ? y : x;
   const int pairs = pair_clusters(num_sms);
   PairArgs a;
-  const long long most = first.tiles256() + second.tiles256() >= pairs ? share_tiles(first, second, pairs, a.live) : 0;
+  const long long most =
+      first.tiles256() + second.tiles256() >= pairs ? share_tiles(first, second, pairs, a.live) : 0;
   const double apart = choose_tiles(x.I, x.J, x.nk(), x.B.mn, aligned_rows(x.e), num_sms).us +
                        choose_tiles(y.I, y.J, y.nk(), y.B.mn, aligned_rows(y.e), num_sms).us;
   if (most > 0 && kPairStart + (double)most * kPairStep < apart) {

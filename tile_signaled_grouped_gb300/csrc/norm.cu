@@ -4,8 +4,9 @@
 //   z = x + r,  mean = sum z / D,  var = sum (z - mean)^2 / D,  rstd = 1 / sqrt(var + eps)
 //   y = (z - mean) rstd w + b
 // z is kept in fp32 between the sum and the norm; y and the stored z are rounded once.
-// A row is read once into the registers of one to 32 warps (EPT elements a thread), so the variance is the sum of squared distances from the mean: no difference
-// of large sums. Bound by the bytes of the rows.
+// A row is read once into the registers of one to 32 warps (EPT elements a thread), so the
+// variance is the sum of squared distances from the mean: no difference of large sums. Bound
+// by the bytes of the rows.
 //
 // Backward, with xhat = (z - mean) rstd and g = dy w:
 //   dx = rstd (g - sum g / D - xhat sum(g xhat) / D) + dz
@@ -14,8 +15,9 @@
 // db in registers; the CTAs' sums go to the workspace, and a second kernel adds them in
 // a fixed order (no atomics: the same bits on every call).
 //
-// Rows longer than the registers hold are read three times (forward) or twice
-// (backward) by a CTA of 1024 threads.
+// Three forms: a row in registers (few rows), a ring of rows in shared memory (many), and rows
+// longer than the registers hold, which a CTA of 1024 threads reads three times (forward) or
+// twice (backward). One row of 7168 takes 3.9 us, 777 of 1531 in wider rows 5.2 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -83,7 +85,8 @@ __device__ __forceinline__ void load_row(const T* row, int first, int step, int 
   using W = typename Word<T, N>::type;
   W u[PERV];
 #pragma unroll
-  for (int i = 0; i < PERV; ++i) u[i] = load_word(reinterpret_cast<const W*>(row) + min(first + i * step, nv - 1));
+  for (int i = 0; i < PERV; ++i)
+    u[i] = load_word(reinterpret_cast<const W*>(row) + min(first + i * step, nv - 1));
 #pragma unroll
   for (int i = 0; i < PERV; ++i) {
     const bool in = live && first + i * step < nv;
@@ -399,7 +402,8 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
 // Rows of any length: each thread adds its columns' products to the CTA's sums in the
 // workspace (no other thread touches them).
 template <typename T, int N>
-__global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kLoopThreads)
+    norm_backward_long_kernel(const __grid_constant__ NormArgs a) {
   constexpr int P = N > 1 ? 1 : kLoopWords;
   __shared__ float red[2][64];
   allow_dependent_launch();
@@ -477,12 +481,14 @@ __global__ void __launch_bounds__(kLoopThreads) norm_backward_long_kernel(const 
 }
 
 // ------------------------------------------------------------------- ring kernels
-// Long matrices: persistent CTAs whose thread 0 keeps the next
-// rows coming in (bulk copies into a ring of shared memory), so that the loads never stop
-// for the reductions of a row: the kernels above only load between a CTA's start and its
-// first reduction (16384 x 4096 bf16 with a residual: 143 us against 95, 5.7 TB/s; backward
-// of 8192 x 7168: 257 us against 86, 5.5 TB/s). wpr warps share a row; a CTA holds as many
-// such groups as its warps allow, each with a ring of its own.
+// Long matrices: persistent CTAs whose groups of warps keep the next rows coming in (bulk copies
+// into a ring of shared memory), so that the loads never stop for the reductions of a row: the
+// kernels above only load between a CTA's start and its first reduction (16384 x 4096 bf16 with
+// a residual: 143 us against 93, 5.8 TB/s; backward of 8192 x 7168: 257 us against 84, 5.6 TB/s).
+// wpr warps share a row; a CTA holds as many such groups as its warps allow, each with a ring of
+// its own. Rows that start anywhere come as the 16-byte blocks that they touch, and vectors are
+// shifted together from two neighbours (8192 x 4097 fp16 with a residual: 230 us by the element
+// against 97, backward 239 against 141).
 constexpr int kMaxRing = 4;  // 2, 3, 4 and 8 stages measured within 2 %
 constexpr int kMaxGroups = 16;
 // Elements a thread. What a row costs beside its elements (waits, reductions, addresses:
@@ -552,7 +558,8 @@ struct Ring {
   __device__ __forceinline__ void load(int i, long long row) const {
     uint64_t* bar = &st->full[i];
     uint8_t* to = smem + (size_t)(i * mats()) * pitch();
-    const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.dy), *r = static_cast<const T*>(a.r);
+    const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.dy);
+    const T* r = static_cast<const T*>(a.r);
     uint8_t *to_dy = to + pitch(), *to_r = to + (BACK ? 2 : 1) * pitch();
     if constexpr (AL) {
       mbar_arrive_expect_tx(bar, bytes() * mats());
@@ -610,8 +617,8 @@ __device__ __forceinline__ void ring_end(const Ring<T, BACK, AL>& g, bool leader
 }
 
 // Two fp32 values in a register pair: one instruction works on both (the same roundings as
-// two). The backward kernel's arithmetic is in pairs (8192 x 7168: 89 -> 86 us, 2048 x 7168:
-// 36 -> 32 us); in the forward kernel they cost more registers than its 64 (90 -> 98 us).
+// two). Backward of 8192 x 7168: 89 -> 86 us, of 2048 x 7168: 36 -> 32 us. The pairs need more
+// registers: the forward kernel takes 128 a thread (with 64 they made it slower, 90 -> 98 us).
 struct F2 {
   unsigned long long v;
   __device__ __forceinline__ F2() {}
@@ -717,7 +724,8 @@ __device__ __forceinline__ void store_vecs(T* row, int v, int nv, int D, const u
     if (v < nv && joined && from + N <= D) {
       *reinterpret_cast<uint4*>(row + from) = b;
     } else if (v < nv) {
-      const uint4 src = make_uint4(joined ? b.x : u.x, joined ? b.y : u.y, joined ? b.z : u.z, joined ? b.w : u.w);
+      const uint4 src = make_uint4(joined ? b.x : u.x, joined ? b.y : u.y, joined ? b.z : u.z,
+                                   joined ? b.w : u.w);
       const T* e = reinterpret_cast<const T*>(&src);
       const int first = joined ? from : v * N, count = min(joined ? N : N - skip, D - first);
 #pragma unroll
@@ -883,7 +891,8 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
 }
 
 template <typename T, typename WT, int EPT, bool AL>
-__global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(32 * max_warps(EPT))
+    norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
   constexpr int N = Vec<T>::kN, PERV = EPT / N;
   allow_dependent_launch();
   extern __shared__ __align__(128) uint8_t ring_smem[];
@@ -926,7 +935,8 @@ __global__ void __launch_bounds__(32 * max_warps(EPT)) norm_backward_ring_kernel
     const uint4 *zs = g.stage(st, 0), *ds = g.stage(st, 1), *us = g.stage(st, 2);
     const uint32_t at_z = AL ? 0u : block_offset(static_cast<const T*>(a.x), a.ld_x, row);
     const uint32_t at_d = AL ? 0u : block_offset(static_cast<const T*>(a.dy), a.ld_dy, row);
-    const uint32_t at_u = AL || a.r == nullptr ? 0u : block_offset(static_cast<const T*>(a.r), a.ld_r, row);
+    const uint32_t at_u =
+        AL || a.r == nullptr ? 0u : block_offset(static_cast<const T*>(a.r), a.ld_r, row);
     const F2 minus_mean(-mean, -mean), rr(rstd, rstd);
     F2 xh[PERV][N / 2], d[PERV][N / 2];
     uint4 up[PERV];

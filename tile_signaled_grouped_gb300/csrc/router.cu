@@ -12,7 +12,8 @@
 // tokens: 16384 x 256 with a bias and 4 of 8 groups, k = 8, takes 16 us (1.1 TB/s of scores)
 // for 670 warp instructions a token: 75 to load, 75 for the scores, 55 to sort a lane's eight,
 // 125 for the groups, 20 a round, 50 to find the ids, 40 to judge how close the order is, 75
-// for the weights (1.7 us of it pass while the last tokens decided in 64 bits end). At few tokens by its chain of warp reductions: 3.2 us for one.
+// for the weights. 1.7 of the 16 us pass while the last tokens decided in 64 bits end. At few
+// tokens it is bound by its chain of warp reductions: 3.2 us for one.
 //
 // Which experts are chosen is decided as in 64 bits. The scores are computed in 32 bits
 // with a known error bound; where two neighbours in the order of the winners (or the
