@@ -118,6 +118,24 @@ def test_scores_within_a_rounding_are_decided_as_in_64_bits():
     check(l, torch.zeros(E).cuda(), 32, "sigmoid", 1, 1, 1, True, 1.0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("topk", [1, 4, 31, 32])
+def test_equal_scores_in_front_of_one_that_only_64_bits_tell_apart(dtype, topk):
+    """Scores that are all 1 in fp32: experts of equal logits come first in the order of fp32
+    and ids, at the border too, and the larger logits behind them have to be found."""
+    n, E = 64, 96
+    g = torch.Generator().manual_seed(14)
+    l = 20.0 + torch.randint(0, 3, (n, E), generator=g).float() * 4
+    l[: n // 2, : E // 2] = 20.0
+    l[0] = 20.0
+    l = l.to(DT[dtype]).cuda()
+    b = torch.zeros(E)
+    check(l, b.cuda(), topk, "sigmoid", 1, 1, 1, True, 1.0)
+    check(l, b.cuda(), topk, "sigmoid", 3, 2, 2, False, 1.0)
+    b[::7] = 2.0
+    check(l, b.cuda(), topk, "sigmoid", 1, 1, 1, False, 1.0)
+
+
 def test_biases_that_mask_and_large_ones():
     l, _ = draw(40, 48, "fp32", False, 5)
     b = torch.zeros(48)

@@ -582,26 +582,35 @@ __global__ void __launch_bounds__(32 * kRouterWarps, PER <= 8 ? 6 : 1)
   if (a.bias != nullptr) {
     // Neighbours of the order within their error, unless score and bias are equal (then
     // the ids decide, as they did).
-    const int ni = __shfl_down_sync(kAll, my_id, 1);
-    bool amb = false;
+    auto differ = [&] {
+      const int ni = __shfl_down_sync(kAll, my_id, 1);
+      return lane < 31 && (load_as_f32(row, a.dtype, my_id) != load_as_f32(row, a.dtype, ni) ||
+                           __ldg(a.bias + my_id) != __ldg(a.bias + ni));
+    };
+    bool close = false;
     if (lane < a.k) {
       const float x = slot[lane].x, y = lane + 1 < a.k ? slot[lane + 1].x : past;
-      amb = x - y <= 2.f * eps + 0x1p-22f * (fabsf(x) + fabsf(y));
-      if (amb && lane < 31)
-        amb = load_as_f32(row, a.dtype, my_id) != load_as_f32(row, a.dtype, ni) ||
-              __ldg(a.bias + my_id) != __ldg(a.bias + ni);
+      close = x - y <= 2.f * eps + 0x1p-22f * (fabsf(x) + fabsf(y));
     }
-    if (__any_sync(kAll, amb)) {
-      // Every candidate that may be among the k: those within the error of the k-th.
-      const float border = slot[a.k - 1].x;
-      const float low = border - (2.f * eps + 0x1p-21f * fabsf(border));
-      while (past >= low && rounds <= 32) round();
-      my_id = slot_id();
-      // Without a candidate in line, `rounds` counts the round that found none.
-      if (past >= low)
-        my_id = settle_all(a, row, kept, buf, lane);
-      else
-        my_id = settle_slots(a, row, my_id, min(rounds - 1, 32), lane);
+    const uint32_t pairs = __ballot_sync(kAll, close);
+    if (pairs != 0) {
+      const bool unlike = differ();
+      bool open_order = close && (unlike || lane == 31);
+      const uint32_t last = 1u << (a.k - 1);
+      if (__any_sync(kAll, open_order) || (pairs & last)) {
+        // Every candidate that may be among the k: those within the error of the k-th. Behind an
+        // equal one in line there may be one that differs.
+        const float border = slot[a.k - 1].x;
+        const float low = border - (2.f * eps + 0x1p-21f * fabsf(border));
+        while (past >= low && rounds <= 32) round();
+        my_id = slot_id();
+        const int m = min(rounds - 1, 32);  // `rounds` counts the one below `low`, or that found none
+        open_order |= differ() & (lane >= a.k - 1) & (lane + 1 < m);
+        if (past >= low)
+          my_id = settle_all(a, row, kept, buf, lane);
+        else if (__any_sync(kAll, open_order))
+          my_id = settle_slots(a, row, my_id, m, lane);
+      }
     }
   }
 
