@@ -66,10 +66,19 @@ __device__ __forceinline__ float act_grad(float z) {
   return 1.f;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cl_addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cl_addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_v4(uint32_t cl_addr, uint32_t x, uint32_t y, uint32_t z,
+                                              uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cl_addr), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+// The halves of a cluster barrier of every thread that orders no memory (a release costs 0.3 us here):
+// after it every CTA of the cluster has started.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ------------------------------------------------------------------- the epilogue
@@ -83,6 +92,11 @@ struct Epilogue {
   int vy, vz, vr;  // bytes on which every row starts: 32, 16 or 0 (any)
   bool vb;         // b starts on 16 bytes
 };
+
+// Whether every row of the outputs and the residual starts on 16 bytes.
+__host__ __device__ inline bool aligned_rows(const Epilogue& e) {
+  return e.vy != 0 && (e.z == nullptr || e.vz != 0) && (e.r == nullptr || e.vr != 0);
+}
 
 // Eight elements of a row from column j: in one or two 16-byte accesses where `vec` and
 // all eight are inside, else one by one.
@@ -216,6 +230,90 @@ __device__ __forceinline__ void finish8(const Epilogue& e, long long i, int j, i
   store8(e.y, e.ytype, i * e.ld_y + j, n, e.vy != 0, v);
 }
 
+// 32 sums of row i from column j, n of them inside the matrix, to the outputs: 32 bytes (a
+// sector) a store where the rows allow it.
+__device__ __forceinline__ void load32(const void* p, int dtype, long long at, float (&f)[32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float t[8];
+    load8(p, dtype, at + 8 * c, 8, true, t);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[8 * c + q] = t[q];
+  }
+}
+__device__ __forceinline__ void store32(void* p, int dtype, long long at, bool wide, const float (&f)[32]) {
+  if (dtype != MOE_FP32 && wide) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (dtype == MOE_BF16) {
+        w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+      } else {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    unsigned short* q = static_cast<unsigned short*>(p) + at;
+    st_global_v8(q, w);
+    st_global_v8(q + 16, w + 8);
+    return;
+  }
+  if (dtype == MOE_FP32 && wide) {
+    float* q = static_cast<float*>(p) + at;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) st_global_v8(q + 8 * c, reinterpret_cast<const uint32_t*>(f) + 8 * c);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float t[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t[q] = f[8 * c + q];
+    store8(p, dtype, at + 8 * c, 8, true, t);
+  }
+}
+template <int ACT>
+__device__ __forceinline__ void act32(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_of<ACT>(v[i]);
+}
+__device__ __forceinline__ void finish32(const Epilogue& e, long long i, int j, int n, float (&v)[32]) {
+  if (n < 32 || !e.vb) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (8 * c < n) {
+        float t[8], b[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) t[q] = v[8 * c + q];
+        bias8(e, j + 8 * c, n - 8 * c, b);
+        finish8(e, i, j + 8 * c, n - 8 * c, b, t);
+      }
+    }
+    return;
+  }
+  if (e.b != nullptr) {
+    float t[32];
+    load32(e.b, e.btype, j, t);
+#pragma unroll
+    for (int q = 0; q < 32; ++q) v[q] += t[q];
+  }
+  if (e.z != nullptr) store32(e.z, e.dtype, i * e.ld_z + j, e.vz >= 32, v);
+  switch (e.act) {  // the same for the whole grid
+    case MOE_ACT_RELU: act32<MOE_ACT_RELU>(v); break;
+    case MOE_ACT_GELU: act32<MOE_ACT_GELU>(v); break;
+    case MOE_ACT_GELU_TANH: act32<MOE_ACT_GELU_TANH>(v); break;
+    case MOE_ACT_SILU: act32<MOE_ACT_SILU>(v); break;
+    default: break;
+  }
+  if (e.r != nullptr) {
+    float t[32];
+    load32(e.r, e.dtype, i * e.ld_r + j, t);
+#pragma unroll
+    for (int q = 0; q < 32; ++q) v[q] += t[q];
+  }
+  store32(e.y, e.ytype, i * e.ld_y + j, e.vy >= 32, v);
+}
+
 // act of a value whose kind is known at run time.
 __device__ __forceinline__ float act_any(float z, int act) {
   switch (act) {
@@ -298,7 +396,8 @@ struct GemmArgs {
   Epilogue e;
   int I, J, nk;       // nk: 64-element blocks of k
   int bn;             // columns of a tile: 16, 32, 64, 128 or 256 (64 or more if B is MN-major)
-  int stages, splits; // splits: CTAs of a cluster that share a tile, each with a range of k
+  int stages, blocks; // blocks: of k in a stage, one or two
+  int splits, splits_log2;  // CTAs of a cluster that share a tile, each with a range of k
   int tiles_i, box_a; // box_a: rows of A's box (K-major)
   bool bf16;
 };
@@ -310,157 +409,150 @@ struct TileSmem {
   int abort;
 };
 
-size_t tile_smem_bytes(int bn, int stages) {
-  const size_t pipe = (size_t)stages * (kABytes + bn * 128);
-  const size_t dump = (size_t)kTileI * (bn + 4) * 4;
-  return 1024 + std::max(pipe, dump) + sizeof(TileSmem);
+__host__ __device__ constexpr size_t part_bytes(int bn) { return (size_t)kTileI * (bn + 4) * 4; }
+// The sums of a split tile come from other CTAs, whose products may be done before this one's:
+// they have memory of their own.
+__host__ __device__ inline size_t tile_pipe_bytes(int bn, int blocks, int stages, int splits) {
+  const size_t pipe = (size_t)stages * blocks * (kABytes + bn * 128);
+  return splits > 1 ? pipe + part_bytes(bn) : pipe > part_bytes(bn) ? pipe : part_bytes(bn);
 }
 
-// This CTA's share of a tile's elements: the partial sums of all S CTAs of the cluster, added
-// in the order of the ranks, through the epilogue. A thread keeps to eight columns, whose
-// bias it has, and takes every (256 S / chunks)-th row; a row's loads from all S are in flight
-// together, since shared memory of another CTA is far away.
+// This CTA's rows of a tile, `own` of them: rank, rank + S, ... The partial sums that all S CTAs
+// of the cluster left in `part` ([S][128 / S][bn + 4]) are added in the order of the ranks and go
+// through the epilogue. A thread keeps to eight columns, whose bias it has.
 template <int S>
-__device__ __forceinline__ void join_tile(const GemmArgs& a, const float* dump, int rank, int rows, int i0,
+__device__ __forceinline__ void join_tile(const GemmArgs& a, const float* part, int rank, int own, int i0,
                                           int j, int c, const float (&bias)[8]) {
-  constexpr int U = S <= 2 ? 2 : 1;
-  const int chunks = a.bn / 8, pitch = a.bn + 4, each = kTileThreads / chunks;
+  constexpr int U = 2;
+  const int chunks = a.bn / 8, pitch = a.bn + 4, each = kTileThreads / chunks, from = kTileI / S * pitch;
   const int n = a.J - j;
   if (n <= 0) return;
-  uint32_t base[S];
-#pragma unroll
-  for (int r = 0; r < S; ++r) base[r] = S > 1 ? map_shared(dump, (uint32_t)r) : 0u;
-  for (int row0 = rank * each + (int)threadIdx.x / chunks; row0 < rows; row0 += U * S * each) {
-    float4 s[U][S], t[U][S];
+  for (int row0 = (int)threadIdx.x / chunks; row0 < own; row0 += U * each) {
+    float v[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = min(row0 + u * S * each, rows - 1) * pitch + c;
+      const float* at = part + min(row0 + u * each, own - 1) * pitch + c;
 #pragma unroll
       for (int r = 0; r < S; ++r) {
-        if (S == 1) {
-          s[u][r] = *reinterpret_cast<const float4*>(dump + at);
-          t[u][r] = *reinterpret_cast<const float4*>(dump + at + 4);
-        } else {
-          s[u][r] = ld_cluster_v4(base[r] + at * 4);
-          t[u][r] = ld_cluster_v4(base[r] + at * 4 + 16);
-        }
+        const float4 s = *reinterpret_cast<const float4*>(at + r * from);
+        const float4 t = *reinterpret_cast<const float4*>(at + r * from + 4);
+        const float w[8] = {s.x, s.y, s.z, s.w, t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[u][x] = r == 0 ? w[x] : v[u][x] + w[x];
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = row0 + u * S * each;
-      if (row >= rows) break;
-      float v[8] = {s[u][0].x, s[u][0].y, s[u][0].z, s[u][0].w, t[u][0].x, t[u][0].y, t[u][0].z, t[u][0].w};
-#pragma unroll
-      for (int r = 1; r < S; ++r) {
-        v[0] += s[u][r].x, v[1] += s[u][r].y, v[2] += s[u][r].z, v[3] += s[u][r].w;
-        v[4] += t[u][r].x, v[5] += t[u][r].y, v[6] += t[u][r].z, v[7] += t[u][r].w;
-      }
-      finish8(a.e, i0 + row, j, n, bias, v);
-    }
+    for (int u = 0; u < U; ++u)
+      if (row0 + u * each < own)
+        finish8(a.e, i0 + rank + (long long)S * (row0 + u * each), j, n, bias, v[u]);
   }
 }
 
 // The same where rows do not start on 16 bytes: neighbouring threads take neighbouring
 // columns, eight elements a thread at a time.
 template <int S>
-__device__ __forceinline__ void join_tile_any(const GemmArgs& a, const float* dump, int rank, int rows,
+__device__ __forceinline__ void join_tile_any(const GemmArgs& a, const float* part, int rank, int own,
                                               int i0, int j0) {
-  const int pitch = a.bn + 4, total = rows * a.bn, shift = 31 - __clz(a.bn);
-  uint32_t base[S];
-#pragma unroll
-  for (int r = 0; r < S; ++r) base[r] = map_shared(dump, (uint32_t)r);
-  for (int it = rank * kTileThreads + (int)threadIdx.x; it < total; it += 8 * S * kTileThreads) {
+  const int pitch = a.bn + 4, total = own * a.bn, shift = 31 - __clz(a.bn), from = kTileI / S * pitch;
+  for (int it = (int)threadIdx.x; it < total; it += 8 * kTileThreads) {
     float v[8], r[8];
     long long i[8], j[8];
     uint32_t mask = 0;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int x = min(it + u * S * kTileThreads, total - 1), c = x & (a.bn - 1), row = x >> shift;
-      const int at = (row * pitch + c) * 4;
-      mask |= (it + u * S * kTileThreads < total && j0 + c < a.J) ? 1u << u : 0u;
-      i[u] = i0 + row;
+      const int x = min(it + u * kTileThreads, total - 1), c = x & (a.bn - 1), row = x >> shift;
+      const float* at = part + row * pitch + c;
+      mask |= (it + u * kTileThreads < total && j0 + c < a.J) ? 1u << u : 0u;
+      i[u] = i0 + rank + (long long)S * row;
       j[u] = min(j0 + c, a.J - 1);
       r[u] = a.e.r != nullptr ? load_as_f32(a.e.r, a.e.dtype, i[u] * a.e.ld_r + j[u]) : 0.f;
       v[u] = a.e.b != nullptr ? load_as_f32(a.e.b, a.e.btype, j[u]) : 0.f;
-      float s[S];
+      float sum = at[0];
 #pragma unroll
-      for (int q = 0; q < S; ++q) s[q] = ld_cluster_f32(base[q] + at);
-#pragma unroll
-      for (int q = 1; q < S; ++q) s[0] += s[q];
-      v[u] += s[0];
+      for (int q = 1; q < S; ++q) sum += at[q * from];
+      v[u] += sum;
     }
     finish_scattered(a.e, i, j, mask, r, v);
   }
 }
 template <int S>
-__device__ __forceinline__ void join(const GemmArgs& a, const float* dump, int rank, int rows, int i0, int j0,
+__device__ __forceinline__ void join(const GemmArgs& a, const float* part, int rank, int own, int i0, int j0,
                                      int c0, const float (&bias)[8]) {
-  if (a.e.vy != 0 && (a.e.z == nullptr || a.e.vz != 0) && (a.e.r == nullptr || a.e.vr != 0))
-    join_tile<S>(a, dump, rank, rows, i0, j0 + c0, c0, bias);
+  if (aligned_rows(a.e))
+    join_tile<S>(a, part, rank, own, i0, j0 + c0, c0, bias);
   else
-    join_tile_any<S>(a, dump, rank, rows, i0, j0);
+    join_tile_any<S>(a, part, rank, own, i0, j0);
 }
 
 // One tile of 128 x bn for each cluster of `splits` CTAs, each of which sums its range of
-// k in its TMEM. The partial sums then meet in shared memory: every CTA adds a share of
-// the tile's elements from all of them, in the order of the ranks, and finishes it. Warp 0
+// k in its TMEM. The partial sums of a row then meet in the shared memory of one of them, which
+// adds them in the order of the ranks and finishes the row. Warp 0
 // loads, warp 1 issues the products, all eight warps empty TMEM. Bound by its start, the
-// pipeline's first loads and the end: 333 x 517 x 1000 takes 9 us, of which its products are at
-// most 16 steps of 0.2 us.
+// pipeline's first loads and the end: 333 x 517 x 1000 takes 6.6 us, 512 x 1024 x 1024 6.1 us, of
+// which its products are 16 steps of 0.16 us. The CTA that finishes a row gets all its sums by
+// stores, and no CTA waits for the others to have read: joining took 2.9 us where it takes 2.2
+// (64 x 1024 x 1024 in four parts) as reads of the others' memory between two barriers.
 template <bool AMN, bool BMN>
 __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_constant__ GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  const int b_bytes = a.bn * 128, stage_bytes = kABytes + b_bytes;
-  const size_t pipe = max((size_t)a.stages * stage_bytes, (size_t)kTileI * (a.bn + 4) * 4);
-  TileSmem& sm = *reinterpret_cast<TileSmem*>(base + pipe);
-  float* dump = reinterpret_cast<float*>(base);  // [128][bn + 4], once the products are done
+  const int b_bytes = a.bn * 128, block_bytes = kABytes + b_bytes, stage_bytes = a.blocks * block_bytes;
+  TileSmem& sm = *reinterpret_cast<TileSmem*>(base + tile_pipe_bytes(a.bn, a.blocks, a.stages, a.splits));
+  // Partial sums, [splits][128 / splits][bn + 4]; where the tile is not split, once the products are done.
+  float* part = reinterpret_cast<float*>(base + (a.splits > 1 ? (size_t)a.stages * stage_bytes : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t cols = a.bn < 32 ? 32 : a.bn;
-  const int rank = (int)(blockIdx.x % a.splits), tile = (int)(blockIdx.x / a.splits);
-  const int i0 = (tile % a.tiles_i) * kTileI, j0 = (tile / a.tiles_i) * a.bn;
-  const int k_lo = (int)((long long)a.nk * rank / a.splits);
-  const int k_hi = (int)((long long)a.nk * (rank + 1) / a.splits);
+  // (No 64-bit divisions and no loop of one thread here: they took 0.4 us of every launch.)
+  const uint32_t rank = blockIdx.x & (uint32_t)(a.splits - 1), tile = blockIdx.x >> a.splits_log2;
+  const uint32_t tj = tile / (uint32_t)a.tiles_i;
+  const int i0 = (int)(tile - tj * (uint32_t)a.tiles_i) * kTileI, j0 = (int)tj * a.bn;
+  const int k_lo = (int)(((long long)a.nk * rank) >> a.splits_log2);
+  const int k_hi = (int)(((long long)a.nk * (rank + 1)) >> a.splits_log2);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+  if (warp == 0) {
+    if (lane < a.stages) {
+      mbar_init(&sm.full[lane], 1);
+      mbar_init(&sm.empty[lane], 1);
     }
-    mbar_init(&sm.done, 1);
+    if (lane == 31) {
+      mbar_init(&sm.done, 1);
+      sm.abort = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    sm.abort = 0;
   }
   if (warp == 1) tmem_alloc(&sm.tmem, cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  if (a.splits > 1) cluster_arrive();  // waited for before this CTA writes to the others
   wait_prior_grid();  // behind a kernel that allows it, all of the above ran beside that one
 
   if (warp == 0) {
     const uint32_t bytes = (AMN ? kABytes : a.box_a * 128) + b_bytes;
     int issued = 0, st = 0;
     uint32_t phase = 1;
-    for (int kb = k_lo; kb < k_hi; ++kb, ++issued) {
+    for (int kb = k_lo; kb < k_hi; kb += a.blocks, ++issued) {
       if (!warp_wait(&sm.empty[st], phase, &sm.abort, 0x01000000u)) break;
       if (elect_one()) {
         uint8_t* as = base + (size_t)st * stage_bytes;
-        uint8_t* bs = as + kABytes;
-        mbar_arrive_expect_tx(&sm.full[st], bytes);
-        if (AMN) {
-          tma_load_2d(as, &a.ta, &sm.full[st], i0, kb * kBlockK);
-          tma_load_2d(as + 8192, &a.ta, &sm.full[st], i0 + 64, kb * kBlockK);
-        } else {
-          tma_load_2d(as, &a.ta, &sm.full[st], kb * kBlockK, i0);
-        }
-        if (BMN) {
-          for (int c = 0; c < a.bn / 64; ++c)
-            tma_load_2d(bs + c * 8192, &a.tb, &sm.full[st], j0 + c * 64, kb * kBlockK);
-        } else {
-          tma_load_2d(bs, &a.tb, &sm.full[st], kb * kBlockK, j0);
+        const int n = min(a.blocks, k_hi - kb);
+        mbar_arrive_expect_tx(&sm.full[st], n * bytes);
+        for (int k = kb; k < kb + n; ++k, as += block_bytes) {
+          uint8_t* bs = as + kABytes;
+          if (AMN) {
+            tma_load_2d(as, &a.ta, &sm.full[st], i0, k * kBlockK);
+            tma_load_2d(as + 8192, &a.ta, &sm.full[st], i0 + 64, k * kBlockK);
+          } else {
+            tma_load_2d(as, &a.ta, &sm.full[st], k * kBlockK, i0);
+          }
+          if (BMN) {
+            for (int c = 0; c < a.bn / 64; ++c)
+              tma_load_2d(bs + c * 8192, &a.tb, &sm.full[st], j0 + c * 64, k * kBlockK);
+          } else {
+            tma_load_2d(bs, &a.tb, &sm.full[st], k * kBlockK, j0);
+          }
         }
       }
       __syncwarp();
@@ -480,13 +572,19 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
     constexpr uint32_t step_a = (AMN ? 2048 : 32) >> 4, step_b = (BMN ? 2048 : 32) >> 4;
     int st = 0;
     uint32_t phase = 0, accumulate = 0, at = 0;  // at: the stage's offset in 16-byte units
-    for (int kb = k_lo; kb < k_hi; ++kb) {
+    for (int kb = k_lo; kb < k_hi; kb += a.blocks) {
       if (!warp_wait(&sm.full[st], phase, &sm.abort, 0x03000000u)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kBlockK / 16; ++k)
           tc_mma(tmem, da + at + k * step_a, db + at + k * step_b, idesc, k != 0 ? 1u : accumulate);
+        if (a.blocks == 2 && kb + 1 < k_hi) {
+          const uint32_t bt = at + (block_bytes >> 4);
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            tc_mma(tmem, da + bt + k * step_a, db + bt + k * step_b, idesc, 1u);
+        }
         tc_commit(&sm.empty[st]);
       }
       __syncwarp();
@@ -505,42 +603,65 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
   volatile int never = 0;
   bool ok = mbar_wait_bounded(&sm.done, 0, &never, 2 * kWaitNs, g_status, 0x04000000u);
   ok = ok && *(volatile int*)&sm.abort == 0;
+  __syncwarp();
   tc_fence_after();
 
-  // TMEM to shared memory: warp w reads lanes 32 (w & 3).. of column half w >> 2.
+  // Warp w reads lanes 32 (w & 3).. of TMEM, of column half w >> 2.
   const int rows = min(kTileI, a.I - i0);
-  const int pitch = a.bn + 4;
-  __syncthreads();  // every wait above is over: the pipeline's memory is free
-  {
-    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
-    for (int c = half * 32; c < a.bn; c += 64) {
+  if (a.splits == 1 && aligned_rows(a.e)) {  // straight to the outputs
+    const int q = warp & 3, row = q * 32 + lane;
+    for (int c = (warp >> 2) * 32; c < a.bn; c += 64) {
       uint32_t v[32];
       tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, v);
       tmem_ld_wait();
-      if (row < rows && k_hi > k_lo) {
+      float f[32];
+#pragma unroll
+      for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
+      const int n = min(a.bn - c, a.J - j0 - c);
+      if (ok && row < rows && n > 0) finish32(a.e, i0 + row, j0 + c, n, f);
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, cols);
+    return;
+  }
+  // TMEM to the memory of the CTA that finishes the row, whose wait is not one for its products.
+  if (a.splits > 1)
+    cluster_wait();
+  else
+    __syncthreads();  // every wait above is over: the pipeline's memory is free
+  const int pitch = a.bn + 4;
+  {
+    const int row = (warp & 3) * 32 + lane, owner = row & (a.splits - 1);
+    const int at = ((int)rank * (kTileI >> a.splits_log2) + (row >> a.splits_log2)) * pitch;
+    const uint32_t to = (a.splits > 1 ? map_shared(part, (uint32_t)owner) : smem_u32(part)) + at * 4;
+    for (int c = (warp >> 2) * 32; c < a.bn; c += 64) {
+      uint32_t v[32];
+      tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
+      tmem_ld_wait();
+      if (row < rows) {
 #pragma unroll
         for (int x = 0; x < 32; x += 4)
-          if (c + x < a.bn)
-            *reinterpret_cast<uint4*>(dump + (size_t)row * pitch + c + x) =
-                make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+          if (c + x < a.bn) st_cluster_v4(to + (c + x) * 4, v[x], v[x + 1], v[x + 2], v[x + 3]);
       }
+      __syncwarp();
     }
   }
   tc_fence_before();
   __syncthreads();
   if (a.splits > 1) cluster_sync_all();
-  if (ok) {
-    switch (a.splits) {
-      case 1: join<1>(a, dump, rank, rows, i0, j0, c0, bias); break;
-      case 2: join<2>(a, dump, rank, rows, i0, j0, c0, bias); break;
-      case 4: join<4>(a, dump, rank, rows, i0, j0, c0, bias); break;
-      default: join<8>(a, dump, rank, rows, i0, j0, c0, bias); break;
-    }
-  }
-  __syncthreads();
-  if (a.splits > 1) cluster_sync_all();  // the others have read this CTA's sums
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, cols);
+  if (!ok) return;
+  const int own = (rows - (int)rank + a.splits - 1) >> a.splits_log2;
+  switch (a.splits) {
+    case 1: join_tile_any<1>(a, part, 0, own, i0, j0); break;
+    case 2: join<2>(a, part, rank, own, i0, j0, c0, bias); break;
+    case 4: join<4>(a, part, rank, own, i0, j0, c0, bias); break;
+    default: join<8>(a, part, rank, own, i0, j0, c0, bias); break;
+  }
 }
 
 // ------------------------------------------------------------------- CTA pairs
@@ -635,90 +756,6 @@ struct PairWalk {
     return true;
   }
 };
-
-// 32 sums of row i from column j, n of them inside the matrix, to the outputs: 32 bytes (a
-// sector) a store where the rows allow it.
-__device__ __forceinline__ void load32(const void* p, int dtype, long long at, float (&f)[32]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float t[8];
-    load8(p, dtype, at + 8 * c, 8, true, t);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) f[8 * c + q] = t[q];
-  }
-}
-__device__ __forceinline__ void store32(void* p, int dtype, long long at, bool wide, const float (&f)[32]) {
-  if (dtype != MOE_FP32 && wide) {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (dtype == MOE_BF16) {
-        w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-      } else {
-        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
-    unsigned short* q = static_cast<unsigned short*>(p) + at;
-    st_global_v8(q, w);
-    st_global_v8(q + 16, w + 8);
-    return;
-  }
-  if (dtype == MOE_FP32 && wide) {
-    float* q = static_cast<float*>(p) + at;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) st_global_v8(q + 8 * c, reinterpret_cast<const uint32_t*>(f) + 8 * c);
-    return;
-  }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float t[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) t[q] = f[8 * c + q];
-    store8(p, dtype, at + 8 * c, 8, true, t);
-  }
-}
-template <int ACT>
-__device__ __forceinline__ void act32(float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_of<ACT>(v[i]);
-}
-__device__ __forceinline__ void finish32(const Epilogue& e, long long i, int j, int n, float (&v)[32]) {
-  if (n < 32 || !e.vb) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (8 * c < n) {
-        float t[8], b[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) t[q] = v[8 * c + q];
-        bias8(e, j + 8 * c, n - 8 * c, b);
-        finish8(e, i, j + 8 * c, n - 8 * c, b, t);
-      }
-    }
-    return;
-  }
-  if (e.b != nullptr) {
-    float t[32];
-    load32(e.b, e.btype, j, t);
-#pragma unroll
-    for (int q = 0; q < 32; ++q) v[q] += t[q];
-  }
-  if (e.z != nullptr) store32(e.z, e.dtype, i * e.ld_z + j, e.vz >= 32, v);
-  switch (e.act) {  // the same for the whole grid
-    case MOE_ACT_RELU: act32<MOE_ACT_RELU>(v); break;
-    case MOE_ACT_GELU: act32<MOE_ACT_GELU>(v); break;
-    case MOE_ACT_GELU_TANH: act32<MOE_ACT_GELU_TANH>(v); break;
-    case MOE_ACT_SILU: act32<MOE_ACT_SILU>(v); break;
-    default: break;
-  }
-  if (e.r != nullptr) {
-    float t[32];
-    load32(e.r, e.dtype, i * e.ld_r + j, t);
-#pragma unroll
-    for (int q = 0; q < 32; ++q) v[q] += t[q];
-  }
-  store32(e.y, e.ytype, i * e.ld_y + j, e.vy >= 32, v);
-}
 
 // A warp's 32 x 32 sums (lane l has row l), `rows` x n of them inside the matrix, where rows do
 // not start on 16 bytes: turned round in shared memory, so that the lanes are neighbouring
@@ -920,7 +957,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // rows of the weights, and the next batch of loads, of the next rows at the end of a row,
 // is on its way while a batch is multiplied. One row by 2048 x 7168: 7.4 to 8.5 us (3.4 to
 // 4 TB/s, of which 2 us are the launch and its first loads); by 8192 x 8192: 26 us, 5.2 TB/s.
-// (16 rows of x in this form took 14 us for 2048 x 7168, where the tiles take 12.)
+// (16 rows of x in this form took 14 us for 2048 x 7168, where the tiles take 9.4.)
 constexpr int kRowsMax = 8;  // rows of x
 constexpr int kRowsWarps = 8;
 constexpr int kRowsUnroll = 8;  // steps of 32 k whose loads are in flight together
@@ -1209,7 +1246,8 @@ cudaError_t launch_tile(const GemmArgs& a, int tiles, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * a.splits));
   cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = tile_smem_bytes(a.bn, a.stages);
+  cfg.dynamicSmemBytes =
+      1024 + tile_pipe_bytes(a.bn, a.blocks, a.stages, a.splits) + sizeof(TileSmem);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1250,10 +1288,6 @@ struct Product {
   int nk() const { return (int)((K + kBlockK - 1) / kBlockK); }
   long long tiles256() const { return ((long long)I + 255) / 256 * (((long long)J + 255) / 256); }
 };
-
-bool aligned_rows(const Epilogue& e) {
-  return e.vy != 0 && (e.z == nullptr || e.vz != 0) && (e.r == nullptr || e.vr != 0);
-}
 
 bool pair_product(const Product& g, bool bf16, PairProduct* p) {
   p->e = g.e;
@@ -1363,12 +1397,13 @@ int gemm_rows(const moe_linear_args* p, const Epilogue& e, int num_sms, cudaStre
 // Which kernel and tiles take a product: the least of an estimate in microseconds, fitted to
 // measurements of 16 to 1024 rows at 2048 x 7168, 8192 x 2048, 1536 x 4096, 4096 x 1024 and
 // 512 x 1000 (within 20 % of them, and its choice within 10 % of the best there).
-// A step of 64 k takes a CTA 0.2 us, or what its bytes take at 165 GB/s an SM or 18 TB/s for
-// all; a pair's 256 x 256 x 64 takes 0.29 us. Starting, filling the pipeline and ending cost
-// 4 us (pairs: 7), an epilogue 0.1 us for 1000 elements (0.35 us where rows do not start on
-// 16 bytes; 7 us for a pair). Joining S partial tiles costs 1.5 us and what S CTAs read from
-// one another's shared memory at 16 GB/s each. Clusters of 1, 2, 4 and 8 of these CTAs: 152,
-// 76, 36 and 15 fit on the GPU at once.
+// A step of 64 k takes a CTA 0.155 us up to 64 columns, 0.225 for 128 (0.29 with one block of k a
+// stage) and 0.34 for 256, or what all CTAs' bytes take at 18 TB/s; a pair's 256 x 256 x 64 takes
+// 0.29 us. Starting, filling the pipeline and the last products take 2 us (pairs, with their end:
+// 7), an epilogue 0.4 us and 0.05 us for 1000 elements (0.35 us where rows do not start on 16
+// bytes; 7 us for a pair). Joining S partial tiles costs 1.4 us and what a CTA's sums take to the
+// others at 22 GB/s.
+// Clusters of 1, 2, 4 and 8 of these CTAs: 152, 76, 36 and 15 fit on the GPU at once.
 constexpr double kPairStart = 7.0, kPairStep = 0.29;
 struct TileChoice {
   int bn, splits;  // bn -1: the pair kernel
@@ -1386,17 +1421,19 @@ TileChoice choose_tiles(int I, int J, int nk, bool b_mn, bool aligned, int num_s
     const long long tiles = ti * ((J + bn - 1) / bn);
     const double bytes = (double)(rows + bn) * 128;
     for (int s = 1; s <= 8; s *= 2) {
-      if (nk < 2 * s && s > 1) break;
+      if (s > 1 && (nk < 2 * s || bn > 128)) break;  // 256 columns leave no room for the sums
       const long long fit = s == 1   ? num_sms
                             : s == 2 ? num_sms / 2
                             : s == 4 ? 36LL * num_sms / 152
                                      : 15LL * num_sms / 152;
       const double waves = (double)((tiles + fit - 1) / std::max(1LL, fit));
       const double busy = (double)(std::min(tiles, fit) * s);
-      const double step = std::max(0.2, std::max(bytes / 165e3, bytes * busy / 18e6));
-      const double join = (s == 1 ? 0.0 : 1.5 + (double)rows * bn * 4 / 16e3) +
-                          rows * bn * (aligned ? s == 1 ? 1e-4 : 0.0 : 3.5e-4) / s;
-      const double us = 4.0 + waves * (step * ((nk + s - 1) / s) + join);
+      const double step = std::max(bn <= 64 ? 0.155 : bn == 256 ? 0.34 : s == 1 ? 0.225 : 0.29,
+                                   bytes * busy / 18e6);
+      const double join = (s == 1 ? 0.4 + (aligned ? rows * bn * 5e-5 : 0.0)
+                                  : 1.4 + (double)rows * bn * 4 / 22e3) +
+                          (aligned ? 0.0 : rows * bn * 3.5e-4 / s);
+      const double us = 2.0 + waves * (step * ((nk + s - 1) / s) + join);
       if (us < best.us) best = TileChoice{bn, s, us};
     }
     if (bn >= J && bn >= 64) break;
@@ -1410,7 +1447,7 @@ int gemm(const Product& g, bool bf16, int num_sms, cudaStream_t s) {
   const long long K = g.K;
   const TileChoice tc = choose_tiles(I, J, nk, B.mn, aligned_rows(g.e), num_sms);
   if (tc.bn < 0) return gemm_pair(g, bf16, num_sms, s);
-  GemmArgs a;
+  GemmArgs a{};
   a.e = g.e;
   a.I = I;
   a.J = J;
@@ -1421,7 +1458,12 @@ int gemm(const Product& g, bool bf16, int num_sms, cudaStream_t s) {
   a.splits = tc.splits;
   const long long tiles = (long long)a.tiles_i * ((J + a.bn - 1) / a.bn);
   if (tiles * a.splits > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  a.stages = std::min<int>(kMaxStages, (int)((kSmemMax - 1024 - sizeof(TileSmem)) / (kABytes + a.bn * 128)));
+  while (1 << a.splits_log2 < a.splits) ++a.splits_log2;
+  // Two blocks of k a stage share what a step of the single threads costs (0.27 us for a block of
+  // 128 x 64 alone, 0.155 in pairs), where three such stages fit.
+  a.blocks = a.bn <= (a.splits > 1 ? 64 : 128) ? 2 : 1;
+  const size_t room = kSmemMax - 1024 - sizeof(TileSmem) - (a.splits > 1 ? part_bytes(a.bn) : 0);
+  a.stages = (int)std::min<size_t>(kMaxStages, room / (a.blocks * (kABytes + a.bn * 128)));
   a.box_a = std::min(kTileI, (I + 7) / 8 * 8);
   const bool ok = (A.mn ? make_map(&a.ta, A.p, bf16, K, I, A.ld, kBlockK)
                         : make_map(&a.ta, A.p, bf16, I, K, A.ld, a.box_a)) &&
