@@ -757,6 +757,30 @@ struct PairWalk {
   }
 };
 
+// n of eight values of one column, ld elements apart: the addresses are a running sum, and where all
+// eight are inside no store has a condition (finish_scattered, with both for each element, took 4
+// to 6 % longer for 1431 and 4096 rows of 7893).
+template <typename T>
+__device__ __forceinline__ void store_column(T* p, long long ld, int n, const float (&f)[8]) {
+  if (n >= 8) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q, p += ld) *p = from_f32<T>(f[q]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q, p += ld)
+      if (q < n) *p = from_f32<T>(f[q]);
+  }
+}
+__device__ __forceinline__ void store_column(void* p, int dtype, long long at, long long ld, int n,
+                                             const float (&f)[8]) {
+  if (dtype == MOE_FP32)
+    store_column(static_cast<float*>(p) + at, ld, n, f);
+  else if (dtype == MOE_BF16)
+    store_column(static_cast<__nv_bfloat16*>(p) + at, ld, n, f);
+  else
+    store_column(static_cast<__half*>(p) + at, ld, n, f);
+}
+
 // A warp's 32 x 32 sums (lane l has row l), `rows` x n of them inside the matrix, where rows do
 // not start on 16 bytes: turned round in shared memory, so that the lanes are neighbouring
 // columns of one row. (Without it, 34 us for a tile.)
@@ -767,19 +791,23 @@ __device__ __forceinline__ void finish_patch(const Epilogue& e, float* patch, lo
   for (int x = 0; x < 32; ++x) patch[lane * kPatchPitch + x] = v[x];
   __syncwarp();
   if (lane >= n) return;
-  const float bias = e.b != nullptr ? load_as_f32(e.b, e.btype, j + lane) : 0.f;
+  const long long c = j + lane;
+  const float bias = e.b != nullptr ? load_as_f32(e.b, e.btype, c) : 0.f;
   for (int r0 = 0; r0 < rows; r0 += 8) {
+    const long long i = i0 + r0;
+    const int m = rows - r0;
     float f[8], t[8];
-    long long i[8], c[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int row = min(r0 + r, rows - 1);
-      i[r] = i0 + row;
-      c[r] = j + lane;
-      t[r] = e.r != nullptr ? load_as_f32(e.r, e.dtype, i[r] * e.ld_r + c[r]) : 0.f;
-      f[r] = patch[row * kPatchPitch + lane] + bias;
+      const int row = min(r, m - 1);
+      t[r] = e.r != nullptr ? load_as_f32(e.r, e.dtype, (i + row) * e.ld_r + c) : 0.f;
+      f[r] = patch[(r0 + row) * kPatchPitch + lane] + bias;
     }
-    finish_scattered(e, i, c, (1u << min(8, rows - r0)) - 1u, t, f);
+    if (e.z != nullptr) store_column(e.z, e.dtype, i * e.ld_z + c, e.ld_z, m, f);
+    act8_any(f, e.act);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) f[r] += t[r];
+    store_column(e.y, e.ytype, i * e.ld_y + c, e.ld_y, m, f);
   }
 }
 
