@@ -273,49 +273,12 @@ def moe_set_schedule(plan, consumer_ctas: int, mgb: int):
     check(lib().moe_set_schedule(plan, consumer_ctas, mgb), "moe_set_schedule")
 
 
-def moe_router(plan, cfg: moe_router_cfg, logits, dtype, n, ld, bias, ids, w, stream):
-    rc = lib().moe_router(plan, cfg, logits, dtype, n, ld, bias, ids, w, stream)
-    if rc:
-        check(rc, "moe_router")
-
-
-def moe_router_backward(cfg: moe_router_cfg, d_w, logits, ids, dtype, n, ld, d_logits, ld_d, stream):
-    rc = lib().moe_router_backward(cfg, d_w, logits, ids, dtype, n, ld, d_logits,
-                                    ld_d, stream)
-    if rc:
-        check(rc, "moe_router_backward")
-
-
-def moe_layer_norm(args: moe_norm_args, stream):
-    rc = lib().moe_layer_norm(args, stream)
-    if rc:
-        check(rc, "moe_layer_norm")
-
-
 def moe_layer_norm_workspace(n: int, D: int) -> int:
     return lib().moe_layer_norm_workspace(n, D)
 
 
-def moe_layer_norm_backward(args: moe_norm_args, workspace, workspace_bytes, stream):
-    rc = lib().moe_layer_norm_backward(args, workspace, workspace_bytes, stream)
-    if rc:
-        check(rc, "moe_layer_norm_backward")
-
-
-def moe_linear(args: moe_linear_args, stream):
-    rc = lib().moe_linear(args, stream)
-    if rc:
-        check(rc, "moe_linear")
-
-
 def moe_linear_workspace(M: int, N: int) -> int:
     return lib().moe_linear_workspace(M, N)
-
-
-def moe_linear_backward(args: moe_linear_args, workspace, workspace_bytes, stream):
-    rc = lib().moe_linear_backward(args, workspace, workspace_bytes, stream)
-    if rc:
-        check(rc, "moe_linear_backward")
 
 
 def moe_ops_status(stream):
