@@ -16,6 +16,7 @@ from tile_signaled_grouped_gb300.workloads import get_workload, make_inputs  # n
 
 
 def main(name="tiny"):
+    torch.manual_seed(0)
     wl = get_workload(name)
     inp = make_inputs(wl, device="cuda")
     d, hidden = wl.d_model, wl.d_ff
