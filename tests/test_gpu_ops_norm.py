@@ -190,3 +190,14 @@ def test_repeats_streams_and_graphs_give_the_same_bits():
     graph.replay()
     want = step()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("n,D,dtype,pad", [(20000, 512, "bf16", 0), (20000, 301, "fp16", 3),
+                                           (12000, 256, "fp32", 0)])
+def test_one_warp_rows_lap_their_ring(n, D, dtype, pad):
+    """Rows that one warp holds, eight and more laps of the ring's stages: a stage may take its
+    next row only once every lane has read this one, the residual's gradient too."""
+    g = torch.Generator().manual_seed(n + D)
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(DT[dtype]).cuda()
+    check(rows(g, n, D, dtype, pad), w, w, rows(g, n, D, dtype, 0, 0.0), rows(g, n, D, dtype, pad, 0.0),
+          rows(g, n, D, dtype, pad, 0.0))

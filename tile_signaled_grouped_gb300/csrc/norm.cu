@@ -838,7 +838,9 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
     }
     float s[1] = {s2.get().x + s2.get().y};
     row_sum<1, 16>(s, red[grp][0], a.wpr, wr, grp);
-    // Every thread has read the stage: it takes the row `stages` ahead.
+    // Every thread has read the stage: it takes the row `stages` ahead. (row_sum's barrier orders
+    // those reads before the copy; a group of one warp meets here.)
+    __syncwarp();
     const long long next = row + (long long)a.stages * g.stride;
     if (t == 0 && next < a.n) g.load(st, next);
     if (++st == a.stages) {
@@ -966,6 +968,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
     }
     float s[2] = {s1.get().x + s1.get().y, s2.get().x + s2.get().y};
     row_sum<2, 16>(s, red[grp][it & 1], a.wpr, wr, grp);
+    __syncwarp();  // as in the forward kernel: the sums need nothing of `up`
     const long long next = row + (long long)a.stages * g.stride;
     if (t == 0 && next < a.n) g.load(st, next);
     if (++st == a.stages) {
