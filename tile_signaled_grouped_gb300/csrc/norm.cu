@@ -501,6 +501,7 @@ constexpr long long kWaitNs = 4000000000LL;  // bound of every device-side wait
 struct RingState {
   uint64_t full[kMaxRing];
   int abort;
+  int stop;  // the first step whose row the leader did not see land in time; -1: none
 };
 
 // A group's ring: a stage holds a row of x (forward) or of z and dy (backward), and of r
@@ -581,6 +582,12 @@ struct Ring {
       if (r != nullptr) copy(to_r, r, a.ld_r, row, bar);
     }
   }
+  // The same once every thread has read the stage. After a wait of the leader's that ran out
+  // nothing is loaded any more: that stage's copy may be in flight, and its barrier, still in
+  // the old phase, must not be armed a second time.
+  __device__ __forceinline__ void refill(int i, long long row) const {
+    if (*(volatile int*)&st->stop < 0) load(i, row);
+  }
 };
 
 // Every thread of the CTA, once `st` of its group is set; `leader`: the group's first thread.
@@ -590,6 +597,7 @@ __device__ __forceinline__ void ring_begin(const Ring<T, BACK, AL>& g, bool lead
     for (int i = 0; i < g.a.stages; ++i) mbar_init(&g.st->full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     g.st->abort = 0;
+    g.st->stop = -1;
   }
   __syncthreads();
   if (leader)
@@ -598,18 +606,23 @@ __device__ __forceinline__ void ring_begin(const Ring<T, BACK, AL>& g, bool lead
       if (row < g.a.n) g.load(i, row);
     }
 }
-// The stage's phase is complete: its row is there. After a wait that ran out the group carries on
+// The stage's phase is complete: the row of step `it` is there. After a wait that ran out the group carries on
 // with what is there (the status says that its results are void), so that every thread
 // meets the same barriers.
 template <typename T, bool BACK, bool AL>
-__device__ __forceinline__ void ring_wait(const Ring<T, BACK, AL>& g, int stage, int phase) {
-  mbar_wait_bounded(&g.st->full[stage], phase, &g.st->abort, kWaitNs, g.a.status, 0x51000000u);
+__device__ __forceinline__ void ring_wait(const Ring<T, BACK, AL>& g, int stage, int phase, bool leader,
+                                          int it) {
+  if (!mbar_wait_bounded(&g.st->full[stage], phase, &g.st->abort, kWaitNs, g.a.status, 0x51000000u) &&
+      leader && g.st->stop < 0)
+    g.st->stop = it;
 }
-// After an abort: the copies in flight of the group's `rows` rows land before it leaves.
+// After an abort: the copies in flight land before the group leaves. It loaded all of its `rows`
+// rows, or those up to the stages ahead of the step where it stopped.
 template <typename T, bool BACK, bool AL>
 __device__ __forceinline__ void ring_end(const Ring<T, BACK, AL>& g, bool leader, int rows) {
   if (leader && *(volatile int*)&g.st->abort) {
     volatile int never = 0;
+    if (g.st->stop >= 0) rows = min(rows, g.st->stop + g.a.stages);
     for (int it = max(0, rows - g.a.stages); it < rows; ++it)
       mbar_wait_bounded(&g.st->full[it % g.a.stages], (it / g.a.stages) & 1, &never, kWaitNs, g.a.status,
                         0x52000000u);
@@ -814,7 +827,7 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
   for (long long row = g.first; row < a.n; row += g.stride, ++it) {
     T* y = static_cast<T*>(a.y) + row * a.ld_y;
     T* z = a.z != nullptr ? static_cast<T*>(a.z) + row * a.ld_z : nullptr;
-    ring_wait(g, st, phase);
+    ring_wait(g, st, phase, t == 0, it);
     const uint4 *xs = g.stage(st, 0), *rs_row = g.stage(st, 1);
     const uint32_t at_x = AL ? 0u : block_offset(static_cast<const T*>(a.x), a.ld_x, row);
     const uint32_t at_r = AL || mats == 1 ? 0u : block_offset(static_cast<const T*>(a.r), a.ld_r, row);
@@ -842,7 +855,7 @@ __global__ void __launch_bounds__(512, 1) norm_ring_kernel(const __grid_constant
     // those reads before the copy; a group of one warp meets here.)
     __syncwarp();
     const long long next = row + (long long)a.stages * g.stride;
-    if (t == 0 && next < a.n) g.load(st, next);
+    if (t == 0 && next < a.n) g.refill(st, next);
     if (++st == a.stages) {
       st = 0;
       phase ^= 1;
@@ -933,7 +946,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
       mean_n = __ldg(a.mean + row + g.stride);
       rstd_n = __ldg(a.rstd + row + g.stride);
     }
-    ring_wait(g, st, phase);
+    ring_wait(g, st, phase, t == 0, it);
     const uint4 *zs = g.stage(st, 0), *ds = g.stage(st, 1), *us = g.stage(st, 2);
     const uint32_t at_z = AL ? 0u : block_offset(static_cast<const T*>(a.x), a.ld_x, row);
     const uint32_t at_d = AL ? 0u : block_offset(static_cast<const T*>(a.dy), a.ld_dy, row);
@@ -970,7 +983,7 @@ __global__ void __launch_bounds__(32 * max_warps(EPT))
     row_sum<2, 16>(s, red[grp][it & 1], a.wpr, wr, grp);
     __syncwarp();  // as in the forward kernel: the sums need nothing of `up`
     const long long next = row + (long long)a.stages * g.stride;
-    if (t == 0 && next < a.n) g.load(st, next);
+    if (t == 0 && next < a.n) g.refill(st, next);
     if (++st == a.stages) {
       st = 0;
       phase ^= 1;
