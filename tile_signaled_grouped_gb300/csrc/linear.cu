@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
     constexpr uint32_t step_a = (AMN ? 2048 : 32) >> 4, step_b = (BMN ? 2048 : 32) >> 4;
     int st = 0;
     uint32_t phase = 0, accumulate = 0, at = 0;  // at: the stage's offset in 16-byte units
-    for (int kb = k_lo; kb < k_hi; kb += a.blocks) {
+    int kb = k_lo;
+    for (; kb < k_hi; kb += a.blocks) {
       if (!warp_wait(&sm.full[st], phase, &sm.abort, 0x03000000u)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -592,7 +593,19 @@ __global__ void __launch_bounds__(kTileThreads) linear_tile_kernel(const __grid_
       next_stage(st, phase, a.stages);
       at = st == 0 ? 0 : at + (stage_bytes >> 4);
     }
+    if (kb < k_hi) {
+      // A wait ran out, perhaps after warp 0 had issued all of its copies: those that may be in
+      // flight, of this step and of the stages after it, land before the CTA leaves.
+      volatile int never = 0;
+      const unsigned long long t0 = globaltimer();
+      for (int n = 0; n < a.stages && kb < k_hi; ++n, kb += a.blocks) {
+        const long long left = kWaitNs - (long long)(globaltimer() - t0);
+        mbar_wait_bounded(&sm.full[st], phase, &never, left > 0 ? left : 0, g_status, 0x05000000u);
+        next_stage(st, phase, a.stages);
+      }
+    }
     // Also after a wait that ran out: no product outlives the CTA.
+    __syncwarp();
     if (elect_one()) tc_commit(&sm.done);
   }
   __syncwarp();
