@@ -956,6 +956,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
       for (int c = half * (kPairCols / 2); c < c1; c += 32) {
         uint32_t v[32];
+        __syncwarp();  // the stores of the columns before may have parted it; the load wants it whole
         tmem_ld32(src + c, v);
         tmem_ld_wait();
         if (c + 32 >= c1) {  // the accumulator is read: it may be overwritten
