@@ -1,5 +1,7 @@
 """The matrix product with its epilogue (ops.linear and its backward) against float64,
 within the rounding errors of the operands' types and of fp32 sums."""
+import math
+
 import pytest
 import torch
 
@@ -216,3 +218,40 @@ def test_repeats_streams_and_graphs_give_the_same_bits():
         assert all(torch.equal(a, b) for a, b in zip(out, want))
     ops.clear_status()
     assert ops.status() == (0, 0)
+
+
+# gelu(z) = z Phi(z), Phi(z) = erfc(-z / sqrt(2)) / 2. In fp32, relative to Phi and in half steps: three
+# roundings of the exponent -z^2 / 2 (1.5 z^2), the exponential and the reciprocal (4 each, and 2 for the
+# latter's argument), 8 terms of a fit and its own error (12), products (3).
+def gelu_steps(z):
+    return 1.5 * z * z + 28
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M", [1, 20])
+def test_gelu_keeps_its_relative_accuracy_below_zero(M, dtype):
+    z = torch.linspace(-9.0, 3.0, 769, device="cuda").to(DT[dtype])
+    x = torch.zeros(M, 8, device="cuda", dtype=DT[dtype])
+    x[:, 0] = 1
+    w = torch.zeros(z.numel(), 8, device="cuda", dtype=DT[dtype])
+    w[:, 0] = z
+    z = z.double()
+    want = R.act(z, "gelu")
+    tol = gelu_steps(z) * R.U32 * want.abs()
+    y, _ = ops.linear(x, w, act="gelu", out_dtype=torch.float32)
+    assert ((y.double() - want).abs() <= tol).all()
+    y, _ = ops.linear(x, w, act="gelu")
+    tol = tol + ROUND[y.dtype] * want.abs() + (2.0 ** -25 if dtype == "fp16" else 0.0)
+    assert ((y.double() - want).abs() <= tol).all()
+
+
+def test_gelu_gradient_below_zero():
+    """gelu' = Phi + z phi: each term to its relative error."""
+    z = torch.linspace(-9.0, 3.0, 769, device="cuda").bfloat16()[None]
+    x, w = torch.zeros(1, 8, device="cuda").bfloat16(), torch.zeros(769, 8, device="cuda").bfloat16()
+    _, _, db = ops.linear_backward(torch.ones_like(z), x, w, z=z, act="gelu", bias=torch.float32)
+    z = z[0].double()
+    cdf = 0.5 * torch.special.erfc(-z * math.sqrt(0.5))
+    pdf = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    tol = gelu_steps(z) * R.U32 * (cdf + (z * pdf).abs())
+    assert ((db.double() - R.act_grad(z, "gelu")).abs() <= tol).all()

@@ -35,13 +35,41 @@ __device__ __forceinline__ float fast_sigmoid(float v) { return __fdividef(1.0f,
 constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluC1 = 0.044715f;
 
+// The normal distribution: returns (1 + erf(z / sqrt(2))) / 2, and in *e exp(-z^2 / 2). The
+// side of 0 that z is on has the tail q = erfc(|z| / sqrt(2)) / 2 = e t R(t), t = 1 / (1 + 0.44 |z| /
+// sqrt(2)): without the exponential it falls only as 1 / |z|, and R is a polynomial fitted to it over
+// |z| < 14, where e leaves fp32, with the largest relative error as small as degree 7 allows
+// (1.9e-7; least squares reweighted by the errors, Lawson's method). So nothing cancels below 0,
+// where 1 + erf keeps multiples of 6e-8 only (4 % of gelu at -5). Within (1.5 z^2 + 25) 2^-24 of
+// itself: three roundings of the exponent, and 25 half steps for the rest. 4096 x 4096 x 1024
+// with this gelu takes 42 us, 47 by erff, 67 by erfcf.
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+  float t, x;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(z), 0.44f * 0.7071067811865476f, 1.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(z * z * -0.7213475204444817f));  // log2(e) / 2
+  float r = 0.035597959f;
+  r = fmaf(r, t, -0.13891378f);
+  r = fmaf(r, t, 0.14823441f);
+  r = fmaf(r, t, -0.0099838804f);
+  r = fmaf(r, t, 0.10784631f);
+  r = fmaf(r, t, 0.10867608f);
+  r = fmaf(r, t, 0.12443229f);
+  r = fmaf(r, t, 0.12411071f);
+  const float q = r * t * x;
+  *e = x;
+  return z < 0.f ? q : 1.0f - q;
+}
+
 // act(z). 0.5 (1 + tanh u) is the sigmoid of 2u. The fast exponential and division are
 // within 1e-6 of themselves, far below half a step of a 16-bit result; an fp32 result is off
 // by that.
 template <int ACT>
 __device__ __forceinline__ float act_of(float z) {
   if (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
-  if (ACT == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+  if (ACT == MOE_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, &e);
+  }
   if (ACT == MOE_ACT_GELU_TANH) return z * fast_sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
   if (ACT == MOE_ACT_SILU) return z * fast_sigmoid(z);
   return z;
@@ -52,9 +80,11 @@ template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   z = z > 30.f ? 30.f : z < -30.f ? -30.f : z;
-  if (ACT == MOE_ACT_GELU)
-    return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) +
-           z * 0.3989422804014327f * __expf(-0.5f * z * z);
+  if (ACT == MOE_ACT_GELU) {
+    float e;
+    const float p = normal_cdf(z, &e);
+    return fmaf(z * 0.3989422804014327f, e, p);  // 1 / sqrt(2 pi)
+  }
   if (ACT == MOE_ACT_GELU_TANH) {
     const float q = fast_sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
     return q + z * q * (1.0f - q) * (2.0f * kGeluC0) * (1.0f + 3.0f * kGeluC1 * z * z);
