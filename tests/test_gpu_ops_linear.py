@@ -255,3 +255,16 @@ def test_gelu_gradient_below_zero():
     pdf = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     tol = gelu_steps(z) * R.U32 * (cdf + (z * pdf).abs())
     assert ((db.double() - R.act_grad(z, "gelu")).abs() <= tol).all()
+
+
+def test_silu_gradient_far_below_zero():
+    """silu'(z) = q (1 + z (1 - q)), relative to itself, in half steps: the exponential 4 + 2.4 |z|,
+    the division 4, the sums and products around them 7. Below the range of fp32 it is 0."""
+    z = torch.tensor([-20.0, -29.5, -30.0, -31.0, -45.0, -60.0, -85.0, -100.0, -1e4, -3e38, -math.inf],
+                     device="cuda").bfloat16()[None]
+    x, w = torch.zeros(1, 8, device="cuda").bfloat16(), torch.zeros(11, 8, device="cuda").bfloat16()
+    _, _, db = ops.linear_backward(torch.ones_like(z), x, w, z=z, act="silu", bias=torch.float32)
+    z = z[0, :7].double()
+    want = R.act_grad(z, "silu")
+    assert ((db[:7].double() - want).abs() <= (2.4 * z.abs() + 16) * R.U32 * want.abs()).all()
+    assert not db[7:].any()

@@ -60,9 +60,9 @@ __device__ __forceinline__ float normal_cdf(float z, float* e) {
   return z < 0.f ? q : 1.0f - q;
 }
 
-// act(z). 0.5 (1 + tanh u) is the sigmoid of 2u. The fast exponential and division are
-// within 1e-6 of themselves, far below half a step of a 16-bit result; an fp32 result is off
-// by that.
+// act(z). 0.5 (1 + tanh u) is the sigmoid of 2u. The fast exponential of v is within
+// (2 + 1.2 |v|) 2^-23 of itself (1e-6 at 6, 1e-5 at 80) and the fast division within 2^-22, far
+// below half a step of a 16-bit result; an fp32 result is off by that. Sigmoids below 2^-126 are 0.
 template <int ACT>
 __device__ __forceinline__ float act_of(float z) {
   if (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
@@ -74,12 +74,14 @@ __device__ __forceinline__ float act_of(float z) {
   if (ACT == MOE_ACT_SILU) return z * fast_sigmoid(z);
   return z;
 }
-// act'(z). Past 30 the derivatives are 0 or 1 to the last bit, and z there would only make
-// infinities times zero; NaN stays.
+// act'(z). z is kept where it makes no infinities times zero: past 30 the derivatives are 1 to
+// the last bit, and below -30 0 in fp32, but for silu's, z exp(z), which is below 1e-36 only
+// from -88 on and 0 here. NaN stays (relu's derivative there is 0).
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  z = z > 30.f ? 30.f : z < -30.f ? -30.f : z;
+  constexpr float kLow = ACT == MOE_ACT_SILU ? -100.f : -30.f;
+  z = z > 30.f ? 30.f : z < kLow ? kLow : z;
   if (ACT == MOE_ACT_GELU) {
     float e;
     const float p = normal_cdf(z, &e);
