@@ -113,3 +113,27 @@ def test_captured_forward_follows_its_input():
     want = blk.forward(x, r)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("make_empty", [
+    lambda n: torch.zeros(n, 16, device="cuda")[:, :0].t(),             # [0, n], columns apart
+    lambda n: torch.zeros(1, n, device="cuda").expand(3, n)[None][:0],  # [0, 3, n], one row thrice
+    lambda n: torch.zeros(1, n, device="cuda").expand(0, n),
+], ids=["transposed", "expanded", "none"])
+def test_no_rows_whatever_the_strides(make_empty):
+    e = make_empty(8)
+    lead = tuple(e.shape[:-1])
+    ids, w = ops.route_experts(e, 2)
+    assert ids.shape == lead + (2,) and w.shape == lead + (2,)
+    assert ops.route_experts_backward(w, e, ids).shape == e.shape
+    one = torch.ones(8, device="cuda")
+    y, z, mean, rstd = ops.layer_norm(e, one, one, residual=e, stats=True)
+    assert y.shape == z.shape == e.shape and mean.shape == lead
+    dx, dw, db = ops.layer_norm_backward(e, e, one, mean, rstd, dz=e)
+    assert dx.shape == e.shape and not dw.any() and not db.any()
+    x, r = e.bfloat16(), make_empty(24).bfloat16()
+    y, z = ops.linear(x, torch.ones(24, 8, device="cuda").bfloat16(), act="silu", residual=r, preact=True)
+    assert y.shape == z.shape == lead + (24,)
+    dx, dw, db = ops.linear_backward(r, x, torch.ones(24, 8, device="cuda").bfloat16(), z=r, act="silu",
+                                     bias=torch.float32)
+    assert dx.shape == x.shape and not dw.any() and not db.any()

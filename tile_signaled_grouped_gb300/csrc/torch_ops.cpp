@@ -70,12 +70,17 @@ Rows rows_of(const Tensor& t, const char* what, int64_t cols = -1) {
   const int64_t dim = t.dim();
   bool ok = dim > 0;
   Rows r{1, dim > 0 ? sizes[dim - 1] : 0, 0};
+  if (t.numel() == 0) {  // no elements: whatever the strides
+    for (int64_t d = 0; d < dim - 1; ++d) r.n *= sizes[d];
+    if (cols >= 0 && r.c != cols) refuse(what, " has rows of ", r.c, " elements: expected ", cols);
+    r.ld = r.c;
+    return r;
+  }
   if (ok) ok = r.c <= 1 || strides[dim - 1] == 1;
   // The dimensions of more than one element before the last: each spans the one after it.
   int64_t step = -1;
   for (int64_t d = dim - 2; ok && d >= 0; --d) {
-    if (sizes[d] == 0) r.n = 0;
-    if (sizes[d] <= 1) continue;
+    if (sizes[d] == 1) continue;
     if (step < 0) {
       r.ld = strides[d];
       ok = r.ld >= r.c;
@@ -85,7 +90,7 @@ Rows rows_of(const Tensor& t, const char* what, int64_t cols = -1) {
     step = strides[d] * sizes[d];
     r.n *= sizes[d];
   }
-  if (!ok && t.numel() > 0)
+  if (!ok)
     refuse(what, " must be rows of contiguous elements, got shape ", sizes, " and strides ", strides);
   if (cols >= 0 && r.c != cols) refuse(what, " has rows of ", r.c, " elements: expected ", cols);
   if (r.n <= 1) r.ld = r.c;
