@@ -490,9 +490,10 @@ size_t moe_linear_workspace(long long M, long long N);
 int moe_linear_backward(const moe_linear_args *args, void *workspace, size_t workspace_bytes,
                         moe_stream_t stream);
 
-/* The products' device waits are bounded; one that runs out sets a sticky status of the
- * device (its results are void). Synchronises `stream` and reads it: *code is 0 or
- * MOE_DEV_TIMEOUT, *detail the wait. */
+/* The device waits of the products and of layer norm are bounded; one that runs out sets a
+ * sticky status of the device (its results are void). Synchronises `stream` and reads the
+ * status of that stream's device, whichever is current (of the current one for a default
+ * stream): *code is 0 or MOE_DEV_TIMEOUT, *detail the wait. */
 int moe_ops_status(moe_stream_t stream, int *code, int *detail);
 int moe_ops_status_clear(moe_stream_t stream);
 

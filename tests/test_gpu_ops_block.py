@@ -137,3 +137,10 @@ def test_no_rows_whatever_the_strides(make_empty):
     dx, dw, db = ops.linear_backward(r, x, torch.ones(24, 8, device="cuda").bfloat16(), z=r, act="silu",
                                      bias=torch.float32)
     assert dx.shape == x.shape and not dw.any() and not db.any()
+
+
+def test_status_of_every_kind_of_stream():
+    st = torch.cuda.Stream()
+    for stream in (None, st, st.cuda_stream, 0, torch.cuda.default_stream()):
+        ops.clear_status(stream)
+        assert ops.status(stream) == (0, 0)

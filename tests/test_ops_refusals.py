@@ -245,3 +245,18 @@ def test_activation_reference_gradient_is_the_difference(kind):
     h = 1e-5
     d = (R.act(z + h, kind) - R.act(z - h, kind)) / (2 * h)
     assert (R.act_grad(z, kind) - d).abs().max() < 1e-8
+
+
+# -------------------------------------------------------------------------------- status
+def test_status_takes_streams_and_raw_handles(monkeypatch):
+    seen = []
+    monkeypatch.setattr(capi, "moe_ops_status", lambda s: seen.append(s) or (0, 0))
+    monkeypatch.setattr(capi, "moe_ops_status_clear", seen.append)
+
+    class Stream:
+        cuda_stream = 77
+
+    for stream in (Stream(), 78, 0):
+        assert ops.status(stream) == (0, 0)
+        ops.clear_status(stream)
+    assert seen == [77, 77, 78, 78, 0, 0]

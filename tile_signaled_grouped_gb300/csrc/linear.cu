@@ -1605,6 +1605,27 @@ bool check_matrix(const void* q, long long ld, long long rows, long long cols, i
 constexpr int kBiasParts = 256;  // row ranges of the column sums at most
 size_t dz_bytes(long long M, long long N) { return ((size_t)M * ((N + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
 
+// A stream's device, current while this lives: the status words are one set for each device.
+struct StreamDevice {
+  int before = -1;
+  bool ok = false;
+  explicit StreamDevice(cudaStream_t s) {
+    int dev = 0;
+    if (cudaGetDevice(&before) != cudaSuccess) return;
+    // The default streams have no device of their own.
+    if (s == nullptr || s == cudaStreamLegacy || s == cudaStreamPerThread)
+      dev = before;
+    else if (cudaStreamGetDevice(s, &dev) != cudaSuccess)
+      return;
+    ok = dev == before || cudaSetDevice(dev) == cudaSuccess;
+  }
+  ~StreamDevice() {
+    if (ok) cudaSetDevice(before);
+  }
+  StreamDevice(const StreamDevice&) = delete;
+  StreamDevice& operator=(const StreamDevice&) = delete;
+};
+
 template <int ACT>
 void launch_act_grad(const ActGradArgs& a, bool vec, dim3 grid, cudaStream_t s) {
   if (vec)
@@ -1787,7 +1808,8 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
 int moe_ops_status(moe_stream_t stream, int* code, int* detail) {
   uint32_t v[2] = {0, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemcpyFromSymbolAsync(v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+  const StreamDevice device(s);
+  if (!device.ok || cudaMemcpyFromSymbolAsync(v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
@@ -1798,9 +1820,10 @@ int moe_ops_status(moe_stream_t stream, int* code, int* detail) {
 }
 
 int moe_ops_status_clear(moe_stream_t stream) {
-  void* p = ops_status();
-  if (p == nullptr ||
-      cudaMemsetAsync(p, 0, sizeof(g_status), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const StreamDevice device(s);
+  void* p = device.ok ? ops_status() : nullptr;
+  if (p == nullptr || cudaMemsetAsync(p, 0, sizeof(g_status), s) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }

@@ -19,6 +19,7 @@ import os
 import torch
 
 from . import capi
+from .runtime import _stream_handle
 
 _SCORES = {"softmax": capi.MOE_SCORE_SOFTMAX, "sigmoid": capi.MOE_SCORE_SIGMOID}
 _native = None
@@ -150,11 +151,21 @@ def linear_backward(dy, x, weight, z=None, act="none", bias=None, dw_dtype=None,
                                                  need_dw)
 
 
+def _device_of(stream):
+    """Makes a torch stream's device current (the library finds that of any other handle but a
+    default stream's, which says nothing of its device)."""
+    device = getattr(stream, "device", None)
+    return contextlib.nullcontext() if device is None else torch.cuda.device(device)
+
+
 def status(stream=None):
-    """(code, detail) of the products' device status: 0, or MOE_DEV_TIMEOUT after a device
-    wait ran out. Synchronises the stream; clear_status() clears it."""
-    return capi.moe_ops_status((stream or torch.cuda.current_stream()).cuda_stream)
+    """(code, detail) of the operators' device status: 0, or MOE_DEV_TIMEOUT after a device
+    wait ran out, on the device of `stream` (a torch stream or a raw handle; default: the current
+    one). Synchronises the stream; clear_status() clears it."""
+    with _device_of(stream):
+        return capi.moe_ops_status(_stream_handle(stream))
 
 
 def clear_status(stream=None):
-    capi.moe_ops_status_clear((stream or torch.cuda.current_stream()).cuda_stream)
+    with _device_of(stream):
+        capi.moe_ops_status_clear(_stream_handle(stream))
