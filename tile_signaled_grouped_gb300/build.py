@@ -4,7 +4,8 @@ binding _torch_ops.so with the host compiler.
 Each translation unit compiles in parallel into _build/, then one nvcc link
 produces tile_signaled_grouped_gb300/libmoe_tsg.so (CUDA runtime linked
 statically, so the library needs only the driver at run time) and one host link the
-binding, which loads that library from its own folder.
+binding, which loads that library from its own folder. Where PyTorch or the headers that
+the binding needs are not installed, the library is built alone.
 """
 from __future__ import annotations
 
@@ -59,11 +60,25 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def _torch() -> str:
+def _torch():
+    """PyTorch's folder, or None where it is not installed."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found")
-    return os.path.dirname(spec.origin)
+    return None if spec is None else os.path.dirname(spec.origin)
+
+
+def binding_lacks():
+    """What the torch binding's build lacks here, in words, or None."""
+    if _torch() is None:
+        return "PyTorch is not installed"
+    for f in (os.path.join(_torch(), "include", "torch", "extension.h"),
+              os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(f):
+            return f"{f} is missing"
+    return None if shutil.which(_cxx()) else f"no host compiler ({_cxx()})"
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
 
 
 def _compile_binding() -> str:
@@ -72,16 +87,17 @@ def _compile_binding() -> str:
     inc = [os.path.join(_torch(), "include"),
            os.path.join(_torch(), "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+    _run([_cxx(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
           *[f for i in inc for f in ("-isystem", i)], "-DTORCH_EXTENSION_NAME=_torch_ops", "-c",
           os.path.join(CSRC, "torch_ops.cpp"), "-o", obj], "the torch binding's compilation")
     return obj
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB] if binding_lacks() else [LIB, BINDING]
+    if not all(map(os.path.exists, made)):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(map(os.path.getmtime, made))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(ROOT, "include", "moe_tsg.h"))
     deps.append(os.path.abspath(__file__))
@@ -94,14 +110,16 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if binding_lacks() else ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose, extra), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     _run(cmd, "nvcc link")
     os.replace(tmp, LIB)
+    if binding is None:
+        return LIB
     tmp = BINDING + ".tmp"
-    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding.result(), "-L" + PKG,
+    _run([_cxx(), "-shared", "-o", tmp, binding.result(), "-L" + PKG,
           "-l:libmoe_tsg.so", "-L" + os.path.join(_torch(), "lib"), "-lc10", "-lc10_cuda",
           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "the torch binding's link")
     os.replace(tmp, BINDING)

@@ -18,7 +18,7 @@ import os
 
 import torch
 
-from . import capi
+from . import build, capi
 from .runtime import _stream_handle
 
 _SCORES = {"softmax": capi.MOE_SCORE_SOFTMAX, "sigmoid": capi.MOE_SCORE_SIGMOID}
@@ -31,8 +31,10 @@ def native():
     global _native
     if _native is None:
         if not os.path.exists(os.path.join(os.path.dirname(capi.LIB_PATH), "_torch_ops.so")):
+            why = build.binding_lacks()
             raise capi.MoeError("_torch_ops.so is missing: the torch binding is not built (run "
-                                "tile_signaled_grouped_gb300.build.build())")
+                                "tile_signaled_grouped_gb300.build.build()"
+                                + (f"; here {why})" if why else ")"))
         from . import _torch_ops
 
         _torch_ops.set_error(capi.MoeError)
