@@ -52,3 +52,19 @@ def test_library_is_built_without_headers_or_compiler_of_the_binding(made, monke
     monkeypatch.undo()
     monkeypatch.setenv("CXX", "no-such-compiler")
     assert "no-such-compiler" in B.binding_lacks()
+
+
+def test_binding_of_another_torch_is_built_anew(made, monkeypatch, tmp_path):
+    include = tmp_path / "torch" / "include" / "torch"
+    include.mkdir(parents=True)
+    (include / "extension.h").touch()
+    monkeypatch.setattr(B, "_torch", lambda: str(tmp_path / "torch"))
+    for version in ("1.0+a", "1.0+b"):
+        (tmp_path / "torch" / "version.py").write_text(f"__version__ = '{version}'")
+        B.build()
+    assert made == ["libmoe_tsg.so", "_torch_ops.so"] * 2
+    B.build()
+    assert len(made) == 4
+    monkeypatch.setattr(B.sysconfig, "get_config_var", lambda name: "cpython-300")
+    B.build()
+    assert len(made) == 6

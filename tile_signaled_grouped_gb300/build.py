@@ -81,6 +81,20 @@ def _cxx() -> str:
     return os.environ.get("CXX", "g++")
 
 
+def _built_for() -> str:
+    """What a binding fits: the Python and the PyTorch it was compiled against."""
+    with open(os.path.join(_torch(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{_torch()}\n{f.read()}"
+
+
+def _binding_fits() -> bool:
+    try:
+        with open(os.path.join(BUILD, "torch_ops.for")) as f:
+            return f.read() == _built_for()
+    except OSError:
+        return False
+
+
 def _compile_binding() -> str:
     obj = os.path.join(BUILD, "torch_ops.o")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -95,7 +109,7 @@ def _compile_binding() -> str:
 
 def _stale() -> bool:
     made = [LIB] if binding_lacks() else [LIB, BINDING]
-    if not all(map(os.path.exists, made)):
+    if not all(map(os.path.exists, made)) or (BINDING in made and not _binding_fits()):
         return True
     t = min(map(os.path.getmtime, made))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
@@ -105,7 +119,8 @@ def _stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile and link; returns the library path. Rebuilds only when sources changed."""
+    """Compile and link; returns the library path. Rebuilds only when sources changed, or what
+    the binding was compiled against."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -123,6 +138,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
           "-l:libmoe_tsg.so", "-L" + os.path.join(_torch(), "lib"), "-lc10", "-lc10_cuda",
           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "the torch binding's link")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "torch_ops.for"), "w") as f:
+        f.write(_built_for())
     return LIB
 
 
