@@ -1333,7 +1333,13 @@ cudaError_t launch_tile(const GemmArgs& a, int tiles, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, linear_tile_kernel<AMN, BMN>, a);
 }
 
-// Clusters of two resident at once on an idle GPU: all of a persistent launch has to be.
+cudaError_t allow_pair_smem() {
+  static std::atomic<uint64_t> ready{0};
+  return allow_smem(reinterpret_cast<const void*>(linear_pair_kernel), &ready);
+}
+
+// Clusters of two resident at once on an idle GPU: all of a persistent launch has to be. The
+// answer is 0 while the kernel may not take its shared memory; what was not told is not kept.
 int pair_clusters(int num_sms) {
   static std::atomic<int> table[64];
   int dev = 0;
@@ -1344,9 +1350,10 @@ int pair_clusters(int num_sms) {
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = kSmemMax;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+  if (allow_pair_smem() != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
-    n = num_sms / 2;
+    return num_sms / 2;
   }
   n = std::min(n, num_sms / 2);
   table[dev].store(n, std::memory_order_relaxed);
@@ -1380,10 +1387,9 @@ bool pair_product(const Product& g, bool bf16, PairProduct* p) {
 }
 
 int launch_pairs(PairArgs& a, int pairs, cudaStream_t s) {
-  static std::atomic<uint64_t> ready{0};
   a.any_rows = a.p[0].any_rows || (a.products == 2 && a.p[1].any_rows);
   a.stages = std::min<int>(kPairMaxStages, (int)((kSmemMax - pair_smem_bytes(0, a.any_rows)) / kPairStageBytes));
-  if (allow_smem(reinterpret_cast<const void*>(linear_pair_kernel), &ready) != cudaSuccess) {
+  if (allow_pair_smem() != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
