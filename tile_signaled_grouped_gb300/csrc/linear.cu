@@ -417,10 +417,10 @@ __device__ __forceinline__ bool elect_one() {
 // Waits of a whole warp: every lane comes out with the same answer, so that no lane leaves
 // a role that the others carry on with.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase, volatile int* abort, uint32_t detail) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, phase, abort, kWaitNs, g_status, detail));
+  return __all_sync(kAll, mbar_wait_bounded(bar, phase, abort, kWaitNs, g_status, detail));
 }
 __device__ __forceinline__ bool warp_pwait(uint64_t* bar, uint32_t phase, volatile int* abort, uint32_t detail) {
-  return __all_sync(0xFFFFFFFFu, pwait(bar, phase, abort, kWaitNs, g_status, detail));
+  return __all_sync(kAll, pwait(bar, phase, abort, kWaitNs, g_status, detail));
 }
 
 struct GemmArgs {

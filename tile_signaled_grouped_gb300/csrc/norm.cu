@@ -28,7 +28,6 @@
 namespace moe {
 namespace {
 
-constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kNormParts = 304;   // CTAs of the backward kernel at most (two for each of 152 SMs)
 constexpr int kLoopThreads = 1024;
 
@@ -49,12 +48,6 @@ struct NormArgs {
   int stages;        // ring kernels: rows of shared memory
   uint32_t* status;  // ring kernels: where a wait that ran out is recorded
 };
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
 
 // What a thread reads at once: N elements, a 16-byte vector of them (the rows start on 16
 // bytes and D is a multiple of N) or one (neighbouring threads then take neighbouring

@@ -56,7 +56,6 @@ int ops_device(int* num_sms) {
 
 namespace {
 
-constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kRouterWarps = 8;
 
 struct RouterArgs {
@@ -73,11 +72,6 @@ struct RouterArgs {
   float scale;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
 // The largest and the smallest value of the warp without its NaN; NaN if there is no other.
 __device__ __forceinline__ float redux_max(float v) {
   float r;
