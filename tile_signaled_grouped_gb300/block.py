@@ -7,7 +7,7 @@
 
 and, for training, the backward pass of everything but the routed experts' weights.
 Argument checks and output allocation are those of ops and runtime, and the computation
-their kernels; only gradients that meet are added by torch.
+their kernels; only gradients that meet are added by torch, in their own 16 bits (a rounding each).
 """
 from __future__ import annotations
 
@@ -77,6 +77,7 @@ class MoEBlock:
             dl = ops.route_experts_backward(d_w, saved["logits"], saved["ids"],
                                             score=ops.score_name(c), renorm=bool(c.renorm),
                                             scale=c.scale)
+            # The products take 16-bit operands: the scores' gradient is rounded once, as dz is.
             dx, g["w_router"], _ = ops.linear_backward(dl.to(dy.dtype), saved["h"], self.w_router)
             d_h = d_h + dx
         # s is the residual of the second product: its gradient dy joins the norm's.

@@ -520,7 +520,7 @@ __device__ __forceinline__ void join(const GemmArgs& a, const float* part, int r
 // k in its TMEM. The partial sums of a row then meet in the shared memory of one of them, which
 // adds them in the order of the ranks and finishes the row. Warp 0
 // loads, warp 1 issues the products, all eight warps empty TMEM. Bound by its start, the
-// pipeline's first loads and the end: 333 x 517 x 1000 takes 6.6 us, 512 x 1024 x 1024 6.1 us, of
+// pipeline's first loads and the end: 333 x 517 x 1000 takes 8.1 us, 512 x 1024 x 1024 6.0 us, of
 // which its products are 16 steps of 0.16 us. The CTA that finishes a row gets all its sums by
 // stores, and no CTA waits for the others to have read: joining took 2.9 us where it takes 2.2
 // (64 x 1024 x 1024 in four parts) as reads of the others' memory between two barriers.
@@ -1029,7 +1029,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // 2 t, 2 t + 1, 2 t + 8, 2 t + 9; both operands agree. `ks` warps share eight rows of the
 // weights, each with a range of k; their sums are added in the warps' order. CTAs walk the
 // rows of the weights, and the next batch of loads, of the next rows at the end of a row,
-// is on its way while a batch is multiplied. One row by 2048 x 7168: 7.4 to 8.5 us (3.4 to
+// is on its way while a batch is multiplied. One row by 2048 x 7168: 7.4 to 8.6 us (3.4 to
 // 4 TB/s, of which 2 us are the launch and its first loads); by 8192 x 8192: 26 us, 5.2 TB/s.
 // (16 rows of x in this form took 14 us for 2048 x 7168, where the tiles take 9.4.)
 constexpr int kRowsMax = 8;  // rows of x
@@ -1323,6 +1323,8 @@ cudaError_t launch_tile(const GemmArgs& a, int tiles, cudaStream_t s) {
   cfg.dynamicSmemBytes =
       1024 + tile_pipe_bytes(a.bn, a.blocks, a.stages, a.splits) + sizeof(TileSmem);
   cfg.stream = s;
+  // May start beside the kernel before it, as launch_behind says: 64 x 1024 x 1024 4.8 us in a
+  // graph and 5.3 without, 5.7 and 8.1 in calls one after another.
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)a.splits, 1, 1};

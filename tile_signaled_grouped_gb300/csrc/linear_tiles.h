@@ -10,7 +10,8 @@ constexpr int kTileI = 128;  // rows of a CTA's tile
 
 // Which kernel and tiles take a product: the least of an estimate in microseconds, fitted to
 // measurements of 16 to 1024 rows at 2048 x 7168, 8192 x 2048, 1536 x 4096, 4096 x 1024 and
-// 512 x 1000 (within 20 % of them, and its choice within 10 % of the best there).
+// 512 x 1000 (within 20 % of them, and its choice within 10 % of the best there; elsewhere up to 17 %
+// were seen: 256 x 4096 x 4096 16.7 us where 64 columns take 14.3).
 // A step of 64 k takes a CTA 0.155 us up to 64 columns, 0.225 for 128 (0.29 with one block of k a
 // stage) and 0.34 for 256, or what all CTAs' bytes take at 18 TB/s; a pair's 256 x 256 x 64 takes
 // 0.29 us. Starting, filling the pipeline and the last products take 2 us (pairs, with their end:

@@ -477,11 +477,11 @@ __global__ void __launch_bounds__(kLoopThreads)
 // Long matrices: persistent CTAs whose groups of warps keep the next rows coming in (bulk copies
 // into a ring of shared memory), so that the loads never stop for the reductions of a row: the
 // kernels above only load between a CTA's start and its first reduction (16384 x 4096 bf16 with
-// a residual: 143 us against 93, 5.8 TB/s; backward of 8192 x 7168: 257 us against 84, 5.6 TB/s).
+// a residual: 143 us against 94, 5.7 TB/s; backward of 8192 x 7168: 257 us against 85, 5.5 TB/s).
 // wpr warps share a row; a CTA holds as many such groups as its warps allow, each with a ring of
 // its own. Rows that start anywhere come as the 16-byte blocks that they touch, and vectors are
 // shifted together from two neighbours (8192 x 4097 fp16 with a residual: 230 us by the element
-// against 97, backward 239 against 141).
+// against 97, backward 239 against 139).
 constexpr int kMaxRing = 4;  // 2, 3, 4 and 8 stages measured within 2 %
 constexpr int kMaxGroups = 16;
 // Elements a thread. What a row costs beside its elements (waits, reductions, addresses:

@@ -8,8 +8,9 @@
 //   largest c_e stay; the k largest c_e of those are chosen (equal: lower id or group)
 //   w_j = s_j                 or  s_j / (sum of the chosen s)      times `scale`
 //
-// A warp takes a token, its experts in the lanes' registers. Bound by instructions at many
-// tokens: 16384 x 256 with a bias and 4 of 8 groups, k = 8, takes 16 us (1.1 TB/s of scores)
+// A warp takes a token, its experts in the lanes' registers. At many tokens neither memory nor
+// the issue slots (68 % full) are the bound, but both the instructions and the rounds that follow
+// one another: 16384 x 256 with a bias and 4 of 8 groups, k = 8, takes 16 us (1.1 TB/s of scores)
 // for 670 warp instructions a token: 75 to load, 75 for the scores, 55 to sort a lane's eight,
 // 125 for the groups, 20 a round, 50 to find the ids, 40 to judge how close the order is, 75
 // for the weights. 1.7 of the 16 us pass while the last tokens decided in 64 bits end. At few

@@ -2,7 +2,7 @@
 // C ABI (include/moe_tsg.h), as the functions of the Python module _torch_ops that ops.py
 // documents. No computation here. In C++ because the host's part is what a small call costs:
 // with the same checks in Python over ctypes it was 14 us (routing, linear), 19 (layer norm)
-// and 24 to 32 (backward passes) on the Grace host, here 8 to 10, 9 to 12 and 14 to 18.
+// and 24 to 32 (backward passes) on a Grace host, here 5 to 10, 6 to 12 and 11 to 18 by the machine.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>

@@ -6,6 +6,9 @@ the library's kernels. A matrix is a tensor whose last dimension is contiguous a
 other dimensions are one run of rows (any 2-D tensor with a row stride; more dimensions
 as `view` can join them).
 
+They are not known to autograd: tensors that require a gradient are taken as their values,
+results carry no history, and a backward pass is the call that bears its name.
+
 Every call is asynchronous on `stream` (default: the current one) and may be captured
 into a CUDA graph after a first call. Outputs are allocated on that stream. Inputs
 written on another stream must be complete before it (an event or a synchronize) and
