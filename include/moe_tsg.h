@@ -389,8 +389,10 @@ typedef struct moe_router_cfg {
 /* For every token: s = score(l), c = s + bias; the topk_groups best groups stay, and of
  * their experts the topk with the largest c, in descending order (equal c: the lower id;
  * equal groups: the lower group). weight = s at the chosen id (without the bias), divided
- * by the sum of the chosen s with renorm, times scale. Without a bias the order of the c
- * is that of the l. The choice is that of 64-bit arithmetic.
+ * by the sum of the chosen s with renorm, times scale. The choice is that of 64-bit arithmetic.
+ * Without a bias the order of the c, and of groups judged by one of them, is that of the l: scores
+ * that even 64 bits round to the same (a sigmoid beyond 37; 0 for l = -inf and for a very low
+ * l) are told apart there, where with a bias they tie.
  * l = -inf masks an expert (s = 0); bias = -inf keeps it from being chosen while another
  * is left. A token whose chosen s are all 0 has weights 0 and valid, distinct ids. A NaN
  * score counts as -inf in the order, and the weights computed from it are NaN.

@@ -82,7 +82,8 @@ def route_experts(logits, topk, score="softmax", bias=None, groups=1, topk_group
     are the s of the chosen experts, divided by their sum with renorm, times scale.
     Returns (ids int32 [..., topk], weights fp32 [..., topk]). bias: fp32 [E], used for
     the choice alone. Masked experts have logits of -inf; a token whose chosen experts are
-    all masked has weights 0. The choice is that of 64-bit arithmetic."""
+    all masked has weights 0. The choice is that of 64-bit arithmetic; without a bias it goes by
+    the logits, which tell scores apart that 64 bits round to the same."""
     if stream is not None:
         with _on(logits, stream):
             return route_experts(logits, topk, score, bias, groups, topk_groups, group_top, renorm,
