@@ -13,91 +13,18 @@
 // TMA stages 64 k-elements of both operands with the 128-byte swizzle, and the tensor
 // cores read either layout, so no operand is ever transposed in memory. The bounds of the
 // tensor maps fill with zeros what lies past M, N and K.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
 
+#include "activations.cuh"
 #include "linear_tiles.h"
-#include "moe_common.cuh"
-#include "ops_common.cuh"
+#include "mma_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr long long kWaitNs = 4000000000LL;  // bound of every device-side wait
-
 // The sticky device status of these kernels: [0] code, [1] detail (moe_ops_status).
 __device__ uint32_t g_status[4];
-
-// ------------------------------------------------------------------- activations
-__device__ __forceinline__ float fast_sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
-
-constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
-constexpr float kGeluC1 = 0.044715f;
-
-// The normal distribution: returns (1 + erf(z / sqrt(2))) / 2, and in *e exp(-z^2 / 2). The
-// side of 0 that z is on has the tail q = erfc(|z| / sqrt(2)) / 2 = e t R(t), t = 1 / (1 + 0.44 |z| /
-// sqrt(2)): without the exponential it falls only as 1 / |z|, and R is a polynomial fitted to it over
-// |z| < 14, where e leaves fp32, with the largest relative error as small as degree 7 allows
-// (1.9e-7; least squares reweighted by the errors, Lawson's method). So nothing cancels below 0,
-// where 1 + erf keeps multiples of 6e-8 only (4 % of gelu at -5). Within (1.5 z^2 + 25) 2^-24 of
-// itself: three roundings of the exponent, and 25 half steps for the rest. 4096 x 4096 x 1024
-// with this gelu takes 42 us, 47 by erff, 67 by erfcf.
-__device__ __forceinline__ float normal_cdf(float z, float* e) {
-  float t, x;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(z), 0.44f * 0.7071067811865476f, 1.0f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(z * z * -0.7213475204444817f));  // log2(e) / 2
-  float r = 0.035597959f;
-  r = fmaf(r, t, -0.13891378f);
-  r = fmaf(r, t, 0.14823441f);
-  r = fmaf(r, t, -0.0099838804f);
-  r = fmaf(r, t, 0.10784631f);
-  r = fmaf(r, t, 0.10867608f);
-  r = fmaf(r, t, 0.12443229f);
-  r = fmaf(r, t, 0.12411071f);
-  const float q = r * t * x;
-  *e = x;
-  return z < 0.f ? q : 1.0f - q;
-}
-
-// act(z). 0.5 (1 + tanh u) is the sigmoid of 2u. The fast exponential of v is within
-// (2 + 1.2 |v|) 2^-23 of itself (1e-6 at 6, 1e-5 at 80) and the fast division within 2^-22, far
-// below half a step of a 16-bit result; an fp32 result is off by that. Sigmoids below 2^-126 are 0.
-template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-  if (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
-  if (ACT == MOE_ACT_GELU) {
-    float e;
-    return z * normal_cdf(z, &e);
-  }
-  if (ACT == MOE_ACT_GELU_TANH) return z * fast_sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
-  if (ACT == MOE_ACT_SILU) return z * fast_sigmoid(z);
-  return z;
-}
-// act'(z). z is kept where it makes no infinities times zero: past 30 the derivatives are 1 to
-// the last bit, and below -30 0 in fp32, but for silu's, z exp(z), which is below 1e-36 only
-// from -88 on and 0 here. NaN stays (relu's derivative there is 0).
-template <int ACT>
-__device__ __forceinline__ float act_grad(float z) {
-  if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  constexpr float kLow = ACT == MOE_ACT_SILU ? -100.f : -30.f;
-  z = z > 30.f ? 30.f : z < kLow ? kLow : z;
-  if (ACT == MOE_ACT_GELU) {
-    float e;
-    const float p = normal_cdf(z, &e);
-    return fmaf(z * 0.3989422804014327f, e, p);  // 1 / sqrt(2 pi)
-  }
-  if (ACT == MOE_ACT_GELU_TANH) {
-    const float q = fast_sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
-    return q + z * q * (1.0f - q) * (2.0f * kGeluC0) * (1.0f + 3.0f * kGeluC1 * z * z);
-  }
-  if (ACT == MOE_ACT_SILU) {
-    const float q = fast_sigmoid(z);
-    return q * (1.0f + z * (1.0f - q));
-  }
-  return 1.f;
-}
 
 __device__ __forceinline__ void st_cluster_v4(uint32_t cl_addr, uint32_t x, uint32_t y, uint32_t z,
                                               uint32_t w) {
@@ -367,60 +294,16 @@ __device__ __forceinline__ void finish1(const Epilogue& e, long long i, long lon
   store_from_f32(e.y, e.ytype, i * e.ld_y + j, v);
 }
 
-// ------------------------------------------------------------------- tensor-core pieces
-// Shared-memory matrix descriptor of an MN-major operand stored by TMA in boxes of 64
-// elements (128 bytes, the swizzle span) x 64 k-rows: 8 KB from one box to the next,
-// 1024 bytes from 8 k-rows to the next 8.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(8192 >> 4) << 16;  // leading-dimension offset: the next 64 elements
-  d |= (uint64_t)(1024 >> 4) << 32;  // stride-dimension offset: the next 8 k
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-// Instruction descriptor: 16-bit A and B of one type, fp32 accumulator, M x N.
-__device__ __forceinline__ uint32_t idesc_16bit(bool bf16, bool a_mn, bool b_mn, int M, int N) {
-  const uint32_t t = bf16 ? 1u : 0u;
-  return (1u << 4) | (t << 7) | (t << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
+// ------------------------------------------------------------------- tiles
 constexpr int kMaxStages = 8;
 constexpr int kABytes = kTileI * kBlockK * 2;  // 16 KB
 constexpr int kTileThreads = 256;
 
-// The next stage of a ring. (A division by the ring's length, which only the launch knows,
-// costs these single threads more than the rest of a step: with `n % stages` a step took
-// 190 ns without any copy or product in it.)
-__device__ __forceinline__ void next_stage(int& st, uint32_t& phase, int stages) {
-  if (++st == stages) {
-    st = 0;
-    phase ^= 1;
-  }
-}
-
-// One lane of a converged warp, the same one every time. The single-thread roles run as whole
-// warps and ask this around what one thread issues: their addresses and descriptors then
-// stay uniform values, which tcgen05 and TMA take as they are.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
-}
-
-// Waits of a whole warp: every lane comes out with the same answer, so that no lane leaves
-// a role that the others carry on with.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase, volatile int* abort, uint32_t detail) {
-  return __all_sync(kAll, mbar_wait_bounded(bar, phase, abort, kWaitNs, g_status, detail));
+  return moe::warp_wait(bar, phase, abort, g_status, detail);
 }
 __device__ __forceinline__ bool warp_pwait(uint64_t* bar, uint32_t phase, volatile int* abort, uint32_t detail) {
-  return __all_sync(kAll, pwait(bar, phase, abort, kWaitNs, g_status, detail));
+  return moe::warp_pwait(bar, phase, abort, g_status, detail);
 }
 
 struct GemmArgs {
@@ -1275,7 +1158,9 @@ __global__ void __launch_bounds__(32 * kBiasWarps)
 }
 
 // ------------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::atomic<void*> cached{nullptr};
   void* fn = cached.load(std::memory_order_relaxed);
   if (fn == nullptr) {
@@ -1289,11 +1174,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
 }
 
+namespace {
+
 // Map of a row-major [rows][cols] matrix of 16-bit elements: boxes of box_rows x 64
 // columns, 128-byte swizzle, zeros outside.
 bool make_map(CUtensorMap* m, const void* p, bool bf16, long long rows, long long cols, long long ld,
               int box_rows) {
-  const auto encode = encoder();
+  const auto encode = tensor_map_encoder();
   if (encode == nullptr) return false;
   if (rows == 1) ld = (cols + 7) / 8 * 8;  // the stride of a single row is never used
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
