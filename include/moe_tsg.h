@@ -479,6 +479,8 @@ typedef struct moe_linear_args {
   void *dw;          /* backward: out [N][K] or NULL */
   void *db;          /* backward: out [N] or NULL */
   long long ld_x, ld_w, ld_r, ld_y, ld_z, ld_dy, ld_dx, ld_dw;
+  const uint8_t *z_scales; /* backward: in [M][ceil(N / 32)] where z are the codes of an 8-bit
+                              checkpoint (moe_checkpoint), else NULL */
 } moe_linear_args;
 
 /* z = x w^T + b, y = act(z) + r: fp32 sums, y and z rounded once from fp32. */
@@ -491,6 +493,121 @@ int moe_linear(const moe_linear_args *args, moe_stream_t stream);
 size_t moe_linear_workspace(long long M, long long N);
 int moe_linear_backward(const moe_linear_args *args, void *workspace, size_t workspace_bytes,
                         moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Tokens as rows in the order of their experts, and back. n = T * topk slots: slot
+ * t * topk + j is choice j of token t.
+ * ------------------------------------------------------------------------- */
+
+/* The stable order of the n slots by expert: offsets, out [E + 1]: expert e has the rows
+ * offsets[e] .. offsets[e + 1] - 1; rows, out [n]: the row of each slot, -1 where ids is not in
+ * 0 .. E - 1; slots, out [n]: the slot of each row, -1 behind the last. A token may choose an
+ * expert twice. n is at most 2^30, E at most 1024. workspace: at least
+ * moe_sort_experts_workspace(n, E) bytes (pure host arithmetic; 0 for few slots), 16-byte aligned,
+ * used until the call has run on the stream. */
+size_t moe_sort_experts_workspace(long long n, int E);
+int moe_sort_experts(const int32_t *ids, long long n, int E, int32_t *slots, int32_t *rows,
+                     int32_t *offsets, void *workspace, size_t workspace_bytes,
+                     moe_stream_t stream);
+
+typedef struct moe_rows_args {
+  long long T, D;          /* tokens; elements of a row */
+  int topk, E;             /* topk 1..32, T * topk at most 2^30; E 1..1024 */
+  int dtype;               /* enum moe_dtype of the matrices */
+  const int32_t *rows;     /* in [T][topk], of moe_sort_experts; outside 0 .. n - 1: no row */
+  const int32_t *offsets;  /* in [E + 1]; the rows from offsets[E] on have no slot */
+  const float *w;          /* combine, backward: in [T][topk]; combine: or NULL, ones */
+  const void *x;           /* rows: in [T][D]; backward: in, the gradient of y */
+  void *y;                 /* combine: out [T][D] */
+  const void *r;           /* combine, backward: in [n][D]; backward: of dtype or e4m3 codes */
+  const uint8_t *r_scales; /* backward: in [n][ceil(D / 32)], the scales of codes, or NULL */
+  void *dr;                /* rows, backward: out [n][D] */
+  float *dw;               /* backward: out [T][topk] */
+  long long ld_x, ld_y, ld_r, ld_scales, ld_dr;
+} moe_rows_args;
+
+/* dr[rows[t][j]] = x[t]; rows without a slot are zero. */
+int moe_expert_rows(const moe_rows_args *args, moe_stream_t stream);
+
+/* y[t] = sum over j of w[t][j] * r[rows[t][j]], in the order of j in fp32, rounded once; slots without
+ * a row have no part in it. With w = NULL it is the gradient of moe_expert_rows. */
+int moe_combine_experts(const moe_rows_args *args, moe_stream_t stream);
+
+/* dr[rows[t][j]] = w[t][j] * x[t] (rows without a slot: zero) and dw[t][j] = the product of x[t]
+ * and r[rows[t][j]] (0 without a row), fp32 sums in a fixed order. */
+int moe_combine_experts_backward(const moe_rows_args *args, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Checkpoints in 8 bits: what a backward pass needs of a forward pass, in half the bytes.
+ * Blocks of 32 elements of a row (the last one of a row may be shorter) share a scale 2^s, stored
+ * as s + 127, with the least s in -127 .. 127 for which the block's largest finite |x| is at most
+ * 448 * 2^s; the code of an element is x * 2^-s rounded to e4m3, to nearest, ties to even, NaN
+ * where x is not finite. Restored, an element is within 2^-4 of itself, or within 2^-10 * 2^s.
+ * ------------------------------------------------------------------------- */
+typedef struct moe_checkpoint_args {
+  long long n, c;   /* rows; elements of a row */
+  int dtype;        /* enum moe_dtype of x */
+  void *x;          /* checkpoint: in [n][c]; restore: out */
+  void *codes;      /* checkpoint: out [n][c] e4m3; restore: in */
+  uint8_t *scales;  /* checkpoint: out [n][ceil(c / 32)]; restore: in */
+  long long ld_x, ld_codes, ld_scales;
+} moe_checkpoint_args;
+int moe_checkpoint(const moe_checkpoint_args *args, moe_stream_t stream);
+/* x = code * 2^s, rounded once to dtype (exact in fp32). */
+int moe_restore(const moe_checkpoint_args *args, moe_stream_t stream);
+
+/* Gated activation of n rows of c elements. dtype is MOE_BF16 or MOE_FP16. The scales' rows are
+ * ceil(c / 32) bytes apart, the codes' rows c. */
+typedef struct moe_gated_args {
+  long long n, c;
+  int dtype;            /* of the matrices that are not codes */
+  int act;              /* enum moe_act */
+  const void *gate;     /* in [n][c]; backward: of dtype, or codes with gate_scales */
+  const void *up;       /* in [n][c], as gate */
+  void *h;              /* out [n][c], act(gate) * up; backward: or NULL */
+  void *gate_codes, *up_codes;       /* forward: out, 8-bit checkpoints of gate and up, or all NULL */
+  uint8_t *gate_scales, *up_scales;  /* forward: out; backward: in, or NULL: gate and up of dtype */
+  const void *dh;       /* backward: in [n][c] */
+  void *dgate, *dup;    /* backward: out [n][c] */
+  long long ld_gate, ld_up, ld_h, ld_dh, ld_dgate, ld_dup;
+} moe_gated_args;
+/* h = act(gate) * up, rounded once from fp32. */
+int moe_gated(const moe_gated_args *args, moe_stream_t stream);
+/* dgate = dh * up * act'(gate), dup = dh * act(gate), h = act(gate) * up once more. */
+int moe_gated_backward(const moe_gated_args *args, moe_stream_t stream);
+
+/* The experts' matrix products: rows sorted by expert (moe_sort_experts), each expert with its own
+ * weights. dtype is MOE_BF16 or MOE_FP16; N and K are multiples of 8, E is at most 1024. All
+ * matrices but `add` have 16-byte aligned bases and leading dimensions (and strides from expert to
+ * expert) that are multiples of 8. */
+typedef struct moe_expert_linear_args {
+  long long n, N, K;      /* rows; features of y; features of x */
+  int E;
+  int dtype;              /* of all matrices but dw */
+  int dwtype;             /* of dw: dtype or MOE_FP32 */
+  const int32_t *offsets; /* in [E + 1], on the device, ascending: expert e has the rows offsets[e] to
+                             offsets[e + 1] - 1; what lies outside 0 .. n is left out */
+  const void *x;          /* in [n][K] (backward: only for dw) */
+  const void *w;          /* in [E][N][K] (backward: only for dx) */
+  void *y;                /* forward: out [n][N] */
+  const void *dy;         /* backward: in [n][N] */
+  const void *add;        /* backward: in [n][K], or NULL */
+  void *dx;               /* backward: out [n][K] or NULL */
+  void *dw;               /* backward: out [E][N][K] or NULL */
+  long long ld_x, ld_w, stride_w, ld_y, ld_dy, ld_add, ld_dx, ld_dw, stride_dw;
+} moe_expert_linear_args;
+
+/* y[r] = w[e] x[r] for the rows of every expert e, fp32 sums, rounded once; rows from offsets[E] on
+ * are zero. */
+int moe_expert_linear(const moe_expert_linear_args *args, moe_stream_t stream);
+
+/* dx[r] = w[e]^T dy[r] + add[r] (rows from offsets[E] on: add alone, or zero);
+ * dw[e] = sum over its rows of dy[r] x[r]^T (zero without rows). fp32 sums in a fixed order, rounded
+ * once. workspace: at least moe_expert_linear_workspace(E) bytes (pure host arithmetic), 256-byte
+ * aligned, for dw; used until the call has run on the stream. */
+size_t moe_expert_linear_workspace(int E);
+int moe_expert_linear_backward(const moe_expert_linear_args *args, void *workspace,
+                               size_t workspace_bytes, moe_stream_t stream);
 
 /* The device waits of the products and of layer norm are bounded; one that runs out sets a
  * sticky status of the device (its results are void). Synchronises `stream` and reads the

@@ -25,7 +25,8 @@ LIB = os.path.join(PKG, "libmoe_tsg.so")
 BINDING = os.path.join(PKG, "_torch_ops.so")
 SOURCES = ["api.cu", "plan.cu", "ffn.cu", "ffn_pair.cu", "consumer.cu", "route_scale.cu", "gate.cu",
            "plan_noalloc.cu", "gate_rows.cu", "router.cu", "norm.cu",
-           "linear.cu"]
+           "linear.cu", "expert_rows.cu", "gated.cu",
+           "expert_linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

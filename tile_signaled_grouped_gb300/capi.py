@@ -66,7 +66,41 @@ class moe_linear_args(ctypes.Structure):
         + [(f, ctypes.c_int) for f in ("dtype", "ytype", "btype", "dwtype", "act")]
         + [(f, ctypes.c_void_p) for f in ("x", "w", "b", "r", "y", "z", "dy", "dx", "dw", "db")]
         + [(f, ctypes.c_longlong) for f in ("ld_x", "ld_w", "ld_r", "ld_y", "ld_z", "ld_dy",
-                                            "ld_dx", "ld_dw")])
+                                            "ld_dx", "ld_dw")]
+        + [("z_scales", ctypes.c_void_p)])
+
+
+class moe_rows_args(ctypes.Structure):
+    _fields_ = (
+        [(f, ctypes.c_longlong) for f in ("T", "D")]
+        + [(f, ctypes.c_int) for f in ("topk", "E", "dtype")]
+        + [(f, ctypes.c_void_p) for f in ("rows", "offsets", "w", "x", "y", "r", "r_scales", "dr", "dw")]
+        + [(f, ctypes.c_longlong) for f in ("ld_x", "ld_y", "ld_r", "ld_scales", "ld_dr")])
+
+
+class moe_checkpoint_args(ctypes.Structure):
+    _fields_ = (
+        [("n", ctypes.c_longlong), ("c", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+        + [(f, ctypes.c_void_p) for f in ("x", "codes", "scales")]
+        + [(f, ctypes.c_longlong) for f in ("ld_x", "ld_codes", "ld_scales")])
+
+
+class moe_gated_args(ctypes.Structure):
+    _fields_ = (
+        [("n", ctypes.c_longlong), ("c", ctypes.c_longlong), ("dtype", ctypes.c_int),
+         ("act", ctypes.c_int)]
+        + [(f, ctypes.c_void_p) for f in ("gate", "up", "h", "gate_codes", "up_codes", "gate_scales",
+                                          "up_scales", "dh", "dgate", "dup")]
+        + [(f, ctypes.c_longlong) for f in ("ld_gate", "ld_up", "ld_h", "ld_dh", "ld_dgate", "ld_dup")])
+
+
+class moe_expert_linear_args(ctypes.Structure):
+    _fields_ = (
+        [(f, ctypes.c_longlong) for f in ("n", "N", "K")]
+        + [(f, ctypes.c_int) for f in ("E", "dtype", "dwtype")]
+        + [(f, ctypes.c_void_p) for f in ("offsets", "x", "w", "y", "dy", "add", "dx", "dw")]
+        + [(f, ctypes.c_longlong) for f in ("ld_x", "ld_w", "stride_w", "ld_y", "ld_dy", "ld_add",
+                                            "ld_dx", "ld_dw", "stride_dw")])
 
 
 def _parse_enums():
@@ -129,6 +163,18 @@ def load():
         "moe_linear": (ip, [P(moe_linear_args), vp]),
         "moe_linear_workspace": (sz, [ll, ll]),
         "moe_linear_backward": (ip, [P(moe_linear_args), vp, sz, vp]),
+        "moe_sort_experts_workspace": (sz, [ll, ip]),
+        "moe_sort_experts": (ip, [vp, ll, ip, vp, vp, vp, vp, sz, vp]),
+        "moe_expert_rows": (ip, [P(moe_rows_args), vp]),
+        "moe_combine_experts": (ip, [P(moe_rows_args), vp]),
+        "moe_combine_experts_backward": (ip, [P(moe_rows_args), vp]),
+        "moe_checkpoint": (ip, [P(moe_checkpoint_args), vp]),
+        "moe_restore": (ip, [P(moe_checkpoint_args), vp]),
+        "moe_gated": (ip, [P(moe_gated_args), vp]),
+        "moe_gated_backward": (ip, [P(moe_gated_args), vp]),
+        "moe_expert_linear": (ip, [P(moe_expert_linear_args), vp]),
+        "moe_expert_linear_workspace": (sz, [ip]),
+        "moe_expert_linear_backward": (ip, [P(moe_expert_linear_args), vp, sz, vp]),
         "moe_ops_status": (ip, [vp, P(ip), P(ip)]),
         "moe_ops_status_clear": (ip, [vp]),
         "moe_layer_norm": (ip, [P(moe_norm_args), vp]),

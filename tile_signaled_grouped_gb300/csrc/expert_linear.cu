@@ -1,0 +1,753 @@
+// The experts' matrix products on tcgen05: rows sorted by expert, each expert with its own weights.
+//
+//   forward   y[r]  = W[e] x[r]             rows r of expert e: offsets[e] .. offsets[e + 1] - 1
+//   backward  dx[r] = W[e]^T dy[r] + add[r]
+//             dW[e] = sum over e's rows of dy[r] x[r]^T
+//
+// How many rows an expert has is known on the device only, and is uneven. So the rows are the columns
+// of the products y^T = W x^T and dx^T = W^T dy^T, whose number a tcgen05.mma takes in steps of 32, and the
+// 256 features of a CTA pair's tile are its rows: an expert with 40 rows costs 64 columns where it would
+// cost a whole tile of 128 or 256 rows. In dW the rows are summed over: tensor maps of each expert's
+// rows, made on the device, fill with zeros what lies past them.
+#include <algorithm>
+#include <atomic>
+
+#include "mma_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxStages = 8;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kFeatures = 256;                  // of a pair's tile
+constexpr int kRows = 256;                      // of a pair's tile at most
+constexpr int kRowStep = 32;                    // columns of a product come in this step
+constexpr int kABytes = 128 * 128;              // a CTA's features of a stage
+constexpr int kStageBytes = kABytes + 128 * 128;  // and half of the pair's rows
+constexpr int kPatchPitch = 80;                 // bytes of a row of 32 features, on 16 bytes
+constexpr int kPatchBytes = kEpiWarps * 32 * kPatchPitch;
+
+struct PairSmem {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  int scratch[33];
+};
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t cl_bar, int x,
+                                                 int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cl_bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// An expert's rows: whatever the offsets hold, inside 0 .. n.
+__device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int E, int n, int* start, int* count) {
+  const int lo = min(max(__ldg(offsets + e), 0), n);
+  const int hi = e < E ? min(max(__ldg(offsets + e + 1), lo), n) : n;
+  *start = lo;
+  *count = hi - lo;
+}
+
+// The barriers and the tensor memory of a pair; both CTAs have them when it returns.
+__device__ __forceinline__ void pair_setup(PairSmem& sm, int stages, int warp) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&sm.full[i], 1);   // rank 0: its arrive.expect_tx (bytes of both CTAs)
+      mbar_init(&sm.empty[i], 1);  // the leader's commit (multicast)
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.tfull[i], 1);              // the leader's commit (multicast)
+      mbar_init(&sm.tempty[i], 2 * kEpiWarps); // rank 0: both CTAs' epilogue warps
+    }
+    mbar_init(&sm.drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    sm.abort = 0;
+  }
+  if (warp == 1) tmem_alloc_pair(&sm.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+}
+// Both CTAs meet: the leader's products (which read both CTAs' shared memory and write both
+// CTAs' TMEM) are done, every copy has landed and every accumulator is read.
+__device__ __forceinline__ void pair_teardown(uint32_t tmem, int warp) {
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+// The loads' warp, at its end: every copy this CTA issued has landed once the products that read its stage
+// are done (with a limit).
+__device__ __forceinline__ void wait_copies(PairSmem& sm, int issued, int stages, uint32_t* status) {
+  volatile int never = 0;
+  const unsigned long long t0 = globaltimer();
+  for (int i = max(0, issued - stages); i < issued; ++i) {
+    const long long left = kWaitNs - (long long)(globaltimer() - t0);
+    pwait(&sm.empty[i % stages], (i / stages) & 1, &never, left > 0 ? left : 0, status, 0x42000000u);
+  }
+}
+// The products' warp, at its end: every product issued is done.
+__device__ __forceinline__ void wait_products(PairSmem& sm, uint32_t* status) {
+  if (elect_one()) tc_commit_pair(&sm.drain, 0x1);
+  __syncwarp();
+  volatile int never = 0;
+  pwait(&sm.drain, 0, &never, kWaitNs, status, 0x43000000u);
+}
+
+// ------------------------------------------------------------------- y and dx
+struct RowsArgs {
+  CUtensorMap tw, tx;  // weights (3-D: experts outermost), rows
+  const int32_t* offsets;
+  void* y;             // [n][ld_y]
+  const void* add;     // [n][ld_add] or null
+  long long ld_y, ld_add;
+  uint32_t* status;
+  int n, E, J, nk;     // J: features of y; nk: 64-element blocks of the sum
+  int tiles_j, stages;
+  bool bf16, w_mn;     // w_mn: W^T, whose features are innermost
+};
+
+// The table of the experts' rows in shared memory, entry E for the rows behind the last expert's
+// (zeros): first row, number, and the tiles of rows before it. An expert's rows are shared out evenly
+// over its tiles.
+struct Table {
+  int *start, *count, *first;
+  int tiles;  // of rows, all of them
+};
+__host__ __device__ constexpr size_t table_bytes(int E) { return (size_t)(3 * (E + 1) + 3) / 4 * 16; }
+__device__ __forceinline__ Table make_table(const RowsArgs& a, int* at, int* scratch) {
+  Table t{at, at + a.E + 1, at + 2 * (a.E + 1), 0};
+  constexpr int kEach = (kMaxExperts + kThreads) / kThreads;  // neighbouring entries a thread
+  int tiles[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x * kEach + i;
+    tiles[i] = 0;
+    if (e <= a.E) {
+      int start, count;
+      rows_of(a.offsets, e, a.E, a.n, &start, &count);
+      t.start[e] = start;
+      t.count[e] = count;
+      tiles[i] = (count + kRows - 1) / kRows;
+    }
+    sum += tiles[i];
+  }
+  int at_tile = block_excl_scan(sum, scratch, &t.tiles);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x * kEach + i;
+    if (e <= a.E) t.first[e] = at_tile;
+    at_tile += tiles[i];
+  }
+  __syncthreads();
+  return t;
+}
+
+// The tiles of a pair: p, p + pairs, ... of the order expert, feature tile, tile of rows, so that
+// tiles that share their weights are neighbours. Every role of both CTAs walks the same.
+struct RowWalk {
+  const RowsArgs& a;
+  const Table& t;
+  int at, pairs;
+  int e, j0, row0, rows, cols;  // the tile: expert, first feature, first row, rows, rows rounded up
+
+  __device__ __forceinline__ RowWalk(const RowsArgs& args, const Table& table, int pair, int n)
+      : a(args), t(table), at(pair - n), pairs(n), e(0), j0(0), row0(0), rows(0), cols(0) {}
+  __device__ __forceinline__ bool next() {
+    at += pairs;
+    const int tile = at / a.tiles_j;
+    if (tile >= t.tiles) return false;
+    int lo = 0, hi = a.E + 1;  // the last expert whose first tile is not past it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (t.first[mid] <= tile)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    e = lo;
+    const int tiles = (t.count[e] + kRows - 1) / kRows, local = at - t.first[e] * a.tiles_j;
+    const int tj = local / tiles, ti = local - tj * tiles;
+    const int per = tiles > 8 ? kRows : ((t.count[e] + tiles - 1) / tiles + kRowStep - 1) / kRowStep * kRowStep;
+    j0 = tj * kFeatures;
+    row0 = t.start[e] + ti * per;
+    rows = min(per, t.count[e] - ti * per);
+    cols = (rows + kRowStep - 1) / kRowStep * kRowStep;
+    return true;
+  }
+  __device__ __forceinline__ int steps() const { return e < a.E ? a.nk : 0; }
+};
+
+__device__ __forceinline__ uint16_t to_16bit(float v, bool bf16) {
+  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expert_rows_product_kernel(const __grid_constant__ RowsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* patches = base + (size_t)a.stages * kStageBytes;
+  int* table_at = reinterpret_cast<int*>(patches + kPatchBytes);
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kPatchBytes + table_bytes(a.E));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const bool lead = crank == 0;
+  pair_setup(sm, a.stages, warp);
+  const uint32_t tmem = sm.tmem;
+  wait_prior_grid();
+  const Table table = make_table(a, table_at, sm.scratch);
+  RowWalk walk(a, table, blockIdx.x >> 1, gridDim.x >> 1);
+
+  if (warp == 0) {
+    int n = 0, st = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    while (ok && walk.next()) {
+      const int j = walk.j0 + (int)crank * 128, half = walk.cols / 2;
+      const int row = walk.row0 + (int)crank * half, boxes = (half + 31) / 32, steps = walk.steps();
+      const uint32_t bytes = 2 * (kABytes + boxes * 4096);
+      for (int kb = 0; kb < steps; ++kb, ++n) {
+        if (!warp_pwait(&sm.empty[st], phase, &sm.abort, a.status, 0x41000000u)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* as = base + (size_t)st * kStageBytes;
+          uint8_t* bs = as + kABytes;
+          if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
+          const uint32_t fb = map_shared(&sm.full[st], 0);
+          const int k0 = kb * kBlockK;
+          if (a.w_mn) {
+            tma_load_3d_pair(as, &a.tw, fb, j, k0, walk.e);
+            tma_load_3d_pair(as + 8192, &a.tw, fb, j + 64, k0, walk.e);
+          } else {
+            tma_load_3d_pair(as, &a.tw, fb, k0, j, walk.e);
+          }
+          for (int b = 0; b < boxes; ++b) tma_load_2d_pair(bs + b * 4096, &a.tx, fb, k0, row + b * 32);
+        }
+        __syncwarp();
+        next_stage(st, phase, a.stages);
+      }
+    }
+    wait_copies(sm, n, a.stages, a.status);
+  } else if (warp == 1 && lead) {
+    const uint32_t s0 = (smem_u32(base) & 0x3FFFFu) >> 4;
+    const uint64_t da = (a.w_mn ? sdesc_mn_sw128(0) : sdesc_k_sw128(0)) + s0;
+    const uint64_t db = sdesc_k_sw128(0) + s0 + (kABytes >> 4);
+    const uint32_t step_a = (a.w_mn ? 2048 : 32) >> 4;
+    int it = 0, st = 0;
+    uint32_t phase = 0, at = 0;  // at: the stage's offset in 16-byte units
+    bool ok = true;
+    for (; ok && walk.next(); ++it) {
+      const uint32_t idesc = idesc_16bit(a.bf16, a.w_mn, false, kFeatures, walk.cols);
+      const int acc = it & 1, steps = walk.steps();
+      if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, a.status, 0x44000000u)) break;
+      tc_fence_after();
+      const uint32_t dt = tmem + (uint32_t)(acc * kRows);
+      for (int kb = 0; kb < steps; ++kb) {
+        if (!warp_pwait(&sm.full[st], phase, &sm.abort, a.status, 0x45000000u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            tc_mma_pair(dt, da + at + k * step_a, db + at + k * (32 >> 4), idesc, (kb | k) != 0 ? 1u : 0u);
+          tc_commit_pair(&sm.empty[st], 0x3);
+        }
+        __syncwarp();
+        next_stage(st, phase, a.stages);
+        at = st == 0 ? 0 : at + (kStageBytes >> 4);
+      }
+      if (ok && elect_one()) tc_commit_pair(&sm.tfull[acc], 0x3);
+      __syncwarp();
+    }
+    wait_products(sm, a.status);
+  } else if (warp >= 2) {
+    // A warp has 32 features (its lane quarter of TMEM) and every other 32 rows of the tile. Turned
+    // round in shared memory, four lanes store the 32 features of a row.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
+    uint8_t* patch = patches + (warp - 2) * 32 * kPatchPitch;
+    unsigned short* y = static_cast<unsigned short*>(a.y);
+    const unsigned short* add = static_cast<const unsigned short*>(a.add);
+    for (int it = 0; walk.next(); ++it) {
+      const int acc = it & 1;
+      if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, a.status, 0x46000000u)) break;
+      tc_fence_after();
+      const int f0 = walk.j0 + (int)crank * 128 + q * 32, nf = a.J - f0;
+      const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kRows);
+      const int chunks = (walk.rows + 31) / 32;
+      const bool zero = walk.e == a.E;
+      int c = half;
+      do {
+        uint32_t v[32];
+        __syncwarp();  // the stores before may have parted it; the load wants it whole
+        if (c < chunks) {
+          tmem_ld32(src + c * 32, v);
+          tmem_ld_wait();
+        }
+        if (c + 2 >= chunks) {  // the accumulator is read: it may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+        }
+        if (c < chunks && nf > 0) {
+          const long long r0 = walk.row0 + c * 32;
+          const int rows = min(32, walk.rows - c * 32);
+          if (a.add != nullptr) {
+            const unsigned short* p = add + r0 * a.ld_add + f0 + lane;
+            uint16_t u[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) u[x] = lane < nf && x < rows ? __ldg(p + x * a.ld_add) : (uint16_t)0;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float f = a.bf16 ? __uint_as_float((uint32_t)u[x] << 16) : __half2float(__ushort_as_half(u[x]));
+              v[x] = __float_as_uint((zero ? 0.f : __uint_as_float(v[x])) + f);
+            }
+          } else if (zero) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = 0;
+          }
+          __syncwarp();  // the patch's last readers
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            *reinterpret_cast<uint16_t*>(patch + x * kPatchPitch + lane * 2) = to_16bit(__uint_as_float(v[x]), a.bf16);
+          __syncwarp();
+          const int f = (lane & 3) * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = (lane >> 2) + 8 * i;
+            const uint4 u = *reinterpret_cast<const uint4*>(patch + x * kPatchPitch + f * 2);
+            if (x < rows && f < nf) *reinterpret_cast<uint4*>(y + (r0 + x) * a.ld_y + f0 + f) = u;
+          }
+        }
+        c += 2;
+      } while (c < chunks);
+    }
+  }
+  pair_teardown(tmem, warp);
+}
+
+// ------------------------------------------------------------------- dW
+struct WeightArgs {
+  const CUtensorMap* maps;  // [E][2]: an expert's rows of dy and of x
+  const int32_t* offsets;
+  void* dw;                 // [E][N][K], rows ld apart, experts `stride`
+  long long ld, stride;
+  uint32_t* status;
+  int n, E, N, K;
+  int tiles_i, tiles_j, stages;
+  bool bf16, fp32;          // of the operands; of dw
+  bool wide;                // rows of dw start on 32 bytes
+};
+
+// Tensor maps of every expert's rows, from maps of all rows: a map's first row and number of rows are
+// the expert's, so that copies read zeros past its last row. Experts without rows have none (theirs are
+// not read).
+struct MapArgs {
+  CUtensorMap ty, tx;
+  const int32_t* offsets;
+  const char *dy, *x;
+  long long row_y, row_x;  // bytes of a row
+  CUtensorMap* maps;
+  int n, E;
+};
+__global__ void __launch_bounds__(32) expert_maps_kernel(const __grid_constant__ MapArgs a) {
+  __shared__ alignas(128) uint32_t map[2][32];
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x, e = blockIdx.x;
+  int start, count;
+  rows_of(a.offsets, e, a.E, a.n, &start, &count);
+  if (count == 0) return;
+  map[0][lane] = reinterpret_cast<const uint32_t*>(&a.ty)[lane];
+  map[1][lane] = reinterpret_cast<const uint32_t*>(&a.tx)[lane];
+  __syncwarp();
+  if (lane < 2) {
+    const uint32_t at = smem_u32(map[lane]);
+    const char* rows = lane == 0 ? a.dy + start * a.row_y : a.x + start * a.row_x;
+    asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(at), "l"(rows)
+                 : "memory");
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(at), "r"(count)
+                 : "memory");
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+            a.maps + 2 * e + i),
+        "r"(smem_u32(map[i]))
+        : "memory");
+}
+__device__ __forceinline__ void acquire_map(const CUtensorMap* m) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
+}
+
+// The tiles of a pair: p, p + pairs, ... of the order expert, columns, rows of dW.
+struct WeightWalk {
+  const WeightArgs& a;
+  int at, pairs;
+  int e, i0, j0, steps;
+
+  __device__ __forceinline__ WeightWalk(const WeightArgs& args, int pair, int n)
+      : a(args), at(pair - n), pairs(n), e(0), i0(0), j0(0), steps(0) {}
+  __device__ __forceinline__ bool next() {
+    at += pairs;
+    const int per = a.tiles_i * a.tiles_j;
+    e = at / per;
+    if (e >= a.E) return false;
+    const int local = at - e * per, tj = local / a.tiles_i;
+    i0 = (local - tj * a.tiles_i) * 256;
+    j0 = tj * 256;
+    int start, count;
+    rows_of(a.offsets, e, a.E, a.n, &start, &count);
+    steps = (count + kBlockK - 1) / kBlockK;
+    return true;
+  }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expert_weights_kernel(const __grid_constant__ WeightArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(base + (size_t)a.stages * kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const bool lead = crank == 0;
+  pair_setup(sm, a.stages, warp);
+  const uint32_t tmem = sm.tmem;
+  wait_prior_grid();
+  WeightWalk walk(a, blockIdx.x >> 1, gridDim.x >> 1);
+
+  if (warp == 0) {
+    constexpr uint32_t bytes = 2 * kStageBytes;
+    int n = 0, st = 0, expert = -1;
+    uint32_t phase = 1;
+    bool ok = true;
+    while (ok && walk.next()) {
+      const CUtensorMap* ty = a.maps + 2 * walk.e;
+      const CUtensorMap* tx = ty + 1;
+      if (walk.e != expert && walk.steps > 0) {
+        acquire_map(ty);
+        acquire_map(tx);
+        expert = walk.e;
+      }
+      const int i = walk.i0 + (int)crank * 128, j = walk.j0 + (int)crank * 128;
+      for (int kb = 0; kb < walk.steps; ++kb, ++n) {
+        if (!warp_pwait(&sm.empty[st], phase, &sm.abort, a.status, 0x51000000u)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* as = base + (size_t)st * kStageBytes;
+          uint8_t* bs = as + kABytes;
+          if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
+          const uint32_t fb = map_shared(&sm.full[st], 0);
+          const int k0 = kb * kBlockK;
+          tma_load_2d_pair(as, ty, fb, i, k0);
+          tma_load_2d_pair(as + 8192, ty, fb, i + 64, k0);
+          tma_load_2d_pair(bs, tx, fb, j, k0);
+          tma_load_2d_pair(bs + 8192, tx, fb, j + 64, k0);
+        }
+        __syncwarp();
+        next_stage(st, phase, a.stages);
+      }
+    }
+    wait_copies(sm, n, a.stages, a.status);
+  } else if (warp == 1 && lead) {
+    const uint32_t idesc = idesc_16bit(a.bf16, true, true, 256, 256);
+    const uint32_t s0 = (smem_u32(base) & 0x3FFFFu) >> 4;
+    const uint64_t da = sdesc_mn_sw128(0) + s0, db = da + (kABytes >> 4);
+    int it = 0, st = 0;
+    uint32_t phase = 0, at = 0;
+    bool ok = true;
+    for (; ok && walk.next(); ++it) {
+      const int acc = it & 1;
+      if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, a.status, 0x54000000u)) break;
+      tc_fence_after();
+      const uint32_t dt = tmem + (uint32_t)(acc * 256);
+      for (int kb = 0; kb < walk.steps; ++kb) {
+        if (!warp_pwait(&sm.full[st], phase, &sm.abort, a.status, 0x55000000u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            tc_mma_pair(dt, da + at + k * (2048 >> 4), db + at + k * (2048 >> 4), idesc, (kb | k) != 0 ? 1u : 0u);
+          tc_commit_pair(&sm.empty[st], 0x3);
+        }
+        __syncwarp();
+        next_stage(st, phase, a.stages);
+        at = st == 0 ? 0 : at + (kStageBytes >> 4);
+      }
+      if (ok && elect_one()) tc_commit_pair(&sm.tfull[acc], 0x3);
+      __syncwarp();
+    }
+    wait_products(sm, a.status);
+  } else if (warp >= 2) {
+    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the columns
+    const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
+    for (int it = 0; walk.next(); ++it) {
+      const int acc = it & 1;
+      if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, a.status, 0x56000000u)) break;
+      tc_fence_after();
+      const int i = walk.i0 + (int)crank * 128 + q * 32 + lane;
+      const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+#pragma unroll 1
+      for (int c = half * 128; c < half * 128 + 128; c += 32) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(src + c, v);
+        tmem_ld_wait();
+        if (c == half * 128 + 96) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+        }
+        if (walk.steps == 0) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = 0;
+        }
+        const int j = walk.j0 + c, nj = a.K - j;
+        if (i >= a.N || nj <= 0) continue;
+        const long long to = walk.e * a.stride + i * a.ld + j;
+        if (a.fp32) {
+          float* p = static_cast<float*>(a.dw) + to;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (8 * x >= nj) break;
+            if (a.wide) {
+              st_global_v8(p + 8 * x, v + 8 * x);
+            } else {
+              reinterpret_cast<uint4*>(p)[2 * x] = make_uint4(v[8 * x], v[8 * x + 1], v[8 * x + 2], v[8 * x + 3]);
+              reinterpret_cast<uint4*>(p)[2 * x + 1] =
+                  make_uint4(v[8 * x + 4], v[8 * x + 5], v[8 * x + 6], v[8 * x + 7]);
+            }
+          }
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float lo = __uint_as_float(v[2 * x]), hi = __uint_as_float(v[2 * x + 1]);
+            w[x] = a.bf16 ? pack2<__nv_bfloat16>(lo, hi) : pack2<__half>(lo, hi);
+          }
+          unsigned short* p = static_cast<unsigned short*>(a.dw) + to;
+          if (a.wide && nj >= 32) {
+            st_global_v8(p, w);
+            st_global_v8(p + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (8 * x < nj)
+                reinterpret_cast<uint4*>(p)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          }
+        }
+      }
+    }
+  }
+  pair_teardown(tmem, warp);
+}
+
+// ------------------------------------------------------------------- host side
+// Map of a matrix of 16-bit elements, [rows][cols] or [experts][rows][cols]: boxes of box_rows x 64
+// columns, 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap* m, const void* p, bool bf16, long long experts, long long rows, long long cols,
+              long long ld, long long stride, int box_rows) {
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  if (rows == 1) ld = cols;  // the stride of a single row, or expert, is never used
+  if (experts == 1) stride = rows * ld;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)experts};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, experts > 0 ? 3 : 2,
+                const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr long long kMaxSize = INT32_MAX / 2;
+
+int check_experts(const moe_expert_linear_args* p) {
+  if (p == nullptr) return MOE_ERR_ARG;
+  if (p->dtype != MOE_BF16 && p->dtype != MOE_FP16) return MOE_ERR_ARG;
+  if (p->n < 0 || p->n > kMaxSize || p->N < 8 || p->N > kMaxSize || p->K < 8 || p->K > kMaxSize || p->N % 8 != 0 ||
+      p->K % 8 != 0 || p->E < 1 || p->E > kMaxExperts || p->offsets == nullptr || !aligned_to(p->offsets, 4))
+    return MOE_ERR_ARG;
+  return MOE_OK;
+}
+// Rows on 16 bytes.
+bool check_matrix(const void* q, long long ld, long long rows, long long cols) {
+  return q != nullptr && aligned_to(q, 16) && (rows <= 1 || (ld >= cols && ld % 8 == 0 && ld <= INT32_MAX));
+}
+bool check_weights(const void* q, long long ld, long long stride, const moe_expert_linear_args* p) {
+  return check_matrix(q, ld, p->N, p->K) &&
+         (p->E == 1 || (stride % 8 == 0 && stride >= (p->N - 1) * ld + p->K && stride <= 1LL << 38));
+}
+int launched(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+size_t smem_bytes(int stages, size_t more) { return 1024 + (size_t)stages * kStageBytes + more + sizeof(PairSmem); }
+int stages_for(size_t more) {
+  return std::min<int>(kMaxStages, (int)((kSmemMax - smem_bytes(0, more)) / kStageBytes));
+}
+
+// y of the forward pass, or dx: `w_mn` takes W^T.
+int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x, bool w_mn, const void* add,
+                 long long ld_add, void* y, long long ld_y, int sms, cudaStream_t s) {
+  RowsArgs a{};
+  a.bf16 = p->dtype == MOE_BF16;
+  a.w_mn = w_mn;
+  a.n = (int)p->n;
+  a.E = p->E;
+  a.J = (int)(w_mn ? p->K : p->N);
+  const long long sum = w_mn ? p->N : p->K;
+  a.nk = (int)((sum + kBlockK - 1) / kBlockK);
+  a.tiles_j = (a.J + kFeatures - 1) / kFeatures;
+  a.offsets = p->offsets;
+  a.y = y;
+  a.ld_y = ld_y;
+  a.add = add;
+  a.ld_add = ld_add;
+  a.status = ops_status();
+  if (a.status == nullptr || !make_map(&a.tw, p->w, a.bf16, p->E, p->N, p->K, p->ld_w, p->stride_w, w_mn ? 64 : 128) ||
+      !make_map(&a.tx, x, a.bf16, 0, p->n, sum, ld_x, 0, 32))
+    return MOE_ERR_CUDA;
+  // Tiles of rows: one for every 256 and one more for each expert at most.
+  const long long tiles = (p->n / kRows + std::min<long long>(p->E + 1, p->n)) * a.tiles_j;
+  if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  const size_t more = kPatchBytes + table_bytes(a.E);
+  a.stages = stages_for(more);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(expert_rows_product_kernel), &ready);
+  if (e == cudaSuccess)
+    e = launch_behind(expert_rows_product_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)),
+                      dim3(kThreads), smem_bytes(a.stages, more), s, a);
+  return launched(e);
+}
+
+int weights_product(const moe_expert_linear_args* p, void* workspace, int sms, cudaStream_t s) {
+  MapArgs m{};
+  const bool bf16 = p->dtype == MOE_BF16;
+  m.offsets = p->offsets;
+  m.dy = static_cast<const char*>(p->dy);
+  m.x = static_cast<const char*>(p->x);
+  m.row_y = p->ld_dy * 2;
+  m.row_x = p->ld_x * 2;
+  m.maps = static_cast<CUtensorMap*>(workspace);
+  m.n = (int)p->n;
+  m.E = p->E;
+  if (!make_map(&m.ty, p->dy, bf16, 0, p->n, p->N, p->ld_dy, 0, 64) ||
+      !make_map(&m.tx, p->x, bf16, 0, p->n, p->K, p->ld_x, 0, 64))
+    return MOE_ERR_CUDA;
+  WeightArgs a{};
+  a.maps = m.maps;
+  a.offsets = p->offsets;
+  a.dw = p->dw;
+  a.ld = p->ld_dw;
+  a.stride = p->stride_dw;
+  a.status = ops_status();
+  if (a.status == nullptr) return MOE_ERR_CUDA;
+  a.n = (int)p->n;
+  a.E = p->E;
+  a.N = (int)p->N;
+  a.K = (int)p->K;
+  a.tiles_i = (a.N + 255) / 256;
+  a.tiles_j = (a.K + 255) / 256;
+  a.bf16 = bf16;
+  a.fp32 = p->dwtype == MOE_FP32;
+  const int per = a.fp32 ? 8 : 16;  // elements of 32 bytes
+  a.wide = aligned_to(p->dw, 32) && a.ld % per == 0 && a.stride % per == 0;
+  const long long tiles = (long long)a.tiles_i * a.tiles_j * a.E;
+  if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  a.stages = stages_for(0);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(expert_weights_kernel), &ready);
+  if (e == cudaSuccess) e = launch_behind(expert_maps_kernel, dim3(p->E), dim3(32), 0, s, m);
+  if (e == cudaSuccess)
+    e = launch_behind(expert_weights_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(kThreads),
+                      smem_bytes(a.stages, 0), s, a);
+  return launched(e);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_expert_linear(const moe_expert_linear_args* p, moe_stream_t stream) {
+  int rc = check_experts(p);
+  if (rc != MOE_OK) return rc;
+  if (p->n == 0) return MOE_OK;
+  if (!check_matrix(p->x, p->ld_x, p->n, p->K) || !check_weights(p->w, p->ld_w, p->stride_w, p) ||
+      !check_matrix(p->y, p->ld_y, p->n, p->N))
+    return MOE_ERR_ARG;
+  int sms = 0;
+  rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  return rows_product(p, p->x, p->ld_x, false, nullptr, 0, p->y, p->ld_y, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_expert_linear_workspace(int E) {
+  return E < 1 || E > kMaxExperts ? 0 : (size_t)E * 2 * sizeof(CUtensorMap);
+}
+
+int moe_expert_linear_backward(const moe_expert_linear_args* p, void* workspace, size_t workspace_bytes,
+                               moe_stream_t stream) {
+  int rc = check_experts(p);
+  if (rc != MOE_OK) return rc;
+  if (p->dwtype != p->dtype && p->dwtype != MOE_FP32) return MOE_ERR_ARG;
+  if (p->dw != nullptr && !check_weights(p->dw, p->ld_dw, p->stride_dw, p)) return MOE_ERR_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if (p->n == 0) {  // no rows: the weights' gradients are zero
+    if (p->dw == nullptr) return MOE_OK;
+    rc = ops_device(&sms);
+    if (rc != MOE_OK) return rc;
+    const size_t b = (size_t)type_bytes(p->dwtype), row = (size_t)p->K * b;
+    for (int e = 0; e < p->E; ++e)
+      if (cudaMemset2DAsync(static_cast<char*>(p->dw) + (size_t)e * p->stride_dw * b,
+                            p->N > 1 ? (size_t)p->ld_dw * b : row, 0, row, (size_t)p->N, s) != cudaSuccess)
+        return launched(cudaErrorUnknown);
+    return MOE_OK;
+  }
+  if (!check_matrix(p->dy, p->ld_dy, p->n, p->N) ||
+      (p->dx != nullptr && (!check_matrix(p->dx, p->ld_dx, p->n, p->K) ||
+                            !check_weights(p->w, p->ld_w, p->stride_w, p) || !aligned_to(p->add, 2) ||
+                            (p->add != nullptr && p->n > 1 && p->ld_add < p->K))) ||
+      (p->dw != nullptr && (!check_matrix(p->x, p->ld_x, p->n, p->K) || workspace == nullptr ||
+                            !aligned_to(workspace, 256))))
+    return MOE_ERR_ARG;
+  if (p->dw != nullptr && workspace_bytes < moe_expert_linear_workspace(p->E)) return MOE_ERR_WORKSPACE;
+  rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  if (p->dx != nullptr)
+    rc = rows_product(p, p->dy, p->ld_dy, true, p->add, p->ld_add, p->dx, p->ld_dx, sms, s);
+  if (rc == MOE_OK && p->dw != nullptr) rc = weights_product(p, workspace, sms, s);
+  return rc;
+}
+
+}  // extern "C"

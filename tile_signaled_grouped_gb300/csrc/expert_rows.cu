@@ -1,0 +1,517 @@
+// Tokens as rows in the order of their experts, and back.
+//
+//   sort      slots (token t, choice j: t topk + j) by expert, earlier slots first:
+//             offsets[e] .. offsets[e + 1] are expert e's rows, rows[slot] a slot's row, slots[row]
+//             a row's slot
+//   rows      r[rows[t, j]] = x[t]
+//   combine   y[t] = sum_j w[t, j] r[rows[t, j]]           (w = 1: the gradient of x from that of r)
+//   backward  dr[rows[t, j]] = w[t, j] dy[t],  dw[t, j] = <dy[t], r[rows[t, j]]>
+//
+// A slot whose expert is out of range has no row (-1), and the rows behind the last are zero. Every
+// row that is read from `rows` is checked against the matrix: an index out of range is no row.
+#include <algorithm>
+#include <atomic>
+
+#include "eight_bits.cuh"
+#include "moe_common.cuh"
+#include "ops_common.cuh"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------- the order
+// A counting sort. The slots are cut into at most kSortChunks chunks of whole warps' ranges; a CTA
+// counts its chunk's experts by warp, and after a scan over the experts, the chunks before and its
+// warps, every warp walks its range in order and hands out rows: a slot's row is its warp's next one
+// of its expert and the lanes before it with the same expert. Integer sums, so the order of
+// the counting does not matter, and the result is the stable order always. One chunk (up to 4096
+// slots) is one launch; otherwise a first launch leaves the chunks' counts.
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortSlots = 8;      // slots of a lane at least
+constexpr int kSortChunks = 148;   // a chunk is a CTA's work, and all of them are read by each
+constexpr int kSortMaxExperts = 1024;
+
+struct SortArgs {
+  const int32_t* ids;
+  int32_t *slots, *rows, *offsets;
+  int32_t* counts;  // [chunks][E], with more than one chunk
+  int n, E, per;    // per: slots of a lane
+};
+
+// Expert of a slot, E for none.
+__device__ __forceinline__ int expert_at(const SortArgs& a, long long i, long long end) {
+  if (i >= end) return a.E;
+  const int e = __ldg(a.ids + i);
+  return (unsigned)e < (unsigned)a.E ? e : a.E;
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ int count[kSortMaxExperts];
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) count[e] = 0;
+  __syncthreads();
+  allow_dependent_launch();
+  wait_prior_grid();
+  const long long lo = (long long)blockIdx.x * kSortThreads * a.per;
+  const long long end = min((long long)a.n, lo + (long long)kSortThreads * a.per);
+  for (long long i = lo + threadIdx.x; i < end; i += kSortThreads) {
+    const int e = expert_at(a, i, end);
+    if (e < a.E) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) a.counts[(size_t)blockIdx.x * a.E + e] = count[e];
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ int next[];  // [warps][E]: counts, then every warp's next row of each expert
+  __shared__ int scratch[33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) next[i] = 0;
+  __syncthreads();
+  allow_dependent_launch();
+  wait_prior_grid();
+  const long long lo = ((long long)blockIdx.x * kSortWarps + warp) * 32 * a.per;
+  const long long end = min((long long)a.n, lo + 32LL * a.per);
+  int* mine = next + warp * a.E;
+  for (long long i = lo + lane; i < end; i += 32) {
+    const int e = expert_at(a, i, end);
+    if (e < a.E) atomicAdd(&mine[e], 1);
+  }
+  __syncthreads();
+  // Two neighbouring experts a thread: their rows of all chunks, and of the chunks before this one.
+  int all[2] = {0, 0}, before[2] = {0, 0};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int e = 2 * threadIdx.x + h;
+    if (e >= a.E) continue;
+    if (gridDim.x > 1) {
+#pragma unroll 8
+      for (int c = 0; c < (int)gridDim.x; ++c) {
+        const int v = __ldcg(a.counts + (size_t)c * a.E + e);
+        all[h] += v;
+        before[h] += c < (int)blockIdx.x ? v : 0;
+      }
+    } else {
+      for (int w = 0; w < kSortWarps; ++w) all[h] += next[w * a.E + e];
+    }
+  }
+  int total;
+  const int first = block_excl_scan(all[0] + all[1], scratch, &total);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int e = 2 * threadIdx.x + h;
+    if (e >= a.E) continue;
+    int at = first + (h == 1 ? all[0] : 0);
+    if (blockIdx.x == 0) a.offsets[e] = at;
+    at += before[h];
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int v = next[w * a.E + e];
+      next[w * a.E + e] = at;
+      at += v;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = total;
+  __syncthreads();
+  for (long long i0 = lo; i0 < end; i0 += 32) {  // whole warps
+    const long long i = i0 + lane;
+    const int e = expert_at(a, i, end);
+    const uint32_t same = __match_any_sync(kAll, e);
+    int row = -1;
+    if (e < a.E) row = mine[e] + __popc(same & ((1u << lane) - 1));
+    __syncwarp();
+    if (e < a.E && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+    if (i < end) a.rows[i] = row;
+    if (row >= 0) a.slots[row] = (int)i;
+  }
+  const long long all_threads = (long long)gridDim.x * kSortThreads;
+  for (long long r = total + (long long)blockIdx.x * kSortThreads + threadIdx.x; r < a.n; r += all_threads)
+    a.slots[r] = -1;
+}
+
+// ------------------------------------------------------------------- rows
+struct RowsArgs {
+  const void* x;         // rows: [T][ld_x]; backward: dy [T][ld_x]
+  void* y;               // combine: out [T][ld_x]
+  const void* r;         // combine, backward: [n][ld_r], or codes
+  void* dr;              // rows, backward: out [n][ld_d]
+  const uint8_t* scales; // backward: [n][ld_s] of the codes
+  const float* w;        // [T][topk] or null
+  float* dw;             // backward: out [T][topk]
+  const int32_t* rows;   // [T][topk]
+  const int32_t* total;  // offsets[E]
+  long long T, n, D, ld_x, ld_r, ld_d, ld_s;  // D, ld_x and ld_d of the copy: in its units
+  int topk;
+};
+
+// The row of a slot, or -1.
+__device__ __forceinline__ int row_of(const RowsArgs& a, long long slot) {
+  const int r = __ldg(a.rows + slot);
+  return r >= 0 && r < a.n ? r : -1;
+}
+
+// Copies of token rows in units U of 16 bytes (or of one element, where rows do not start on 16
+// bytes). A warp takes 128 units of a token: it reads them once and writes them to the token's
+// topk rows. Bound by the bytes written.
+constexpr int kRowWarps = 8, kCopyUnits = 4;
+template <typename U>
+__global__ void __launch_bounds__(32 * kRowWarps) expert_rows_kernel(const __grid_constant__ RowsArgs a) {
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * kRowWarps;
+  const long long me = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const long long chunks = (a.D + 32 * kCopyUnits - 1) / (32 * kCopyUnits);
+  const U* x = static_cast<const U*>(a.x);
+  U* out = static_cast<U*>(a.dr);
+  for (long long u = me; u < a.T * chunks; u += warps) {
+    const long long t = u / chunks, c = (u - t * chunks) * 32 * kCopyUnits + lane;
+    const int mine = lane < a.topk ? row_of(a, t * a.topk + lane) : -1;
+    U v[kCopyUnits];
+#pragma unroll
+    for (int i = 0; i < kCopyUnits; ++i)
+      if (c + 32 * i < a.D) v[i] = __ldg(x + t * a.ld_x + c + 32 * i);
+    for (int j = 0; j < a.topk; ++j) {
+      const int row = __shfl_sync(kAll, mine, j);
+      if (row < 0) continue;
+#pragma unroll
+      for (int i = 0; i < kCopyUnits; ++i)
+        if (c + 32 * i < a.D) out[row * a.ld_d + c + 32 * i] = v[i];
+    }
+  }
+  const long long total = min(max((long long)__ldg(a.total), 0LL), a.n);
+  for (long long row = total + me; row < a.n; row += warps)
+    for (long long c = lane; c < a.D; c += 32) out[row * a.ld_d + c] = U{};
+}
+
+// N elements as fp32: a vector of 16 bytes, or one.
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, float (&f)[N]) {
+  if constexpr (N == 1)
+    f[0] = to_f32(*p);
+  else
+    unpack<T>(__ldg(reinterpret_cast<const uint4*>(p)), f);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_n(T* p, const float (&f)[N]) {
+  if constexpr (N == 1)
+    *p = from_f32<T>(f[0]);
+  else
+    *reinterpret_cast<uint4*>(p) = pack<T>(f);
+}
+
+// The weighted sum of a token's rows, in the order of its slots, fp32. A warp takes 64 vectors of a
+// token; four rows' loads leave before the first is added. A row that a slot has not is no term of
+// the sum (not one times zero: what lies there may be NaN). Bound by the bytes of the rows.
+constexpr int kSumSlots = 4, kSumUnits = 2;
+template <typename T, int N>
+__global__ void __launch_bounds__(32 * kRowWarps) combine_kernel(const __grid_constant__ RowsArgs a) {
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * kRowWarps;
+  const long long width = a.D / N, chunks = (width + 32 * kSumUnits - 1) / (32 * kSumUnits);
+  const T* r = static_cast<const T*>(a.r);
+  T* y = static_cast<T*>(a.y);
+  for (long long u = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < a.T * chunks; u += warps) {
+    const long long t = u / chunks, c = (u - t * chunks) * 32 * kSumUnits + lane;
+    int mine = -1;
+    float weight = 1.f;
+    if (lane < a.topk) {
+      mine = row_of(a, t * a.topk + lane);
+      if (a.w != nullptr) weight = __ldg(a.w + t * a.topk + lane);
+    }
+    float sum[kSumUnits][N];
+#pragma unroll
+    for (int i = 0; i < kSumUnits; ++i)
+#pragma unroll
+      for (int q = 0; q < N; ++q) sum[i][q] = 0.f;
+    for (int j0 = 0; j0 < a.topk; j0 += kSumSlots) {
+      float v[kSumSlots][kSumUnits][N];
+      int row[kSumSlots];
+#pragma unroll
+      for (int j = 0; j < kSumSlots; ++j) {
+        row[j] = j0 + j < a.topk ? __shfl_sync(kAll, mine, j0 + j) : -1;
+#pragma unroll
+        for (int i = 0; i < kSumUnits; ++i)
+          if (row[j] >= 0 && c + 32 * i < width) load_n<T, N>(r + row[j] * a.ld_r + (c + 32 * i) * N, v[j][i]);
+      }
+#pragma unroll
+      for (int j = 0; j < kSumSlots; ++j) {
+        const float w = j0 + j < a.topk ? __shfl_sync(kAll, weight, j0 + j) : 0.f;
+        if (row[j] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < kSumUnits; ++i)
+#pragma unroll
+          for (int q = 0; q < N; ++q) sum[i][q] = fmaf(w, v[j][i][q], sum[i][q]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSumUnits; ++i)
+      if (c + 32 * i < width) store_n<T, N>(y + t * a.ld_x + (c + 32 * i) * N, sum[i]);
+  }
+}
+
+// Gradients of the rows and weights. A CTA takes one token, its warps walk the row together: a
+// vector of dy meets those of eight rows, which it is multiplied into (dw) and, times the weight,
+// written to (dr). The warps' partial products are added in their order. EIGHT: the rows kept are codes.
+// Bound by the bytes of the rows.
+constexpr int kBackSlots = 8;
+template <typename T, int N, bool EIGHT>
+__global__ void __launch_bounds__(256) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ float part[8][kBackSlots];
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const long long width = a.D / N;
+  const T* kept = static_cast<const T*>(a.r);
+  const uint8_t* codes = static_cast<const uint8_t*>(a.r);
+  T* dr = static_cast<T*>(a.dr);
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const T* dy = static_cast<const T*>(a.x) + t * a.ld_x;
+    for (int j0 = 0; j0 < a.topk; j0 += kBackSlots) {
+      long long row[kBackSlots];
+      float w[kBackSlots], dot[kBackSlots];
+#pragma unroll
+      for (int j = 0; j < kBackSlots; ++j) {
+        const bool in = j0 + j < a.topk;
+        row[j] = in ? row_of(a, t * a.topk + j0 + j) : -1;
+        w[j] = in ? __ldg(a.w + t * a.topk + j0 + j) : 0.f;
+        dot[j] = 0.f;
+      }
+      for (long long c = threadIdx.x; c < width; c += blockDim.x) {
+        float d[N], v[kBackSlots][N];
+        load_n<T, N>(dy + c * N, d);
+#pragma unroll
+        for (int j = 0; j < kBackSlots; ++j) {
+          if (row[j] < 0) continue;
+          if constexpr (EIGHT)
+            decode<N>(codes + row[j] * a.ld_r + c * N,
+                      scale_value(__ldg(a.scales + row[j] * a.ld_s + c * N / kScaleBlock)), v[j]);
+          else
+            load_n<T, N>(kept + row[j] * a.ld_r + c * N, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kBackSlots; ++j) {
+          if (row[j] < 0) continue;
+          float s[N];
+#pragma unroll
+          for (int q = 0; q < N; ++q) {
+            dot[j] = fmaf(d[q], v[j][q], dot[j]);
+            s[q] = w[j] * d[q];
+          }
+          store_n<T, N>(dr + row[j] * a.ld_d + c * N, s);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBackSlots; ++j) {
+        dot[j] = warp_sum(dot[j]);
+        if (lane == 0) part[warp][j] = dot[j];
+      }
+      __syncthreads();
+      if (threadIdx.x < kBackSlots && j0 + (int)threadIdx.x < a.topk) {
+        float s = 0.f;
+        for (int v = 0; v < warps; ++v) s += part[v][threadIdx.x];
+        a.dw[t * a.topk + j0 + threadIdx.x] = s;
+      }
+      __syncthreads();
+    }
+  }
+  const long long total = min(max((long long)__ldg(a.total), 0LL), a.n);
+  for (long long r = total + blockIdx.x; r < a.n; r += gridDim.x)
+    for (long long c = threadIdx.x; c < a.D; c += blockDim.x) dr[r * a.ld_d + c] = from_f32<T>(0.f);
+}
+
+// ------------------------------------------------------------------- host side
+constexpr long long kMaxRows = INT32_MAX / 2;
+
+int check_rows(const moe_rows_args* p) {
+  if (p == nullptr || p->T < 0 || p->topk < 1 || p->topk > 32 || p->T * p->topk > kMaxRows || p->E < 1 ||
+      p->E > kSortMaxExperts || p->D < 1 || p->D > INT32_MAX / 2)
+    return MOE_ERR_ARG;
+  return type_bytes(p->dtype) == 0 ? MOE_ERR_ARG : MOE_OK;
+}
+bool check_order(const moe_rows_args* p) {
+  return p->rows != nullptr && p->offsets != nullptr && aligned_to(p->rows, 4) && aligned_to(p->offsets, 4);
+}
+bool check_matrix(const void* q, long long ld, long long rows, long long cols, int bytes) {
+  return q != nullptr && aligned_to(q, (size_t)bytes) && (rows <= 1 || (ld >= cols && ld <= INT32_MAX));
+}
+bool vector_rows(const void* q, long long ld, long long rows, int bytes, int vector) {
+  return aligned_to(q, (size_t)vector) && (rows <= 1 || ld * bytes % vector == 0);
+}
+RowsArgs rows_args(const moe_rows_args* p) {
+  RowsArgs a{};
+  a.rows = p->rows;
+  a.total = p->offsets + p->E;
+  a.T = p->T;
+  a.n = p->T * p->topk;
+  a.D = p->D;
+  a.ld_x = p->ld_x;
+  a.ld_r = p->ld_r;
+  a.ld_d = p->ld_dr;
+  a.w = p->w;
+  a.topk = p->topk;
+  return a;
+}
+unsigned row_grid(long long units) {
+  return (unsigned)std::min<long long>((units + kRowWarps - 1) / kRowWarps, 1 << 20);
+}
+int launched(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
+template <typename U>
+int launch_rows(const RowsArgs& a, cudaStream_t s) {
+  const long long chunks = (a.D + 32 * kCopyUnits - 1) / (32 * kCopyUnits);
+  return launched(launch_behind(expert_rows_kernel<U>, dim3(row_grid(a.T * chunks)), dim3(32 * kRowWarps), 0, s, a));
+}
+
+template <typename T>
+int launch_combine(const RowsArgs& a, bool vec, cudaStream_t s) {
+  constexpr int N = Vec<T>::kN;
+  const long long width = vec ? a.D / N : a.D, chunks = (width + 32 * kSumUnits - 1) / (32 * kSumUnits);
+  const dim3 grid(row_grid(a.T * chunks)), block(32 * kRowWarps);
+  return launched(vec ? launch_behind(combine_kernel<T, N>, grid, block, 0, s, a)
+                      : launch_behind(combine_kernel<T, 1>, grid, block, 0, s, a));
+}
+
+template <typename T>
+int launch_backward(const RowsArgs& a, bool vec, cudaStream_t s) {
+  constexpr int N = Vec<T>::kN;
+  const long long width = vec ? a.D / N : a.D;
+  // Warps of a token: four vectors of a lane each, eight warps at most.
+  const unsigned warps = (unsigned)std::min<long long>(8, std::max<long long>(1, width / 128));
+  const dim3 grid((unsigned)std::min<long long>(a.T, 1 << 20)), block(32 * warps);
+  if (a.scales != nullptr)
+    return launched(vec ? launch_behind(combine_backward_kernel<T, N, true>, grid, block, 0, s, a)
+                        : launch_behind(combine_backward_kernel<T, 1, true>, grid, block, 0, s, a));
+  return launched(vec ? launch_behind(combine_backward_kernel<T, N, false>, grid, block, 0, s, a)
+                      : launch_behind(combine_backward_kernel<T, 1, false>, grid, block, 0, s, a));
+}
+
+// Slots of a lane, so that there are at most kSortChunks chunks.
+int sort_per(long long n) {
+  const long long most = (long long)kSortThreads * kSortChunks;
+  return (int)std::max<long long>(kSortSlots, (n + most - 1) / most);
+}
+long long sort_chunks(long long n) {
+  const long long chunk = (long long)kSortThreads * sort_per(n);
+  return std::max<long long>(1, (n + chunk - 1) / chunk);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_sort_experts_workspace(long long n, int E) {
+  if (n < 1 || n > kMaxRows || E < 1 || E > kSortMaxExperts) return 0;
+  const long long chunks = sort_chunks(n);
+  return chunks > 1 ? (size_t)chunks * E * sizeof(int32_t) : 0;
+}
+
+int moe_sort_experts(const int32_t* ids, long long n, int E, int32_t* slots, int32_t* rows, int32_t* offsets,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (n < 0 || n > kMaxRows || E < 1 || E > kSortMaxExperts || offsets == nullptr || !aligned_to(offsets, 4) ||
+      (n > 0 && (ids == nullptr || slots == nullptr || rows == nullptr)) || !aligned_to(ids, 4) ||
+      !aligned_to(slots, 4) || !aligned_to(rows, 4))
+    return MOE_ERR_ARG;
+  const size_t need = moe_sort_experts_workspace(n, E);
+  if (need > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return MOE_ERR_ARG;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  int sms = 0;
+  const int rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  SortArgs a{ids, slots, rows, offsets, static_cast<int32_t*>(workspace), (int)n, E, sort_per(n)};
+  const dim3 grid((unsigned)sort_chunks(n)), block(kSortThreads);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(sort_kernel), &ready);
+  if (e == cudaSuccess && grid.x > 1) e = launch_behind(sort_count_kernel, grid, block, 0, s, a);
+  if (e == cudaSuccess)
+    e = launch_behind(sort_kernel, grid, block, (size_t)kSortWarps * E * sizeof(int), s, a);
+  return launched(e);
+}
+
+int moe_expert_rows(const moe_rows_args* p, moe_stream_t stream) {
+  int rc = check_rows(p);
+  if (rc != MOE_OK) return rc;
+  if (p->T == 0) return MOE_OK;
+  const int b = type_bytes(p->dtype);
+  if (!check_order(p) || !check_matrix(p->x, p->ld_x, p->T, p->D, b) ||
+      !check_matrix(p->dr, p->ld_dr, p->T * p->topk, p->D, b))
+    return MOE_ERR_ARG;
+  int sms = 0;
+  rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  RowsArgs a = rows_args(p);
+  a.x = p->x;
+  a.dr = p->dr;
+  if (p->D * b % 16 == 0 && vector_rows(p->x, p->ld_x, p->T, b, 16) && vector_rows(p->dr, p->ld_dr, a.n, b, 16)) {
+    a.D = a.D * b / 16;
+    a.ld_x = a.ld_x * b / 16;
+    a.ld_d = a.ld_d * b / 16;
+    return launch_rows<uint4>(a, s);
+  }
+  return b == 4 ? launch_rows<uint32_t>(a, s) : launch_rows<uint16_t>(a, s);
+}
+
+int moe_combine_experts(const moe_rows_args* p, moe_stream_t stream) {
+  int rc = check_rows(p);
+  if (rc != MOE_OK) return rc;
+  if (p->T == 0) return MOE_OK;
+  const int b = type_bytes(p->dtype);
+  if (!check_order(p) || !check_matrix(p->y, p->ld_y, p->T, p->D, b) ||
+      !check_matrix(p->r, p->ld_r, p->T * p->topk, p->D, b) || !aligned_to(p->w, 4))
+    return MOE_ERR_ARG;
+  int sms = 0;
+  rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  RowsArgs a = rows_args(p);
+  a.y = p->y;
+  a.ld_x = p->ld_y;
+  a.r = p->r;
+  const bool vec =
+      p->D * b % 16 == 0 && vector_rows(p->y, p->ld_y, p->T, b, 16) && vector_rows(p->r, p->ld_r, a.n, b, 16);
+  return p->dtype == MOE_FP32   ? launch_combine<float>(a, vec, s)
+         : p->dtype == MOE_BF16 ? launch_combine<__nv_bfloat16>(a, vec, s)
+                                : launch_combine<__half>(a, vec, s);
+}
+
+int moe_combine_experts_backward(const moe_rows_args* p, moe_stream_t stream) {
+  int rc = check_rows(p);
+  if (rc != MOE_OK) return rc;
+  if (p->T == 0) return MOE_OK;
+  const int b = type_bytes(p->dtype), kb = p->r_scales != nullptr ? 1 : b;
+  const long long n = p->T * p->topk;
+  if (!check_order(p) || !check_matrix(p->x, p->ld_x, p->T, p->D, b) || !check_matrix(p->r, p->ld_r, n, p->D, kb) ||
+      !check_matrix(p->dr, p->ld_dr, n, p->D, b) || p->w == nullptr || !aligned_to(p->w, 4) || p->dw == nullptr ||
+      !aligned_to(p->dw, 4) || (p->r_scales != nullptr && n > 1 && p->ld_scales < scale_blocks(p->D)))
+    return MOE_ERR_ARG;
+  int sms = 0;
+  rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  RowsArgs a = rows_args(p);
+  a.x = p->x;
+  a.r = p->r;
+  a.dr = p->dr;
+  a.scales = p->r_scales;
+  a.ld_s = p->ld_scales;
+  a.dw = p->dw;
+  // A vector of codes has as many elements as one of 16 bytes of the type.
+  const bool vec = p->D * b % 16 == 0 && vector_rows(p->x, p->ld_x, p->T, b, 16) &&
+                   vector_rows(p->dr, p->ld_dr, n, b, 16) && vector_rows(p->r, p->ld_r, n, kb, 16 / b * kb);
+  return p->dtype == MOE_FP32   ? launch_backward<float>(a, vec, s)
+         : p->dtype == MOE_BF16 ? launch_backward<__nv_bfloat16>(a, vec, s)
+                                : launch_backward<__half>(a, vec, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,395 @@
+// The gated activation of the experts, h = act(gate) up, and its backward pass, and checkpoints of
+// activations in 8 bits (eight_bits.cuh has the format):
+//
+//   forward     h = act(gate) up, and the checkpoints of gate and up from the same reads
+//   backward    dgate = dh up act'(gate), dup = dh act(gate), and h again, which the product
+//               after it needs and nobody kept; gate and up as they were or from their checkpoints
+//   checkpoint  codes and scales of a matrix;  restore: the matrix that they stand for
+//
+// Elementwise, so bound by the bytes; all arithmetic is fp32, each output is rounded once. A warp
+// takes kUnits vectors of 16 bytes a lane, whose loads all leave before the first is used. A block
+// of 32 elements lies in neighbouring lanes, whose largest |x| meet by shuffles. Rows that do not start on
+// 16 bytes go by single elements, a lane each.
+#include <algorithm>
+
+#include "activations.cuh"
+#include "eight_bits.cuh"
+#include "moe_common.cuh"
+#include "ops_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;
+
+// Where a warp works: a row and its first column there.
+struct Walk {
+  long long chunks, units;  // units of a row; of all rows
+  __device__ __forceinline__ Walk(long long n, long long c, int span) : chunks((c + span - 1) / span) {
+    units = n * chunks;
+  }
+  __device__ __forceinline__ long long first() const {
+    return (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  }
+  __device__ __forceinline__ long long step() const { return (long long)gridDim.x * kWarps; }
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, float (&f)[N]) {
+  if constexpr (N == 1)
+    f[0] = to_f32(*p);
+  else
+    unpack<T>(__ldg(reinterpret_cast<const uint4*>(p)), f);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_n(T* p, const float (&f)[N]) {
+  if constexpr (N == 1)
+    *p = from_f32<T>(f[0]);
+  else
+    *reinterpret_cast<uint4*>(p) = pack<T>(f);
+}
+
+// N elements of a block, whose other elements the neighbouring lanes have (zeros outside the row),
+// to codes and, by the block's first lane, the scale. Whole warps.
+template <int N>
+__device__ __forceinline__ void encode_block(const float (&f)[N], bool in, uint8_t* codes, uint8_t* scales,
+                                             int lane) {
+  constexpr int kLanes = kScaleBlock / N;
+  uint32_t most = 0;
+#pragma unroll
+  for (int q = 0; q < N; ++q) most = max(most, finite_bits(f[q]));
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) most = max(most, __shfl_xor_sync(kAll, most, o));
+  if (!in) return;
+  const uint32_t s = scale_of(most);
+  const float inverse = scale_inverse(s);
+  if constexpr (N == 1) {
+    *codes = encode1(f[0], inverse);
+  } else {
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      w[i] = encode2(f[4 * i], f[4 * i + 1], inverse) | encode2(f[4 * i + 2], f[4 * i + 3], inverse) << 16;
+    if constexpr (N == 8)
+      *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(codes) = w[0];
+  }
+  if (lane % kLanes == 0) *scales = (uint8_t)s;
+}
+
+// ------------------------------------------------------------------- checkpoint and restore
+struct CheckArgs {
+  void* x;
+  uint8_t *codes, *scales;
+  long long n, c, ld_x, ld_codes, ld_scales;
+};
+constexpr int kCheckUnits = 4;
+
+template <typename T, int N>
+__global__ void __launch_bounds__(32 * kWarps) checkpoint_kernel(const __grid_constant__ CheckArgs a) {
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const Walk k(a.n, a.c, 32 * N * kCheckUnits);
+  for (long long u = k.first(); u < k.units; u += k.step()) {
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kCheckUnits + lane * N;
+    const T* x = static_cast<const T*>(a.x) + i * a.ld_x;
+    float f[kCheckUnits][N];
+#pragma unroll
+    for (int q = 0; q < kCheckUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      if (c < a.c) {
+        load_n<T, N>(x + c, f[q]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[q][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kCheckUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      encode_block<N>(f[q], c < a.c, a.codes + i * a.ld_codes + c, a.scales + i * a.ld_scales + c / kScaleBlock,
+                      lane);
+    }
+  }
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(32 * kWarps) restore_kernel(const __grid_constant__ CheckArgs a) {
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const Walk k(a.n, a.c, 32 * N * kCheckUnits);
+  for (long long u = k.first(); u < k.units; u += k.step()) {
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kCheckUnits + lane * N;
+    T* x = static_cast<T*>(a.x) + i * a.ld_x;
+    float f[kCheckUnits][N];
+#pragma unroll
+    for (int q = 0; q < kCheckUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      if (c < a.c)
+        decode<N>(a.codes + i * a.ld_codes + c,
+                  scale_value(__ldg(a.scales + i * a.ld_scales + c / kScaleBlock)), f[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kCheckUnits; ++q)
+      if (c0 + 32 * N * q < a.c) store_n<T, N>(x + c0 + 32 * N * q, f[q]);
+  }
+}
+
+// ------------------------------------------------------------------- the gated activation
+struct GatedArgs {
+  const void *gate, *up, *dh;
+  void *h, *dgate, *dup;
+  uint8_t *gate_codes, *up_codes, *gate_scales, *up_scales;
+  long long n, c, ld_gate, ld_up, ld_h, ld_dh, ld_dgate, ld_dup;
+  long long ld_codes, ld_scales;
+};
+constexpr int kGatedUnits = 2;
+
+template <typename T, int ACT, int N, bool KEEP>
+__global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constant__ GatedArgs a) {
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const Walk k(a.n, a.c, 32 * N * kGatedUnits);
+  for (long long u = k.first(); u < k.units; u += k.step()) {
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kGatedUnits + lane * N;
+    const T* gate = static_cast<const T*>(a.gate) + i * a.ld_gate;
+    const T* up = static_cast<const T*>(a.up) + i * a.ld_up;
+    float g[kGatedUnits][N], v[kGatedUnits][N];
+#pragma unroll
+    for (int q = 0; q < kGatedUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      if (c < a.c) {
+        load_n<T, N>(gate + c, g[q]);
+        load_n<T, N>(up + c, v[q]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) g[q][e] = v[q][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kGatedUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      if (KEEP) {
+        const long long code = i * a.ld_codes + c, scale = i * a.ld_scales + c / kScaleBlock;
+        encode_block<N>(g[q], c < a.c, a.gate_codes + code, a.gate_scales + scale, lane);
+        encode_block<N>(v[q], c < a.c, a.up_codes + code, a.up_scales + scale, lane);
+      }
+      if (c < a.c) {
+        float h[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[e] = act_of<ACT>(g[q][e]) * v[q][e];
+        store_n<T, N>(static_cast<T*>(a.h) + i * a.ld_h + c, h);
+      }
+    }
+  }
+}
+
+template <typename T, int ACT, int N, bool KEPT>
+__global__ void __launch_bounds__(32 * kWarps) gated_backward_kernel(const __grid_constant__ GatedArgs a) {
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const Walk k(a.n, a.c, 32 * N * kGatedUnits);
+  for (long long u = k.first(); u < k.units; u += k.step()) {
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kGatedUnits + lane * N;
+    float g[kGatedUnits][N], v[kGatedUnits][N], d[kGatedUnits][N];
+#pragma unroll
+    for (int q = 0; q < kGatedUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      if (c >= a.c) continue;
+      if constexpr (KEPT) {
+        const long long code = i * a.ld_codes + c, scale = i * a.ld_scales + c / kScaleBlock;
+        decode<N>(static_cast<const uint8_t*>(a.gate) + code, scale_value(__ldg(a.gate_scales + scale)), g[q]);
+        decode<N>(static_cast<const uint8_t*>(a.up) + code, scale_value(__ldg(a.up_scales + scale)), v[q]);
+      } else {
+        load_n<T, N>(static_cast<const T*>(a.gate) + i * a.ld_gate + c, g[q]);
+        load_n<T, N>(static_cast<const T*>(a.up) + i * a.ld_up + c, v[q]);
+      }
+      load_n<T, N>(static_cast<const T*>(a.dh) + i * a.ld_dh + c, d[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kGatedUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      if (c >= a.c) continue;
+      float act[N], o[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        act[e] = act_of<ACT>(g[q][e]);
+        o[e] = d[q][e] * v[q][e] * act_grad<ACT>(g[q][e]);
+      }
+      store_n<T, N>(static_cast<T*>(a.dgate) + i * a.ld_dgate + c, o);
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = d[q][e] * act[e];
+      store_n<T, N>(static_cast<T*>(a.dup) + i * a.ld_dup + c, o);
+      if (a.h != nullptr) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] = act[e] * v[q][e];
+        store_n<T, N>(static_cast<T*>(a.h) + i * a.ld_h + c, o);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host side
+constexpr long long kMaxSize = INT32_MAX / 2;
+
+bool check_matrix(const void* q, long long ld, long long rows, long long cols, int bytes) {
+  return q != nullptr && aligned_to(q, (size_t)bytes) && (rows <= 1 || (ld >= cols && ld <= INT32_MAX));
+}
+bool vector_rows(const void* q, long long ld, long long rows, int bytes, int vector) {
+  return aligned_to(q, (size_t)vector) && (rows <= 1 || ld * bytes % vector == 0);
+}
+unsigned grid_of(long long n, long long c, int span) {
+  const long long units = n * ((c + span - 1) / span);
+  return (unsigned)std::min<long long>((units + kWarps - 1) / kWarps, 1 << 20);
+}
+int launched(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
+template <typename T>
+int launch_checkpoint(const CheckArgs& a, bool vec, bool restore, cudaStream_t s) {
+  constexpr int N = Vec<T>::kN;
+  const dim3 grid(grid_of(a.n, a.c, 32 * kCheckUnits * (vec ? N : 1))), block(32 * kWarps);
+  if (restore)
+    return launched(vec ? launch_behind(restore_kernel<T, N>, grid, block, 0, s, a)
+                        : launch_behind(restore_kernel<T, 1>, grid, block, 0, s, a));
+  return launched(vec ? launch_behind(checkpoint_kernel<T, N>, grid, block, 0, s, a)
+                      : launch_behind(checkpoint_kernel<T, 1>, grid, block, 0, s, a));
+}
+
+int checkpoint(const moe_checkpoint_args* p, bool restore, moe_stream_t stream) {
+  if (p == nullptr || p->n < 0 || p->n > kMaxSize || p->c < 1 || p->c > kMaxSize) return MOE_ERR_ARG;
+  const int b = type_bytes(p->dtype);
+  if (b == 0) return MOE_ERR_ARG;
+  if (p->n == 0) return MOE_OK;
+  if (!check_matrix(p->x, p->ld_x, p->n, p->c, b) || !check_matrix(p->codes, p->ld_codes, p->n, p->c, 1) ||
+      !check_matrix(p->scales, p->ld_scales, p->n, scale_blocks(p->c), 1))
+    return MOE_ERR_ARG;
+  int sms = 0;
+  const int rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  CheckArgs a{p->x,      static_cast<uint8_t*>(p->codes), p->scales, p->n, p->c, p->ld_x, p->ld_codes,
+              p->ld_scales};
+  // Whole blocks in one run of memory: one long row.
+  if (a.n > 1 && a.c % kScaleBlock == 0 && a.ld_x == a.c && a.ld_codes == a.c &&
+      a.ld_scales == a.c / kScaleBlock) {
+    a.c *= a.n;
+    a.n = 1;
+  }
+  const bool vec = a.c * b % 16 == 0 && vector_rows(a.x, a.ld_x, a.n, b, 16) &&
+                   vector_rows(a.codes, a.ld_codes, a.n, 1, 16 / b);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return p->dtype == MOE_FP32   ? launch_checkpoint<float>(a, vec, restore, s)
+         : p->dtype == MOE_BF16 ? launch_checkpoint<__nv_bfloat16>(a, vec, restore, s)
+                                : launch_checkpoint<__half>(a, vec, restore, s);
+}
+
+template <typename T, int ACT>
+int launch_gated(const GatedArgs& a, bool vec, bool kept, bool backward, cudaStream_t s) {
+  constexpr int N = Vec<T>::kN;
+  const dim3 grid(grid_of(a.n, a.c, 32 * kGatedUnits * (vec ? N : 1))), block(32 * kWarps);
+  auto go = [&](auto* v, auto* e) {
+    return launched(vec ? launch_behind(v, grid, block, 0, s, a) : launch_behind(e, grid, block, 0, s, a));
+  };
+  if (backward)
+    return kept ? go(gated_backward_kernel<T, ACT, N, true>, gated_backward_kernel<T, ACT, 1, true>)
+                : go(gated_backward_kernel<T, ACT, N, false>, gated_backward_kernel<T, ACT, 1, false>);
+  return kept ? go(gated_kernel<T, ACT, N, true>, gated_kernel<T, ACT, 1, true>)
+              : go(gated_kernel<T, ACT, N, false>, gated_kernel<T, ACT, 1, false>);
+}
+template <typename T>
+int launch_gated(int act, const GatedArgs& a, bool vec, bool kept, bool backward, cudaStream_t s) {
+  switch (act) {
+    case MOE_ACT_RELU: return launch_gated<T, MOE_ACT_RELU>(a, vec, kept, backward, s);
+    case MOE_ACT_GELU: return launch_gated<T, MOE_ACT_GELU>(a, vec, kept, backward, s);
+    case MOE_ACT_GELU_TANH: return launch_gated<T, MOE_ACT_GELU_TANH>(a, vec, kept, backward, s);
+    case MOE_ACT_SILU: return launch_gated<T, MOE_ACT_SILU>(a, vec, kept, backward, s);
+    default: return launch_gated<T, MOE_ACT_NONE>(a, vec, kept, backward, s);
+  }
+}
+
+int gated(const moe_gated_args* p, bool backward, moe_stream_t stream) {
+  if (p == nullptr || p->n < 0 || p->n > kMaxSize || p->c < 1 || p->c > kMaxSize) return MOE_ERR_ARG;
+  if ((p->dtype != MOE_BF16 && p->dtype != MOE_FP16) || p->act < MOE_ACT_NONE || p->act > MOE_ACT_SILU)
+    return MOE_ERR_ARG;
+  if (p->n == 0) return MOE_OK;
+  const bool kept = p->gate_scales != nullptr;
+  if (kept != (p->up_scales != nullptr)) return MOE_ERR_ARG;
+  const int in = backward && kept ? 1 : 2;
+  const long long ld_gate = in == 1 ? p->c : p->ld_gate, ld_up = in == 1 ? p->c : p->ld_up;
+  if (!check_matrix(p->gate, ld_gate, p->n, p->c, in) || !check_matrix(p->up, ld_up, p->n, p->c, in))
+    return MOE_ERR_ARG;
+  if (backward) {
+    if (!check_matrix(p->dh, p->ld_dh, p->n, p->c, 2) || !check_matrix(p->dgate, p->ld_dgate, p->n, p->c, 2) ||
+        !check_matrix(p->dup, p->ld_dup, p->n, p->c, 2) ||
+        (p->h != nullptr && !check_matrix(p->h, p->ld_h, p->n, p->c, 2)))
+      return MOE_ERR_ARG;
+  } else if (!check_matrix(p->h, p->ld_h, p->n, p->c, 2) ||
+             (kept != (p->gate_codes != nullptr)) || (kept != (p->up_codes != nullptr))) {
+    return MOE_ERR_ARG;
+  }
+  int sms = 0;
+  const int rc = ops_device(&sms);
+  if (rc != MOE_OK) return rc;
+  GatedArgs a{};
+  a.gate = p->gate;
+  a.up = p->up;
+  a.dh = p->dh;
+  a.h = p->h;
+  a.dgate = p->dgate;
+  a.dup = p->dup;
+  a.gate_codes = static_cast<uint8_t*>(p->gate_codes);
+  a.up_codes = static_cast<uint8_t*>(p->up_codes);
+  a.gate_scales = p->gate_scales;
+  a.up_scales = p->up_scales;
+  a.n = p->n;
+  a.c = p->c;
+  a.ld_gate = ld_gate;
+  a.ld_up = ld_up;
+  a.ld_h = p->ld_h;
+  a.ld_dh = p->ld_dh;
+  a.ld_dgate = p->ld_dgate;
+  a.ld_dup = p->ld_dup;
+  a.ld_codes = a.c;
+  a.ld_scales = scale_blocks(a.c);
+  auto whole = [&](const void* q, long long ld) { return q == nullptr || ld == a.c; };
+  // Whole blocks in one run of memory: one long row.
+  if (a.n > 1 && a.c % kScaleBlock == 0 && a.ld_gate == a.c && a.ld_up == a.c && whole(a.h, a.ld_h) &&
+      (!backward || (a.ld_dh == a.c && a.ld_dgate == a.c && a.ld_dup == a.c))) {
+    a.c *= a.n;
+    a.n = 1;
+  }
+  auto rows = [&](const void* q, long long ld) { return q == nullptr || vector_rows(q, ld, a.n, 2, 16); };
+  bool vec = a.c % 8 == 0 && rows(a.h, a.ld_h);
+  if (backward)
+    vec = vec && rows(a.dh, a.ld_dh) && rows(a.dgate, a.ld_dgate) && rows(a.dup, a.ld_dup);
+  if (in == 1)
+    vec = vec && aligned_to(a.gate, 8) && aligned_to(a.up, 8);
+  else
+    vec = vec && rows(a.gate, a.ld_gate) && rows(a.up, a.ld_up);
+  if (kept && !backward) vec = vec && aligned_to(a.gate_codes, 8) && aligned_to(a.up_codes, 8);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return p->dtype == MOE_BF16 ? launch_gated<__nv_bfloat16>(p->act, a, vec, kept, backward, s)
+                              : launch_gated<__half>(p->act, a, vec, kept, backward, s);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_checkpoint(const moe_checkpoint_args* p, moe_stream_t stream) { return checkpoint(p, false, stream); }
+int moe_restore(const moe_checkpoint_args* p, moe_stream_t stream) { return checkpoint(p, true, stream); }
+int moe_gated(const moe_gated_args* p, moe_stream_t stream) { return gated(p, false, stream); }
+int moe_gated_backward(const moe_gated_args* p, moe_stream_t stream) { return gated(p, true, stream); }
+
+}  // extern "C"

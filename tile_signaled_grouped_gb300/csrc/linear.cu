@@ -17,6 +17,7 @@
 #include <atomic>
 
 #include "activations.cuh"
+#include "eight_bits.cuh"
 #include "linear_tiles.h"
 #include "mma_common.cuh"
 
@@ -1037,10 +1038,11 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2) linear_rows_kernel(const _
 // ------------------------------------------------------------------- dz and db
 struct ActGradArgs {
   const void* dy;
-  const void* z;  // null without an activation
+  const void* z;  // null without an activation; codes where it was kept in 8 bits
+  const uint8_t* z_scales;
   void* dz;       // null: only the sums
   float* part;    // [gridDim.y][N] column sums, or null
-  long long ld_dy, ld_z, ld_dz;
+  long long ld_dy, ld_z, ld_dz, ld_scales;
   int M, N, dtype, rows;  // rows of a CTA
 };
 
@@ -1058,9 +1060,9 @@ __device__ __forceinline__ void unpack8(const uint4& u, int dtype, float (&f)[8]
 // columns of four rows at a time, warp w rows 4 w .. of every 32, and all eight loads leave
 // before the first is used; the eight warps' sums are added in order: 10.9 us for 4096 x 1536
 // (3.5 TB/s; cold, under a profiler). Otherwise a thread takes one column, so that neighbouring
-// threads read neighbouring elements.
+// threads read neighbouring elements. EIGHT: z was kept in 8 bits.
 constexpr int kActRows = 4;
-template <int ACT, bool VEC>
+template <int ACT, bool VEC, bool EIGHT>
 __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
   __shared__ float red[VEC ? 8 : 1][32][9];
   allow_dependent_launch();
@@ -1072,17 +1074,23 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
     const int j = (blockIdx.x * 32 + lane) * 8;
     const unsigned short* dy = static_cast<const unsigned short*>(a.dy) + j;
     const unsigned short* z = static_cast<const unsigned short*>(a.z) + j;
+    const uint8_t* codes = static_cast<const uint8_t*>(a.z) + j;
+    const uint8_t* scales = a.z_scales + j / kScaleBlock;
     float s[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) s[q] = 0.f;
     if (j < a.N) {
       for (int i0 = lo + warp * kActRows; i0 < hi; i0 += 8 * kActRows) {
-        uint4 du[kActRows], zu[kActRows];
+        uint4 du[kActRows], zu[EIGHT ? 1 : kActRows];
+        float zf[EIGHT ? kActRows : 1][8];
 #pragma unroll
         for (int r = 0; r < kActRows; ++r) {
           const long long i = min(i0 + r, hi - 1);
           du[r] = __ldg(reinterpret_cast<const uint4*>(dy + i * a.ld_dy));
-          if (ACT != MOE_ACT_NONE) zu[r] = __ldg(reinterpret_cast<const uint4*>(z + i * a.ld_z));
+          if constexpr (EIGHT)
+            decode<8>(codes + i * a.ld_z, scale_value(__ldg(scales + i * a.ld_scales)), zf[r]);
+          else if (ACT != MOE_ACT_NONE)
+            zu[r] = __ldg(reinterpret_cast<const uint4*>(z + i * a.ld_z));
         }
 #pragma unroll
         for (int r = 0; r < kActRows; ++r) {
@@ -1091,7 +1099,12 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
             unpack8(du[r], a.dtype, d);
             if (ACT != MOE_ACT_NONE) {
               float v[8];
-              unpack8(zu[r], a.dtype, v);
+              if constexpr (EIGHT) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = zf[r][q];
+              } else {
+                unpack8(zu[r], a.dtype, v);
+              }
 #pragma unroll
               for (int q = 0; q < 8; ++q) d[q] *= act_grad<ACT>(v[q]);
             }
@@ -1116,7 +1129,14 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
       for (int r = 0; r < kActRows; ++r) {
         const long long i = min(i0 + r, hi - 1);
         d[r] = load_as_f32(a.dy, a.dtype, i * a.ld_dy + j);
-        z[r] = ACT != MOE_ACT_NONE ? load_as_f32(a.z, a.dtype, i * a.ld_z + j) : 0.f;
+        if constexpr (EIGHT) {
+          float v[1];
+          decode<1>(static_cast<const uint8_t*>(a.z) + i * a.ld_z + j,
+                    scale_value(__ldg(a.z_scales + i * a.ld_scales + j / kScaleBlock)), v);
+          z[r] = v[0];
+        } else {
+          z[r] = ACT != MOE_ACT_NONE ? load_as_f32(a.z, a.dtype, i * a.ld_z + j) : 0.f;
+        }
       }
 #pragma unroll
       for (int r = 0; r < kActRows; ++r) {
@@ -1476,10 +1496,19 @@ struct StreamDevice {
 
 template <int ACT>
 void launch_act_grad(const ActGradArgs& a, bool vec, dim3 grid, cudaStream_t s) {
+  if constexpr (ACT != MOE_ACT_NONE) {
+    if (a.z_scales != nullptr) {
+      if (vec)
+        act_grad_kernel<ACT, true, true><<<grid, 256, 0, s>>>(a);
+      else
+        act_grad_kernel<ACT, false, true><<<grid, 256, 0, s>>>(a);
+      return;
+    }
+  }
   if (vec)
-    act_grad_kernel<ACT, true><<<grid, 256, 0, s>>>(a);
+    act_grad_kernel<ACT, true, false><<<grid, 256, 0, s>>>(a);
   else
-    act_grad_kernel<ACT, false><<<grid, 256, 0, s>>>(a);
+    act_grad_kernel<ACT, false, false><<<grid, 256, 0, s>>>(a);
 }
 
 }  // namespace
@@ -1586,7 +1615,9 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
   }
   const bool act = p->act != MOE_ACT_NONE;
   if (!check_matrix(p->dy, p->ld_dy, p->M, p->N, p->dtype, true) ||
-      !check_matrix(p->z, p->ld_z, p->M, p->N, p->dtype, act) ||
+      (p->z_scales == nullptr ? !check_matrix(p->z, p->ld_z, p->M, p->N, p->dtype, act)
+                              : !act || p->z == nullptr ||
+                                    (p->M > 1 && (p->ld_z < p->N || p->ld_z > INT32_MAX))) ||
       !check_matrix(p->dx, p->ld_dx, p->M, p->K, p->dtype, false) ||
       (p->dx != nullptr && !check_operand(p->w, p->ld_w, p->N, p->K)) ||
       (p->dw != nullptr && !check_operand(p->x, p->ld_x, p->M, p->K)) || workspace == nullptr ||
@@ -1605,6 +1636,8 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
     ActGradArgs g{};
     g.dy = p->dy;
     g.z = p->z;
+    g.z_scales = p->z_scales;
+    g.ld_scales = scale_blocks(p->N);
     g.dz = copy ? workspace : nullptr;
     g.part = p->db != nullptr ? reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(M, N))
                               : nullptr;
@@ -1615,7 +1648,8 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
     g.N = N;
     g.dtype = p->dtype;
     const bool vec = N % 8 == 0 && row_bytes(p->dy, p->ld_dy, p->dtype, M) != 0 &&
-                     (!act || row_bytes(p->z, p->ld_z, p->dtype, M) != 0);
+                     (!act || (p->z_scales != nullptr ? aligned_to(p->z, 8) && (M == 1 || p->ld_z % 8 == 0)
+                                                      : row_bytes(p->z, p->ld_z, p->dtype, M) != 0));
     const int bx = (N + 255) / 256;
     const int want = std::max(1, std::min(kBiasParts, 8 * sms / bx));  // ranges: eight CTAs an SM
     g.rows = ((M + want - 1) / want + 8 * kActRows - 1) / (8 * kActRows) * (8 * kActRows);

@@ -384,10 +384,52 @@ std::tuple<Tensor, OptTensor> linear(const Tensor& x, const Tensor& weight, cons
   return {y, z};
 }
 
+// Codes and scales of an 8-bit checkpoint.
+void check_kept(const Tensor& codes, const Tensor& scales, const char* what, const Tensor& beside) {
+  if (codes.scalar_type() != at::kFloat8_e4m3fn || codes.dim() < 1 || !codes.is_contiguous())
+    refuse(what, "'s codes must be contiguous float8_e4m3fn, got ", codes.sizes(), " of ",
+           codes.scalar_type());
+  const auto shape = with_last(codes, (codes.size(-1) + 31) / 32);
+  if (scales.scalar_type() != at::kByte || scales.sizes() != at::IntArrayRef(shape) ||
+      !scales.is_contiguous())
+    refuse(what, "'s scales must be contiguous uint8 of shape ", shape, ", got ", scales.sizes(), " of ",
+           scales.scalar_type());
+  same_device(codes, beside, what);
+  same_device(scales, beside, what);
+}
+// A matrix from its checkpoint, on the stream of `l`.
+Tensor restored(const Tensor& codes, const Tensor& scales, at::ScalarType type, const Launch& l) {
+  Tensor x = empty(codes.sizes(), type, codes);
+  const int64_t c = codes.size(-1);
+  if (x.numel() == 0) return x;
+  moe_checkpoint_args a{};
+  a.n = codes.numel() / c;
+  a.c = c;
+  a.dtype = type_of(type);
+  a.x = x.data_ptr();
+  a.codes = codes.data_ptr();
+  a.scales = static_cast<uint8_t*>(scales.data_ptr());
+  a.ld_x = a.ld_codes = c;
+  a.ld_scales = (c + 31) / 32;
+  call("moe_restore", [&] { return moe_restore(&a, l.stream); });
+  return x;
+}
+
+// x and z: matrices, or (with scales) the codes of their checkpoints. x is restored for the product that
+// reads it; z is read as it is kept.
 std::tuple<OptTensor, OptTensor, OptTensor> linear_backward(
-    const Tensor& dy, const Tensor& x, const Tensor& weight, const OptTensor& z,
-    const std::string& act, const py::object& bias, const py::object& dw_dtype, bool need_dx,
-    bool need_dw) {
+    const Tensor& dy, const Tensor& kept_x, const OptTensor& x_scales, const Tensor& weight,
+    const OptTensor& z, const OptTensor& z_scales, const std::string& act, const py::object& bias,
+    const py::object& dw_dtype, bool need_dx, bool need_dw) {
+  std::optional<Launch> restoring;
+  Tensor x = kept_x;
+  if (x_scales.has_value()) {
+    checked_type(dy, "dy", true);
+    check_kept(kept_x, *x_scales, "x", dy);
+    restoring.emplace(dy);
+    x = need_dw ? restored(kept_x, *x_scales, dy.scalar_type(), *restoring)
+                : empty(kept_x.sizes(), dy.scalar_type(), dy);
+  }
   const int dt = checked_type(x, "x", true);
   const Rows rx = operand(x, "x", -1, x);
   if (weight.dim() != 2) refuse("weight must be [N, K], got ", weight.sizes());
@@ -399,7 +441,11 @@ std::tuple<OptTensor, OptTensor, OptTensor> linear_backward(
   same_shape(dy, shape, x, "dy");
   const Rows rdy = rows_of(dy, "dy", rw.n);
   Rows rz{};
-  if (z.has_value()) {
+  if (z_scales.has_value()) {
+    check_kept(*z, *z_scales, "z", x);
+    if (z->sizes() != at::IntArrayRef(shape)) refuse("z must be ", shape, ", got ", z->sizes());
+    rz = {0, rw.n, rw.n};
+  } else if (z.has_value()) {
     same_shape(*z, shape, x, "z");
     rz = rows_of(*z, "z", rw.n);
   }
@@ -430,8 +476,349 @@ std::tuple<OptTensor, OptTensor, OptTensor> linear_backward(
   a.ld_z = rz.ld;
   a.ld_dy = rdy.ld;
   a.ld_dx = a.ld_dw = rx.c;
+  a.z_scales = static_cast<const uint8_t*>(ptr(z_scales));
   call("moe_linear_backward", [&] { return moe_linear_backward(&a, work.data_ptr(), size, l.stream); });
   return {dx, dw, db};
+}
+
+// ------------------------------------------------------------------------------- expert rows
+// The order of a batch: rows [..., topk] and offsets [E + 1].
+struct Order {
+  int64_t n, T, topk, E;
+};
+Order order_of(const Tensor& rows, const Tensor& offsets, const Tensor& beside) {
+  if (rows.scalar_type() != at::kInt || rows.dim() < 1 || !rows.is_contiguous())
+    refuse("the order's rows must be contiguous int32 [..., topk], got ", rows.sizes(), " of ",
+           rows.scalar_type());
+  if (offsets.scalar_type() != at::kInt || offsets.dim() != 1 || offsets.size(0) < 2 ||
+      !offsets.is_contiguous())
+    refuse("offsets must be contiguous int32 [E + 1], got ", offsets.sizes(), " of ",
+           offsets.scalar_type());
+  same_device(rows, beside, "the order");
+  same_device(offsets, beside, "offsets");
+  const int64_t topk = rows.size(-1);
+  if (topk < 1 || topk > 32) refuse("the order's rows have ", topk, " choices: expected 1 to 32");
+  return {rows.numel(), rows.numel() / topk, topk, offsets.size(0) - 1};
+}
+moe_rows_args rows_args(const Order& o, const Tensor& rows, const Tensor& offsets, int dtype, int64_t D) {
+  moe_rows_args a{};
+  a.T = o.T;
+  a.D = D;
+  a.topk = as_int(o.topk);
+  a.E = as_int(o.E);
+  a.dtype = dtype;
+  a.rows = static_cast<const int32_t*>(rows.data_ptr());
+  a.offsets = static_cast<const int32_t*>(offsets.data_ptr());
+  return a;
+}
+void check_weights(const Tensor& w, const Tensor& rows) {
+  if (w.scalar_type() != at::kFloat || w.sizes() != rows.sizes() || !w.is_contiguous() ||
+      w.device() != rows.device())
+    refuse("w must be contiguous float32 of shape ", rows.sizes(), " beside the order, got ", w.sizes(),
+           " of ", w.scalar_type(), " on ", w.device());
+}
+void check_tokens(const Tensor& x, const Tensor& rows, const char* what) {
+  if (x.dim() != rows.dim() || x.sizes().slice(0, x.dim() - 1) != rows.sizes().slice(0, rows.dim() - 1))
+    refuse(what, " has shape ", x.sizes(), " for an order of rows ", rows.sizes());
+}
+// n rows of the matrix r.
+Rows expert_matrix(const Tensor& r, const char* what, int64_t n) {
+  const Rows m = rows_of(r, what);
+  if (m.n != n) refuse(what, " has ", m.n, " rows: expected ", n, ", one for every slot");
+  return m;
+}
+
+std::tuple<Tensor, Tensor, Tensor> sort_experts(const Tensor& ids, int64_t E) {
+  if (ids.scalar_type() != at::kInt || ids.dim() < 1 || !ids.is_contiguous())
+    refuse("ids must be contiguous int32 [..., topk], got ", ids.sizes(), " of ", ids.scalar_type());
+  if (E < 1 || E > 1024) refuse("E is ", E, ": expected 1 to 1024");
+  const Launch l(ids);
+  const int64_t n = ids.numel();
+  Tensor slots = empty({n}, at::kInt, ids), rows = empty(ids.sizes(), at::kInt, ids),
+         offsets = empty({E + 1}, at::kInt, ids), work;
+  const size_t size = moe_sort_experts_workspace(n, (int)E);
+  if (size > 0) work = empty({(int64_t)size}, at::kByte, ids);
+  call("moe_sort_experts", [&] {
+    return moe_sort_experts(static_cast<const int32_t*>(ids.data_ptr()), n, (int)E,
+                            static_cast<int32_t*>(slots.data_ptr()), static_cast<int32_t*>(rows.data_ptr()),
+                            static_cast<int32_t*>(offsets.data_ptr()), size > 0 ? work.data_ptr() : nullptr,
+                            size, l.stream);
+  });
+  return {slots, rows, offsets};
+}
+
+Tensor expert_rows(const Tensor& x, const Tensor& rows, const Tensor& offsets) {
+  const Order o = order_of(rows, offsets, x);
+  const Rows r = rows_of(x, "x");
+  const int dt = checked_type(x, "x");
+  check_tokens(x, rows, "x");
+  const Launch l(x);
+  Tensor out = empty({o.n, r.c}, x.scalar_type(), x);
+  moe_rows_args a = rows_args(o, rows, offsets, dt, r.c);
+  a.x = x.data_ptr();
+  a.dr = out.data_ptr();
+  a.ld_x = r.ld;
+  a.ld_dr = r.c;
+  call("moe_expert_rows", [&] { return moe_expert_rows(&a, l.stream); });
+  return out;
+}
+
+Tensor combine_experts(const Tensor& r, const OptTensor& w, const Tensor& rows, const Tensor& offsets) {
+  const Order o = order_of(rows, offsets, r);
+  const int dt = checked_type(r, "r");
+  const Rows m = expert_matrix(r, "r", o.n);
+  if (w.has_value()) check_weights(*w, rows);
+  const Launch l(r);
+  Tensor y = empty(with_last(rows, m.c), r.scalar_type(), r);
+  moe_rows_args a = rows_args(o, rows, offsets, dt, m.c);
+  a.w = static_cast<const float*>(ptr(w));
+  a.r = r.data_ptr();
+  a.y = y.data_ptr();
+  a.ld_r = m.ld;
+  a.ld_y = m.c;
+  call("moe_combine_experts", [&] { return moe_combine_experts(&a, l.stream); });
+  return y;
+}
+
+std::tuple<Tensor, Tensor> combine_experts_backward(const Tensor& dy, const Tensor& r, const OptTensor& scales,
+                                                    const Tensor& w, const Tensor& rows, const Tensor& offsets) {
+  const Order o = order_of(rows, offsets, dy);
+  const int dt = checked_type(dy, "dy");
+  const Rows d = rows_of(dy, "dy");
+  check_tokens(dy, rows, "dy");
+  check_weights(w, rows);
+  if (scales.has_value())
+    check_kept(r, *scales, "r", dy);
+  else if (r.scalar_type() != dy.scalar_type())
+    refuse("r has type ", r.scalar_type(), ": expected ", dy.scalar_type(), " or a checkpoint");
+  same_device(r, dy, "r");
+  const Rows m = expert_matrix(r, "r", o.n);
+  if (m.c != d.c) refuse("r has rows of ", m.c, " elements: expected ", d.c);
+  const Launch l(dy);
+  Tensor dr = empty({o.n, d.c}, dy.scalar_type(), dy), dw = empty(rows.sizes(), at::kFloat, dy);
+  moe_rows_args a = rows_args(o, rows, offsets, dt, d.c);
+  a.w = static_cast<const float*>(w.data_ptr());
+  a.x = dy.data_ptr();
+  a.r = r.data_ptr();
+  a.r_scales = static_cast<const uint8_t*>(ptr(scales));
+  a.dr = dr.data_ptr();
+  a.dw = static_cast<float*>(dw.data_ptr());
+  a.ld_x = d.ld;
+  a.ld_r = m.ld;
+  a.ld_scales = (d.c + 31) / 32;
+  a.ld_dr = d.c;
+  call("moe_combine_experts_backward", [&] { return moe_combine_experts_backward(&a, l.stream); });
+  return {dr, dw};
+}
+
+// ------------------------------------------------------------------------------- expert linear
+// Weights [E, N, K]: rows on 16 bytes, experts a multiple of 8 elements apart.
+struct Experts {
+  int64_t N, K, ld, stride;
+};
+Experts expert_weights(const Tensor& w, const Tensor& x, const Tensor& offsets) {
+  if (offsets.scalar_type() != at::kInt || offsets.dim() != 1 || !offsets.is_contiguous() ||
+      offsets.size(0) < 2)
+    refuse("offsets must be contiguous int32 [E + 1], got ", offsets.sizes(), " of ", offsets.scalar_type());
+  same_device(offsets, x, "offsets");
+  if (w.dim() != 3 || w.size(0) != offsets.size(0) - 1)
+    refuse("weight must be [E, N, K] with E = ", offsets.size(0) - 1, ", got ", w.sizes());
+  if (w.scalar_type() != x.scalar_type())
+    refuse("weight has type ", w.scalar_type(), ": expected ", x.scalar_type());
+  same_device(w, x, "weight");
+  const Experts e{w.size(1), w.size(2), w.stride(1), w.stride(0)};
+  if (e.N % 8 != 0 || e.K % 8 != 0 || e.N < 1 || e.K < 1)
+    refuse("weight must have N and K that are multiples of 8, got ", w.sizes());
+  if (w.stride(2) != 1 || e.ld % 8 != 0 || e.ld < e.K ||
+      (w.size(0) > 1 && (e.stride % 8 != 0 || e.stride < (e.N - 1) * e.ld + e.K)) ||
+      reinterpret_cast<uintptr_t>(w.data_ptr()) % 16 != 0)
+    refuse("weight must have contiguous rows that start on 16 bytes, got strides ", w.strides());
+  return e;
+}
+moe_expert_linear_args expert_args(const Experts& e, const Tensor& w, const Tensor& offsets, int dtype,
+                                   int64_t n) {
+  moe_expert_linear_args a{};
+  a.n = n;
+  a.N = e.N;
+  a.K = e.K;
+  a.E = as_int(w.size(0));
+  a.dtype = a.dwtype = dtype;
+  a.offsets = static_cast<const int32_t*>(offsets.data_ptr());
+  a.w = w.data_ptr();
+  a.ld_w = e.ld;
+  a.stride_w = e.stride;
+  return a;
+}
+
+Tensor expert_linear(const Tensor& x, const Tensor& weight, const Tensor& offsets) {
+  const int dt = checked_type(x, "x", true);
+  const Experts e = expert_weights(weight, x, offsets);
+  const Rows r = operand(x, "x", e.K, x);
+  const Launch l(x);
+  Tensor y = empty(with_last(x, e.N), x.scalar_type(), x);
+  moe_expert_linear_args a = expert_args(e, weight, offsets, dt, r.n);
+  a.x = x.data_ptr();
+  a.y = y.data_ptr();
+  a.ld_x = r.ld;
+  a.ld_y = e.N;
+  call("moe_expert_linear", [&] { return moe_expert_linear(&a, l.stream); });
+  return y;
+}
+
+std::tuple<OptTensor, OptTensor> expert_linear_backward(const Tensor& dy, const Tensor& x, const Tensor& weight,
+                                                        const Tensor& offsets, const OptTensor& add,
+                                                        const py::object& dw_dtype, bool need_dx, bool need_dw) {
+  const int dt = checked_type(x, "x", true);
+  const Experts e = expert_weights(weight, x, offsets);
+  const Rows r = operand(x, "x", e.K, x);
+  same_shape(dy, with_last(x, e.N), x, "dy");
+  const Rows d = operand(dy, "dy", e.N, x);
+  Rows ra{};
+  if (add.has_value()) {
+    if (!need_dx) refuse("add is a part of dx, which is not asked for");
+    same_shape(*add, x.sizes(), x, "add");
+    ra = rows_of(*add, "add", e.K);
+  }
+  const at::ScalarType wt = x_or_fp32(dw_dtype, "dw_dtype", x, x.scalar_type());
+  const Launch l(x);
+  OptTensor dx, dw;
+  Tensor work;
+  size_t size = 0;
+  moe_expert_linear_args a = expert_args(e, weight, offsets, dt, r.n);
+  if (need_dx) dx = empty(x.sizes(), x.scalar_type(), x);
+  if (need_dw) {
+    dw = empty(weight.sizes(), wt, x);
+    size = moe_expert_linear_workspace(a.E);
+    work = empty({(int64_t)size}, at::kByte, x);
+  }
+  a.dwtype = type_of(wt);
+  a.x = x.data_ptr();
+  a.dy = dy.data_ptr();
+  a.add = ptr(add);
+  a.dx = ptr(dx);
+  a.dw = ptr(dw);
+  a.ld_x = r.ld;
+  a.ld_dy = d.ld;
+  a.ld_add = ra.ld;
+  a.ld_dx = a.ld_dw = e.K;
+  a.stride_dw = e.N * e.K;
+  call("moe_expert_linear_backward",
+       [&] { return moe_expert_linear_backward(&a, size > 0 ? work.data_ptr() : nullptr, size, l.stream); });
+  return {dx, dw};
+}
+
+// ------------------------------------------------------------------------------- checkpoints
+std::tuple<Tensor, Tensor> checkpoint(const Tensor& x) {
+  const Rows r = rows_of(x, "x");
+  const int dt = checked_type(x, "x");
+  const Launch l(x);
+  Tensor codes = empty(x.sizes(), at::kFloat8_e4m3fn, x), scales = empty(with_last(x, (r.c + 31) / 32), at::kByte, x);
+  if (x.numel() == 0) return {codes, scales};
+  moe_checkpoint_args a{};
+  a.n = r.n;
+  a.c = r.c;
+  a.dtype = dt;
+  a.x = x.data_ptr();
+  a.codes = codes.data_ptr();
+  a.scales = static_cast<uint8_t*>(scales.data_ptr());
+  a.ld_x = r.ld;
+  a.ld_codes = r.c;
+  a.ld_scales = (r.c + 31) / 32;
+  call("moe_checkpoint", [&] { return moe_checkpoint(&a, l.stream); });
+  return {codes, scales};
+}
+
+Tensor restore(const Tensor& codes, const Tensor& scales, const py::object& dtype) {
+  check_kept(codes, scales, "the checkpoint", codes);
+  at::ScalarType t = at::ScalarType::Undefined;
+  if (THPDtype_Check(dtype.ptr())) t = reinterpret_cast<THPDtype*>(dtype.ptr())->scalar_type;
+  if (type_of(t) < 0) refuse("dtype ", std::string(py::str(dtype)), ": expected bfloat16, float16 or float32");
+  const Launch l(codes);
+  return restored(codes, scales, t, l);
+}
+
+// ------------------------------------------------------------------------------- gated
+moe_gated_args gated_args(const Tensor& beside, int64_t n, int64_t c, const std::string& act) {
+  moe_gated_args a{};
+  a.n = n;
+  a.c = c;
+  a.dtype = type_of(beside.scalar_type());
+  a.act = act_of(act);
+  return a;
+}
+
+std::tuple<Tensor, OptTensor, OptTensor, OptTensor, OptTensor> gated(const Tensor& gate, const Tensor& up,
+                                                                    const std::string& act, bool keep) {
+  checked_type(gate, "gate", true);
+  const Rows g = rows_of(gate, "gate");
+  same_shape(up, gate.sizes(), gate, "up");
+  const Rows u = rows_of(up, "up", g.c);
+  moe_gated_args a = gated_args(gate, g.n, g.c, act);
+  const Launch l(gate);
+  Tensor h = empty(gate.sizes(), gate.scalar_type(), gate);
+  OptTensor gc, gs, uc, us;
+  if (keep) {
+    const auto blocks = with_last(gate, (g.c + 31) / 32);
+    gc = empty(gate.sizes(), at::kFloat8_e4m3fn, gate);
+    uc = empty(gate.sizes(), at::kFloat8_e4m3fn, gate);
+    gs = empty(blocks, at::kByte, gate);
+    us = empty(blocks, at::kByte, gate);
+  }
+  if (h.numel() == 0) return {h, gc, gs, uc, us};
+  a.gate = gate.data_ptr();
+  a.up = up.data_ptr();
+  a.h = h.data_ptr();
+  a.gate_codes = ptr(gc);
+  a.up_codes = ptr(uc);
+  a.gate_scales = static_cast<uint8_t*>(ptr(gs));
+  a.up_scales = static_cast<uint8_t*>(ptr(us));
+  a.ld_gate = g.ld;
+  a.ld_up = u.ld;
+  a.ld_h = g.c;
+  call("moe_gated", [&] { return moe_gated(&a, l.stream); });
+  return {h, gc, gs, uc, us};
+}
+
+std::tuple<Tensor, Tensor, OptTensor> gated_backward(const Tensor& dh, const Tensor& gate,
+                                                     const OptTensor& gate_scales, const Tensor& up,
+                                                     const OptTensor& up_scales, const std::string& act,
+                                                     bool need_h) {
+  checked_type(dh, "dh", true);
+  const Rows d = rows_of(dh, "dh");
+  if (gate_scales.has_value() != up_scales.has_value())
+    refuse("gate and up must be both matrices or both checkpoints");
+  Rows g{0, d.c, d.c}, u = g;
+  if (gate_scales.has_value()) {
+    check_kept(gate, *gate_scales, "gate", dh);
+    check_kept(up, *up_scales, "up", dh);
+    if (gate.sizes() != dh.sizes() || up.sizes() != dh.sizes())
+      refuse("gate and up must be ", dh.sizes(), ", got ", gate.sizes(), " and ", up.sizes());
+  } else {
+    same_shape(gate, dh.sizes(), dh, "gate");
+    same_shape(up, dh.sizes(), dh, "up");
+    g = rows_of(gate, "gate", d.c);
+    u = rows_of(up, "up", d.c);
+  }
+  moe_gated_args a = gated_args(dh, d.n, d.c, act);
+  const Launch l(dh);
+  Tensor dg = empty(dh.sizes(), dh.scalar_type(), dh), du = empty(dh.sizes(), dh.scalar_type(), dh);
+  OptTensor h;
+  if (need_h) h = empty(dh.sizes(), dh.scalar_type(), dh);
+  if (dh.numel() == 0) return {dg, du, h};
+  a.gate = gate.data_ptr();
+  a.up = up.data_ptr();
+  a.gate_scales = static_cast<uint8_t*>(ptr(gate_scales));
+  a.up_scales = static_cast<uint8_t*>(ptr(up_scales));
+  a.dh = dh.data_ptr();
+  a.dgate = dg.data_ptr();
+  a.dup = du.data_ptr();
+  a.h = ptr(h);
+  a.ld_gate = g.ld;
+  a.ld_up = u.ld;
+  a.ld_dh = d.ld;
+  a.ld_dgate = a.ld_dup = a.ld_h = d.c;
+  call("moe_gated_backward", [&] { return moe_gated_backward(&a, l.stream); });
+  return {dg, du, h};
 }
 
 }  // namespace
@@ -445,4 +832,14 @@ PYBIND11_MODULE(_torch_ops, m) {
   m.def("layer_norm_backward", torch::wrap_pybind_function(&layer_norm_backward));
   m.def("linear", torch::wrap_pybind_function(&linear));
   m.def("linear_backward", torch::wrap_pybind_function(&linear_backward));
+  m.def("sort_experts", torch::wrap_pybind_function(&sort_experts));
+  m.def("expert_rows", torch::wrap_pybind_function(&expert_rows));
+  m.def("combine_experts", torch::wrap_pybind_function(&combine_experts));
+  m.def("combine_experts_backward", torch::wrap_pybind_function(&combine_experts_backward));
+  m.def("expert_linear", torch::wrap_pybind_function(&expert_linear));
+  m.def("expert_linear_backward", torch::wrap_pybind_function(&expert_linear_backward));
+  m.def("checkpoint", torch::wrap_pybind_function(&checkpoint));
+  m.def("restore", torch::wrap_pybind_function(&restore));
+  m.def("gated", torch::wrap_pybind_function(&gated));
+  m.def("gated_backward", torch::wrap_pybind_function(&gated_backward));
 }

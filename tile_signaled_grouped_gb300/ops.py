@@ -1,6 +1,8 @@
-"""The operators of a transformer block around the routed experts, on torch tensors.
+"""The operators of a transformer block around and inside the routed experts, on torch tensors.
 
-route_experts, layer_norm and linear with their backward passes: argument checks and
+route_experts, layer_norm and linear, the way to the experts' rows and back (sort_experts, expert_rows,
+combine_experts), the experts' products (expert_linear) and their activation (gated), with their
+backward passes, and activations kept in 8 bits (checkpoint, restore): argument checks and
 output allocation over the C ABI, in csrc/torch_ops.cpp; every computation is a launch of
 the library's kernels. A matrix is a tensor whose last dimension is contiguous and whose
 other dimensions are one run of rows (any 2-D tensor with a row stride; more dimensions
@@ -18,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -145,16 +148,149 @@ def linear(x, weight, bias=None, act="none", residual=None, preact=False, out_dt
 def linear_backward(dy, x, weight, z=None, act="none", bias=None, dw_dtype=None, need_dx=True,
                     need_dw=True, stream=None):
     """(dx, dweight, dbias) of linear from the gradient dy of y (which is the residual's
-    gradient too), for its x, weight, act and the z that it returned with preact.
+    gradient too), for its x, weight, act and the z that it returned with preact. x, z or both may be
+    their Checkpoints.
 
     bias: the type of dbias (x's or torch.float32), or None for no dbias. dweight has
     dw_dtype (x's type or fp32; default x's). The products take dy act'(z) rounded to x's
     type."""
     if stream is not None:
-        with _on(x, stream):
+        with _on(dy, stream):
             return linear_backward(dy, x, weight, z, act, bias, dw_dtype, need_dx, need_dw)
-    return (_native or native()).linear_backward(dy, x, weight, z, act, bias, dw_dtype, need_dx,
+    x, xs = x if isinstance(x, Checkpoint) else (x, None)
+    z, zs = z if isinstance(z, Checkpoint) else (z, None)
+    return (_native or native()).linear_backward(dy, x, xs, weight, z, zs, act, bias, dw_dtype, need_dx,
                                                  need_dw)
+
+
+# -------------------------------------------------------------------------- checkpoints
+class Checkpoint(NamedTuple):
+    """A tensor [..., c] kept in 8 bits for a backward pass: codes (float8_e4m3fn [..., c]) and
+    scales (uint8 [..., ceil(c / 32)]). An element is code * 2^(scale - 127); 32 elements of a row
+    share a scale, the least for which the largest of them is at most 448 times it."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def checkpoint(x, stream=None):
+    """x [..., c] (bf16, fp16 or fp32) as a Checkpoint: each element is within 2^-4 of itself, or
+    within 2^-10 of its block's scale; what is not finite becomes NaN."""
+    if stream is not None:
+        with _on(x, stream):
+            return checkpoint(x)
+    return Checkpoint(*(_native or native()).checkpoint(x))
+
+
+def restore(kept, dtype, stream=None):
+    """The tensor [..., c] that a Checkpoint stands for, in bf16, fp16 or fp32, contiguous."""
+    if stream is not None:
+        with _on(kept.codes, stream):
+            return restore(kept, dtype)
+    return (_native or native()).restore(kept.codes, kept.scales, dtype)
+
+
+# ----------------------------------------------------------------- rows sorted by expert
+class ExpertOrder(NamedTuple):
+    """A batch's slots (choice j of token t: t * topk + j) in the order of their experts: slots int32 [n],
+    the slot of every row (-1 behind the last row); rows int32 [..., topk], the row of every slot (-1:
+    it has none); offsets int32 [E + 1]: expert e has the rows offsets[e] to offsets[e + 1] - 1."""
+    slots: torch.Tensor
+    rows: torch.Tensor
+    offsets: torch.Tensor
+
+
+def sort_experts(ids, E, stream=None):
+    """The ExpertOrder of ids int32 [..., topk] (as route_experts returns them) among E experts, up to
+    1024. Earlier slots come first in an expert's rows. A slot whose id is not in 0 .. E - 1 (-1, say)
+    has no row."""
+    if stream is not None:
+        with _on(ids, stream):
+            return sort_experts(ids, E)
+    return ExpertOrder(*(_native or native()).sort_experts(ids, E))
+
+
+def expert_rows(x, order, stream=None):
+    """The tokens x [..., D] (bf16, fp16 or fp32) as the rows [n, D] of an order, n its number of
+    slots: row order.rows[t, j] is token t. Rows behind the last are zero."""
+    if stream is not None:
+        with _on(x, stream):
+            return expert_rows(x, order)
+    return (_native or native()).expert_rows(x, order.rows, order.offsets)
+
+
+def expert_rows_backward(d_rows, order, stream=None):
+    """The gradient of expert_rows' x from that of its rows [n, D]: a token's is the sum of its
+    rows', added in fp32 and rounded once."""
+    return combine_experts(d_rows, None, order, stream)
+
+
+def combine_experts(r, w, order, stream=None):
+    """y [..., D]: y[t] = sum over j of w[t, j] * r[order.rows[t, j]], added in fp32 in the order of j and
+    rounded once, for the experts' rows r [n, D] (bf16, fp16 or fp32) and weights w fp32 [..., topk] (None:
+    ones). Slots without a row have no part in it."""
+    if stream is not None:
+        with _on(r, stream):
+            return combine_experts(r, w, order)
+    return (_native or native()).combine_experts(r, w, order.rows, order.offsets)
+
+
+def combine_experts_backward(dy, r, w, order, stream=None):
+    """(d_r, d_w) of combine_experts from the gradient dy of y, for its r (or the Checkpoint of r), w and
+    order. d_r has dy's type, and zeros behind the last row; d_w is fp32, 0 for slots without a row."""
+    if stream is not None:
+        with _on(dy, stream):
+            return combine_experts_backward(dy, r, w, order)
+    r, scales = r if isinstance(r, Checkpoint) else (r, None)
+    return (_native or native()).combine_experts_backward(dy, r, scales, w, order.rows, order.offsets)
+
+
+# ----------------------------------------------------------------------- expert products
+def expert_linear(x, weight, offsets, stream=None):
+    """y [n, N]: y[r] = weight[e] x[r] for the rows offsets[e] to offsets[e + 1] - 1 of every expert e, with
+    fp32 sums; zeros in the rows from offsets[E] on.
+
+    x: [n, K], weight: [E, N, K], both bf16 or both fp16, N and K multiples of 8, rows on 16
+    bytes; offsets: int32 [E + 1] on the device, as sort_experts returns them."""
+    if stream is not None:
+        with _on(x, stream):
+            return expert_linear(x, weight, offsets)
+    return (_native or native()).expert_linear(x, weight, offsets)
+
+
+def expert_linear_backward(dy, x, weight, offsets, add=None, dw_dtype=None, need_dx=True, need_dw=True,
+                           stream=None):
+    """(dx, dweight) of expert_linear from the gradient dy of y, for its x, weight and offsets. add [n, K] of
+    x's type is added to dx before it is rounded (the gradient through another product of the same x).
+    dweight has dw_dtype (x's type or fp32; default x's); it is zero for experts without rows."""
+    if stream is not None:
+        with _on(x, stream):
+            return expert_linear_backward(dy, x, weight, offsets, add, dw_dtype, need_dx, need_dw)
+    return (_native or native()).expert_linear_backward(dy, x, weight, offsets, add, dw_dtype, need_dx,
+                                                        need_dw)
+
+
+# ------------------------------------------------------------------------ gated activation
+def gated(gate, up, act="silu", checkpoint=False, stream=None):
+    """(h, kept): h = act(gate) * up, for gate and up [..., F] both bf16 or both fp16 (columns of one
+    matrix, say); act as in linear. kept (with checkpoint, else None): the Checkpoints of gate and
+    up for gated_backward."""
+    if stream is not None:
+        with _on(gate, stream):
+            return gated(gate, up, act, checkpoint)
+    h, gc, gs, uc, us = (_native or native()).gated(gate, up, act, checkpoint)
+    return h, (Checkpoint(gc, gs), Checkpoint(uc, us)) if checkpoint else None
+
+
+def gated_backward(dh, gate, up, act="silu", need_h=False, stream=None):
+    """(d_gate, d_up, h) of gated from the gradient dh of h, for its gate and up or the Checkpoints of both.
+    h, act(gate) * up once more (with need_h, else None), is what the product after it was given,
+    or stands for it where gate and up are Checkpoints."""
+    if stream is not None:
+        with _on(dh, stream):
+            return gated_backward(dh, gate, up, act, need_h)
+    gate, gs = gate if isinstance(gate, Checkpoint) else (gate, None)
+    up, us = up if isinstance(up, Checkpoint) else (up, None)
+    return (_native or native()).gated_backward(dh, gate, gs, up, us, act, need_h)
 
 
 def _device_of(stream):
