@@ -75,6 +75,32 @@ __device__ __forceinline__ float act_grad(float z) {
   return 1.f;
 }
 
+// act(z), and in *d act'(z), as act_of and act_grad have them (bit for bit: where act_grad keeps z
+// inside its limits, what it takes of z there is 0 or 1 on both sides of them): the exponential is shared.
+template <int ACT>
+__device__ __forceinline__ float act_both(float z, float* d) {
+  if (ACT == MOE_ACT_SILU || ACT == MOE_ACT_GELU || ACT == MOE_ACT_GELU_TANH) {
+    constexpr float kLow = ACT == MOE_ACT_SILU ? -100.f : -30.f;
+    const float v = z > 30.f ? 30.f : z < kLow ? kLow : z;
+    if (ACT == MOE_ACT_GELU) {
+      float e;
+      const float p = normal_cdf(z, &e);
+      *d = fmaf(v * 0.3989422804014327f, e, p);
+      return z * p;
+    }
+    if (ACT == MOE_ACT_GELU_TANH) {
+      const float q = fast_sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
+      *d = q + v * q * (1.0f - q) * (2.0f * kGeluC0) * (1.0f + 3.0f * kGeluC1 * v * v);
+      return z * q;
+    }
+    const float q = fast_sigmoid(z);
+    *d = q * (1.0f + v * (1.0f - q));
+    return z * q;
+  }
+  *d = act_grad<ACT>(z);
+  return act_of<ACT>(z);
+}
+
 }  // namespace moe
 
 #endif  // __CUDACC__

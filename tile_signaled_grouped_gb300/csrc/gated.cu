@@ -35,13 +35,6 @@ struct Walk {
 };
 
 template <typename T, int N>
-__device__ __forceinline__ void load_n(const T* p, float (&f)[N]) {
-  if constexpr (N == 1)
-    f[0] = to_f32(*p);
-  else
-    unpack<T>(__ldg(reinterpret_cast<const uint4*>(p)), f);
-}
-template <typename T, int N>
 __device__ __forceinline__ void store_n(T* p, const float (&f)[N]) {
   if constexpr (N == 1)
     *p = from_f32<T>(f[0]);
@@ -49,34 +42,38 @@ __device__ __forceinline__ void store_n(T* p, const float (&f)[N]) {
     *reinterpret_cast<uint4*>(p) = pack<T>(f);
 }
 
-// N elements of a block, whose other elements the neighbouring lanes have (zeros outside the row),
-// to codes and, by the block's first lane, the scale. Whole warps.
-template <int N>
-__device__ __forceinline__ void encode_block(const float (&f)[N], bool in, uint8_t* codes, uint8_t* scales,
-                                             int lane) {
-  constexpr int kLanes = kScaleBlock / N;
-  uint32_t most = 0;
-#pragma unroll
-  for (int q = 0; q < N; ++q) most = max(most, finite_bits(f[q]));
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) most = max(most, __shfl_xor_sync(kAll, most, o));
-  if (!in) return;
-  const uint32_t s = scale_of(most);
-  const float inverse = scale_inverse(s);
-  if constexpr (N == 1) {
-    *codes = encode1(f[0], inverse);
-  } else {
-    uint32_t w[N / 4];
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-      w[i] = encode2(f[4 * i], f[4 * i + 1], inverse) | encode2(f[4 * i + 2], f[4 * i + 3], inverse) << 16;
-    if constexpr (N == 8)
-      *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
+// N elements as they lie in memory: a vector of 16 bytes, or one element.
+template <typename T, int N>
+struct Raw {
+  typename std::conditional<N == 1, T, uint4>::type u;
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (N == 1)
+      u = *p;
     else
-      *reinterpret_cast<uint32_t*>(codes) = w[0];
+      u = __ldg(reinterpret_cast<const uint4*>(p));
   }
-  if (lane % kLanes == 0) *scales = (uint8_t)s;
-}
+  __device__ __forceinline__ void clear() {
+    if constexpr (N == 1)
+      u = from_f32<T>(0.f);
+    else
+      u = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+    if constexpr (N == 1)
+      f[0] = to_f32(u);
+    else
+      unpack<T>(u, f);
+  }
+  __device__ __forceinline__ void encode(bool in, uint8_t* codes, uint8_t* scales, int lane) const {
+    if constexpr (N == 8) {
+      encode_block16<T>(u, in, codes, scales, lane);
+    } else {
+      float f[N];
+      get(f);
+      encode_block<N>(f, in, codes, scales, lane);
+    }
+  }
+};
 
 // ------------------------------------------------------------------- checkpoint and restore
 struct CheckArgs {
@@ -95,46 +92,57 @@ __global__ void __launch_bounds__(32 * kWarps) checkpoint_kernel(const __grid_co
   for (long long u = k.first(); u < k.units; u += k.step()) {
     const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kCheckUnits + lane * N;
     const T* x = static_cast<const T*>(a.x) + i * a.ld_x;
-    float f[kCheckUnits][N];
-#pragma unroll
-    for (int q = 0; q < kCheckUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      if (c < a.c) {
-        load_n<T, N>(x + c, f[q]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) f[q][e] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kCheckUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      encode_block<N>(f[q], c < a.c, a.codes + i * a.ld_codes + c, a.scales + i * a.ld_scales + c / kScaleBlock,
-                      lane);
-    }
-  }
-}
-
-template <typename T, int N>
-__global__ void __launch_bounds__(32 * kWarps) restore_kernel(const __grid_constant__ CheckArgs a) {
-  allow_dependent_launch();
-  wait_prior_grid();
-  const int lane = threadIdx.x & 31;
-  const Walk k(a.n, a.c, 32 * N * kCheckUnits);
-  for (long long u = k.first(); u < k.units; u += k.step()) {
-    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kCheckUnits + lane * N;
-    T* x = static_cast<T*>(a.x) + i * a.ld_x;
-    float f[kCheckUnits][N];
+    Raw<T, N> v[kCheckUnits];
 #pragma unroll
     for (int q = 0; q < kCheckUnits; ++q) {
       const long long c = c0 + 32 * N * q;
       if (c < a.c)
-        decode<N>(a.codes + i * a.ld_codes + c,
-                  scale_value(__ldg(a.scales + i * a.ld_scales + c / kScaleBlock)), f[q]);
+        v[q].load(x + c);
+      else
+        v[q].clear();
     }
 #pragma unroll
-    for (int q = 0; q < kCheckUnits; ++q)
-      if (c0 + 32 * N * q < a.c) store_n<T, N>(x + c0 + 32 * N * q, f[q]);
+    for (int q = 0; q < kCheckUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      v[q].encode(c < a.c, a.codes + i * a.ld_codes + c, a.scales + i * a.ld_scales + c / kScaleBlock, lane);
+    }
+  }
+}
+
+// N codes a lane: 16, in two or four stores, where they start on 16 bytes.
+template <typename T, int N>
+__global__ void __launch_bounds__(32 * kWarps) restore_kernel(const __grid_constant__ CheckArgs a) {
+  constexpr int kUnits = N == 16 ? 2 : 4, kStore = N < Vec<T>::kN ? N : Vec<T>::kN;
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const Walk k(a.n, a.c, 32 * N * kUnits);
+  for (long long u = k.first(); u < k.units; u += k.step()) {
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kUnits + lane * N;
+    T* x = static_cast<T*>(a.x) + i * a.ld_x;
+    Codes<N> v[kUnits];
+    uint8_t s[kUnits];
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+      const long long c = c0 + 32 * N * q;
+      if (c < a.c) {
+        v[q].load(a.codes + i * a.ld_codes + c);
+        s[q] = __ldg(a.scales + i * a.ld_scales + c / kScaleBlock);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+      if (c0 + 32 * N * q >= a.c) continue;
+      float f[N];
+      v[q].get(scale_value(s[q]), f);
+#pragma unroll
+      for (int p = 0; p < N; p += kStore) {
+        float o[kStore];
+#pragma unroll
+        for (int e = 0; e < kStore; ++e) o[e] = f[p + e];
+        store_n<T, kStore>(x + c0 + 32 * N * q + p, o);
+      }
+    }
   }
 }
 
@@ -158,16 +166,16 @@ __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constan
     const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kGatedUnits + lane * N;
     const T* gate = static_cast<const T*>(a.gate) + i * a.ld_gate;
     const T* up = static_cast<const T*>(a.up) + i * a.ld_up;
-    float g[kGatedUnits][N], v[kGatedUnits][N];
+    Raw<T, N> g[kGatedUnits], v[kGatedUnits];
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
       const long long c = c0 + 32 * N * q;
       if (c < a.c) {
-        load_n<T, N>(gate + c, g[q]);
-        load_n<T, N>(up + c, v[q]);
+        g[q].load(gate + c);
+        v[q].load(up + c);
       } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) g[q][e] = v[q][e] = 0.f;
+        g[q].clear();
+        v[q].clear();
       }
     }
 #pragma unroll
@@ -175,13 +183,15 @@ __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constan
       const long long c = c0 + 32 * N * q;
       if (KEEP) {
         const long long code = i * a.ld_codes + c, scale = i * a.ld_scales + c / kScaleBlock;
-        encode_block<N>(g[q], c < a.c, a.gate_codes + code, a.gate_scales + scale, lane);
-        encode_block<N>(v[q], c < a.c, a.up_codes + code, a.up_scales + scale, lane);
+        g[q].encode(c < a.c, a.gate_codes + code, a.gate_scales + scale, lane);
+        v[q].encode(c < a.c, a.up_codes + code, a.up_scales + scale, lane);
       }
       if (c < a.c) {
-        float h[N];
+        float x[N], h[N];
+        g[q].get(x);
+        v[q].get(h);
 #pragma unroll
-        for (int e = 0; e < N; ++e) h[e] = act_of<ACT>(g[q][e]) * v[q][e];
+        for (int e = 0; e < N; ++e) h[e] *= act_of<ACT>(x[e]);
         store_n<T, N>(static_cast<T*>(a.h) + i * a.ld_h + c, h);
       }
     }
@@ -196,38 +206,51 @@ __global__ void __launch_bounds__(32 * kWarps) gated_backward_kernel(const __gri
   const Walk k(a.n, a.c, 32 * N * kGatedUnits);
   for (long long u = k.first(); u < k.units; u += k.step()) {
     const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kGatedUnits + lane * N;
-    float g[kGatedUnits][N], v[kGatedUnits][N], d[kGatedUnits][N];
+    typename std::conditional<KEPT, Codes<N>, Raw<T, N>>::type g[kGatedUnits], v[kGatedUnits];
+    uint8_t gs[kGatedUnits], vs[kGatedUnits];
+    Raw<T, N> d[kGatedUnits];
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
       const long long c = c0 + 32 * N * q;
       if (c >= a.c) continue;
       if constexpr (KEPT) {
         const long long code = i * a.ld_codes + c, scale = i * a.ld_scales + c / kScaleBlock;
-        decode<N>(static_cast<const uint8_t*>(a.gate) + code, scale_value(__ldg(a.gate_scales + scale)), g[q]);
-        decode<N>(static_cast<const uint8_t*>(a.up) + code, scale_value(__ldg(a.up_scales + scale)), v[q]);
+        g[q].load(static_cast<const uint8_t*>(a.gate) + code);
+        v[q].load(static_cast<const uint8_t*>(a.up) + code);
+        gs[q] = __ldg(a.gate_scales + scale);
+        vs[q] = __ldg(a.up_scales + scale);
       } else {
-        load_n<T, N>(static_cast<const T*>(a.gate) + i * a.ld_gate + c, g[q]);
-        load_n<T, N>(static_cast<const T*>(a.up) + i * a.ld_up + c, v[q]);
+        g[q].load(static_cast<const T*>(a.gate) + i * a.ld_gate + c);
+        v[q].load(static_cast<const T*>(a.up) + i * a.ld_up + c);
       }
-      load_n<T, N>(static_cast<const T*>(a.dh) + i * a.ld_dh + c, d[q]);
+      d[q].load(static_cast<const T*>(a.dh) + i * a.ld_dh + c);
     }
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
       const long long c = c0 + 32 * N * q;
       if (c >= a.c) continue;
-      float act[N], o[N];
+      float x[N], y[N], dh[N], o[N];
+      if constexpr (KEPT) {
+        g[q].get(scale_value(gs[q]), x);
+        v[q].get(scale_value(vs[q]), y);
+      } else {
+        g[q].get(x);
+        v[q].get(y);
+      }
+      d[q].get(dh);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        act[e] = act_of<ACT>(g[q][e]);
-        o[e] = d[q][e] * v[q][e] * act_grad<ACT>(g[q][e]);
+        float slope;
+        x[e] = act_both<ACT>(x[e], &slope);
+        o[e] = dh[e] * y[e] * slope;
       }
       store_n<T, N>(static_cast<T*>(a.dgate) + i * a.ld_dgate + c, o);
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = d[q][e] * act[e];
+      for (int e = 0; e < N; ++e) o[e] = dh[e] * x[e];
       store_n<T, N>(static_cast<T*>(a.dup) + i * a.ld_dup + c, o);
       if (a.h != nullptr) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = act[e] * v[q][e];
+        for (int e = 0; e < N; ++e) o[e] = x[e] * y[e];
         store_n<T, N>(static_cast<T*>(a.h) + i * a.ld_h + c, o);
       }
     }
@@ -256,10 +279,16 @@ int launched(cudaError_t e) {
 template <typename T>
 int launch_checkpoint(const CheckArgs& a, bool vec, bool restore, cudaStream_t s) {
   constexpr int N = Vec<T>::kN;
-  const dim3 grid(grid_of(a.n, a.c, 32 * kCheckUnits * (vec ? N : 1))), block(32 * kWarps);
-  if (restore)
+  const dim3 block(32 * kWarps);
+  if (restore) {
+    if (vec && a.c % 16 == 0 && vector_rows(a.codes, a.ld_codes, a.n, 1, 16))
+      return launched(
+          launch_behind(restore_kernel<T, 16>, dim3(grid_of(a.n, a.c, 32 * 16 * 2)), block, 0, s, a));
+    const dim3 grid(grid_of(a.n, a.c, 32 * 4 * (vec ? N : 1)));
     return launched(vec ? launch_behind(restore_kernel<T, N>, grid, block, 0, s, a)
                         : launch_behind(restore_kernel<T, 1>, grid, block, 0, s, a));
+  }
+  const dim3 grid(grid_of(a.n, a.c, 32 * kCheckUnits * (vec ? N : 1)));
   return launched(vec ? launch_behind(checkpoint_kernel<T, N>, grid, block, 0, s, a)
                       : launch_behind(checkpoint_kernel<T, 1>, grid, block, 0, s, a));
 }
