@@ -24,8 +24,8 @@ constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kFeatures = 256;                  // of a pair's tile
 constexpr int kRows = 256;                      // of a pair's tile at most
 constexpr int kRowStep = 32;                    // columns of a product come in this step
-constexpr int kABytes = 128 * 128;              // a CTA's features of a stage
-constexpr int kStageBytes = kABytes + 128 * 128;  // and half of the pair's rows
+constexpr int kABytes = 128 * 128;              // a CTA's features of a block of 64 k
+constexpr int kBlockBytes = kABytes + 128 * 128;  // and half of the pair's rows
 constexpr int kPatchPitch = 80;                 // bytes of a row of 32 features, on 16 bytes
 constexpr int kPatchBytes = kEpiWarps * 32 * kPatchPitch;
 
@@ -107,7 +107,7 @@ __device__ __forceinline__ void wait_products(PairSmem& sm, uint32_t* status) {
 
 // ------------------------------------------------------------------- y and dx
 struct RowsArgs {
-  CUtensorMap tw, tx;  // weights (3-D: experts outermost), rows
+  CUtensorMap tw, tx, tx4;  // weights (3-D: experts outermost), 32 rows, 128 rows
   const int32_t* offsets;
   void* y;             // [n][ld_y]
   const void* add;     // [n][ld_add] or null
@@ -117,6 +117,7 @@ struct RowsArgs {
   int tiles_j, stages;
   bool bf16, w_mn;     // w_mn: W^T, whose features are innermost
 };
+constexpr int kBlocks = 2;  // of 64 k in a stage
 
 // The table of the experts' rows in shared memory, entry E for the rows behind the last expert's
 // (zeros): first row, number, and the tiles of rows before it. An expert's rows are shared out evenly
@@ -198,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* patches = base + (size_t)a.stages * kStageBytes;
+  uint8_t* patches = base + (size_t)a.stages * kBlocks * kBlockBytes;
   int* table_at = reinterpret_cast<int*>(patches + kPatchBytes);
   PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kPatchBytes + table_bytes(a.E));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -206,6 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool lead = crank == 0;
   pair_setup(sm, a.stages, warp);
   const uint32_t tmem = sm.tmem;
+  allow_dependent_launch();
   wait_prior_grid();
   const Table table = make_table(a, table_at, sm.scratch);
   RowWalk walk(a, table, blockIdx.x >> 1, gridDim.x >> 1);
@@ -217,25 +219,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (ok && walk.next()) {
       const int j = walk.j0 + (int)crank * 128, half = walk.cols / 2;
       const int row = walk.row0 + (int)crank * half, boxes = (half + 31) / 32, steps = walk.steps();
-      const uint32_t bytes = 2 * (kABytes + boxes * 4096);
-      for (int kb = 0; kb < steps; ++kb, ++n) {
+      const bool four = boxes > 2;  // one copy of 128 rows
+      const uint32_t bytes = 2 * (kABytes + (four ? 4 : boxes) * 4096);
+      for (int kb = 0; kb < steps; kb += kBlocks, ++n) {
         if (!warp_pwait(&sm.empty[st], phase, &sm.abort, a.status, 0x41000000u)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          uint8_t* as = base + (size_t)st * kStageBytes;
-          uint8_t* bs = as + kABytes;
-          if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
+          uint8_t* as = base + (size_t)st * (kBlocks * kBlockBytes);
+          const int blocks = min(kBlocks, steps - kb);
+          if (lead) mbar_arrive_expect_tx(&sm.full[st], blocks * bytes);
           const uint32_t fb = map_shared(&sm.full[st], 0);
-          const int k0 = kb * kBlockK;
-          if (a.w_mn) {
-            tma_load_3d_pair(as, &a.tw, fb, j, k0, walk.e);
-            tma_load_3d_pair(as + 8192, &a.tw, fb, j + 64, k0, walk.e);
-          } else {
-            tma_load_3d_pair(as, &a.tw, fb, k0, j, walk.e);
+          for (int k0 = kb * kBlockK; k0 < (kb + blocks) * kBlockK; k0 += kBlockK, as += kBlockBytes) {
+            uint8_t* bs = as + kABytes;
+            if (a.w_mn) {
+              tma_load_3d_pair(as, &a.tw, fb, j, k0, walk.e);
+              tma_load_3d_pair(as + 8192, &a.tw, fb, j + 64, k0, walk.e);
+            } else {
+              tma_load_3d_pair(as, &a.tw, fb, k0, j, walk.e);
+            }
+            if (four) {
+              tma_load_2d_pair(bs, &a.tx4, fb, k0, row);
+            } else {
+              tma_load_2d_pair(bs, &a.tx, fb, k0, row);
+              if (boxes == 2) tma_load_2d_pair(bs + 4096, &a.tx, fb, k0, row + 32);
+            }
           }
-          for (int b = 0; b < boxes; ++b) tma_load_2d_pair(bs + b * 4096, &a.tx, fb, k0, row + b * 32);
         }
         __syncwarp();
         next_stage(st, phase, a.stages);
@@ -256,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, a.status, 0x44000000u)) break;
       tc_fence_after();
       const uint32_t dt = tmem + (uint32_t)(acc * kRows);
-      for (int kb = 0; kb < steps; ++kb) {
+      for (int kb = 0; kb < steps; kb += kBlocks) {
         if (!warp_pwait(&sm.full[st], phase, &sm.abort, a.status, 0x45000000u)) {
           ok = false;
           break;
@@ -266,11 +276,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k)
             tc_mma_pair(dt, da + at + k * step_a, db + at + k * (32 >> 4), idesc, (kb | k) != 0 ? 1u : 0u);
+          if (kb + 1 < steps) {
+            const uint32_t bt = at + (kBlockBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < kBlockK / 16; ++k)
+              tc_mma_pair(dt, da + bt + k * step_a, db + bt + k * (32 >> 4), idesc, 1u);
+          }
           tc_commit_pair(&sm.empty[st], 0x3);
         }
         __syncwarp();
         next_stage(st, phase, a.stages);
-        at = st == 0 ? 0 : at + (kStageBytes >> 4);
+        at = st == 0 ? 0 : at + (kBlocks * kBlockBytes >> 4);
       }
       if (ok && elect_one()) tc_commit_pair(&sm.tfull[acc], 0x3);
       __syncwarp();
@@ -426,17 +442,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  PairSmem& sm = *reinterpret_cast<PairSmem*>(base + (size_t)a.stages * kStageBytes);
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(base + (size_t)a.stages * kBlockBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
   pair_setup(sm, a.stages, warp);
   const uint32_t tmem = sm.tmem;
+  allow_dependent_launch();
   wait_prior_grid();
   WeightWalk walk(a, blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
-    constexpr uint32_t bytes = 2 * kStageBytes;
+    constexpr uint32_t bytes = 2 * kBlockBytes;
     int n = 0, st = 0, expert = -1;
     uint32_t phase = 1;
     bool ok = true;
@@ -455,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         if (elect_one()) {
-          uint8_t* as = base + (size_t)st * kStageBytes;
+          uint8_t* as = base + (size_t)st * kBlockBytes;
           uint8_t* bs = as + kABytes;
           if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
           const uint32_t fb = map_shared(&sm.full[st], 0);
@@ -496,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         next_stage(st, phase, a.stages);
-        at = st == 0 ? 0 : at + (kStageBytes >> 4);
+        at = st == 0 ? 0 : at + (kBlockBytes >> 4);
       }
       if (ok && elect_one()) tc_commit_pair(&sm.tfull[acc], 0x3);
       __syncwarp();
@@ -608,9 +625,10 @@ int launched(cudaError_t e) {
   cudaGetLastError();
   return MOE_ERR_CUDA;
 }
-size_t smem_bytes(int stages, size_t more) { return 1024 + (size_t)stages * kStageBytes + more + sizeof(PairSmem); }
-int stages_for(size_t more) {
-  return std::min<int>(kMaxStages, (int)((kSmemMax - smem_bytes(0, more)) / kStageBytes));
+size_t smem_bytes(size_t stages, size_t more) { return 1024 + stages + more + sizeof(PairSmem); }
+// Stages of `bytes` that fit beside `more`.
+int stages_for(size_t bytes, size_t more) {
+  return std::min<int>(kMaxStages, (int)((kSmemMax - smem_bytes(0, more)) / bytes));
 }
 
 // y of the forward pass, or dx: `w_mn` takes W^T.
@@ -632,18 +650,20 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   a.ld_add = ld_add;
   a.status = ops_status();
   if (a.status == nullptr || !make_map(&a.tw, p->w, a.bf16, p->E, p->N, p->K, p->ld_w, p->stride_w, w_mn ? 64 : 128) ||
-      !make_map(&a.tx, x, a.bf16, 0, p->n, sum, ld_x, 0, 32))
+      !make_map(&a.tx, x, a.bf16, 0, p->n, sum, ld_x, 0, 32) ||
+      !make_map(&a.tx4, x, a.bf16, 0, p->n, sum, ld_x, 0, 128))
     return MOE_ERR_CUDA;
   // Tiles of rows: one for every 256 and one more for each expert at most.
   const long long tiles = (p->n / kRows + std::min<long long>(p->E + 1, p->n)) * a.tiles_j;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t more = kPatchBytes + table_bytes(a.E);
-  a.stages = stages_for(more);
+  constexpr size_t kStage = kBlocks * kBlockBytes;
+  a.stages = stages_for(kStage, more);
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(expert_rows_product_kernel), &ready);
   if (e == cudaSuccess)
     e = launch_behind(expert_rows_product_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)),
-                      dim3(kThreads), smem_bytes(a.stages, more), s, a);
+                      dim3(kThreads), smem_bytes(a.stages * kStage, more), s, a);
   return launched(e);
 }
 
@@ -681,13 +701,13 @@ int weights_product(const moe_expert_linear_args* p, void* workspace, int sms, c
   a.wide = aligned_to(p->dw, 32) && a.ld % per == 0 && a.stride % per == 0;
   const long long tiles = (long long)a.tiles_i * a.tiles_j * a.E;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
-  a.stages = stages_for(0);
+  a.stages = stages_for(kBlockBytes, 0);
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(expert_weights_kernel), &ready);
   if (e == cudaSuccess) e = launch_behind(expert_maps_kernel, dim3(p->E), dim3(32), 0, s, m);
   if (e == cudaSuccess)
     e = launch_behind(expert_weights_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(kThreads),
-                      smem_bytes(a.stages, 0), s, a);
+                      smem_bytes((size_t)a.stages * kBlockBytes, 0), s, a);
   return launched(e);
 }
 
