@@ -603,11 +603,8 @@ int moe_expert_linear(const moe_expert_linear_args *args, moe_stream_t stream);
 
 /* dx[r] = w[e]^T dy[r] + add[r] (rows from offsets[E] on: add alone, or zero);
  * dw[e] = sum over its rows of dy[r] x[r]^T (zero without rows). fp32 sums in a fixed order, rounded
- * once. workspace: at least moe_expert_linear_workspace(E) bytes (pure host arithmetic), 256-byte
- * aligned, for dw; used until the call has run on the stream. */
-size_t moe_expert_linear_workspace(int E);
-int moe_expert_linear_backward(const moe_expert_linear_args *args, void *workspace,
-                               size_t workspace_bytes, moe_stream_t stream);
+ * once. */
+int moe_expert_linear_backward(const moe_expert_linear_args *args, moe_stream_t stream);
 
 /* The device waits of the products and of layer norm are bounded; one that runs out sets a
  * sticky status of the device (its results are void). Synchronises `stream` and reads the

@@ -173,8 +173,7 @@ def load():
         "moe_gated": (ip, [P(moe_gated_args), vp]),
         "moe_gated_backward": (ip, [P(moe_gated_args), vp]),
         "moe_expert_linear": (ip, [P(moe_expert_linear_args), vp]),
-        "moe_expert_linear_workspace": (sz, [ip]),
-        "moe_expert_linear_backward": (ip, [P(moe_expert_linear_args), vp, sz, vp]),
+        "moe_expert_linear_backward": (ip, [P(moe_expert_linear_args), vp]),
         "moe_ops_status": (ip, [vp, P(ip), P(ip)]),
         "moe_ops_status_clear": (ip, [vp]),
         "moe_layer_norm": (ip, [P(moe_norm_args), vp]),

@@ -9,6 +9,7 @@
 
 #include <type_traits>
 
+#include "any_rows.cuh"
 #include "ops_common.cuh"
 
 namespace moe {
@@ -43,109 +44,89 @@ __device__ __forceinline__ uint32_t encode2(float a, float b, float inverse) {
   return __nv_cvt_float2_to_fp8x2(make_float2(code_input(a, inverse), code_input(b, inverse)), __NV_SATFINITE,
                                   __NV_E4M3);
 }
-__device__ __forceinline__ uint8_t encode1(float a, float inverse) {
-  return __nv_cvt_float_to_fp8(code_input(a, inverse), __NV_SATFINITE, __NV_E4M3);
-}
 __device__ __forceinline__ float2 decode2(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// N consecutive codes of one block as they lie in memory (the address is a multiple of N), and times 2^s.
-template <int N>
+// N consecutive codes from code c of a row of `width`, as they lie in memory (zeros outside), and times
+// 2^s. ANY: the row starts anywhere; else on N bytes, and whole vectors are inside or outside.
+template <int N, bool ANY>
 struct Codes {
-  uint32_t w[(N + 3) / 4];
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (N == 16) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    } else if constexpr (N == 8) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = u.x, w[1] = u.y;
-    } else if constexpr (N == 4) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  Words<N> v;
+  __device__ __forceinline__ void load(const uint8_t* row, long long c, long long width) {
+    if constexpr (ANY) {
+      v = load_any<N>(row + c, bytes_left<uint8_t>(c, width));
     } else {
-      static_assert(N == 1, "16, 8, 4 or 1 codes");
-      w[0] = __ldg(p);
+      v = Words<N>{};
+      if (c < width) v = load_words<N>(row + c);
     }
   }
   __device__ __forceinline__ void get(float scale, float (&f)[N]) const {
-    if constexpr (N == 1) {
-      f[0] = decode2(w[0]).x * scale;
-    } else {
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float2 d = decode2(w[i / 2] >> (16 * (i & 1)) & 0xFFFFu);
-        f[2 * i] = d.x * scale;
-        f[2 * i + 1] = d.y * scale;
-      }
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 d = decode2(v.w[i / 2] >> (16 * (i & 1)) & 0xFFFFu);
+      f[2 * i] = d.x * scale;
+      f[2 * i + 1] = d.y * scale;
     }
   }
 };
-template <int N>
-__device__ __forceinline__ void decode(const uint8_t* p, float scale, float (&f)[N]) {
-  Codes<N> c;
-  c.load(p);
-  c.get(scale, f);
+// The codes of one element.
+__device__ __forceinline__ float decode1(const uint8_t* p, float scale) { return decode2(__ldg(p)).x * scale; }
+
+// The codes of N elements from element c of a row of `width`, and their block's scale, for elements
+// whose largest finite |x| in the block (other lanes have the rest of it) has the bits `most`.
+// FINITE: all of the block are. Whole warps where ANY.
+template <int N, bool ANY, bool FINITE>
+__device__ __forceinline__ void store_codes(const float (&f)[N], uint32_t most, uint8_t* codes, uint8_t* scales,
+                                            long long c, long long width, int lane) {
+  const uint32_t s = scale_of(most);
+  const float inverse = scale_inverse(s);
+  Words<N> o;
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const float* g = f + 4 * i;
+    if constexpr (FINITE)
+      o.w[i] = __nv_cvt_float2_to_fp8x2(make_float2(g[0] * inverse, g[1] * inverse), __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(g[2] * inverse, g[3] * inverse), __NV_SATFINITE,
+                                                  __NV_E4M3) << 16;
+    else
+      o.w[i] = encode2(g[0], g[1], inverse) | encode2(g[2], g[3], inverse) << 16;
+  }
+  if constexpr (ANY)
+    store_any<N, 1>(codes + c, c == 0, bytes_left<uint8_t>(c, width), o, lane, kOwn<true, true>);
+  else if (c < width)
+    store_words<N>(codes + c, o);
+  if (c < width && c % kScaleBlock == 0 && (!ANY || lane < kOwn<true, true>)) scales[c / kScaleBlock] = (uint8_t)s;
 }
 
-// N elements of a block, whose other elements the neighbouring lanes have (zeros outside the row),
-// to codes and, by the block's first lane, the scale. Whole warps.
-template <int N>
-__device__ __forceinline__ void encode_block(const float (&f)[N], bool in, uint8_t* codes, uint8_t* scales,
-                                             int lane) {
-  constexpr int kLanes = kScaleBlock / N;
+// A lane's vector of a row to codes; the block's other elements are in the neighbouring lanes, c is a
+// multiple of the vector. Whole warps. Of 16-bit types the bits of |x| are in the order of |x|, so two
+// elements at a time give the largest; only where that is not finite do they have to be looked
+// at one by one (131 instructions for eight elements one by one, 60 so).
+template <typename T, bool ANY>
+__device__ __forceinline__ void encode_vec(const RowVec<T, ANY>& x, uint8_t* codes, uint8_t* scales, long long c,
+                                           long long width, int lane) {
+  constexpr int N = Vec<T>::kN;
+  float f[N];
+  if constexpr (sizeof(T) == 2) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu, kInf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    uint32_t m = __vmaxu2(__vmaxu2(x.v.w[0] & kAbs, x.v.w[1] & kAbs), __vmaxu2(x.v.w[2] & kAbs, x.v.w[3] & kAbs));
+    m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 2));
+    m = max(m & 0xFFFFu, m >> 16);
+    if (!__any_sync(kAll, m >= kInf)) {
+      x.get(f);
+      store_codes<N, ANY, true>(f, __float_as_uint(unpack2<T>(m).x), codes, scales, c, width, lane);
+      return;
+    }
+  }
+  x.get(f);
   uint32_t most = 0;
 #pragma unroll
   for (int q = 0; q < N; ++q) most = max(most, finite_bits(f[q]));
 #pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) most = max(most, __shfl_xor_sync(kAll, most, o));
-  if (!in) return;
-  const uint32_t s = scale_of(most);
-  const float inverse = scale_inverse(s);
-  if constexpr (N == 1) {
-    *codes = encode1(f[0], inverse);
-  } else {
-    uint32_t w[N / 4];
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-      w[i] = encode2(f[4 * i], f[4 * i + 1], inverse) | encode2(f[4 * i + 2], f[4 * i + 3], inverse) << 16;
-    if constexpr (N == 8)
-      *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(codes) = w[0];
-  }
-  if (lane % kLanes == 0) *scales = (uint8_t)s;
-}
-
-// The same for eight elements of 16 bits as they lie in memory. The bits of |x| are in the order of
-// |x|, so two elements at a time give the largest; only where that is not finite do the
-// elements have to be looked at one by one. (131 instructions for eight elements of 16 bits by
-// encode_block, 60 so.)
-template <typename T>
-__device__ __forceinline__ void encode_block16(const uint4& u, bool in, uint8_t* codes, uint8_t* scales, int lane) {
-  constexpr uint32_t kAbs = 0x7FFF7FFFu, kInf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-  uint32_t m = __vmaxu2(__vmaxu2(u.x & kAbs, u.y & kAbs), __vmaxu2(u.z & kAbs, u.w & kAbs));
-  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 1));
-  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 2));
-  m = max(m & 0xFFFFu, m >> 16);
-  if (__any_sync(kAll, m >= kInf)) {
-    float f[8];
-    unpack<T>(u, f);
-    encode_block<8>(f, in, codes, scales, lane);
-    return;
-  }
-  if (!in) return;
-  const uint32_t s = scale_of(__float_as_uint(unpack2<T>(m).x));
-  const float inverse = scale_inverse(s);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack2<T>(w[i]);
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(p.x * inverse, p.y * inverse), __NV_SATFINITE, __NV_E4M3);
-  }
-  *reinterpret_cast<uint2*>(codes) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-  if ((lane & 3) == 0) *scales = (uint8_t)s;
+  for (int o = 1; o < kScaleBlock / N; o <<= 1) most = max(most, __shfl_xor_sync(kAll, most, o));
+  store_codes<N, ANY, false>(f, most, codes, scales, c, width, lane);
 }
 
 #endif  // __CUDACC__

@@ -7,8 +7,8 @@
 // How many rows an expert has is known on the device only, and is uneven. So the rows are the columns
 // of the products y^T = W x^T and dx^T = W^T dy^T, whose number a tcgen05.mma takes in steps of 32, and the
 // 256 features of a CTA pair's tile are its rows: an expert with 40 rows costs 64 columns where it would
-// cost a whole tile of 128 or 256 rows. In dW the rows are summed over: tensor maps of each expert's
-// rows, made on the device, fill with zeros what lies past them.
+// cost a whole tile of 128 or 256 rows. In dW the rows are summed over, 64 at a time, and those past an expert's
+// last are zeroed in shared memory.
 #include <algorithm>
 #include <atomic>
 
@@ -24,6 +24,7 @@ constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kFeatures = 256;                  // of a pair's tile
 constexpr int kRows = 256;                      // of a pair's tile at most
 constexpr int kRowStep = 32;                    // columns of a product come in this step
+constexpr int kGroup = 8;                       // tiles of rows that walk the features together
 constexpr int kABytes = 128 * 128;              // a CTA's features of a block of 64 k
 constexpr int kBlockBytes = kABytes + 128 * 128;  // and half of the pair's rows
 constexpr int kPatchPitch = 80;                 // bytes of a row of 32 features, on 16 bytes
@@ -33,6 +34,7 @@ struct PairSmem {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
+  uint64_t last[kMaxStages];  // dW: this CTA's copies of a block with rows past the expert's last
   uint32_t tmem;
   int abort;
   int scratch[33];
@@ -56,10 +58,12 @@ __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int E, in
 }
 
 // The barriers and the tensor memory of a pair; both CTAs have them when it returns.
-__device__ __forceinline__ void pair_setup(PairSmem& sm, int stages, int warp) {
+// `full`: arrivals that fill a stage.
+__device__ __forceinline__ void pair_setup(PairSmem& sm, int stages, int warp, int full) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&sm.full[i], 1);   // rank 0: its arrive.expect_tx (bytes of both CTAs)
+      mbar_init(&sm.full[i], full);  // rank 0: its arrive.expect_tx (bytes of both CTAs) is one
+      mbar_init(&sm.last[i], 1);
       mbar_init(&sm.empty[i], 1);  // the leader's commit (multicast)
     }
     for (int i = 0; i < 2; ++i) {
@@ -107,7 +111,7 @@ __device__ __forceinline__ void wait_products(PairSmem& sm, uint32_t* status) {
 
 // ------------------------------------------------------------------- y and dx
 struct RowsArgs {
-  CUtensorMap tw, tx, tx4;  // weights (3-D: experts outermost), 32 rows, 128 rows
+  CUtensorMap tw, tx[4];  // weights (3-D: experts outermost); 16, 32, 64 and 128 rows
   const int32_t* offsets;
   void* y;             // [n][ld_y]
   const void* add;     // [n][ld_add] or null
@@ -179,8 +183,13 @@ struct RowWalk {
     }
     e = lo;
     const int tiles = (t.count[e] + kRows - 1) / kRows, local = at - t.first[e] * a.tiles_j;
-    const int tj = local / tiles, ti = local - tj * tiles;
-    const int per = tiles > 8 ? kRows : ((t.count[e] + tiles - 1) / tiles + kRowStep - 1) / kRowStep * kRowStep;
+    // Groups of kGroup tiles of rows, inside a group feature by feature: the tiles in flight share their
+    // operands in L2 (all tiles of rows of a feature tile first took 185 us where this takes 149 for 16384
+    // rows of one expert, 2048 x 4096).
+    const int g = local / (kGroup * a.tiles_j), r = local - g * kGroup * a.tiles_j;
+    const int in_group = min(kGroup, tiles - g * kGroup), tj = r / in_group, ti = g * kGroup + r - tj * in_group;
+    const int even = ((t.count[e] + tiles - 1) / tiles + kRowStep - 1) / kRowStep * kRowStep;
+    const int per = tiles > 8 ? kRows : even;  // of more than eight the last might be left without rows
     j0 = tj * kFeatures;
     row0 = t.start[e] + ti * per;
     rows = min(per, t.count[e] - ti * per);
@@ -205,9 +214,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
-  pair_setup(sm, a.stages, warp);
+  pair_setup(sm, a.stages, warp, 1);
   const uint32_t tmem = sm.tmem;
-  allow_dependent_launch();
   wait_prior_grid();
   const Table table = make_table(a, table_at, sm.scratch);
   RowWalk walk(a, table, blockIdx.x >> 1, gridDim.x >> 1);
@@ -218,9 +226,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && walk.next()) {
       const int j = walk.j0 + (int)crank * 128, half = walk.cols / 2;
-      const int row = walk.row0 + (int)crank * half, boxes = (half + 31) / 32, steps = walk.steps();
-      const bool four = boxes > 2;  // one copy of 128 rows
-      const uint32_t bytes = 2 * (kABytes + (four ? 4 : boxes) * 4096);
+      const int row = walk.row0 + (int)crank * half, steps = walk.steps();
+      const uint32_t bytes = 2 * (kABytes + half * 128);
       for (int kb = 0; kb < steps; kb += kBlocks, ++n) {
         if (!warp_pwait(&sm.empty[st], phase, &sm.abort, a.status, 0x41000000u)) {
           ok = false;
@@ -239,11 +246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
               tma_load_3d_pair(as, &a.tw, fb, k0, j, walk.e);
             }
-            if (four) {
-              tma_load_2d_pair(bs, &a.tx4, fb, k0, row);
-            } else {
-              tma_load_2d_pair(bs, &a.tx, fb, k0, row);
-              if (boxes == 2) tma_load_2d_pair(bs + 4096, &a.tx, fb, k0, row + 32);
+            // 128 rows, or those of 64, 32 and 16 that make up a half: no more than the products take.
+#pragma unroll
+            for (int b = 3, at = 0; b >= 0; --b) {
+              if (half & (16 << b)) {
+                tma_load_2d_pair(bs + at * 128, &a.tx[b], fb, k0, row + at);
+                at += 16 << b;
+              }
             }
           }
         }
@@ -360,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- dW
 struct WeightArgs {
-  const CUtensorMap* maps;  // [E][2]: an expert's rows of dy and of x
+  CUtensorMap ty, tx;  // rows of dy and of x
   const int32_t* offsets;
   void* dw;                 // [E][N][K], rows ld apart, experts `stride`
   long long ld, stride;
@@ -371,57 +380,14 @@ struct WeightArgs {
   bool wide;                // rows of dw start on 32 bytes
 };
 
-// Tensor maps of every expert's rows, from maps of all rows: a map's first row and number of rows are
-// the expert's, so that copies read zeros past its last row. Experts without rows have none (theirs are
-// not read).
-struct MapArgs {
-  CUtensorMap ty, tx;
-  const int32_t* offsets;
-  const char *dy, *x;
-  long long row_y, row_x;  // bytes of a row
-  CUtensorMap* maps;
-  int n, E;
-};
-__global__ void __launch_bounds__(32) expert_maps_kernel(const __grid_constant__ MapArgs a) {
-  __shared__ alignas(128) uint32_t map[2][32];
-  allow_dependent_launch();
-  wait_prior_grid();
-  const int lane = threadIdx.x, e = blockIdx.x;
-  int start, count;
-  rows_of(a.offsets, e, a.E, a.n, &start, &count);
-  if (count == 0) return;
-  map[0][lane] = reinterpret_cast<const uint32_t*>(&a.ty)[lane];
-  map[1][lane] = reinterpret_cast<const uint32_t*>(&a.tx)[lane];
-  __syncwarp();
-  if (lane < 2) {
-    const uint32_t at = smem_u32(map[lane]);
-    const char* rows = lane == 0 ? a.dy + start * a.row_y : a.x + start * a.row_x;
-    asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(at), "l"(rows)
-                 : "memory");
-    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(at), "r"(count)
-                 : "memory");
-  }
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    asm volatile(
-        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
-            a.maps + 2 * e + i),
-        "r"(smem_u32(map[i]))
-        : "memory");
-}
-__device__ __forceinline__ void acquire_map(const CUtensorMap* m) {
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
-}
-
 // The tiles of a pair: p, p + pairs, ... of the order expert, columns, rows of dW.
 struct WeightWalk {
   const WeightArgs& a;
   int at, pairs;
-  int e, i0, j0, steps;
+  int e, i0, j0, start, count, steps;  // the expert's rows; blocks of 64 of them
 
   __device__ __forceinline__ WeightWalk(const WeightArgs& args, int pair, int n)
-      : a(args), at(pair - n), pairs(n), e(0), i0(0), j0(0), steps(0) {}
+      : a(args), at(pair - n), pairs(n), e(0), i0(0), j0(0), start(0), count(0), steps(0) {}
   __device__ __forceinline__ bool next() {
     at += pairs;
     const int per = a.tiles_i * a.tiles_j;
@@ -430,14 +396,13 @@ struct WeightWalk {
     const int local = at - e * per, tj = local / a.tiles_i;
     i0 = (local - tj * a.tiles_i) * 256;
     j0 = tj * 256;
-    int start, count;
     rows_of(a.offsets, e, a.E, a.n, &start, &count);
     steps = (count + kBlockK - 1) / kBlockK;
     return true;
   }
 };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
     expert_weights_kernel(const __grid_constant__ WeightArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -446,25 +411,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
-  pair_setup(sm, a.stages, warp);
+  pair_setup(sm, a.stages, warp, 2);
   const uint32_t tmem = sm.tmem;
-  allow_dependent_launch();
   wait_prior_grid();
   WeightWalk walk(a, blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
-    constexpr uint32_t bytes = 2 * kBlockBytes;
-    int n = 0, st = 0, expert = -1;
+    int n = 0, st = 0;
     uint32_t phase = 1;
     bool ok = true;
     while (ok && walk.next()) {
-      const CUtensorMap* ty = a.maps + 2 * walk.e;
-      const CUtensorMap* tx = ty + 1;
-      if (walk.e != expert && walk.steps > 0) {
-        acquire_map(ty);
-        acquire_map(tx);
-        expert = walk.e;
-      }
       const int i = walk.i0 + (int)crank * 128, j = walk.j0 + (int)crank * 128;
       for (int kb = 0; kb < walk.steps; ++kb, ++n) {
         if (!warp_pwait(&sm.empty[st], phase, &sm.abort, a.status, 0x51000000u)) {
@@ -474,13 +430,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           uint8_t* as = base + (size_t)st * kBlockBytes;
           uint8_t* bs = as + kABytes;
-          if (lead) mbar_arrive_expect_tx(&sm.full[st], bytes);
-          const uint32_t fb = map_shared(&sm.full[st], 0);
-          const int k0 = kb * kBlockK;
-          tma_load_2d_pair(as, ty, fb, i, k0);
-          tma_load_2d_pair(as + 8192, ty, fb, i + 64, k0);
-          tma_load_2d_pair(bs, tx, fb, j, k0);
-          tma_load_2d_pair(bs + 8192, tx, fb, j + 64, k0);
+          const int row = walk.start + kb * kBlockK;
+          uint32_t bar;
+          if (walk.count - kb * kBlockK < kBlockK) {  // the warps that clear the rest fill this stage
+            mbar_arrive_expect_tx(&sm.last[st], kBlockBytes);
+            bar = map_shared(&sm.last[st], crank);
+          } else {
+            if (lead) {
+              mbar_arrive_expect_tx(&sm.full[st], 2 * kBlockBytes);
+              mbar_arrive(&sm.full[st]);
+            }
+            bar = map_shared(&sm.full[st], 0);
+          }
+          tma_load_2d_pair(as, &a.ty, bar, i, row);
+          tma_load_2d_pair(as + 8192, &a.ty, bar, i + 64, row);
+          tma_load_2d_pair(bs, &a.tx, bar, j, row);
+          tma_load_2d_pair(bs + 8192, &a.tx, bar, j + 64, row);
         }
         __syncwarp();
         next_stage(st, phase, a.stages);
@@ -519,6 +484,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     wait_products(sm, a.status);
+  } else if (warp == 2 + kEpiWarps) {
+    // Clears the rows past the expert's last in this CTA's half of its last block: they are another
+    // expert's (or what lies behind the rows), and a NaN there times zero would be one. A block is
+    // 64 rows of 128 bytes for each 64 columns; the swizzle stays inside a row.
+    int n = 0;
+    uint32_t used = 0;  // bit i: the phase of last[i]
+    while (walk.next()) {
+      n += walk.steps;
+      const int rows = walk.count - (walk.steps - 1) * kBlockK;
+      if (walk.steps == 0 || rows == kBlockK) continue;
+      const int st = (n - 1) % a.stages;
+      if (!warp_pwait(&sm.last[st], (used >> st) & 1, &sm.abort, a.status, 0x57000000u)) break;
+      used ^= 1u << st;
+      uint8_t* at = base + (size_t)st * kBlockBytes;
+      for (int o = rows * 128 + lane * 16; o < 8192; o += 512) {
+#pragma unroll
+        for (int b = 0; b < kBlockBytes / 8192; ++b) *reinterpret_cast<uint4*>(at + b * 8192 + o) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the products read by the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared(&sm.full[st], 0));
+    }
   } else if (warp >= 2) {
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the columns
     const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
@@ -649,10 +636,10 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   a.add = add;
   a.ld_add = ld_add;
   a.status = ops_status();
-  if (a.status == nullptr || !make_map(&a.tw, p->w, a.bf16, p->E, p->N, p->K, p->ld_w, p->stride_w, w_mn ? 64 : 128) ||
-      !make_map(&a.tx, x, a.bf16, 0, p->n, sum, ld_x, 0, 32) ||
-      !make_map(&a.tx4, x, a.bf16, 0, p->n, sum, ld_x, 0, 128))
+  if (a.status == nullptr || !make_map(&a.tw, p->w, a.bf16, p->E, p->N, p->K, p->ld_w, p->stride_w, w_mn ? 64 : 128))
     return MOE_ERR_CUDA;
+  for (int b = 0; b < 4; ++b)
+    if (!make_map(&a.tx[b], x, a.bf16, 0, p->n, sum, ld_x, 0, 16 << b)) return MOE_ERR_CUDA;
   // Tiles of rows: one for every 256 and one more for each expert at most.
   const long long tiles = (p->n / kRows + std::min<long long>(p->E + 1, p->n)) * a.tiles_j;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
@@ -667,22 +654,12 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   return launched(e);
 }
 
-int weights_product(const moe_expert_linear_args* p, void* workspace, int sms, cudaStream_t s) {
-  MapArgs m{};
-  const bool bf16 = p->dtype == MOE_BF16;
-  m.offsets = p->offsets;
-  m.dy = static_cast<const char*>(p->dy);
-  m.x = static_cast<const char*>(p->x);
-  m.row_y = p->ld_dy * 2;
-  m.row_x = p->ld_x * 2;
-  m.maps = static_cast<CUtensorMap*>(workspace);
-  m.n = (int)p->n;
-  m.E = p->E;
-  if (!make_map(&m.ty, p->dy, bf16, 0, p->n, p->N, p->ld_dy, 0, 64) ||
-      !make_map(&m.tx, p->x, bf16, 0, p->n, p->K, p->ld_x, 0, 64))
-    return MOE_ERR_CUDA;
+int weights_product(const moe_expert_linear_args* p, int sms, cudaStream_t s) {
   WeightArgs a{};
-  a.maps = m.maps;
+  const bool bf16 = p->dtype == MOE_BF16;
+  if (!make_map(&a.ty, p->dy, bf16, 0, p->n, p->N, p->ld_dy, 0, kBlockK) ||
+      !make_map(&a.tx, p->x, bf16, 0, p->n, p->K, p->ld_x, 0, kBlockK))
+    return MOE_ERR_CUDA;
   a.offsets = p->offsets;
   a.dw = p->dw;
   a.ld = p->ld_dw;
@@ -704,9 +681,8 @@ int weights_product(const moe_expert_linear_args* p, void* workspace, int sms, c
   a.stages = stages_for(kBlockBytes, 0);
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(expert_weights_kernel), &ready);
-  if (e == cudaSuccess) e = launch_behind(expert_maps_kernel, dim3(p->E), dim3(32), 0, s, m);
   if (e == cudaSuccess)
-    e = launch_behind(expert_weights_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(kThreads),
+    e = launch_behind(expert_weights_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(kThreads + 32),
                       smem_bytes((size_t)a.stages * kBlockBytes, 0), s, a);
   return launched(e);
 }
@@ -731,12 +707,7 @@ int moe_expert_linear(const moe_expert_linear_args* p, moe_stream_t stream) {
   return rows_product(p, p->x, p->ld_x, false, nullptr, 0, p->y, p->ld_y, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t moe_expert_linear_workspace(int E) {
-  return E < 1 || E > kMaxExperts ? 0 : (size_t)E * 2 * sizeof(CUtensorMap);
-}
-
-int moe_expert_linear_backward(const moe_expert_linear_args* p, void* workspace, size_t workspace_bytes,
-                               moe_stream_t stream) {
+int moe_expert_linear_backward(const moe_expert_linear_args* p, moe_stream_t stream) {
   int rc = check_experts(p);
   if (rc != MOE_OK) return rc;
   if (p->dwtype != p->dtype && p->dwtype != MOE_FP32) return MOE_ERR_ARG;
@@ -758,15 +729,13 @@ int moe_expert_linear_backward(const moe_expert_linear_args* p, void* workspace,
       (p->dx != nullptr && (!check_matrix(p->dx, p->ld_dx, p->n, p->K) ||
                             !check_weights(p->w, p->ld_w, p->stride_w, p) || !aligned_to(p->add, 2) ||
                             (p->add != nullptr && p->n > 1 && p->ld_add < p->K))) ||
-      (p->dw != nullptr && (!check_matrix(p->x, p->ld_x, p->n, p->K) || workspace == nullptr ||
-                            !aligned_to(workspace, 256))))
+      (p->dw != nullptr && !check_matrix(p->x, p->ld_x, p->n, p->K)))
     return MOE_ERR_ARG;
-  if (p->dw != nullptr && workspace_bytes < moe_expert_linear_workspace(p->E)) return MOE_ERR_WORKSPACE;
   rc = ops_device(&sms);
   if (rc != MOE_OK) return rc;
   if (p->dx != nullptr)
     rc = rows_product(p, p->dy, p->ld_dy, true, p->add, p->ld_add, p->dx, p->ld_dx, sms, s);
-  if (rc == MOE_OK && p->dw != nullptr) rc = weights_product(p, workspace, sms, s);
+  if (rc == MOE_OK && p->dw != nullptr) rc = weights_product(p, sms, s);
   return rc;
 }
 

@@ -184,37 +184,21 @@ __global__ void __launch_bounds__(32 * kRowWarps) expert_rows_kernel(const __gri
     for (long long c = lane; c < a.D; c += 32) out[row * a.ld_d + c] = U{};
 }
 
-// N elements as fp32: a vector of 16 bytes, or one.
-template <typename T, int N>
-__device__ __forceinline__ void load_n(const T* p, float (&f)[N]) {
-  if constexpr (N == 1)
-    f[0] = to_f32(*p);
-  else
-    unpack<T>(__ldg(reinterpret_cast<const uint4*>(p)), f);
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_n(T* p, const float (&f)[N]) {
-  if constexpr (N == 1)
-    *p = from_f32<T>(f[0]);
-  else
-    *reinterpret_cast<uint4*>(p) = pack<T>(f);
-}
-
 // The weighted sum of a token's rows, in the order of its slots, fp32. A warp takes 64 vectors of a
 // token; four rows' loads leave before the first is added. A row that a slot has not is no term of
 // the sum (not one times zero: what lies there may be NaN). Bound by the bytes of the rows.
+// ANY: rows that do not start on 16 bytes.
 constexpr int kSumSlots = 4, kSumUnits = 2;
-template <typename T, int N>
+template <typename T, bool ANY>
 __global__ void __launch_bounds__(32 * kRowWarps) combine_kernel(const __grid_constant__ RowsArgs a) {
+  constexpr int N = Vec<T>::kN, kLanes = kOwn<ANY> * N, kSpan = kLanes * kSumUnits;
   allow_dependent_launch();
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * kRowWarps;
-  const long long width = a.D / N, chunks = (width + 32 * kSumUnits - 1) / (32 * kSumUnits);
+  const long long warps = (long long)gridDim.x * kRowWarps, chunks = (a.D + kSpan - 1) / kSpan;
   const T* r = static_cast<const T*>(a.r);
-  T* y = static_cast<T*>(a.y);
   for (long long u = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < a.T * chunks; u += warps) {
-    const long long t = u / chunks, c = (u - t * chunks) * 32 * kSumUnits + lane;
+    const long long t = u / chunks, c = (u - t * chunks) * kSpan + lane * N;
     int mine = -1;
     float weight = 1.f;
     if (lane < a.topk) {
@@ -227,53 +211,55 @@ __global__ void __launch_bounds__(32 * kRowWarps) combine_kernel(const __grid_co
 #pragma unroll
       for (int q = 0; q < N; ++q) sum[i][q] = 0.f;
     for (int j0 = 0; j0 < a.topk; j0 += kSumSlots) {
-      float v[kSumSlots][kSumUnits][N];
+      RowVec<T, ANY> v[kSumSlots][kSumUnits];
       int row[kSumSlots];
 #pragma unroll
       for (int j = 0; j < kSumSlots; ++j) {
-        row[j] = j0 + j < a.topk ? __shfl_sync(kAll, mine, j0 + j) : -1;
+        row[j] = __shfl_sync(kAll, mine, min(j0 + j, 31));  // lanes from topk on have none
+        if (row[j] < 0) continue;
 #pragma unroll
-        for (int i = 0; i < kSumUnits; ++i)
-          if (row[j] >= 0 && c + 32 * i < width) load_n<T, N>(r + row[j] * a.ld_r + (c + 32 * i) * N, v[j][i]);
+        for (int i = 0; i < kSumUnits; ++i) v[j][i].load(r + row[j] * a.ld_r, c + kLanes * i, a.D);
       }
 #pragma unroll
       for (int j = 0; j < kSumSlots; ++j) {
-        const float w = j0 + j < a.topk ? __shfl_sync(kAll, weight, j0 + j) : 0.f;
+        const float w = __shfl_sync(kAll, weight, min(j0 + j, 31));
         if (row[j] < 0) continue;
 #pragma unroll
-        for (int i = 0; i < kSumUnits; ++i)
+        for (int i = 0; i < kSumUnits; ++i) {
+          float f[N];
+          v[j][i].get(f);
 #pragma unroll
-          for (int q = 0; q < N; ++q) sum[i][q] = fmaf(w, v[j][i][q], sum[i][q]);
+          for (int q = 0; q < N; ++q) sum[i][q] = fmaf(w, f[q], sum[i][q]);
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < kSumUnits; ++i)
-      if (c + 32 * i < width) store_n<T, N>(y + t * a.ld_x + (c + 32 * i) * N, sum[i]);
+    for (int i = 0; i < kSumUnits; ++i) {
+      if (ANY && c - lane * N + kLanes * i >= a.D) break;  // the whole warp is past the row
+      store_vec<ANY>(static_cast<T*>(a.y) + t * a.ld_x, c + kLanes * i, a.D, sum[i], lane);
+    }
   }
 }
 
-// Elements of a row that was kept, N at a time, as they lie in memory.
-template <typename T, int N, bool EIGHT>
+// Elements of a row that was kept, a vector of T at a time, as they lie in memory.
+template <typename T, bool EIGHT, bool ANY>
 struct Kept {
-  typename std::conditional<EIGHT, Codes<N>, typename std::conditional<N == 1, T, uint4>::type>::type u;
+  static constexpr int N = Vec<T>::kN;
+  typename std::conditional<EIGHT, Codes<N, ANY>, RowVec<T, ANY>>::type u;
   uint8_t scale;
   __device__ __forceinline__ void load(const RowsArgs& a, long long row, int c) {
     if constexpr (EIGHT) {
-      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r + c * N);
-      scale = __ldg(a.scales + row * a.ld_s + c * N / kScaleBlock);
-    } else if constexpr (N == 1) {
-      u = static_cast<const T*>(a.r)[row * a.ld_r + c];
+      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, c, ANY ? a.D : c + N);
+      scale = !ANY || c < a.D ? __ldg(a.scales + row * a.ld_s + c / kScaleBlock) : 0;
     } else {
-      u = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.r) + row * a.ld_r) + c);
+      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, ANY ? a.D : c + N);
     }
   }
   __device__ __forceinline__ void get(float (&f)[N]) const {
     if constexpr (EIGHT)
       u.get(scale_value(scale), f);
-    else if constexpr (N == 1)
-      f[0] = to_f32(u);
     else
-      unpack<T>(u, f);
+      u.get(f);
   }
 };
 
@@ -284,13 +270,13 @@ struct Kept {
 // of eight warps fit on an SM (as fp32 the eight vectors took 121 registers, and 328 us where this takes
 // 126 for 4096 tokens of 8 x 7168 from codes).
 constexpr int kBackSlots = 8;
-template <typename T, int N, bool EIGHT>
-__global__ void __launch_bounds__(256, 3) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
+template <typename T, bool EIGHT, bool ANY>
+__global__ void __launch_bounds__(256, ANY ? 2 : 3) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
+  constexpr int N = Vec<T>::kN, kSpan = kOwn<ANY> * N;
   __shared__ float part[8][kBackSlots];
   allow_dependent_launch();
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int width = (int)(a.D / N);
   T* dr = static_cast<T*>(a.dr);
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const T* dy = static_cast<const T*>(a.x) + t * a.ld_x;
@@ -304,23 +290,29 @@ __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const __grid_c
         w[j] = in ? __ldg(a.w + t * a.topk + j0 + j) : 0.f;
         dot[j] = 0.f;
       }
-      for (int c = threadIdx.x; c < width; c += blockDim.x) {
-        Kept<T, N, EIGHT> v[kBackSlots];
-        float d[N];
-        load_n<T, N>(dy + (long long)c * N, d);
+      for (int c0 = warp * kSpan; c0 < a.D; c0 += warps * kSpan) {
+        const int c = c0 + lane * N;
+        if (!ANY && c >= a.D) break;
+        Kept<T, EIGHT, ANY> v[kBackSlots];
+        RowVec<T, ANY> x;
+        x.load(dy, c, ANY ? a.D : c + N);  // without ANY, c is inside
 #pragma unroll
         for (int j = 0; j < kBackSlots; ++j)
           if (row[j] >= 0) v[j].load(a, row[j], c);
+        float d[N];
+        x.get(d);
 #pragma unroll
         for (int j = 0; j < kBackSlots; ++j) {
           if (row[j] < 0) continue;
           float f[N];
           v[j].get(f);
+          if (!ANY || lane < kOwn<ANY>) {
 #pragma unroll
-          for (int q = 0; q < N; ++q) dot[j] = fmaf(d[q], f[q], dot[j]);
+            for (int q = 0; q < N; ++q) dot[j] = fmaf(d[q], f[q], dot[j]);
+          }
 #pragma unroll
           for (int q = 0; q < N; ++q) f[q] = w[j] * d[q];
-          store_n<T, N>(dr + row[j] * a.ld_d + (long long)c * N, f);
+          store_vec<ANY>(dr + row[j] * a.ld_d, c, ANY ? a.D : c + N, f, lane);
         }
       }
 #pragma unroll
@@ -391,25 +383,22 @@ int launch_rows(const RowsArgs& a, cudaStream_t s) {
 
 template <typename T>
 int launch_combine(const RowsArgs& a, bool vec, cudaStream_t s) {
-  constexpr int N = Vec<T>::kN;
-  const long long width = vec ? a.D / N : a.D, chunks = (width + 32 * kSumUnits - 1) / (32 * kSumUnits);
-  const dim3 grid(row_grid(a.T * chunks)), block(32 * kRowWarps);
-  return launched(vec ? launch_behind(combine_kernel<T, N>, grid, block, 0, s, a)
-                      : launch_behind(combine_kernel<T, 1>, grid, block, 0, s, a));
+  const int span = (vec ? 32 : kOwn<true>) * Vec<T>::kN * kSumUnits;
+  const dim3 grid(row_grid(a.T * ((a.D + span - 1) / span))), block(32 * kRowWarps);
+  return launched(vec ? launch_behind(combine_kernel<T, false>, grid, block, 0, s, a)
+                      : launch_behind(combine_kernel<T, true>, grid, block, 0, s, a));
 }
 
 template <typename T>
 int launch_backward(const RowsArgs& a, bool vec, cudaStream_t s) {
-  constexpr int N = Vec<T>::kN;
-  const long long width = vec ? a.D / N : a.D;
   // Warps of a token: four vectors of a lane each, eight warps at most.
-  const unsigned warps = (unsigned)std::min<long long>(8, std::max<long long>(1, width / 128));
+  const unsigned warps = (unsigned)std::min<long long>(8, std::max<long long>(1, a.D / Vec<T>::kN / 128));
   const dim3 grid((unsigned)std::min<long long>(a.T, 1 << 20)), block(32 * warps);
   if (a.scales != nullptr)
-    return launched(vec ? launch_behind(combine_backward_kernel<T, N, true>, grid, block, 0, s, a)
-                        : launch_behind(combine_backward_kernel<T, 1, true>, grid, block, 0, s, a));
-  return launched(vec ? launch_behind(combine_backward_kernel<T, N, false>, grid, block, 0, s, a)
-                      : launch_behind(combine_backward_kernel<T, 1, false>, grid, block, 0, s, a));
+    return launched(vec ? launch_behind(combine_backward_kernel<T, true, false>, grid, block, 0, s, a)
+                        : launch_behind(combine_backward_kernel<T, true, true>, grid, block, 0, s, a));
+  return launched(vec ? launch_behind(combine_backward_kernel<T, false, false>, grid, block, 0, s, a)
+                      : launch_behind(combine_backward_kernel<T, false, true>, grid, block, 0, s, a));
 }
 
 // Slots of a lane, so that there are at most kSortChunks chunks.

@@ -9,7 +9,7 @@
 // Elementwise, so bound by the bytes; all arithmetic is fp32, each output is rounded once. A warp
 // takes kUnits vectors of 16 bytes a lane, whose loads all leave before the first is used. A block
 // of 32 elements lies in neighbouring lanes, whose largest |x| meet by shuffles. Rows that do not start on
-// 16 bytes go by single elements, a lane each.
+// 16 bytes: any_rows.cuh.
 #include <algorithm>
 
 #include "activations.cuh"
@@ -34,47 +34,6 @@ struct Walk {
   __device__ __forceinline__ long long step() const { return (long long)gridDim.x * kWarps; }
 };
 
-template <typename T, int N>
-__device__ __forceinline__ void store_n(T* p, const float (&f)[N]) {
-  if constexpr (N == 1)
-    *p = from_f32<T>(f[0]);
-  else
-    *reinterpret_cast<uint4*>(p) = pack<T>(f);
-}
-
-// N elements as they lie in memory: a vector of 16 bytes, or one element.
-template <typename T, int N>
-struct Raw {
-  typename std::conditional<N == 1, T, uint4>::type u;
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (N == 1)
-      u = *p;
-    else
-      u = __ldg(reinterpret_cast<const uint4*>(p));
-  }
-  __device__ __forceinline__ void clear() {
-    if constexpr (N == 1)
-      u = from_f32<T>(0.f);
-    else
-      u = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void get(float (&f)[N]) const {
-    if constexpr (N == 1)
-      f[0] = to_f32(u);
-    else
-      unpack<T>(u, f);
-  }
-  __device__ __forceinline__ void encode(bool in, uint8_t* codes, uint8_t* scales, int lane) const {
-    if constexpr (N == 8) {
-      encode_block16<T>(u, in, codes, scales, lane);
-    } else {
-      float f[N];
-      get(f);
-      encode_block<N>(f, in, codes, scales, lane);
-    }
-  }
-};
-
 // ------------------------------------------------------------------- checkpoint and restore
 struct CheckArgs {
   void* x;
@@ -83,56 +42,51 @@ struct CheckArgs {
 };
 constexpr int kCheckUnits = 4;
 
-template <typename T, int N>
+template <typename T, bool ANY>
 __global__ void __launch_bounds__(32 * kWarps) checkpoint_kernel(const __grid_constant__ CheckArgs a) {
+  constexpr int N = Vec<T>::kN;
   allow_dependent_launch();
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const Walk k(a.n, a.c, 32 * N * kCheckUnits);
+  constexpr int kSpan = kOwn<ANY, true> * N;  // elements that a warp stores at a time
+  const Walk k(a.n, a.c, kSpan * kCheckUnits);
   for (long long u = k.first(); u < k.units; u += k.step()) {
-    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kCheckUnits + lane * N;
-    const T* x = static_cast<const T*>(a.x) + i * a.ld_x;
-    Raw<T, N> v[kCheckUnits];
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * kSpan * kCheckUnits + lane * N;
+    RowVec<T, ANY> v[kCheckUnits];
+#pragma unroll
+    for (int q = 0; q < kCheckUnits; ++q)
+      v[q].load(static_cast<const T*>(a.x) + i * a.ld_x, c0 + kSpan * q, a.c);
 #pragma unroll
     for (int q = 0; q < kCheckUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      if (c < a.c)
-        v[q].load(x + c);
-      else
-        v[q].clear();
-    }
-#pragma unroll
-    for (int q = 0; q < kCheckUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      v[q].encode(c < a.c, a.codes + i * a.ld_codes + c, a.scales + i * a.ld_scales + c / kScaleBlock, lane);
+      if (ANY && c0 - lane * N + kSpan * q >= a.c) break;  // the whole warp is past the row
+      encode_vec<T, ANY>(v[q], a.codes + i * a.ld_codes, a.scales + i * a.ld_scales, c0 + kSpan * q, a.c, lane);
     }
   }
 }
 
 // N codes a lane: 16, in two or four stores, where they start on 16 bytes.
-template <typename T, int N>
+template <typename T, int N, bool ANY>
 __global__ void __launch_bounds__(32 * kWarps) restore_kernel(const __grid_constant__ CheckArgs a) {
-  constexpr int kUnits = N == 16 ? 2 : 4, kStore = N < Vec<T>::kN ? N : Vec<T>::kN;
+  constexpr int kUnits = N == 16 ? 2 : 4, kStore = Vec<T>::kN;
   allow_dependent_launch();
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const Walk k(a.n, a.c, 32 * N * kUnits);
+  constexpr int kSpan = kOwn<ANY> * N;
+  const Walk k(a.n, a.c, kSpan * kUnits);
   for (long long u = k.first(); u < k.units; u += k.step()) {
-    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kUnits + lane * N;
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * kSpan * kUnits + lane * N;
     T* x = static_cast<T*>(a.x) + i * a.ld_x;
-    Codes<N> v[kUnits];
+    Codes<N, ANY> v[kUnits];
     uint8_t s[kUnits];
 #pragma unroll
     for (int q = 0; q < kUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      if (c < a.c) {
-        v[q].load(a.codes + i * a.ld_codes + c);
-        s[q] = __ldg(a.scales + i * a.ld_scales + c / kScaleBlock);
-      }
+      const long long c = c0 + kSpan * q;
+      v[q].load(a.codes + i * a.ld_codes, c, a.c);
+      s[q] = c < a.c ? __ldg(a.scales + i * a.ld_scales + c / kScaleBlock) : 0;
     }
 #pragma unroll
     for (int q = 0; q < kUnits; ++q) {
-      if (c0 + 32 * N * q >= a.c) continue;
+      if (ANY && c0 - lane * N + kSpan * q >= a.c) break;  // the whole warp is past the row
       float f[N];
       v[q].get(scale_value(s[q]), f);
 #pragma unroll
@@ -140,7 +94,7 @@ __global__ void __launch_bounds__(32 * kWarps) restore_kernel(const __grid_const
         float o[kStore];
 #pragma unroll
         for (int e = 0; e < kStore; ++e) o[e] = f[p + e];
-        store_n<T, kStore>(x + c0 + 32 * N * q + p, o);
+        store_vec<ANY>(x, c0 + kSpan * q + p, a.c, o, lane);
       }
     }
   }
@@ -156,79 +110,74 @@ struct GatedArgs {
 };
 constexpr int kGatedUnits = 2;
 
-template <typename T, int ACT, int N, bool KEEP>
+template <typename T, int ACT, bool ANY, bool KEEP>
 __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constant__ GatedArgs a) {
+  constexpr int N = Vec<T>::kN;
   allow_dependent_launch();
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const Walk k(a.n, a.c, 32 * N * kGatedUnits);
+  constexpr int kLanes = kOwn<ANY, KEEP>, kSpan = kLanes * N;
+  const Walk k(a.n, a.c, kSpan * kGatedUnits);
   for (long long u = k.first(); u < k.units; u += k.step()) {
-    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kGatedUnits + lane * N;
-    const T* gate = static_cast<const T*>(a.gate) + i * a.ld_gate;
-    const T* up = static_cast<const T*>(a.up) + i * a.ld_up;
-    Raw<T, N> g[kGatedUnits], v[kGatedUnits];
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * kSpan * kGatedUnits + lane * N;
+    RowVec<T, ANY> g[kGatedUnits], v[kGatedUnits];
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      if (c < a.c) {
-        g[q].load(gate + c);
-        v[q].load(up + c);
-      } else {
-        g[q].clear();
-        v[q].clear();
-      }
+      if (ANY && c0 - lane * N + kSpan * q >= a.c) break;
+      g[q].load(static_cast<const T*>(a.gate) + i * a.ld_gate, c0 + kSpan * q, a.c);
+      v[q].load(static_cast<const T*>(a.up) + i * a.ld_up, c0 + kSpan * q, a.c);
     }
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
+      const long long c = c0 + kSpan * q;
+      if (ANY && c - lane * N >= a.c) break;  // the whole warp is past the row
       if (KEEP) {
-        const long long code = i * a.ld_codes + c, scale = i * a.ld_scales + c / kScaleBlock;
-        g[q].encode(c < a.c, a.gate_codes + code, a.gate_scales + scale, lane);
-        v[q].encode(c < a.c, a.up_codes + code, a.up_scales + scale, lane);
+        encode_vec<T, ANY>(g[q], a.gate_codes + i * a.ld_codes, a.gate_scales + i * a.ld_scales, c, a.c, lane);
+        encode_vec<T, ANY>(v[q], a.up_codes + i * a.ld_codes, a.up_scales + i * a.ld_scales, c, a.c, lane);
       }
-      if (c < a.c) {
-        float x[N], h[N];
-        g[q].get(x);
-        v[q].get(h);
+      float x[N], h[N];
+      g[q].get(x);
+      v[q].get(h);
 #pragma unroll
-        for (int e = 0; e < N; ++e) h[e] *= act_of<ACT>(x[e]);
-        store_n<T, N>(static_cast<T*>(a.h) + i * a.ld_h + c, h);
-      }
+      for (int e = 0; e < N; ++e) h[e] *= act_of<ACT>(x[e]);
+      store_vec<ANY>(static_cast<T*>(a.h) + i * a.ld_h, c, a.c, h, lane, kLanes);
     }
   }
 }
 
-template <typename T, int ACT, int N, bool KEPT>
+template <typename T, int ACT, bool ANY, bool KEPT>
 __global__ void __launch_bounds__(32 * kWarps) gated_backward_kernel(const __grid_constant__ GatedArgs a) {
+  constexpr int N = Vec<T>::kN;
   allow_dependent_launch();
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const Walk k(a.n, a.c, 32 * N * kGatedUnits);
+  constexpr int kSpan = kOwn<ANY> * N;
+  const Walk k(a.n, a.c, kSpan * kGatedUnits);
   for (long long u = k.first(); u < k.units; u += k.step()) {
-    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * 32 * N * kGatedUnits + lane * N;
-    typename std::conditional<KEPT, Codes<N>, Raw<T, N>>::type g[kGatedUnits], v[kGatedUnits];
+    const long long i = u / k.chunks, c0 = (u - i * k.chunks) * kSpan * kGatedUnits + lane * N;
+    typename std::conditional<KEPT, Codes<N, ANY>, RowVec<T, ANY>>::type g[kGatedUnits], v[kGatedUnits];
     uint8_t gs[kGatedUnits], vs[kGatedUnits];
-    Raw<T, N> d[kGatedUnits];
+    RowVec<T, ANY> d[kGatedUnits];
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      if (c >= a.c) continue;
+      const long long c = c0 + kSpan * q;
+      if (ANY && c - lane * N >= a.c) break;  // the whole warp is past the row
       if constexpr (KEPT) {
-        const long long code = i * a.ld_codes + c, scale = i * a.ld_scales + c / kScaleBlock;
-        g[q].load(static_cast<const uint8_t*>(a.gate) + code);
-        v[q].load(static_cast<const uint8_t*>(a.up) + code);
-        gs[q] = __ldg(a.gate_scales + scale);
-        vs[q] = __ldg(a.up_scales + scale);
+        g[q].load(static_cast<const uint8_t*>(a.gate) + i * a.ld_codes, c, a.c);
+        v[q].load(static_cast<const uint8_t*>(a.up) + i * a.ld_codes, c, a.c);
+        const long long scale = i * a.ld_scales + c / kScaleBlock;
+        gs[q] = c < a.c ? __ldg(a.gate_scales + scale) : 0;
+        vs[q] = c < a.c ? __ldg(a.up_scales + scale) : 0;
       } else {
-        g[q].load(static_cast<const T*>(a.gate) + i * a.ld_gate + c);
-        v[q].load(static_cast<const T*>(a.up) + i * a.ld_up + c);
+        g[q].load(static_cast<const T*>(a.gate) + i * a.ld_gate, c, a.c);
+        v[q].load(static_cast<const T*>(a.up) + i * a.ld_up, c, a.c);
       }
-      d[q].load(static_cast<const T*>(a.dh) + i * a.ld_dh + c);
+      d[q].load(static_cast<const T*>(a.dh) + i * a.ld_dh, c, a.c);
     }
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
-      const long long c = c0 + 32 * N * q;
-      if (c >= a.c) continue;
+      const long long c = c0 + kSpan * q;
+      if (ANY && c - lane * N >= a.c) break;  // the whole warp is past the row
       float x[N], y[N], dh[N], o[N];
       if constexpr (KEPT) {
         g[q].get(scale_value(gs[q]), x);
@@ -244,14 +193,14 @@ __global__ void __launch_bounds__(32 * kWarps) gated_backward_kernel(const __gri
         x[e] = act_both<ACT>(x[e], &slope);
         o[e] = dh[e] * y[e] * slope;
       }
-      store_n<T, N>(static_cast<T*>(a.dgate) + i * a.ld_dgate + c, o);
+      store_vec<ANY>(static_cast<T*>(a.dgate) + i * a.ld_dgate, c, a.c, o, lane);
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = dh[e] * x[e];
-      store_n<T, N>(static_cast<T*>(a.dup) + i * a.ld_dup + c, o);
+      store_vec<ANY>(static_cast<T*>(a.dup) + i * a.ld_dup, c, a.c, o, lane);
       if (a.h != nullptr) {
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] = x[e] * y[e];
-        store_n<T, N>(static_cast<T*>(a.h) + i * a.ld_h + c, o);
+        store_vec<ANY>(static_cast<T*>(a.h) + i * a.ld_h, c, a.c, o, lane);
       }
     }
   }
@@ -280,17 +229,16 @@ template <typename T>
 int launch_checkpoint(const CheckArgs& a, bool vec, bool restore, cudaStream_t s) {
   constexpr int N = Vec<T>::kN;
   const dim3 block(32 * kWarps);
-  if (restore) {
-    if (vec && a.c % 16 == 0 && vector_rows(a.codes, a.ld_codes, a.n, 1, 16))
-      return launched(
-          launch_behind(restore_kernel<T, 16>, dim3(grid_of(a.n, a.c, 32 * 16 * 2)), block, 0, s, a));
-    const dim3 grid(grid_of(a.n, a.c, 32 * 4 * (vec ? N : 1)));
-    return launched(vec ? launch_behind(restore_kernel<T, N>, grid, block, 0, s, a)
-                        : launch_behind(restore_kernel<T, 1>, grid, block, 0, s, a));
-  }
-  const dim3 grid(grid_of(a.n, a.c, 32 * kCheckUnits * (vec ? N : 1)));
-  return launched(vec ? launch_behind(checkpoint_kernel<T, N>, grid, block, 0, s, a)
-                      : launch_behind(checkpoint_kernel<T, 1>, grid, block, 0, s, a));
+  if (restore && vec && a.c % 16 == 0 && vector_rows(a.codes, a.ld_codes, a.n, 1, 16))
+    return launched(
+        launch_behind(restore_kernel<T, 16, false>, dim3(grid_of(a.n, a.c, 32 * 16 * 2)), block, 0, s, a));
+  const int lanes = vec ? 32 : restore ? kOwn<true> : kOwn<true, true>;
+  const dim3 grid(grid_of(a.n, a.c, lanes * kCheckUnits * N));
+  if (restore)
+    return launched(vec ? launch_behind(restore_kernel<T, N, false>, grid, block, 0, s, a)
+                        : launch_behind(restore_kernel<T, N, true>, grid, block, 0, s, a));
+  return launched(vec ? launch_behind(checkpoint_kernel<T, false>, grid, block, 0, s, a)
+                      : launch_behind(checkpoint_kernel<T, true>, grid, block, 0, s, a));
 }
 
 int checkpoint(const moe_checkpoint_args* p, bool restore, moe_stream_t stream) {
@@ -322,16 +270,16 @@ int checkpoint(const moe_checkpoint_args* p, bool restore, moe_stream_t stream) 
 
 template <typename T, int ACT>
 int launch_gated(const GatedArgs& a, bool vec, bool kept, bool backward, cudaStream_t s) {
-  constexpr int N = Vec<T>::kN;
-  const dim3 grid(grid_of(a.n, a.c, 32 * kGatedUnits * (vec ? N : 1))), block(32 * kWarps);
+  const int lanes = vec ? 32 : kept && !backward ? kOwn<true, true> : kOwn<true>;
+  const dim3 grid(grid_of(a.n, a.c, lanes * kGatedUnits * Vec<T>::kN)), block(32 * kWarps);
   auto go = [&](auto* v, auto* e) {
     return launched(vec ? launch_behind(v, grid, block, 0, s, a) : launch_behind(e, grid, block, 0, s, a));
   };
   if (backward)
-    return kept ? go(gated_backward_kernel<T, ACT, N, true>, gated_backward_kernel<T, ACT, 1, true>)
-                : go(gated_backward_kernel<T, ACT, N, false>, gated_backward_kernel<T, ACT, 1, false>);
-  return kept ? go(gated_kernel<T, ACT, N, true>, gated_kernel<T, ACT, 1, true>)
-              : go(gated_kernel<T, ACT, N, false>, gated_kernel<T, ACT, 1, false>);
+    return kept ? go(gated_backward_kernel<T, ACT, false, true>, gated_backward_kernel<T, ACT, true, true>)
+                : go(gated_backward_kernel<T, ACT, false, false>, gated_backward_kernel<T, ACT, true, false>);
+  return kept ? go(gated_kernel<T, ACT, false, true>, gated_kernel<T, ACT, true, true>)
+              : go(gated_kernel<T, ACT, false, false>, gated_kernel<T, ACT, true, false>);
 }
 template <typename T>
 int launch_gated(int act, const GatedArgs& a, bool vec, bool kept, bool backward, cudaStream_t s) {

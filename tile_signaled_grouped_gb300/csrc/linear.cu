@@ -1087,10 +1087,13 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
         for (int r = 0; r < kActRows; ++r) {
           const long long i = min(i0 + r, hi - 1);
           du[r] = __ldg(reinterpret_cast<const uint4*>(dy + i * a.ld_dy));
-          if constexpr (EIGHT)
-            decode<8>(codes + i * a.ld_z, scale_value(__ldg(scales + i * a.ld_scales)), zf[r]);
-          else if (ACT != MOE_ACT_NONE)
+          if constexpr (EIGHT) {
+            Codes<8, false> u;
+            u.load(codes + i * a.ld_z, 0, 8);
+            u.get(scale_value(__ldg(scales + i * a.ld_scales)), zf[r]);
+          } else if (ACT != MOE_ACT_NONE) {
             zu[r] = __ldg(reinterpret_cast<const uint4*>(z + i * a.ld_z));
+          }
         }
 #pragma unroll
         for (int r = 0; r < kActRows; ++r) {
@@ -1130,10 +1133,8 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
         const long long i = min(i0 + r, hi - 1);
         d[r] = load_as_f32(a.dy, a.dtype, i * a.ld_dy + j);
         if constexpr (EIGHT) {
-          float v[1];
-          decode<1>(static_cast<const uint8_t*>(a.z) + i * a.ld_z + j,
-                    scale_value(__ldg(a.z_scales + i * a.ld_scales + j / kScaleBlock)), v);
-          z[r] = v[0];
+          z[r] = decode1(static_cast<const uint8_t*>(a.z) + i * a.ld_z + j,
+                         scale_value(__ldg(a.z_scales + i * a.ld_scales + j / kScaleBlock)));
         } else {
           z[r] = ACT != MOE_ACT_NONE ? load_as_f32(a.z, a.dtype, i * a.ld_z + j) : 0.f;
         }

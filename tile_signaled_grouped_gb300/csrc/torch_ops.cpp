@@ -665,34 +665,36 @@ Tensor expert_linear(const Tensor& x, const Tensor& weight, const Tensor& offset
   return y;
 }
 
-std::tuple<OptTensor, OptTensor> expert_linear_backward(const Tensor& dy, const Tensor& x, const Tensor& weight,
+// x: needed for dw alone.
+std::tuple<OptTensor, OptTensor> expert_linear_backward(const Tensor& dy, const OptTensor& rows, const Tensor& weight,
                                                         const Tensor& offsets, const OptTensor& add,
                                                         const py::object& dw_dtype, bool need_dx, bool need_dw) {
-  const int dt = checked_type(x, "x", true);
-  const Experts e = expert_weights(weight, x, offsets);
-  const Rows r = operand(x, "x", e.K, x);
-  same_shape(dy, with_last(x, e.N), x, "dy");
-  const Rows d = operand(dy, "dy", e.N, x);
+  const int dt = checked_type(dy, "dy", true);
+  const Experts e = expert_weights(weight, dy, offsets);
+  const Rows d = operand(dy, "dy", e.N, dy);
+  const auto shape = with_last(dy, e.K);
+  Rows r{d.n, e.K, 0};
+  if (rows.has_value()) {
+    same_shape(*rows, shape, dy, "x");
+    r = operand(*rows, "x", e.K, dy);
+  } else if (need_dw) {
+    refuse("x is needed for dweight");
+  }
+  const Tensor& x = dy;  // whose type and device all have
   Rows ra{};
   if (add.has_value()) {
     if (!need_dx) refuse("add is a part of dx, which is not asked for");
-    same_shape(*add, x.sizes(), x, "add");
+    same_shape(*add, shape, x, "add");
     ra = rows_of(*add, "add", e.K);
   }
   const at::ScalarType wt = x_or_fp32(dw_dtype, "dw_dtype", x, x.scalar_type());
   const Launch l(x);
   OptTensor dx, dw;
-  Tensor work;
-  size_t size = 0;
   moe_expert_linear_args a = expert_args(e, weight, offsets, dt, r.n);
-  if (need_dx) dx = empty(x.sizes(), x.scalar_type(), x);
-  if (need_dw) {
-    dw = empty(weight.sizes(), wt, x);
-    size = moe_expert_linear_workspace(a.E);
-    work = empty({(int64_t)size}, at::kByte, x);
-  }
+  if (need_dx) dx = empty(shape, x.scalar_type(), x);
+  if (need_dw) dw = empty(weight.sizes(), wt, x);
   a.dwtype = type_of(wt);
-  a.x = x.data_ptr();
+  a.x = ptr(rows);
   a.dy = dy.data_ptr();
   a.add = ptr(add);
   a.dx = ptr(dx);
@@ -702,8 +704,7 @@ std::tuple<OptTensor, OptTensor> expert_linear_backward(const Tensor& dy, const 
   a.ld_add = ra.ld;
   a.ld_dx = a.ld_dw = e.K;
   a.stride_dw = e.N * e.K;
-  call("moe_expert_linear_backward",
-       [&] { return moe_expert_linear_backward(&a, size > 0 ? work.data_ptr() : nullptr, size, l.stream); });
+  call("moe_expert_linear_backward", [&] { return moe_expert_linear_backward(&a, l.stream); });
   return {dx, dw};
 }
 

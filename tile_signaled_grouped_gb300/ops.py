@@ -259,11 +259,11 @@ def expert_linear(x, weight, offsets, stream=None):
 
 def expert_linear_backward(dy, x, weight, offsets, add=None, dw_dtype=None, need_dx=True, need_dw=True,
                            stream=None):
-    """(dx, dweight) of expert_linear from the gradient dy of y, for its x, weight and offsets. add [n, K] of
-    x's type is added to dx before it is rounded (the gradient through another product of the same x).
+    """(dx, dweight) of expert_linear from the gradient dy of y, for its x (None without need_dw), weight and
+    offsets. add [n, K] of x's type is added to dx before it is rounded (the gradient through another product of the same x).
     dweight has dw_dtype (x's type or fp32; default x's); it is zero for experts without rows."""
     if stream is not None:
-        with _on(x, stream):
+        with _on(dy, stream):
             return expert_linear_backward(dy, x, weight, offsets, add, dw_dtype, need_dx, need_dw)
     return (_native or native()).expert_linear_backward(dy, x, weight, offsets, add, dw_dtype, need_dx,
                                                         need_dw)
