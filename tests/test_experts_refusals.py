@@ -33,9 +33,9 @@ def test_sort_refuses():
     need = capi.lib().moe_sort_experts_workspace(100000, 4)
     assert need > 0 and f(64, 100000, 4, 64, 64, 64, 64, need - 1, None) == WORKSPACE
     size = capi.lib().moe_sort_experts_workspace
-    assert size(0, 4) == size(-1, 4) == size(10, 0) == size(10, 1025) == size(4096, 1024) == 0
+    assert size(0, 4) == size(-1, 4) == size(10, 0) == size(10, 1025) == size(2048, 1024) == 0
     # at most 148 chunks of counts, however many slots
-    assert max(size(n, 256) for n in (4097, 10 ** 6, 1 << 29)) <= 148 * 256 * 4
+    assert max(size(n, 256) for n in (2049, 10 ** 6, 1 << 29)) <= 148 * 256 * 4
 
 
 ROWS = dict(T=5, D=16, topk=2, E=4, dtype=capi.MOE_BF16, rows=64, offsets=64, w=64, x=64, y=64, r=64, dr=64, dw=64,

@@ -11,6 +11,7 @@
 // last are zeroed in shared memory.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "mma_common.cuh"
 
@@ -47,6 +48,13 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(cl_bar), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// An epilogue warp has read its part of an accumulator: its loads are complete (tcgen05.wait::ld) and nothing
+// else of it is the products' business, so the arrival orders no memory. (A release would wait for the warp's
+// stores to the outputs before it: 656 us where this takes XXX, dW of 128 experts of 64 rows, 2048 x 4096.)
+__device__ __forceinline__ void arrive_read(uint32_t cl_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 
 // An expert's rows: whatever the offsets hold, inside 0 .. n.
@@ -119,7 +127,7 @@ struct RowsArgs {
   uint32_t* status;
   int n, E, J, nk;     // J: features of y; nk: 64-element blocks of the sum
   int tiles_j, stages;
-  bool bf16, w_mn;     // w_mn: W^T, whose features are innermost
+  bool w_mn;           // W^T, whose features are innermost
 };
 constexpr int kBlocks = 2;  // of 64 k in a stage
 
@@ -199,10 +207,7 @@ struct RowWalk {
   __device__ __forceinline__ int steps() const { return e < a.E ? a.nk : 0; }
 };
 
-__device__ __forceinline__ uint16_t to_16bit(float v, bool bf16) {
-  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-}
-
+template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_rows_product_kernel(const __grid_constant__ RowsArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -211,6 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* patches = base + (size_t)a.stages * kBlocks * kBlockBytes;
   int* table_at = reinterpret_cast<int*>(patches + kPatchBytes);
   PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kPatchBytes + table_bytes(a.E));
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
@@ -270,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, at = 0;  // at: the stage's offset in 16-byte units
     bool ok = true;
     for (; ok && walk.next(); ++it) {
-      const uint32_t idesc = idesc_16bit(a.bf16, a.w_mn, false, kFeatures, walk.cols);
+      const uint32_t idesc = idesc_16bit(kBf16, a.w_mn, false, kFeatures, walk.cols);
       const int acc = it & 1, steps = walk.steps();
       if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, a.status, 0x44000000u)) break;
       tc_fence_after();
@@ -328,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (c + 2 >= chunks) {  // the accumulator is read: it may be overwritten
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+          if (lane == 0) arrive_read(tempty[acc]);
         }
         if (c < chunks && nf > 0) {
           const long long r0 = walk.row0 + c * 32;
@@ -340,17 +346,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 32; ++x) u[x] = lane < nf && x < rows ? __ldg(p + x * a.ld_add) : (uint16_t)0;
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-              const float f = a.bf16 ? __uint_as_float((uint32_t)u[x] << 16) : __half2float(__ushort_as_half(u[x]));
-              v[x] = __float_as_uint((zero ? 0.f : __uint_as_float(v[x])) + f);
+              v[x] = __float_as_uint((zero ? 0.f : __uint_as_float(v[x])) + unpack2<T>(u[x]).x);
             }
           } else if (zero) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = 0;
           }
           __syncwarp();  // the patch's last readers
+          // (Two roundings in one instruction: conversions are what an epilogue is slow at.)
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            *reinterpret_cast<uint16_t*>(patch + x * kPatchPitch + lane * 2) = to_16bit(__uint_as_float(v[x]), a.bf16);
+          for (int x = 0; x < 32; x += 2) {
+            const uint32_t w = pack2<T>(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+            uint8_t* to = patch + x * kPatchPitch + lane * 2;
+            *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
+            *reinterpret_cast<uint16_t*>(to + kPatchPitch) = (uint16_t)(w >> 16);
+          }
           __syncwarp();
           const int f = (lane & 3) * 8;
 #pragma unroll
@@ -376,11 +386,10 @@ struct WeightArgs {
   uint32_t* status;
   int n, E, N, K;
   int tiles_i, tiles_j, stages;
-  bool bf16, fp32;          // of the operands; of dw
-  bool wide;                // rows of dw start on 32 bytes
 };
 
-// The tiles of a pair: p, p + pairs, ... of the order expert, columns, rows of dW.
+// The tiles of a pair: p, p + pairs, ... of the order expert, rows, columns of dW: the tiles in flight
+// write whole rows.
 struct WeightWalk {
   const WeightArgs& a;
   int at, pairs;
@@ -393,21 +402,25 @@ struct WeightWalk {
     const int per = a.tiles_i * a.tiles_j;
     e = at / per;
     if (e >= a.E) return false;
-    const int local = at - e * per, tj = local / a.tiles_i;
-    i0 = (local - tj * a.tiles_i) * 256;
-    j0 = tj * 256;
+    const int local = at - e * per, ti = local / a.tiles_j;
+    i0 = ti * 256;
+    j0 = (local - ti * a.tiles_j) * 256;
     rows_of(a.offsets, e, a.E, a.n, &start, &count);
     steps = (count + kBlockK - 1) / kBlockK;
     return true;
   }
 };
 
+// T: the operands' type; O: dW's, T or float.
+template <typename T, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
     expert_weights_kernel(const __grid_constant__ WeightArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  PairSmem& sm = *reinterpret_cast<PairSmem*>(base + (size_t)a.stages * kBlockBytes);
+  uint8_t* patches = base + (size_t)a.stages * kBlockBytes;
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kPatchBytes);
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
@@ -453,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
     }
     wait_copies(sm, n, a.stages, a.status);
   } else if (warp == 1 && lead) {
-    const uint32_t idesc = idesc_16bit(a.bf16, true, true, 256, 256);
+    const uint32_t idesc = idesc_16bit(kBf16, true, true, 256, 256);
     const uint32_t s0 = (smem_u32(base) & 0x3FFFFu) >> 4;
     const uint64_t da = sdesc_mn_sw128(0) + s0, db = da + (kABytes >> 4);
     int it = 0, st = 0;
@@ -509,6 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
   } else if (warp >= 2) {
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the columns
     const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
+    uint8_t* patch = patches + (warp - 2) * 32 * kPatchPitch;
     for (int it = 0; walk.next(); ++it) {
       const int acc = it & 1;
       if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, a.status, 0x56000000u)) break;
@@ -524,44 +538,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
         if (c == half * 128 + 96) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+          if (lane == 0) arrive_read(tempty[acc]);
         }
         if (walk.steps == 0) {
 #pragma unroll
           for (int x = 0; x < 32; ++x) v[x] = 0;
         }
-        const int j = walk.j0 + c, nj = a.K - j;
-        if (i >= a.N || nj <= 0) continue;
-        const long long to = walk.e * a.stride + i * a.ld + j;
-        if (a.fp32) {
-          float* p = static_cast<float*>(a.dw) + to;
+        // Rows of 64 bytes, turned round in shared memory so that four lanes store a row's: such stores
+        // write 6.6 TB/s here, rows of one lane each 4.9 in 32 bytes and 2.6 in 16.
+        constexpr int kPart = 64 / (int)sizeof(O);  // columns of 64 bytes
+        const int rows = a.N - (walk.i0 + (int)crank * 128 + q * 32);
+        O* to = static_cast<O*>(a.dw) + walk.e * a.stride + (long long)(i - lane) * a.ld;  // the warp's first row
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (8 * x >= nj) break;
-            if (a.wide) {
-              st_global_v8(p + 8 * x, v + 8 * x);
-            } else {
-              reinterpret_cast<uint4*>(p)[2 * x] = make_uint4(v[8 * x], v[8 * x + 1], v[8 * x + 2], v[8 * x + 3]);
-              reinterpret_cast<uint4*>(p)[2 * x + 1] =
-                  make_uint4(v[8 * x + 4], v[8 * x + 5], v[8 * x + 6], v[8 * x + 7]);
-            }
-          }
-        } else {
+        for (int h = 0; h < 32; h += kPart) {
           uint32_t w[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const float lo = __uint_as_float(v[2 * x]), hi = __uint_as_float(v[2 * x + 1]);
-            w[x] = a.bf16 ? pack2<__nv_bfloat16>(lo, hi) : pack2<__half>(lo, hi);
+            if constexpr (sizeof(O) == 4)
+              w[x] = v[h + x];
+            else
+              w[x] = pack2<T>(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
           }
-          unsigned short* p = static_cast<unsigned short*>(a.dw) + to;
-          if (a.wide && nj >= 32) {
-            st_global_v8(p, w);
-            st_global_v8(p + 16, w + 8);
-          } else {
+          __syncwarp();  // the patch's last readers
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (8 * x < nj)
-                reinterpret_cast<uint4*>(p)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4*>(patch + lane * kPatchPitch + x * 16) =
+                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          __syncwarp();
+          const int j = walk.j0 + c + h + (lane & 3) * (kPart / 4);  // this lane's columns
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = (lane >> 2) + 8 * x;
+            const uint4 u = *reinterpret_cast<const uint4*>(patch + r * kPatchPitch + (lane & 3) * 16);
+            if (r < rows && j < a.K) *reinterpret_cast<uint4*>(to + r * a.ld + j) = u;
           }
         }
       }
@@ -618,11 +627,19 @@ int stages_for(size_t bytes, size_t more) {
   return std::min<int>(kMaxStages, (int)((kSmemMax - smem_bytes(0, more)) / bytes));
 }
 
+template <auto kKernel, typename A>
+int launch_pairs(unsigned pairs, int threads, size_t smem, cudaStream_t s, const A& a) {
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kKernel), &ready);
+  if (e == cudaSuccess) e = launch_behind(kKernel, dim3(2 * pairs), dim3((unsigned)threads), smem, s, a);
+  return launched(e);
+}
+
 // y of the forward pass, or dx: `w_mn` takes W^T.
 int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x, bool w_mn, const void* add,
                  long long ld_add, void* y, long long ld_y, int sms, cudaStream_t s) {
   RowsArgs a{};
-  a.bf16 = p->dtype == MOE_BF16;
+  const bool bf16 = p->dtype == MOE_BF16;
   a.w_mn = w_mn;
   a.n = (int)p->n;
   a.E = p->E;
@@ -636,22 +653,20 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   a.add = add;
   a.ld_add = ld_add;
   a.status = ops_status();
-  if (a.status == nullptr || !make_map(&a.tw, p->w, a.bf16, p->E, p->N, p->K, p->ld_w, p->stride_w, w_mn ? 64 : 128))
+  if (a.status == nullptr || !make_map(&a.tw, p->w, bf16, p->E, p->N, p->K, p->ld_w, p->stride_w, w_mn ? 64 : 128))
     return MOE_ERR_CUDA;
   for (int b = 0; b < 4; ++b)
-    if (!make_map(&a.tx[b], x, a.bf16, 0, p->n, sum, ld_x, 0, 16 << b)) return MOE_ERR_CUDA;
+    if (!make_map(&a.tx[b], x, bf16, 0, p->n, sum, ld_x, 0, 16 << b)) return MOE_ERR_CUDA;
   // Tiles of rows: one for every 256 and one more for each expert at most.
   const long long tiles = (p->n / kRows + std::min<long long>(p->E + 1, p->n)) * a.tiles_j;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t more = kPatchBytes + table_bytes(a.E);
   constexpr size_t kStage = kBlocks * kBlockBytes;
   a.stages = stages_for(kStage, more);
-  static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(expert_rows_product_kernel), &ready);
-  if (e == cudaSuccess)
-    e = launch_behind(expert_rows_product_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)),
-                      dim3(kThreads), smem_bytes(a.stages * kStage, more), s, a);
-  return launched(e);
+  const unsigned pairs = (unsigned)std::min<long long>(sms / 2, tiles);
+  const size_t smem = smem_bytes(a.stages * kStage, more);
+  return bf16 ? launch_pairs<expert_rows_product_kernel<__nv_bfloat16>>(pairs, kThreads, smem, s, a)
+              : launch_pairs<expert_rows_product_kernel<__half>>(pairs, kThreads, smem, s, a);
 }
 
 int weights_product(const moe_expert_linear_args* p, int sms, cudaStream_t s) {
@@ -672,19 +687,16 @@ int weights_product(const moe_expert_linear_args* p, int sms, cudaStream_t s) {
   a.K = (int)p->K;
   a.tiles_i = (a.N + 255) / 256;
   a.tiles_j = (a.K + 255) / 256;
-  a.bf16 = bf16;
-  a.fp32 = p->dwtype == MOE_FP32;
-  const int per = a.fp32 ? 8 : 16;  // elements of 32 bytes
-  a.wide = aligned_to(p->dw, 32) && a.ld % per == 0 && a.stride % per == 0;
   const long long tiles = (long long)a.tiles_i * a.tiles_j * a.E;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
-  a.stages = stages_for(kBlockBytes, 0);
-  static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(expert_weights_kernel), &ready);
-  if (e == cudaSuccess)
-    e = launch_behind(expert_weights_kernel, dim3(2 * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(kThreads + 32),
-                      smem_bytes((size_t)a.stages * kBlockBytes, 0), s, a);
-  return launched(e);
+  a.stages = stages_for(kBlockBytes, kPatchBytes);
+  const unsigned pairs = (unsigned)std::min<long long>(sms / 2, tiles);
+  const size_t smem = smem_bytes((size_t)a.stages * kBlockBytes, kPatchBytes);
+  if (p->dwtype == MOE_FP32)
+    return bf16 ? launch_pairs<expert_weights_kernel<__nv_bfloat16, float>>(pairs, kThreads + 32, smem, s, a)
+                : launch_pairs<expert_weights_kernel<__half, float>>(pairs, kThreads + 32, smem, s, a);
+  return bf16 ? launch_pairs<expert_weights_kernel<__nv_bfloat16, __nv_bfloat16>>(pairs, kThreads + 32, smem, s, a)
+              : launch_pairs<expert_weights_kernel<__half, __half>>(pairs, kThreads + 32, smem, s, a);
 }
 
 }  // namespace

@@ -24,11 +24,11 @@ namespace {
 // counts its chunk's experts by warp, and after a scan over the experts, the chunks before and its
 // warps, every warp walks its range in order and hands out rows: a slot's row is its warp's next one
 // of its expert and the lanes before it with the same expert. Integer sums, so the order of
-// the counting does not matter, and the result is the stable order always. One chunk (up to 4096
+// the counting does not matter, and the result is the stable order always. One chunk (up to 2048
 // slots) is one launch; otherwise a first launch leaves the chunks' counts.
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortSlots = 8;      // slots of a lane at least
+constexpr int kSortSlots = 4;      // slots of a lane at least, and read at a time
 constexpr int kSortChunks = 148;   // a chunk is a CTA's work, and all of them are read by each
 constexpr int kSortMaxExperts = 1024;
 
@@ -54,9 +54,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
   wait_prior_grid();
   const long long lo = (long long)blockIdx.x * kSortThreads * a.per;
   const long long end = min((long long)a.n, lo + (long long)kSortThreads * a.per);
-  for (long long i = lo + threadIdx.x; i < end; i += kSortThreads) {
-    const int e = expert_at(a, i, end);
-    if (e < a.E) atomicAdd(&count[e], 1);
+  for (long long i = lo + threadIdx.x; i < end; i += kSortThreads * kSortSlots) {
+    int e[kSortSlots];
+#pragma unroll
+    for (int u = 0; u < kSortSlots; ++u) e[u] = expert_at(a, i + u * kSortThreads, end);
+#pragma unroll
+    for (int u = 0; u < kSortSlots; ++u)
+      if (e[u] < a.E) atomicAdd(&count[e[u]], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) a.counts[(size_t)blockIdx.x * a.E + e] = count[e];
@@ -73,9 +77,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   const long long lo = ((long long)blockIdx.x * kSortWarps + warp) * 32 * a.per;
   const long long end = min((long long)a.n, lo + 32LL * a.per);
   int* mine = next + warp * a.E;
-  for (long long i = lo + lane; i < end; i += 32) {
-    const int e = expert_at(a, i, end);
-    if (e < a.E) atomicAdd(&mine[e], 1);
+  for (long long i = lo + lane; i < end; i += 32 * kSortSlots) {
+    int e[kSortSlots];
+#pragma unroll
+    for (int u = 0; u < kSortSlots; ++u) e[u] = expert_at(a, i + u * 32, end);
+#pragma unroll
+    for (int u = 0; u < kSortSlots; ++u)
+      if (e[u] < a.E) atomicAdd(&mine[e[u]], 1);
   }
   __syncthreads();
   // Two neighbouring experts a thread: their rows of all chunks, and of the chunks before this one.
@@ -112,17 +120,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = total;
   __syncthreads();
-  for (long long i0 = lo; i0 < end; i0 += 32) {  // whole warps
-    const long long i = i0 + lane;
-    const int e = expert_at(a, i, end);
-    const uint32_t same = __match_any_sync(kAll, e);
-    int row = -1;
-    if (e < a.E) row = mine[e] + __popc(same & ((1u << lane) - 1));
-    __syncwarp();
-    if (e < a.E && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-    if (i < end) a.rows[i] = row;
-    if (row >= 0) a.slots[row] = (int)i;
+  for (long long i0 = lo; i0 < end; i0 += 32 * kSortSlots) {  // whole warps
+    int e[kSortSlots];
+#pragma unroll
+    for (int u = 0; u < kSortSlots; ++u) e[u] = expert_at(a, i0 + u * 32 + lane, end);
+#pragma unroll
+    for (int u = 0; u < kSortSlots; ++u) {
+      const long long i = i0 + u * 32 + lane;
+      if (i - lane >= end) break;
+      const uint32_t same = __match_any_sync(kAll, e[u]);
+      int row = -1;
+      if (e[u] < a.E) row = mine[e[u]] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (e[u] < a.E && lane == __ffs(same) - 1) mine[e[u]] += __popc(same);
+      __syncwarp();
+      if (i < end) a.rows[i] = row;
+      if (row >= 0) a.slots[row] = (int)i;
+    }
   }
   const long long all_threads = (long long)gridDim.x * kSortThreads;
   for (long long r = total + (long long)blockIdx.x * kSortThreads + threadIdx.x; r < a.n; r += all_threads)
@@ -235,7 +249,6 @@ __global__ void __launch_bounds__(32 * kRowWarps) combine_kernel(const __grid_co
     }
 #pragma unroll
     for (int i = 0; i < kSumUnits; ++i) {
-      if (ANY && c - lane * N + kLanes * i >= a.D) break;  // the whole warp is past the row
       store_vec<ANY>(static_cast<T*>(a.y) + t * a.ld_x, c + kLanes * i, a.D, sum[i], lane);
     }
   }

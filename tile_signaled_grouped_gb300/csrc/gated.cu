@@ -58,7 +58,6 @@ __global__ void __launch_bounds__(32 * kWarps) checkpoint_kernel(const __grid_co
       v[q].load(static_cast<const T*>(a.x) + i * a.ld_x, c0 + kSpan * q, a.c);
 #pragma unroll
     for (int q = 0; q < kCheckUnits; ++q) {
-      if (ANY && c0 - lane * N + kSpan * q >= a.c) break;  // the whole warp is past the row
       encode_vec<T, ANY>(v[q], a.codes + i * a.ld_codes, a.scales + i * a.ld_scales, c0 + kSpan * q, a.c, lane);
     }
   }
@@ -86,7 +85,6 @@ __global__ void __launch_bounds__(32 * kWarps) restore_kernel(const __grid_const
     }
 #pragma unroll
     for (int q = 0; q < kUnits; ++q) {
-      if (ANY && c0 - lane * N + kSpan * q >= a.c) break;  // the whole warp is past the row
       float f[N];
       v[q].get(scale_value(s[q]), f);
 #pragma unroll
@@ -123,14 +121,12 @@ __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constan
     RowVec<T, ANY> g[kGatedUnits], v[kGatedUnits];
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
-      if (ANY && c0 - lane * N + kSpan * q >= a.c) break;
       g[q].load(static_cast<const T*>(a.gate) + i * a.ld_gate, c0 + kSpan * q, a.c);
       v[q].load(static_cast<const T*>(a.up) + i * a.ld_up, c0 + kSpan * q, a.c);
     }
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
       const long long c = c0 + kSpan * q;
-      if (ANY && c - lane * N >= a.c) break;  // the whole warp is past the row
       if (KEEP) {
         encode_vec<T, ANY>(g[q], a.gate_codes + i * a.ld_codes, a.gate_scales + i * a.ld_scales, c, a.c, lane);
         encode_vec<T, ANY>(v[q], a.up_codes + i * a.ld_codes, a.up_scales + i * a.ld_scales, c, a.c, lane);
@@ -161,7 +157,6 @@ __global__ void __launch_bounds__(32 * kWarps) gated_backward_kernel(const __gri
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
       const long long c = c0 + kSpan * q;
-      if (ANY && c - lane * N >= a.c) break;  // the whole warp is past the row
       if constexpr (KEPT) {
         g[q].load(static_cast<const uint8_t*>(a.gate) + i * a.ld_codes, c, a.c);
         v[q].load(static_cast<const uint8_t*>(a.up) + i * a.ld_codes, c, a.c);
@@ -177,7 +172,6 @@ __global__ void __launch_bounds__(32 * kWarps) gated_backward_kernel(const __gri
 #pragma unroll
     for (int q = 0; q < kGatedUnits; ++q) {
       const long long c = c0 + kSpan * q;
-      if (ANY && c - lane * N >= a.c) break;  // the whole warp is past the row
       float x[N], y[N], dh[N], o[N];
       if constexpr (KEPT) {
         g[q].get(scale_value(gs[q]), x);
