@@ -28,8 +28,9 @@ constexpr int kRowStep = 32;                    // columns of a product come in 
 constexpr int kGroup = 8;                       // tiles of rows that walk the features together
 constexpr int kABytes = 128 * 128;              // a CTA's features of a block of 64 k
 constexpr int kBlockBytes = kABytes + 128 * 128;  // and half of the pair's rows
-constexpr int kPatchPitch = 80;                 // bytes of a row of 32 features, on 16 bytes
-constexpr int kPatchBytes = kEpiWarps * 32 * kPatchPitch;
+constexpr int kPatchBytes = 32 * 64;            // of an epilogue warp: 32 rows of 64 bytes
+constexpr int kWeightEpiWarps = 16;             // dW: its epilogues have most to write
+constexpr int kWeightThreads = 32 * (3 + kWeightEpiWarps);
 
 struct PairSmem {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -50,9 +51,13 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Piece `k` (16 bytes) of row r of a patch: eight lanes that take one piece of eight rows each, or four of
+// two, meet no bank twice.
+__device__ __forceinline__ int patch_at(int r, int k) { return r * 64 + ((k ^ (r >> 1)) & 3) * 16; }
+
 // An epilogue warp has read its part of an accumulator: its loads are complete (tcgen05.wait::ld) and nothing
 // else of it is the products' business, so the arrival orders no memory. (A release would wait for the warp's
-// stores to the outputs before it: 656 us where this takes XXX, dW of 128 experts of 64 rows, 2048 x 4096.)
+// stores to the outputs before it: 656 us where this takes 513, dW of 128 experts of 64 rows, 2048 x 4096.)
 __device__ __forceinline__ void arrive_read(uint32_t cl_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
@@ -66,8 +71,8 @@ __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int E, in
 }
 
 // The barriers and the tensor memory of a pair; both CTAs have them when it returns.
-// `full`: arrivals that fill a stage.
-__device__ __forceinline__ void pair_setup(PairSmem& sm, int stages, int warp, int full) {
+// `full`: arrivals that fill a stage; `epi`: epilogue warps of a CTA.
+__device__ __forceinline__ void pair_setup(PairSmem& sm, int stages, int warp, int full, int epi) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&sm.full[i], full);  // rank 0: its arrive.expect_tx (bytes of both CTAs) is one
@@ -76,7 +81,7 @@ __device__ __forceinline__ void pair_setup(PairSmem& sm, int stages, int warp, i
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.tfull[i], 1);              // the leader's commit (multicast)
-      mbar_init(&sm.tempty[i], 2 * kEpiWarps); // rank 0: both CTAs' epilogue warps
+      mbar_init(&sm.tempty[i], 2 * epi);       // rank 0: both CTAs' epilogue warps
     }
     mbar_init(&sm.drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -214,13 +219,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* patches = base + (size_t)a.stages * kBlocks * kBlockBytes;
-  int* table_at = reinterpret_cast<int*>(patches + kPatchBytes);
-  PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kPatchBytes + table_bytes(a.E));
+  int* table_at = reinterpret_cast<int*>(patches + kEpiWarps * kPatchBytes);
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kEpiWarps * kPatchBytes + table_bytes(a.E));
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
-  pair_setup(sm, a.stages, warp, 1);
+  pair_setup(sm, a.stages, warp, 1, kEpiWarps);
   const uint32_t tmem = sm.tmem;
   wait_prior_grid();
   const Table table = make_table(a, table_at, sm.scratch);
@@ -312,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // round in shared memory, four lanes store the 32 features of a row.
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
-    uint8_t* patch = patches + (warp - 2) * 32 * kPatchPitch;
+    uint8_t* patch = patches + (warp - 2) * kPatchBytes;
     unsigned short* y = static_cast<unsigned short*>(a.y);
     const unsigned short* add = static_cast<const unsigned short*>(a.add);
     for (int it = 0; walk.next(); ++it) {
@@ -357,16 +362,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
             const uint32_t w = pack2<T>(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-            uint8_t* to = patch + x * kPatchPitch + lane * 2;
+            uint8_t* to = patch + patch_at(x, lane >> 3) + (lane & 7) * 2;  // and the same of row x + 1
             *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
-            *reinterpret_cast<uint16_t*>(to + kPatchPitch) = (uint16_t)(w >> 16);
+            *reinterpret_cast<uint16_t*>(to + 64) = (uint16_t)(w >> 16);
           }
           __syncwarp();
           const int f = (lane & 3) * 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = (lane >> 2) + 8 * i;
-            const uint4 u = *reinterpret_cast<const uint4*>(patch + x * kPatchPitch + f * 2);
+            const uint4 u = *reinterpret_cast<const uint4*>(patch + patch_at(x, lane & 3));
             if (x < rows && f < nf) *reinterpret_cast<uint4*>(y + (r0 + x) * a.ld_y + f0 + f) = u;
           }
         }
@@ -413,18 +418,18 @@ struct WeightWalk {
 
 // T: the operands' type; O: dW's, T or float.
 template <typename T, typename O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
     expert_weights_kernel(const __grid_constant__ WeightArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* patches = base + (size_t)a.stages * kBlockBytes;
-  PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kPatchBytes);
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(patches + kWeightEpiWarps * kPatchBytes);
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool lead = crank == 0;
-  pair_setup(sm, a.stages, warp, 2);
+  pair_setup(sm, a.stages, warp, 2, kWeightEpiWarps);
   const uint32_t tmem = sm.tmem;
   wait_prior_grid();
   WeightWalk walk(a, blockIdx.x >> 1, gridDim.x >> 1);
@@ -497,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
       __syncwarp();
     }
     wait_products(sm, a.status);
-  } else if (warp == 2 + kEpiWarps) {
+  } else if (warp == 2 + kWeightEpiWarps) {
     // Clears the rows past the expert's last in this CTA's half of its last block: they are another
     // expert's (or what lies behind the rows), and a NaN there times zero would be one. A block is
     // 64 rows of 128 bytes for each 64 columns; the swizzle stays inside a row.
@@ -520,9 +525,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
       if (lane == 0) mbar_arrive_cluster(map_shared(&sm.full[st], 0));
     }
   } else if (warp >= 2) {
-    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the columns
+    constexpr int kColumns = 256 * 4 / kWeightEpiWarps;
+    const int q = warp & 3, from = ((warp - 2) >> 2) * kColumns;  // TMEM lane quarter, first column
     const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
-    uint8_t* patch = patches + (warp - 2) * 32 * kPatchPitch;
+    uint8_t* patch = patches + (warp - 2) * kPatchBytes;
     for (int it = 0; walk.next(); ++it) {
       const int acc = it & 1;
       if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, a.status, 0x56000000u)) break;
@@ -530,12 +536,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
       const int i = walk.i0 + (int)crank * 128 + q * 32 + lane;
       const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
 #pragma unroll 1
-      for (int c = half * 128; c < half * 128 + 128; c += 32) {
+      for (int c = from; c < from + kColumns; c += 32) {
         uint32_t v[32];
         __syncwarp();
         tmem_ld32(src + c, v);
         tmem_ld_wait();
-        if (c == half * 128 + 96) {
+        if (c + 32 == from + kColumns) {  // the accumulator is read: it may be overwritten
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_read(tempty[acc]);
@@ -562,14 +568,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 32, 1)
           __syncwarp();  // the patch's last readers
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4*>(patch + lane * kPatchPitch + x * 16) =
+            *reinterpret_cast<uint4*>(patch + patch_at(lane, x)) =
                 make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
           __syncwarp();
           const int j = walk.j0 + c + h + (lane & 3) * (kPart / 4);  // this lane's columns
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int r = (lane >> 2) + 8 * x;
-            const uint4 u = *reinterpret_cast<const uint4*>(patch + r * kPatchPitch + (lane & 3) * 16);
+            const uint4 u = *reinterpret_cast<const uint4*>(patch + patch_at(r, lane & 3));
             if (r < rows && j < a.K) *reinterpret_cast<uint4*>(to + r * a.ld + j) = u;
           }
         }
@@ -660,7 +666,7 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   // Tiles of rows: one for every 256 and one more for each expert at most.
   const long long tiles = (p->n / kRows + std::min<long long>(p->E + 1, p->n)) * a.tiles_j;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
-  const size_t more = kPatchBytes + table_bytes(a.E);
+  const size_t more = kEpiWarps * kPatchBytes + table_bytes(a.E);
   constexpr size_t kStage = kBlocks * kBlockBytes;
   a.stages = stages_for(kStage, more);
   const unsigned pairs = (unsigned)std::min<long long>(sms / 2, tiles);
@@ -689,14 +695,15 @@ int weights_product(const moe_expert_linear_args* p, int sms, cudaStream_t s) {
   a.tiles_j = (a.K + 255) / 256;
   const long long tiles = (long long)a.tiles_i * a.tiles_j * a.E;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
-  a.stages = stages_for(kBlockBytes, kPatchBytes);
+  constexpr size_t kMore = kWeightEpiWarps * kPatchBytes;
+  a.stages = stages_for(kBlockBytes, kMore);
   const unsigned pairs = (unsigned)std::min<long long>(sms / 2, tiles);
-  const size_t smem = smem_bytes((size_t)a.stages * kBlockBytes, kPatchBytes);
+  const size_t smem = smem_bytes((size_t)a.stages * kBlockBytes, kMore);
   if (p->dwtype == MOE_FP32)
-    return bf16 ? launch_pairs<expert_weights_kernel<__nv_bfloat16, float>>(pairs, kThreads + 32, smem, s, a)
-                : launch_pairs<expert_weights_kernel<__half, float>>(pairs, kThreads + 32, smem, s, a);
-  return bf16 ? launch_pairs<expert_weights_kernel<__nv_bfloat16, __nv_bfloat16>>(pairs, kThreads + 32, smem, s, a)
-              : launch_pairs<expert_weights_kernel<__half, __half>>(pairs, kThreads + 32, smem, s, a);
+    return bf16 ? launch_pairs<expert_weights_kernel<__nv_bfloat16, float>>(pairs, kWeightThreads, smem, s, a)
+                : launch_pairs<expert_weights_kernel<__half, float>>(pairs, kWeightThreads, smem, s, a);
+  return bf16 ? launch_pairs<expert_weights_kernel<__nv_bfloat16, __nv_bfloat16>>(pairs, kWeightThreads, smem, s, a)
+              : launch_pairs<expert_weights_kernel<__half, __half>>(pairs, kWeightThreads, smem, s, a);
 }
 
 }  // namespace
