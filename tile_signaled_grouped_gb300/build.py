@@ -137,7 +137,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     tmp = BINDING + ".tmp"
     _run([_cxx(), "-shared", "-o", tmp, binding.result(), "-L" + PKG,
           "-l:libmoe_tsg.so", "-L" + os.path.join(_torch(), "lib"), "-lc10", "-lc10_cuda",
-          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "the torch binding's link")
+          "-ltorch_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "the torch binding's link")
     os.replace(tmp, BINDING)
     with open(os.path.join(BUILD, "torch_ops.for"), "w") as f:
         f.write(_built_for())

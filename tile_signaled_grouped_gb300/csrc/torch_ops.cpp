@@ -3,6 +3,7 @@
 // documents. No computation here. In C++ because the host's part is what a small call costs:
 // with the same checks in Python over ctypes it was 14 us (routing, linear), 19 (layer norm)
 // and 24 to 32 (backward passes) on a Grace host, here 5 to 10, 6 to 12 and 11 to 18 by the machine.
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -130,8 +131,10 @@ Rows operand(const Tensor& t, const char* what, int64_t cols, const Tensor& x) {
 // A size in an int's field; what it cannot hold is beyond every limit of such a field.
 int as_int(int64_t v) { return (int)std::min<int64_t>(v, INT32_MAX); }
 void* ptr(const OptTensor& t) { return t.has_value() ? t->data_ptr() : nullptr; }
+// A tensor beside x (which is on a CUDA device), without the dispatcher: each is a good part of a
+// small call's time.
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& x) {
-  return at::empty(shape, x.options().dtype(type));
+  return Tensor(at::detail::empty_cuda(shape, type, x.device(), std::nullopt));
 }
 std::vector<int64_t> with_last(const Tensor& t, int64_t last) {
   std::vector<int64_t> s(t.sizes().begin(), t.sizes().end());
