@@ -481,6 +481,8 @@ typedef struct moe_linear_args {
   long long ld_x, ld_w, ld_r, ld_y, ld_z, ld_dy, ld_dx, ld_dw;
   const uint8_t *z_scales; /* backward: in [M][ceil(N / 32)] where z are the codes of an 8-bit
                               checkpoint (moe_checkpoint), else NULL */
+  const uint8_t *x_scales; /* backward: in [M][ceil(K / 32)] where x are such codes, rows of K bytes
+                              (K a multiple of 8, 8-byte aligned), else NULL */
 } moe_linear_args;
 
 /* z = x w^T + b, y = act(z) + r: fp32 sums, y and z rounded once from fp32. */
@@ -489,8 +491,10 @@ int moe_linear(const moe_linear_args *args, moe_stream_t stream);
 /* dz = dy * act'(z); db = sum over rows of dz; dx = dz w; dw = dz^T x. The products take
  * dz rounded to dtype, db takes it in fp32; all sums are fp32, in a fixed order.
  * workspace: at least moe_linear_workspace(M, N) bytes (pure host arithmetic), 256-byte
- * aligned, used until the call has run on the stream. */
+ * aligned, used until the call has run on the stream; where dw is made from a checkpoint of x, and
+ * moe_linear_kept_bytes(M, K) more, for x in dtype. */
 size_t moe_linear_workspace(long long M, long long N);
+size_t moe_linear_kept_bytes(long long M, long long K);
 int moe_linear_backward(const moe_linear_args *args, void *workspace, size_t workspace_bytes,
                         moe_stream_t stream);
 

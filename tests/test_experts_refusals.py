@@ -109,6 +109,20 @@ def test_expert_products_refuse():
     assert lib.moe_expert_linear_backward(args(capi.moe_expert_linear_args, **{**ok, "n": 0, "dw": None}), None) == 0
 
 
+def test_linear_refuses_checkpoints():
+    lib = capi.lib()
+    ok = dict(M=5, N=16, K=24, dtype=capi.MOE_BF16, ytype=capi.MOE_BF16, btype=capi.MOE_BF16, dwtype=capi.MOE_BF16,
+              act=capi.MOE_ACT_SILU, x=64, w=64, z=64, dy=64, dx=64, dw=64, db=64, ld_x=24, ld_w=24, ld_z=16, ld_dy=16,
+              ld_dx=24, ld_dw=24, z_scales=64, x_scales=64)
+    size = lib.moe_linear_workspace(5, 16) + lib.moe_linear_kept_bytes(5, 24)
+    f = lambda n, **bad: lib.moe_linear_backward(  # noqa: E731
+        args(capi.moe_linear_args, **{**ok, **bad}), 256, n, None)
+    for bad in (dict(z=None), dict(ld_z=15), dict(act=capi.MOE_ACT_NONE), dict(x=None), dict(x=68), dict(K=20)):
+        assert f(size, **bad) == ARG, bad
+    assert f(size - 1) == WORKSPACE
+    assert lib.moe_linear_kept_bytes(5, 24) == 5 * 24 * 2 and lib.moe_linear_kept_bytes(0, 24) == 0
+
+
 def bf(*shape):
     return torch.zeros(*shape, dtype=torch.bfloat16)
 
@@ -187,7 +201,10 @@ def test_tensors_are_refused():
     refuses("both", ops.gated_backward, bf(8, 40), kept, bf(8, 40))
     refuses("must be", ops.gated_backward, bf(7, 40), kept, kept)
 
-    refuses("CUDA", ops.linear_backward, dy, kept, bf(16, 40), need_dw=False)
+    refuses("CUDA", ops.linear_backward, bf(8, 16), kept, bf(16, 40), need_dw=False)
+    refuses("dy must", ops.linear_backward, dy, kept, bf(16, 40))
+    odd = ops.Checkpoint(torch.zeros(8, 12).to(torch.float8_e4m3fn), torch.zeros(8, 1, dtype=torch.uint8))
+    refuses("multiple of 8", ops.linear_backward, bf(8, 16), odd, bf(16, 16)[:, :12])
     refuses("z must", ops.linear_backward, dy, x, bf(16, 24), z=kept, act="silu")
     refuses("z is needed", ops.linear_backward, dy, x, bf(16, 24), z=kept)
     refuses("keep", Experts, weight, weight, bf(3, 24, 16), keep="4 bits")

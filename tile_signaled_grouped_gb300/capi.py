@@ -67,7 +67,7 @@ class moe_linear_args(ctypes.Structure):
         + [(f, ctypes.c_void_p) for f in ("x", "w", "b", "r", "y", "z", "dy", "dx", "dw", "db")]
         + [(f, ctypes.c_longlong) for f in ("ld_x", "ld_w", "ld_r", "ld_y", "ld_z", "ld_dy",
                                             "ld_dx", "ld_dw")]
-        + [("z_scales", ctypes.c_void_p)])
+        + [("z_scales", ctypes.c_void_p), ("x_scales", ctypes.c_void_p)])
 
 
 class moe_rows_args(ctypes.Structure):
@@ -162,6 +162,7 @@ def load():
         "moe_router": (ip, [vp, P(moe_router_cfg), vp, ip, ll, ll, vp, vp, vp, vp]),
         "moe_linear": (ip, [P(moe_linear_args), vp]),
         "moe_linear_workspace": (sz, [ll, ll]),
+        "moe_linear_kept_bytes": (sz, [ll, ll]),
         "moe_linear_backward": (ip, [P(moe_linear_args), vp, sz, vp]),
         "moe_sort_experts_workspace": (sz, [ll, ip]),
         "moe_sort_experts": (ip, [vp, ll, ip, vp, vp, vp, vp, sz, vp]),

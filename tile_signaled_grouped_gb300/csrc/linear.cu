@@ -1042,8 +1042,15 @@ struct ActGradArgs {
   const uint8_t* z_scales;
   void* dz;       // null: only the sums
   float* part;    // [gridDim.y][N] column sums, or null
+  void* db;       // with one range of rows: the sums go here, of btype, or null
+  // x restored from its checkpoint by the CTAs behind the ranges, in units of eight elements; or 0 units.
+  const uint8_t *x_codes, *x_scales;
+  void* x;
+  long long units;
   long long ld_dy, ld_z, ld_dz, ld_scales;
+  int K;
   int M, N, dtype, rows;  // rows of a CTA
+  int btype, ranges;
 };
 
 // Eight elements of 16 bits as fp32.
@@ -1062,11 +1069,46 @@ __device__ __forceinline__ void unpack8(const uint4& u, int dtype, float (&f)[8]
 // (3.5 TB/s; cold, under a profiler). Otherwise a thread takes one column, so that neighbouring
 // threads read neighbouring elements. EIGHT: z was kept in 8 bits.
 constexpr int kActRows = 4;
+constexpr int kRestoreUnits = 4;  // of a thread
+
+// Eight elements a unit of x from its codes; the rows of x are K elements, of whole units. CTA `block` of
+// `blocks`.
+__device__ __forceinline__ void restore_units(const ActGradArgs& a, long long block, long long blocks) {
+  const int per = a.K / 8;
+  const long long scales = (a.K + kScaleBlock - 1) / kScaleBlock;
+  for (long long first = block * (256 * kRestoreUnits) + threadIdx.x; first < a.units;
+       first += blocks * (256 * kRestoreUnits)) {
+    Codes<8, false> codes[kRestoreUnits];
+    uint8_t scale[kRestoreUnits];
+#pragma unroll
+    for (int i = 0; i < kRestoreUnits; ++i) {
+      const long long u = first + i * 256;
+      if (u >= a.units) continue;
+      const long long row = a.units <= INT32_MAX ? (int)u / per : u / per;
+      codes[i].v = load_words<8>(a.x_codes + u * 8);
+      scale[i] = __ldg(a.x_scales + row * scales + (u - row * per) * 8 / kScaleBlock);
+    }
+#pragma unroll
+    for (int i = 0; i < kRestoreUnits; ++i) {
+      const long long u = first + i * 256;
+      if (u >= a.units) continue;
+      float f[8];
+      codes[i].get(scale_value(scale[i]), f);
+      store8(a.x, a.dtype, u * 8, 8, true, f);
+    }
+  }
+}
+
 template <int ACT, bool VEC, bool EIGHT>
 __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
   __shared__ float red[VEC ? 8 : 1][32][9];
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int)blockIdx.y >= a.ranges) {
+    restore_units(a, (long long)(blockIdx.y - a.ranges) * gridDim.x + blockIdx.x,
+                  (long long)(gridDim.y - a.ranges) * gridDim.x);
+    return;
+  }
   const int lo = blockIdx.y * a.rows, hi = min(a.M, lo + a.rows);
   const int c = blockIdx.x * 256 + threadIdx.x;  // the column whose sum this thread writes
   float sum = 0.f;
@@ -1118,7 +1160,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
         }
       }
     }
-    if (a.part == nullptr) return;
+    if (a.part == nullptr && a.db == nullptr) return;
 #pragma unroll
     for (int q = 0; q < 8; ++q) red[warp][lane][q] = s[q];
     __syncthreads();
@@ -1148,9 +1190,13 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
         }
       }
     }
-    if (a.part == nullptr) return;
+    if (a.part == nullptr && a.db == nullptr) return;
   }
-  if (c < a.N) a.part[(size_t)blockIdx.y * a.N + c] = sum;
+  if (c >= a.N) return;
+  if (a.db != nullptr)
+    store_from_f32(a.db, a.btype, c, sum + 0.f);  // 0 for -0, as a sum over ranges has it
+  else
+    a.part[(size_t)blockIdx.y * a.N + c] = sum;
 }
 
 // db from the row ranges' sums: sixteen warps share the ranges, then their sums in order.
@@ -1586,8 +1632,10 @@ int moe_linear(const moe_linear_args* p, moe_stream_t stream) {
 
 size_t moe_linear_workspace(long long M, long long N) {
   if (M < 1 || N < 1) return 0;
-  return dz_bytes(M, N) + (size_t)kBiasParts * N * sizeof(float);
+  return dz_bytes(M, N) + ((size_t)kBiasParts * N * sizeof(float) + 255) / 256 * 256;
 }
+
+size_t moe_linear_kept_bytes(long long M, long long K) { return M < 1 || K < 1 ? 0 : (size_t)M * K * 2; }
 
 int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t workspace_bytes,
                         moe_stream_t stream) {
@@ -1621,10 +1669,14 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
                                     (p->M > 1 && (p->ld_z < p->N || p->ld_z > INT32_MAX))) ||
       !check_matrix(p->dx, p->ld_dx, p->M, p->K, p->dtype, false) ||
       (p->dx != nullptr && !check_operand(p->w, p->ld_w, p->N, p->K)) ||
-      (p->dw != nullptr && !check_operand(p->x, p->ld_x, p->M, p->K)) || workspace == nullptr ||
+      (p->dw != nullptr && (p->x_scales == nullptr ? !check_operand(p->x, p->ld_x, p->M, p->K)
+                                                   : p->x == nullptr || !aligned_to(p->x, 8) || p->K % 8 != 0)) ||
+      workspace == nullptr ||
       !aligned_to(workspace, 256))
     return MOE_ERR_ARG;
-  if (workspace_bytes < moe_linear_workspace(p->M, p->N)) return MOE_ERR_WORKSPACE;
+  if (workspace_bytes < moe_linear_workspace(p->M, p->N) +
+                            (p->x_scales != nullptr && p->dw != nullptr ? moe_linear_kept_bytes(p->M, p->K) : 0))
+    return MOE_ERR_WORKSPACE;
   rc = ops_device(&sms);
   if (rc != MOE_OK) return rc;
   const int M = (int)p->M, N = (int)p->N;
@@ -1633,29 +1685,46 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
   const bool copy = act || !check_operand(p->dy, p->ld_dy, M, N);
   const long long ld_dz = copy ? (p->N + 7) / 8 * 8 : p->ld_dy;
   const void* dz = copy ? workspace : p->dy;
-  if (copy || p->db != nullptr) {
+  // x in its type: as it is, or restored behind dz and its sums.
+  const bool restore = p->x_scales != nullptr && p->dw != nullptr;
+  char* const more = static_cast<char*>(workspace) + moe_linear_workspace(p->M, p->N);
+  const void* x = restore ? more : p->x;
+  const long long ld_x = restore ? p->K : p->ld_x;
+  if (copy || p->db != nullptr || restore) {
     ActGradArgs g{};
     g.dy = p->dy;
     g.z = p->z;
     g.z_scales = p->z_scales;
     g.ld_scales = scale_blocks(p->N);
     g.dz = copy ? workspace : nullptr;
-    g.part = p->db != nullptr ? reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(M, N))
-                              : nullptr;
     g.ld_dy = p->ld_dy;
     g.ld_z = p->ld_z;
     g.ld_dz = ld_dz;
     g.M = M;
     g.N = N;
+    g.K = (int)p->K;
     g.dtype = p->dtype;
+    g.btype = p->btype;
     const bool vec = N % 8 == 0 && row_bytes(p->dy, p->ld_dy, p->dtype, M) != 0 &&
                      (!act || (p->z_scales != nullptr ? aligned_to(p->z, 8) && (M == 1 || p->ld_z % 8 == 0)
                                                       : row_bytes(p->z, p->ld_z, p->dtype, M) != 0));
     const int bx = (N + 255) / 256;
     const int want = std::max(1, std::min(kBiasParts, 8 * sms / bx));  // ranges: eight CTAs an SM
     g.rows = ((M + want - 1) / want + 8 * kActRows - 1) / (8 * kActRows) * (8 * kActRows);
-    const int by = (M + g.rows - 1) / g.rows;
-    const dim3 grid((unsigned)bx, (unsigned)by);
+    g.ranges = copy || p->db != nullptr ? (M + g.rows - 1) / g.rows : 0;
+    if (p->db != nullptr && g.ranges == 1)
+      g.db = p->db;
+    else if (p->db != nullptr)
+      g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(M, N));
+    long long blocks = 0;
+    if (restore) {
+      g.x_codes = static_cast<const uint8_t*>(p->x);
+      g.x_scales = p->x_scales;
+      g.x = more;
+      g.units = p->M * p->K / 8;
+      blocks = std::min<long long>((g.units + 256 * kRestoreUnits - 1) / (256 * kRestoreUnits), 16 * sms);
+    }
+    const dim3 grid((unsigned)bx, (unsigned)(g.ranges + (blocks + bx - 1) / bx));
     switch (p->act) {
       case MOE_ACT_RELU: launch_act_grad<MOE_ACT_RELU>(g, vec, grid, s); break;
       case MOE_ACT_GELU: launch_act_grad<MOE_ACT_GELU>(g, vec, grid, s); break;
@@ -1664,8 +1733,9 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
       default: launch_act_grad<MOE_ACT_NONE>(g, vec, grid, s); break;
     }
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    if (p->db != nullptr && launch_behind(bias_grad_kernel, dim3((N + 31) / 32), dim3(32 * kBiasWarps), 0, s,
-                                          (const float*)g.part, by, N, p->btype, p->db) != cudaSuccess)
+    if (g.part != nullptr &&
+        launch_behind(bias_grad_kernel, dim3((N + 31) / 32), dim3(32 * kBiasWarps), 0, s, (const float*)g.part,
+                      g.ranges, N, p->btype, p->db) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   Epilogue e{};
@@ -1677,7 +1747,7 @@ int moe_linear_backward(const moe_linear_args* p, void* workspace, size_t worksp
   to_x.e.ld_y = p->ld_dx;
   to_x.e.ytype = p->dtype;
   to_x.e.vy = row_bytes(p->dx, p->ld_dx, p->dtype, M);
-  Product to_w{{dz, ld_dz, true}, {p->x, p->ld_x, true}, N, (int)p->K, M, e};
+  Product to_w{{dz, ld_dz, true}, {x, ld_x, true}, N, (int)p->K, M, e};
   to_w.e.y = p->dw;
   to_w.e.ld_y = p->ld_dw;
   to_w.e.ytype = p->dwtype;

@@ -418,29 +418,27 @@ Tensor restored(const Tensor& codes, const Tensor& scales, at::ScalarType type, 
   return x;
 }
 
-// x and z: matrices, or (with scales) the codes of their checkpoints. x is restored for the product that
-// reads it; z is read as it is kept.
+// x and z: matrices, or (with scales) the codes of their checkpoints.
 std::tuple<OptTensor, OptTensor, OptTensor> linear_backward(
     const Tensor& dy, const Tensor& kept_x, const OptTensor& x_scales, const Tensor& weight,
     const OptTensor& z, const OptTensor& z_scales, const std::string& act, const py::object& bias,
     const py::object& dw_dtype, bool need_dx, bool need_dw) {
-  std::optional<Launch> restoring;
-  Tensor x = kept_x;
+  const Tensor& x = x_scales.has_value() ? dy : kept_x;  // of the type and device that all have
+  const int dt = checked_type(x, x_scales.has_value() ? "dy" : "x", true);
+  Rows rx;
   if (x_scales.has_value()) {
-    checked_type(dy, "dy", true);
     check_kept(kept_x, *x_scales, "x", dy);
-    restoring.emplace(dy);
-    x = need_dw ? restored(kept_x, *x_scales, dy.scalar_type(), *restoring)
-                : empty(kept_x.sizes(), dy.scalar_type(), dy);
+    rx = rows_of(kept_x, "x");
+    if (rx.c % 8 != 0) refuse("x has rows of ", rx.c, " elements: expected a multiple of 8 for a checkpoint");
+  } else {
+    rx = operand(x, "x", -1, x);
   }
-  const int dt = checked_type(x, "x", true);
-  const Rows rx = operand(x, "x", -1, x);
   if (weight.dim() != 2) refuse("weight must be [N, K], got ", weight.sizes());
   const Rows rw = operand(weight, "weight", rx.c, x);
   moe_linear_args a{};
   a.act = act_of(act);
   if (z.has_value() == (a.act == MOE_ACT_NONE)) refuse("z is needed with an activation, and only then");
-  const auto shape = with_last(x, rw.n);
+  const auto shape = with_last(kept_x, rw.n);
   same_shape(dy, shape, x, "dy");
   const Rows rdy = rows_of(dy, "dy", rw.n);
   Rows rz{};
@@ -456,10 +454,11 @@ std::tuple<OptTensor, OptTensor, OptTensor> linear_backward(
   const at::ScalarType bt = x_or_fp32(bias, "bias", x, at::ScalarType::Undefined);
   const Launch l(x);
   OptTensor dx, dw, db;
-  if (need_dx) dx = empty(x.sizes(), x.scalar_type(), x);
+  if (need_dx) dx = empty(kept_x.sizes(), x.scalar_type(), x);
   if (need_dw) dw = empty({rw.n, rx.c}, wt, x);
   if (bt != at::ScalarType::Undefined) db = empty({rw.n}, bt, x);
-  const size_t size = moe_linear_workspace(rx.n, rw.n);
+  const size_t size =
+      moe_linear_workspace(rx.n, rw.n) + (x_scales.has_value() && need_dw ? moe_linear_kept_bytes(rx.n, rx.c) : 0);
   Tensor work = empty({(int64_t)size}, at::kByte, x);
   a.M = rx.n;
   a.N = rw.n;
@@ -467,7 +466,7 @@ std::tuple<OptTensor, OptTensor, OptTensor> linear_backward(
   a.dtype = a.ytype = dt;
   a.btype = db.has_value() ? type_of(bt) : dt;
   a.dwtype = type_of(wt);
-  a.x = x.data_ptr();
+  a.x = kept_x.data_ptr();
   a.w = weight.data_ptr();
   a.z = ptr(z);
   a.dy = dy.data_ptr();
@@ -480,6 +479,7 @@ std::tuple<OptTensor, OptTensor, OptTensor> linear_backward(
   a.ld_dy = rdy.ld;
   a.ld_dx = a.ld_dw = rx.c;
   a.z_scales = static_cast<const uint8_t*>(ptr(z_scales));
+  a.x_scales = static_cast<const uint8_t*>(ptr(x_scales));
   call("moe_linear_backward", [&] { return moe_linear_backward(&a, work.data_ptr(), size, l.stream); });
   return {dx, dw, db};
 }
