@@ -582,7 +582,7 @@ int moe_gated_backward(const moe_gated_args *args, moe_stream_t stream);
 
 /* The experts' matrix products: rows sorted by expert (moe_sort_experts), each expert with its own
  * weights. dtype is MOE_BF16 or MOE_FP16; N and K are multiples of 8, E is at most 1024. All
- * matrices but `add` have 16-byte aligned bases and leading dimensions (and strides from expert to
+ * matrices have 16-byte aligned bases and leading dimensions (and strides from expert to
  * expert) that are multiples of 8. */
 typedef struct moe_expert_linear_args {
   long long n, N, K;      /* rows; features of y; features of x */

@@ -103,7 +103,7 @@ def test_expert_products_refuse():
     for bad in both + (dict(y=None), dict(y=72), dict(ld_y=8), dict(ld_y=20)):
         assert lib.moe_expert_linear(args(capi.moe_expert_linear_args, **{**ok, **bad}), None) == ARG, bad
     for bad in both + (dict(dwtype=capi.MOE_FP16), dict(dy=None), dict(dy=72), dict(ld_dy=8), dict(dx=72), dict(ld_dx=20),
-                       dict(dw=72), dict(ld_dw=28), dict(stride_dw=380), dict(add=65), dict(add=64, ld_add=16)):
+                       dict(dw=72), dict(ld_dw=28), dict(stride_dw=380), dict(add=72), dict(add=64, ld_add=16), dict(add=64, ld_add=28)):
         assert lib.moe_expert_linear_backward(args(capi.moe_expert_linear_args, **{**ok, **bad}), None) == ARG, bad
     assert lib.moe_expert_linear(args(capi.moe_expert_linear_args, **{**ok, "n": 0, "x": None}), None) == 0
     assert lib.moe_expert_linear_backward(args(capi.moe_expert_linear_args, **{**ok, "n": 0, "dw": None}), None) == 0
@@ -183,6 +183,7 @@ def test_tensors_are_refused():
     refuses("x must be", ops.expert_linear_backward, dy, bf(5, 24), weight, off)
     refuses("x is needed", ops.expert_linear_backward, dy, None, weight, off)
     refuses("add must", ops.expert_linear_backward, dy, x, weight, off, add=bf(6, 16))
+    refuses("16 bytes", ops.expert_linear_backward, dy, x, weight, off, add=bf(6, 25)[:, :24])
     refuses("not asked for", ops.expert_linear_backward, dy, x, weight, off, add=x, need_dx=False)
     refuses("dw_dtype", ops.expert_linear_backward, dy, x, weight, off, dw_dtype=torch.float16)
 

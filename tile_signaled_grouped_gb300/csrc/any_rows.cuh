@@ -159,6 +159,104 @@ __device__ __forceinline__ void store_vec(T* row, long long c, long long width, 
   }
 }
 
+// Four bytes of a row a lane (two elements of 16 bits, one of 32), for kernels with many rows in and out,
+// where the shifting of long vectors is most of the work (see the kernels that use them).
+template <typename T>
+struct RowWord {
+  static constexpr int N = 4 / (int)sizeof(T);
+  uint32_t a, b;  // the aligned words that hold the elements; put together once they are used, so that
+                  // no load waits for another
+  int odd;        // the elements begin in the middle of a
+  // The elements from e of a row of `width`. Reads whole words with an element of the row in them.
+  __device__ __forceinline__ void load(const T* row, long long e, long long width) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(row + e) & ~(uintptr_t)3);
+    odd = N == 2 ? (int)(reinterpret_cast<uintptr_t>(row + e) >> 1 & 1) : 0;
+    const bool second = N == 2 && e + 1 >= 0 && e + 1 < width;  // that element is in the row
+    a = b = 0;
+    if ((e >= 0 && e < width) || (odd == 0 && second)) a = __ldg(p);
+    if (odd != 0 && second) b = __ldg(p + 1);
+  }
+  // Zeros outside the row.
+  __device__ __forceinline__ void get(long long e, long long width, float (&f)[N]) const {
+    if constexpr (N == 1) {
+      f[0] = __uint_as_float(a);
+    } else {
+      const float2 p = unpack2<T>(__funnelshift_r(a, b, 16 * odd));
+      f[0] = e >= 0 && e < width ? p.x : 0.f;
+      f[1] = e + 1 >= 0 && e + 1 < width ? p.y : 0.f;
+    }
+  }
+};
+// The same for rows that mostly lie as the kernel's words do: one load for them, single elements else.
+template <typename T>
+struct LikeWord {
+  static constexpr int N = 4 / (int)sizeof(T);
+  uint32_t w;
+  __device__ __forceinline__ void load(const T* row, long long e, long long width) {
+    const T* p = row + e;
+    if constexpr (N == 1) {
+      w = e >= 0 && e < width ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+    } else {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+      if (e >= 0 && e + 1 < width && (reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+        w = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else {
+        const uint32_t lo = e >= 0 && e < width ? __ldg(h) : 0u;
+        w = lo | (e + 1 >= 0 && e + 1 < width ? (uint32_t)__ldg(h + 1) << 16 : 0u);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+    if constexpr (N == 1) {
+      f[0] = __uint_as_float(w);
+    } else {
+      const float2 p = unpack2<T>(w);
+      f[0] = p.x;
+      f[1] = p.y;
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t pack_word(const float (&f)[4 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4)
+    return __float_as_uint(f[0]);
+  else
+    return pack2<T>(f[0], f[1]);
+}
+// The elements from e, whose address lies on four bytes.
+template <typename T>
+__device__ __forceinline__ void store_word(T* row, long long e, long long width, uint32_t w) {
+  T* p = row + e;
+  if constexpr (sizeof(T) == 4) {
+    if (e >= 0 && e < width) *reinterpret_cast<uint32_t*>(p) = w;
+  } else {
+    unsigned short* h = reinterpret_cast<unsigned short*>(p);
+    if (e >= 0 && e + 1 < width) {
+      *reinterpret_cast<uint32_t*>(p) = w;
+    } else {
+      if (e >= 0 && e < width) h[0] = (unsigned short)w;
+      if (e + 1 >= 0 && e + 1 < width) h[1] = (unsigned short)(w >> 16);
+    }
+  }
+}
+// The elements from e of a whole warp's, anywhere: lanes are neighbours, lane 0's first.
+template <typename T>
+__device__ __forceinline__ void store_word_any(T* row, long long e, long long width, uint32_t w, int lane) {
+  if (sizeof(T) == 4 || (reinterpret_cast<uintptr_t>(row + e) & 2) == 0) {  // the same in every lane
+    store_word(row, e, width, w);
+    return;
+  }
+  // The word before this lane's second element: the lane before has its first half.
+  const uint32_t before = __shfl_up_sync(kAll, w, 1);
+  unsigned short* h = reinterpret_cast<unsigned short*>(row + e);
+  if (lane == 0) {
+    if (e >= 0 && e < width) h[0] = (unsigned short)w;
+  } else {
+    store_word(row, e - 1, width, __byte_perm(before, w, 0x5432));
+  }
+  if (lane == 31 && e + 1 >= 0 && e + 1 < width) h[1] = (unsigned short)(w >> 16);
+}
+
 }  // namespace moe
 
 #endif  // __CUDACC__

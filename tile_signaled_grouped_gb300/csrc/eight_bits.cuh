@@ -70,6 +70,23 @@ struct Codes {
     }
   }
 };
+// N elements from element e of a row of `width` and of codes that start anywhere; zeros outside it.
+template <int N>
+struct CodeWord {
+  uint8_t code[N], scale[N];
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, long long e, long long width) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool in = e + i >= 0 && e + i < width;
+      code[i] = in ? __ldg(codes + e + i) : 0;
+      scale[i] = in ? __ldg(scales + (e + i) / kScaleBlock) : 0;
+    }
+  }
+  __device__ __forceinline__ void get(long long, long long, float (&f)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = decode2(code[i]).x * scale_value(scale[i]);
+  }
+};
 // The codes of one element.
 __device__ __forceinline__ float decode1(const uint8_t* p, float scale) { return decode2(__ldg(p)).x * scale; }
 

@@ -255,25 +255,38 @@ __global__ void __launch_bounds__(32 * kRowWarps) combine_kernel(const __grid_co
 }
 
 // Elements of a row that was kept, a vector of T at a time, as they lie in memory.
-template <typename T, bool EIGHT, bool ANY>
+template <typename T, bool EIGHT>
 struct Kept {
   static constexpr int N = Vec<T>::kN;
-  typename std::conditional<EIGHT, Codes<N, ANY>, RowVec<T, ANY>>::type u;
+  typename std::conditional<EIGHT, Codes<N, false>, RowVec<T, false>>::type u;
   uint8_t scale;
   __device__ __forceinline__ void load(const RowsArgs& a, long long row, int c) {
     if constexpr (EIGHT) {
-      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, c, ANY ? a.D : c + N);
-      scale = !ANY || c < a.D ? __ldg(a.scales + row * a.ld_s + c / kScaleBlock) : 0;
+      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, c, c + N);
+      scale = __ldg(a.scales + row * a.ld_s + c / kScaleBlock);
     } else {
-      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, ANY ? a.D : c + N);
+      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, c + N);
     }
   }
-  __device__ __forceinline__ void get(float (&f)[N]) const {
+  __device__ __forceinline__ void get(int, long long, float (&f)[N]) const {
     if constexpr (EIGHT)
       u.get(scale_value(scale), f);
     else
       u.get(f);
   }
+};
+// The same a word at a time, of rows that start anywhere.
+template <typename T, bool EIGHT>
+struct KeptWord {
+  static constexpr int N = RowWord<T>::N;
+  typename std::conditional<EIGHT, CodeWord<N>, RowWord<T>>::type u;
+  __device__ __forceinline__ void load(const RowsArgs& a, long long row, int c) {
+    if constexpr (EIGHT)
+      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, a.scales + row * a.ld_s, c, a.D);
+    else
+      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, a.D);
+  }
+  __device__ __forceinline__ void get(int c, long long width, float (&f)[N]) const { u.get(c, width, f); }
 };
 
 // Gradients of the rows and weights. A CTA takes one token, its warps walk the row together: a
@@ -281,11 +294,12 @@ struct Kept {
 // written to (dr). The warps' partial products are added in their order. EIGHT: the rows kept are codes.
 // Bound by the bytes of the rows: all eight loads leave before the first is used, and three CTAs
 // of eight warps fit on an SM (as fp32 the eight vectors took 121 registers, and 328 us where this takes
-// 126 for 4096 tokens of 8 x 7168 from codes).
+// 126 for 4096 tokens of 8 x 7168 from codes). ANY: rows that start anywhere go by words (8192 tokens of
+// 8 x 2049 take 211 us so, and 261 by vectors shifted together).
 constexpr int kBackSlots = 8;
 template <typename T, bool EIGHT, bool ANY>
-__global__ void __launch_bounds__(256, ANY ? 2 : 3) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
-  constexpr int N = Vec<T>::kN, kSpan = kOwn<ANY> * N;
+__global__ void __launch_bounds__(256, 3) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
+  constexpr int N = ANY ? RowWord<T>::N : Vec<T>::kN, kSpan = 32 * N;
   __shared__ float part[8][kBackSlots];
   allow_dependent_launch();
   wait_prior_grid();
@@ -306,26 +320,30 @@ __global__ void __launch_bounds__(256, ANY ? 2 : 3) combine_backward_kernel(cons
       for (int c0 = warp * kSpan; c0 < a.D; c0 += warps * kSpan) {
         const int c = c0 + lane * N;
         if (!ANY && c >= a.D) break;
-        Kept<T, EIGHT, ANY> v[kBackSlots];
-        RowVec<T, ANY> x;
+        typename std::conditional<ANY, KeptWord<T, EIGHT>, Kept<T, EIGHT>>::type v[kBackSlots];
+        typename std::conditional<ANY, RowWord<T>, RowVec<T, false>>::type x;
         x.load(dy, c, ANY ? a.D : c + N);  // without ANY, c is inside
 #pragma unroll
         for (int j = 0; j < kBackSlots; ++j)
           if (row[j] >= 0) v[j].load(a, row[j], c);
         float d[N];
-        x.get(d);
+        if constexpr (ANY)
+          x.get(c, a.D, d);
+        else
+          x.get(d);
 #pragma unroll
         for (int j = 0; j < kBackSlots; ++j) {
           if (row[j] < 0) continue;
           float f[N];
-          v[j].get(f);
-          if (!ANY || lane < kOwn<ANY>) {
+          v[j].get(c, a.D, f);
 #pragma unroll
-            for (int q = 0; q < N; ++q) dot[j] = fmaf(d[q], f[q], dot[j]);
-          }
+          for (int q = 0; q < N; ++q) dot[j] = fmaf(d[q], f[q], dot[j]);
 #pragma unroll
           for (int q = 0; q < N; ++q) f[q] = w[j] * d[q];
-          store_vec<ANY>(dr + row[j] * a.ld_d, c, ANY ? a.D : c + N, f, lane);
+          if constexpr (ANY)
+            store_word_any(dr + row[j] * a.ld_d, c, a.D, pack_word<T>(f), lane);
+          else
+            store_vec<false>(dr + row[j] * a.ld_d, c, c + N, f, lane);
         }
       }
 #pragma unroll
@@ -405,7 +423,8 @@ int launch_combine(const RowsArgs& a, bool vec, cudaStream_t s) {
 template <typename T>
 int launch_backward(const RowsArgs& a, bool vec, cudaStream_t s) {
   // Warps of a token: four vectors of a lane each, eight warps at most.
-  const unsigned warps = (unsigned)std::min<long long>(8, std::max<long long>(1, a.D / Vec<T>::kN / 128));
+  const long long width = a.D / (vec ? Vec<T>::kN : RowWord<T>::N);
+  const unsigned warps = (unsigned)std::min<long long>(8, std::max<long long>(1, width / 128));
   const dim3 grid((unsigned)std::min<long long>(a.T, 1 << 20)), block(32 * warps);
   if (a.scales != nullptr)
     return launched(vec ? launch_behind(combine_backward_kernel<T, true, false>, grid, block, 0, s, a)

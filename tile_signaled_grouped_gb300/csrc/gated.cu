@@ -200,6 +200,57 @@ __global__ void __launch_bounds__(32 * kWarps) gated_backward_kernel(const __gri
   }
 }
 
+// The same for whole values in rows that start anywhere: a word of 4 bytes a lane, by the place of dgate, as
+// which the other outputs mostly lie; the inputs are read by their own places. (By vectors shifted together,
+// with 600 instructions a vector, 65536 rows of 2049 took 602 us; this takes 343. From codes it is the other
+// way round: 491 by vectors, 725 by words.)
+constexpr int kWordUnits = 4;
+template <typename T, int ACT>
+__global__ void __launch_bounds__(32 * kWarps) gated_backward_words_kernel(const __grid_constant__ GatedArgs a) {
+  constexpr int N = LikeWord<T>::N;
+  allow_dependent_launch();
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const Walk k(a.n, a.c + N - 1, 32 * N * kWordUnits);
+  for (long long u = k.first(); u < k.units; u += k.step()) {
+    const long long i = u / k.chunks;
+    T* dgate = static_cast<T*>(a.dgate) + i * a.ld_dgate;
+    const int lead = N == 2 && (reinterpret_cast<uintptr_t>(dgate) & 2) != 0 ? 1 : 0;
+    const long long e0 = ((u - i * k.chunks) * 32 * kWordUnits + lane) * N - lead;
+    LikeWord<T> g[kWordUnits], v[kWordUnits], d[kWordUnits];
+#pragma unroll
+    for (int q = 0; q < kWordUnits; ++q) {
+      const long long e = e0 + 32 * N * q;
+      g[q].load(static_cast<const T*>(a.gate) + i * a.ld_gate, e, a.c);
+      v[q].load(static_cast<const T*>(a.up) + i * a.ld_up, e, a.c);
+      d[q].load(static_cast<const T*>(a.dh) + i * a.ld_dh, e, a.c);
+    }
+#pragma unroll
+    for (int q = 0; q < kWordUnits; ++q) {
+      const long long e = e0 + 32 * N * q;
+      float x[N], y[N], dh[N], o[N];
+      g[q].get(x);
+      v[q].get(y);
+      d[q].get(dh);
+#pragma unroll
+      for (int p = 0; p < N; ++p) {
+        float slope;
+        x[p] = act_both<ACT>(x[p], &slope);
+        o[p] = dh[p] * y[p] * slope;
+      }
+      store_word(dgate, e, a.c, pack_word<T>(o));
+#pragma unroll
+      for (int p = 0; p < N; ++p) o[p] = dh[p] * x[p];
+      store_word_any(static_cast<T*>(a.dup) + i * a.ld_dup, e, a.c, pack_word<T>(o), lane);
+      if (a.h != nullptr) {
+#pragma unroll
+        for (int p = 0; p < N; ++p) o[p] = x[p] * y[p];
+        store_word_any(static_cast<T*>(a.h) + i * a.ld_h, e, a.c, pack_word<T>(o), lane);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------- host side
 constexpr long long kMaxSize = INT32_MAX / 2;
 
@@ -264,14 +315,16 @@ int checkpoint(const moe_checkpoint_args* p, bool restore, moe_stream_t stream) 
 
 template <typename T, int ACT>
 int launch_gated(const GatedArgs& a, bool vec, bool kept, bool backward, cudaStream_t s) {
-  const int lanes = vec ? 32 : kept && !backward ? kOwn<true, true> : kOwn<true>;
-  const dim3 grid(grid_of(a.n, a.c, lanes * kGatedUnits * Vec<T>::kN)), block(32 * kWarps);
+  const bool words = backward && !kept && !vec;
+  const int lanes = vec || words ? 32 : kept && !backward ? kOwn<true, true> : kOwn<true>;
+  const dim3 grid(grid_of(a.n, a.c, lanes * (words ? kWordUnits * LikeWord<T>::N : kGatedUnits * Vec<T>::kN)));
+  const dim3 block(32 * kWarps);
   auto go = [&](auto* v, auto* e) {
     return launched(vec ? launch_behind(v, grid, block, 0, s, a) : launch_behind(e, grid, block, 0, s, a));
   };
   if (backward)
     return kept ? go(gated_backward_kernel<T, ACT, false, true>, gated_backward_kernel<T, ACT, true, true>)
-                : go(gated_backward_kernel<T, ACT, false, false>, gated_backward_kernel<T, ACT, true, false>);
+                : go(gated_backward_kernel<T, ACT, false, false>, gated_backward_words_kernel<T, ACT>);
   return kept ? go(gated_kernel<T, ACT, false, true>, gated_kernel<T, ACT, true, true>)
               : go(gated_kernel<T, ACT, false, false>, gated_kernel<T, ACT, true, false>);
 }

@@ -688,7 +688,7 @@ std::tuple<OptTensor, OptTensor> expert_linear_backward(const Tensor& dy, const 
   if (add.has_value()) {
     if (!need_dx) refuse("add is a part of dx, which is not asked for");
     same_shape(*add, shape, x, "add");
-    ra = rows_of(*add, "add", e.K);
+    ra = operand(*add, "add", e.K, x);
   }
   const at::ScalarType wt = x_or_fp32(dw_dtype, "dw_dtype", x, x.scalar_type());
   const Launch l(x);

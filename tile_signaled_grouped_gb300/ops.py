@@ -260,7 +260,8 @@ def expert_linear(x, weight, offsets, stream=None):
 def expert_linear_backward(dy, x, weight, offsets, add=None, dw_dtype=None, need_dx=True, need_dw=True,
                            stream=None):
     """(dx, dweight) of expert_linear from the gradient dy of y, for its x (None without need_dw), weight and
-    offsets. add [n, K] of x's type is added to dx before it is rounded (the gradient through another product of the same x).
+    offsets. add [n, K] of x's type, rows on 16 bytes, is added to dx before it is rounded (the gradient through
+    another product of the same x).
     dweight has dw_dtype (x's type or fp32; default x's); it is zero for experts without rows."""
     if stream is not None:
         with _on(dy, stream):
