@@ -295,9 +295,9 @@ struct KeptWord {
 // Bound by the bytes of the rows: all eight loads leave before the first is used, and three CTAs
 // of eight warps fit on an SM (as fp32 the eight vectors took 121 registers, and 328 us where this takes
 // 126 for 4096 tokens of 8 x 7168 from codes). ANY: rows that start anywhere go by words (8192 tokens of
-// 8 x 2049 take 211 us so, and 261 by vectors shifted together).
+// 8 x 2049 take 211 us so, and 261 by vectors shifted together). DY_ANY: dy's alone do.
 constexpr int kBackSlots = 8;
-template <typename T, bool EIGHT, bool ANY>
+template <typename T, bool EIGHT, bool ANY, bool DY_ANY>
 __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int N = ANY ? RowWord<T>::N : Vec<T>::kN, kSpan = 32 * N;
   __shared__ float part[8][kBackSlots];
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const __grid_c
         const int c = c0 + lane * N;
         if (!ANY && c >= a.D) break;
         typename std::conditional<ANY, KeptWord<T, EIGHT>, Kept<T, EIGHT>>::type v[kBackSlots];
-        typename std::conditional<ANY, RowWord<T>, RowVec<T, false>>::type x;
-        x.load(dy, c, ANY ? a.D : c + N);  // without ANY, c is inside
+        typename std::conditional<ANY, RowWord<T>, RowVec<T, DY_ANY>>::type x;
+        x.load(dy, c, ANY || DY_ANY ? a.D : c + N);  // without ANY, c is inside
 #pragma unroll
         for (int j = 0; j < kBackSlots; ++j)
           if (row[j] >= 0) v[j].load(a, row[j], c);
@@ -421,16 +421,19 @@ int launch_combine(const RowsArgs& a, bool vec, cudaStream_t s) {
 }
 
 template <typename T>
-int launch_backward(const RowsArgs& a, bool vec, cudaStream_t s) {
+int launch_backward(const RowsArgs& a, bool vec, bool dy, cudaStream_t s) {
   // Warps of a token: four vectors of a lane each, eight warps at most.
   const long long width = a.D / (vec ? Vec<T>::kN : RowWord<T>::N);
   const unsigned warps = (unsigned)std::min<long long>(8, std::max<long long>(1, width / 128));
   const dim3 grid((unsigned)std::min<long long>(a.T, 1 << 20)), block(32 * warps);
+  auto go = [&](auto* kernel) { return launched(launch_behind(kernel, grid, block, 0, s, a)); };
   if (a.scales != nullptr)
-    return launched(vec ? launch_behind(combine_backward_kernel<T, true, false>, grid, block, 0, s, a)
-                        : launch_behind(combine_backward_kernel<T, true, true>, grid, block, 0, s, a));
-  return launched(vec ? launch_behind(combine_backward_kernel<T, false, false>, grid, block, 0, s, a)
-                      : launch_behind(combine_backward_kernel<T, false, true>, grid, block, 0, s, a));
+    return !vec ? go(combine_backward_kernel<T, true, true, false>)
+           : dy ? go(combine_backward_kernel<T, true, false, false>)
+                : go(combine_backward_kernel<T, true, false, true>);
+  return !vec ? go(combine_backward_kernel<T, false, true, false>)
+         : dy ? go(combine_backward_kernel<T, false, false, false>)
+              : go(combine_backward_kernel<T, false, false, true>);
 }
 
 // Slots of a lane, so that there are at most kSortChunks chunks.
@@ -548,11 +551,12 @@ int moe_combine_experts_backward(const moe_rows_args* p, moe_stream_t stream) {
   a.ld_s = p->ld_scales;
   a.dw = p->dw;
   // A vector of codes has as many elements as one of 16 bytes of the type.
-  const bool vec = p->D * b % 16 == 0 && vector_rows(p->x, p->ld_x, p->T, b, 16) &&
-                   vector_rows(p->dr, p->ld_dr, n, b, 16) && vector_rows(p->r, p->ld_r, n, kb, 16 / b * kb);
-  return p->dtype == MOE_FP32   ? launch_backward<float>(a, vec, s)
-         : p->dtype == MOE_BF16 ? launch_backward<__nv_bfloat16>(a, vec, s)
-                                : launch_backward<__half>(a, vec, s);
+  const bool vec = p->D * b % 16 == 0 && vector_rows(p->dr, p->ld_dr, n, b, 16) &&
+                   vector_rows(p->r, p->ld_r, n, kb, 16 / b * kb);
+  const bool dy = vector_rows(p->x, p->ld_x, p->T, b, 16);
+  return p->dtype == MOE_FP32   ? launch_backward<float>(a, vec, dy, s)
+         : p->dtype == MOE_BF16 ? launch_backward<__nv_bfloat16>(a, vec, dy, s)
+                                : launch_backward<__half>(a, vec, dy, s);
 }
 
 }  // extern "C"
