@@ -231,7 +231,7 @@ def test_bad_rows_stay_in_their_expert():
 def test_offsets_outside_the_rows_are_left_out():
     """Offsets that do not ascend or leave 0 .. n touch nothing outside the matrices."""
     offsets, n, x, weight, dy, _ = experts_case(([40, 50, 60], 0, 64, 64, "bf16", 0))
-    for bad in ([-7, 40, 90, 150], [0, 40, 90, 10 ** 6], [0, 40, 40, 40]):
+    for bad in ([-7, 40, 90, 150], [0, 40, 90, 10 ** 6], [0, 40, 40, 40], [150, 150, 150, 150]):
         off = torch.tensor(bad, dtype=torch.int32, device="cuda")
         inside = off.clamp(0, n)
         y = ops.expert_linear(x, weight, off)
@@ -240,6 +240,60 @@ def test_offsets_outside_the_rows_are_left_out():
         dx, dw = ops.expert_linear_backward(dy, x, weight, off)
         close(dw, X.weights_grad(dy, x, inside)[0], 2 * (100 + 24) * R.U32 * X.weights_grad(dy, x, inside)[1])
     assert ops.status() == (0, 0)
+
+
+def test_offsets_that_descend_end_in_order():
+    """Experts that claim the same rows: what they write is anyone's, but nothing else is touched and
+    the call ends."""
+    offsets, n, x, weight, dy, _ = experts_case(([40, 50, 60], 0, 64, 64, "bf16", 0))
+    for bad in ([0, 90, 40, 150], [150, 0, 150, 0], [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, -2 ** 31]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        y = ops.expert_linear(x, weight, off)
+        dx, dw = ops.expert_linear_backward(dy, x, weight, off)
+        torch.cuda.synchronize()
+        assert y.shape == (n, 64) and dx.shape == (n, 64) and dw.shape == (3, 64, 64)
+    assert ops.status() == (0, 0)
+
+
+def test_more_than_2_31_elements():
+    """Rows whose elements, and weights whose elements, do not fit 32 bits: the last ones are right."""
+    T, topk, D, E = 40000, 8, 8192, 16
+    ids = draw_ids(gen(T, D), T, E, topk, False)
+    order = ops.sort_experts(ids, E)
+    x = matrix(gen(T), T, D, "bf16")
+    r = ops.expert_rows(x, order)
+    assert r.numel() > 2 ** 31
+    at = torch.tensor([0, 1, T * topk // 2, T * topk - 2, T * topk - 1], device="cuda")
+    assert torch.equal(r[at], x[order.slots[at].long() // topk])
+    kept = ops.checkpoint(r)
+    some = ops.checkpoint(r[at])
+    assert torch.equal(kept.codes[at].view(torch.uint8), some.codes.view(torch.uint8))
+    assert torch.equal(kept.scales[at], some.scales)
+    h, (g8, _) = ops.gated(r, r, checkpoint=True)
+    assert torch.equal(h[at], ops.gated(r[at], r[at])[0])
+    assert torch.equal(g8.codes[at].view(torch.uint8), some.codes.view(torch.uint8))
+    w = torch.rand(T, topk, device="cuda")
+    tok = torch.tensor([0, T // 2, T - 1], device="cuda")
+    want, tol = X.combine(r, w[tok], order.rows[tok])
+    close(ops.combine_experts(r, w, order)[tok], want, tol)
+    dr, dw = ops.combine_experts_backward(x, kept, w, order)
+    assert torch.equal(dr[at], (x[order.slots[at].long() // topk].float() * w.view(-1)[order.slots[at].long()][:, None])
+                       .bfloat16())
+    del r, kept, h, g8, dr
+    E, N, K = 40, 8192, 8192  # dW of 2.7e9 elements
+    weight = torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda")
+    weight[-1].normal_(std=K ** -0.5)
+    weight[0].normal_(std=K ** -0.5)
+    offsets = torch.tensor([0] + [5] * (E - 1) + [12], dtype=torch.int32, device="cuda")
+    x, dy = matrix(gen(1), 12, K, "bf16"), matrix(gen(2), 12, N, "bf16")
+    y = ops.expert_linear(x, weight, offsets)
+    for e, rows in ((0, slice(0, 5)), (E - 1, slice(5, 12))):
+        x64, w64 = x[rows].double(), weight[e].double()
+        close(y[rows], x64 @ w64.t(), R.product_error(x64, w64.t(), K))
+    _, dw = ops.expert_linear_backward(dy, x, weight, offsets, need_dx=False)
+    d64, x64 = dy[5:].double(), x[5:].double()
+    close(dw[-1], d64.t() @ x64, R.product_error(d64.t(), x64, 7))
+    assert not dw[1:-1].any()
 
 
 def test_no_rows():

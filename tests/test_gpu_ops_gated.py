@@ -182,3 +182,11 @@ def test_linear_backward_from_checkpoints(M, N, K, dtype, act, bias):
         only = ops.linear_backward(dy, x8, w, z=z8, act=act, need_dw=False)
         assert torch.equal(only[0], dx) and only[1] is None
     assert ops.status() == (0, 0)
+
+
+def test_linear_backward_from_checkpoints_of_no_rows():
+    none = ops.checkpoint(torch.empty(0, 24, device="cuda").bfloat16())
+    dy, w = torch.empty(0, 16, device="cuda").bfloat16(), torch.ones(16, 24, device="cuda").bfloat16()
+    dx, dw, db = ops.linear_backward(dy, none, w, z=ops.checkpoint(dy), act="silu", bias=torch.float32)
+    assert dx.shape == (0, 24) and not dw.any() and not db.any()
+    assert ops.restore(none, torch.float16).shape == (0, 24)

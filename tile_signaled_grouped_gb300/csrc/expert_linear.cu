@@ -132,6 +132,7 @@ struct RowsArgs {
   uint32_t* status;
   int n, E, J, nk;     // J: features of y; nk: 64-element blocks of the sum
   int tiles_j, stages;
+  int most;            // tiles of rows at most
   bool w_mn;           // W^T, whose features are innermost
 };
 constexpr int kBlocks = 2;  // of 64 k in a stage
@@ -168,6 +169,7 @@ __device__ __forceinline__ Table make_table(const RowsArgs& a, int* at, int* scr
     if (e <= a.E) t.first[e] = at_tile;
     at_tile += tiles[i];
   }
+  t.tiles = min(t.tiles, a.most);
   __syncthreads();
   return t;
 }
@@ -183,31 +185,35 @@ struct RowWalk {
   __device__ __forceinline__ RowWalk(const RowsArgs& args, const Table& table, int pair, int n)
       : a(args), t(table), at(pair - n), pairs(n), e(0), j0(0), row0(0), rows(0), cols(0) {}
   __device__ __forceinline__ bool next() {
-    at += pairs;
-    const int tile = at / a.tiles_j;
-    if (tile >= t.tiles) return false;
-    int lo = 0, hi = a.E + 1;  // the last expert whose first tile is not past it
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (t.first[mid] <= tile)
-        lo = mid;
-      else
-        hi = mid;
+    while (true) {
+      at += pairs;
+      const int tile = at / a.tiles_j;
+      if (tile >= t.tiles) return false;
+      int lo = 0, hi = a.E + 1;  // the last expert whose first tile is not past it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (t.first[mid] <= tile)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      e = lo;
+      // Groups of kGroup tiles of rows, inside a group feature by feature: the tiles in flight share their
+      // operands in L2 (all tiles of rows of a feature tile first took 185 us where this takes 149 for 16384
+      // rows of one expert, 2048 x 4096).
+      const int tiles = (t.count[e] + kRows - 1) / kRows, local = at - t.first[e] * a.tiles_j;
+      const int g = local / (kGroup * a.tiles_j), r = local - g * kGroup * a.tiles_j;
+      const int in_group = max(min(kGroup, tiles - g * kGroup), 1), tj = r / in_group;
+      const int ti = g * kGroup + r - tj * in_group;
+      const int even = ((t.count[e] + tiles - 1) / max(tiles, 1) + kRowStep - 1) / kRowStep * kRowStep;
+      const int per = tiles > 8 ? kRows : even;  // of more than eight the last might be left without rows
+      j0 = tj * kFeatures;
+      row0 = t.start[e] + ti * per;
+      rows = min(per, t.count[e] - ti * per);
+      cols = (rows + kRowStep - 1) / kRowStep * kRowStep;
+      // (Offsets that do not ascend may make more tiles than an int counts: no rows then.)
+      if (ti >= 0 && rows > 0) return true;
     }
-    e = lo;
-    const int tiles = (t.count[e] + kRows - 1) / kRows, local = at - t.first[e] * a.tiles_j;
-    // Groups of kGroup tiles of rows, inside a group feature by feature: the tiles in flight share their
-    // operands in L2 (all tiles of rows of a feature tile first took 185 us where this takes 149 for 16384
-    // rows of one expert, 2048 x 4096).
-    const int g = local / (kGroup * a.tiles_j), r = local - g * kGroup * a.tiles_j;
-    const int in_group = min(kGroup, tiles - g * kGroup), tj = r / in_group, ti = g * kGroup + r - tj * in_group;
-    const int even = ((t.count[e] + tiles - 1) / tiles + kRowStep - 1) / kRowStep * kRowStep;
-    const int per = tiles > 8 ? kRows : even;  // of more than eight the last might be left without rows
-    j0 = tj * kFeatures;
-    row0 = t.start[e] + ti * per;
-    rows = min(per, t.count[e] - ti * per);
-    cols = (rows + kRowStep - 1) / kRowStep * kRowStep;
-    return true;
   }
   __device__ __forceinline__ int steps() const { return e < a.E ? a.nk : 0; }
 };
@@ -678,7 +684,8 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   for (int b = 0; b < 4; ++b)
     if (!make_map(&a.tx[b], x, bf16, 0, p->n, sum, ld_x, 0, 16 << b)) return MOE_ERR_CUDA;
   // Tiles of rows: one for every 256 and one more for each expert at most.
-  const long long tiles = (p->n / kRows + std::min<long long>(p->E + 1, p->n)) * a.tiles_j;
+  a.most = (int)(p->n / kRows + std::min<long long>(p->E + 1, p->n));
+  const long long tiles = (long long)a.most * a.tiles_j;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t more = kEpiWarps * kPatchBytes + table_bytes(a.E);
   constexpr size_t kStage = kBlocks * kBlockBytes;
