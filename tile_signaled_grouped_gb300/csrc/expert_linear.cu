@@ -497,7 +497,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
     int it = 0, st = 0;
     uint32_t phase = 0, at = 0;
     bool ok = true;
-    for (; ok && walk.next(); ++it) {
+    while (ok && walk.next()) {
+      if (walk.steps == 0) continue;  // zeros: the epilogue's alone
       const int acc = it & 1;
       if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, a.status, 0x54000000u)) break;
       tc_fence_after();
@@ -520,6 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
       }
       if (ok && elect_one()) tc_commit_pair(&sm.tfull[acc], 0x3);
       __syncwarp();
+      ++it;
     }
     wait_products(sm, a.status);
   } else if (warp == 2 + kWeightEpiWarps) {
@@ -549,11 +551,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
     const int q = warp & 3, from = ((warp - 2) >> 2) * kColumns;  // TMEM lane quarter, first column
     const uint32_t tempty[2] = {map_shared(&sm.tempty[0], 0), map_shared(&sm.tempty[1], 0)};
     uint8_t* patch = patches + (warp - 2) * kPatchBytes;
-    for (int it = 0; walk.next(); ++it) {
+    int it = 0;
+    while (walk.next()) {
+      const int i = walk.i0 + (int)crank * 128 + q * 32 + lane;
+      O* to = static_cast<O*>(a.dw) + walk.e * a.stride + (long long)(i - lane) * a.ld;  // the warp's first row
+      const int rows = a.N - (i - lane);
+      if (walk.steps == 0) {  // an expert without rows
+        constexpr int kLanes = kColumns * (int)sizeof(O) / 16;  // of a row
+        const int j = walk.j0 + from + lane % kLanes * (16 / (int)sizeof(O));
+#pragma unroll 4
+        for (int r = lane / kLanes; r < 32; r += 32 / kLanes)
+          if (r < rows && j < a.K) *reinterpret_cast<uint4*>(to + r * a.ld + j) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
       const int acc = it & 1;
       if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, a.status, 0x56000000u)) break;
+      ++it;
       tc_fence_after();
-      const int i = walk.i0 + (int)crank * 128 + q * 32 + lane;
       const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
 #pragma unroll 1
       for (int c = from; c < from + kColumns; c += 32) {
@@ -566,15 +580,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_read(tempty[acc]);
         }
-        if (walk.steps == 0) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] = 0;
-        }
         // Rows of 64 bytes, turned round in shared memory so that four lanes store a row's: such stores
         // write 6.6 TB/s here, rows of one lane each 4.9 in 32 bytes and 2.6 in 16.
         constexpr int kPart = 64 / (int)sizeof(O);  // columns of 64 bytes
-        const int rows = a.N - (walk.i0 + (int)crank * 128 + q * 32);
-        O* to = static_cast<O*>(a.dw) + walk.e * a.stride + (long long)(i - lane) * a.ld;  // the warp's first row
 #pragma unroll
         for (int h = 0; h < 32; h += kPart) {
           uint32_t w[16];
