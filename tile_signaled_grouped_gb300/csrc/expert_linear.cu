@@ -62,6 +62,13 @@ __device__ __forceinline__ void arrive_read(uint32_t cl_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // An expert's rows: whatever the offsets hold, inside 0 .. n.
 __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int E, int n, int* start, int* count) {
   const int lo = min(max(__ldg(offsets + e), 0), n);
@@ -405,6 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------- dW
 struct WeightArgs {
   CUtensorMap ty, tx;  // rows of dy and of x
+  CUtensorMap tw;      // dW, 32 rows of 64 bytes
   const int32_t* offsets;
   void* dw;                 // [E][N][K], rows ld apart, experts `stride`
   long long ld, stride;
@@ -593,22 +601,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
             else
               w[x] = pack2<T>(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
           }
-          __syncwarp();  // the patch's last readers
+          if (lane == 0) bulk_wait_read<0>();  // the patch's last copy
+          __syncwarp();
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             *reinterpret_cast<uint4*>(patch + patch_at(lane, x)) =
                 make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          const int j = walk.j0 + c + h + (lane & 3) * (kPart / 4);  // this lane's columns
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = (lane >> 2) + 8 * x;
-            const uint4 u = *reinterpret_cast<const uint4*>(patch + patch_at(r, lane & 3));
-            if (r < rows && j < a.K) *reinterpret_cast<uint4*>(to + r * a.ld + j) = u;
+          const int j = walk.j0 + c + h;
+          if (rows > 0 && j < a.K && lane == 0) {
+            tma_store_3d(&a.tw, patch, j, i, walk.e);
+            bulk_commit();
           }
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   pair_teardown(tmem, warp);
 }
@@ -669,6 +679,23 @@ int launch_pairs(unsigned pairs, int threads, size_t smem, cudaStream_t s, const
   return launched(e);
 }
 
+// Map of dW for stores: boxes of 32 rows of 64 bytes, whose 64-byte swizzle is that of the patches.
+bool make_store_map(CUtensorMap* m, const moe_expert_linear_args* p) {
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t b = (cuuint64_t)type_bytes(p->dwtype);
+  const long long ld = p->N == 1 ? p->K : p->ld_dw, stride = p->E == 1 ? p->N * ld : p->stride_dw;
+  cuuint64_t dims[3] = {(cuuint64_t)p->K, (cuuint64_t)p->N, (cuuint64_t)p->E};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * b, (cuuint64_t)stride * b};
+  cuuint32_t box[3] = {(cuuint32_t)(64 / b), 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType t = p->dwtype == MOE_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : p->dwtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return encode(m, t, 3, p->dw, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // y of the forward pass, or dx: `w_mn` takes W^T.
 int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x, bool w_mn, const void* add,
                  long long ld_add, void* y, long long ld_y, int sms, cudaStream_t s) {
@@ -708,7 +735,7 @@ int weights_product(const moe_expert_linear_args* p, int sms, cudaStream_t s) {
   WeightArgs a{};
   const bool bf16 = p->dtype == MOE_BF16;
   if (!make_map(&a.ty, p->dy, bf16, 0, p->n, p->N, p->ld_dy, 0, kBlockK) ||
-      !make_map(&a.tx, p->x, bf16, 0, p->n, p->K, p->ld_x, 0, kBlockK))
+      !make_map(&a.tx, p->x, bf16, 0, p->n, p->K, p->ld_x, 0, kBlockK) || !make_store_map(&a.tw, p))
     return MOE_ERR_CUDA;
   a.offsets = p->offsets;
   a.dw = p->dw;
