@@ -67,10 +67,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a) {
-  extern __shared__ int next[];  // [warps][E]: counts, then every warp's next row of each expert
+  extern __shared__ int next[];  // [warps][E]: counts, then every warp's next row of each expert; [2][E]: sums
   __shared__ int scratch[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) next[i] = 0;
+  for (int i = threadIdx.x; i < (kSortWarps + 2) * a.E; i += kSortThreads) next[i] = 0;
   __syncthreads();
   allow_dependent_launch();
   wait_prior_grid();
@@ -86,22 +86,37 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
       if (e[u] < a.E) atomicAdd(&mine[e[u]], 1);
   }
   __syncthreads();
-  // Two neighbouring experts a thread: their rows of all chunks, and of the chunks before this one.
-  int all[2] = {0, 0}, before[2] = {0, 0};
+  // Every expert's rows of all chunks, and of the chunks before this one: the threads share the chunks'
+  // counts, so that each has few to wait for.
+  int* sum = next + kSortWarps * a.E;  // [2][E]
+  if (gridDim.x > 1) {
+    const int groups = max(1, kSortThreads / a.E);
+    for (int i = threadIdx.x; i < groups * a.E; i += kSortThreads) {
+      const int g = i / a.E, e = i - g * a.E;
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int c = g; c < (int)gridDim.x; c += groups) {
+        const int v = __ldcg(a.counts + (size_t)c * a.E + e);
+        all += v;
+        before += c < (int)blockIdx.x ? v : 0;
+      }
+      atomicAdd(&sum[e], all);
+      atomicAdd(&sum[a.E + e], before);
+    }
+  } else {
+    for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+      int all = 0;
+      for (int w = 0; w < kSortWarps; ++w) all += next[w * a.E + e];
+      sum[e] = all;
+    }
+  }
+  __syncthreads();
+  int all[2], before[2];  // of two neighbouring experts a thread
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int e = 2 * threadIdx.x + h;
-    if (e >= a.E) continue;
-    if (gridDim.x > 1) {
-#pragma unroll 8
-      for (int c = 0; c < (int)gridDim.x; ++c) {
-        const int v = __ldcg(a.counts + (size_t)c * a.E + e);
-        all[h] += v;
-        before[h] += c < (int)blockIdx.x ? v : 0;
-      }
-    } else {
-      for (int w = 0; w < kSortWarps; ++w) all[h] += next[w * a.E + e];
-    }
+    all[h] = e < a.E ? sum[e] : 0;
+    before[h] = e < a.E ? sum[a.E + e] : 0;
   }
   int total;
   const int first = block_excl_scan(all[0] + all[1], scratch, &total);
@@ -478,7 +493,7 @@ int moe_sort_experts(const int32_t* ids, long long n, int E, int32_t* slots, int
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(sort_kernel), &ready);
   if (e == cudaSuccess && grid.x > 1) e = launch_behind(sort_count_kernel, grid, block, 0, s, a);
   if (e == cudaSuccess)
-    e = launch_behind(sort_kernel, grid, block, (size_t)kSortWarps * E * sizeof(int), s, a);
+    e = launch_behind(sort_kernel, grid, block, (size_t)(kSortWarps + 2) * E * sizeof(int), s, a);
   return launched(e);
 }
 
