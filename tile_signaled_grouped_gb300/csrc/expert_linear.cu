@@ -55,6 +55,30 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
 // two, meet no bank twice.
 __device__ __forceinline__ int patch_at(int r, int k) { return r * 64 + ((k ^ (r >> 1)) & 3) * 16; }
 
+// 16 lanes x 32 columns of TMEM as 8 x 8 pieces: of the columns 8 i .. a thread has, in v[4 i], v[4 i + 1], the
+// columns 2 (lane & 3) and the next of lane / 4, in the other two those of lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_pieces(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+// Four 8 x 8 pieces of 16 bits, each thread with two neighbours of a row as above, to or from shared memory
+// turned round: lane l's address is that of column l & 7 of piece l >> 3.
+__device__ __forceinline__ void store_turned(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+__device__ __forceinline__ void load_turned(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // An epilogue warp has read its part of an accumulator: its loads are complete (tcgen05.wait::ld) and nothing
 // else of it is the products' business, so the arrival orders no memory. (A release would wait for the warp's
 // stores to the outputs before it: 656 us where this takes 513, dW of 128 experts of 64 rows, 2048 x 4096.)
@@ -181,45 +205,68 @@ __device__ __forceinline__ Table make_table(const RowsArgs& a, int* at, int* scr
   return t;
 }
 
+// x / d for d = 1 .. 8 and x below 2^29: the product with 2^32 / d rounded up is off by less than x d.
+__constant__ uint32_t kInverse[9] = {0,          0,          0x80000000u, 0x55555556u, 0x40000000u,
+                                     0x33333334u, 0x2AAAAAABu, 0x24924925u, 0x20000000u};
+__device__ __forceinline__ int small_quotient(int x, int d) {
+  return d <= 1 ? x : (int)__umulhi((uint32_t)x, kInverse[d]);
+}
+
 // The tiles of a pair: p, p + pairs, ... of the order expert, feature tile, tile of rows, so that
-// tiles that share their weights are neighbours. Every role of both CTAs walks the same.
+// tiles that share their weights are neighbours. Every role of both CTAs walks the same, as whole warps:
+// with a search by one thread and five divisions a tile took each of them 1400 cycles, more than the
+// products of a short sum.
 struct RowWalk {
   const RowsArgs& a;
   const Table& t;
-  int at, pairs;
+  int tile, part;        // tile of rows among all experts', and the rest: the position is tile * tiles_j + part
+  int step_tile, step_part;
   int e, j0, row0, rows, cols;  // the tile: expert, first feature, first row, rows, rows rounded up
 
   __device__ __forceinline__ RowWalk(const RowsArgs& args, const Table& table, int pair, int n)
-      : a(args), t(table), at(pair - n), pairs(n), e(0), j0(0), row0(0), rows(0), cols(0) {}
+      : a(args), t(table), e(0), j0(0), row0(0), rows(0), cols(0) {
+    step_tile = n / a.tiles_j;
+    step_part = n - step_tile * a.tiles_j;
+    tile = pair / a.tiles_j - step_tile;
+    part = pair - pair / a.tiles_j * a.tiles_j - step_part;
+  }
   __device__ __forceinline__ bool next() {
+    const int lane = threadIdx.x & 31;
+    constexpr int kSpan = (kMaxExperts + 32) / 32;  // entries of a lane in the first of two steps: 33
     while (true) {
-      at += pairs;
-      const int tile = at / a.tiles_j;
-      if (tile >= t.tiles) return false;
-      int lo = 0, hi = a.E + 1;  // the last expert whose first tile is not past it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (t.first[mid] <= tile)
-          lo = mid;
-        else
-          hi = mid;
+      tile += step_tile;
+      part += step_part;
+      if (part >= a.tiles_j) {
+        part -= a.tiles_j;
+        ++tile;
       }
-      e = lo;
+      if (tile >= t.tiles) return false;
+      // The last expert whose first tile is not past it.
+      const bool at = lane * kSpan <= a.E && t.first[min(lane * kSpan, a.E)] <= tile;
+      const int base = (31 - __clz((int)(__ballot_sync(kAll, at) | 1u))) * kSpan, mine = base + 1 + lane;
+      const bool in = mine <= a.E && t.first[min(mine, a.E)] <= tile;
+      e = min(base + __popc(__ballot_sync(kAll, in)), a.E);
       // Groups of kGroup tiles of rows, inside a group feature by feature: the tiles in flight share their
       // operands in L2 (all tiles of rows of a feature tile first took 185 us where this takes 149 for 16384
-      // rows of one expert, 2048 x 4096).
-      const int tiles = (t.count[e] + kRows - 1) / kRows, local = at - t.first[e] * a.tiles_j;
-      const int g = local / (kGroup * a.tiles_j), r = local - g * kGroup * a.tiles_j;
-      const int in_group = max(min(kGroup, tiles - g * kGroup), 1), tj = r / in_group;
-      const int ti = g * kGroup + r - tj * in_group;
-      const int even = ((t.count[e] + tiles - 1) / max(tiles, 1) + kRowStep - 1) / kRowStep * kRowStep;
-      const int per = tiles > 8 ? kRows : even;  // of more than eight the last might be left without rows
+      // rows of one expert, 2048 x 4096). Up to kGroup tiles share an expert's rows evenly; of more the last
+      // might be left without any.
+      const int count = t.count[e], tiles = (count + kRows - 1) / kRows;
+      int local = (tile - t.first[e]) * a.tiles_j + part, from = 0, in_group = tiles, per = kRows;
+      if (tiles <= kGroup) {
+        per = (small_quotient(count + tiles - 1, tiles) + kRowStep - 1) / kRowStep * kRowStep;
+      } else {
+        const int g = local / (kGroup * a.tiles_j);
+        local -= g * kGroup * a.tiles_j;
+        from = g * kGroup;
+        in_group = min(kGroup, tiles - from);
+      }
+      const int tj = small_quotient(local, in_group), ti = from + local - tj * in_group;
       j0 = tj * kFeatures;
       row0 = t.start[e] + ti * per;
-      rows = min(per, t.count[e] - ti * per);
+      rows = min(per, count - ti * per);
       cols = (rows + kRowStep - 1) / kRowStep * kRowStep;
       // (Offsets that do not ascend may make more tiles than an int counts: no rows then.)
-      if (ti >= 0 && rows > 0) return true;
+      if (in_group > 0 && ti >= 0 && rows > 0) return true;
     }
   }
   __device__ __forceinline__ int steps() const { return e < a.E ? a.nk : 0; }
@@ -358,10 +405,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, a.status, 0x46000000u)) break;
       tc_fence_after();
       do {
-        uint32_t v[32];
+        uint32_t va[16], vb[16];  // the first 16 features and the others
         __syncwarp();  // the stores before may have parted it; the load wants it whole
         if (c < chunks) {
-          tmem_ld32(src + c * 32, v);
+          tmem_ld_pieces(src + c * 32, va);
+          tmem_ld_pieces(src + (16u << 16) + c * 32, vb);
           tmem_ld_wait();
         }
         if (c + 2 >= chunks) {  // the accumulator is read: it may be overwritten
@@ -380,18 +428,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (c + 2 < chunks) fetch(c + 2);
             __syncwarp();
           }
-          // (Two roundings in one instruction: conversions are what an epilogue is slow at.)
+          // Eight rows at a time, turned round as they are stored (element by element, 32 stores of 2 bytes,
+          // a chunk took 1050 cycles).
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            uint16_t* to = reinterpret_cast<uint16_t*>(patch + patch_at(x, lane >> 3)) + (lane & 7);
-            float lo = zero ? 0.f : __uint_as_float(v[x]), hi = zero ? 0.f : __uint_as_float(v[x + 1]);
-            if (a.add != nullptr) {  // row x + 1 lies 64 bytes on
-              lo += unpack2<T>(to[0]).x;
-              hi += unpack2<T>(to[32]).x;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t at = smem_u32(patch + patch_at(8 * i + (lane & 7), lane >> 3));
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (a.add != nullptr) load_turned(at, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t* v = (k < 2 ? va : vb) + 4 * i + 2 * (k & 1);
+              float lo = zero ? 0.f : __uint_as_float(v[0]), hi = zero ? 0.f : __uint_as_float(v[1]);
+              if (a.add != nullptr) {
+                const float2 f = unpack2<T>(w[k]);
+                lo += f.x;
+                hi += f.y;
+              }
+              w[k] = pack2<T>(lo, hi);
             }
-            const uint32_t w = pack2<T>(lo, hi);
-            to[0] = (uint16_t)w;
-            to[32] = (uint16_t)(w >> 16);
+            store_turned(at, w);
           }
           __syncwarp();
           const int f = (lane & 3) * 8;
@@ -425,17 +480,25 @@ struct WeightArgs {
 // write whole rows.
 struct WeightWalk {
   const WeightArgs& a;
-  int at, pairs;
+  int per, local, step_e, step_local;  // tiles of an expert; the position is e * per + local
   int e, i0, j0, start, count, steps;  // the expert's rows; blocks of 64 of them
 
   __device__ __forceinline__ WeightWalk(const WeightArgs& args, int pair, int n)
-      : a(args), at(pair - n), pairs(n), e(0), i0(0), j0(0), start(0), count(0), steps(0) {}
+      : a(args), per(a.tiles_i * a.tiles_j), i0(0), j0(0), start(0), count(0), steps(0) {
+    step_e = n / per;
+    step_local = n - step_e * per;
+    e = pair / per - step_e;
+    local = pair - pair / per * per - step_local;
+  }
   __device__ __forceinline__ bool next() {
-    at += pairs;
-    const int per = a.tiles_i * a.tiles_j;
-    e = at / per;
+    e += step_e;
+    local += step_local;
+    if (local >= per) {
+      local -= per;
+      ++e;
+    }
     if (e >= a.E) return false;
-    const int local = at - e * per, ti = local / a.tiles_j;
+    const int ti = local / a.tiles_j;
     i0 = ti * 256;
     j0 = (local - ti * a.tiles_j) * 256;
     rows_of(a.offsets, e, a.E, a.n, &start, &count);
