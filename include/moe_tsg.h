@@ -602,13 +602,17 @@ typedef struct moe_expert_linear_args {
 } moe_expert_linear_args;
 
 /* y[r] = w[e] x[r] for the rows of every expert e, fp32 sums, rounded once; rows from offsets[E] on
- * are zero. */
-int moe_expert_linear(const moe_expert_linear_args *args, moe_stream_t stream);
+ * are zero. workspace: at least moe_expert_linear_workspace(n, N, K, E) bytes (pure host arithmetic;
+ * 0 but for few rows and a long sum), 16-byte aligned, used until the call has run on the stream. */
+size_t moe_expert_linear_workspace(long long n, long long features, long long sum, int E);
+int moe_expert_linear(const moe_expert_linear_args *args, void *workspace, size_t workspace_bytes,
+                      moe_stream_t stream);
 
 /* dx[r] = w[e]^T dy[r] + add[r] (rows from offsets[E] on: add alone, or zero);
  * dw[e] = sum over its rows of dy[r] x[r]^T (zero without rows). fp32 sums in a fixed order, rounded
- * once. */
-int moe_expert_linear_backward(const moe_expert_linear_args *args, moe_stream_t stream);
+ * once. workspace: for dx, at least moe_expert_linear_workspace(n, K, N, E) bytes, as above. */
+int moe_expert_linear_backward(const moe_expert_linear_args *args, void *workspace,
+                               size_t workspace_bytes, moe_stream_t stream);
 
 /* The device waits of the products and of layer norm are bounded; one that runs out sets a
  * sticky status of the device (its results are void). Synchronises `stream` and reads the

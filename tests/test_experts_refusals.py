@@ -101,12 +101,24 @@ def test_expert_products_refuse():
             dict(dtype=capi.MOE_FP32), dict(offsets=None), dict(offsets=66), dict(w=None), dict(w=72), dict(ld_w=16),
             dict(ld_w=28), dict(stride_w=376), dict(stride_w=388), dict(x=None), dict(x=72), dict(ld_x=28), dict(ld_x=16))
     for bad in both + (dict(y=None), dict(y=72), dict(ld_y=8), dict(ld_y=20)):
-        assert lib.moe_expert_linear(args(capi.moe_expert_linear_args, **{**ok, **bad}), None) == ARG, bad
+        assert lib.moe_expert_linear(args(capi.moe_expert_linear_args, **{**ok, **bad}), None, 0, None) == ARG, bad
     for bad in both + (dict(dwtype=capi.MOE_FP16), dict(dy=None), dict(dy=72), dict(ld_dy=8), dict(dx=72), dict(ld_dx=20),
                        dict(dw=72), dict(ld_dw=28), dict(stride_dw=380), dict(add=72), dict(add=64, ld_add=16), dict(add=64, ld_add=28)):
-        assert lib.moe_expert_linear_backward(args(capi.moe_expert_linear_args, **{**ok, **bad}), None) == ARG, bad
-    assert lib.moe_expert_linear(args(capi.moe_expert_linear_args, **{**ok, "n": 0, "x": None}), None) == 0
-    assert lib.moe_expert_linear_backward(args(capi.moe_expert_linear_args, **{**ok, "n": 0, "dw": None}), None) == 0
+        assert lib.moe_expert_linear_backward(args(capi.moe_expert_linear_args, **{**ok, **bad}), None, 0, None) == ARG, bad
+    assert lib.moe_expert_linear(args(capi.moe_expert_linear_args, **{**ok, "n": 0, "x": None}), None, 0, None) == 0
+    assert lib.moe_expert_linear_backward(args(capi.moe_expert_linear_args, **{**ok, "n": 0, "dw": None}), None, 0,
+                                          None) == 0
+    # a long sum over few rows is shared out: parts of 4 bytes an element, up to eight
+    size = lib.moe_expert_linear_workspace
+    assert size(5, 16, 24, 3) == size(0, 16, 8192, 3) == size(8, 2048, 7168, 64) == 0
+    assert size(2, 256, 7168, 64) == 8 * 2 * 256 * 4 and size(5, 512, 2048, 3) == 4 * 5 * 512 * 4
+    need = size(5, 16, 8192, 3)
+    wide = {**ok, "K": 8192, "ld_x": 8192, "ld_w": 8192, "stride_w": 8192 * 16}
+    tall = {**ok, "N": 8192, "K": 16, "ld_y": 8192, "ld_dy": 8192, "stride_w": 24 * 8192, "dw": None}
+    for call, a in ((lib.moe_expert_linear, wide), (lib.moe_expert_linear_backward, tall)):
+        a = args(capi.moe_expert_linear_args, **a)
+        assert call(a, None, need, None) == call(a, 72, need, None) == ARG
+        assert call(a, 64, need - 1, None) == WORKSPACE
 
 
 def test_linear_refuses_checkpoints():

@@ -148,6 +148,11 @@ PRODUCTS = [
     ([17, 2, 90] * 40, 5, 72, 328, "fp16", 8),
     ([5] * 1024, 1, 16, 24, "bf16", 0),
     ([2500, 3, 100], 300, 304, 520, "bf16", 0),
+    # sums shared out over pairs, forward and (N large) in dx
+    ([1, 0, 1], 0, 256, 7168, "bf16", 0),
+    ([40, 0, 300], 9, 264, 2056, "fp16", 8),
+    ([3, 2], 1, 8192, 128, "bf16", 0),
+    ([700], 0, 4104, 136, "fp16", 0),
 ]
 
 

@@ -173,8 +173,9 @@ def load():
         "moe_restore": (ip, [P(moe_checkpoint_args), vp]),
         "moe_gated": (ip, [P(moe_gated_args), vp]),
         "moe_gated_backward": (ip, [P(moe_gated_args), vp]),
-        "moe_expert_linear": (ip, [P(moe_expert_linear_args), vp]),
-        "moe_expert_linear_backward": (ip, [P(moe_expert_linear_args), vp]),
+        "moe_expert_linear_workspace": (sz, [ll, ll, ll, ip]),
+        "moe_expert_linear": (ip, [P(moe_expert_linear_args), vp, sz, vp]),
+        "moe_expert_linear_backward": (ip, [P(moe_expert_linear_args), vp, sz, vp]),
         "moe_ops_status": (ip, [vp, P(ip), P(ip)]),
         "moe_ops_status_clear": (ip, [vp]),
         "moe_layer_norm": (ip, [P(moe_norm_args), vp]),

@@ -162,8 +162,10 @@ struct RowsArgs {
   long long ld_y, ld_add;
   uint32_t* status;
   int n, E, J, nk;     // J: features of y; nk: 64-element blocks of the sum
-  int tiles_j, stages;
+  int tiles_j, stages; // tiles_j: tiles of features times splits
   int most;            // tiles of rows at most
+  int split_bits;      // 2^split_bits pairs share a tile, each with a range of the sum
+  float* part;         // [splits][n][J], their sums, or null
   bool w_mn;           // W^T, whose features are innermost
 };
 constexpr int kBlocks = 2;  // of 64 k in a stage
@@ -222,9 +224,10 @@ struct RowWalk {
   int tile, part;        // tile of rows among all experts', and the rest: the position is tile * tiles_j + part
   int step_tile, step_part;
   int e, j0, row0, rows, cols;  // the tile: expert, first feature, first row, rows, rows rounded up
+  int split, k0, k1;            // which part of the sum, its blocks
 
   __device__ __forceinline__ RowWalk(const RowsArgs& args, const Table& table, int pair, int n)
-      : a(args), t(table), e(0), j0(0), row0(0), rows(0), cols(0) {
+      : a(args), t(table), e(0), j0(0), row0(0), rows(0), cols(0), split(0), k0(0), k1(0) {
     step_tile = n / a.tiles_j;
     step_part = n - step_tile * a.tiles_j;
     tile = pair / a.tiles_j - step_tile;
@@ -261,7 +264,10 @@ struct RowWalk {
         in_group = min(kGroup, tiles - from);
       }
       const int tj = small_quotient(local, in_group), ti = from + local - tj * in_group;
-      j0 = tj * kFeatures;
+      j0 = (tj >> a.split_bits) * kFeatures;
+      split = tj & ((1 << a.split_bits) - 1);
+      k0 = (int)((long long)a.nk * split >> a.split_bits);
+      k1 = (int)((long long)a.nk * (split + 1) >> a.split_bits);
       row0 = t.start[e] + ti * per;
       rows = min(per, count - ti * per);
       cols = (rows + kRowStep - 1) / kRowStep * kRowStep;
@@ -269,7 +275,7 @@ struct RowWalk {
       if (in_group > 0 && ti >= 0 && rows > 0) return true;
     }
   }
-  __device__ __forceinline__ int steps() const { return e < a.E ? a.nk : 0; }
+  __device__ __forceinline__ int steps() const { return e < a.E ? k1 - k0 : 0; }
 };
 
 template <typename T>
@@ -309,7 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int blocks = min(kBlocks, steps - kb);
           if (lead) mbar_arrive_expect_tx(&sm.full[st], blocks * bytes);
           const uint32_t fb = map_shared(&sm.full[st], 0);
-          for (int k0 = kb * kBlockK; k0 < (kb + blocks) * kBlockK; k0 += kBlockK, as += kBlockBytes) {
+          const int end = (walk.k0 + kb + blocks) * kBlockK;
+          for (int k0 = (walk.k0 + kb) * kBlockK; k0 < end; k0 += kBlockK, as += kBlockBytes) {
             uint8_t* bs = as + kABytes;
             if (a.w_mn) {
               tma_load_3d_pair(as, &a.tw, fb, j, k0, walk.e);
@@ -420,6 +427,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (c < chunks && nf > 0) {
           const long long r0 = walk.row0 + c * 32;
           const int rows = min(32, walk.rows - c * 32);
+          if (a.part != nullptr) {  // few rows: each thread its own sums, eight features together
+            float* to = a.part + ((long long)walk.split * a.n + r0) * a.J + f0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int f = (lane >> 2) + (i & 2 ? 8 : 0) + (i & 16), x = (i >> 2 & 3) * 8 + 2 * (lane & 3) + (i & 1);
+              const uint32_t v = i < 16 ? va[i & 15] : vb[i & 15];
+              if (x < rows && f < nf) to[(long long)x * a.J + f] = zero ? 0.f : __uint_as_float(v);
+            }
+            c += 2;
+            continue;
+          }
           __syncwarp();  // the patch's last readers
           if (a.add != nullptr) {
 #pragma unroll
@@ -464,6 +482,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pair_teardown(tmem, warp);
 }
 
+// The parts' sums of every element, in their order, with what is added, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) expert_join_kernel(const __grid_constant__ RowsArgs a) {
+  wait_prior_grid();
+  const long long per = a.J / 8, all = a.n * per;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+    const long long row = i / per, c = (i - row * per) * 8;
+    float f[8];
+    for (int s = 0; s < 1 << a.split_bits; ++s) {
+      const float4* q = reinterpret_cast<const float4*>(a.part + ((long long)s * a.n + row) * a.J + c);
+      const float4 u = q[0], v = q[1];
+      const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = s == 0 ? w[k] : f[k] + w[k];
+    }
+    if (a.add != nullptr) {
+      float g[8];
+      unpack<T>(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.add) + row * a.ld_add + c)), g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] += g[k];
+    }
+    *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.ld_y + c) = pack<T>(f);
+  }
+}
+
 // ------------------------------------------------------------------- dW
 struct WeightArgs {
   CUtensorMap ty, tx;  // rows of dy and of x
@@ -481,10 +524,11 @@ struct WeightArgs {
 struct WeightWalk {
   const WeightArgs& a;
   int per, local, step_e, step_local;  // tiles of an expert; the position is e * per + local
-  int e, i0, j0, start, count, steps;  // the expert's rows; blocks of 64 of them
+  int e, i0, j0, cols;      // the tile: expert, first row and column, columns: 256, or 128 at the right edge
+  int start, count, steps;  // the expert's rows; blocks of 64 of them
 
   __device__ __forceinline__ WeightWalk(const WeightArgs& args, int pair, int n)
-      : a(args), per(a.tiles_i * a.tiles_j), i0(0), j0(0), start(0), count(0), steps(0) {
+      : a(args), per(a.tiles_i * a.tiles_j), i0(0), j0(0), cols(0), start(0), count(0), steps(0) {
     step_e = n / per;
     step_local = n - step_e * per;
     e = pair / per - step_e;
@@ -501,6 +545,7 @@ struct WeightWalk {
     const int ti = local / a.tiles_j;
     i0 = ti * 256;
     j0 = (local - ti * a.tiles_j) * 256;
+    cols = a.K - j0 <= 128 ? 128 : 256;
     rows_of(a.offsets, e, a.E, a.n, &start, &count);
     steps = (count + kBlockK - 1) / kBlockK;
     return true;
@@ -530,7 +575,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
     uint32_t phase = 1;
     bool ok = true;
     while (ok && walk.next()) {
-      const int i = walk.i0 + (int)crank * 128, j = walk.j0 + (int)crank * 128;
+      const int half = walk.cols / 2, i = walk.i0 + (int)crank * 128, j = walk.j0 + (int)crank * half;
+      const uint32_t bytes = kABytes + half * 128;
       for (int kb = 0; kb < walk.steps; ++kb, ++n) {
         if (!warp_pwait(&sm.empty[st], phase, &sm.abort, a.status, 0x51000000u)) {
           ok = false;
@@ -542,11 +588,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
           const int row = walk.start + kb * kBlockK;
           uint32_t bar;
           if (walk.count - kb * kBlockK < kBlockK) {  // the warps that clear the rest fill this stage
-            mbar_arrive_expect_tx(&sm.last[st], kBlockBytes);
+            mbar_arrive_expect_tx(&sm.last[st], bytes);
             bar = map_shared(&sm.last[st], crank);
           } else {
             if (lead) {
-              mbar_arrive_expect_tx(&sm.full[st], 2 * kBlockBytes);
+              mbar_arrive_expect_tx(&sm.full[st], 2 * bytes);
               mbar_arrive(&sm.full[st]);
             }
             bar = map_shared(&sm.full[st], 0);
@@ -554,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
           tma_load_2d_pair(as, &a.ty, bar, i, row);
           tma_load_2d_pair(as + 8192, &a.ty, bar, i + 64, row);
           tma_load_2d_pair(bs, &a.tx, bar, j, row);
-          tma_load_2d_pair(bs + 8192, &a.tx, bar, j + 64, row);
+          if (half > 64) tma_load_2d_pair(bs + 8192, &a.tx, bar, j + 64, row);
         }
         __syncwarp();
         next_stage(st, phase, a.stages);
@@ -562,7 +608,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
     }
     wait_copies(sm, n, a.stages, a.status);
   } else if (warp == 1 && lead) {
-    const uint32_t idesc = idesc_16bit(kBf16, true, true, 256, 256);
     const uint32_t s0 = (smem_u32(base) & 0x3FFFFu) >> 4;
     const uint64_t da = sdesc_mn_sw128(0) + s0, db = da + (kABytes >> 4);
     int it = 0, st = 0;
@@ -573,7 +618,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
       const int acc = it & 1;
       if (!warp_pwait(&sm.tempty[acc], ((it >> 1) & 1) ^ 1, &sm.abort, a.status, 0x54000000u)) break;
       tc_fence_after();
-      const uint32_t dt = tmem + (uint32_t)(acc * 256);
+      const uint32_t dt = tmem + (uint32_t)(acc * 256), idesc = idesc_16bit(kBf16, true, true, 256, walk.cols);
       for (int kb = 0; kb < walk.steps; ++kb) {
         if (!warp_pwait(&sm.full[st], phase, &sm.abort, a.status, 0x55000000u)) {
           ok = false;
@@ -759,9 +804,29 @@ bool make_store_map(CUtensorMap* m, const moe_expert_linear_args* p) {
                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How many pairs share a tile's sum (as a power of two), where its tiles leave half of 76 pairs idle or more and each
+// gets eight blocks of 64 at least. Two rows of 256 features, a sum of 7168, eight parts: 9.2 us where one pair a
+// tile takes 24; of 512 features and 2048, four parts: 7.6 and 10; eight rows of 1024 and 7168, two: 26 and 31.
+// Sums below 32 blocks are left alone: the launch that joins the parts takes the 2 us that it saves.
+int split_bits(long long n, long long J, long long sum, int E) {
+  constexpr int kPairs = 76;
+  const long long most = n / kRows + std::min<long long>(E + 1, n), tiles = most * ((J + kFeatures - 1) / kFeatures);
+  const long long nk = (sum + kBlockK - 1) / kBlockK;
+  int bits = 0;
+  while (bits < 3 && nk >> (bits + 1) >= 8 && (tiles << (bits + 1)) <= kPairs) ++bits;
+  return nk >= 32 ? bits : 0;
+}
+
+int check_parts(const moe_expert_linear_args* p, long long features, long long sum, const void* workspace,
+                size_t bytes) {
+  const size_t need = moe_expert_linear_workspace(p->n, features, sum, p->E);
+  if (need > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return MOE_ERR_ARG;
+  return bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
 // y of the forward pass, or dx: `w_mn` takes W^T.
 int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x, bool w_mn, const void* add,
-                 long long ld_add, void* y, long long ld_y, int sms, cudaStream_t s) {
+                 long long ld_add, void* y, long long ld_y, int sms, void* workspace, cudaStream_t s) {
   RowsArgs a{};
   const bool bf16 = p->dtype == MOE_BF16;
   a.w_mn = w_mn;
@@ -770,7 +835,9 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   a.J = (int)(w_mn ? p->K : p->N);
   const long long sum = w_mn ? p->N : p->K;
   a.nk = (int)((sum + kBlockK - 1) / kBlockK);
-  a.tiles_j = (a.J + kFeatures - 1) / kFeatures;
+  a.split_bits = split_bits(p->n, a.J, sum, p->E);
+  a.tiles_j = (a.J + kFeatures - 1) / kFeatures << a.split_bits;
+  if (a.split_bits > 0) a.part = static_cast<float*>(workspace);
   a.offsets = p->offsets;
   a.y = y;
   a.ld_y = ld_y;
@@ -790,8 +857,12 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
   a.stages = stages_for(kStage, more);
   const unsigned pairs = (unsigned)std::min<long long>(sms / 2, tiles);
   const size_t smem = smem_bytes(a.stages * kStage, more);
-  return bf16 ? launch_pairs<expert_rows_product_kernel<__nv_bfloat16>>(pairs, kThreads, smem, s, a)
-              : launch_pairs<expert_rows_product_kernel<__half>>(pairs, kThreads, smem, s, a);
+  const int rc = bf16 ? launch_pairs<expert_rows_product_kernel<__nv_bfloat16>>(pairs, kThreads, smem, s, a)
+                      : launch_pairs<expert_rows_product_kernel<__half>>(pairs, kThreads, smem, s, a);
+  if (rc != MOE_OK || a.part == nullptr) return rc;
+  const dim3 grid((unsigned)std::min<long long>((p->n * (a.J / 8) + 255) / 256, 8 * sms));
+  return launched(bf16 ? launch_behind(expert_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a)
+                       : launch_behind(expert_join_kernel<__half>, grid, dim3(256), 0, s, a));
 }
 
 int weights_product(const moe_expert_linear_args* p, int sms, cudaStream_t s) {
@@ -832,20 +903,30 @@ using namespace moe;
 
 extern "C" {
 
-int moe_expert_linear(const moe_expert_linear_args* p, moe_stream_t stream) {
+size_t moe_expert_linear_workspace(long long n, long long features, long long sum, int E) {
+  if (n < 1 || features < 1 || sum < 1 || E < 1) return 0;
+  const int bits = split_bits(n, features, sum, E);
+  return bits == 0 ? 0 : ((size_t)n * features * sizeof(float)) << bits;
+}
+
+int moe_expert_linear(const moe_expert_linear_args* p, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   int rc = check_experts(p);
   if (rc != MOE_OK) return rc;
   if (p->n == 0) return MOE_OK;
   if (!check_matrix(p->x, p->ld_x, p->n, p->K) || !check_weights(p->w, p->ld_w, p->stride_w, p) ||
       !check_matrix(p->y, p->ld_y, p->n, p->N))
     return MOE_ERR_ARG;
+  rc = check_parts(p, p->N, p->K, workspace, workspace_bytes);
+  if (rc != MOE_OK) return rc;
   int sms = 0;
   rc = ops_device(&sms);
   if (rc != MOE_OK) return rc;
-  return rows_product(p, p->x, p->ld_x, false, nullptr, 0, p->y, p->ld_y, sms, reinterpret_cast<cudaStream_t>(stream));
+  return rows_product(p, p->x, p->ld_x, false, nullptr, 0, p->y, p->ld_y, sms, workspace,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
-int moe_expert_linear_backward(const moe_expert_linear_args* p, moe_stream_t stream) {
+int moe_expert_linear_backward(const moe_expert_linear_args* p, void* workspace, size_t workspace_bytes,
+                               moe_stream_t stream) {
   int rc = check_experts(p);
   if (rc != MOE_OK) return rc;
   if (p->dwtype != p->dtype && p->dwtype != MOE_FP32) return MOE_ERR_ARG;
@@ -869,10 +950,11 @@ int moe_expert_linear_backward(const moe_expert_linear_args* p, moe_stream_t str
                             (p->add != nullptr && !check_matrix(p->add, p->ld_add, p->n, p->K)))) ||
       (p->dw != nullptr && !check_matrix(p->x, p->ld_x, p->n, p->K)))
     return MOE_ERR_ARG;
+  if (p->dx != nullptr && (rc = check_parts(p, p->K, p->N, workspace, workspace_bytes)) != MOE_OK) return rc;
   rc = ops_device(&sms);
   if (rc != MOE_OK) return rc;
   if (p->dx != nullptr)
-    rc = rows_product(p, p->dy, p->ld_dy, true, p->add, p->ld_add, p->dx, p->ld_dx, sms, s);
+    rc = rows_product(p, p->dy, p->ld_dy, true, p->add, p->ld_add, p->dx, p->ld_dx, sms, workspace, s);
   if (rc == MOE_OK && p->dw != nullptr) rc = weights_product(p, sms, s);
   return rc;
 }

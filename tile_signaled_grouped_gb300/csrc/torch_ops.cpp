@@ -653,6 +653,18 @@ moe_expert_linear_args expert_args(const Experts& e, const Tensor& w, const Tens
   return a;
 }
 
+// A workspace of a call, which may need none.
+struct Scratch {
+  Tensor t;
+  void* p = nullptr;
+  size_t size;
+  Scratch(size_t bytes, const Tensor& x) : size(bytes) {
+    if (bytes == 0) return;
+    t = empty({(int64_t)bytes}, at::kByte, x);
+    p = t.data_ptr();
+  }
+};
+
 Tensor expert_linear(const Tensor& x, const Tensor& weight, const Tensor& offsets) {
   const int dt = checked_type(x, "x", true);
   const Experts e = expert_weights(weight, x, offsets);
@@ -664,7 +676,8 @@ Tensor expert_linear(const Tensor& x, const Tensor& weight, const Tensor& offset
   a.y = y.data_ptr();
   a.ld_x = r.ld;
   a.ld_y = e.N;
-  call("moe_expert_linear", [&] { return moe_expert_linear(&a, l.stream); });
+  const Scratch work(moe_expert_linear_workspace(a.n, a.N, a.K, a.E), x);
+  call("moe_expert_linear", [&] { return moe_expert_linear(&a, work.p, work.size, l.stream); });
   return y;
 }
 
@@ -707,7 +720,9 @@ std::tuple<OptTensor, OptTensor> expert_linear_backward(const Tensor& dy, const 
   a.ld_add = ra.ld;
   a.ld_dx = a.ld_dw = e.K;
   a.stride_dw = e.N * e.K;
-  call("moe_expert_linear_backward", [&] { return moe_expert_linear_backward(&a, l.stream); });
+  const Scratch work(need_dx ? moe_expert_linear_workspace(a.n, a.K, a.N, a.E) : 0, x);
+  call("moe_expert_linear_backward",
+       [&] { return moe_expert_linear_backward(&a, work.p, work.size, l.stream); });
   return {dx, dw};
 }
 
