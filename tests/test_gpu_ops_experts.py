@@ -71,6 +71,9 @@ ROWS = [
     (37, 11, 3, 70, "fp16", 3, True), (64, 8, 2, 128, "bf16", 0, False), (129, 40, 32, 40, "bf16", 8, True),
     (200, 16, 5, 1000, "fp32", 0, True), (1001, 120, 6, 1531, "fp16", 5, True), (333, 7, 2, 2056, "fp32", 4, False),
     (777, 128, 8, 4096, "bf16", 0, True), (64, 16, 9, 520, "bf16", 0, True),
+    # few rows a token, by several vectors of each
+    (900, 5, 1, 2056, "bf16", 0, True), (3000, 6, 2, 264, "fp16", 0, True), (500, 7, 3, 1032, "fp32", 0, False),
+    (600, 9, 4, 1001, "fp16", 0, True), (700, 8, 1, 4765, "bf16", 0, False), (300, 30, 4, 1537, "fp32", 2, True),
 ]
 
 

@@ -275,12 +275,12 @@ struct Kept {
   static constexpr int N = Vec<T>::kN;
   typename std::conditional<EIGHT, Codes<N, false>, RowVec<T, false>>::type u;
   uint8_t scale;
-  __device__ __forceinline__ void load(const RowsArgs& a, long long row, int c) {
+  __device__ __forceinline__ void load(const RowsArgs& a, long long row, int c, long long width) {
     if constexpr (EIGHT) {
-      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, c, c + N);
-      scale = __ldg(a.scales + row * a.ld_s + c / kScaleBlock);
+      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, c, width);
+      scale = c < width ? __ldg(a.scales + row * a.ld_s + c / kScaleBlock) : 0;
     } else {
-      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, c + N);
+      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, width);
     }
   }
   __device__ __forceinline__ void get(int, long long, float (&f)[N]) const {
@@ -295,11 +295,11 @@ template <typename T, bool EIGHT>
 struct KeptWord {
   static constexpr int N = RowWord<T>::N;
   typename std::conditional<EIGHT, CodeWord<N>, RowWord<T>>::type u;
-  __device__ __forceinline__ void load(const RowsArgs& a, long long row, int c) {
+  __device__ __forceinline__ void load(const RowsArgs& a, long long row, int c, long long width) {
     if constexpr (EIGHT)
-      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, a.scales + row * a.ld_s, c, a.D);
+      u.load(static_cast<const uint8_t*>(a.r) + row * a.ld_r, a.scales + row * a.ld_s, c, width);
     else
-      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, a.D);
+      u.load(static_cast<const T*>(a.r) + row * a.ld_r, c, width);
   }
   __device__ __forceinline__ void get(int c, long long width, float (&f)[N]) const { u.get(c, width, f); }
 };
@@ -307,26 +307,29 @@ struct KeptWord {
 // Gradients of the rows and weights. A CTA takes one token, its warps walk the row together: a
 // vector of dy meets those of eight rows, which it is multiplied into (dw) and, times the weight,
 // written to (dr). The warps' partial products are added in their order. EIGHT: the rows kept are codes.
-// Bound by the bytes of the rows: all eight loads leave before the first is used, and three CTAs
-// of eight warps fit on an SM (as fp32 the eight vectors took 121 registers, and 328 us where this takes
+// Bound by the bytes of the rows: all eight loads leave before the first is used, and 24 warps
+// fit on an SM (as fp32 the eight vectors took 121 registers, and 328 us where this takes
 // 126 for 4096 tokens of 8 x 7168 from codes). ANY: rows that start anywhere go by words (8192 tokens of
-// 8 x 2049 take 211 us so, and 261 by vectors shifted together). DY_ANY: dy's alone do.
-constexpr int kBackSlots = 8;
-template <typename T, bool EIGHT, bool ANY, bool DY_ANY>
-__global__ void __launch_bounds__(256, 3) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
-  constexpr int N = ANY ? RowWord<T>::N : Vec<T>::kN, kSpan = 32 * N;
-  __shared__ float part[8][kBackSlots];
+// 8 x 2049 take 208 us so, and 261 by vectors shifted together). DY_ANY: dy's alone start anywhere.
+// SLOTS: rows at a time, and 8 / SLOTS vectors of each: of one, two or four rows a token as many loads are in
+// flight as of eight (4096 x 1 x 7168 33 us by two rows, 51 by eight; 7273 x 1 x 6841 109 by four and 226;
+// 8192 x 4 x 2048 from codes 40 by four, 48 by eight or two).
+constexpr int kBackLoads = 8, kBackWarps = 24;
+template <typename T, bool EIGHT, bool ANY, bool DY_ANY, int SLOTS>
+__global__ void __launch_bounds__(32 * kBackWarps, 1) combine_backward_kernel(const __grid_constant__ RowsArgs a) {
+  constexpr int N = ANY ? RowWord<T>::N : Vec<T>::kN, kUnits = kBackLoads / SLOTS, kSpan = 32 * N * kUnits;
+  __shared__ float part[kBackWarps][SLOTS];
   allow_dependent_launch();
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   T* dr = static_cast<T*>(a.dr);
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const T* dy = static_cast<const T*>(a.x) + t * a.ld_x;
-    for (int j0 = 0; j0 < a.topk; j0 += kBackSlots) {
-      int row[kBackSlots];
-      float w[kBackSlots], dot[kBackSlots];
+    for (int j0 = 0; j0 < a.topk; j0 += SLOTS) {
+      int row[SLOTS];
+      float w[SLOTS], dot[SLOTS];
 #pragma unroll
-      for (int j = 0; j < kBackSlots; ++j) {
+      for (int j = 0; j < SLOTS; ++j) {
         const bool in = j0 + j < a.topk;
         row[j] = in ? row_of(a, t * a.topk + j0 + j) : -1;
         w[j] = in ? __ldg(a.w + t * a.topk + j0 + j) : 0.f;
@@ -335,39 +338,51 @@ __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const __grid_c
       for (int c0 = warp * kSpan; c0 < a.D; c0 += warps * kSpan) {
         const int c = c0 + lane * N;
         if (!ANY && c >= a.D) break;
-        typename std::conditional<ANY, KeptWord<T, EIGHT>, Kept<T, EIGHT>>::type v[kBackSlots];
-        typename std::conditional<ANY, RowWord<T>, RowVec<T, DY_ANY>>::type x;
-        x.load(dy, c, ANY || DY_ANY ? a.D : c + N);  // without ANY, c is inside
+        typename std::conditional<ANY, KeptWord<T, EIGHT>, Kept<T, EIGHT>>::type v[SLOTS][kUnits];
+        typename std::conditional<ANY, RowWord<T>, RowVec<T, DY_ANY>>::type x[kUnits];
 #pragma unroll
-        for (int j = 0; j < kBackSlots; ++j)
-          if (row[j] >= 0) v[j].load(a, row[j], c);
-        float d[N];
-        if constexpr (ANY)
-          x.get(c, a.D, d);
-        else
-          x.get(d);
+        for (int i = 0; i < kUnits; ++i)
+          x[i].load(dy, c + 32 * N * i, ANY || DY_ANY || kUnits > 1 ? a.D : c + N);  // else c is inside
 #pragma unroll
-        for (int j = 0; j < kBackSlots; ++j) {
+        for (int j = 0; j < SLOTS; ++j) {
           if (row[j] < 0) continue;
-          float f[N];
-          v[j].get(c, a.D, f);
 #pragma unroll
-          for (int q = 0; q < N; ++q) dot[j] = fmaf(d[q], f[q], dot[j]);
+          for (int i = 0; i < kUnits; ++i) v[j][i].load(a, row[j], c + 32 * N * i, ANY || kUnits > 1 ? a.D : c + N);
+        }
+        float d[kUnits][N];
 #pragma unroll
-          for (int q = 0; q < N; ++q) f[q] = w[j] * d[q];
+        for (int i = 0; i < kUnits; ++i) {
           if constexpr (ANY)
-            store_word_any(dr + row[j] * a.ld_d, c, a.D, pack_word<T>(f), lane);
+            x[i].get(c + 32 * N * i, a.D, d[i]);
           else
-            store_vec<false>(dr + row[j] * a.ld_d, c, c + N, f, lane);
+            x[i].get(d[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+          if (row[j] < 0) continue;
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int ci = c + 32 * N * i;
+            float f[N];
+            v[j][i].get(ci, a.D, f);
+#pragma unroll
+            for (int q = 0; q < N; ++q) dot[j] = fmaf(d[i][q], f[q], dot[j]);
+#pragma unroll
+            for (int q = 0; q < N; ++q) f[q] = w[j] * d[i][q];
+            if constexpr (ANY)
+              store_word_any(dr + row[j] * a.ld_d, ci, a.D, pack_word<T>(f), lane);
+            else
+              store_vec<false>(dr + row[j] * a.ld_d, ci, kUnits > 1 ? a.D : ci + N, f, lane);
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < kBackSlots; ++j) {
+      for (int j = 0; j < SLOTS; ++j) {
         dot[j] = warp_sum(dot[j]);
         if (lane == 0) part[warp][j] = dot[j];
       }
       __syncthreads();
-      if (threadIdx.x < kBackSlots && j0 + (int)threadIdx.x < a.topk) {
+      if (threadIdx.x < SLOTS && j0 + (int)threadIdx.x < a.topk) {
         float s = 0.f;
         for (int v = 0; v < warps; ++v) s += part[v][threadIdx.x];
         a.dw[t * a.topk + j0 + threadIdx.x] = s;
@@ -436,19 +451,27 @@ int launch_combine(const RowsArgs& a, bool vec, cudaStream_t s) {
 }
 
 template <typename T>
-int launch_backward(const RowsArgs& a, bool vec, bool dy, cudaStream_t s) {
-  // Warps of a token: four vectors of a lane each, eight warps at most.
+int launch_backward(const RowsArgs& a, bool vec, bool dy, int sms, cudaStream_t s) {
+  // Warps of a token: four vectors of a lane each, eight warps at most; where the tokens then leave room on
+  // the SMs, as many more as fill it.
   const long long width = a.D / (vec ? Vec<T>::kN : RowWord<T>::N);
-  const unsigned warps = (unsigned)std::min<long long>(8, std::max<long long>(1, width / 128));
-  const dim3 grid((unsigned)std::min<long long>(a.T, 1 << 20)), block(32 * warps);
+  const long long few = std::min<long long>(8, std::max<long long>(1, width / 128));
+  const long long fill = std::min<long long>({kBackWarps, (long long)kBackWarps * sms / a.T, (width + 31) / 32});
+  const dim3 grid((unsigned)std::min<long long>(a.T, 1 << 20)), block(32 * (unsigned)std::max(few, fill));
   auto go = [&](auto* kernel) { return launched(launch_behind(kernel, grid, block, 0, s, a)); };
-  if (a.scales != nullptr)
-    return !vec ? go(combine_backward_kernel<T, true, true, false>)
-           : dy ? go(combine_backward_kernel<T, true, false, false>)
-                : go(combine_backward_kernel<T, true, false, true>);
-  return !vec ? go(combine_backward_kernel<T, false, true, false>)
-         : dy ? go(combine_backward_kernel<T, false, false, false>)
-              : go(combine_backward_kernel<T, false, false, true>);
+  auto slots = [&](auto n) {
+    constexpr int N = decltype(n)::value, kAny = std::max(N, 4);
+    if (a.scales != nullptr)
+      return !vec ? go(combine_backward_kernel<T, true, true, false, kAny>)
+             : dy ? go(combine_backward_kernel<T, true, false, false, N>)
+                  : go(combine_backward_kernel<T, true, false, true, N>);
+    return !vec ? go(combine_backward_kernel<T, false, true, false, kAny>)
+           : dy ? go(combine_backward_kernel<T, false, false, false, N>)
+                : go(combine_backward_kernel<T, false, false, true, N>);
+  };
+  return a.topk <= 2   ? slots(std::integral_constant<int, 2>{})
+         : a.topk <= 4 ? slots(std::integral_constant<int, 4>{})
+                       : slots(std::integral_constant<int, kBackLoads>{});
 }
 
 // Slots of a lane, so that there are at most kSortChunks chunks.
@@ -569,9 +592,9 @@ int moe_combine_experts_backward(const moe_rows_args* p, moe_stream_t stream) {
   const bool vec = p->D * b % 16 == 0 && vector_rows(p->dr, p->ld_dr, n, b, 16) &&
                    vector_rows(p->r, p->ld_r, n, kb, 16 / b * kb);
   const bool dy = vector_rows(p->x, p->ld_x, p->T, b, 16);
-  return p->dtype == MOE_FP32   ? launch_backward<float>(a, vec, dy, s)
-         : p->dtype == MOE_BF16 ? launch_backward<__nv_bfloat16>(a, vec, dy, s)
-                                : launch_backward<__half>(a, vec, dy, s);
+  return p->dtype == MOE_FP32   ? launch_backward<float>(a, vec, dy, sms, s)
+         : p->dtype == MOE_BF16 ? launch_backward<__nv_bfloat16>(a, vec, dy, sms, s)
+                                : launch_backward<__half>(a, vec, dy, sms, s);
 }
 
 }  // extern "C"
