@@ -278,6 +278,10 @@ struct RowWalk {
   __device__ __forceinline__ int steps() const { return e < a.E ? k1 - k0 : 0; }
 };
 
+// y = W x or dx = W^T dy + add. Bound by the weights' bytes for few rows of an expert (8 rows of 8 experts,
+// 2048 x 7168: 42 us, 5.5 TB/s), by the products for many (8192 rows of 8, 8192 x 2048: 158 us, 1.74 PFLOP/s),
+// and between the two by what crosses between the dies (32768 uneven rows of 128, 2048 x 4096: 465 to 505 us,
+// 5.0 to 5.2 TB/s cross).
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_rows_product_kernel(const __grid_constant__ RowsArgs a) {
@@ -552,7 +556,11 @@ struct WeightWalk {
   }
 };
 
-// T: the operands' type; O: dW's, T or float.
+// dW[e] = sum over the rows of e of dy[r] x[r]^T: both operands lie row by row, so both go to the tensor cores with
+// the sum outermost, 64 rows at a time. With few rows of many experts it is bound by what it writes, dW once
+// (64 experts of 4 rows, 2048 x 4096: 195 us, 5.5 TB/s; 128 of 32: 375, 5.9; 5 of 64 with rows: 171, 6.3), with
+// many by the products (16384 rows of one, 2048 x 4096: 154 us, 1.78 PFLOP/s). No split of the sum: a pair's tile
+// takes all rows of its expert. T: the operands' type; O: dW's, T or float.
 template <typename T, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
     expert_weights_kernel(const __grid_constant__ WeightArgs a) {
@@ -656,7 +664,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
       uint8_t* at = base + (size_t)st * kBlockBytes;
       for (int o = rows * 128 + lane * 16; o < 8192; o += 512) {
 #pragma unroll
-        for (int b = 0; b < kBlockBytes / 8192; ++b) *reinterpret_cast<uint4*>(at + b * 8192 + o) = make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < kBlockBytes / 8192; ++b)
+          *reinterpret_cast<uint4*>(at + b * 8192 + o) = make_uint4(0, 0, 0, 0);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the products read by the async proxy
       __syncwarp();
@@ -696,8 +705,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_read(tempty[acc]);
         }
-        // Rows of 64 bytes, turned round in shared memory so that four lanes store a row's: such stores
-        // write 6.6 TB/s here, rows of one lane each 4.9 in 32 bytes and 2.6 in 16.
+        // 32 rows of 64 bytes by way of shared memory, from which a copy takes them (dW of 128 experts of 128
+        // rows, 2048 x 4096: 441 us; stored by the lanes, four of them a row, 463; of 64 experts of 4 rows 197
+        // and 232).
         constexpr int kPart = 64 / (int)sizeof(O);  // columns of 64 bytes
 #pragma unroll
         for (int h = 0; h < 32; h += kPart) {
