@@ -218,6 +218,34 @@ def test_whole_numbers_are_exact(case):
     assert int(offsets[-1]) == total
 
 
+def test_shared_sums_replayed_beside_other_calls():
+    """A sum that pairs share has its parts in a workspace of its call: a captured call, replayed on new values
+    between calls on another stream, gives what each alone gives, bit by bit."""
+    offsets, n, x, weight, dy, _ = experts_case(([2, 0, 3, 1], 2, 256, 4096, "bf16", 0))
+    other = experts_case(([1, 1, 1, 1], 0, 256, 4096, "bf16", 0))
+    want_other = ops.expert_linear(other[2], other[3], other[0])
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    ops.expert_linear(x, weight, offsets)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = ops.expert_linear(x, weight, offsets)
+        dx, _ = ops.expert_linear_backward(x, None, weight.transpose(1, 2).contiguous(), offsets, need_dw=False)
+    g = gen(77)
+    for counts in ([2, 0, 3, 1], [0, 0, 0, 0], [8, 0, 0, 0], [1, 1, 4, 2]):
+        x.copy_(matrix(g, n, 4096, "bf16"))
+        offsets.copy_(torch.tensor([0] + counts, device="cuda").cumsum(0).int())
+        want = ops.expert_linear(x, weight, offsets)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            got_other = [ops.expert_linear(other[2], other[3], other[0]) for _ in range(3)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and (y[sum(counts):] == 0).all()
+        assert torch.equal(dx, want)  # the same product, by the weights the other way round
+        assert all(torch.equal(o, want_other) for o in got_other)
+
+
 def test_bad_rows_stay_in_their_expert():
     """NaN and infinities of one expert's rows reach neither another's rows nor its weights' gradient."""
     case = ([70, 3, 65, 130], 0, 200, 136, "bf16", 0)
