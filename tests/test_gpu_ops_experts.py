@@ -156,6 +156,8 @@ PRODUCTS = [
     ([40, 0, 300], 9, 264, 2056, "fp16", 8),
     ([3, 2], 1, 8192, 128, "bf16", 0),
     ([700], 0, 4104, 136, "fp16", 0),
+    # dW in fp32 by parts of the rows, the last whole or of one row
+    ([1536, 0, 769, 768, 2048], 3, 264, 136, "bf16", 0),
 ]
 
 

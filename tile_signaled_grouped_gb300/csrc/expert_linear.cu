@@ -93,6 +93,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // An expert's rows: whatever the offsets hold, inside 0 .. n.
 __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int E, int n, int* start, int* count) {
   const int lo = min(max(__ldg(offsets + e), 0), n);
@@ -523,22 +530,45 @@ struct WeightArgs {
   int tiles_i, tiles_j, stages;
 };
 
+// The tensor cores' fp32 sums lose what lies below their last bit at every step, so their error grows with the
+// number of rows: relative to dW 2.3e-7 for 256, 1.0e-6 for 1024, 9e-6 for 8192, 3.8e-5 for 32768. An fp32 dW
+// therefore takes a tile's rows in parts, which are added to what is stored by copies that add (fp32, rounded to
+// nearest, one after the other): 7e-7 for any number. (16384 rows, 2048 x 4096: 157 us in one part, 223 by parts
+// of 1024, 255 by 768, 313 by 512.) In 16 bits the rounding of dW is a thousand times as much: one part.
+constexpr int kPartRows = 768;
+
 // The tiles of a pair: p, p + pairs, ... of the order expert, rows, columns of dW: the tiles in flight
-// write whole rows.
+// write whole rows. PART: rows of a sum that the tensor cores take at once; the parts of a tile come one after
+// the other.
+template <int PART>
 struct WeightWalk {
   const WeightArgs& a;
   int per, local, step_e, step_local;  // tiles of an expert; the position is e * per + local
   int e, i0, j0, cols;      // the tile: expert, first row and column, columns: 256, or 128 at the right edge
-  int start, count, steps;  // the expert's rows; blocks of 64 of them
+  int start, count, steps;  // the expert's rows, or a part of them; blocks of 64 of them
+  int left;                 // rows of the parts after it
+  bool more;                // a part after the first
 
   __device__ __forceinline__ WeightWalk(const WeightArgs& args, int pair, int n)
-      : a(args), per(a.tiles_i * a.tiles_j), i0(0), j0(0), cols(0), start(0), count(0), steps(0) {
+      : a(args), per(a.tiles_i * a.tiles_j), i0(0), j0(0), cols(0), start(0), count(0), steps(0), left(0), more(false) {
     step_e = n / per;
     step_local = n - step_e * per;
     e = pair / per - step_e;
     local = pair - pair / per * per - step_local;
   }
+  __device__ __forceinline__ void take() {
+    left = max(count - PART, 0);
+    count = min(count, PART);
+    steps = (count + kBlockK - 1) / kBlockK;
+  }
   __device__ __forceinline__ bool next() {
+    more = left > 0;
+    if (more) {
+      start += count;
+      count = left;
+      take();
+      return true;
+    }
     e += step_e;
     local += step_local;
     if (local >= per) {
@@ -551,7 +581,7 @@ struct WeightWalk {
     j0 = (local - ti * a.tiles_j) * 256;
     cols = a.K - j0 <= 128 ? 128 : 256;
     rows_of(a.offsets, e, a.E, a.n, &start, &count);
-    steps = (count + kBlockK - 1) / kBlockK;
+    take();
     return true;
   }
 };
@@ -559,8 +589,8 @@ struct WeightWalk {
 // dW[e] = sum over the rows of e of dy[r] x[r]^T: both operands lie row by row, so both go to the tensor cores with
 // the sum outermost, 64 rows at a time. With few rows of many experts it is bound by what it writes, dW once
 // (64 experts of 4 rows, 2048 x 4096: 195 us, 5.5 TB/s; 128 of 32: 375, 5.9; 5 of 64 with rows: 171, 6.3), with
-// many by the products (16384 rows of one, 2048 x 4096: 154 us, 1.78 PFLOP/s). No split of the sum: a pair's tile
-// takes all rows of its expert. T: the operands' type; O: dW's, T or float.
+// many by the products (16384 rows of one, 2048 x 4096: 154 us, 1.78 PFLOP/s). A pair's tile takes all rows
+// of its expert, for an fp32 dW in parts (kPartRows). T: the operands' type; O: dW's, T or float.
 template <typename T, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
     expert_weights_kernel(const __grid_constant__ WeightArgs a) {
@@ -576,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
   pair_setup(sm, a.stages, warp, 2, kWeightEpiWarps);
   const uint32_t tmem = sm.tmem;
   wait_prior_grid();
-  WeightWalk walk(a, blockIdx.x >> 1, gridDim.x >> 1);
+  WeightWalk<sizeof(O) == 4 ? kPartRows : INT32_MAX> walk(a, blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
     int n = 0, st = 0;
@@ -693,6 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
       if (!warp_pwait(&sm.tfull[acc], (it >> 1) & 1, &sm.abort, a.status, 0x56000000u)) break;
       ++it;
       tc_fence_after();
+      if (walk.more && lane == 0) bulk_wait_all();  // what is added to has been written
       const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
 #pragma unroll 1
       for (int c = from; c < from + kColumns; c += 32) {
@@ -729,7 +760,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWeightThreads, 1)
           __syncwarp();
           const int j = walk.j0 + c + h;
           if (rows > 0 && j < a.K && lane == 0) {
-            tma_store_3d(&a.tw, patch, j, i, walk.e);
+            if (sizeof(O) == 4 && walk.more)
+              tma_add_3d(&a.tw, patch, j, i, walk.e);
+            else
+              tma_store_3d(&a.tw, patch, j, i, walk.e);
             bulk_commit();
           }
         }
