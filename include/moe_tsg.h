@@ -601,14 +601,14 @@ typedef struct moe_expert_linear_args {
   long long ld_x, ld_w, stride_w, ld_y, ld_dy, ld_add, ld_dx, ld_dw, stride_dw;
 } moe_expert_linear_args;
 
-/* y[r] = w[e] x[r] for the rows of every expert e, fp32 sums, rounded once; rows from offsets[E] on
- * are zero. workspace: at least moe_expert_linear_workspace(n, N, K, E) bytes (pure host arithmetic;
+/* y[r] = w[e] x[r] for the rows of every expert e, fp32 sums, rounded once; rows before offsets[0] and
+ * from offsets[E] on are zero. workspace: at least moe_expert_linear_workspace(n, N, K, E) bytes (pure host arithmetic;
  * 0 but for few rows and a long sum), 16-byte aligned, used until the call has run on the stream. */
 size_t moe_expert_linear_workspace(long long n, long long features, long long sum, int E);
 int moe_expert_linear(const moe_expert_linear_args *args, void *workspace, size_t workspace_bytes,
                       moe_stream_t stream);
 
-/* dx[r] = w[e]^T dy[r] + add[r] (rows from offsets[E] on: add alone, or zero);
+/* dx[r] = w[e]^T dy[r] + add[r] (rows before offsets[0] and from offsets[E] on: add alone, or zero);
  * dw[e] = sum over its rows of dy[r] x[r]^T (zero without rows). fp32 sums in a fixed order, rounded
  * once. workspace: for dx, at least moe_expert_linear_workspace(n, K, N, E) bytes, as above. */
 int moe_expert_linear_backward(const moe_expert_linear_args *args, void *workspace,

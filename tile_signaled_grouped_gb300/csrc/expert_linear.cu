@@ -100,10 +100,11 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* s
                : "memory");
 }
 
-// An expert's rows: whatever the offsets hold, inside 0 .. n.
+// The rows of expert e, whatever the offsets hold inside 0 .. n; as e = E those behind the last expert's, as
+// E + 1 those before the first's.
 __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int E, int n, int* start, int* count) {
-  const int lo = min(max(__ldg(offsets + e), 0), n);
-  const int hi = e < E ? min(max(__ldg(offsets + e + 1), lo), n) : n;
+  const int lo = e <= E ? min(max(__ldg(offsets + e), 0), n) : 0;
+  const int hi = e < E ? min(max(__ldg(offsets + e + 1), lo), n) : e == E ? n : min(max(__ldg(offsets), 0), n);
   *start = lo;
   *count = hi - lo;
 }
@@ -177,23 +178,23 @@ struct RowsArgs {
 };
 constexpr int kBlocks = 2;  // of 64 k in a stage
 
-// The table of the experts' rows in shared memory, entry E for the rows behind the last expert's
-// (zeros): first row, number, and the tiles of rows before it. An expert's rows are shared out evenly
-// over its tiles.
+// The table of the experts' rows in shared memory, entries E and E + 1 for the rows behind the last
+// expert's and before the first's (zeros): first row, number, and the tiles of rows before it. An
+// expert's rows are shared out evenly over its tiles.
 struct Table {
   int *start, *count, *first;
   int tiles;  // of rows, all of them
 };
-__host__ __device__ constexpr size_t table_bytes(int E) { return (size_t)(3 * (E + 1) + 3) / 4 * 16; }
+__host__ __device__ constexpr size_t table_bytes(int E) { return (size_t)(3 * (E + 2) + 3) / 4 * 16; }
 __device__ __forceinline__ Table make_table(const RowsArgs& a, int* at, int* scratch) {
-  Table t{at, at + a.E + 1, at + 2 * (a.E + 1), 0};
-  constexpr int kEach = (kMaxExperts + kThreads) / kThreads;  // neighbouring entries a thread
+  Table t{at, at + a.E + 2, at + 2 * (a.E + 2), 0};
+  constexpr int kEach = (kMaxExperts + 1 + kThreads) / kThreads;  // neighbouring entries a thread
   int tiles[kEach], sum = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x * kEach + i;
     tiles[i] = 0;
-    if (e <= a.E) {
+    if (e <= a.E + 1) {
       int start, count;
       rows_of(a.offsets, e, a.E, a.n, &start, &count);
       t.start[e] = start;
@@ -206,7 +207,7 @@ __device__ __forceinline__ Table make_table(const RowsArgs& a, int* at, int* scr
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x * kEach + i;
-    if (e <= a.E) t.first[e] = at_tile;
+    if (e <= a.E + 1) t.first[e] = at_tile;
     at_tile += tiles[i];
   }
   t.tiles = min(t.tiles, a.most);
@@ -242,7 +243,7 @@ struct RowWalk {
   }
   __device__ __forceinline__ bool next() {
     const int lane = threadIdx.x & 31;
-    constexpr int kSpan = (kMaxExperts + 32) / 32;  // entries of a lane in the first of two steps: 33
+    constexpr int kSpan = (kMaxExperts + 1 + 32) / 32;  // entries of a lane in the first of two steps: 33
     while (true) {
       tile += step_tile;
       part += step_part;
@@ -252,10 +253,11 @@ struct RowWalk {
       }
       if (tile >= t.tiles) return false;
       // The last expert whose first tile is not past it.
-      const bool at = lane * kSpan <= a.E && t.first[min(lane * kSpan, a.E)] <= tile;
+      const int last = a.E + 1;
+      const bool at = lane * kSpan <= last && t.first[min(lane * kSpan, last)] <= tile;
       const int base = (31 - __clz((int)(__ballot_sync(kAll, at) | 1u))) * kSpan, mine = base + 1 + lane;
-      const bool in = mine <= a.E && t.first[min(mine, a.E)] <= tile;
-      e = min(base + __popc(__ballot_sync(kAll, in)), a.E);
+      const bool in = mine <= last && t.first[min(mine, last)] <= tile;
+      e = min(base + __popc(__ballot_sync(kAll, in)), last);
       // Groups of kGroup tiles of rows, inside a group feature by feature: the tiles in flight share their
       // operands in L2 (all tiles of rows of a feature tile first took 185 us where this takes 149 for 16384
       // rows of one expert, 2048 x 4096). Up to kGroup tiles share an expert's rows evenly; of more the last
@@ -405,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int f0 = walk.j0 + (int)crank * 128 + q * 32, nf = a.J - f0;
       const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kRows);
       const int chunks = (walk.rows + 31) / 32;
-      const bool zero = walk.e == a.E;
+      const bool zero = walk.e >= a.E;
       int c = half;
       // What is added to 32 rows, as it is stored: four lanes a row. On its way before the sums are waited for.
       uint4 u[4];
@@ -892,8 +894,8 @@ int rows_product(const moe_expert_linear_args* p, const void* x, long long ld_x,
     return MOE_ERR_CUDA;
   for (int b = 0; b < 4; ++b)
     if (!make_map(&a.tx[b], x, bf16, 0, p->n, sum, ld_x, 0, 16 << b)) return MOE_ERR_CUDA;
-  // Tiles of rows: one for every 256 and one more for each expert at most.
-  a.most = (int)(p->n / kRows + std::min<long long>(p->E + 1, p->n));
+  // Tiles of rows: one for every 256 and one more for each entry of the table at most.
+  a.most = (int)(p->n / kRows + std::min<long long>(p->E + 2, p->n));
   const long long tiles = (long long)a.most * a.tiles_j;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t more = kEpiWarps * kPatchBytes + table_bytes(a.E);

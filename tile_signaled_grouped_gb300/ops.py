@@ -247,10 +247,11 @@ def combine_experts_backward(dy, r, w, order, stream=None):
 # ----------------------------------------------------------------------- expert products
 def expert_linear(x, weight, offsets, stream=None):
     """y [n, N]: y[r] = weight[e] x[r] for the rows offsets[e] to offsets[e + 1] - 1 of every expert e, with
-    fp32 sums; zeros in the rows from offsets[E] on.
+    fp32 sums; zeros in the rows before offsets[0] and from offsets[E] on.
 
     x: [n, K], weight: [E, N, K], both bf16 or both fp16, N and K multiples of 8, rows on 16
-    bytes; offsets: int32 [E + 1] on the device, as sort_experts returns them."""
+    bytes; offsets: int32 [E + 1] on the device, ascending, as sort_experts returns them (or a part of
+    them, for the experts that weight then holds)."""
     if stream is not None:
         with _on(x, stream):
             return expert_linear(x, weight, offsets)
