@@ -1067,7 +1067,9 @@ __device__ __forceinline__ void unpack8(const uint4& u, int dtype, float (&f)[8]
 // columns of four rows at a time, warp w rows 4 w .. of every 32, and all eight loads leave
 // before the first is used; the eight warps' sums are added in order: 10.9 us for 4096 x 1536
 // (3.5 TB/s; cold, under a profiler). Otherwise a thread takes one column, so that neighbouring
-// threads read neighbouring elements. EIGHT: z was kept in 8 bits.
+// threads read neighbouring elements. EIGHT: z was kept in 8 bits. RESTORE: CTAs behind the ranges restore x;
+// compiled into the others too, they took the scalar forms from 28 registers to 40, six CTAs an SM for the
+// eight that the ranges are cut for, and so to a second wave (8192 x 4100 with silu 253 us where this takes 139).
 constexpr int kActRows = 4;
 constexpr int kRestoreUnits = 4;  // of a thread
 
@@ -1099,15 +1101,17 @@ __device__ __forceinline__ void restore_units(const ActGradArgs& a, long long bl
   }
 }
 
-template <int ACT, bool VEC, bool EIGHT>
+template <int ACT, bool VEC, bool EIGHT, bool RESTORE>
 __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
   __shared__ float red[VEC ? 8 : 1][32][9];
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if ((int)blockIdx.y >= a.ranges) {
-    restore_units(a, (long long)(blockIdx.y - a.ranges) * gridDim.x + blockIdx.x,
-                  (long long)(gridDim.y - a.ranges) * gridDim.x);
-    return;
+  if constexpr (RESTORE) {
+    if ((int)blockIdx.y >= a.ranges) {
+      restore_units(a, (long long)(blockIdx.y - a.ranges) * gridDim.x + blockIdx.x,
+                    (long long)(gridDim.y - a.ranges) * gridDim.x);
+      return;
+    }
   }
   const int lo = blockIdx.y * a.rows, hi = min(a.M, lo + a.rows);
   const int c = blockIdx.x * 256 + threadIdx.x;  // the column whose sum this thread writes
@@ -1541,21 +1545,23 @@ struct StreamDevice {
   StreamDevice& operator=(const StreamDevice&) = delete;
 };
 
+template <int ACT, bool EIGHT>
+void launch_act_grad(const ActGradArgs& a, bool vec, dim3 grid, cudaStream_t s) {
+  if (a.units > 0 && vec)
+    act_grad_kernel<ACT, true, EIGHT, true><<<grid, 256, 0, s>>>(a);
+  else if (a.units > 0)
+    act_grad_kernel<ACT, false, EIGHT, true><<<grid, 256, 0, s>>>(a);
+  else if (vec)
+    act_grad_kernel<ACT, true, EIGHT, false><<<grid, 256, 0, s>>>(a);
+  else
+    act_grad_kernel<ACT, false, EIGHT, false><<<grid, 256, 0, s>>>(a);
+}
 template <int ACT>
 void launch_act_grad(const ActGradArgs& a, bool vec, dim3 grid, cudaStream_t s) {
   if constexpr (ACT != MOE_ACT_NONE) {
-    if (a.z_scales != nullptr) {
-      if (vec)
-        act_grad_kernel<ACT, true, true><<<grid, 256, 0, s>>>(a);
-      else
-        act_grad_kernel<ACT, false, true><<<grid, 256, 0, s>>>(a);
-      return;
-    }
+    if (a.z_scales != nullptr) return launch_act_grad<ACT, true>(a, vec, grid, s);
   }
-  if (vec)
-    act_grad_kernel<ACT, true, false><<<grid, 256, 0, s>>>(a);
-  else
-    act_grad_kernel<ACT, false, false><<<grid, 256, 0, s>>>(a);
+  launch_act_grad<ACT, false>(a, vec, grid, s);
 }
 
 }  // namespace
