@@ -546,7 +546,9 @@ int moe_combine_experts_backward(const moe_rows_args *args, moe_stream_t stream)
  * Blocks of 32 elements of a row (the last one of a row may be shorter) share a scale 2^s, stored
  * as s + 127, with the least s in -127 .. 127 for which the block's largest finite |x| is at most
  * 448 * 2^s; the code of an element is x * 2^-s rounded to e4m3, to nearest, ties to even, NaN
- * where x is not finite. Restored, an element is within 2^-4 of itself, or within 2^-10 * 2^s.
+ * where x is not finite, and the code below where that one would stand for more than dtype holds
+ * (|x| from 63488 on in fp16, from 1.9375 * 2^127 on in the others). Restored in dtype, an element is
+ * within 2^-4 of itself, or within 2^-10 * 2^s.
  * ------------------------------------------------------------------------- */
 typedef struct moe_checkpoint_args {
   long long n, c;   /* rows; elements of a row */

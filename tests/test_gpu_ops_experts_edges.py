@@ -101,3 +101,49 @@ def test_offsets_that_leave_no_rows_inside():
         assert torch.equal(dx, want.to(x.dtype)) and torch.equal(dx2, (want + add.double()).to(x.dtype)), bad
         assert torch.equal(dw.double(), X.weights_grad(dy, x, inside)[0]), bad
     assert ops.status() == (0, 0)
+
+
+# e: the type's largest exponent. |x| from 1.9375 2^e on is nearest to 2^(e + 1), which the type does not hold.
+TOP = {torch.float16: (15, 65504.0, 63456.0), torch.bfloat16: (127, 3.3895313892515355e38, 1.9296875 * 2.0 ** 127),
+       torch.float32: (127, 3.4028234663852886e38, 3.29e38)}
+
+
+@pytest.mark.parametrize("dtype", TOP, ids=str)
+@pytest.mark.parametrize("c", [64, 77, 512])
+def test_the_largest_numbers_stay_finite_in_8_bits(dtype, c):
+    """A type's largest numbers are kept as 1.875 2^e: 2^-4 of them is what the code loses at most, and the one
+    above would come back as an infinity."""
+    e, most, below = TOP[dtype]
+    x = torch.full((3, c), 2.0 ** (e - 3), device="cuda").to(dtype)
+    special = torch.tensor([most, -most, 1.9375 * 2.0 ** e, -1.9375 * 2.0 ** e, below, 1.75 * 2.0 ** e, -0.0, 1.0])
+    x[0, :8] = special.to(dtype)
+    x[1, c - 8:] = special.to(dtype)
+    x[2, 3], x[2, 5] = most, float("inf")  # the others of a block with an infinity
+    kept = ops.checkpoint(x)
+    back = ops.restore(kept, dtype)
+    assert torch.equal(torch.isnan(back), torch.isinf(x)) and not torch.isinf(back).any()
+    want = torch.tensor([1.875, -1.875, 1.875, -1.875, 1.875, 1.75], dtype=torch.float64) * 2.0 ** e
+    assert torch.equal(back[0, :6].double().cpu(), want) and torch.equal(back[1, c - 8:c - 2].double().cpu(), want)
+    assert float(back[2, 3].double()) == 1.875 * 2.0 ** e
+    finite = torch.isfinite(x) & (x.abs() > 2.0 ** e / 2 ** 10)
+    x64 = x.double()
+    assert ((back.double() - x64).abs() <= 2.0 ** -4 * x64.abs())[finite].all()
+    if dtype == torch.float32:
+        return
+    # as gate and up, kept by the launch that multiplies them, and read in place of them
+    _, both = ops.gated(x, x, checkpoint=True)
+    for k in both:
+        assert torch.equal(k.codes.view(torch.uint8), kept.codes.view(torch.uint8))
+        assert torch.equal(k.scales, kept.scales)
+    small = torch.full_like(x, 2.0 ** -14)
+    dg, du, _ = ops.gated_backward(small[:2], *(ops.Checkpoint(k.codes[:2], k.scales[:2]) for k in both), act="relu")
+    assert torch.isfinite(dg).all() and torch.isfinite(du).all()
+
+
+def test_linear_backward_from_the_largest_numbers():
+    """dW of an x at the end of fp16's range, from 8 bits: the product of 61440 with the rows' 2^-12."""
+    x = torch.full((40, 64), 65504.0, dtype=torch.float16, device="cuda")
+    dy = torch.full((40, 16), 2.0 ** -12, dtype=torch.float16, device="cuda")
+    w = torch.zeros(16, 64, dtype=torch.float16, device="cuda")
+    _, dw, _ = ops.linear_backward(dy, ops.checkpoint(x), w, need_dx=False)
+    assert (dw == 40 * 61440 * 2.0 ** -12).all()

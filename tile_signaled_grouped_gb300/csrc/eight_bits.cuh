@@ -2,7 +2,9 @@
 // s + 127), the least for which the block's largest finite |x| is at most 448 2^s, the largest e4m3
 // number; a code is x 2^-s rounded to e4m3, to nearest, ties to even. Scaling by a power of two is
 // exact, so the rounding to the code is the only error: 2^-4 of x at most, or 2^-10 2^s. What is not
-// finite becomes NaN (an infinity that came back as 448 2^s would hide an overflow).
+// finite becomes NaN (an infinity that came back as 448 2^s would hide an overflow). From 1.9375 2^e on, e the
+// largest exponent of x's type, the nearest code stands for 2^(e + 1), an infinity in that type: there it
+// is the one below, 1.875 2^e, which is within 2^-4 of x too.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -90,19 +92,26 @@ struct CodeWord {
 // The codes of one element.
 __device__ __forceinline__ float decode1(const uint8_t* p, float scale) { return decode2(__ldg(p)).x * scale; }
 
-// The codes of N elements from element c of a row of `width`, and their block's scale, for elements
+// The codes of N elements of T from element c of a row of `width`, and their block's scale, for elements
 // whose largest finite |x| in the block (other lanes have the rest of it) has the bits `most`.
-// FINITE: all of the block are. Whole warps where ANY.
-template <int N, bool ANY, bool FINITE>
-__device__ __forceinline__ void store_codes(const float (&f)[N], uint32_t most, uint8_t* codes, uint8_t* scales,
+// PLAIN: all of the block are finite and below 1.9375 2^e. Whole warps where ANY.
+template <typename T, bool ANY, bool PLAIN, int N>
+__device__ __forceinline__ void store_codes(float (&f)[N], uint32_t most, uint8_t* codes, uint8_t* scales,
                                             long long c, long long width, int lane) {
   const uint32_t s = scale_of(most);
   const float inverse = scale_inverse(s);
+  constexpr uint32_t kExponent = std::is_same<T, __half>::value ? 0x47000000u : 0x7F000000u;
+  constexpr uint32_t kTop = kExponent | 0x780000u, kBelow = kExponent | 0x700000u;  // 1.9375 and 1.875
+  if (!PLAIN && most >= kTop) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (finite_bits(f[i]) >= kTop) f[i] = copysignf(__uint_as_float(kBelow), f[i]);
+  }
   Words<N> o;
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     const float* g = f + 4 * i;
-    if constexpr (FINITE)
+    if constexpr (PLAIN)
       o.w[i] = __nv_cvt_float2_to_fp8x2(make_float2(g[0] * inverse, g[1] * inverse), __NV_SATFINITE, __NV_E4M3) |
                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(g[2] * inverse, g[3] * inverse), __NV_SATFINITE,
                                                   __NV_E4M3) << 16;
@@ -118,7 +127,7 @@ __device__ __forceinline__ void store_codes(const float (&f)[N], uint32_t most, 
 
 // A lane's vector of a row to codes; the block's other elements are in the neighbouring lanes, c is a
 // multiple of the vector. Whole warps. Of 16-bit types the bits of |x| are in the order of |x|, so two
-// elements at a time give the largest; only where that is not finite do they have to be looked
+// elements at a time give the largest; only where that is 1.9375 2^e or more do they have to be looked
 // at one by one (131 instructions for eight elements one by one, 60 so).
 template <typename T, bool ANY>
 __device__ __forceinline__ void encode_vec(const RowVec<T, ANY>& x, uint8_t* codes, uint8_t* scales, long long c,
@@ -126,14 +135,14 @@ __device__ __forceinline__ void encode_vec(const RowVec<T, ANY>& x, uint8_t* cod
   constexpr int N = Vec<T>::kN;
   float f[N];
   if constexpr (sizeof(T) == 2) {
-    constexpr uint32_t kAbs = 0x7FFF7FFFu, kInf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    constexpr uint32_t kAbs = 0x7FFF7FFFu, kTop = std::is_same<T, __half>::value ? 0x7BC0u : 0x7F78u;
     uint32_t m = __vmaxu2(__vmaxu2(x.v.w[0] & kAbs, x.v.w[1] & kAbs), __vmaxu2(x.v.w[2] & kAbs, x.v.w[3] & kAbs));
     m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 1));
     m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 2));
     m = max(m & 0xFFFFu, m >> 16);
-    if (!__any_sync(kAll, m >= kInf)) {
+    if (!__any_sync(kAll, m >= kTop)) {
       x.get(f);
-      store_codes<N, ANY, true>(f, __float_as_uint(unpack2<T>(m).x), codes, scales, c, width, lane);
+      store_codes<T, ANY, true>(f, __float_as_uint(unpack2<T>(m).x), codes, scales, c, width, lane);
       return;
     }
   }
@@ -143,7 +152,7 @@ __device__ __forceinline__ void encode_vec(const RowVec<T, ANY>& x, uint8_t* cod
   for (int q = 0; q < N; ++q) most = max(most, finite_bits(f[q]));
 #pragma unroll
   for (int o = 1; o < kScaleBlock / N; o <<= 1) most = max(most, __shfl_xor_sync(kAll, most, o));
-  store_codes<N, ANY, false>(f, most, codes, scales, c, width, lane);
+  store_codes<T, ANY, false>(f, most, codes, scales, c, width, lane);
 }
 
 #endif  // __CUDACC__

@@ -174,7 +174,7 @@ class Checkpoint(NamedTuple):
 
 def checkpoint(x, stream=None):
     """x [..., c] (bf16, fp16 or fp32) as a Checkpoint: each element is within 2^-4 of itself, or
-    within 2^-10 of its block's scale; what is not finite becomes NaN."""
+    within 2^-10 of its block's scale; what is finite stays so in x's type, what is not becomes NaN."""
     if stream is not None:
         with _on(x, stream):
             return checkpoint(x)
