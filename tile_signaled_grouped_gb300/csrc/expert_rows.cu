@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(32 * kBackWarps, 1) combine_backward_kernel(co
 constexpr long long kMaxRows = INT32_MAX / 2;
 
 int check_rows(const moe_rows_args* p) {
-  if (p == nullptr || p->T < 0 || p->topk < 1 || p->topk > 32 || p->T * p->topk > kMaxRows || p->E < 1 ||
+  if (p == nullptr || p->T < 0 || p->topk < 1 || p->topk > 32 || p->T > kMaxRows / p->topk || p->E < 1 ||
       p->E > kSortMaxExperts || p->D < 1 || p->D > INT32_MAX / 2)
     return MOE_ERR_ARG;
   return type_bytes(p->dtype) == 0 ? MOE_ERR_ARG : MOE_OK;
