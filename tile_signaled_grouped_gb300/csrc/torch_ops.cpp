@@ -584,7 +584,10 @@ Tensor combine_experts(const Tensor& r, const OptTensor& w, const Tensor& rows, 
 }
 
 std::tuple<Tensor, Tensor> combine_experts_backward(const Tensor& dy, const Tensor& r, const OptTensor& scales,
-                                                    const Tensor& w, const Tensor& rows, const Tensor& offsets) {
+                                                    const OptTensor& weights, const Tensor& rows,
+                                                    const Tensor& offsets) {
+  if (!weights.has_value()) refuse("w is None: without weights the gradient of r is expert_rows(dy, order)");
+  const Tensor& w = *weights;
   const Order o = order_of(rows, offsets, dy);
   const int dt = checked_type(dy, "dy");
   const Rows d = rows_of(dy, "dy");

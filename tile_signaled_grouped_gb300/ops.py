@@ -236,7 +236,8 @@ def combine_experts(r, w, order, stream=None):
 
 def combine_experts_backward(dy, r, w, order, stream=None):
     """(d_r, d_w) of combine_experts from the gradient dy of y, for its r (or the Checkpoint of r), w and
-    order. d_r has dy's type, and zeros behind the last row; d_w is fp32, 0 for slots without a row."""
+    order. d_r has dy's type, and zeros behind the last row; d_w is fp32, 0 for slots without a row. (Without
+    weights, w None there, d_r is expert_rows(dy, order).)"""
     if stream is not None:
         with _on(dy, stream):
             return combine_experts_backward(dy, r, w, order)
