@@ -8,8 +8,11 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from tests import experts_ref as X  # noqa: E402
-from tests.test_gpu_ops_experts import experts_case  # noqa: E402
+from tests import ops_ref as R  # noqa: E402
+from tests.test_gpu_ops_experts import draw_ids, experts_case, gen, matrix  # noqa: E402
+from tests.test_gpu_ops_linear import close  # noqa: E402
 from tile_signaled_grouped_gb300 import capi, ops  # noqa: E402
+from tile_signaled_grouped_gb300.block import Experts  # noqa: E402
 
 TYPE = {torch.bfloat16: capi.MOE_BF16, torch.float16: capi.MOE_FP16, torch.float32: capi.MOE_FP32}
 
@@ -147,3 +150,117 @@ def test_linear_backward_from_the_largest_numbers():
     w = torch.zeros(16, 64, dtype=torch.float16, device="cuda")
     _, dw, _ = ops.linear_backward(dy, ops.checkpoint(x), w, need_dx=False)
     assert (dw == 40 * 61440 * 2.0 ** -12).all()
+
+
+# T, E, topk, D, dtype, pad of the rows, pad of dy, drop: rows on 16 bytes, dy's alone elsewhere
+DY_ANYWHERE = [(T, E, topk, D, dtype, pad, 1 + 2 * (topk % 3), drop)
+               for T, E, topk, D, drop in ((1, 4, 1, 8, False), (300, 5, 1, 2056, True), (257, 6, 2, 264, True),
+                                           (100, 9, 4, 1032, False), (77, 30, 8, 4096, True), (64, 16, 11, 520, True))
+               for dtype, pad in (("bf16", 0), ("fp16", 8), ("fp32", 4))]
+
+
+@pytest.mark.parametrize("case", DY_ANYWHERE, ids=str)
+def test_combine_gradient_of_a_dy_that_starts_anywhere(case):
+    """dy as columns of something wider: the rows go by vectors, dy alone by two of them shifted together. The
+    same bits as with a dy of its own, from values and from codes."""
+    T, E, topk, D, dtype, pad, pad_dy, drop = case
+    g = gen(T, E, D)
+    order = ops.sort_experts(draw_ids(g, T, E, topk, drop), E)
+    n, total = T * topk, int(order.offsets[-1])
+    r, dy = matrix(g, n, D, dtype, pad), matrix(g, T, D, dtype, pad_dy)
+    r[total:] = float("nan")
+    dy.as_strided((T - 1, pad_dy), (D + pad_dy, 1), dy.storage_offset() + D)[:] = float("nan")  # between its rows
+    w = torch.rand(T, topk, generator=g, device="cuda")
+    for kept in (r, ops.checkpoint(r)):
+        want = ops.combine_experts_backward(dy.clone(memory_format=torch.contiguous_format), kept, w, order)
+        for a, b in zip(ops.combine_experts_backward(dy, kept, w, order), want):
+            assert torch.equal(a, b)
+    want_r, want_w, tol = X.combine_backward(dy, r, w, order.rows, n)
+    dr, dw = ops.combine_experts_backward(dy, r, w, order)
+    close(dr, want_r, R.U32 * want_r.abs())
+    close(dw, want_w, tol)
+    # without weights
+    ones = torch.ones_like(w)
+    assert torch.equal(ops.combine_experts_backward(dy, r, ones, order)[0], ops.expert_rows(dy, order))
+    assert ops.status() == (0, 0)
+
+
+@pytest.mark.parametrize("n,c", [(1, 1), (1, 7), (3, 33), (40, 136), (65, 1531), (7, 4104)])
+@pytest.mark.parametrize("at", [(0, 1, 0), (1, 0, 1), (1, 1, 0), (0, 0, 1)], ids=str)
+def test_gated_gradients_that_start_in_different_places(n, c, at):
+    """By the C ABI, dgate, dup and h in rows of their own, some of them off a word's beginning: the same bits as by
+    ops, and nothing beside the rows."""
+    g = gen(n, c)
+    dt = torch.float16 if c % 2 else torch.bfloat16
+    gate, up, dh = (torch.randn(n, c, generator=g, device="cuda").to(dt) for _ in range(3))
+    want = ops.gated_backward(dh, gate, up, need_h=True)
+    for pads in ((1, 1, 1), (2, 3, 4)):  # rows that all lie alike, and rows that do not
+        wide = [nan(n * (c + p) + 2, dtype=dt) for p in pads]
+        out = [t[a:a + n * (c + p)].view(n, c + p)[:, :c] for t, a, p in zip(wide, at, pads)]
+        c_call("moe_gated_backward", capi.moe_gated_args, n=n, c=c, dtype=TYPE[dt], act=capi.MOE_ACT_SILU, gate=gate,
+               up=up, dh=dh, dgate=out[0], dup=out[1], h=out[2], ld_gate=c, ld_up=c, ld_dh=c, ld_dgate=c + pads[0],
+               ld_dup=c + pads[1], ld_h=c + pads[2])
+        for o, v, t in zip(out, want, wide):
+            assert torch.equal(o, v) and int(torch.isnan(t).sum()) == t.numel() - n * c
+    assert ops.status() == (0, 0)
+
+
+def test_a_long_sum_in_fp32_keeps_its_accuracy():
+    """dW of 32768 rows of one expert. The rows are taken 768 at a time: 48 steps of the tensor cores, which drop what
+    lies below the sum's last bit (2^-23 of it a step at most), and 43 parts, each added with a rounding (2^-24).
+    Running sums are no larger than the last, in the norm. In one part it would be 2048 steps, and is 3.8e-5."""
+    n, N, K = 32768, 256, 512
+    g = gen(n, N, K)
+    x, dy = matrix(g, n, K, "bf16"), matrix(g, n, N, "bf16")
+    offsets = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    weight = torch.zeros(1, N, K, dtype=torch.bfloat16, device="cuda")
+    _, dw = ops.expert_linear_backward(dy, x, weight, offsets, dw_dtype=torch.float32, need_dx=False)
+    want = dy.double().t() @ x.double()
+    parts = -(-n // 768)
+    assert (dw[0].double() - want).norm() <= (48 * 2.0 ** -23 + parts * 2.0 ** -24) * want.norm()
+
+
+def test_weights_and_rows_that_are_parts_of_others():
+    """Gate and up as halves of one matrix of every expert, every other expert of a stack, and x and dy as columns
+    of wider rows: the same bits as of copies."""
+    counts, E, F, K = [70, 0, 300, 9], 4, 136, 264
+    g = gen(E, F, K)
+    n = sum(counts)
+    offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).int()
+    both = matrix(g, 2 * E * 2 * F, K, "bf16", 8, K ** -0.5).unflatten(0, (2 * E, 2 * F))
+    wide_x, wide_dy = matrix(g, n, 3 * K, "bf16"), matrix(g, n, 2 * F, "bf16")
+    for weight in (both[:E, :F], both[:E, F:], both[::2, :F], both[1::2, F:]):
+        x, dy = wide_x[:, K:2 * K], wide_dy[:, F:]
+        own = [t.contiguous() for t in (x, dy, weight)]
+        assert torch.equal(ops.expert_linear(x, weight, offsets), ops.expert_linear(own[0], own[2], offsets))
+        got = ops.expert_linear_backward(dy, x, weight, offsets, add=wide_x[:, :K])
+        want = ops.expert_linear_backward(own[1], own[0], own[2], offsets, add=wide_x[:, :K].contiguous())
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert ops.status() == (0, 0)
+
+
+@pytest.mark.parametrize("keep", ["8 bits", "whole"])
+def test_experts_of_batches_and_of_nothing(keep):
+    """Tokens [2, 3, 5, D] as [30, D]; none at all; none that any expert was chosen for."""
+    g = gen(8, 4)
+    E, F, D, topk = 6, 40, 72, 3
+    weights = [matrix(g, E * a, b, "bf16", 0, b ** -0.5).unflatten(0, (E, a)) for a, b in ((F, D), (F, D), (D, F))]
+    ex = Experts(*weights, keep=keep)
+    h, dy = matrix(g, 30, D, "bf16"), matrix(g, 30, D, "bf16")
+    ids, w = draw_ids(g, 30, E, topk, True), torch.rand(30, topk, generator=g, device="cuda")
+    y, saved = ex.forward(h, ids, w, save=True)
+    grads = ex.backward(dy, saved)
+    shape = (2, 3, 5)
+    y4, saved4 = ex.forward(h.view(*shape, D), ids.view(*shape, topk), w.view(*shape, topk), save=True)
+    assert y4.shape == (*shape, D) and torch.equal(y4.view(30, D), y)
+    for k, v in ex.backward(dy.view(*shape, D), saved4).items():
+        assert torch.equal(v.view(grads[k].shape), grads[k]), k
+
+    y, saved = ex.forward(h[:0], ids[:0], w[:0], save=True)
+    grads = ex.backward(dy[:0], saved)
+    assert y.shape == (0, D) and grads["h"].shape == (0, D) and grads["w"].shape == (0, topk)
+    assert not any(grads[k].any() for k in ("w_gate", "w_up", "w_down"))
+    y, saved = ex.forward(h, torch.full_like(ids, -1), w, save=True)
+    grads = ex.backward(dy, saved)
+    assert not y.any() and not any(v.any() for v in grads.values())
+    assert ops.status() == (0, 0)
