@@ -260,8 +260,8 @@ struct RowWalk {
       e = min(base + __popc(__ballot_sync(kAll, in)), last);
       // Groups of kGroup tiles of rows, inside a group feature by feature: the tiles in flight share their
       // operands in L2 (all tiles of rows of a feature tile first took 185 us where this takes 149 for 16384
-      // rows of one expert, 2048 x 4096). Up to kGroup tiles share an expert's rows evenly; of more the last
-      // might be left without any.
+      // rows of one expert, 2048 x 4096). Up to kGroup tiles share an expert's rows evenly, which is as far as
+      // the quotient goes; of more the last alone is shorter.
       const int count = t.count[e], tiles = (count + kRows - 1) / kRows;
       int local = (tile - t.first[e]) * a.tiles_j + part, from = 0, in_group = tiles, per = kRows;
       if (tiles <= kGroup) {
@@ -533,10 +533,13 @@ struct WeightArgs {
 };
 
 // The tensor cores' fp32 sums lose what lies below their last bit at every step, so their error grows with the
-// number of rows: relative to dW 2.3e-7 for 256, 1.0e-6 for 1024, 9e-6 for 8192, 3.8e-5 for 32768. An fp32 dW
-// therefore takes a tile's rows in parts, which are added to what is stored by copies that add (fp32, rounded to
-// nearest, one after the other): 7e-7 for any number. (16384 rows, 2048 x 4096: 157 us in one part, 223 by parts
-// of 1024, 255 by 768, 313 by 512.) In 16 bits the rounding of dW is a thousand times as much: one part.
+// number of rows: relative to dW's norm 3.4e-7 for 256 random rows, 9.4e-7 for 768, then 1.2e-9 a row (3.8e-5 for
+// 32768). An fp32 dW therefore takes a tile's rows in parts, which are added to what is stored by copies that add
+// (fp32, rounded to nearest, one after the other): 1.0e-6 up to 262144 rows, 1.2e-6 for 1048576, the parts'
+// own roundings. (16384 rows, 2048 x 4096: 157 us in one part, 223 by parts of 1024, 255 by 768, 313 by 512.) In 16
+// bits there is one part: the rounding of dW itself is 2.1e-4 of its norm in fp16 and 1.7e-3 in bf16, which
+// the sum's error reaches at some 170000 rows of one expert in fp16 and at 1.4 million in bf16 (in all,
+// 262144 rows in fp16 are off by 3.7e-4, 1048576 in bf16 by 2.1e-3).
 constexpr int kPartRows = 768;
 
 // The tiles of a pair: p, p + pairs, ... of the order expert, rows, columns of dW: the tiles in flight

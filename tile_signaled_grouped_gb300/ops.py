@@ -149,11 +149,12 @@ def linear_backward(dy, x, weight, z=None, act="none", bias=None, dw_dtype=None,
                     need_dw=True, stream=None):
     """(dx, dweight, dbias) of linear from the gradient dy of y (which is the residual's
     gradient too), for its x, weight, act and the z that it returned with preact. x, z or both may be
-    their Checkpoints.
+    their Checkpoints, that of x where its rows hold a multiple of 8 elements.
 
     bias: the type of dbias (x's or torch.float32), or None for no dbias. dweight has
     dw_dtype (x's type or fp32; default x's). The products take dy act'(z) rounded to x's
-    type."""
+    type. An fp32 dweight loses about 1.2e-9 of its norm for each row that is summed at once (1e-5 for 65536
+    rows of 256 x 512); expert_linear_backward's does not."""
     if stream is not None:
         with _on(dy, stream):
             return linear_backward(dy, x, weight, z, act, bias, dw_dtype, need_dx, need_dw)
@@ -264,7 +265,9 @@ def expert_linear_backward(dy, x, weight, offsets, add=None, dw_dtype=None, need
     """(dx, dweight) of expert_linear from the gradient dy of y, for its x (None without need_dw), weight and
     offsets. add [n, K] of x's type, rows on 16 bytes, is added to dx before it is rounded (the gradient through
     another product of the same x).
-    dweight has dw_dtype (x's type or fp32; default x's); it is zero for experts without rows."""
+    dweight has dw_dtype (x's type or fp32; default x's); it is zero for experts without rows. In fp32 it is
+    within 1.2e-6 of its norm up to a million rows of an expert. In 16 bits its fp32 sum loses 1.2e-9 of the
+    norm for each row: from some 170000 rows of one expert in fp16, 1.4 million in bf16, take fp32 for accuracy."""
     if stream is not None:
         with _on(dy, stream):
             return expert_linear_backward(dy, x, weight, offsets, add, dw_dtype, need_dx, need_dw)
