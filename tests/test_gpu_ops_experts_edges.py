@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 from tests import experts_ref as X  # noqa: E402
 from tests import ops_ref as R  # noqa: E402
 from tests.test_gpu_ops_experts import draw_ids, experts_case, gen, matrix  # noqa: E402
-from tests.test_gpu_ops_linear import close  # noqa: E402
+from tests.test_gpu_ops_linear import DT, close  # noqa: E402
 from tile_signaled_grouped_gb300 import capi, ops  # noqa: E402
 from tile_signaled_grouped_gb300.block import Experts  # noqa: E402
 
@@ -95,7 +95,8 @@ def test_some_experts_of_an_order():
 def test_offsets_that_leave_no_rows_inside():
     """As test_offsets_outside_the_rows_are_left_out, into NaN, and dx too."""
     _, n, x, weight, dy, add = experts_case(([40, 50, 60], 0, 64, 64, "bf16", 0), whole=True)
-    for bad in ([-7, 40, 90, 150], [0, 40, 90, 10 ** 6], [0, 40, 40, 40], [150, 150, 150, 150], [7, 7, 10 ** 6, 10 ** 6]):
+    for bad in ([-7, 40, 90, 150], [0, 40, 90, 10 ** 6], [0, 40, 40, 40], [150, 150, 150, 150],
+                [7, 7, 10 ** 6, 10 ** 6]):
         off = torch.tensor(bad, dtype=torch.int32, device="cuda")
         inside = off.clamp(0, n)
         y, dx, dx2, dw = products_into_nan(x, weight, dy, add, off)
@@ -263,4 +264,136 @@ def test_experts_of_batches_and_of_nothing(keep):
     y, saved = ex.forward(h, torch.full_like(ids, -1), w, save=True)
     grads = ex.backward(dy, saved)
     assert not y.any() and not any(v.any() for v in grads.values())
+    assert ops.status() == (0, 0)
+
+
+# ------------------------------------------------------------------- outputs inside something wider
+class Wide:
+    """An output [n, c] from element `at` of a buffer full of one byte, in rows of `ld`; untouched() says that nothing
+    beside its rows was written."""
+
+    def __init__(self, n, c, ld, at, dtype, experts=1, stride=0):
+        size = torch.empty(0, dtype=dtype).element_size()
+        self.bytes = torch.full(((at + (experts - 1) * stride + n * ld + 64) * size,), 0x5A, dtype=torch.uint8,
+                                device="cuda")
+        self.all = self.bytes.view(dtype)
+        self.t = self.all.as_strided((experts, n, c), (stride, ld, 1), at)
+        if experts == 1:
+            self.t = self.t[0]
+        self.n, self.c, self.ld, self.at, self.size, self.experts, self.stride = n, c, ld, at, size, experts, stride
+
+    def untouched(self):
+        mask = torch.ones(self.bytes.numel() // self.size, dtype=torch.bool, device="cuda")
+        mask.as_strided((self.experts, self.n, self.c), (self.stride, self.ld, 1), self.at)[:] = False
+        return bool((self.bytes.view(-1, self.size)[mask] == 0x5A).all())
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,topk,D,pad,at", [(5, 2, 1, 2, 1), (33, 3, 70, 3, 5), (40, 8, 264, 8, 8),
+                                             (17, 1, 1531, 5, 3), (50, 4, 520, 1, 0), (29, 2, 33, 31, 7)])
+def test_rows_into_wider_rows(T, topk, D, pad, at, dtype):
+    """By the C ABI, rows, sums and their gradients inside something wider: the same bits as by ops, and nothing
+    beside."""
+    g = gen(T, D)
+    dt, E, n = DT[dtype], 11, T * topk
+    order = ops.sort_experts(draw_ids(g, T, E, topk, True), E)
+    x, r, w = matrix(g, T, D, dtype), matrix(g, n, D, dtype), torch.rand(T, topk, generator=g, device="cuda")
+    same = dict(T=T, D=D, topk=topk, E=E, dtype=TYPE[dt], rows=order.rows, offsets=order.offsets)
+    out = Wide(n, D, D + pad, at, dt)
+    c_call("moe_expert_rows", capi.moe_rows_args, **same, x=x, ld_x=D, dr=out.t, ld_dr=out.ld)
+    assert torch.equal(out.t, ops.expert_rows(x, order)) and out.untouched()
+    for weights in (w, None):
+        out = Wide(T, D, D + pad, at, dt)
+        c_call("moe_combine_experts", capi.moe_rows_args, **same, w=weights, r=r, ld_r=D, y=out.t, ld_y=out.ld)
+        assert torch.equal(bits(out.t), bits(ops.combine_experts(r, weights, order))) and out.untouched()
+    kept = ops.checkpoint(r)
+    for src, scales in ((r, None), (kept.codes, kept.scales)):
+        out, dw = Wide(n, D, D + pad, at, dt), Wide(T, topk, topk, 1, torch.float32)
+        c_call("moe_combine_experts_backward", capi.moe_rows_args, **same, w=w, x=x, ld_x=D, r=src, ld_r=D,
+               r_scales=scales, ld_scales=-(-D // 32), dr=out.t, ld_dr=out.ld, dw=dw.t)
+        want, _ = ops.combine_experts_backward(x, r if scales is None else kept, w, order)
+        assert torch.equal(bits(out.t), bits(want)) and out.untouched() and dw.untouched()
+        # sums over the columns are shared out by where rows start: within their own errors
+        values = r if scales is None else ops.restore(kept, torch.float32)
+        close(dw.t, *X.combine_backward(x, values, w, order.rows, n)[1:])
+    assert ops.status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("n,c,pad,at", [(1, 1, 0, 1), (3, 31, 2, 3), (5, 64, 32, 8), (9, 136, 8, 16), (40, 1531, 5, 5),
+                                        (6, 4096, 1, 0), (65, 128, 5, 0)])
+def test_checkpoints_into_wider_rows(n, c, pad, at, dtype):
+    """As above, codes and scales in rows of their own, and restored into wider rows from them."""
+    dt = DT[dtype]
+    x = matrix(gen(n, c), n, c, dtype)
+    want, blocks = ops.checkpoint(x), -(-c // 32)
+    codes, scales = Wide(n, c, c + pad, at, torch.uint8), Wide(n, blocks, blocks + pad, at, torch.uint8)
+    back = Wide(n, c, c + pad, at, dt)
+    same = dict(n=n, c=c, dtype=TYPE[dt], codes=codes.t, scales=scales.t, ld_codes=codes.ld, ld_scales=scales.ld)
+    c_call("moe_checkpoint", capi.moe_checkpoint_args, **same, x=x, ld_x=c)
+    assert torch.equal(codes.t, want.codes.view(torch.uint8)) and torch.equal(scales.t, want.scales)
+    c_call("moe_restore", capi.moe_checkpoint_args, **same, x=back.t, ld_x=back.ld)
+    assert torch.equal(bits(back.t), bits(ops.restore(want, dt)))
+    assert codes.untouched() and scales.untouched() and back.untouched()
+
+
+@pytest.mark.parametrize("n,c,pad,at", [(1, 1, 0, 1), (3, 33, 2, 3), (9, 136, 8, 16), (40, 1531, 5, 5),
+                                        (6, 4104, 1, 0)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_gated_into_wider_rows(n, c, pad, at, keep):
+    """As above; the codes' rows are c apart, from any byte on."""
+    g = gen(n, c)
+    dt = torch.float16 if c % 2 else torch.bfloat16
+    gate, up, dh = (torch.randn(n, c, generator=g, device="cuda").to(dt) for _ in range(3))
+    want, kept = ops.gated(gate, up, checkpoint=True)
+    blocks = -(-c // 32)
+    h = Wide(n, c, c + pad, at, dt)
+    parts = [Wide(n, m, m, at, torch.uint8) for m in (c, blocks, c, blocks)] if keep else [None] * 4
+    named = dict(zip(("gate_codes", "gate_scales", "up_codes", "up_scales"), (p and p.t for p in parts)))
+    both = dict(n=n, c=c, dtype=TYPE[dt], act=capi.MOE_ACT_SILU)
+    c_call("moe_gated", capi.moe_gated_args, **both, **named, gate=gate, up=up, ld_gate=c, ld_up=c, h=h.t, ld_h=h.ld)
+    assert torch.equal(bits(h.t), bits(want)) and h.untouched()
+    if keep:
+        for p, v in zip(parts, (*kept[0], *kept[1])):
+            assert torch.equal(p.t, v.view(torch.uint8)) and p.untouched()
+        gate, up = parts[0].t, parts[2].t
+    scales = dict(gate_scales=parts[1].t, up_scales=parts[3].t) if keep else {}
+    out = [Wide(n, c, c + pad, at, dt) for _ in range(3)]
+    c_call("moe_gated_backward", capi.moe_gated_args, **both, **scales, gate=gate, up=up, ld_gate=c, ld_up=c, dh=dh,
+           ld_dh=c, dgate=out[0].t, dup=out[1].t, h=out[2].t, ld_dgate=c + pad, ld_dup=c + pad, ld_h=c + pad)
+    src = kept if keep else (gate, up)
+    for o, v in zip(out, ops.gated_backward(dh, *src, need_h=True)):
+        assert torch.equal(bits(o.t), bits(v)) and o.untouched()
+    assert ops.status() == (0, 0)
+
+
+@pytest.mark.parametrize("case", [([5, 0, 40], 3, 8, 8, "bf16", 0), ([300, 1, 0, 70], 0, 264, 136, "fp16", 0),
+                                  ([1000], 9, 200, 1000, "bf16", 0), ([2, 0, 1], 0, 256, 4096, "bf16", 0),
+                                  ([1600, 0, 769], 0, 72, 328, "fp16", 0), ([0, 0], 0, 40, 24, "bf16", 0)],
+                         ids=lambda c: f"{len(c[0])}x{sum(c[0])}+{c[1]} {c[2:]}")
+def test_products_into_wider_rows(case):
+    """y and dx in wider rows; dW of every expert in wider rows, experts further apart than they need."""
+    offsets, n, x, weight, dy, add = experts_case(case)
+    E, N, K = weight.shape
+    lib, dt = capi.lib(), x.dtype
+    y, dx = Wide(max(n, 1), N, N + 8, 8, dt), Wide(max(n, 1), K, K + 16, 16, dt)
+    work = nan(max(lib.moe_expert_linear_workspace(n, N, K, E), lib.moe_expert_linear_workspace(n, K, N, E)) // 4 + 4,
+               dtype=torch.float32).view(torch.uint8)
+    same = dict(n=n, N=N, K=K, E=E, dtype=TYPE[dt], offsets=offsets, w=weight, ld_w=K, stride_w=N * K)
+    if n:
+        c_call("moe_expert_linear", capi.moe_expert_linear_args, work, **same, x=x, ld_x=K, y=y.t, ld_y=y.ld)
+        assert torch.equal(y.t, ops.expert_linear(x, weight, offsets)) and y.untouched()
+    for wt in (dt, torch.float32):
+        dw = Wide(N, K, K + 24, 8, wt, E, N * (K + 24) + 40)
+        c_call("moe_expert_linear_backward", capi.moe_expert_linear_args, work, **same, dwtype=TYPE[wt], x=x, ld_x=K,
+               dy=dy, ld_dy=N, add=add, ld_add=K, dx=dx.t if n else None, ld_dx=dx.ld, dw=dw.t, ld_dw=dw.ld,
+               stride_dw=dw.stride)
+        want, want_w = ops.expert_linear_backward(dy, x, weight, offsets, add=add, dw_dtype=wt)
+        assert torch.equal(dw.t.view(E, N, K) if E == 1 else dw.t, want_w) and dw.untouched()
+        if n:
+            assert torch.equal(dx.t, want) and dx.untouched()
     assert ops.status() == (0, 0)
